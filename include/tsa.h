@@ -48,7 +48,8 @@ enum {
     TSA_ERR_WORKSPACE = -6,      /* sample: workspace NULL or smaller than required */
     TSA_ERR_CUDA = -7,           /* a CUDA runtime call failed (launch / attribute) */
     TSA_ERR_DEVICE_TIMEOUT = -8, /* a kernel's bounded wait ran out (see tsa_device_status) */
-    TSA_ERR_ALIGN = -9           /* a pointer is not aligned to its element size */
+    TSA_ERR_ALIGN = -9,          /* a pointer is not aligned to its element size */
+    TSA_ERR_VALUE = -10          /* a scalar parameter is out of its range or not finite */
 };
 
 /* Largest vocabulary a row may have, per element type (elements). */
@@ -287,6 +288,85 @@ int tsa_selective_log_softmax(const void *logits, tsa_dtype dtype, int64_t B, in
                               int64_t logits_row_stride, const int32_t *bitmask, int64_t mask_row_stride,
                               const float *temperature, float temperature_s, const int64_t *index,
                               float *out, void *stream);
+
+/*
+ * policy_loss -- the clipped policy loss of sampled tokens with a KL term and
+ * an entropy bonus, and its gradient on the logits, in one call.  The rows and
+ * tokens are those of sample and selective_log_softmax.  With x = l / T over a
+ * row's allowed tokens, p = softmax(x), lp = ln p[token], H = -sum p ln p and
+ * r = exp(lp - old):
+ *   row_loss = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *              + kl_coef (exp(ref - lp) - (ref - lp) - 1) - entropy_coef H
+ *   loss     = sum over rows of weight * row_loss
+ *   grad     = d loss / d logits: weight / T (c (1{j = token} - p_j)
+ *              + entropy_coef p_j (ln p_j + H)), c the derivative of the first
+ *              two terms by lp (-A r where the unclipped branch is taken).
+ *   logits, dtype, B, V, logits_row_stride, bitmask, mask_row_stride,
+ *   temperature, temperature_s: as for selective_log_softmax
+ *   tokens       [B] int64; a token outside [0, V) (sample's -1 for a row
+ *                with nothing allowed) skips its row
+ *   old_logprob, advantage  [B] float; an advantage of 0 contributes 0 even
+ *                where the ratio overflows
+ *   ref_logprob  [B] float or NULL: no KL term
+ *   weight       [B] float or NULL: 1 / B for every row; 0 skips a row
+ *   clip_low, clip_high >= 0, kl_coef, entropy_coef: finite (TSA_ERR_VALUE)
+ *   loss_out     [1] float (0 for B == 0); row_loss_out, logprob_out [B] float
+ *   entropy_out  [B] float or NULL
+ *   grad_out     [B, grad_row_stride] of dtype, or NULL for the loss alone; it
+ *                may be `logits` itself (same row stride), and otherwise must
+ *                not overlap it.  Fastest where its rows start at the same
+ *                address modulo 16 bytes as the logits' rows.
+ * A skipped row's logits are not read; its loss, log-probability, entropy and
+ * gradient are 0.  A row whose token the mask excludes, or whose mask leaves
+ * nothing, also has loss and gradient 0; its logprob_out is -inf, or NaN for
+ * the empty row.  NaN logits count as -inf; a +inf logit makes its row NaN.
+ * Rows are read from HBM once.  The sums run in fp32 and the loss over rows in
+ * a fixed order: equal calls give equal bits.
+ */
+int tsa_policy_loss(const void *logits, tsa_dtype dtype, int64_t B, int64_t V, int64_t logits_row_stride,
+                    const int32_t *bitmask, int64_t mask_row_stride, const float *temperature,
+                    float temperature_s, const int64_t *tokens, const float *old_logprob,
+                    const float *advantage, const float *ref_logprob, const float *weight, float clip_low,
+                    float clip_high, float kl_coef, float entropy_coef, float *loss_out,
+                    float *row_loss_out, float *logprob_out, float *entropy_out, void *grad_out,
+                    int64_t grad_row_stride, void *stream);
+
+/*
+ * preference_loss -- the loss of preferred over rejected answers from their
+ * paired log-ratios, and its gradient on the logits.  The N rows of logits are
+ * the tokens of 2 P sequences one after another: sequence s is rows
+ * seq_start[s] .. seq_start[s + 1] - 1, pair p is sequence p (preferred) and
+ * sequence P + p (rejected).  With lp_i row i's log-probability of its token,
+ *   R_s  = sum_{i in s} weight_i (lp_i - ref_i)   (average: divided by
+ *          sum_{i in s} weight_i; 0 for a sequence without counted rows)
+ *   h_p  = beta (R_p - R_{P+p}) - margin
+ *   pair_loss_p = (1 - label_smoothing) ln(1 + e^-h) + label_smoothing ln(1 + e^h)
+ *   loss = mean of the pair losses,  reward_s = beta R_s
+ *   grad = d loss / d logits
+ *   logits, dtype, N, V, logits_row_stride, tokens: rows as above; temperature
+ *                one value for every row (<= 0: 1)
+ *   seq_start    [2 P + 1] int64 device pointer, not decreasing, within
+ *                [0, N]; rows outside every sequence get gradient 0, and
+ *                values out of range are brought into it
+ *   weight       [N] float or NULL (1): 0 skips a row (prompt or padding)
+ *   ref_logprob  [N] float or NULL (reference-free)
+ *   0 <= label_smoothing <= 1, beta and margin finite (TSA_ERR_VALUE)
+ *   loss_out     [1] float; pair_loss_out [P], reward_out [2 P], logprob_out
+ *                [N] float
+ *   grad_out     as for policy_loss
+ *   workspace    at least tsa_preference_loss_workspace_bytes(N) bytes,
+ *                256-byte aligned
+ * Skipped and excluded rows as in policy_loss.  A row's coefficient needs
+ * every row of its pair, so the logits are read twice, the second time from
+ * the row last read back to the first.
+ */
+int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t V, int64_t logits_row_stride,
+                        float temperature, const int64_t *tokens, const int64_t *seq_start, int64_t P,
+                        const float *weight, const float *ref_logprob, float beta, float label_smoothing,
+                        float margin, int average, float *loss_out, float *pair_loss_out, float *reward_out,
+                        float *logprob_out, void *grad_out, int64_t grad_row_stride, void *workspace,
+                        size_t workspace_bytes, void *stream);
+size_t tsa_preference_loss_workspace_bytes(int64_t N);
 
 /* Human-readable name of a status code. */
 const char *tsa_status_string(int status);

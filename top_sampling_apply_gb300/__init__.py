@@ -11,14 +11,14 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional, Union
+from typing import NamedTuple, Optional, Union
 
 import torch
 
 from . import _build
 
-__all__ = ["apply_token_bitmask", "sample", "topk", "device_status", "max_vocab", "load_library",
-           "TSAError"]
+__all__ = ["apply_token_bitmask", "sample", "topk", "policy_loss", "preference_loss", "PolicyLoss",
+           "PreferenceLoss", "device_status", "max_vocab", "load_library", "TSAError"]
 
 _DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _lock = threading.Lock()
@@ -63,6 +63,12 @@ def load_library(path: Optional[str] = None):
         lib.tsa_lm_head_topk_workspace_bytes.argtypes = [i64, i64, i32]
         lib.tsa_lm_head_topk_workspace_bytes.restype = sz
         lib.tsa_selective_log_softmax.argtypes = [P, ci, i64, i64, i64, P, i64, P, f32, P, P, P]
+        lib.tsa_policy_loss.argtypes = [P, ci, i64, i64, i64, P, i64, P, f32, P, P, P, P, P, f32, f32, f32,
+                                        f32, P, P, P, P, P, i64, P]
+        lib.tsa_preference_loss.argtypes = [P, ci, i64, i64, i64, f32, P, P, i64, P, P, f32, f32, f32, ci,
+                                            P, P, P, P, P, i64, P, sz, P]
+        lib.tsa_preference_loss_workspace_bytes.argtypes = [i64]
+        lib.tsa_preference_loss_workspace_bytes.restype = sz
         lib.tsa_sample_workspace_bytes.argtypes = [i64, i64, ci]
         lib.tsa_sample_workspace_bytes.restype = sz
         lib.tsa_topk_workspace_bytes.argtypes = [i64, i64, i32, ci]
@@ -75,6 +81,7 @@ def load_library(path: Optional[str] = None):
         lib.tsa_max_vocab.restype = i64
         for fn in ("tsa_apply_token_bitmask", "tsa_sample", "tsa_sample_noalloc", "tsa_topk",
                    "tsa_sample_icdf", "tsa_bitmask_from_allowed", "tsa_sample_sequential", "tsa_lm_head_topk",
+                   "tsa_policy_loss", "tsa_preference_loss",
                    "tsa_device_status", "tsa_selftest_wait_timeout"):
             getattr(lib, fn).restype = ci
         _lib = lib
@@ -359,6 +366,126 @@ def topk(logits: torch.Tensor, k: int):
     _check(lib.tsa_topk(_ptr(logits), _DT[logits.dtype], B, V, stride, int(k), _ptr(values),
                         _ptr(indices), None, 0, _stream(logits)))
     return values, indices
+
+
+def _vec(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, dev, name: str):
+    """Checks an optional contiguous [n] tensor and returns it."""
+    if t is not None and (t.dtype != dtype or t.device != dev or t.shape != (n,) or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s [%d] tensor on %s" % (name, dtype, n, dev))
+    return t
+
+
+def _grad_rows(grad, logits: torch.Tensor) -> Optional[torch.Tensor]:
+    """The tensor a call writes its gradient to: none, the caller's, or a new
+    one whose rows start at the logits' alignment (the fast path)."""
+    if isinstance(grad, torch.Tensor):
+        if grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != logits.device \
+                or (grad.shape[0] > 0 and grad.stride(1) != 1):
+            raise ValueError("grad must have the logits' shape, dtype and device and unit stride along V")
+        return grad
+    if not grad:
+        return None
+    B, V = logits.shape
+    es = logits.element_size()
+    per = 16 // es
+    stride = V + (logits.stride(0) - V) % per
+    first = logits.data_ptr() % 16 // es
+    buf = torch.empty(B * stride + first, dtype=logits.dtype, device=logits.device)
+    return buf[first:].as_strided((B, V), (stride, 1)) if B else logits.new_empty(B, V)
+
+
+class PolicyLoss(NamedTuple):
+    """What ``policy_loss`` returns."""
+    loss: torch.Tensor  # float32 scalar: the weighted sum over rows
+    row_loss: torch.Tensor  # float32 [B]
+    logprob: torch.Tensor  # float32 [B]: ln p of each row's token
+    entropy: Optional[torch.Tensor]  # float32 [B]
+    grad: Optional[torch.Tensor]  # [B, V] of the logits' dtype: d loss / d logits
+
+
+def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: torch.Tensor, advantage: torch.Tensor,
+                ref_logprob: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0, entropy_coef: float = 0.0,
+                temperature: Param = 1.0, bitmask: Optional[torch.Tensor] = None, return_entropy: bool = False,
+                grad: Union[bool, torch.Tensor] = True) -> PolicyLoss:
+    """The clipped policy loss of sampled tokens, with a KL term against
+    ``ref_logprob`` and an entropy bonus, and its gradient on the logits.
+
+    A row's loss is -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef
+    (exp(ref - lp) - (ref - lp) - 1) - entropy_coef H, with lp the row's
+    ``selective_log_softmax`` at its token and r = exp(lp - old_logprob); the loss is the
+    sum of ``weight`` times it (None: the mean).  ``tokens`` as ``sample`` gives them: a
+    token of -1 skips its row, as a weight of 0 does, and skipped rows' logits are not read.
+    ``grad``: True for a new tensor, a tensor to write (``logits`` itself for in place), or
+    False for the loss alone.  There is no autograd graph: the gradient is returned, and
+    ``logits.backward(r.grad)`` carries it further."""
+    lib = load_library()
+    B, V, stride = _rows(logits)
+    dev = logits.device
+    _vec(tokens, B, torch.int64, dev, "tokens")
+    _vec(old_logprob, B, torch.float32, dev, "old_logprob")
+    _vec(advantage, B, torch.float32, dev, "advantage")
+    _vec(ref_logprob, B, torch.float32, dev, "ref_logprob")
+    _vec(weight, B, torch.float32, dev, "weight")
+    T, Ts = _param(temperature, B, torch.float32, dev)
+    mstride = _mask_stride(bitmask, B, V, dev)
+    logits = logits.detach()
+    g = _grad_rows(grad, logits)
+    n = 3 * B if return_entropy else 2 * B
+    out = torch.empty(n + 1, dtype=torch.float32, device=dev)
+    loss, row, lp = out[n], out[:B], out[B:2 * B]
+    ent = out[2 * B:n] if return_entropy else None
+    _check(lib.tsa_policy_loss(_ptr(logits), _DT[logits.dtype], B, V, stride, _ptr(bitmask), mstride, _ptr(T),
+                               float(Ts), _ptr(tokens), _ptr(old_logprob), _ptr(advantage), _ptr(ref_logprob),
+                               _ptr(weight), float(clip_low), float(clip_high), float(kl_coef),
+                               float(entropy_coef), _ptr(loss), _ptr(row), _ptr(lp), _ptr(ent), _ptr(g),
+                               g.stride(0) if g is not None else 0, _stream(logits)))
+    return PolicyLoss(loss, row, lp, ent, g)
+
+
+class PreferenceLoss(NamedTuple):
+    """What ``preference_loss`` returns."""
+    loss: torch.Tensor  # float32 scalar: the mean over pairs
+    pair_loss: torch.Tensor  # float32 [P]
+    reward: torch.Tensor  # float32 [2 P]: beta times each sequence's log-ratio
+    logprob: torch.Tensor  # float32 [N]
+    grad: Optional[torch.Tensor]  # [N, V] of the logits' dtype
+
+
+def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, seq_start: torch.Tensor,
+                    weight: Optional[torch.Tensor] = None, ref_logprob: Optional[torch.Tensor] = None,
+                    beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0, average: bool = False,
+                    temperature: float = 1.0, grad: Union[bool, torch.Tensor] = True) -> PreferenceLoss:
+    """The loss of preferred over rejected answers from paired log-ratios, and its
+    gradient on the logits.
+
+    The rows are the tokens of 2 P sequences one after another, the preferred answers first:
+    sequence s is rows ``seq_start[s]`` to ``seq_start[s + 1]`` (int64 [2 P + 1] on the logits'
+    device), pair p is sequences p and P + p.  A sequence's log-ratio is the sum of
+    ``weight`` times (log-probability - ``ref_logprob``) over its rows, divided by the sum of
+    the weights with ``average``.  A weight of 0 skips a row (its logits are not read)."""
+    lib = load_library()
+    N, V, stride = _rows(logits)
+    dev = logits.device
+    if seq_start.dim() != 1 or seq_start.numel() % 2 == 0:
+        raise ValueError("seq_start must have 2 P + 1 entries")
+    P = (seq_start.numel() - 1) // 2
+    _vec(seq_start, 2 * P + 1, torch.int64, dev, "seq_start")
+    _vec(tokens, N, torch.int64, dev, "tokens")
+    _vec(weight, N, torch.float32, dev, "weight")
+    _vec(ref_logprob, N, torch.float32, dev, "ref_logprob")
+    logits = logits.detach()
+    g = _grad_rows(grad, logits)
+    out = torch.empty(N + 3 * P + 1, dtype=torch.float32, device=dev)
+    lp, pair, reward, loss = out[:N], out[N:N + P], out[N + P:N + 3 * P], out[N + 3 * P]
+    nws = int(lib.tsa_preference_loss_workspace_bytes(N))
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    _check(lib.tsa_preference_loss(_ptr(logits), _DT[logits.dtype], N, V, stride, float(temperature), _ptr(tokens),
+                                   _ptr(seq_start), P, _ptr(weight), _ptr(ref_logprob), float(beta),
+                                   float(label_smoothing), float(margin), int(bool(average)), _ptr(loss),
+                                   _ptr(pair), _ptr(reward), _ptr(lp), _ptr(g),
+                                   g.stride(0) if g is not None else 0, _ptr(ws), nws, _stream(logits)))
+    return PreferenceLoss(loss, pair, reward, lp, g)
 
 
 def device_status(clear: bool = True) -> int:

@@ -143,6 +143,7 @@ const char *tsa_status_string(int status) {
     case TSA_ERR_CUDA: return "CUDA runtime error";
     case TSA_ERR_DEVICE_TIMEOUT: return "a device-side bounded wait ran out";
     case TSA_ERR_ALIGN: return "pointer not aligned to its element size";
+    case TSA_ERR_VALUE: return "a scalar parameter is out of its range or not finite";
     default: return "unknown status";
     }
 }
@@ -159,6 +160,9 @@ static int check_rows(const void *logits, int dtype, int64_t B, int64_t V, int64
 }  // extern "C"
 
 namespace tsa {
+int rows_check_args(const void *logits, int dtype, int64_t B, int64_t V, int64_t stride) {
+    return check_rows(logits, dtype, B, V, stride);
+}
 int sample_check_args(const void *logits, int dtype, int64_t B, int64_t V, int64_t stride, const int32_t *mask,
                       int64_t mstride, const float *temperature, const int32_t *top_k, const float *top_p,
                       const float *min_p, const int64_t *tokens, const float *vstar) {

@@ -53,6 +53,8 @@ bool choose_split(int64_t V, int esize, size_t slice_target, size_t slice_max, i
 // sizes) once per device; returns 0 or -1.
 int prepare_kernel(const void *fn, size_t smem, int cluster);
 
+// The checks every call makes of its rows of logits; TSA_OK or a status.
+int rows_check_args(const void *logits, int dtype, int64_t B, int64_t V, int64_t stride);
 // The argument checks of tsa_sample (everything but the workspace); returns
 // TSA_OK or the status tsa_sample would return.
 int sample_check_args(const void *logits, int dtype, int64_t B, int64_t V, int64_t stride, const int32_t *mask,
@@ -133,6 +135,47 @@ int floor_mask_launch(const void *logits, int dtype, int64_t B, int64_t V, int64
 int logprob_launch(const void *logits, int dtype, int64_t B, int64_t V, int64_t stride, const int32_t *mask,
                    int64_t mstride, const float *temperature, float temperature_s, const int64_t *index,
                    float *out, cudaStream_t st);
+// The row losses: policy (mode 0, with or without a gradient) and the sums a
+// preference loss needs (mode 1); then the preference loss's pairs and the
+// gradient of rows whose sums are known.
+struct RowLossArgs {
+    const void *logits;
+    int64_t B, V, stride;
+    const int32_t *mask;
+    int64_t mstride;
+    const float *temperature;
+    float temperature_s;
+    const int64_t *tokens;
+    const float *weight;
+    float weight_s;  // every row's weight when `weight` is NULL
+    const float *old_logprob, *advantage, *ref_logprob;
+    float clip_lo, clip_hi, kl, ent;  // the ratio's bounds, the KL and entropy coefficients
+    float *row_loss, *logprob, *entropy;
+    void *grad;
+    int64_t gstride;
+    float *row_m, *row_z, *coef;  // mode 1: a row's maximum, its sum, and the gradient's coefficient
+};
+struct PairArgs {
+    int64_t P, N;
+    const int64_t *seq_start;
+    const float *logprob, *ref_logprob, *weight;
+    float beta, smooth, margin;
+    int average;
+    float *pair_loss, *reward, *coef;
+};
+int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cudaStream_t st);
+int row_grad_launch(const RowLossArgs &args, int dtype, cudaStream_t st);
+int pair_launch(const PairArgs &args, const RowLossArgs &rows, cudaStream_t st);
+// out[0] = sum_i w_i x_i over the entries with w_i != 0 (w NULL: w_s each).
+int weighted_sum_launch(const float *x, const float *w, float w_s, int64_t n, float *out, cudaStream_t st);
+// The kernels of one element type: mode, gradient, entropy; streaming (0) or on chip (1).
+const void *row_loss_kernel_f32(int mode, bool grad, bool ent, int form);
+const void *row_loss_kernel_f16(int mode, bool grad, bool ent, int form);
+const void *row_loss_kernel_bf16(int mode, bool grad, bool ent, int form);
+const void *row_grad_kernel_f32();
+const void *row_grad_kernel_f16();
+const void *row_grad_kernel_bf16();
+
 int selftest_launch(uint32_t limit_us, cudaStream_t st);
 
 }  // namespace tsa

@@ -1,0 +1,159 @@
+// Host side of the row losses, the preference loss's pairs and the final sums.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "tsa_device.cuh"
+#include "tsa_host.h"
+#include "tsa_loss.cuh"
+
+namespace tsa {
+
+namespace {
+
+constexpr int kSumThreads = 1024;
+constexpr int kPairThreads = 256;
+
+// Block sum of doubles in a fixed order; the result on every thread.  These
+// sums are over rows, not logits (thousands of terms, not hundreds of
+// millions), so fp64 costs nothing and a sequence's log-ratio keeps the
+// differences that cancel in it.
+template <int THREADS>
+__device__ double block_sum(double v, double *sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    __syncthreads();  // sh may hold an earlier sum
+    if (lane == 0) sh[warp] = v;
+    __syncthreads();
+    double s = 0.0;
+    for (int i = 0; i < THREADS / 32; ++i) s += sh[i];
+    return s;
+}
+
+// One CTA, a fixed order: the same loss for the same rows on every call.
+__global__ void __launch_bounds__(kSumThreads) weighted_sum_kernel(const float *x, const float *w, float w_s,
+                                                                   int64_t n, float *out) {
+    __shared__ double sh[kSumThreads / 32];
+    pdl_wait_primary();
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kSumThreads) {
+        const float wi = w ? w[i] : w_s;
+        if (wi != 0.f) s += (double)wi * (double)x[i];
+    }
+    s = block_sum<kSumThreads>(s, sh);
+    if (threadIdx.x == 0) out[0] = (float)s;
+}
+
+// One CTA a pair: the two sequences' log-ratios, the pair's loss, and the
+// coefficient of each of their rows.  With h = beta (R_c - R_r) - margin,
+//     loss = (1 - eps) ln(1 + e^-h) + eps ln(1 + e^h),
+//     d loss / dh = -(1 - eps) / (1 + e^h) + eps / (1 + e^-h).
+// A row counts if its weight is not 0, its token is in the vocabulary
+// (skipped rows have Z = 1, m = 0 and log-probability 0, and the sums' pass
+// left their coefficient 0) and its log-probability is not -inf.
+__global__ void __launch_bounds__(kPairThreads) pair_kernel(PairArgs a, RowLossArgs r) {
+    __shared__ double sh[kPairThreads / 32];
+    pdl_wait_primary();
+    const int64_t p = blockIdx.x;
+    double R[2], W[2];
+    int64_t lo[2], hi[2];
+    auto counts = [&](int64_t i) {
+        const int64_t tok = r.tokens[i];
+        return (a.weight ? a.weight[i] : 1.f) != 0.f && tok >= 0 && tok < r.V && a.logprob[i] != -INFINITY &&
+               r.row_m[i] != -INFINITY;
+    };
+    for (int s = 0; s < 2; ++s) {
+        const int64_t q = p + s * a.P;
+        lo[s] = min(max(a.seq_start[q], (int64_t)0), a.N);
+        hi[s] = min(max(a.seq_start[q + 1], lo[s]), a.N);
+        double sum = 0.0, n = 0.0;
+        for (int64_t i = lo[s] + threadIdx.x; i < hi[s]; i += kPairThreads) {
+            if (!counts(i)) continue;
+            const double w = a.weight ? a.weight[i] : 1.f;
+            sum += w * ((double)a.logprob[i] - (a.ref_logprob ? (double)a.ref_logprob[i] : 0.0));
+            n += w;
+        }
+        R[s] = block_sum<kPairThreads>(sum, sh);
+        W[s] = 1.0;
+        if (a.average) {
+            n = block_sum<kPairThreads>(n, sh);
+            W[s] = n != 0.0 ? 1.0 / n : 0.0;
+            R[s] *= W[s];
+        }
+    }
+    const double h = (double)a.beta * (R[0] - R[1]) - (double)a.margin, e = (double)a.smooth;
+    const float hf = (float)h;
+    // ln(1 + e^-|h|) and the two logistic values from one exponential
+    const float q = expf(-fabsf(hf)), l1 = log1pf(q), big = 1.f / (1.f + q), small = q / (1.f + q);
+    const float plus = hf > 0.f ? big : small, minus = hf > 0.f ? small : big;  // s(h), s(-h)
+    if (threadIdx.x == 0) {
+        const float soft_m = l1 + fmaxf(-hf, 0.f), soft_p = l1 + fmaxf(hf, 0.f);
+        a.pair_loss[p] = h != h ? hf : (1.f - a.smooth) * soft_m + (a.smooth != 0.f ? a.smooth * soft_p : 0.f);
+        a.reward[p] = (float)((double)a.beta * R[0]);
+        a.reward[p + a.P] = (float)((double)a.beta * R[1]);
+    }
+    const double dh = h != h ? h : -(1.0 - e) * (double)minus + e * (double)plus;
+    for (int s = 0; s < 2; ++s) {
+        const double d = (s == 0 ? dh : -dh) * (double)a.beta / (double)a.P * W[s];
+        for (int64_t i = lo[s] + threadIdx.x; i < hi[s]; i += kPairThreads)
+            if (counts(i)) a.coef[i] = (float)(d * (double)(a.weight ? a.weight[i] : 1.f));
+    }
+}
+
+const void *loss_kernel(int dtype, int mode, bool grad, bool ent, int form) {
+    return dtype == 0 ? row_loss_kernel_f32(mode, grad, ent, form)
+                      : (dtype == 1 ? row_loss_kernel_f16(mode, grad, ent, form)
+                                    : row_loss_kernel_bf16(mode, grad, ent, form));
+}
+
+// A launch that may start its prologue while the kernel before it drains;
+// such a kernel waits for it before it touches memory.
+int launch_pdl(const void *fn, dim3 grid, int threads, void **params, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, params) == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cudaStream_t st) {
+    const void *fn = loss_kernel(dtype, mode, args.grad != nullptr, ent, 0);
+    RowLossArgs a = args;
+    void *params[] = {&a};
+    return cudaLaunchKernel(fn, dim3((unsigned)args.B), dim3(loss_detail::kStreamThreads), params, 0, st) ==
+                   cudaSuccess
+               ? 0
+               : -1;
+}
+
+int row_grad_launch(const RowLossArgs &args, int dtype, cudaStream_t st) {
+    const void *fn = dtype == 0 ? row_grad_kernel_f32() : (dtype == 1 ? row_grad_kernel_f16() : row_grad_kernel_bf16());
+    const int64_t per = (int64_t)loss_detail::kKnownThreads * loss_detail::kKnownU * (dtype == 0 ? 4 : 8);
+    const unsigned slices = (unsigned)((args.V + per - 1) / per);
+    const unsigned y = (unsigned)(args.B < 32768 ? args.B : 32768);
+    const unsigned z = (unsigned)((args.B + y - 1) / y);
+    RowLossArgs a = args;
+    void *params[] = {&a};
+    return launch_pdl(fn, dim3(slices, y, z), loss_detail::kKnownThreads, params, st);
+}
+
+int pair_launch(const PairArgs &args, const RowLossArgs &rows, cudaStream_t st) {
+    PairArgs a = args;
+    RowLossArgs r = rows;
+    void *params[] = {&a, &r};
+    return launch_pdl(reinterpret_cast<const void *>(&pair_kernel), dim3((unsigned)args.P), kPairThreads, params, st);
+}
+
+int weighted_sum_launch(const float *x, const float *w, float w_s, int64_t n, float *out, cudaStream_t st) {
+    void *params[] = {&x, &w, &w_s, &n, &out};
+    return launch_pdl(reinterpret_cast<const void *>(&weighted_sum_kernel), dim3(1), kSumThreads, params, st);
+}
+
+}  // namespace tsa
