@@ -368,6 +368,67 @@ int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t 
                         size_t workspace_bytes, void *stream);
 size_t tsa_preference_loss_workspace_bytes(int64_t N);
 
+/*
+ * adamw_step -- one AdamW step over many tensors in one call, with 32-bit or
+ * 8-bit states.  For every element, with g the gradient times *grad_scale:
+ *   m' = beta1 m + (1 - beta1) g
+ *   v' = beta2 v + (1 - beta2) g^2
+ *   p' = p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^step) m' / (sqrt(v' / (1 - beta2^step)) + eps)
+ * computed in fp32 from the unrounded m' and v'.
+ *   tensors      HOST array of `count` descriptions, read during the call; its
+ *                pointers are device pointers to contiguous elements, aligned
+ *                to their element size (16-byte aligned ones take the fastest
+ *                path); n may be 0 and may pass 2^32.  No two may overlap.
+ *   param_dtype  TSA_F32 or TSA_BF16; grad_dtype any tsa_dtype
+ *   state_bits   32: exp_avg, exp_avg_sq are float [n]; the *_exp pointers are
+ *                not used.  8: they are uint8 [n], and exp_avg_exp,
+ *                exp_avg_sq_exp uint8 [ceil(n / 256)] (all 0 for a new state).
+ *   lr, eps, weight_decay >= 0; 0 <= beta1, beta2 < 1; step >= 1 counts from 1
+ *                (TSA_ERR_VALUE)
+ *   grad_scale   device pointer to one float, or NULL for 1: the clipping or
+ *                inverse loss scale.  If it is not finite, the step changes
+ *                nothing.
+ *   seed, offset the key of the random words used in rounding; advance offset
+ *                every step
+ * bf16 parameters are rounded stochastically: an update far below half a step
+ * of the parameter still moves it in the mean.
+ * An 8-bit state holds blocks of 256 elements, each with one exponent b (the
+ * *_exp byte: the largest biased exponent in the block less 30 for exp_avg_sq
+ * and less 14 for exp_avg, at least 0).  A code c != 0 stands for the float
+ * with bits (c + 8 b) << 20, eight steps an octave: c is 1 to 255 for
+ * exp_avg_sq, 1 to 127 for exp_avg, whose bit 7 is the sign; 0 stands for 0.
+ * exp_avg is rounded to nearest (ties to even); exp_avg_sq stochastically
+ * (nearest rounding would lose every change of less than half a step, and a
+ * step of beta2 = 0.999 changes it by a thousandth), and a value above 0 never
+ * becomes 0.
+ * A non-finite gradient element makes its parameter NaN; its 8-bit states take
+ * their largest code and leave their block's exponent alone.
+ */
+typedef struct {
+    void *param;             /* [n] of param_dtype, updated */
+    const void *grad;        /* [n] of grad_dtype */
+    void *exp_avg;           /* [n], updated */
+    void *exp_avg_sq;        /* [n], updated */
+    uint8_t *exp_avg_exp;    /* [ceil(n / 256)], 8-bit states only */
+    uint8_t *exp_avg_sq_exp; /* [ceil(n / 256)], 8-bit states only */
+    int64_t n;
+} tsa_adamw_tensor;
+int tsa_adamw_step(const tsa_adamw_tensor *tensors, int64_t count, tsa_dtype param_dtype,
+                   tsa_dtype grad_dtype, int32_t state_bits, double lr, double beta1, double beta2,
+                   double eps, double weight_decay, int64_t step, const float *grad_scale, uint64_t seed,
+                   uint64_t offset, void *stream);
+
+/*
+ * adamw_state_values -- the values that 8-bit states stand for, as bf16 (which
+ * holds them exactly): for checkpoints and inspection.
+ *   tensors      as for adamw_step with state_bits 8 (param and grad unused)
+ *   exp_avg_out, exp_avg_sq_out  HOST arrays of `count` device pointers to
+ *                bf16 [n]
+ */
+int tsa_adamw_state_values(const tsa_adamw_tensor *tensors, int64_t count, void *const *exp_avg_out,
+                           void *const *exp_avg_sq_out, void *stream);
+
 /* Human-readable name of a status code. */
 const char *tsa_status_string(int status);
 

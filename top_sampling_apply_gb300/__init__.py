@@ -18,7 +18,7 @@ import torch
 from . import _build
 
 __all__ = ["apply_token_bitmask", "sample", "topk", "policy_loss", "preference_loss", "PolicyLoss",
-           "PreferenceLoss", "device_status", "max_vocab", "load_library", "TSAError"]
+           "PreferenceLoss", "AdamWPlan", "adamw_state", "adamw_plan", "adamw_step", "adamw_state_values", "device_status", "max_vocab", "load_library", "TSAError"]
 
 _DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _lock = threading.Lock()
@@ -69,6 +69,9 @@ def load_library(path: Optional[str] = None):
                                             P, P, P, P, P, i64, P, sz, P]
         lib.tsa_preference_loss_workspace_bytes.argtypes = [i64]
         lib.tsa_preference_loss_workspace_bytes.restype = sz
+        f64 = ctypes.c_double
+        lib.tsa_adamw_step.argtypes = [P, i64, ci, ci, i32, f64, f64, f64, f64, f64, i64, P, u64, u64, P]
+        lib.tsa_adamw_state_values.argtypes = [P, i64, P, P, P]
         lib.tsa_sample_workspace_bytes.argtypes = [i64, i64, ci]
         lib.tsa_sample_workspace_bytes.restype = sz
         lib.tsa_topk_workspace_bytes.argtypes = [i64, i64, i32, ci]
@@ -81,7 +84,8 @@ def load_library(path: Optional[str] = None):
         lib.tsa_max_vocab.restype = i64
         for fn in ("tsa_apply_token_bitmask", "tsa_sample", "tsa_sample_noalloc", "tsa_topk",
                    "tsa_sample_icdf", "tsa_bitmask_from_allowed", "tsa_sample_sequential", "tsa_lm_head_topk",
-                   "tsa_policy_loss", "tsa_preference_loss",
+                   "tsa_policy_loss", "tsa_preference_loss", "tsa_adamw_step",
+                   "tsa_adamw_state_values",
                    "tsa_device_status", "tsa_selftest_wait_timeout"):
             getattr(lib, fn).restype = ci
         _lib = lib
@@ -486,6 +490,122 @@ def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, seq_start: torch
                                    _ptr(pair), _ptr(reward), _ptr(lp), _ptr(g),
                                    g.stride(0) if g is not None else 0, _ptr(ws), nws, _stream(logits)))
     return PreferenceLoss(loss, pair, reward, lp, g)
+
+
+class _AdamTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_exp", ctypes.c_void_p),
+                ("exp_avg_sq_exp", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class AdamWPlan:
+    """A list of parameters with their gradients and states, laid out once for
+    ``adamw_step``.  It holds the tensors; a gradient that becomes another tensor needs a new
+    plan (zero gradients in place between steps)."""
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, exp_avg_exp, exp_avg_sq_exp, bits):
+        self.params, self.grads = params, grads
+        self.exp_avg, self.exp_avg_sq = exp_avg, exp_avg_sq
+        self.exp_avg_exp, self.exp_avg_sq_exp = exp_avg_exp, exp_avg_sq_exp
+        self.bits = bits
+        self.device = params[0].device if params else torch.device("cuda")
+        self.param_dtype = params[0].dtype if params else torch.float32
+        self.grad_dtype = grads[0].dtype if grads else torch.float32
+        self._table = (_AdamTensor * max(1, len(params)))()
+        for i, p in enumerate(params):
+            t = self._table[i]
+            t.param, t.grad, t.n = p.data_ptr(), grads[i].data_ptr(), p.numel()
+            t.exp_avg, t.exp_avg_sq = exp_avg[i].data_ptr(), exp_avg_sq[i].data_ptr()
+            if bits == 8:
+                t.exp_avg_exp, t.exp_avg_sq_exp = exp_avg_exp[i].data_ptr(), exp_avg_sq_exp[i].data_ptr()
+
+
+def adamw_state(params, bits: int = 32):
+    """Zero states for ``adamw_plan``: lists (exp_avg, exp_avg_sq, exp_avg_exp, exp_avg_sq_exp);
+    float32 and None, None for 32 bits, uint8 codes and a uint8 exponent a block of 256 for 8."""
+    if bits not in (8, 32):
+        raise ValueError("bits must be 8 or 32")
+    dt = torch.float32 if bits == 32 else torch.uint8
+    m, v = ([torch.zeros(p.shape, dtype=dt, device=p.device) for p in params] for _ in range(2))
+    if bits == 32:
+        return m, v, None, None
+    me, ve = ([torch.zeros((p.numel() + 255) // 256, dtype=torch.uint8, device=p.device) for p in params]
+              for _ in range(2))
+    return m, v, me, ve
+
+
+def adamw_plan(params, grads, exp_avg, exp_avg_sq, exp_avg_exp=None, exp_avg_sq_exp=None) -> AdamWPlan:
+    """Checks and lays out the tensors of ``adamw_step``: contiguous CUDA tensors, parameters
+    float32 or bfloat16, gradients float32, float16 or bfloat16, states float32 or uint8 with a
+    uint8 exponent a block of 256 (see ``adamw_state``)."""
+    params, grads, exp_avg, exp_avg_sq = list(params), list(grads), list(exp_avg), list(exp_avg_sq)
+    n = len(params)
+    bits = 8 if exp_avg and exp_avg[0].dtype == torch.uint8 else 32
+    lists = [("params", params), ("grads", grads), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)]
+    if bits == 8:
+        if exp_avg_exp is None or exp_avg_sq_exp is None:
+            raise ValueError("8-bit states need exp_avg_exp and exp_avg_sq_exp")
+        exp_avg_exp, exp_avg_sq_exp = list(exp_avg_exp), list(exp_avg_sq_exp)
+        lists += [("exp_avg_exp", exp_avg_exp), ("exp_avg_sq_exp", exp_avg_sq_exp)]
+    elif exp_avg_exp is not None or exp_avg_sq_exp is not None:
+        raise ValueError("32-bit states have no exponents")
+    for name, seq in lists:
+        if len(seq) != n:
+            raise ValueError("%s must have as many tensors as params" % name)
+    if n:
+        dev = params[0].device
+        dts = {"params": params[0].dtype, "grads": grads[0].dtype}
+        state = torch.uint8 if bits == 8 else torch.float32
+        if not params[0].is_cuda:
+            raise ValueError("params must be CUDA tensors")
+        if dts["params"] not in (torch.float32, torch.bfloat16) or dts["grads"] not in _DT:
+            raise ValueError("params must be float32 or bfloat16, grads float32, float16 or bfloat16")
+        for name, seq in lists:
+            dt = dts.get(name, state)
+            for i, t in enumerate(seq):
+                want = (params[i].numel() + 255) // 256 if name.endswith("_exp") else params[i].numel()
+                if t.device != dev or t.dtype != dt or not t.is_contiguous() or t.numel() != want:
+                    raise ValueError("%s[%d] must be a contiguous %s tensor of %d elements on %s"
+                                     % (name, i, dt, want, dev))
+    return AdamWPlan(params, grads, exp_avg, exp_avg_sq, exp_avg_exp, exp_avg_sq_exp, bits)
+
+
+def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.01, grad_scale: Optional[torch.Tensor] = None, seed: int = 0,
+               offset: int = 0) -> None:
+    """One AdamW step over every tensor of the plan, in place.
+
+    ``step`` counts from 1 (bias correction).  ``grad_scale``: a float32 [1] tensor that
+    multiplies the gradients; a value that is not finite skips the step.  ``seed``, ``offset``
+    key the random rounding of bf16 parameters and 8-bit second moments; advance ``offset``
+    every step."""
+    lib = load_library()
+    _vec(grad_scale, 1, torch.float32, plan.device, "grad_scale")
+    _check(lib.tsa_adamw_step(plan._table, len(plan.params), _DT[plan.param_dtype], _DT[plan.grad_dtype], plan.bits,
+                              float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), int(step),
+                              _ptr(grad_scale), int(seed) & 0xFFFFFFFFFFFFFFFF, int(offset) & 0xFFFFFFFFFFFFFFFF,
+                              torch.cuda.current_stream(plan.device).cuda_stream))
+
+
+def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
+    """The values that a plan's 8-bit states stand for, as lists of bfloat16 tensors (which hold
+    them exactly): (exp_avg, exp_avg_sq), for checkpoints and inspection."""
+    lib = load_library()
+    if plan.bits != 8:
+        raise ValueError("32-bit states are their own values")
+    outs = []
+    for given, like in ((exp_avg_out, plan.exp_avg), (exp_avg_sq_out, plan.exp_avg_sq)):
+        given = [torch.empty(t.shape, dtype=torch.bfloat16, device=t.device) for t in like] if given is None \
+            else list(given)
+        if len(given) != len(like) or any(g.dtype != torch.bfloat16 or g.device != t.device
+                                          or g.numel() != t.numel() or not g.is_contiguous()
+                                          for g, t in zip(given, like)):
+            raise ValueError("outputs must be contiguous bfloat16 tensors of the states' sizes")
+        outs.append(given)
+    ptrs = [(ctypes.c_void_p * max(1, len(o)))(*[t.data_ptr() for t in o]) for o in outs]
+    _check(lib.tsa_adamw_state_values(plan._table, len(plan.params), ptrs[0], ptrs[1],
+                                      torch.cuda.current_stream(plan.device).cuda_stream))
+    return outs[0], outs[1]
 
 
 def device_status(clear: bool = True) -> int:

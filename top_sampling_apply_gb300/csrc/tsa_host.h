@@ -176,6 +176,26 @@ const void *row_grad_kernel_f32();
 const void *row_grad_kernel_f16();
 const void *row_grad_kernel_bf16();
 
+// AdamW over many tensors: one tensor's pointers, and the step's numbers.
+struct AdamTensor {
+    void *param;
+    const void *grad;
+    void *m, *v;
+    uint8_t *me, *ve;
+    int64_t n;
+};
+struct AdamArgs {
+    float b1, b1c, b2, b2c;        // the two decay rates and one less each
+    float keep, rate, rsc2, eps;   // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t), eps
+    const float *scale;
+    uint64_t seed, offset;
+    uint32_t first;                // list index of the launch's first tensor (its random row)
+};
+int adamw_launch(const AdamTensor *tensors, int64_t count, int param_dtype, int grad_dtype, int bits,
+                 const AdamArgs &args, cudaStream_t st);
+// param, grad: the bf16 outputs of m and v
+int adamw_values_launch(const AdamTensor *tensors, int64_t count, cudaStream_t st);
+
 int selftest_launch(uint32_t limit_us, cudaStream_t st);
 
 }  // namespace tsa

@@ -1,10 +1,13 @@
 // C-ABI entry points of the training-side calls: argument checks and launches.
 #include <cuda_runtime.h>
 #include <math.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "../../include/tsa.h"
 #include "tsa_host.h"
+
+#include <new>
 
 using namespace tsa;
 
@@ -23,6 +26,27 @@ int check_grad(const void *logits, const void *grad, int dtype, int64_t B, int64
     if (!aligned(grad, es)) return TSA_ERR_ALIGN;
     if (grad == logits && gstride != stride) return TSA_ERR_SHAPE;
     (void)B;
+    return TSA_OK;
+}
+
+static_assert(sizeof(AdamTensor) == sizeof(tsa_adamw_tensor) && offsetof(AdamTensor, n) == offsetof(tsa_adamw_tensor, n),
+              "the C description of a tensor is passed to the kernels as it is");
+
+// The pointers of a list of tensors: present and aligned where n > 0.
+int check_tensors(const tsa_adamw_tensor *t, int64_t count, size_t ps, size_t gs, int bits, bool step) {
+    if (count < 0 || count > 0x7FFFFFFFll) return TSA_ERR_SHAPE;
+    if (count > 0 && !t) return TSA_ERR_NULL;
+    for (int64_t i = 0; i < count; ++i) {
+        // one random word an element from a 32-bit counter of groups of four
+        if (t[i].n < 0 || t[i].n > (1ll << 34)) return TSA_ERR_SHAPE;
+        if (t[i].n == 0) continue;
+        if ((step && (!t[i].param || !t[i].grad)) || !t[i].exp_avg || !t[i].exp_avg_sq ||
+            (bits == 8 && (!t[i].exp_avg_exp || !t[i].exp_avg_sq_exp)))
+            return TSA_ERR_NULL;
+        if ((step && (!aligned(t[i].param, ps) || !aligned(t[i].grad, gs))) ||
+            (bits == 32 && (!aligned(t[i].exp_avg, 4) || !aligned(t[i].exp_avg_sq, 4))))
+            return TSA_ERR_ALIGN;
+    }
     return TSA_OK;
 }
 
@@ -152,6 +176,62 @@ int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t 
     a.grad = grad_out;
     a.gstride = grad_row_stride;
     return row_grad_launch(a, dtype, s) == 0 ? TSA_OK : TSA_ERR_CUDA;
+}
+
+int tsa_adamw_step(const tsa_adamw_tensor *tensors, int64_t count, tsa_dtype param_dtype, tsa_dtype grad_dtype,
+                   int32_t state_bits, double lr, double beta1, double beta2, double eps, double weight_decay,
+                   int64_t step, const float *grad_scale, uint64_t seed, uint64_t offset, void *stream) {
+    if ((param_dtype != TSA_F32 && param_dtype != TSA_BF16) ||
+        (grad_dtype != TSA_F32 && grad_dtype != TSA_F16 && grad_dtype != TSA_BF16))
+        return TSA_ERR_DTYPE;
+    if ((state_bits != 8 && state_bits != 32) || step < 1 || !(lr >= 0.0) || !isfinite(lr) || !(eps >= 0.0) ||
+        !isfinite(eps) || !(weight_decay >= 0.0) || !isfinite(weight_decay) || !(beta1 >= 0.0 && beta1 < 1.0) ||
+        !(beta2 >= 0.0 && beta2 < 1.0))
+        return TSA_ERR_VALUE;
+    const int st = check_tensors(tensors, count, param_dtype == TSA_F32 ? 4 : 2, grad_dtype == TSA_F32 ? 4 : 2,
+                                 state_bits, true);
+    if (st != TSA_OK) return st;
+    if (!aligned(grad_scale, 4)) return TSA_ERR_ALIGN;
+    if (count == 0) return TSA_OK;
+    AdamArgs a = {};
+    a.b1 = (float)beta1;
+    a.b1c = (float)(1.0 - beta1);
+    a.b2 = (float)beta2;
+    a.b2c = (float)(1.0 - beta2);
+    a.keep = (float)(1.0 - lr * weight_decay);
+    a.rate = (float)(lr / (1.0 - pow(beta1, (double)step)));
+    a.rsc2 = (float)(1.0 / sqrt(1.0 - pow(beta2, (double)step)));
+    a.eps = (float)eps;
+    a.scale = grad_scale;
+    a.seed = seed;
+    a.offset = offset;
+    return adamw_launch(reinterpret_cast<const AdamTensor *>(tensors), count, param_dtype, grad_dtype, state_bits, a,
+                        (cudaStream_t)stream) == 0
+               ? TSA_OK
+               : TSA_ERR_CUDA;
+}
+
+int tsa_adamw_state_values(const tsa_adamw_tensor *tensors, int64_t count, void *const *exp_avg_out,
+                           void *const *exp_avg_sq_out, void *stream) {
+    const int st = check_tensors(tensors, count, 1, 1, 8, false);
+    if (st != TSA_OK) return st;
+    if (count == 0) return TSA_OK;
+    if (!exp_avg_out || !exp_avg_sq_out) return TSA_ERR_NULL;
+    for (int64_t i = 0; i < count; ++i) {
+        if (tensors[i].n == 0) continue;
+        if (!exp_avg_out[i] || !exp_avg_sq_out[i]) return TSA_ERR_NULL;
+        if (!aligned(exp_avg_out[i], 2) || !aligned(exp_avg_sq_out[i], 2)) return TSA_ERR_ALIGN;
+    }
+    AdamTensor *list = new (std::nothrow) AdamTensor[(size_t)count];
+    if (!list) return TSA_ERR_CUDA;
+    for (int64_t i = 0; i < count; ++i) {
+        list[i] = reinterpret_cast<const AdamTensor *>(tensors)[i];
+        list[i].param = exp_avg_out[i];
+        list[i].grad = exp_avg_sq_out[i];
+    }
+    const int r = adamw_values_launch(list, count, (cudaStream_t)stream);
+    delete[] list;
+    return r == 0 ? TSA_OK : TSA_ERR_CUDA;
 }
 
 }  // extern "C"
