@@ -429,6 +429,33 @@ int tsa_adamw_step(const tsa_adamw_tensor *tensors, int64_t count, tsa_dtype par
 int tsa_adamw_state_values(const tsa_adamw_tensor *tensors, int64_t count, void *const *exp_avg_out,
                            void *const *exp_avg_sq_out, void *stream);
 
+/*
+ * lm_head_logprob -- selective_log_softmax of scores that are never written:
+ * with z = hidden . weight^T (+ bias), capped to softcap tanh(z / softcap)
+ * where softcap > 0, out[m] = ln softmax(z[m] / T over the allowed
+ * tokens)[tokens[m]].  The log-probabilities of sampled tokens under a rollout
+ * or reference policy, which policy_loss and preference_loss take as inputs.
+ *   hidden       bf16 [M, hidden_row_stride], M >= 0
+ *   weight       bf16 [V, weight_row_stride]; H a multiple of 8, 8 <= H <=
+ *                16384; both row strides multiples of 8 elements and both
+ *                bases 16-byte aligned (TSA_ERR_ALIGN)
+ *   bias         float [V] or NULL; softcap >= 0, finite (0: none)
+ *   bitmask, mask_row_stride, temperature, temperature_s: as for
+ *                selective_log_softmax, one row for each hidden row
+ *   tokens       [M] int64; out [M] float, with selective_log_softmax's special
+ *                values (-inf for a disallowed token; NaN for a token outside
+ *                [0, V) or a row with no allowed finite score)
+ *   workspace    at least tsa_lm_head_logprob_workspace_bytes(M, V) bytes,
+ *                256-byte aligned
+ * bf16 products, fp32 sums.  The weight is read once for up to 8192 rows.
+ */
+int tsa_lm_head_logprob(const void *hidden, int64_t M, int64_t H, int64_t hidden_row_stride,
+                        const void *weight, int64_t V, int64_t weight_row_stride, const float *bias,
+                        float softcap, const int32_t *bitmask, int64_t mask_row_stride,
+                        const float *temperature, float temperature_s, const int64_t *tokens, float *out,
+                        void *workspace, size_t workspace_bytes, void *stream);
+size_t tsa_lm_head_logprob_workspace_bytes(int64_t M, int64_t V);
+
 /* Human-readable name of a status code. */
 const char *tsa_status_string(int status);
 

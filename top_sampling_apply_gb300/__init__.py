@@ -18,7 +18,7 @@ import torch
 from . import _build
 
 __all__ = ["apply_token_bitmask", "sample", "topk", "policy_loss", "preference_loss", "PolicyLoss",
-           "PreferenceLoss", "AdamWPlan", "adamw_state", "adamw_plan", "adamw_step", "adamw_state_values", "device_status", "max_vocab", "load_library", "TSAError"]
+           "PreferenceLoss", "lm_head_logprob", "AdamWPlan", "adamw_state", "adamw_plan", "adamw_step", "adamw_state_values", "device_status", "max_vocab", "load_library", "TSAError"]
 
 _DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _lock = threading.Lock()
@@ -69,6 +69,9 @@ def load_library(path: Optional[str] = None):
                                             P, P, P, P, P, i64, P, sz, P]
         lib.tsa_preference_loss_workspace_bytes.argtypes = [i64]
         lib.tsa_preference_loss_workspace_bytes.restype = sz
+        lib.tsa_lm_head_logprob.argtypes = [P, i64, i64, i64, P, i64, i64, P, f32, P, i64, P, f32, P, P, P, sz, P]
+        lib.tsa_lm_head_logprob_workspace_bytes.argtypes = [i64, i64]
+        lib.tsa_lm_head_logprob_workspace_bytes.restype = sz
         f64 = ctypes.c_double
         lib.tsa_adamw_step.argtypes = [P, i64, ci, ci, i32, f64, f64, f64, f64, f64, i64, P, u64, u64, P]
         lib.tsa_adamw_state_values.argtypes = [P, i64, P, P, P]
@@ -84,7 +87,7 @@ def load_library(path: Optional[str] = None):
         lib.tsa_max_vocab.restype = i64
         for fn in ("tsa_apply_token_bitmask", "tsa_sample", "tsa_sample_noalloc", "tsa_topk",
                    "tsa_sample_icdf", "tsa_bitmask_from_allowed", "tsa_sample_sequential", "tsa_lm_head_topk",
-                   "tsa_policy_loss", "tsa_preference_loss", "tsa_adamw_step",
+                   "tsa_policy_loss", "tsa_preference_loss", "tsa_lm_head_logprob", "tsa_adamw_step",
                    "tsa_adamw_state_values",
                    "tsa_device_status", "tsa_selftest_wait_timeout"):
             getattr(lib, fn).restype = ci
@@ -490,6 +493,37 @@ def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, seq_start: torch
                                    _ptr(pair), _ptr(reward), _ptr(lp), _ptr(g),
                                    g.stride(0) if g is not None else 0, _ptr(ws), nws, _stream(logits)))
     return PreferenceLoss(loss, pair, reward, lp, g)
+
+
+def lm_head_logprob(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.Tensor,
+                    bias: Optional[torch.Tensor] = None, softcap: float = 0.0, temperature: Param = 1.0,
+                    bitmask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``selective_log_softmax`` of hidden @ weight^T (+ bias, capped to softcap tanh(z /
+    softcap) where softcap > 0) at ``tokens``, float32 [M], without writing the scores.
+    hidden bf16 [M, H], weight bf16 [V, H] (unit stride along H); temperature and bitmask as
+    there.  The log-probabilities under a rollout or reference policy that ``policy_loss`` and
+    ``preference_loss`` take."""
+    lib = load_library()
+    for t, name in ((hidden, "hidden"), (weight, "weight")):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 2 or t.stride(1) != 1:
+            raise ValueError("%s must be a CUDA bfloat16 2-D tensor with unit stride along H" % name)
+    M, H = hidden.shape
+    V = weight.shape[0]
+    dev = hidden.device
+    if weight.shape[1] != H or weight.device != dev:
+        raise ValueError("weight must be [V, H] on the hidden rows' device")
+    _vec(tokens, M, torch.int64, dev, "tokens")
+    _vec(bias, V, torch.float32, dev, "bias")
+    _vec(out, M, torch.float32, dev, "out")
+    T, Ts = _param(temperature, M, torch.float32, dev)
+    mstride = _mask_stride(bitmask, M, V, dev)
+    res = out if out is not None else torch.empty(M, dtype=torch.float32, device=dev)
+    nws = int(lib.tsa_lm_head_logprob_workspace_bytes(M, V))
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    _check(lib.tsa_lm_head_logprob(_ptr(hidden), M, H, hidden.stride(0), _ptr(weight), V, weight.stride(0),
+                                   _ptr(bias), float(softcap), _ptr(bitmask), mstride, _ptr(T), float(Ts),
+                                   _ptr(tokens), _ptr(res), _ptr(ws), nws, _stream(hidden)))
+    return res
 
 
 class _AdamTensor(ctypes.Structure):

@@ -196,6 +196,27 @@ int adamw_launch(const AdamTensor *tensors, int64_t count, int param_dtype, int 
 // param, grad: the bf16 outputs of m and v
 int adamw_values_launch(const AdamTensor *tensors, int64_t count, cudaStream_t st);
 
+// The log-probability of a token from the hidden rows.
+struct LmLogprobArgs {
+    const uint16_t *hidden;  // bf16 [M, hstride]
+    int64_t M, H, hstride;
+    const uint16_t *weight;  // bf16 [V, wstride]
+    int64_t V, wstride;
+    const float *bias;       // [V] or NULL
+    float cap;               // 0: none
+    const int32_t *mask;
+    int64_t mstride;
+    const float *temperature;
+    float temperature_s;
+    const int64_t *tokens;
+    float *out;
+    float2 *part;            // [parts][rows]: a part's largest score and its sum against it
+    float *tok;              // [rows]: the token's score
+};
+constexpr int64_t kLmRows = 8192;  // rows a pass over the weight takes
+int64_t lm_logprob_parts(int64_t M, int64_t V);
+int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st);
+
 int selftest_launch(uint32_t limit_us, cudaStream_t st);
 
 }  // namespace tsa

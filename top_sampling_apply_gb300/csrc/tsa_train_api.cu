@@ -234,4 +234,54 @@ int tsa_adamw_state_values(const tsa_adamw_tensor *tensors, int64_t count, void 
     return r == 0 ? TSA_OK : TSA_ERR_CUDA;
 }
 
+size_t tsa_lm_head_logprob_workspace_bytes(int64_t M, int64_t V) {
+    if (M < 1 || V < 1) return 0;
+    const int64_t rows = M < kLmRows ? M : kLmRows;
+    return align256((size_t)rows * 4) + align256((size_t)lm_logprob_parts(rows, V) * (size_t)rows * sizeof(float2));
+}
+
+int tsa_lm_head_logprob(const void *hidden, int64_t M, int64_t H, int64_t hidden_row_stride, const void *weight,
+                        int64_t V, int64_t weight_row_stride, const float *bias, float softcap,
+                        const int32_t *bitmask, int64_t mask_row_stride, const float *temperature,
+                        float temperature_s, const int64_t *tokens, float *out, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    if (M < 0 || M > 0x7FFFFFFFll || H < 8 || H > 16384 || H % 8 != 0 || V < 1 || V > tsa_max_vocab(TSA_BF16) ||
+        hidden_row_stride < H || weight_row_stride < H)
+        return TSA_ERR_SHAPE;
+    if (!(softcap >= 0.f) || !isfinite(softcap)) return TSA_ERR_VALUE;
+    if (M == 0) return TSA_OK;
+    if (!hidden || !weight || !tokens || !out) return TSA_ERR_NULL;
+    if (bitmask && mask_row_stride < (V + 31) / 32) return TSA_ERR_STRIDE;
+    if (!aligned(hidden, 16) || !aligned(weight, 16) || hidden_row_stride % 8 != 0 || weight_row_stride % 8 != 0 ||
+        !aligned(bias, 4) || !aligned(bitmask, 4) || !aligned(temperature, 4) || !aligned(tokens, 8) ||
+        !aligned(out, 4))
+        return TSA_ERR_ALIGN;
+    const size_t need = tsa_lm_head_logprob_workspace_bytes(M, V);
+    if (!workspace || workspace_bytes < need) return TSA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return TSA_ERR_ALIGN;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    for (int64_t m = 0; m < M; m += kLmRows) {  // the passes share the workspace, one after another
+        LmLogprobArgs a = {};
+        a.M = M - m < kLmRows ? M - m : kLmRows;
+        a.hidden = static_cast<const uint16_t *>(hidden) + m * hidden_row_stride;
+        a.H = H;
+        a.hstride = hidden_row_stride;
+        a.weight = static_cast<const uint16_t *>(weight);
+        a.V = V;
+        a.wstride = weight_row_stride;
+        a.bias = bias;
+        a.cap = softcap;
+        a.mask = bitmask ? bitmask + m * mask_row_stride : nullptr;
+        a.mstride = mask_row_stride;
+        a.temperature = temperature ? temperature + m : nullptr;
+        a.temperature_s = temperature_s;
+        a.tokens = tokens + m;
+        a.out = out + m;
+        a.tok = reinterpret_cast<float *>(ws);
+        a.part = reinterpret_cast<float2 *>(ws + align256((size_t)(M < kLmRows ? M : kLmRows) * 4));
+        if (lm_logprob_launch(a, (cudaStream_t)stream) != 0) return TSA_ERR_CUDA;
+    }
+    return TSA_OK;
+}
+
 }  // extern "C"
