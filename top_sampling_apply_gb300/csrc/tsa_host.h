@@ -216,6 +216,7 @@ struct LmLogprobArgs {
 constexpr int64_t kLmRows = 8192;  // rows a pass over the weight takes
 int64_t lm_logprob_parts(int64_t M, int64_t V);
 int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st);
+unsigned int *lm_logprob_status_ptr();
 
 int selftest_launch(uint32_t limit_us, cudaStream_t st);
 

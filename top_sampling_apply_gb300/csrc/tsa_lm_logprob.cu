@@ -4,6 +4,7 @@
 // without writing the scores.  A first kernel forms, for every part of the
 // vocabulary and every row, the largest score m and Z = sum exp((z - m) / T),
 // and stores the token's own score; a second one joins a row's parts.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -15,7 +16,6 @@ namespace tsa {
 namespace {
 
 constexpr float kLog2eH = 1.4426950408889634f;
-constexpr int kPlainThreads = 256, kPlainChunk = 256, kPlainRows = 4;
 
 __device__ __forceinline__ float row_temp(const LmLogprobArgs &a, int64_t row) {
     const float T = a.temperature ? __ldg(a.temperature + row) : a.temperature_s;
@@ -34,42 +34,308 @@ __device__ __forceinline__ float soft_cap(float z, float cap, float k) {
     return cap > 0.f ? cap - __fdividef(2.f * cap, 1.f + ex2_approx(z * k)) : z;
 }
 
-__global__ void __launch_bounds__(kPlainThreads) lm_logprob_plain_kernel(LmLogprobArgs a) {
-    __shared__ float2 sh[kPlainThreads / 32][kPlainRows];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t v0 = (int64_t)blockIdx.x * kPlainChunk, m0 = (int64_t)blockIdx.y * kPlainRows;
-    const float k = a.cap > 0.f ? 2.f * kLog2eH / a.cap : 0.f;
-    float2 s[kPlainRows];
-    float c2[kPlainRows];
-    for (int r = 0; r < kPlainRows; ++r) {
-        s[r] = make_float2(-INFINITY, 0.f);
-        c2[r] = m0 + r < a.M ? kLog2eH / row_temp(a, m0 + r) : 1.f;
+// ------------------------------------------------------------ tensor memory
+// tcgen05 (PTX ISA): one thread issues D[128, N] += A[128, 16] B[N, 16]^T from
+// two shared-memory tiles into tensor memory; a warp reads its 32 lanes of D.
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void mma_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void mma_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// Arrive on `bar` once every MMA this thread has issued so far is complete.
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+template <int N> struct TmemLoad;
+template <> struct TmemLoad<16> {
+    __device__ static __forceinline__ void ld(uint32_t a, uint32_t (&r)[16]) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(a)
+            : "memory");
     }
-    for (int64_t v = v0 + warp; v < v0 + kPlainChunk && v < a.V; v += kPlainThreads / 32) {
-        float d[kPlainRows] = {};
-        for (int64_t h = lane; h < a.H; h += 32) {
-            const float w = Elem<2>::load1(a.weight + v * a.wstride, h);
-            for (int r = 0; r < kPlainRows; ++r)
-                if (m0 + r < a.M) d[r] = fmaf(w, Elem<2>::load1(a.hidden + (m0 + r) * a.hstride, h), d[r]);
-        }
-        for (int r = 0; r < kPlainRows; ++r) {
-            if (m0 + r >= a.M) break;
-            float z = warp_sum_f32(d[r]);
-            if (a.bias) z += a.bias[v];
-            z = fmaxf(soft_cap(z, a.cap, k), -INFINITY);
-            if (a.mask && !(((uint32_t)a.mask[(m0 + r) * a.mstride + (v >> 5)] >> (v & 31)) & 1u)) z = -INFINITY;
-            if (lane == 0 && a.tokens[m0 + r] == v) a.tok[m0 + r] = z;
-            if (z > -INFINITY) s[r] = join(s[r], make_float2(z, 1.f), c2[r]);
-        }
+};
+template <> struct TmemLoad<32> {
+    __device__ static __forceinline__ void ld(uint32_t a, uint32_t (&r)[32]) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+              "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+              "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+            : "r"(a)
+            : "memory");
     }
-    if (lane == 0)
-        for (int r = 0; r < kPlainRows; ++r) sh[warp][r] = s[r];
+};
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// A tile of 64 bf16 columns, 128 bytes a row, as TMA writes it with the
+// 128-byte swizzle: rows follow one another, eight rows (1,024 bytes) repeat
+// the pattern, K is contiguous.  The 16 columns of step k start 32 k bytes in.
+__device__ __forceinline__ uint64_t smem_tile(const void *p) {
+    return ((uint64_t)(smem_u32(p) >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int32_t x, int32_t y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ unsigned int g_lm_logprob_status;
+
+// A bounded wait whose outcome the whole warp shares.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, &g_lm_logprob_status));
+}
+
+// ------------------------------------------------------------ the products
+// One persistent CTA an SM.  Warp 0 fetches tiles of 64 columns of H by TMA
+// into a ring of stages, warp 1 issues the products, and warps 2 to 5 reduce
+// the finished scores from one half of tensor memory while the next tile's
+// products fill the other half.
+//
+// ROWS = false (few rows): the 128 lanes of tensor memory are vocabulary
+// entries and the N columns are the hidden rows, so the weight is all that
+// moves and nothing of the products is padding but N's remainder.  A thread
+// keeps one (m, Z) a hidden row over all its CTA's tiles; one part a CTA.
+// ROWS = true: the lanes are 128 hidden rows and the columns N vocabulary
+// entries; a thread reduces its row's N scores by itself.  Tiles go through
+// the hidden rows first, so that a weight tile is fetched from HBM once and
+// from L2 by the other row blocks.  One part a tile of the vocabulary.
+constexpr int kTcThreads = 192;
+constexpr int kTcK = 64;
+
+template <int N, bool ROWS, int STAGES>
+struct TcShape {
+    static constexpr int A_BYTES = 128 * kTcK * 2, B_BYTES = N * kTcK * 2;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int SMEM = STAGES * STAGE + 1024;
+    static constexpr int COLS = 2 * N < 32 ? 32 : 2 * N;
+    // instruction descriptor: fp32 sums of bf16 products, both operands K-major, M = 128
+    static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N / 8) << 17) | (8u << 24);
+};
+
+template <int N, bool ROWS, int STAGES>
+__global__ void __launch_bounds__(kTcThreads, 1) lm_logprob_kernel(const __grid_constant__ CUtensorMap map_a,
+                                                                   const __grid_constant__ CUtensorMap map_b,
+                                                                   LmLogprobArgs a, int64_t tiles, int row_blocks) {
+    using S = TcShape<N, ROWS, STAGES>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[STAGES], empty[STAGES], done[2], drained[2], last;
+    __shared__ uint32_t tmem_slot;
+    __shared__ float2 s_part[4][ROWS ? 1 : N];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kblocks = (int)((a.H + kTcK - 1) / kTcK);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&done[i], 1);
+            mbar_init(&drained[i], 128);
+        }
+        mbar_init(&last, 1);
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc(&tmem_slot, S::COLS);
+    mma_fence_before();
     __syncthreads();
-    if (threadIdx.x < kPlainRows && m0 + threadIdx.x < a.M) {
-        float2 t = sh[0][threadIdx.x];
-        for (int w = 1; w < kPlainThreads / 32; ++w) t = join(t, sh[w][threadIdx.x], c2[threadIdx.x]);
-        a.part[(int64_t)blockIdx.x * a.M + m0 + threadIdx.x] = t;
+    mma_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const int32_t va = ROWS ? (int32_t)(t % row_blocks) * 128 : (int32_t)t * 128;
+                const int32_t vb = ROWS ? (int32_t)(t / row_blocks) * N : 0;
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const uint32_t s = it % STAGES;
+                    if (!mbar_wait_bounded(&empty[s], ((it / STAGES) & 1u) ^ 1u, &g_lm_logprob_status)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = ring + (size_t)s * S::STAGE;
+                    mbar_arrive_expect_tx(&full[s], S::STAGE);
+                    tma_tile(st, &map_a, kb * kTcK, va, &full[s]);
+                    tma_tile(st + S::A_BYTES, &map_b, kb * kTcK, vb, &full[s]);
+                }
+            }
+            // No copy may land, and no commit arrive, after the CTA is gone:
+            // wait for the last use of each stage (the copies alone if a wait
+            // above gave up).
+            const uint32_t n = it < STAGES ? it : STAGES;
+            for (uint32_t i = it - n; i < it; ++i)
+                mbar_wait_bounded(ok ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u,
+                                  &g_lm_logprob_status);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0, j = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++j) {
+                const uint32_t b = j & 1u;
+                if (!mbar_wait_bounded(&drained[b], ((j >> 1) & 1u) ^ 1u, &g_lm_logprob_status)) break;
+                mma_fence_after();
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const uint32_t s = it % STAGES;
+                    if (!mbar_wait_bounded(&full[s], (it / STAGES) & 1u, &g_lm_logprob_status)) {
+                        ok = false;
+                        break;
+                    }
+                    mma_fence_after();
+                    const uint8_t *st = ring + (size_t)s * S::STAGE;
+                    const uint64_t da = smem_tile(st), db = smem_tile(st + S::A_BYTES);
+#pragma unroll
+                    for (int k = 0; k < kTcK / 16; ++k)
+                        mma_bf16(tmem + b * N, da + 2 * k, db + 2 * k, S::IDESC, kb > 0 || k > 0);
+                    mma_commit(&empty[s]);
+                }
+                if (ok) mma_commit(&done[b]);
+            }
+            // the products are finished before tensor memory is freed
+            mma_commit(&last);
+            mbar_wait_bounded(&last, 0, &g_lm_logprob_status);
+        }
+    } else {
+        const int quarter = warp & 3;  // a warp reads the lanes of its number modulo 4
+        const uint32_t lane_at = (uint32_t)quarter << 21;
+        const float kcap = a.cap > 0.f ? 2.f * kLog2eH / a.cap : 0.f;
+        uint32_t j = 0;
+        if constexpr (ROWS) {
+            for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
+                const uint32_t b = j & 1u;
+                const int64_t row = (t % row_blocks) * 128 + quarter * 32 + lane;
+                const int64_t v0 = (t / row_blocks) * N;
+                const bool in = row < a.M;
+                const float c2 = in ? kLog2eH / row_temp(a, row) : 1.f;
+                const int64_t want = in ? __ldg(a.tokens + row) - v0 : -1;
+                const int32_t *mrow = a.mask && in ? a.mask + row * a.mstride : nullptr;
+                if (!warp_wait(&done[b], (j >> 1) & 1u)) break;
+                mma_fence_after();
+                float2 st = make_float2(-INFINITY, 0.f);
+#pragma unroll 1
+                for (int c = 0; c < N; c += 32) {
+                    const int64_t left = a.V - (v0 + c);
+                    if (left <= 0) break;
+                    uint32_t r[32];
+                    __syncwarp();
+                    TmemLoad<32>::ld(tmem + lane_at + b * N + c, r);
+                    uint32_t bits = left < 32 ? (1u << left) - 1u : 0xFFFFFFFFu;
+                    if (mrow) bits &= (uint32_t)__ldg(mrow + ((v0 + c) >> 5));
+                    tmem_wait_ld();
+                    float z[32], top = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {
+                        float x = __uint_as_float(r[q]);
+                        if (a.bias) x += left < 32 && q >= left ? 0.f : __ldg(a.bias + v0 + c + q);
+                        if (a.cap > 0.f) x = soft_cap(x, a.cap, kcap);
+                        z[q] = (bits >> q) & 1u ? fmaxf(x, -INFINITY) : -INFINITY;
+                        top = fmaxf(top, z[q]);
+                    }
+                    const int64_t w = want - c;
+                    if (w >= 0 && w < 32) {
+                        float x = -INFINITY;
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            if (q == (int)w) x = z[q];
+                        a.tok[row] = x;
+                    }
+                    if (top > -INFINITY) {
+                        if (top > st.x) st = join(st, make_float2(top, 0.f), c2);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) st.y += ex2_approx((z[q] - st.x) * c2);
+                    }
+                }
+                mma_fence_before();
+                mbar_arrive(&drained[b]);
+                if (in) a.part[(t / row_blocks) * a.M + row] = st;
+            }
+        } else {
+            float2 st[N];
+#pragma unroll
+            for (int q = 0; q < N; ++q) st[q] = make_float2(-INFINITY, 0.f);
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
+                const uint32_t b = j & 1u;
+                const int64_t w0 = t * 128 + quarter * 32, v = w0 + lane;
+                const float bias = a.bias && v < a.V ? __ldg(a.bias + v) : 0.f;
+                if (!warp_wait(&done[b], (j >> 1) & 1u)) {
+                    ok = false;
+                    break;
+                }
+                mma_fence_after();
+                uint32_t r[N];
+                TmemLoad<N>::ld(tmem + lane_at + b * N, r);
+                tmem_wait_ld();
+                mma_fence_before();
+                mbar_arrive(&drained[b]);
+#pragma unroll
+                for (int q = 0; q < N; ++q) {
+                    if (q >= a.M) break;
+                    float x = fmaxf(soft_cap(__uint_as_float(r[q]) + bias, a.cap, kcap), -INFINITY);
+                    if (v >= a.V) x = -INFINITY;
+                    if (a.mask && w0 < a.V &&
+                        !(((uint32_t)__ldg(a.mask + q * a.mstride + (w0 >> 5)) >> lane) & 1u))
+                        x = -INFINITY;
+                    if (__ldg(a.tokens + q) == v) a.tok[q] = x;
+                    if (x > -INFINITY) st[q] = join(st[q], make_float2(x, 1.f), kLog2eH / row_temp(a, q));
+                }
+            }
+            if (ok) {
+#pragma unroll
+                for (int q = 0; q < N; ++q) {
+                    if (q >= a.M) break;
+                    const float c2 = kLog2eH / row_temp(a, q);
+                    float2 x = st[q];
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) {
+                        float2 y;
+                        y.x = __shfl_xor_sync(0xFFFFFFFFu, x.x, o);
+                        y.y = __shfl_xor_sync(0xFFFFFFFFu, x.y, o);
+                        x = join(x, y, c2);
+                    }
+                    if (lane == 0) s_part[quarter][q] = x;
+                }
+            }
+        }
     }
+    __syncthreads();
+    if constexpr (!ROWS) {
+        if (threadIdx.x < N && (int64_t)threadIdx.x < a.M) {
+            const float c2 = kLog2eH / row_temp(a, threadIdx.x);
+            float2 x = s_part[0][threadIdx.x];
+            for (int w = 1; w < 4; ++w) x = join(x, s_part[w][threadIdx.x], c2);
+            a.part[(int64_t)blockIdx.x * a.M + threadIdx.x] = x;
+        }
+    }
+    if (warp == 1) tmem_free(tmem, S::COLS);
 }
 
 // A row's parts: 32 rows a CTA, 16 threads a row, then a tree over them.
@@ -102,16 +368,91 @@ __global__ void __launch_bounds__(32 * kJoinY) lm_logprob_join_kernel(LmLogprobA
 
 }  // namespace
 
-int64_t lm_logprob_parts(int64_t, int64_t V) { return (V + kPlainChunk - 1) / kPlainChunk; }
+// The row-block form needs full blocks to be worth its padding; up to 32 rows
+// are columns instead.
+constexpr int64_t kLmFew = 32;
+
+namespace {
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+    static EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) !=
+                cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            return (EncodeFn) nullptr;
+        return (EncodeFn)p;
+    }();
+    return fn;
+}
+
+// bf16 [rows, cols] with `stride` elements a row, in boxes of 64 columns.
+bool make_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t stride, int box_rows) {
+    const EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {kTcK, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+        return 152;
+    return n;
+}
+
+template <int N, bool ROWS, int STAGES>
+int launch_products(const LmLogprobArgs &args, int64_t *parts, cudaStream_t st) {
+    using S = TcShape<N, ROWS, STAGES>;
+    const void *fn = reinterpret_cast<const void *>(&lm_logprob_kernel<N, ROWS, STAGES>);
+    CUtensorMap ma, mb;
+    if (!make_map(&ma, ROWS ? args.hidden : args.weight, args.H, ROWS ? args.M : args.V,
+                  ROWS ? args.hstride : args.wstride, 128) ||
+        !make_map(&mb, ROWS ? args.weight : args.hidden, args.H, ROWS ? args.V : args.M,
+                  ROWS ? args.wstride : args.hstride, N))
+        return -1;
+    if (prepare_kernel(fn, S::SMEM, 1) != 0) return -1;
+    int row_blocks = ROWS ? (int)((args.M + 127) / 128) : 1;
+    int64_t tiles = ROWS ? row_blocks * ((args.V + N - 1) / N) : (args.V + 127) / 128;
+    const int64_t grid = tiles < sm_count() ? tiles : sm_count();
+    *parts = ROWS ? tiles / row_blocks : grid;
+    LmLogprobArgs a = args;
+    void *params[] = {&ma, &mb, &a, &tiles, &row_blocks};
+    return cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kTcThreads), params, S::SMEM, st) == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+// The most parts any form writes: a vocabulary tile of 128, or a CTA an SM.
+int64_t lm_logprob_parts(int64_t, int64_t V) {
+    const int64_t n = (V + 127) / 128;
+    return n < 256 ? 256 : n;
+}
 
 int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st) {
-    int64_t parts = lm_logprob_parts(args.M, args.V);
+    int64_t parts = 0;
+    int r;
+    if (args.M <= 16)
+        r = launch_products<16, false, 11>(args, &parts, st);
+    else if (args.M <= kLmFew)
+        r = launch_products<32, false, 10>(args, &parts, st);
+    else if (args.M <= 128)
+        r = launch_products<128, true, 6>(args, &parts, st);
+    else
+        r = launch_products<256, true, 4>(args, &parts, st);
+    if (r != 0) return -1;
     LmLogprobArgs a = args;
     void *params[] = {&a, &parts};
-    const dim3 grid((unsigned)parts, (unsigned)((a.M + kPlainRows - 1) / kPlainRows));
-    if (cudaLaunchKernel(reinterpret_cast<const void *>(&lm_logprob_plain_kernel), grid, dim3(kPlainThreads), params, 0,
-                         st) != cudaSuccess)
-        return -1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.M + 31) / 32));
     cfg.blockDim = dim3(32, kJoinY);
@@ -124,6 +465,12 @@ int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st) {
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&lm_logprob_join_kernel), params) == cudaSuccess
                ? 0
                : -1;
+}
+
+unsigned int *lm_logprob_status_ptr() {
+    void *p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_lm_logprob_status) != cudaSuccess) return nullptr;
+    return reinterpret_cast<unsigned int *>(p);
 }
 
 }  // namespace tsa
