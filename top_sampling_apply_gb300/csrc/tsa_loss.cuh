@@ -430,6 +430,210 @@ __global__ void __launch_bounds__(kStreamThreads) row_loss_stream_kernel(RowLoss
     }
 }
 
+// ------------------------------------------------------------ the row, once
+// A cluster of C CTAs holds a row in registers: 512 threads with eight 16-byte
+// vectors each are 64 KB a CTA, so that a row of 128,256 logits takes four
+// CTAs in 16 bits and eight in fp32.  Every vector is loaded once, all of a
+// thread's loads in flight together; the maximum, the sums and the gradient
+// are formed from the registers; the CTAs exchange three numbers through
+// distributed shared memory.  Two CTAs on an SM overlap one's loads with the
+// other's arithmetic and stores.
+constexpr int kRowVecs = 8, kRowThreads = 512;
+
+// Pairs of fp32 values: one instruction a pair for sums and products.
+__device__ __forceinline__ unsigned long long pair_of(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split_pair(unsigned long long r, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// e and, with an entropy, the bounded exponents of two logits.
+template <bool ENT>
+__device__ __forceinline__ void exp_pair(float a, float b, unsigned long long negm, unsigned long long c2,
+                                         unsigned long long &e, unsigned long long &y) {
+    y = mul2(add2(pair_of(a, b), negm), c2);
+    float p, q;
+    split_pair(y, p, q);
+    if (ENT) {
+        p = fmaxf(p, kLowExp);
+        q = fmaxf(q, kLowExp);
+        y = pair_of(p, q);
+    }
+    e = pair_of(ex2_approx(p), ex2_approx(q));
+}
+
+template <int DT, int MODE, bool GRAD, bool ENT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(RowLossArgs r) {
+    using E = Elem<DT>;
+    constexpr int AE = E::AE, U = kRowVecs;
+    __shared__ RowStat sh[THREADS / 32];
+    __shared__ RowStat peers[8];
+    const int tid = threadIdx.x;
+    const uint32_t C = cluster_nctarank(), rank = cluster_ctarank();
+    const int64_t row = blockIdx.x / C;
+    if (C > 1) cluster_arrive();  // a CTA's shared memory is written by others only once all have started
+    const uint8_t *rp = static_cast<const uint8_t *>(r.logits) + (size_t)row * r.stride * E::SIZE;
+    uint8_t *gp = GRAD ? static_cast<uint8_t *>(r.grad) + (size_t)row * r.gstride * E::SIZE : nullptr;
+    const int32_t *mrow = r.mask ? r.mask + (size_t)row * r.mstride : nullptr;
+    const Slice32 g = make_slice32<AE, E::SIZE>(rp, (int32_t)r.V, rank, C);
+    const bool same = GRAD && ((reinterpret_cast<uintptr_t>(rp) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0;
+    // one element of the misaligned head (first CTA) or tail (last CTA)
+    int32_t ie = -1;
+    if (rank == 0 && tid < g.head) ie = tid;
+    if (rank == C - 1 && tid >= 8 && tid - 8 < g.tail) ie = (int32_t)r.V - g.tail + (tid - 8);
+    const int32_t e_first = g.head + (g.vc0 + tid) * AE;  // this thread's first vector
+    float w;
+    int64_t tok;
+    const bool named = row_named(r, row, &w, &tok);
+    auto store_vec = [&](int u, const uint4 &x) {
+        const int32_t e0 = e_first + u * THREADS * AE;
+        if (same) {
+            __stcs(reinterpret_cast<uint4 *>(gp + (size_t)e0 * E::SIZE), x);
+        } else {
+            float f[AE];
+            E::unpack(x, f);
+#pragma unroll
+            for (int q = 0; q < AE; ++q) Pack<DT>::store1(gp, e0 + q, f[q]);  // exact: f holds type values
+        }
+    };
+    if (!named) {
+        if (rank == 0 && tid == 0) skip_row<MODE>(r, row);
+        if (GRAD) {
+#pragma unroll 1
+            for (int u = 0; u < U; ++u)
+                if (tid + u * THREADS < g.nv) store_vec(u, make_uint4(0u, 0u, 0u, 0u));
+            if (ie >= 0) Pack<DT>::store1(gp, ie, 0.f);
+        }
+        if (C > 1) cluster_wait();
+        return;
+    }
+    uint4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (tid + u * THREADS < g.nv)  // a plain load: the gradient may be written over the logits
+            x[u] = *reinterpret_cast<const uint4 *>(rp + (size_t)(e_first + u * THREADS * AE) * E::SIZE);
+    float xe = -INFINITY;
+    if (ie >= 0 && (!mrow || allowed_bit(mrow, ie))) xe = load_clean(rp, DT, ie);
+    const float T = row_temperature(r, row), c2 = kLog2eL / T;
+    const float xt = token_logit(r, rp, mrow, DT, tok);
+    // the largest logit of the thread
+    float mx = xe;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (tid + u * THREADS < g.nv) {
+            if (mrow) {
+                const int32_t e = e_first + u * THREADS * AE;
+                const uint32_t lo = (uint32_t)__ldg(mrow + (e >> 5));
+                const uint32_t hi = ((e & 31) + AE > 32) ? (uint32_t)__ldg(mrow + (e >> 5) + 1) : 0u;
+                mask_vec<DT>(x[u], __funnelshift_r(lo, hi, (uint32_t)(e & 31)) & ((1u << AE) - 1u));
+            }
+            Pack<DT>::clean(x[u]);
+            mx = fmaxf(mx, Pack<DT>::vmax(x[u]));
+        }
+    }
+    RowStat s = {mx, 0.f, 0.f};
+    if (mx > -INFINITY) {
+        const unsigned long long negm = pair_of(-mx, -mx), cc = pair_of(c2, c2);
+        unsigned long long Z = pair_of(0.f, 0.f), t = Z;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (tid + u * THREADS < g.nv) {
+                float f[AE];
+                E::unpack(x[u], f);
+#pragma unroll
+                for (int q = 0; q < AE; q += 2) {
+                    unsigned long long e, y;
+                    exp_pair<ENT>(f[q], f[q + 1], negm, cc, e, y);
+                    Z = add2(Z, e);
+                    if (ENT) t = fma2(e, y, t);
+                }
+            }
+        }
+        if (ie >= 0) {
+            unsigned long long e, y;
+            exp_pair<ENT>(xe, -INFINITY, negm, cc, e, y);
+            Z = add2(Z, e);
+            if (ENT) t = fma2(e, y, t);
+        }
+        float a, b;
+        split_pair(Z, a, b);
+        s.Z = a + b;
+        if (ENT) {
+            split_pair(t, a, b);
+            s.t = a + b;
+        }
+    }
+    stat_block(s, sh, c2, THREADS / 32);
+    if (C > 1) {
+        cluster_wait();
+        if (tid < (int)C) {
+            const uint32_t at = dsmem_addr(&peers[rank], (uint32_t)tid);
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(s.m) : "memory");
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(s.Z) : "memory");
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(s.t) : "memory");
+        }
+        cluster_sync();
+        s = peers[0];
+        for (uint32_t i = 1; i < C; ++i) s = merge(s, peers[i], c2);
+    }
+    if (s.m == INFINITY) s.Z = __int_as_float(0x7FC00000);
+    const RowScalars gs = finish_row<MODE, ENT>(r, row, s, xt, T, w, rank == 0 && tid == 0);
+    if (!GRAD) return;
+    // a row that does not count (its token masked) has a = b = 0: zeros
+    const bool live = xt > -INFINITY;
+    const GradCoef k = live ? grad_coef<ENT>(gs, s) : GradCoef{0.f, 0.f};
+    const float m = live ? s.m : 0.f;
+    const unsigned long long negm = pair_of(-m, -m), cc = pair_of(c2, c2), k1 = pair_of(k.k1, k.k1),
+                             k2 = pair_of(k.k2, k.k2);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (tid + u * THREADS < g.nv) {
+            float f[AE];
+            if (live) {
+                E::unpack(x[u], f);
+#pragma unroll
+                for (int q = 0; q < AE; q += 2) {
+                    unsigned long long e, y;
+                    exp_pair<ENT>(f[q], f[q + 1], negm, cc, e, y);
+                    split_pair(mul2(e, ENT ? fma2(k2, y, k1) : k1), f[q], f[q + 1]);
+                }
+                const int32_t at = (int32_t)tok - (e_first + u * THREADS * AE);
+                if (at >= 0 && at < AE) {
+#pragma unroll
+                    for (int q = 0; q < AE; ++q)
+                        if (q == at) f[q] = __fadd_rn(f[q], gs.a);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < AE; ++q) f[q] = 0.f;
+            }
+            store_vec(u, Pack<DT>::vec(f));
+        }
+    }
+    if (ie >= 0) {
+        float f = live ? grad_el<ENT>(xe, m, c2, k) : 0.f;
+        if (live && ie == (int32_t)tok) f = __fadd_rn(f, gs.a);
+        Pack<DT>::store1(gp, ie, f);
+    }
+}
+
 // ------------------------------------------------------------ known sums
 // The gradient of a row whose m, Z and coefficient are known:
 // coef / T (1{j = i} - p_j), element by element; grid (slices of a row, rows).
