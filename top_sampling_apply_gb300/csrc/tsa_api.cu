@@ -23,7 +23,7 @@ struct Prepared {
     int cluster16;
 };
 std::mutex g_mu;
-Prepared g_prepared[64];
+Prepared g_prepared[128];
 int g_nprepared = 0;
 
 int esize_of(int dtype) { return dtype == TSA_F32 ? 4 : 2; }
@@ -81,7 +81,7 @@ int prepare_kernel(const void *fn, size_t smem, int cluster) {
     for (int i = 0; i < g_nprepared; ++i)
         if (g_prepared[i].fn == fn && g_prepared[i].device == dev) p = &g_prepared[i];
     if (!p) {
-        if (g_nprepared == 64) return -1;
+        if (g_nprepared == 128) return -1;
         p = &g_prepared[g_nprepared++];
         p->fn = fn;
         p->device = dev;
@@ -428,14 +428,15 @@ int tsa_topk(const void *logits, tsa_dtype dtype, int64_t B, int64_t V, int64_t 
 
 int tsa_device_status(int clear) {
     if (cudaDeviceSynchronize() != cudaSuccess) return TSA_ERR_CUDA;
-    unsigned int *ptrs[8] = {sample_status_ptr(),         sample_row_status_ptr(),
+    unsigned int *ptrs[9] = {sample_status_ptr(),         sample_row_status_ptr(),
                              topk_status_ptr(),           nullptr,
                              sample_row_spec_status_ptr_f32(), sample_row_spec_status_ptr_f16(),
-                             sample_row_spec_status_ptr_bf16(), lm_logprob_status_ptr()};
+                             sample_row_spec_status_ptr_bf16(), lm_logprob_status_ptr(),
+                             row_loss_status_ptr()};
     void *p = nullptr;
     if (cudaGetSymbolAddress(&p, g_selftest_status) == cudaSuccess) ptrs[3] = (unsigned int *)p;
     unsigned int any = 0;
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 9; ++i) {
         if (!ptrs[i]) return TSA_ERR_CUDA;
         unsigned int v = 0;
         if (cudaMemcpy(&v, ptrs[i], sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return TSA_ERR_CUDA;

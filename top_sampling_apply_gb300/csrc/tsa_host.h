@@ -164,6 +164,7 @@ struct PairArgs {
     float *pair_loss, *reward, *coef;
 };
 int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cudaStream_t st);
+unsigned int *row_loss_status_ptr();
 int row_grad_launch(const RowLossArgs &args, int dtype, cudaStream_t st);
 int pair_launch(const PairArgs &args, const RowLossArgs &rows, cudaStream_t st);
 // out[0] = sum_i w_i x_i over the entries with w_i != 0 (w NULL: w_s each).

@@ -2,6 +2,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "tsa_device.cuh"
 #include "tsa_host.h"
 #include "tsa_loss.cuh"
@@ -100,6 +102,8 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(PairArgs a, RowLossA
     }
 }
 
+__device__ unsigned int g_loss_status;
+
 const void *loss_kernel(int dtype, int mode, bool grad, bool ent, int form) {
     return dtype == 0 ? row_loss_kernel_f32(mode, grad, ent, form)
                       : (dtype == 1 ? row_loss_kernel_f16(mode, grad, ent, form)
@@ -136,11 +140,41 @@ static int row_cluster(int64_t B, int64_t V, int es) {
     return C;
 }
 
+unsigned int *row_loss_status_ptr() {
+    void *p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_loss_status) != cudaSuccess) return nullptr;
+    return reinterpret_cast<unsigned int *>(p);
+}
+
+// Clusters of C CTAs that the GPU runs at once; asked once a kernel, size and
+// device.
+static int64_t resident_clusters(const void *fn, const cudaLaunchConfig_t &cfg, int C) {
+    struct Known {
+        const void *fn;
+        int device, C, n;
+    };
+    static std::mutex mu;
+    static Known known[256];
+    static int count = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < count; ++i)
+        if (known[i].fn == fn && known[i].device == dev && known[i].C == C) return known[i].n;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) return 0;
+    if (count < 256) known[count++] = Known{fn, dev, C, n};
+    return n;
+}
+
 int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cudaStream_t st) {
     const int C = row_cluster(args.B, args.V, dtype == 0 ? 4 : 2);
     const void *fn = loss_kernel(dtype, mode, args.grad != nullptr, ent, C > 0 ? 1 : 0);
     RowLossArgs a = args;
-    void *params[] = {&a};
+    int lg = C == 8 ? 3 : C >> 1;
+    unsigned int *status = row_loss_status_ptr();
+    if (!status) return -1;
+    void *params[] = {&a, &lg, &status};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(args.B * (C > 0 ? C : 1)));
     cfg.blockDim = dim3((unsigned)(C > 0 ? loss_detail::kRowThreads : loss_detail::kStreamThreads));
@@ -152,6 +186,13 @@ int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cuda
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (C > 0) cfg.dynamicSmemBytes = loss_detail::kRowSmem;
+    if (C > 0 && prepare_kernel(fn, loss_detail::kRowSmem, 1) != 0) return -1;
+    if (C > 0) {  // rows go round the clusters that run at once
+        const int64_t n = resident_clusters(fn, cfg, C);
+        if (n < 1) return -1;
+        if (args.B > n) cfg.gridDim.x = (unsigned)(n * C);
+    }
     return cudaLaunchKernelExC(&cfg, fn, params) == cudaSuccess ? 0 : -1;
 }
 

@@ -431,13 +431,20 @@ __global__ void __launch_bounds__(kStreamThreads) row_loss_stream_kernel(RowLoss
 }
 
 // ------------------------------------------------------------ the row, once
-// A cluster of C CTAs holds a row in registers: 512 threads with eight 16-byte
-// vectors each are 64 KB a CTA, so that a row of 128,256 logits takes four
-// CTAs in 16 bits and eight in fp32.  Every vector is loaded once, all of a
-// thread's loads in flight together; the maximum, the sums and the gradient
-// are formed from the registers; the CTAs exchange three numbers through
-// distributed shared memory.  Two CTAs on an SM overlap one's loads with the
-// other's arithmetic and stores.
+// A cluster of C CTAs takes a row: 512 threads with eight 16-byte vectors each
+// are 64 KB a CTA, so that a row of 128,256 logits takes four CTAs in 16 bits
+// and eight in fp32.  Clusters are persistent.  A row's share comes by one bulk
+// copy into shared memory, goes to registers at once, and the next row's copy
+// starts as soon as every warp has read it, so that HBM works while the
+// maximum, the sums and the gradient are formed from the registers.  The warps
+// send their (m, Z, t) to every CTA of the cluster (asynchronous stores that
+// count on the receiver's barrier); one warp a CTA joins them and finishes the
+// row for the others.
+//
+// The issue slots are the scarce part: reading and writing a bf16 logit at
+// 6.7 TB/s leaves 22 instructions an element.  So 16-bit maxima and the NaN
+// test work on pairs, sums and products on packed fp32 pairs, addresses are
+// one base and constants, and a row's scalars are computed by one warp.
 constexpr int kRowVecs = 8, kRowThreads = 512;
 
 // Pairs of fp32 values: one instruction a pair for sums and products.
@@ -479,159 +486,267 @@ __device__ __forceinline__ void exp_pair(float a, float b, unsigned long long ne
     e = pair_of(ex2_approx(p), ex2_approx(q));
 }
 
-template <int DT, int MODE, bool GRAD, bool ENT, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(RowLossArgs r) {
+// A CTA's share of one row: this thread's first vector's element, the CTA's
+// vectors, and its one element of the misaligned head (first CTA) or tail
+// (last CTA), -1 for none.  2^lg CTAs share the row's vectors.
+struct RowPlace {
+    int32_t first, nv, ie;
+};
+template <int DT>
+__device__ __forceinline__ RowPlace place_row(const RowLossArgs &r, int64_t row, uint32_t rank, int lg) {
     using E = Elem<DT>;
-    constexpr int AE = E::AE, U = kRowVecs;
-    __shared__ RowStat sh[THREADS / 32];
-    __shared__ RowStat peers[8];
-    const int tid = threadIdx.x;
-    const uint32_t C = cluster_nctarank(), rank = cluster_ctarank();
-    const int64_t row = blockIdx.x / C;
-    if (C > 1) cluster_arrive();  // a CTA's shared memory is written by others only once all have started
-    const uint8_t *rp = static_cast<const uint8_t *>(r.logits) + (size_t)row * r.stride * E::SIZE;
-    uint8_t *gp = GRAD ? static_cast<uint8_t *>(r.grad) + (size_t)row * r.gstride * E::SIZE : nullptr;
-    const int32_t *mrow = r.mask ? r.mask + (size_t)row * r.mstride : nullptr;
-    const Slice32 g = make_slice32<AE, E::SIZE>(rp, (int32_t)r.V, rank, C);
-    const bool same = GRAD && ((reinterpret_cast<uintptr_t>(rp) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0;
-    // one element of the misaligned head (first CTA) or tail (last CTA)
-    int32_t ie = -1;
-    if (rank == 0 && tid < g.head) ie = tid;
-    if (rank == C - 1 && tid >= 8 && tid - 8 < g.tail) ie = (int32_t)r.V - g.tail + (tid - 8);
-    const int32_t e_first = g.head + (g.vc0 + tid) * AE;  // this thread's first vector
+    const uintptr_t at = reinterpret_cast<uintptr_t>(r.logits) + (size_t)row * r.stride * E::SIZE;
+    const int32_t V = (int32_t)r.V, tid = (int32_t)threadIdx.x;
+    const int32_t head = min((int32_t)((0u - (uint32_t)at) & 15u) / E::SIZE, V);
+    const int32_t nvec = (V - head) / E::AE, tail = (V - head) & (E::AE - 1);
+    const int32_t c0 = (int32_t)((rank * (uint32_t)nvec) >> lg), c1 = (int32_t)(((rank + 1) * (uint32_t)nvec) >> lg);
+    RowPlace p;
+    p.first = head + (c0 + tid) * E::AE;
+    p.nv = c1 - c0;
+    p.ie = -1;
+    if (rank == 0 && tid < head) p.ie = tid;
+    if (rank + 1 == 1u << lg && tid >= 8 && tid - 8 < tail) p.ie = V - tail + (tid - 8);
+    return p;
+}
+// The largest of the warp's values (no NaN among them), on every lane.
+__device__ __forceinline__ float warp_max(float x) {
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(x));
+    return m;
+}
+
+__device__ __forceinline__ void send_stat(float4 *slot, uint64_t *bar, uint32_t rank, float m, float Z, float t) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %3}, [%4];" ::"r"(
+            dsmem_addr(slot, rank)),
+        "f"(m), "f"(Z), "f"(t), "r"(dsmem_addr(bar, rank))
+        : "memory");
+}
+__device__ __forceinline__ void arrive_one(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+constexpr size_t kRowSmem = (size_t)kRowThreads * kRowVecs * 16;
+
+template <int DT, int MODE, bool GRAD, bool ENT>
+__global__ void __launch_bounds__(kRowThreads, 2) row_loss_kernel(RowLossArgs r, int lg, unsigned int *status) {
+    using E = Elem<DT>;
+    constexpr int AE = E::AE, U = kRowVecs, THREADS = kRowThreads, WARPS = THREADS / 32;
+    extern __shared__ __align__(128) uint4 buf[];  // the CTA's vectors of a row, padded with -inf
+    __shared__ float4 stats[2][8 * WARPS];         // every warp of the cluster, for this row and the next
+    __shared__ uint64_t full, empty, joined[2];
+    __shared__ float4 finished;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t C = 1u << lg, rank = C > 1 ? cluster_ctarank() : 0u;
+    const int64_t step = gridDim.x >> lg;
+    int64_t row = blockIdx.x >> lg;
+    const uint4 none = DT == 0 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
+                       : DT == 1 ? make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u)
+                                 : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+    if (tid == 0) {
+        mbar_init(&full, 1);
+        mbar_init(&empty, WARPS);
+        mbar_init(&joined[0], 1);
+        mbar_init(&joined[1], 1);
+        mbar_init_fence();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) buf[tid + u * THREADS] = none;
+    fence_proxy_async_smem();
+    if (C > 1)
+        cluster_sync();  // every CTA's barriers stand before another CTA counts on them
+    else
+        __syncthreads();
+    const bool fixed = ((size_t)r.stride * E::SIZE) % 16 == 0;  // every row lies alike
+    auto logits_at = [&](int64_t b) { return static_cast<const uint8_t *>(r.logits) + (size_t)b * r.stride * E::SIZE; };
+    auto zero_row = [&](int64_t b) {
+        if (rank == 0 && tid == 0) skip_row<MODE>(r, b);
+        if (!GRAD) return;
+        const RowPlace q = place_row<DT>(r, b, rank, lg);
+        uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)b * r.gstride * E::SIZE;
+        if (((reinterpret_cast<uintptr_t>(logits_at(b)) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0) {
+            for (int v = tid; v < q.nv; v += THREADS)
+                __stcs(reinterpret_cast<uint4 *>(gp + (size_t)(q.first + (v - tid) * AE) * E::SIZE),
+                       make_uint4(0u, 0u, 0u, 0u));
+        } else {
+            for (int i = tid; i < q.nv * AE; i += THREADS) Pack<DT>::store1(gp, q.first - tid * AE + i, 0.f);
+        }
+        if (q.ie >= 0) Pack<DT>::store1(gp, q.ie, 0.f);
+    };
+    auto fetch = [&](int64_t b, const RowPlace &q) {  // by thread 0: the CTA's share of a row
+        mbar_arrive_expect_tx(&full, (uint32_t)q.nv * 16u);
+        if (q.nv > 0)
+            bulk_g2s(buf, logits_at(b) + (size_t)(q.first - tid * AE) * E::SIZE, (uint32_t)q.nv * 16u, &full);
+    };
     float w;
     int64_t tok;
-    const bool named = row_named(r, row, &w, &tok);
-    auto store_vec = [&](int u, const uint4 &x) {
-        const int32_t e0 = e_first + u * THREADS * AE;
-        if (same) {
-            __stcs(reinterpret_cast<uint4 *>(gp + (size_t)e0 * E::SIZE), x);
-        } else {
-            float f[AE];
-            E::unpack(x, f);
-#pragma unroll
-            for (int q = 0; q < AE; ++q) Pack<DT>::store1(gp, e0 + q, f[q]);  // exact: f holds type values
-        }
-    };
-    if (!named) {
-        if (rank == 0 && tid == 0) skip_row<MODE>(r, row);
-        if (GRAD) {
-#pragma unroll 1
-            for (int u = 0; u < U; ++u)
-                if (tid + u * THREADS < g.nv) store_vec(u, make_uint4(0u, 0u, 0u, 0u));
-            if (ie >= 0) Pack<DT>::store1(gp, ie, 0.f);
-        }
-        if (C > 1) cluster_wait();
-        return;
+    while (row < r.B && !row_named(r, row, &w, &tok)) {
+        zero_row(row);
+        row += step;
     }
-    uint4 x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (tid + u * THREADS < g.nv)  // a plain load: the gradient may be written over the logits
-            x[u] = *reinterpret_cast<const uint4 *>(rp + (size_t)(e_first + u * THREADS * AE) * E::SIZE);
-    float xe = -INFINITY;
-    if (ie >= 0 && (!mrow || allowed_bit(mrow, ie))) xe = load_clean(rp, DT, ie);
-    const float T = row_temperature(r, row), c2 = kLog2eL / T;
-    const float xt = token_logit(r, rp, mrow, DT, tok);
-    // the largest logit of the thread
-    float mx = xe;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (tid + u * THREADS < g.nv) {
-            if (mrow) {
-                const int32_t e = e_first + u * THREADS * AE;
-                const uint32_t lo = (uint32_t)__ldg(mrow + (e >> 5));
-                const uint32_t hi = ((e & 31) + AE > 32) ? (uint32_t)__ldg(mrow + (e >> 5) + 1) : 0u;
-                mask_vec<DT>(x[u], __funnelshift_r(lo, hi, (uint32_t)(e & 31)) & ((1u << AE) - 1u));
-            }
-            Pack<DT>::clean(x[u]);
-            mx = fmaxf(mx, Pack<DT>::vmax(x[u]));
-        }
-    }
-    RowStat s = {mx, 0.f, 0.f};
-    if (mx > -INFINITY) {
-        const unsigned long long negm = pair_of(-mx, -mx), cc = pair_of(c2, c2);
-        unsigned long long Z = pair_of(0.f, 0.f), t = Z;
+    RowPlace p = place_row<DT>(r, row < r.B ? row : 0, rank, lg);
+    if (row < r.B && tid == 0) fetch(row, p);
+    bool ok = true;  // a wait that ran out ends all waiting; the status word tells
+    for (uint32_t turn = 0; row < r.B; ++turn) {
+        const uint32_t half = turn & 1u;
+        if (tid == 0) mbar_arrive_expect_tx(&joined[half], (uint32_t)(WARPS << lg) * 16u);
+        const uint8_t *rp = logits_at(row);
+        const int32_t *mrow = r.mask ? r.mask + (size_t)row * r.mstride : nullptr;
+        const float T = row_temperature(r, row), c2 = kLog2eL / T;
+        const float xt = token_logit(r, rp, mrow, DT, tok);
+        float xe = -INFINITY;
+        if (p.ie >= 0 && (!mrow || allowed_bit(mrow, p.ie))) xe = load_clean(rp, DT, p.ie);
+        // the next row that counts
+        int64_t next = row + step, tok_next = -1;
+        float w_next = 0.f;
+        while (next < r.B && !row_named(r, next, &w_next, &tok_next)) next += step;
+        const RowPlace pn = fixed || next >= r.B ? p : place_row<DT>(r, next, rank, lg);
+        const int nu = (p.nv + THREADS - 1) / THREADS;
+
+        ok = ok && mbar_wait_bounded(&full, turn & 1u, status);
+        uint4 x[U];
+        // The token's logit belongs to the row, so it may raise a warp's
+        // reference; and a warp has then read it before it sends its sums,
+        // after which another CTA may write a gradient over it.
+        float mx = fmaxf(xe, xt);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (tid + u * THREADS < g.nv) {
-                float f[AE];
-                E::unpack(x[u], f);
+            if (u < nu) {
+                x[u] = buf[tid + u * THREADS];
+                if (mrow && tid + u * THREADS < p.nv) {
+                    const int32_t e = p.first + u * THREADS * AE;
+                    const uint32_t lo = (uint32_t)__ldg(mrow + (e >> 5));
+                    const uint32_t hi = ((e & 31) + AE > 32) ? (uint32_t)__ldg(mrow + (e >> 5) + 1) : 0u;
+                    mask_vec<DT>(x[u], __funnelshift_r(lo, hi, (uint32_t)(e & 31)) & ((1u << AE) - 1u));
+                }
+                Pack<DT>::clean(x[u]);
+                mx = fmaxf(mx, Pack<DT>::vmax(x[u]));
+            }
+        }
+        if (pn.nv < p.nv) {  // shared memory past the next row's share is padding again
+            __syncthreads();
+            if (tid < p.nv - pn.nv) buf[pn.nv + tid] = none;
+        }
+        mx = warp_max(mx);
+        if (lane == 0) arrive_one(&empty);
+        if (tid == 0) {
+            ok = ok && mbar_wait_bounded(&empty, turn & 1u, status);
+            if (next < r.B) {
+                fence_proxy_async_smem();
+                fetch(next, pn);
+            }
+        }
+        __syncwarp();
+        float sz = 0.f, st = 0.f;
+        if (mx > -INFINITY) {
+            const unsigned long long negm = pair_of(-mx, -mx), cc = pair_of(c2, c2);
+            unsigned long long Z = pair_of(0.f, 0.f), t = Z;
 #pragma unroll
-                for (int q = 0; q < AE; q += 2) {
-                    unsigned long long e, y;
-                    exp_pair<ENT>(f[q], f[q + 1], negm, cc, e, y);
-                    Z = add2(Z, e);
-                    if (ENT) t = fma2(e, y, t);
+            for (int u = 0; u < U; ++u) {
+                if (u < nu) {
+                    float f[AE];
+                    E::unpack(x[u], f);
+#pragma unroll
+                    for (int q = 0; q < AE; q += 2) {
+                        unsigned long long e, y;
+                        exp_pair<ENT>(f[q], f[q + 1], negm, cc, e, y);
+                        Z = add2(Z, e);
+                        if (ENT) t = fma2(e, y, t);
+                    }
+                }
+            }
+            if (p.ie >= 0) {
+                unsigned long long e, y;
+                exp_pair<ENT>(xe, -INFINITY, negm, cc, e, y);
+                Z = add2(Z, e);
+                if (ENT) t = fma2(e, y, t);
+            }
+            float a, b;
+            split_pair(Z, a, b);
+            sz = warp_sum_f32(a + b);
+            if (ENT) {
+                split_pair(t, a, b);
+                st = warp_sum_f32(a + b);
+            }
+        }
+        // These slots were last read two rows ago: a warp sends a row's sums
+        // only after its CTA has finished the row before, for which it had
+        // every other CTA's sums of that row.
+        if (lane < (int)C) send_stat(&stats[half][(int)rank * WARPS + warp], &joined[half], (uint32_t)lane, mx, sz, st);
+        if (warp == 0) {
+            ok = ok && mbar_wait_bounded(&joined[half], (turn >> 1) & 1u, status);
+            if (GRAD || rank == 0) {
+                const int n = WARPS << lg;
+                RowStat s = {-INFINITY, 0.f, 0.f};
+                for (int i = lane; i < n; i += 32) s.m = fmaxf(s.m, stats[half][i].x);
+                s.m = warp_max(s.m);
+                for (int i = lane; i < n; i += 32) {
+                    const float4 v = stats[half][i];
+                    const float d = v.x == s.m ? 0.f : fmaxf((v.x - s.m) * c2, kLowExp), f = ex2_approx(d);
+                    s.Z = fmaf(v.y, f, s.Z);
+                    if (ENT) s.t = fmaf(fmaf(v.y, d, v.z), f, s.t);
+                }
+                s.Z = s.m == INFINITY ? __int_as_float(0x7FC00000) : warp_sum_f32(s.Z);
+                if (ENT) s.t = warp_sum_f32(s.t);
+                const RowScalars gs = finish_row<MODE, ENT>(r, row, s, xt, T, w, rank == 0 && lane == 0);
+                if (GRAD && lane == 0) {
+                    // a row that does not count (its token masked) gets zeros
+                    const GradCoef kc = xt > -INFINITY ? grad_coef<ENT>(gs, s) : GradCoef{0.f, 0.f};
+                    finished = make_float4(kc.k1, kc.k2, gs.a, s.m);
                 }
             }
         }
-        if (ie >= 0) {
-            unsigned long long e, y;
-            exp_pair<ENT>(xe, -INFINITY, negm, cc, e, y);
-            Z = add2(Z, e);
-            if (ENT) t = fma2(e, y, t);
-        }
-        float a, b;
-        split_pair(Z, a, b);
-        s.Z = a + b;
-        if (ENT) {
-            split_pair(t, a, b);
-            s.t = a + b;
-        }
-    }
-    stat_block(s, sh, c2, THREADS / 32);
-    if (C > 1) {
-        cluster_wait();
-        if (tid < (int)C) {
-            const uint32_t at = dsmem_addr(&peers[rank], (uint32_t)tid);
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(s.m) : "memory");
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(s.Z) : "memory");
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(s.t) : "memory");
-        }
-        cluster_sync();
-        s = peers[0];
-        for (uint32_t i = 1; i < C; ++i) s = merge(s, peers[i], c2);
-    }
-    if (s.m == INFINITY) s.Z = __int_as_float(0x7FC00000);
-    const RowScalars gs = finish_row<MODE, ENT>(r, row, s, xt, T, w, rank == 0 && tid == 0);
-    if (!GRAD) return;
-    // a row that does not count (its token masked) has a = b = 0: zeros
-    const bool live = xt > -INFINITY;
-    const GradCoef k = live ? grad_coef<ENT>(gs, s) : GradCoef{0.f, 0.f};
-    const float m = live ? s.m : 0.f;
-    const unsigned long long negm = pair_of(-m, -m), cc = pair_of(c2, c2), k1 = pair_of(k.k1, k.k1),
-                             k2 = pair_of(k.k2, k.k2);
+        __syncthreads();
+        if (GRAD) {
+            const float4 fin = finished;
+            const GradCoef k = {fin.x, fin.y};
+            const float m = fin.w;
+            const bool live = xt > -INFINITY;
+            uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)row * r.gstride * E::SIZE;
+            const bool same = ((reinterpret_cast<uintptr_t>(rp) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0;
+            uint8_t *gv = gp + (size_t)p.first * E::SIZE;
+            const unsigned long long negm = pair_of(-m, -m), cc = pair_of(c2, c2), k1 = pair_of(k.k1, k.k1),
+                                     k2 = pair_of(k.k2, k.k2);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (tid + u * THREADS < g.nv) {
-            float f[AE];
+            for (int u = 0; u < U; ++u) {
+                if (u < nu) {
+                    float f[AE];
+                    E::unpack(x[u], f);
+#pragma unroll
+                    for (int q = 0; q < AE; q += 2) {
+                        unsigned long long e, y;
+                        exp_pair<ENT>(f[q], f[q + 1], negm, cc, e, y);
+                        split_pair(mul2(e, ENT ? fma2(k2, y, k1) : k1), f[q], f[q + 1]);
+                    }
+                    if (!live) {
+#pragma unroll
+                        for (int q = 0; q < AE; ++q) f[q] = 0.f;
+                    }
+                    if (tid + u * THREADS < p.nv) {
+                        if (same) {
+                            __stcs(reinterpret_cast<uint4 *>(gv) + u * THREADS, Pack<DT>::vec(f));
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < AE; ++q) Pack<DT>::store1(gv, u * THREADS * AE + q, f[q]);
+                        }
+                    }
+                }
+            }
+            if (p.ie >= 0) Pack<DT>::store1(gp, p.ie, live ? grad_el<ENT>(xe, m, c2, k) : 0.f);
             if (live) {
-                E::unpack(x[u], f);
-#pragma unroll
-                for (int q = 0; q < AE; q += 2) {
-                    unsigned long long e, y;
-                    exp_pair<ENT>(f[q], f[q + 1], negm, cc, e, y);
-                    split_pair(mul2(e, ENT ? fma2(k2, y, k1) : k1), f[q], f[q + 1]);
-                }
-                const int32_t at = (int32_t)tok - (e_first + u * THREADS * AE);
-                if (at >= 0 && at < AE) {
-#pragma unroll
-                    for (int q = 0; q < AE; ++q)
-                        if (q == at) f[q] = __fadd_rn(f[q], gs.a);
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < AE; ++q) f[q] = 0.f;
+                // the token's element once more, by the thread that wrote it
+                const int32_t rel = (int32_t)tok - (p.first - tid * AE);
+                const bool mine = p.ie == (int32_t)tok ||
+                                  (rel >= 0 && rel < p.nv * AE && (rel / AE) % THREADS == tid);
+                if (mine) Pack<DT>::store1(gp, tok, __fadd_rn(grad_el<ENT>(xt, m, c2, k), fin.z));
             }
-            store_vec(u, Pack<DT>::vec(f));
         }
+        for (row += step; row < next; row += step) zero_row(row);
+        row = next;
+        w = w_next;
+        tok = tok_next;
+        p = pn;
     }
-    if (ie >= 0) {
-        float f = live ? grad_el<ENT>(xe, m, c2, k) : 0.f;
-        if (live && ie == (int32_t)tok) f = __fadd_rn(f, gs.a);
-        Pack<DT>::store1(gp, ie, f);
-    }
+    if (C > 1) cluster_sync();  // no CTA leaves while another may still write to it
 }
 
 // ------------------------------------------------------------ known sums

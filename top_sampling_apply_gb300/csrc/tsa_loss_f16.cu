@@ -8,7 +8,7 @@ namespace {
 template <int MODE, bool GRAD, bool ENT>
 const void *pick(int form) {
     using namespace loss_detail;
-    return form == 1 ? reinterpret_cast<const void *>(&row_loss_kernel<1, MODE, GRAD, ENT, kRowThreads>)
+    return form == 1 ? reinterpret_cast<const void *>(&row_loss_kernel<1, MODE, GRAD, ENT>)
                      : reinterpret_cast<const void *>(&row_loss_stream_kernel<1, MODE, GRAD, ENT>);
 }
 
