@@ -375,11 +375,24 @@ def topk(logits: torch.Tensor, k: int):
     return values, indices
 
 
-def _vec(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, dev, name: str):
-    """Checks an optional contiguous [n] tensor and returns it."""
-    if t is not None and (t.dtype != dtype or t.device != dev or t.shape != (n,) or not t.is_contiguous()):
-        raise ValueError("%s must be a contiguous %s [%d] tensor on %s" % (name, dtype, n, dev))
-    return t
+def _vec(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, index: int, name: str):
+    """Checks an optional contiguous [n] tensor on CUDA device ``index``; its address, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 1 or t.size(0) != n or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s [%d] tensor on cuda:%d" % (name, dtype, n, index))
+    return t.data_ptr()
+
+
+def _temperature(x: Param, n: int, index: int):
+    """(address or None, scalar) of a temperature."""
+    if isinstance(x, torch.Tensor) and x.dim() > 0:
+        return _vec(x, n, torch.float32, index, "temperature"), 0.0
+    return None, float(x)
+
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _grad_rows(grad, logits: torch.Tensor) -> Optional[torch.Tensor]:
@@ -393,12 +406,14 @@ def _grad_rows(grad, logits: torch.Tensor) -> Optional[torch.Tensor]:
     if not grad:
         return None
     B, V = logits.shape
+    first = logits.data_ptr() % 16
+    if first == 0 and logits.stride(0) == V or B == 0:
+        return torch.empty((B, V), dtype=logits.dtype, device=logits.device)
     es = logits.element_size()
-    per = 16 // es
-    stride = V + (logits.stride(0) - V) % per
-    first = logits.data_ptr() % 16 // es
+    first //= es
+    stride = V + (logits.stride(0) - V) % (16 // es)
     buf = torch.empty(B * stride + first, dtype=logits.dtype, device=logits.device)
-    return buf[first:].as_strided((B, V), (stride, 1)) if B else logits.new_empty(B, V)
+    return buf[first:].as_strided((B, V), (stride, 1))
 
 
 class PolicyLoss(NamedTuple):
@@ -426,28 +441,27 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: torch.T
     ``grad``: True for a new tensor, a tensor to write (``logits`` itself for in place), or
     False for the loss alone.  There is no autograd graph: the gradient is returned, and
     ``logits.backward(r.grad)`` carries it further."""
-    lib = load_library()
+    lib = _lib or load_library()
     B, V, stride = _rows(logits)
-    dev = logits.device
-    _vec(tokens, B, torch.int64, dev, "tokens")
-    _vec(old_logprob, B, torch.float32, dev, "old_logprob")
-    _vec(advantage, B, torch.float32, dev, "advantage")
-    _vec(ref_logprob, B, torch.float32, dev, "ref_logprob")
-    _vec(weight, B, torch.float32, dev, "weight")
-    T, Ts = _param(temperature, B, torch.float32, dev)
-    mstride = _mask_stride(bitmask, B, V, dev)
-    logits = logits.detach()
+    dev = logits.get_device()
+    tok = _vec(tokens, B, torch.int64, dev, "tokens")
+    old = _vec(old_logprob, B, torch.float32, dev, "old_logprob")
+    adv = _vec(advantage, B, torch.float32, dev, "advantage")
+    ref = _vec(ref_logprob, B, torch.float32, dev, "ref_logprob")
+    wgt = _vec(weight, B, torch.float32, dev, "weight")
+    T, Ts = _temperature(temperature, B, dev)
+    mstride = 0 if bitmask is None else _mask_stride(bitmask, B, V, logits.device)
     g = _grad_rows(grad, logits)
-    n = 3 * B if return_entropy else 2 * B
-    out = torch.empty(n + 1, dtype=torch.float32, device=dev)
-    loss, row, lp = out[n], out[:B], out[B:2 * B]
-    ent = out[2 * B:n] if return_entropy else None
-    _check(lib.tsa_policy_loss(_ptr(logits), _DT[logits.dtype], B, V, stride, _ptr(bitmask), mstride, _ptr(T),
-                               float(Ts), _ptr(tokens), _ptr(old_logprob), _ptr(advantage), _ptr(ref_logprob),
-                               _ptr(weight), float(clip_low), float(clip_high), float(kl_coef),
-                               float(entropy_coef), _ptr(loss), _ptr(row), _ptr(lp), _ptr(ent), _ptr(g),
-                               g.stride(0) if g is not None else 0, _stream(logits)))
-    return PolicyLoss(loss, row, lp, ent, g)
+    loss = torch.empty((), dtype=torch.float32, device=logits.device)
+    rows = torch.empty((3 if return_entropy else 2, B), dtype=torch.float32, device=logits.device).unbind(0)
+    ent = rows[2] if return_entropy else None
+    _check(lib.tsa_policy_loss(logits.data_ptr(), _DT[logits.dtype], B, V, stride,
+                               None if bitmask is None else bitmask.data_ptr(), mstride, T, Ts, tok, old, adv, ref,
+                               wgt, clip_low, clip_high, kl_coef, entropy_coef, loss.data_ptr(),
+                               rows[0].data_ptr(), rows[1].data_ptr(), None if ent is None else ent.data_ptr(),
+                               None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
+                               _raw_stream(dev)))
+    return PolicyLoss(loss, rows[0], rows[1], ent, g)
 
 
 class PreferenceLoss(NamedTuple):
@@ -471,27 +485,27 @@ def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, seq_start: torch
     device), pair p is sequences p and P + p.  A sequence's log-ratio is the sum of
     ``weight`` times (log-probability - ``ref_logprob``) over its rows, divided by the sum of
     the weights with ``average``.  A weight of 0 skips a row (its logits are not read)."""
-    lib = load_library()
+    lib = _lib or load_library()
     N, V, stride = _rows(logits)
-    dev = logits.device
+    dev = logits.get_device()
     if seq_start.dim() != 1 or seq_start.numel() % 2 == 0:
         raise ValueError("seq_start must have 2 P + 1 entries")
-    P = (seq_start.numel() - 1) // 2
-    _vec(seq_start, 2 * P + 1, torch.int64, dev, "seq_start")
-    _vec(tokens, N, torch.int64, dev, "tokens")
-    _vec(weight, N, torch.float32, dev, "weight")
-    _vec(ref_logprob, N, torch.float32, dev, "ref_logprob")
-    logits = logits.detach()
+    P = seq_start.numel() // 2
+    start = _vec(seq_start, 2 * P + 1, torch.int64, dev, "seq_start")
+    tok = _vec(tokens, N, torch.int64, dev, "tokens")
+    wgt = _vec(weight, N, torch.float32, dev, "weight")
+    ref = _vec(ref_logprob, N, torch.float32, dev, "ref_logprob")
     g = _grad_rows(grad, logits)
-    out = torch.empty(N + 3 * P + 1, dtype=torch.float32, device=dev)
-    lp, pair, reward, loss = out[:N], out[N:N + P], out[N + P:N + 3 * P], out[N + 3 * P]
-    nws = int(lib.tsa_preference_loss_workspace_bytes(N))
-    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-    _check(lib.tsa_preference_loss(_ptr(logits), _DT[logits.dtype], N, V, stride, float(temperature), _ptr(tokens),
-                                   _ptr(seq_start), P, _ptr(weight), _ptr(ref_logprob), float(beta),
-                                   float(label_smoothing), float(margin), int(bool(average)), _ptr(loss),
-                                   _ptr(pair), _ptr(reward), _ptr(lp), _ptr(g),
-                                   g.stride(0) if g is not None else 0, _ptr(ws), nws, _stream(logits)))
+    lp = torch.empty(N, dtype=torch.float32, device=logits.device)
+    loss, pair, reward = torch.empty(3 * P + 1, dtype=torch.float32, device=logits.device).split([1, P, 2 * P])
+    loss = loss.view(())
+    nws = lib.tsa_preference_loss_workspace_bytes(N)
+    ws = torch.empty(nws, dtype=torch.uint8, device=logits.device) if nws else None
+    _check(lib.tsa_preference_loss(logits.data_ptr(), _DT[logits.dtype], N, V, stride, temperature, tok, start, P,
+                                   wgt, ref, beta, label_smoothing, margin, 1 if average else 0, loss.data_ptr(),
+                                   pair.data_ptr(), reward.data_ptr(), lp.data_ptr(),
+                                   None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
+                                   None if ws is None else ws.data_ptr(), nws, _raw_stream(dev)))
     return PreferenceLoss(loss, pair, reward, lp, g)
 
 
@@ -503,26 +517,27 @@ def lm_head_logprob(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.Te
     hidden bf16 [M, H], weight bf16 [V, H] (unit stride along H); temperature and bitmask as
     there.  The log-probabilities under a rollout or reference policy that ``policy_loss`` and
     ``preference_loss`` take."""
-    lib = load_library()
+    lib = _lib or load_library()
     for t, name in ((hidden, "hidden"), (weight, "weight")):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 2 or t.stride(1) != 1:
+        if t.dtype is not torch.bfloat16 or not t.is_cuda or t.dim() != 2 or t.stride(1) != 1:
             raise ValueError("%s must be a CUDA bfloat16 2-D tensor with unit stride along H" % name)
     M, H = hidden.shape
-    V = weight.shape[0]
-    dev = hidden.device
-    if weight.shape[1] != H or weight.device != dev:
+    V = weight.size(0)
+    dev = hidden.get_device()
+    if weight.size(1) != H or weight.get_device() != dev:
         raise ValueError("weight must be [V, H] on the hidden rows' device")
-    _vec(tokens, M, torch.int64, dev, "tokens")
-    _vec(bias, V, torch.float32, dev, "bias")
-    _vec(out, M, torch.float32, dev, "out")
-    T, Ts = _param(temperature, M, torch.float32, dev)
-    mstride = _mask_stride(bitmask, M, V, dev)
-    res = out if out is not None else torch.empty(M, dtype=torch.float32, device=dev)
-    nws = int(lib.tsa_lm_head_logprob_workspace_bytes(M, V))
-    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-    _check(lib.tsa_lm_head_logprob(_ptr(hidden), M, H, hidden.stride(0), _ptr(weight), V, weight.stride(0),
-                                   _ptr(bias), float(softcap), _ptr(bitmask), mstride, _ptr(T), float(Ts),
-                                   _ptr(tokens), _ptr(res), _ptr(ws), nws, _stream(hidden)))
+    tok = _vec(tokens, M, torch.int64, dev, "tokens")
+    b = _vec(bias, V, torch.float32, dev, "bias")
+    res = torch.empty(M, dtype=torch.float32, device=hidden.device) if out is None else out
+    to = _vec(res, M, torch.float32, dev, "out")
+    T, Ts = _temperature(temperature, M, dev)
+    mstride = 0 if bitmask is None else _mask_stride(bitmask, M, V, hidden.device)
+    nws = lib.tsa_lm_head_logprob_workspace_bytes(M, V)
+    ws = torch.empty(nws, dtype=torch.uint8, device=hidden.device) if nws else None
+    _check(lib.tsa_lm_head_logprob(hidden.data_ptr(), M, H, hidden.stride(0), weight.data_ptr(), V,
+                                   weight.stride(0), b, softcap, None if bitmask is None else bitmask.data_ptr(),
+                                   mstride, T, Ts, tok, to, None if ws is None else ws.data_ptr(), nws,
+                                   _raw_stream(dev)))
     return res
 
 
@@ -542,9 +557,8 @@ class AdamWPlan:
         self.exp_avg, self.exp_avg_sq = exp_avg, exp_avg_sq
         self.exp_avg_exp, self.exp_avg_sq_exp = exp_avg_exp, exp_avg_sq_exp
         self.bits = bits
-        self.device = params[0].device if params else torch.device("cuda")
-        self.param_dtype = params[0].dtype if params else torch.float32
-        self.grad_dtype = grads[0].dtype if grads else torch.float32
+        self.index = params[0].get_device() if params else torch.cuda.current_device()
+        self._dts = (_DT[params[0].dtype], _DT[grads[0].dtype]) if params else (0, 0)
         self._table = (_AdamTensor * max(1, len(params)))()
         for i, p in enumerate(params):
             t = self._table[i]
@@ -613,12 +627,11 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
     multiplies the gradients; a value that is not finite skips the step.  ``seed``, ``offset``
     key the random rounding of bf16 parameters and 8-bit second moments; advance ``offset``
     every step."""
-    lib = load_library()
-    _vec(grad_scale, 1, torch.float32, plan.device, "grad_scale")
-    _check(lib.tsa_adamw_step(plan._table, len(plan.params), _DT[plan.param_dtype], _DT[plan.grad_dtype], plan.bits,
-                              float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), int(step),
-                              _ptr(grad_scale), int(seed) & 0xFFFFFFFFFFFFFFFF, int(offset) & 0xFFFFFFFFFFFFFFFF,
-                              torch.cuda.current_stream(plan.device).cuda_stream))
+    lib = _lib or load_library()
+    scale = _vec(grad_scale, 1, torch.float32, plan.index, "grad_scale")
+    _check(lib.tsa_adamw_step(plan._table, len(plan.params), plan._dts[0], plan._dts[1], plan.bits, lr, beta1, beta2,
+                              eps, weight_decay, step, scale, int(seed) & 0xFFFFFFFFFFFFFFFF,
+                              int(offset) & 0xFFFFFFFFFFFFFFFF, _raw_stream(plan.index)))
 
 
 def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
@@ -638,7 +651,7 @@ def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
         outs.append(given)
     ptrs = [(ctypes.c_void_p * max(1, len(o)))(*[t.data_ptr() for t in o]) for o in outs]
     _check(lib.tsa_adamw_state_values(plan._table, len(plan.params), ptrs[0], ptrs[1],
-                                      torch.cuda.current_stream(plan.device).cuda_stream))
+                                      _raw_stream(plan.index)))
     return outs[0], outs[1]
 
 
