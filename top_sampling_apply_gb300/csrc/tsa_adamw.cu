@@ -71,34 +71,43 @@ __device__ __forceinline__ int find_tensor(const AdamTable<N> &tab, uint32_t chu
 __device__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 __device__ __forceinline__ bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
+// Eight consecutive elements as they lie in memory (whole: 16-byte aligned and
+// all there; else element by element, 0 past cnt), and as floats.
 template <int DT>
-__device__ __forceinline__ float load1(const void *base, int64_t i) {
-    if constexpr (DT == 0) return static_cast<const float *>(base)[i];
-    if constexpr (DT == 1) return __half2float(static_cast<const __half *>(base)[i]);
-    return __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[i]);
-}
-// Eight consecutive elements (k < cnt valid; the rest 0), as floats.
-template <int DT>
-__device__ __forceinline__ void load8(const void *base, int64_t i, int cnt, bool vec, float (&x)[8]) {
-    using E = Elem<DT>;
-    if (vec && cnt == 8) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + (size_t)i * E::SIZE);
-        E::unpack(__ldcs(p), x);
-        if constexpr (DT == 0) {
-            const uint4 q = __ldcs(p + 1);
-            x[4] = __uint_as_float(q.x);
-            x[5] = __uint_as_float(q.y);
-            x[6] = __uint_as_float(q.z);
-            x[7] = __uint_as_float(q.w);
+struct Eight {
+    uint4 w[DT == 0 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *base, int64_t i, int cnt, bool whole) {
+        if (whole) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + i * (DT == 0 ? 4 : 2));
+            w[0] = __ldcs(p);
+            if constexpr (DT == 0) w[1] = __ldcs(p + 1);
+            return;
         }
-        return;
-    }
+        uint32_t u[DT == 0 ? 8 : 4] = {};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = k < cnt ? load1<DT>(base, i + k) : 0.f;
-}
-__device__ __forceinline__ void store8_f32(void *base, int64_t i, int cnt, bool vec, const float (&x)[8]) {
+        for (int k = 0; k < 8; ++k) {
+            if (k >= cnt) continue;
+            if constexpr (DT == 0)
+                u[k] = static_cast<const uint32_t *>(base)[i + k];
+            else
+                u[k >> 1] |= (uint32_t)static_cast<const uint16_t *>(base)[i + k] << (16 * (k & 1));
+        }
+        w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        if constexpr (DT == 0) w[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    }
+    __device__ __forceinline__ void floats(float (&x)[8]) const {
+        Elem<DT>::unpack(w[0], x);
+        if constexpr (DT == 0) {
+            x[4] = __uint_as_float(w[1].x);
+            x[5] = __uint_as_float(w[1].y);
+            x[6] = __uint_as_float(w[1].z);
+            x[7] = __uint_as_float(w[1].w);
+        }
+    }
+};
+__device__ __forceinline__ void store8_f32(void *base, int64_t i, int cnt, bool whole, const float (&x)[8]) {
     float *p = static_cast<float *>(base) + i;
-    if (vec && cnt == 8) {
+    if (whole) {
         __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
         __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
         return;
@@ -107,16 +116,16 @@ __device__ __forceinline__ void store8_f32(void *base, int64_t i, int cnt, bool 
     for (int k = 0; k < 8; ++k)
         if (k < cnt) p[k] = x[k];
 }
-__device__ __forceinline__ uint2 load_codes(const uint8_t *base, int64_t i, int cnt, bool vec) {
-    if (vec && cnt == 8) return __ldcs(reinterpret_cast<const uint2 *>(base + i));
+__device__ __forceinline__ uint2 load_codes(const uint8_t *base, int64_t i, int cnt, bool whole) {
+    if (whole) return __ldcs(reinterpret_cast<const uint2 *>(base + i));
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         if (k < cnt) w[k >> 2] |= (uint32_t)base[i + k] << (8 * (k & 3));
     return make_uint2(w[0], w[1]);
 }
-__device__ __forceinline__ void store_codes(uint8_t *base, int64_t i, int cnt, bool vec, uint2 c) {
-    if (vec && cnt == 8) {
+__device__ __forceinline__ void store_codes(uint8_t *base, int64_t i, int cnt, bool whole, uint2 c) {
+    if (whole) {
         __stcs(reinterpret_cast<uint2 *>(base + i), c);
         return;
     }
@@ -149,110 +158,300 @@ __device__ __forceinline__ uint32_t block_base(const uint32_t (&mag)[8], uint32_
     return top > span ? top - span : 0u;
 }
 
+// ------------------------------------------------------------ 8-bit codes
+// Two ways to read and write codes.  The general one handles code 0, values
+// under a block's range and non-finite ones, element by element in integers:
+// with them alone a step takes 106 instructions an element, 70 of them on the
+// half-rate integer pipe, and that bounded it (48 million bf16 parameters: 197
+// us).  With the others it takes 57, and 108 us.
+// The other one is for a warp whose 256 elements need none of that:
+//   - exp_avg's codes from 9 on are the bytes of e4m3, so
+//     the conversion instructions read and round (to nearest, ties to even)
+//     two at once, on values scaled by a power of two;
+//   - exp_avg_sq's are taken from the upper byte of the shifted float bits.
+// A warp decides by votes, on the codes it read and on those it would write.
+
+// Any of four codes under 9, or 127 (e4m3's NaN).  Codes under 8 are subnormal
+// in e4m3, and 8 may have been rounded up from there, on a coarser grid.
+__device__ __forceinline__ bool not_e4m3(uint32_t w) {
+    const uint32_t x = w & 0x7F7F7F7Fu;
+    return ((x + 0x77777777u) & ~(x + 0x01010101u) & 0x80808080u) != 0x80808080u;
+}
+__device__ __forceinline__ bool zero_byte(uint32_t w) { return ((w - 0x01010101u) & ~w & 0x80808080u) != 0u; }
+__device__ __forceinline__ float two_to(uint32_t biased) { return __uint_as_float(biased << 23); }
+
+// A code's value is 2^(b - 120) times its e4m3 value.
+__device__ __forceinline__ void decode_m_fast(uint2 c, uint32_t b, float (&m)[8]) {
+    const float sc = two_to(b + 7u);
+    const unsigned long long s2 = pair_of(sc, sc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t lo, hi;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(h ? c.y : c.x));
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+        const float2 d = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        split_pair(mul2(pair_of(a.x, a.y), s2), m[4 * h], m[4 * h + 1]);
+        split_pair(mul2(pair_of(d.x, d.y), s2), m[4 * h + 2], m[4 * h + 3]);
+    }
+}
+__device__ __forceinline__ void decode_v_fast(uint2 c, uint32_t b, float (&v)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        v[q] = __uint_as_float(__byte_perm(q < 4 ? c.x : c.y, 0u, 0x4440u | (uint32_t)(q & 3)) * 0x100000u + (b << 23));
+}
+__device__ __forceinline__ uint2 encode_m_fast(const float (&m)[8], uint32_t b) {
+    const float sc = two_to(247u - b);
+    const unsigned long long s2 = pair_of(sc, sc);
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float a, d, e, f;
+        split_pair(mul2(pair_of(m[4 * h], m[4 * h + 1]), s2), a, d);
+        split_pair(mul2(pair_of(m[4 * h + 2], m[4 * h + 3]), s2), e, f);
+        asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+            : "=r"(w[h])
+            : "f"(a), "f"(d), "f"(e), "f"(f));
+    }
+    return make_uint2(w[0], w[1]);
+}
+// Code c is byte 3 of 16 (bits + 16 r - (8 b << 20)), for v > 0 brought up to code 1.
+__device__ __forceinline__ uint2 encode_v_fast(const float (&v)[8], uint32_t b, const uint32_t (&word)[8]) {
+    const float low = __uint_as_float((8u * b + 1u) << 20);
+    const uint32_t off = b << 27;
+    uint32_t u[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        u[q] = __float_as_uint(fmaxf(v[q], low)) * 16u + (__byte_perm(word[q], 0u, 0x4104u) - off);
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        w[h] = __byte_perm(__byte_perm(u[4 * h], u[4 * h + 1], 0x0073u), __byte_perm(u[4 * h + 2], u[4 * h + 3], 0x0073u),
+                           0x5410u);
+    return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ uint2 encode_m_any(const float (&m)[8], uint32_t b, int cnt) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const uint32_t mag = q < cnt ? __float_as_uint(m[q]) & 0x7FFFFFFFu : 0u;
+        const int32_t r = (int32_t)((mag + 0x7FFFFu + ((mag >> 20) & 1u)) >> 20) - (int32_t)(8u * b);
+        const uint32_t c = finite_bits(mag) ? (uint32_t)min(max(r, 0), 127) : 127u;
+        w[q >> 2] |= (c | (m[q] < 0.f ? 128u : 0u)) << (8 * (q & 3));
+    }
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ uint2 encode_v_any(const float (&v)[8], uint32_t b, const uint32_t (&word)[8], int cnt) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const uint32_t mag = q < cnt ? __float_as_uint(v[q]) & 0x7FFFFFFFu : 0u;
+        const int32_t r = (int32_t)((mag + ((word[q] & 0xFFFFu) << 4)) >> 20) - (int32_t)(8u * b);
+        const uint32_t c = finite_bits(mag) ? (uint32_t)min(max(r, 1), 255) : 255u;
+        w[q >> 2] |= (mag ? c : 0u) << (8 * (q & 3));
+    }
+    return make_uint2(w[0], w[1]);
+}
+// The base of a block of finite values with an element that is not (those
+// leave the base alone).
+__device__ __forceinline__ uint32_t finite_base(const float (&x)[8], uint32_t span, int cnt) {
+    uint32_t mag[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) mag[q] = q < cnt ? __float_as_uint(x[q]) & 0x7FFFFFFFu : 0u;
+    return block_base(mag, span);
+}
+
+// The step's numbers as pairs.
+struct AdamPairs {
+    unsigned long long scale, b1, b1c, b2, b2c, rsc2, eps, rate, keep;
+};
+// m, v, p of eight elements by one step.  PLAIN: v' is normal, so its root
+// needs no lower bound.
+template <bool PLAIN>
+__device__ __forceinline__ void step8(const AdamPairs &a, const float (&g)[8], float (&p)[8], float (&m)[8],
+                                      float (&v)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) {
+        const unsigned long long gs = mul2(pair_of(g[q], g[q + 1]), a.scale);
+        const unsigned long long mm = add2(mul2(a.b1, pair_of(m[q], m[q + 1])), mul2(a.b1c, gs));
+        const unsigned long long vv = add2(mul2(a.b2, pair_of(v[q], v[q + 1])), mul2(a.b2c, mul2(gs, gs)));
+        split_pair(mm, m[q], m[q + 1]);
+        split_pair(vv, v[q], v[q + 1]);
+        // The root of v' (2^-126 at least: a smaller one's root is below
+        // 2^-63 either way) and the reciprocal, each within 2^-22: the
+        // update, some thousandths of p, is within 2^-20 of itself.
+        float r0, r1, d0, d1;
+        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(PLAIN ? v[q] : fmaxf(v[q], 0x1p-126f)));
+        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(PLAIN ? v[q + 1] : fmaxf(v[q + 1], 0x1p-126f)));
+        split_pair(fma2(pair_of(r0, r1), a.rsc2, a.eps), d0, d1);
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d0));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d1));
+        split_pair(fma2(a.rate, mul2(mm, pair_of(d0, d1)), mul2(pair_of(p[q], p[q + 1]), a.keep)), p[q], p[q + 1]);
+    }
+}
+__device__ __forceinline__ void words8(const AdamArgs &a, uint32_t row, uint32_t quad, uint32_t (&word)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint4 w = token_block(a.seed, a.offset, row, quad + h);
+        word[4 * h] = w.x;
+        word[4 * h + 1] = w.y;
+        word[4 * h + 2] = w.z;
+        word[4 * h + 3] = w.w;
+    }
+}
+// Eight parameters as they are stored: fp32, or bf16 by adding 16 random bits
+// below the kept ones.  An infinity stays one; a NaN might pass through the
+// sign, so a sum over the elements looks for one.
+template <int PD>
+__device__ __forceinline__ void store_params(void *base, int64_t i, int cnt, bool whole, const float (&p)[8],
+                                             const uint32_t (&word)[8]) {
+    if constexpr (PD == 0) {
+        store8_f32(base, i, cnt, whole, p);
+    } else {
+        uint32_t w[4];
+        float s0, s1;
+        split_pair(add2(add2(pair_of(p[0], p[1]), pair_of(p[2], p[3])), add2(pair_of(p[4], p[5]), pair_of(p[6], p[7]))),
+                   s0, s1);
+        const float any = s0 + s1;
+        if (any == any) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                w[q] = __byte_perm(__float_as_uint(p[2 * q]) + (word[2 * q] >> 16),
+                                   __float_as_uint(p[2 * q + 1]) + (word[2 * q + 1] >> 16), 0x7632u);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                w[q] = bf16_stochastic(p[2 * q], word[2 * q]) | (bf16_stochastic(p[2 * q + 1], word[2 * q + 1]) << 16);
+        }
+        uint16_t *d = static_cast<uint16_t *>(base) + i;
+        if (whole) {
+            __stcs(reinterpret_cast<uint4 *>(d), make_uint4(w[0], w[1], w[2], w[3]));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < cnt) d[q] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
+        }
+    }
+}
+// The 8-bit states of eight elements, in the fast forms; false where v' (and
+// so a gradient) is not finite.
+__device__ __forceinline__ bool encode_fast(const float (&m)[8], const float (&v)[8], const uint32_t (&word)[8],
+                                            uint2 &cm, uint2 &cv, uint32_t &bm, uint32_t &bv) {
+    float tm = 0.f;
+    uint32_t tv = 0u;
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) {
+        tm = fmaxf(fmaxf(tm, fabsf(m[q])), fabsf(m[q + 1]));
+        tv = max(max(tv, __float_as_uint(v[q])), __float_as_uint(v[q + 1]));
+    }
+    tv = __reduce_max_sync(0xFFFFFFFFu, tv);
+    const uint32_t em = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tm)) >> 23;
+    if (!finite_bits(tv)) return false;
+    bm = em > 14u ? em - 14u : 0u;
+    bv = (tv >> 23) > 30u ? (tv >> 23) - 30u : 0u;
+    cm = encode_m_fast(m, bm);
+    cv = encode_v_fast(v, bv, word);
+    if (not_e4m3(cm.x) || not_e4m3(cm.y)) cm = encode_m_any(m, bm, 8);
+    return true;
+}
+
 template <int PD, int GD, int BITS, int N>
-__global__ void __launch_bounds__(kAdThreads) adamw_kernel(const __grid_constant__ AdamTable<N> tab,
+__global__ void __launch_bounds__(kAdThreads, BITS == 8 ? 4 : 1) adamw_kernel(const __grid_constant__ AdamTable<N> tab,
                                                            const __grid_constant__ AdamArgs a) {
     const float scale = a.scale ? *a.scale : 1.f;
     if (!(fabsf(scale) < INFINITY)) return;
     const int k = find_tensor(tab, blockIdx.x);
-    const AdamTensor &t = tab.t[k];
+    const AdamTensor t = tab.t[k];
     const int64_t n = t.n;
     const bool vec = aligned16(t.param) && aligned16(t.grad) &&
                      (BITS == 32 ? aligned16(t.m) && aligned16(t.v) : aligned8(t.m) && aligned8(t.v));
-    const int64_t first = (int64_t)(blockIdx.x - tab.start[k]) * tab.iters * kAdIter;
     const int lane = threadIdx.x & 31;
+    const uint32_t row = a.first + (uint32_t)k;
+    const AdamPairs c = {pair_of(scale, scale),     pair_of(a.b1, a.b1),   pair_of(a.b1c, a.b1c),
+                         pair_of(a.b2, a.b2),       pair_of(a.b2c, a.b2c), pair_of(a.rsc2, a.rsc2),
+                         pair_of(a.eps, a.eps),     pair_of(-a.rate, -a.rate), pair_of(a.keep, a.keep)};
+    // the warp's blocks of 256 elements
+    int64_t wb = (int64_t)(blockIdx.x - tab.start[k]) * tab.iters * kAdIter + (threadIdx.x >> 5) * 256;
+    int64_t end = wb + (int64_t)tab.iters * kAdIter;
+    if (end > n) end = n;
+    // Lane j holds the exponents of the warp's j-th block (at most 16), read
+    // before the first and written after the last: a byte written beside
+    // bytes that are still to be read made each read wait for the write.
+    const int64_t my_block = (wb >> 8) + (int64_t)lane * (kAdIter / 256);
+    const bool have = BITS == 8 && lane < tab.iters && my_block * 256 < n;
+    uint32_t em_all = have ? t.me[my_block] : 0u, ev_all = have ? t.ve[my_block] : 0u;
+    int turn = 0;
 #pragma unroll 1
-    for (int it = 0; it < tab.iters; ++it) {
-        // the warp's 256 elements; whole warps leave together
-        const int64_t wb = first + (int64_t)it * kAdIter + (threadIdx.x >> 5) * 256;
-        if (wb >= n) return;
+    for (; wb < end; wb += kAdIter, ++turn) {
         const int64_t i = wb + lane * kAdPer;
-        const int cnt = i >= n ? 0 : (n - i < 8 ? (int)(n - i) : 8);
+        const bool full = wb + 256 <= n, whole = vec && full;
+        const int cnt = full ? 8 : (n - i >= 8 ? 8 : (n > i ? (int)(n - i) : 0));
         float g[8], p[8], m[8], v[8];
-        load8<GD>(t.grad, i, cnt, vec, g);
-        load8<PD>(t.param, i, cnt, vec, p);
+        uint32_t word[8] = {};
+        Eight<GD> eg;
+        Eight<PD> ep;
+        eg.load(t.grad, i, cnt, whole);
+        ep.load(t.param, i, cnt, whole);
         if constexpr (BITS == 32) {
-            load8<0>(t.m, i, cnt, vec, m);
-            load8<0>(t.v, i, cnt, vec, v);
+            Eight<0> em, ev;
+            em.load(t.m, i, cnt, whole);
+            ev.load(t.v, i, cnt, whole);
+            if constexpr (PD == 2) words8(a, row, (uint32_t)(i >> 2), word);
+            eg.floats(g);
+            ep.floats(p);
+            em.floats(m);
+            ev.floats(v);
+            step8<false>(c, g, p, m, v);
+            store_params<PD>(t.param, i, cnt, whole, p, word);
+            store8_f32(t.m, i, cnt, whole, m);
+            store8_f32(t.v, i, cnt, whole, v);
         } else {
-            const uint2 cm = load_codes(static_cast<const uint8_t *>(t.m), i, cnt, vec);
-            const uint2 cv = load_codes(static_cast<const uint8_t *>(t.v), i, cnt, vec);
-            const uint32_t mb = 8u * t.me[wb >> 8], vb = 8u * t.ve[wb >> 8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                m[q] = decode_m(((q < 4 ? cm.x : cm.y) >> (8 * (q & 3))) & 255u, mb);
-                v[q] = decode_v(((q < 4 ? cv.x : cv.y) >> (8 * (q & 3))) & 255u, vb);
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const float gs = __fmul_rn(g[q], scale);
-            m[q] = __fadd_rn(__fmul_rn(a.b1, m[q]), __fmul_rn(a.b1c, gs));
-            v[q] = __fadd_rn(__fmul_rn(a.b2, v[q]), __fmul_rn(a.b2c, __fmul_rn(gs, gs)));
-            float root;
-            asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[q]));
-            // within 2^-21 of the quotient, times an update of some thousandths of p
-            const float upd = __fdividef(m[q], fmaf(root, a.rsc2, a.eps));
-            p[q] = fmaf(-a.rate, upd, p[q] * a.keep);
-        }
-        uint32_t word[8];
-        if constexpr (BITS == 8 || PD == 2) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 w = token_block(a.seed, a.offset, a.first + (uint32_t)k, (uint32_t)(i >> 2) + h);
-                word[4 * h] = w.x;
-                word[4 * h + 1] = w.y;
-                word[4 * h + 2] = w.z;
-                word[4 * h + 3] = w.w;
-            }
-        }
-        if constexpr (PD == 0) {
-            store8_f32(t.param, i, cnt, vec, p);
-        } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                w[q] = bf16_stochastic(p[2 * q], word[2 * q]) | (bf16_stochastic(p[2 * q + 1], word[2 * q + 1]) << 16);
-            uint16_t *d = static_cast<uint16_t *>(t.param) + i;
-            if (vec && cnt == 8) {
-                __stcs(reinterpret_cast<uint4 *>(d), make_uint4(w[0], w[1], w[2], w[3]));
+            uint2 cm = load_codes(static_cast<const uint8_t *>(t.m), i, cnt, whole);
+            uint2 cv = load_codes(static_cast<const uint8_t *>(t.v), i, cnt, whole);
+            uint32_t bm = __shfl_sync(0xFFFFFFFFu, em_all, turn), bv = __shfl_sync(0xFFFFFFFFu, ev_all, turn);
+            words8(a, row, (uint32_t)(i >> 2), word);  // under the loads
+            eg.floats(g);
+            ep.floats(p);
+            if (!__any_sync(0xFFFFFFFFu, not_e4m3(cm.x) || not_e4m3(cm.y))) {
+                decode_m_fast(cm, bm, m);
             } else {
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (q < cnt) d[q] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
+                for (int q = 0; q < 8; ++q) m[q] = decode_m(((q < 4 ? cm.x : cm.y) >> (8 * (q & 3))) & 255u, 8u * bm);
+            }
+            // beta2 and the base keep v' above 0 (and normal) where v is
+            bool done = false;
+            if (full && bv >= 32u && a.b2 >= 0x1p-16f &&
+                !__any_sync(0xFFFFFFFFu, zero_byte(cv.x) || zero_byte(cv.y))) {
+                decode_v_fast(cv, bv, v);
+                step8<true>(c, g, p, m, v);
+                done = encode_fast(m, v, word, cm, cv, bm, bv);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = decode_v(((q < 4 ? cv.x : cv.y) >> (8 * (q & 3))) & 255u, 8u * bv);
+                step8<false>(c, g, p, m, v);
+            }
+            if (!done) {
+                bm = finite_base(m, 14u, cnt);
+                bv = finite_base(v, 30u, cnt);
+                cm = encode_m_any(m, bm, cnt);
+                cv = encode_v_any(v, bv, word, cnt);
+            }
+            store_params<PD>(t.param, i, cnt, whole, p, word);
+            store_codes(static_cast<uint8_t *>(t.m), i, cnt, whole, cm);
+            store_codes(static_cast<uint8_t *>(t.v), i, cnt, whole, cv);
+            if (lane == turn) {
+                em_all = bm;
+                ev_all = bv;
             }
         }
-        if constexpr (BITS == 32) {
-            store8_f32(t.m, i, cnt, vec, m);
-            store8_f32(t.v, i, cnt, vec, v);
-        } else {
-            uint32_t mag[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) mag[q] = q < cnt ? __float_as_uint(m[q]) & 0x7FFFFFFFu : 0u;
-            const uint32_t bm = block_base(mag, 14u);
-            uint32_t cm[2] = {0u, 0u}, cv[2] = {0u, 0u};
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int32_t r = (int32_t)((mag[q] + 0x7FFFFu + ((mag[q] >> 20) & 1u)) >> 20) - (int32_t)(8u * bm);
-                const uint32_t c = finite_bits(mag[q]) ? (uint32_t)min(max(r, 0), 127) : 127u;
-                cm[q >> 2] |= (c | (m[q] < 0.f ? 128u : 0u)) << (8 * (q & 3));
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) mag[q] = q < cnt ? __float_as_uint(v[q]) & 0x7FFFFFFFu : 0u;
-            const uint32_t bv = block_base(mag, 30u);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int32_t r = (int32_t)((mag[q] + ((word[q] & 0xFFFFu) << 4)) >> 20) - (int32_t)(8u * bv);
-                uint32_t c = finite_bits(mag[q]) ? (uint32_t)min(max(r, 1), 255) : 255u;
-                cv[q >> 2] |= (mag[q] ? c : 0u) << (8 * (q & 3));
-            }
-            store_codes(static_cast<uint8_t *>(t.m), i, cnt, vec, make_uint2(cm[0], cm[1]));
-            store_codes(static_cast<uint8_t *>(t.v), i, cnt, vec, make_uint2(cv[0], cv[1]));
-            if (lane == 0) {
-                t.me[wb >> 8] = (uint8_t)bm;
-                t.ve[wb >> 8] = (uint8_t)bv;
-            }
-        }
+    }
+    if (have) {
+        t.me[my_block] = (uint8_t)em_all;
+        t.ve[my_block] = (uint8_t)ev_all;
     }
 }
 
@@ -270,8 +469,8 @@ __global__ void __launch_bounds__(kAdThreads) adamw_values_kernel(const __grid_c
         const int64_t i = first + (int64_t)it * kAdIter + threadIdx.x * kAdPer;
         if (i >= n) return;
         const int cnt = n - i < 8 ? (int)(n - i) : 8;
-        const uint2 cm = load_codes(static_cast<const uint8_t *>(t.m), i, cnt, vec);
-        const uint2 cv = load_codes(static_cast<const uint8_t *>(t.v), i, cnt, vec);
+        const uint2 cm = load_codes(static_cast<const uint8_t *>(t.m), i, cnt, vec && cnt == 8);
+        const uint2 cv = load_codes(static_cast<const uint8_t *>(t.v), i, cnt, vec && cnt == 8);
         const uint32_t mb = 8u * t.me[i >> 8], vb = 8u * t.ve[i >> 8];
         uint32_t wm[4], wv[4];
 #pragma unroll
@@ -315,12 +514,17 @@ const void *adam_kernel(int pd, int gd, int bits) {
     return nullptr;
 }
 
-// A chunk's length: 2,048 elements while that leaves the GPU few chunks, so
-// that small lists spread over every SM, and up to 8,192 for large ones, which
-// then pay the tensor search once in four steps.
-int chunk_iters(int64_t total) {
+// A chunk's length in steps of 2,048 elements: one while that leaves the GPU
+// few chunks, so that small lists spread over every SM.  Large lists take up
+// to 4 with fp32 states (100 million parameters: 402 us; 8 steps 407, 16
+// 414), which end more evenly, and up to 16 with 8-bit ones (256 million: 811
+// us with the values' call; 8 steps 816, 4 steps 843), where a warp keeps its
+// blocks' exponents over a chunk.
+int chunk_iters(int64_t total, int most) {
     const int64_t steps = (total + kAdIter - 1) / kAdIter;
-    return steps >= 152 * 8 * 4 ? 4 : (steps >= 152 * 8 * 2 ? 2 : 1);
+    int n = 1;
+    while (n < most && steps >= 152 * 8 * 2 * n) n *= 2;
+    return n;
 }
 
 template <int N>
@@ -362,7 +566,7 @@ int64_t total_of(const AdamTensor *tensors, int64_t count) {
 
 int adamw_launch(const AdamTensor *tensors, int64_t count, int param_dtype, int grad_dtype, int bits,
                  const AdamArgs &args, cudaStream_t st) {
-    const int iters = chunk_iters(total_of(tensors, count));
+    const int iters = chunk_iters(total_of(tensors, count), bits == 8 ? 16 : 4);
     if (count <= kAdFew)
         return launch_table<kAdFew>(tensors, count, adam_kernel<kAdFew>(param_dtype, grad_dtype, bits), &args, iters,
                                     st);
@@ -371,7 +575,7 @@ int adamw_launch(const AdamTensor *tensors, int64_t count, int param_dtype, int 
 }
 
 int adamw_values_launch(const AdamTensor *tensors, int64_t count, cudaStream_t st) {
-    const int iters = chunk_iters(total_of(tensors, count));
+    const int iters = chunk_iters(total_of(tensors, count), 4);
     if (count <= kAdFew)
         return launch_table<kAdFew>(tensors, count, reinterpret_cast<const void *>(&adamw_values_kernel<kAdFew>),
                                     nullptr, iters, st);

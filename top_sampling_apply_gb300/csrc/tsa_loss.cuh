@@ -447,30 +447,6 @@ __global__ void __launch_bounds__(kStreamThreads) row_loss_stream_kernel(RowLoss
 // one base and constants, and a row's scalars are computed by one warp.
 constexpr int kRowVecs = 8, kRowThreads = 512;
 
-// Pairs of fp32 values: one instruction a pair for sums and products.
-__device__ __forceinline__ unsigned long long pair_of(float a, float b) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void split_pair(unsigned long long r, float &a, float &b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 // e and, with an entropy, the bounded exponents of two logits.
 template <bool ENT>
 __device__ __forceinline__ void exp_pair(float a, float b, unsigned long long negm, unsigned long long c2,
