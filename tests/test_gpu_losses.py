@@ -274,6 +274,44 @@ def test_policy_equal_calls_equal_bits_and_streams(tsa):
         assert torch.equal(p, q)
 
 
+@pytest.mark.parametrize("grad", [True, False])
+@pytest.mark.parametrize("dtype,B,V", [(torch.bfloat16, 400, 33000), (torch.float32, 150, 40000),
+                                       (torch.float16, 2500, 301), (torch.bfloat16, 130, 140000)])
+def test_policy_many_rows_with_gaps(tsa, grad, dtype, B, V):
+    # more rows than run at once, with single, short and long runs of skipped rows among them; the
+    # rows repeat a few reference rows, so that the definition is evaluated once for each
+    rng = np.random.default_rng(B)
+    c = policy_case(rng, 5, V, dtype, False, False, 0.1, 0.02)
+    ref = reference(c)
+    pick = rng.integers(0, 5, B)
+    w = rng.random(B).astype(np.float32) + 0.1
+    skip = rng.random(B) < 0.2
+    skip[B // 3:B // 2] = True
+    skip[-3:] = True
+    w[skip] = 0.0
+    g = lambda a: f32(np.asarray(a)[pick])  # noqa: E731
+    x = c["x"].to(DEV)[torch.from_numpy(pick).to(DEV)]
+    x[torch.from_numpy(skip).to(DEV)] = float("nan")
+    r = tsa.policy_loss(x, torch.from_numpy(c["tok"][pick]).to(DEV), g(c["old"]), g(c["adv"]), ref_logprob=g(c["refl"]),
+                        weight=f32(w), clip_low=0.2, clip_high=0.3, kl_coef=0.1, entropy_coef=0.02,
+                        return_entropy=True, grad=grad)
+    live = ~skip
+    one = tsa.policy_loss(c["x"].to(DEV), torch.from_numpy(c["tok"]).to(DEV), f32(c["old"]), f32(c["adv"]),
+                          ref_logprob=f32(c["refl"]), weight=f32(np.ones(5)), clip_low=0.2, clip_high=0.3,
+                          kl_coef=0.1, entropy_coef=0.02, return_entropy=True)
+    tl = eps(V) + 3 * U * np.abs(ref["logprob"])
+    check("logprob", r.logprob, np.where(live, ref["logprob"][pick], 0.0), tl[pick])
+    check("entropy", r.entropy, np.where(live, ref["entropy"][pick], 0.0), 4 * eps(V) * (1 + ref["entropy"][pick]))
+    # the same row at another weight: the gradient is that many times the gradient at weight 1, each
+    # rounded a few times in fp32 and once to its type
+    if grad:
+        base = one.grad.double()
+        for b in range(B):
+            got, want = r.grad[b].double(), base[pick[b]] * float(w[b])
+            tol = want.abs() * (2 * OUT[dtype] + 2 ** -20) + 2 * TINY[dtype]
+            assert torch.all((got - want).abs() <= tol + 2 ** -18 * want.abs().max()), b
+
+
 def test_policy_empty_batch(tsa):
     z = torch.empty(0, 50, device=DEV)
     e = torch.empty(0, device=DEV)

@@ -165,14 +165,19 @@ struct PairArgs {
 };
 int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cudaStream_t st);
 unsigned int *row_loss_status_ptr();
-int row_grad_launch(const RowLossArgs &args, int dtype, cudaStream_t st);
+// The gradient of rows whose sums are known, and the pairs' mean loss.
+int row_grad_launch(const RowLossArgs &args, int dtype, const float *pair_loss, int64_t pairs, float *loss,
+                    cudaStream_t st);
 int pair_launch(const PairArgs &args, const RowLossArgs &rows, cudaStream_t st);
 // out[0] = sum_i w_i x_i over the entries with w_i != 0 (w NULL: w_s each).
 int weighted_sum_launch(const float *x, const float *w, float w_s, int64_t n, float *out, cudaStream_t st);
-// The kernels of one element type: mode, gradient, entropy; streaming (0) or on chip (1).
-const void *row_loss_kernel_f32(int mode, bool grad, bool ent, int form);
-const void *row_loss_kernel_f16(int mode, bool grad, bool ent, int form);
-const void *row_loss_kernel_bf16(int mode, bool grad, bool ent, int form);
+// The kernels of one element type: mode, gradient, entropy.
+const void *row_loss_kernel_f32(int mode, bool grad, bool ent);
+const void *row_loss_kernel_f16(int mode, bool grad, bool ent);
+const void *row_loss_kernel_bf16(int mode, bool grad, bool ent);
+const void *row_held_kernel_f32(bool ent);
+const void *row_held_kernel_f16(bool ent);
+const void *row_held_kernel_bf16(bool ent);
 const void *row_grad_kernel_f32();
 const void *row_grad_kernel_f16();
 const void *row_grad_kernel_bf16();

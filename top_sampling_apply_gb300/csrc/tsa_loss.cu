@@ -12,25 +12,10 @@ namespace tsa {
 
 namespace {
 
+using loss_detail::block_sum;
+
 constexpr int kSumThreads = 1024;
 constexpr int kPairThreads = 256;
-
-// Block sum of doubles in a fixed order; the result on every thread.  These
-// sums are over rows, not logits (thousands of terms, not hundreds of
-// millions), so fp64 costs nothing and a sequence's log-ratio keeps the
-// differences that cancel in it.
-template <int THREADS>
-__device__ double block_sum(double v, double *sh) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();  // sh may hold an earlier sum
-    if (lane == 0) sh[warp] = v;
-    __syncthreads();
-    double s = 0.0;
-    for (int i = 0; i < THREADS / 32; ++i) s += sh[i];
-    return s;
-}
 
 // One CTA, a fixed order: the same loss for the same rows on every call.
 __global__ void __launch_bounds__(kSumThreads) weighted_sum_kernel(const float *x, const float *w, float w_s,
@@ -55,6 +40,7 @@ __global__ void __launch_bounds__(kSumThreads) weighted_sum_kernel(const float *
 // left their coefficient 0) and its log-probability is not -inf.
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(PairArgs a, RowLossArgs r) {
     __shared__ double sh[kPairThreads / 32];
+    pdl_launch_dependents();
     pdl_wait_primary();
     const int64_t p = blockIdx.x;
     double R[2], W[2];
@@ -104,10 +90,10 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(PairArgs a, RowLossA
 
 __device__ unsigned int g_loss_status;
 
-const void *loss_kernel(int dtype, int mode, bool grad, bool ent, int form) {
-    return dtype == 0 ? row_loss_kernel_f32(mode, grad, ent, form)
-                      : (dtype == 1 ? row_loss_kernel_f16(mode, grad, ent, form)
-                                    : row_loss_kernel_bf16(mode, grad, ent, form));
+const void *loss_kernel(int dtype, int mode, bool grad, bool ent) {
+    return dtype == 0 ? row_loss_kernel_f32(mode, grad, ent)
+                      : (dtype == 1 ? row_loss_kernel_f16(mode, grad, ent)
+                                    : row_loss_kernel_bf16(mode, grad, ent));
 }
 
 // A launch that may start its prologue while the kernel before it drains;
@@ -126,19 +112,6 @@ int launch_pdl(const void *fn, dim3 grid, int threads, void **params, cudaStream
 }
 
 }  // namespace
-
-// The CTAs a row takes on chip, 0 if its vectors do not fit eight of them.
-// Few rows are spread further, down to one vector a thread, while that still
-// leaves SMs idle: 8 rows of 8,192 fp32 logits use 32 CTAs instead of 8.
-static int row_cluster(int64_t B, int64_t V, int es) {
-    const int64_t nvec = V * es / 16 + 1;
-    const int64_t one = (int64_t)loss_detail::kRowThreads, per = one * loss_detail::kRowVecs;
-    int C = 1;
-    while (C <= 8 && (nvec + C - 1) / C > per) C *= 2;
-    if (C > 8) return 0;
-    while (C < 8 && B * C * 2 <= 152 && nvec / (2 * C) >= one) C *= 2;
-    return C;
-}
 
 unsigned int *row_loss_status_ptr() {
     void *p = nullptr;
@@ -167,43 +140,95 @@ static int64_t resident_clusters(const void *fn, const cudaLaunchConfig_t &cfg, 
     return n;
 }
 
-int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cudaStream_t st) {
-    const int C = row_cluster(args.B, args.V, dtype == 0 ? 4 : 2);
-    const void *fn = loss_kernel(dtype, mode, args.grad != nullptr, ent, C > 0 ? 1 : 0);
-    RowLossArgs a = args;
-    int lg = C == 8 ? 3 : C >> 1;
-    unsigned int *status = row_loss_status_ptr();
-    if (!status) return -1;
-    void *params[] = {&a, &lg, &status};
+// The CTAs that share a streamed row.  With a gradient, enough that L2 keeps
+// part of a row until its second reading.  Fewer rows than SMs are spread
+// further, down to 256 vectors a CTA.
+static int row_cluster(int64_t B, int64_t V, int es, bool grad) {
+    const int64_t bytes = V * es;
+    int C = 1;
+    if (grad)
+        while (C < loss_detail::kRowMaxCluster && bytes > (int64_t)C * 132 * 1024) C *= 2;
+    while (C < loss_detail::kRowMaxCluster && B * C * 2 <= 152 && bytes / 16 >= 512 * C) C *= 2;
+    return C;
+}
+
+// The CTAs that hold a row together, 0 if its vectors do not fit eight.  Fewer
+// rows than SMs are spread further, down to one vector a thread: 8 rows of
+// 8,192 fp32 logits use 64 CTAs instead of 8.
+static int held_cluster(int64_t B, int64_t V, int es) {
+    const int64_t nvec = V * es / 16 + 1;
+    const int64_t one = loss_detail::kHeldThreads, per = one * loss_detail::kHeldVecs;
+    int C = 1;
+    while (C <= loss_detail::kHeldCluster && (nvec + C - 1) / C > per) C *= 2;
+    if (C > loss_detail::kHeldCluster) return 0;
+    while (C < loss_detail::kHeldCluster && B * C * 2 <= 152 && nvec / (2 * C) >= one) C *= 2;
+    return C;
+}
+
+// A launch of clusters of C CTAs, a row each; more rows than clusters that run
+// at once go round them.
+static int launch_rows(const void *fn, int64_t B, int C, int threads, size_t smem, void **params, cudaStream_t st) {
+    if (prepare_kernel(fn, smem, C) != 0) return -1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(args.B * (C > 0 ? C : 1)));
-    cfg.blockDim = dim3((unsigned)(C > 0 ? loss_detail::kRowThreads : loss_detail::kStreamThreads));
+    cfg.gridDim = dim3((unsigned)((B < 65536 ? B : 65536) * C));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)(C > 0 ? C : 1);
+    attr[0].val.clusterDim.x = (unsigned)C;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (C > 0) cfg.dynamicSmemBytes = loss_detail::kRowSmem;
-    if (C > 0 && prepare_kernel(fn, loss_detail::kRowSmem, 1) != 0) return -1;
-    if (C > 0) {  // rows go round the clusters that run at once
-        const int64_t n = resident_clusters(fn, cfg, C);
-        if (n < 1) return -1;
-        if (args.B > n) cfg.gridDim.x = (unsigned)(n * C);
-    }
+    const int64_t n = resident_clusters(fn, cfg, C);
+    if (n < 1) return -1;
+    if (B > n) cfg.gridDim.x = (unsigned)(n * C);
     return cudaLaunchKernelExC(&cfg, fn, params) == cudaSuccess ? 0 : -1;
 }
 
-int row_grad_launch(const RowLossArgs &args, int dtype, cudaStream_t st) {
+int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cudaStream_t st) {
+    using namespace loss_detail;
+    const int es = dtype == 0 ? 4 : 2;
+    const bool grad = args.grad != nullptr;
+    RowLossArgs a = args;
+    unsigned int *status = row_loss_status_ptr();
+    if (!status) return -1;
+    const int H = grad ? held_cluster(args.B, args.V, es) : 0;
+    if (H > 0) {
+        const void *fn = dtype == 0 ? row_held_kernel_f32(ent)
+                                    : (dtype == 1 ? row_held_kernel_f16(ent) : row_held_kernel_bf16(ent));
+        int lg = 0;
+        while ((1 << lg) < H) ++lg;
+        void *params[] = {&a, &lg, &status};
+        return launch_rows(fn, args.B, H, kHeldThreads, kHeldSmem, params, st);
+    }
+    const int C = row_cluster(args.B, args.V, es, grad);
+    int lg = 0;
+    while ((1 << lg) < C) ++lg;
+    const int64_t vecs = (args.V * es / 16 + C - 1) / C;  // a CTA's vectors at most
+    int stages = (int)((vecs + kRowStage - 1) / kRowStage);
+    if (stages < 1) stages = 1;
+    // a stage as long as fits, in whole steps of the working warps
+    int nu = (int)((vecs < kRowStage ? vecs : kRowStage) + kRowUsers - 1) / kRowUsers;
+    if (nu < 1) nu = 1;
+    // about 48 KB of stages between a row's last sum and its first gradient
+    const int64_t bytes = (vecs * 16 + stages - 1) / stages;
+    int lag = (int)((49152 + bytes) / (bytes + 1));
+    lag = lag < 1 ? 1 : (lag > kRowMaxLag ? kRowMaxLag : lag);
+    void *params[] = {&a, &lg, &stages, &nu, &lag, &status};
+    return launch_rows(loss_kernel(dtype, mode, grad, ent), args.B, C, kRowThreads, kRowSmem, params, st);
+}
+
+int row_grad_launch(const RowLossArgs &args, int dtype, const float *pair_loss, int64_t pairs, float *loss,
+                    cudaStream_t st) {
     const void *fn = dtype == 0 ? row_grad_kernel_f32() : (dtype == 1 ? row_grad_kernel_f16() : row_grad_kernel_bf16());
     const int64_t per = (int64_t)loss_detail::kKnownThreads * loss_detail::kKnownU * (dtype == 0 ? 4 : 8);
     const unsigned slices = (unsigned)((args.V + per - 1) / per);
     const unsigned y = (unsigned)(args.B < 32768 ? args.B : 32768);
     const unsigned z = (unsigned)((args.B + y - 1) / y);
     RowLossArgs a = args;
-    void *params[] = {&a};
+    void *params[] = {&a, &pair_loss, &pairs, &loss};
     return launch_pdl(fn, dim3(slices, y, z), loss_detail::kKnownThreads, params, st);
 }
 

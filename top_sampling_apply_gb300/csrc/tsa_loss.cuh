@@ -51,10 +51,13 @@ template <> struct Pack<0> {
         v.z = __float_as_uint(fmaxf(__uint_as_float(v.z), -INFINITY));
         v.w = __float_as_uint(fmaxf(__uint_as_float(v.w), -INFINITY));
     }
-    __device__ static __forceinline__ float vmax(const uint4 &v) {
-        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
-                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    // the larger of two words' values, NaN if one is; a word's value
+    __device__ static __forceinline__ uint32_t top2(uint32_t a, uint32_t b) {
+        float d;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+        return __float_as_uint(d);
     }
+    __device__ static __forceinline__ float top(uint32_t w) { return __uint_as_float(w); }
 };
 template <> struct Pack<1> {
     __device__ static __forceinline__ uint32_t two(float lo, float hi) {
@@ -78,9 +81,15 @@ template <> struct Pack<1> {
         v.z = max2(v.z, 0xFC00FC00u);
         v.w = max2(v.w, 0xFC00FC00u);
     }
-    __device__ static __forceinline__ float vmax(const uint4 &v) {
-        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
-        return fmaxf(Elem<1>::h2f(m & 0xFFFFu), Elem<1>::h2f(m >> 16));
+    __device__ static __forceinline__ uint32_t top2(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    __device__ static __forceinline__ float top(uint32_t w) {
+        float d;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(Elem<1>::h2f(w & 0xFFFFu)), "f"(Elem<1>::h2f(w >> 16)));
+        return d;
     }
 };
 template <> struct Pack<2> {
@@ -105,9 +114,15 @@ template <> struct Pack<2> {
         v.z = max2(v.z, 0xFF80FF80u);
         v.w = max2(v.w, 0xFF80FF80u);
     }
-    __device__ static __forceinline__ float vmax(const uint4 &v) {
-        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
-        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    __device__ static __forceinline__ uint32_t top2(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    __device__ static __forceinline__ float top(uint32_t w) {
+        float d;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(__uint_as_float(w << 16)), "f"(__uint_as_float(w & 0xFFFF0000u)));
+        return d;
     }
 };
 
@@ -212,23 +227,7 @@ __device__ __forceinline__ float policy_row(const RowLossArgs &r, int64_t row, f
     return loss - r.ent * H;
 }
 
-// ------------------------------------------------------------ the row, twice
-// One CTA a row: the sums in one read, the gradient in a second one, which
-// comes from L2 while the rows in flight fit there (152 rows of 128,256 bf16
-// logits are 39 MB).  Every row length, alignment and stride; rows that fit a
-// cluster's registers take row_loss_kernel instead.
-constexpr int kStreamThreads = 512;
-constexpr int kStreamU = 4;  // 16-byte vectors in flight a thread
-
-__device__ __forceinline__ void stat_block(RowStat &s, RowStat *sh, float c2, int warps) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    s = warp_merge(s, c2);
-    if (lane == 0) sh[warp] = s;
-    __syncthreads();
-    s = lane < warps ? sh[lane] : RowStat{-INFINITY, 0.f, 0.f};
-    s = warp_merge(s, c2);
-}
-
+// ------------------------------------------------------------ a finished row
 // Fills row outputs (by one thread) and returns the gradient's numbers.
 template <int MODE, bool ENT>
 __device__ __forceinline__ RowScalars finish_row(const RowLossArgs &r, int64_t row, const RowStat &s, float xt,
@@ -303,155 +302,64 @@ __device__ __forceinline__ float grad_el(float x, float m, float c2, const GradC
     return __fmul_rn(e, ENT ? fmaf(k.k2, y, k.k1) : k.k1);
 }
 
-template <int DT, int MODE, bool GRAD, bool ENT>
-__global__ void __launch_bounds__(kStreamThreads) row_loss_stream_kernel(RowLossArgs r) {
-    using E = Elem<DT>;
-    constexpr int AE = E::AE;
-    __shared__ RowStat sh[kStreamThreads / 32];
-    const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x;
-    const uint8_t *rp = static_cast<const uint8_t *>(r.logits) + (size_t)row * r.stride * E::SIZE;
-    uint8_t *gp = GRAD ? static_cast<uint8_t *>(r.grad) + (size_t)row * r.gstride * E::SIZE : nullptr;
-    const int32_t *mrow = r.mask ? r.mask + (size_t)row * r.mstride : nullptr;
-    const int32_t V = (int32_t)r.V;
-    const Slice32 g = make_slice32<AE, E::SIZE>(rp, V, 0, 1);
-    const bool same = GRAD && ((reinterpret_cast<uintptr_t>(rp) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0;
-    float w;
-    int64_t tok;
-    const bool named = row_named(r, row, &w, &tok);
-    if (!named) {
-        if (tid == 0) skip_row<MODE>(r, row);
-        if (GRAD) {
-            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-            if (same) {
-                for (int32_t v = tid; v < g.nvec; v += kStreamThreads)
-                    __stcs(reinterpret_cast<uint4 *>(gp + (size_t)(g.head + v * AE) * E::SIZE), z);
-                if (tid < g.head) Pack<DT>::store1(gp, tid, 0.f);
-                if (tid < g.tail) Pack<DT>::store1(gp, g.head + g.nvec * AE + tid, 0.f);
-            } else {
-                for (int32_t i = tid; i < V; i += kStreamThreads) Pack<DT>::store1(gp, i, 0.f);
-            }
-        }
-        return;
-    }
-    const float T = row_temperature(r, row), c2 = kLog2eL / T;
-    const float xt = token_logit(r, rp, mrow, DT, tok);
-    auto fetch = [&](int32_t v, uint4 &x) {  // a cleaned, masked vector
-        const int32_t e = g.head + v * AE;
-        // a plain load: the gradient may be written over the logits
-        x = *reinterpret_cast<const uint4 *>(rp + (size_t)e * E::SIZE);
-        if (mrow) {
-            const uint32_t lo = (uint32_t)__ldg(mrow + (e >> 5));
-            const uint32_t hi = ((e & 31) + AE > 32) ? (uint32_t)__ldg(mrow + (e >> 5) + 1) : 0u;
-            mask_vec<DT>(x, __funnelshift_r(lo, hi, (uint32_t)(e & 31)) & ((1u << AE) - 1u));
-        }
-        Pack<DT>::clean(x);
-    };
-    auto fetch1 = [&](int32_t i) {
-        return mrow && !allowed_bit(mrow, i) ? -INFINITY : load_clean(rp, DT, i);
-    };
-    RowStat s = {-INFINITY, 0.f, 0.f};
-    auto add1 = [&](float x) {
-        if (x > -INFINITY) s = merge(s, RowStat{x, x == INFINITY ? __int_as_float(0x7FC00000) : 1.f, 0.f}, c2);
-    };
-    if (tid < g.head) add1(fetch1(tid));
-    if (tid < g.tail) add1(fetch1(g.head + g.nvec * AE + tid));
-    for (int32_t v0 = tid; v0 < g.nvec; v0 += kStreamThreads * kStreamU) {
-        uint4 x[kStreamU];
-        float bm = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kStreamU; ++u) {
-            const int32_t v = v0 + u * kStreamThreads;
-            if (v < g.nvec)
-                fetch(v, x[u]);
-            else {
-                float none[AE];
-#pragma unroll
-                for (int k = 0; k < AE; ++k) none[k] = -INFINITY;
-                x[u] = Pack<DT>::vec(none);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kStreamU; ++u) bm = fmaxf(bm, Pack<DT>::vmax(x[u]));
-        if (bm > s.m) s = merge(s, RowStat{bm, 0.f, 0.f}, c2);
-        if (s.m > -INFINITY) {
-#pragma unroll
-            for (int u = 0; u < kStreamU; ++u) {
-                float f[AE];
-                E::unpack(x[u], f);
-#pragma unroll
-                for (int k = 0; k < AE; ++k) {
-                    float y = expo(f[k], s.m, c2);
-                    if (ENT) y = fmaxf(y, kLowExp);
-                    const float e = ex2_approx(y);
-                    s.Z += e;
-                    if (ENT) s.t = fmaf(e, y, s.t);
-                }
-            }
-        }
-    }
-    stat_block(s, sh, c2, kStreamThreads / 32);
-    if (s.m == INFINITY) s.Z = __int_as_float(0x7FC00000);
-    const RowScalars gs = finish_row<MODE, ENT>(r, row, s, xt, T, w, tid == 0);
-    if (!GRAD) return;
-    // a row that does not count (its token masked) has a = b = 0: zeros
-    const bool live = xt > -INFINITY;
-    const GradCoef k = live ? grad_coef<ENT>(gs, s) : GradCoef{0.f, 0.f};
-    const float m = live ? s.m : 0.f;
-    auto grad1 = [&](float x) { return grad_el<ENT>(x, m, c2, k); };
-    auto store_el = [&](int32_t i) {
-        float f = live ? grad1(fetch1(i)) : 0.f;
-        if (i == tok && live) f = __fadd_rn(f, gs.a);
-        Pack<DT>::store1(gp, i, f);
-    };
-    if (!same) {
-        for (int32_t i = tid; i < V; i += kStreamThreads) store_el(i);
-        return;
-    }
-    if (tid < g.head) store_el(tid);
-    if (tid < g.tail) store_el(g.head + g.nvec * AE + tid);
-    for (int32_t v = tid; v < g.nvec; v += kStreamThreads) {
-        float f[AE];
-        if (live) {
-            uint4 x;
-            fetch(v, x);
-            E::unpack(x, f);
-            const int32_t e0 = g.head + v * AE;
-#pragma unroll
-            for (int q = 0; q < AE; ++q) {
-                f[q] = grad1(f[q]);
-                if (e0 + q == (int32_t)tok) f[q] = __fadd_rn(f[q], gs.a);
-            }
-        } else {
-#pragma unroll
-            for (int q = 0; q < AE; ++q) f[q] = 0.f;
-        }
-        __stcs(reinterpret_cast<uint4 *>(gp + (size_t)(g.head + v * AE) * E::SIZE), Pack<DT>::vec(f));
-    }
-}
-
-// ------------------------------------------------------------ the row, once
-// A cluster of C CTAs takes a row: 512 threads with eight 16-byte vectors each
-// are 64 KB a CTA, so that a row of 128,256 logits takes four CTAs in 16 bits
-// and eight in fp32.  Clusters are persistent.  A row's share comes by one bulk
-// copy into shared memory, goes to registers at once, and the next row's copy
-// starts as soon as every warp has read it, so that HBM works while the
-// maximum, the sums and the gradient are formed from the registers.  The warps
-// send their (m, Z, t) to every CTA of the cluster (asynchronous stores that
-// count on the receiver's barrier); one warp a CTA joins them and finishes the
-// row for the others.
+// ------------------------------------------------------------ the rows, streamed
+// One persistent CTA an SM takes rows as streams of 56 KB stages through a ring
+// in shared memory, filled by bulk copies.  Fourteen warps reduce the stages of
+// one row (m, Z, t, against a reference a warp) and, in turn with them, write
+// the gradient of the row before from its stages, which come a second time,
+// from L2: a row is 256 KB for 128,256 logits in 16 bits, and the two rows of
+// every SM are 78 MB.  Between a row's last sum and its first gradient stage
+// lies a stage of the next row, during which a warp of its own joins the sums
+// and finishes the row.  So no warp waits for another in the middle of a row,
+// HBM is read and written all the time, and what a row costs by itself is
+// spread over its whole length.  Longer rows are shared by the C CTAs of a
+// cluster, so that the rows in flight still fit L2; only the finishing warps
+// talk to one another then.
 //
-// The issue slots are the scarce part: reading and writing a bf16 logit at
-// 6.7 TB/s leaves 22 instructions an element.  So 16-bit maxima and the NaN
-// test work on pairs, sums and products on packed fp32 pairs, addresses are
-// one base and constants, and a row's scalars are computed by one warp.
-constexpr int kRowVecs = 8, kRowThreads = 512;
+// The issue slots are scarce too: reading and writing a bf16 logit at 6.7 TB/s
+// leaves 22 instructions an element.  16-bit maxima and the NaN test work on
+// pairs, sums and products on packed fp32 pairs.
+constexpr int kRowVecs = 8;                               // 16-byte vectors a thread in a stage
+constexpr int kRowWarps = 14, kRowUsers = 32 * kRowWarps; // the warps that work on stages
+constexpr int kRowThreads = kRowUsers + 64;               // one more to copy, one to finish rows
+constexpr int kRowStage = kRowUsers * kRowVecs;           // vectors a stage
+constexpr int kRowSlots = 3;                              // stages in shared memory
+constexpr int kRowRing = 16;                              // rows under way at most
+constexpr int kRowMaxCluster = 8;
+constexpr int kRowMaxLag = 8;
 
+// A row's (or a warp's) reference as its exponents are formed from it.  Near 0
+// the exponent is one fused multiply-add, l c2 - R with R = m c2 rounded; the
+// rounding (at most 2^-10 for |R| < 2^14, known exactly by one more fma) scales
+// every term alike and is taken out of the sums.  Far from 0 it is (l - m) c2.
+struct Ref {
+    unsigned long long c2, neg;  // pairs: c2, and -R or -m
+    bool near;
+};
+__device__ __forceinline__ bool near_zero(float m, float c2) { return fabsf(m * c2) < 16384.f; }
+__device__ __forceinline__ Ref make_ref(float m, float c2) {
+    Ref r;
+    r.near = near_zero(m, c2);
+    const float n = r.near ? -__fmul_rn(m, c2) : -m;
+    r.c2 = pair_of(c2, c2);
+    r.neg = pair_of(n, n);
+    return r;
+}
+// How far the near form's exponents lie above (l - m) c2, and 2 to minus that.
+__device__ __forceinline__ float near_shift(float m, float c2, float *f) {
+    if (!near_zero(m, c2)) {
+        *f = 1.f;
+        return 0.f;
+    }
+    const float d = fmaf(m, c2, -__fmul_rn(m, c2)), z = -kLn2 * d;
+    *f = fmaf(z, fmaf(z, 0.5f, 1.f), 1.f);
+    return d;
+}
 // e and, with an entropy, the bounded exponents of two logits.
-template <bool ENT>
-__device__ __forceinline__ void exp_pair(float a, float b, unsigned long long negm, unsigned long long c2,
-                                         unsigned long long &e, unsigned long long &y) {
-    y = mul2(add2(pair_of(a, b), negm), c2);
+template <bool ENT, bool NEAR>
+__device__ __forceinline__ void exp_pair(float a, float b, const Ref &r, unsigned long long &e, unsigned long long &y) {
+    const unsigned long long x = pair_of(a, b);
+    y = NEAR ? fma2(x, r.c2, r.neg) : mul2(add2(x, r.neg), r.c2);
     float p, q;
     split_pair(y, p, q);
     if (ENT) {
@@ -460,6 +368,19 @@ __device__ __forceinline__ void exp_pair(float a, float b, unsigned long long ne
         y = pair_of(p, q);
     }
     e = pair_of(ex2_approx(p), ex2_approx(q));
+}
+// A gradient element of one logit, with the bits of the paired form.
+template <bool ENT>
+__device__ __forceinline__ float ref_grad(float x, const Ref &r, float k1, float k2) {
+    unsigned long long e, y;
+    if (r.near)
+        exp_pair<ENT, true>(x, x, r, e, y);
+    else
+        exp_pair<ENT, false>(x, x, r, e, y);
+    float a, b;
+    const unsigned long long kk = pair_of(k1, k1);
+    split_pair(mul2(e, ENT ? fma2(pair_of(k2, k2), y, kk) : kk), a, b);
+    return a;
 }
 
 // A CTA's share of one row: this thread's first vector's element, the CTA's
@@ -491,6 +412,12 @@ __device__ __forceinline__ float warp_max(float x) {
     return m;
 }
 
+// The same, NaN if one of them is.
+__device__ __forceinline__ float warp_top(float x) {
+    float m;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(x));
+    return m;
+}
 __device__ __forceinline__ void send_stat(float4 *slot, uint64_t *bar, uint32_t rank, float m, float Z, float t) {
     asm volatile(
         "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %3}, [%4];" ::"r"(
@@ -501,23 +428,542 @@ __device__ __forceinline__ void send_stat(float4 *slot, uint64_t *bar, uint32_t 
 __device__ __forceinline__ void arrive_one(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-constexpr size_t kRowSmem = (size_t)kRowThreads * kRowVecs * 16;
+constexpr size_t kRowSmem = (size_t)kRowSlots * kRowStage * 16;
 
+// What a row's threads need to know of it.
+struct RowMeta {
+    int64_t row, tok;  // row = B: there are no more
+    float w, T, c2, xt;
+};
+
+// A warp's running sums against its reference m: in the form that m calls for
+// (see Ref).
+struct WarpSums {
+    float m, Z, t;  // m is the warp's, Z and t the thread's
+};
+// A larger reference: Z and t are brought from the old one's form to the new one's.
+template <bool ENT>
+__device__ __forceinline__ void raise(WarpSums &s, float m, float c2) {
+    if (s.m > -INFINITY) {
+        float fo, fn;
+        const float d0 = near_shift(s.m, c2, &fo), d1 = near_shift(m, c2, &fn);
+        // from the old form to the old m, to the new m, to the new form
+        const float d = fmaxf((s.m - m) * c2, kLowExp), f = ex2_approx(d) * fo * (2.f - fn);
+        // y_new = y_old - d0 + (m_old - m_new) c2 + d1
+        if (ENT) s.t = f * fmaf(s.Z, d - d0 + d1, s.t);
+        s.Z *= f;
+    }
+    s.m = m;
+}
+// Z and t of the first nu of a thread's vectors.
+template <int DT, bool ENT, bool NEAR, int U>
+__device__ __forceinline__ void add_vecs(const uint4 (&x)[U], int nu, const Ref &ref, WarpSums &s) {
+    constexpr int AE = Elem<DT>::AE;
+    unsigned long long Z = pair_of(s.Z, 0.f), Z2 = pair_of(0.f, 0.f), t = pair_of(s.t, 0.f), e, y;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (u < nu) {
+            float f[AE];
+            Elem<DT>::unpack(x[u], f);
+#pragma unroll
+            for (int q = 0; q < AE; q += 4) {
+                exp_pair<ENT, NEAR>(f[q], f[q + 1], ref, e, y);
+                Z = add2(Z, e);
+                if (ENT) t = fma2(e, y, t);
+                exp_pair<ENT, NEAR>(f[q + 2], f[q + 3], ref, e, y);
+                Z2 = add2(Z2, e);
+                if (ENT) t = fma2(e, y, t);
+            }
+        }
+    }
+    float a, b;
+    split_pair(add2(Z, Z2), a, b);
+    s.Z = a + b;
+    if (ENT) {
+        split_pair(t, a, b);
+        s.t = a + b;
+    }
+}
+// The largest logit of the warp among the first nu vectors of its threads, NaN
+// if there is one; and the vectors with -inf in the place of NaN.
+template <int DT, int U>
+__device__ __forceinline__ float largest(const uint4 (&x)[U], int nu) {
+    using P = Pack<DT>;
+    uint32_t w[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+#pragma unroll
+    for (int u = 1; u < U; ++u) {
+        if (u < nu) {
+            w[0] = P::top2(w[0], x[u].x);
+            w[1] = P::top2(w[1], x[u].y);
+            w[2] = P::top2(w[2], x[u].z);
+            w[3] = P::top2(w[3], x[u].w);
+        }
+    }
+    return warp_top(P::top(P::top2(P::top2(w[0], w[1]), P::top2(w[2], w[3]))));
+}
+template <int DT, int U>
+__device__ __forceinline__ void clean_all(uint4 (&x)[U], int nu) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (u < nu) Pack<DT>::clean(x[u]);
+}
+template <int DT>
+__device__ __forceinline__ uint4 none_vec() {
+    return DT == 0   ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
+           : DT == 1 ? make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u)
+                     : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+}
+// The mask bits of the vector whose first element is e, in two words.
+template <int AE>
+__device__ __forceinline__ void mask_words(const int32_t *mrow, int32_t e, bool in, uint32_t &lo, uint32_t &hi) {
+    lo = in ? (uint32_t)__ldg(mrow + (e >> 5)) : 0u;
+    hi = in && (e & 31) + AE > 32 ? (uint32_t)__ldg(mrow + (e >> 5) + 1) : 0u;
+}
+template <int AE>
+__device__ __forceinline__ uint32_t mask_bits(uint32_t lo, uint32_t hi, int32_t e) {
+    return __funnelshift_r(lo, hi, (uint32_t)(e & 31)) & ((1u << AE) - 1u);
+}
+
+// The gradient of a vector: k1 e + k2 e y, in place of the logits.
+template <int DT, bool ENT, bool NEAR>
+__device__ __forceinline__ void grad_vec(uint4 &x, const Ref &ref, float k1, float k2) {
+    constexpr int AE = Elem<DT>::AE;
+    const unsigned long long a = pair_of(k1, k1), b = pair_of(k2, k2);
+    float f[AE];
+    Elem<DT>::unpack(x, f);
+#pragma unroll
+    for (int q = 0; q < AE; q += 2) {
+        unsigned long long e, y;
+        exp_pair<ENT, NEAR>(f[q], f[q + 1], ref, e, y);
+        split_pair(mul2(e, ENT ? fma2(b, y, a) : a), f[q], f[q + 1]);
+    }
+    x = Pack<DT>::vec(f);
+}
+
+// `stages`: a CTA's stages of a row, of nu * kRowUsers vectors each (the last
+// ones may be short or empty); `lag`: the stages between a row's last sum and
+// its first gradient.
 template <int DT, int MODE, bool GRAD, bool ENT>
-__global__ void __launch_bounds__(kRowThreads, 2) row_loss_kernel(RowLossArgs r, int lg, unsigned int *status) {
+__global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r, int lg, int stages, int nu, int lag,
+                                                                  unsigned int *status) {
     using E = Elem<DT>;
-    constexpr int AE = E::AE, U = kRowVecs, THREADS = kRowThreads, WARPS = THREADS / 32;
-    extern __shared__ __align__(128) uint4 buf[];  // the CTA's vectors of a row, padded with -inf
-    __shared__ float4 stats[2][8 * WARPS];         // every warp of the cluster, for this row and the next
+    constexpr int AE = E::AE, U = kRowVecs, S = kRowSlots, RING = kRowRing;
+    extern __shared__ __align__(128) uint4 ring[];
+    __shared__ float4 sums[RING][kRowWarps];           // a row's (m, Z, t) by warp
+    __shared__ float4 peers[RING][kRowMaxCluster];     // and by CTA of the cluster
+    __shared__ float4 finished[RING];                  // k1, k2, a and m of a finished row
+    __shared__ RowMeta meta[RING];
+    __shared__ uint32_t dirty[RING];                   // whether a row has a NaN
+    __shared__ uint64_t full[S], empty[S];             // a stage has come; every warp has read it
+    __shared__ uint64_t known[RING], summed[RING], joined[RING], fin[RING];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t C = 1u << lg, rank = C > 1 ? cluster_ctarank() : 0u;
+    const int64_t step = gridDim.x >> lg, first_row = blockIdx.x >> lg;
+    const bool fixed = ((size_t)r.stride * E::SIZE) % 16 == 0;  // every row lies alike
+    auto logits_at = [&](int64_t b) { return static_cast<const uint8_t *>(r.logits) + (size_t)b * r.stride * E::SIZE; };
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kRowWarps);
+        }
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(&known[i], 1);
+            mbar_init(&summed[i], kRowWarps);
+            mbar_init(&joined[i], 1);
+            mbar_init(&fin[i], 1);
+        }
+        mbar_init_fence();
+    }
+    if (C > 1)
+        cluster_sync();  // every CTA's barriers stand before another CTA counts on them
+    else
+        __syncthreads();
+    pdl_launch_dependents();  // the next kernel waits for this one's end before it reads
+    const int stage = nu * kRowUsers;
+    const int delay = stages + lag;  // a gradient stage follows its sums' stage by this many
+    bool ok = true;                  // a wait that ran out ends all waiting; the status word tells
+
+    if (warp == kRowWarps) {
+        // ---- copies: sums' stages and gradient stages in the order of their use
+        RowMeta mine;
+        uint32_t found = 0;
+        int64_t base = first_row;
+        uint32_t slot = 0, phase = 1;
+        auto copy = [&](int64_t row, int s) {
+            const RowPlace p = place_row<DT>(r, row, rank, lg);
+            int cnt = p.nv - s * stage;
+            cnt = cnt < 0 ? 0 : (cnt > stage ? stage : cnt);
+            if (lane == 0) {
+                ok = ok && mbar_wait_bounded(&empty[slot], phase, status);
+                mbar_arrive_expect_tx(&full[slot], (uint32_t)cnt * 16u);
+                if (cnt > 0)
+                    bulk_g2s(ring + slot * kRowStage,
+                             logits_at(row) + (size_t)(p.first - tid * AE) * E::SIZE + (size_t)s * stage * 16u,
+                             (uint32_t)cnt * 16u, &full[slot]);
+            }
+            if (++slot == S) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        };
+        int64_t row1 = 0;
+        uint32_t k1 = 0, k2 = 0;
+        int s1 = 0, s2 = 0;
+        bool end1 = false;
+        for (int g = 0;; ++g) {
+            if (!end1) {
+                if (s1 == 0) {
+                    // the next row that counts: 32 rows looked at together
+                    while (found == 0 && base < r.B) {
+                        const int64_t b = base + lane * step;
+                        float w = 0.f;
+                        int64_t tok = -1;
+                        const bool named = b < r.B && row_named(r, b, &w, &tok);
+                        if (named) {
+                            mine.row = b;
+                            mine.tok = tok;
+                            mine.w = w;
+                            mine.T = row_temperature(r, b);
+                            mine.c2 = kLog2eL / mine.T;
+                            mine.xt = token_logit(r, logits_at(b), r.mask ? r.mask + (size_t)b * r.mstride : nullptr,
+                                                  DT, tok);
+                        }
+                        found = __ballot_sync(0xFFFFFFFFu, named);
+                        base += 32 * step;
+                    }
+                    const int who = found ? __ffs((int)found) - 1 : 0;
+                    end1 = found == 0;
+                    found &= found - 1;
+                    row1 = end1 ? r.B : __shfl_sync(0xFFFFFFFFu, mine.row, who);
+                    if (lane == who) {
+                        RowMeta m = mine;
+                        m.row = row1;
+                        meta[k1 % RING] = m;
+                        dirty[k1 % RING] = 0u;
+                        arrive_one(&known[k1 % RING]);
+                    }
+                    __syncwarp();
+                }
+                if (!end1) {
+                    copy(row1, s1);
+                    if (++s1 == stages) {
+                        s1 = 0;
+                        ++k1;
+                    }
+                }
+            }
+            if (GRAD && g >= delay && k2 < k1) {
+                copy(meta[k2 % RING].row, s2);
+                if (++s2 == stages) {
+                    s2 = 0;
+                    ++k2;
+                }
+            }
+            if (end1 && (!GRAD || k2 == k1)) break;
+        }
+    } else if (warp == kRowWarps + 1) {
+        // ---- finished rows
+        for (uint32_t k = 0;; ++k) {
+            const uint32_t i = k % RING, phase = (k / RING) & 1u;
+            ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_bounded(&known[i], phase, status));
+            const RowMeta mt = meta[i];
+            if (!ok || mt.row >= r.B) break;
+            if (C > 1 && lane == 0) mbar_arrive_expect_tx(&joined[i], C * 16u);
+            ok = ok && mbar_wait_bounded(&summed[i], phase, status);
+            auto join = [&](const float4 v, bool in) {
+                RowStat s;
+                s.m = warp_max(in ? v.x : -INFINITY);
+                const float d = in ? (v.x == s.m ? 0.f : fmaxf((v.x - s.m) * mt.c2, kLowExp)) : kLowExp;
+                const float f = ex2_approx(d);
+                s.Z = warp_sum_f32(in ? v.y * f : 0.f);
+                s.t = ENT ? warp_sum_f32(in ? fmaf(v.y, d, v.z) * f : 0.f) : 0.f;
+                return s;
+            };
+            RowStat s = join(lane < kRowWarps ? sums[i][lane] : make_float4(0.f, 0.f, 0.f, 0.f), lane < kRowWarps);
+            if (C > 1) {
+                if (lane < (int)C) send_stat(&peers[i][rank], &joined[i], (uint32_t)lane, s.m, s.Z, s.t);
+                ok = ok && mbar_wait_bounded(&joined[i], phase, status);
+                s = join(lane < (int)C ? peers[i][lane] : make_float4(0.f, 0.f, 0.f, 0.f), lane < (int)C);
+            }
+            if (s.m == INFINITY) s.Z = __int_as_float(0x7FC00000);
+            const RowScalars gs = finish_row<MODE, ENT>(r, mt.row, s, mt.xt, mt.T, mt.w, rank == 0 && lane == 0);
+            if (lane == 0) {
+                // a row that does not count (its token masked) gets zeros
+                GradCoef kc = mt.xt > -INFINITY ? grad_coef<ENT>(gs, s) : GradCoef{0.f, 0.f};
+                float f;
+                const float d = near_shift(s.m, mt.c2, &f);
+                finished[i] = make_float4(f * fmaf(-d, kc.k2, kc.k1), f * kc.k2, gs.a, s.m);
+                arrive_one(&fin[i]);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---- stages
+        RowPlace p = place_row<DT>(r, 0, rank, lg);
+        uint32_t slot = 0, phase = 0;
+        int64_t zero = first_row;  // the next row that is either counted or set to 0
+        uint32_t k1 = 0, k2 = 0;
+        int s1 = 0, s2 = 0;
+        bool end1 = false;
+        WarpSums sum = {-INFINITY, 0.f, 0.f};
+        // a stage's vectors, masked; past cnt -inf
+        auto take = [&](uint4 (&x)[U], int cnt, int32_t e0, int64_t row) {
+            uint32_t lo[U], hi[U];
+            if (r.mask) {  // under the wait
+                const int32_t *mrow = r.mask + (size_t)row * r.mstride;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    mask_words<AE>(mrow, e0 + u * kRowUsers * AE, u < nu && tid + u * kRowUsers < cnt, lo[u], hi[u]);
+            }
+            ok = ok && mbar_wait_bounded(&full[slot], phase, status);
+            const uint4 *in = ring + slot * kRowStage + tid;
+            if (cnt >= stage) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u < nu) x[u] = in[u * kRowUsers];
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    x[u] = none_vec<DT>();
+                    if (u < nu && tid + u * kRowUsers < cnt) x[u] = in[u * kRowUsers];
+                }
+            }
+            if (r.mask) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u < nu) mask_vec<DT>(x[u], mask_bits<AE>(lo[u], hi[u], e0 + u * kRowUsers * AE));
+            }
+        };
+        auto release = [&]() {  // the warp has its vectors in registers
+            __syncwarp();
+            if (lane == 0) arrive_one(&empty[slot]);
+            if (++slot == S) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        };
+        auto extra = [&](int64_t row, int32_t ie) {  // the element outside the vectors
+            if (r.mask && !allowed_bit(r.mask + (size_t)row * r.mstride, ie)) return -INFINITY;
+            return load_clean(logits_at(row), DT, ie);
+        };
+        for (int g = 0;; ++g) {
+            if (!end1) {
+                const uint32_t i = k1 % RING;
+                if (s1 == 0) {
+                    ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_bounded(&known[i], (k1 / RING) & 1u, status));
+                    const int64_t row = ok ? meta[i].row : r.B;
+                    end1 = row >= r.B;
+                    for (; zero < row; zero += step) {  // rows that do not count
+                        if (rank == 0 && tid == 0) skip_row<MODE>(r, zero);
+                        if (!GRAD) continue;
+                        const RowPlace q = place_row<DT>(r, zero, rank, lg);
+                        uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)zero * r.gstride * E::SIZE;
+                        if (((reinterpret_cast<uintptr_t>(logits_at(zero)) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) ==
+                            0) {
+                            for (int v = tid; v < q.nv; v += kRowUsers)
+                                __stcs(reinterpret_cast<uint4 *>(gp + (size_t)(q.first + (v - tid) * AE) * E::SIZE),
+                                       make_uint4(0u, 0u, 0u, 0u));
+                        } else {
+                            for (int v = tid; v < q.nv * AE; v += kRowUsers)
+                                Pack<DT>::store1(gp, q.first - tid * AE + v, 0.f);
+                        }
+                        if (q.ie >= 0) Pack<DT>::store1(gp, q.ie, 0.f);
+                    }
+                    zero = row + step;
+                }
+                if (!end1) {
+                    const int64_t row = meta[i].row;
+                    const float c2 = meta[i].c2;
+                    if (!fixed) p = place_row<DT>(r, row, rank, lg);
+                    uint4 x[U];
+                    take(x, p.nv - s1 * stage, p.first + s1 * stage * AE, row);
+                    float top = largest<DT>(x, nu);
+                    release();
+                    if (top != top) {  // NaN counts as -inf
+                        clean_all<DT>(x, nu);
+                        top = largest<DT>(x, nu);
+                        if (lane == 0) dirty[i] = 1u;
+                    }
+                    float xe = -INFINITY;
+                    if (s1 == 0) {
+                        if (p.ie >= 0) xe = extra(row, p.ie);
+                        top = warp_max(fmaxf(top, xe));
+                    }
+                    if (top > sum.m) raise<ENT>(sum, top, c2);
+                    if (sum.m > -INFINITY) {
+                        const Ref ref = make_ref(sum.m, c2);
+                        if (ref.near)
+                            add_vecs<DT, ENT, true>(x, nu, ref, sum);
+                        else
+                            add_vecs<DT, ENT, false>(x, nu, ref, sum);
+                        if (s1 == 0 && p.ie >= 0) {
+                            unsigned long long e, y;
+                            if (ref.near)
+                                exp_pair<ENT, true>(xe, -INFINITY, ref, e, y);
+                            else
+                                exp_pair<ENT, false>(xe, -INFINITY, ref, e, y);
+                            float a, b, ignored;
+                            split_pair(e, a, ignored);
+                            split_pair(y, b, ignored);
+                            sum.Z += a;
+                            if (ENT) sum.t = fmaf(a, b, sum.t);
+                        }
+                    }
+                    if (++s1 == stages) {
+                        // the warp's sums against m itself
+                        float Z = warp_sum_f32(sum.Z), t = ENT ? warp_sum_f32(sum.t) : 0.f;
+                        if (sum.m > -INFINITY) {
+                            float f;
+                            const float d = near_shift(sum.m, c2, &f);
+                            if (ENT) t = f * fmaf(-d, Z, t);
+                            Z *= f;
+                        }
+                        // rows are finished in order; half a ring behind at most
+                        if (!GRAD && k1 >= RING / 2)
+                            ok = ok && mbar_wait_bounded(&fin[(k1 - RING / 2) % RING], ((k1 - RING / 2) / RING) & 1u,
+                                                         status);
+                        if (lane == 0) {
+                            sums[i][warp] = make_float4(sum.m, Z, t, 0.f);
+                            arrive_one(&summed[i]);
+                        }
+                        sum = {-INFINITY, 0.f, 0.f};
+                        s1 = 0;
+                        ++k1;
+                    }
+                }
+            }
+            if (GRAD && g >= delay && k2 < k1) {
+                const uint32_t i = k2 % RING;
+                if (s2 == 0) ok = ok && mbar_wait_bounded(&fin[i], (k2 / RING) & 1u, status);
+                const int64_t row = meta[i].row;
+                const float4 k = finished[i];
+                const float xt = meta[i].xt;
+                const bool live = xt > -INFINITY;
+                const Ref ref = make_ref(live ? k.w : 0.f, meta[i].c2);
+                const RowPlace q = fixed ? p : place_row<DT>(r, row, rank, lg);
+                uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)row * r.gstride * E::SIZE;
+                const bool same =
+                    ((reinterpret_cast<uintptr_t>(logits_at(row)) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0;
+                const int cnt = q.nv - s2 * stage;
+                uint4 x[U];
+                take(x, cnt, q.first + s2 * stage * AE, row);
+                release();
+                if (dirty[i]) clean_all<DT>(x, nu);
+                uint8_t *gv = gp + (size_t)(q.first + s2 * stage * AE) * E::SIZE;
+                if (live && ref.near && same && cnt >= stage) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (u < nu) {
+                            grad_vec<DT, ENT, true>(x[u], ref, k.x, k.y);
+                            __stcs(reinterpret_cast<uint4 *>(gv) + u * kRowUsers, x[u]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (u < nu && tid + u * kRowUsers < cnt) {
+                            if (!live)
+                                x[u] = make_uint4(0u, 0u, 0u, 0u);
+                            else if (ref.near)
+                                grad_vec<DT, ENT, true>(x[u], ref, k.x, k.y);
+                            else
+                                grad_vec<DT, ENT, false>(x[u], ref, k.x, k.y);
+                            if (same) {
+                                __stcs(reinterpret_cast<uint4 *>(gv) + u * kRowUsers, x[u]);
+                            } else {
+                                float f[AE];
+                                E::unpack(x[u], f);
+#pragma unroll
+                                for (int j = 0; j < AE; ++j) Pack<DT>::store1(gv, u * kRowUsers * AE + j, f[j]);
+                            }
+                        }
+                    }
+                }
+                if (s2 == 0 && q.ie >= 0)
+                    Pack<DT>::store1(gp, q.ie, live ? ref_grad<ENT>(extra(row, q.ie), ref, k.x, k.y) : 0.f);
+                if (live) {
+                    // the token's element once more, by the thread that wrote it
+                    const int32_t tok = (int32_t)meta[i].tok, rel = tok - (q.first - tid * AE) - s2 * stage * AE;
+                    const bool mine = (s2 == 0 && q.ie == tok) || (rel >= 0 && rel < stage * AE && rel < cnt * AE &&
+                                                                   (rel / AE) % kRowUsers == tid);
+                    if (mine) Pack<DT>::store1(gp, tok, __fadd_rn(ref_grad<ENT>(xt, ref, k.x, k.y), k.z));
+                }
+                if (++s2 == stages) {
+                    s2 = 0;
+                    ++k2;
+                }
+            }
+            if (end1 && (!GRAD || k2 == k1)) break;
+        }
+    }
+    __syncwarp();
+    if (C > 1) cluster_sync();  // no CTA leaves while another may still write to it
+}
+
+// ------------------------------------------------------------ the rows, held
+// The policy loss with its gradient, for rows that eight CTAs can hold: a
+// cluster of C CTAs of 512 threads keeps a row in registers, 8 vectors a
+// thread (64 KB a CTA: four CTAs for 128,256 logits in 16 bits, eight in fp32).
+// A CTA's share comes by one bulk copy into shared memory and goes to registers
+// at once; the next row's copy starts as soon as every warp has read it.  The
+// warps send their sums to every CTA of the cluster (asynchronous stores that
+// count on the receiver's barrier).  HBM reads every logit once and L2 is not
+// needed, where the streamed form reads it a second time from L2, which keeps
+// little of it beside the gradient's stores: 4,096 x 128,256 bf16 take 434 us
+// there.
+//
+// Two CTAs share an SM, so that one's exchange passes under the other's
+// arithmetic, and the issue slots decide (13 instructions an element where the
+// first form took 27).  What a row needs once, one warp does for all, another
+// one each row: one starts the next copy, one looks for the row after it, one
+// joins the sums and finishes.  4,096 x 128,256 bf16, an eighth of the rows
+// skipped: 353 us, 5.6 TB/s; with 256 threads of 16 vectors 366 us, with four
+// CTAs of 256 threads an SM, and clusters of 16 for fp32, 347 us.
+constexpr int kHeldVecs = 8, kHeldThreads = 512, kHeldWarps = kHeldThreads / 32;
+constexpr int kHeldCluster = 8;
+constexpr size_t kHeldSmem = (size_t)kHeldThreads * kHeldVecs * 16;
+
+// The first row from b on (by steps) that counts, by one warp; row = B if none.
+template <int DT>
+__device__ __forceinline__ RowMeta find_row(const RowLossArgs &r, int64_t b, int64_t step) {
+    RowMeta m = {r.B, -1, 0.f, 1.f, 1.f, -INFINITY};
+    float w = 0.f;
+    int64_t tok = 0;
+    while (b < r.B && !row_named(r, b, &w, &tok)) b += step;
+    if (b < r.B) {
+        m.row = b;
+        m.tok = tok;
+        m.w = w;
+        m.T = row_temperature(r, b);
+        m.c2 = kLog2eL / m.T;
+        m.xt = token_logit(r, static_cast<const uint8_t *>(r.logits) + (size_t)b * r.stride * Elem<DT>::SIZE,
+                           r.mask ? r.mask + (size_t)b * r.mstride : nullptr, DT, tok);
+    }
+    return m;
+}
+
+template <int DT, bool ENT>
+__global__ void __launch_bounds__(kHeldThreads, 2) row_held_kernel(RowLossArgs r, int lg, unsigned int *status) {
+    using E = Elem<DT>;
+    constexpr int AE = E::AE, U = kHeldVecs, THREADS = kHeldThreads, WARPS = kHeldWarps;
+    extern __shared__ __align__(128) uint4 ring[];               // the CTA's vectors of a row
+    __shared__ float4 stats[2][kHeldCluster * WARPS];            // the cluster's warps, this row and the next
+    __shared__ RowMeta meta[4];
+    __shared__ float4 finished;                                  // k1, k2, a and m
     __shared__ uint64_t full, empty, joined[2];
-    __shared__ float4 finished;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t C = 1u << lg, rank = C > 1 ? cluster_ctarank() : 0u;
     const int64_t step = gridDim.x >> lg;
-    int64_t row = blockIdx.x >> lg;
-    const uint4 none = DT == 0 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
-                       : DT == 1 ? make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u)
-                                 : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+    int64_t zero = blockIdx.x >> lg;  // the next row that is either counted or set to 0
+    const bool fixed = ((size_t)r.stride * E::SIZE) % 16 == 0;  // every row lies alike
+    RowPlace p = place_row<DT>(r, 0, rank, lg);
+    auto logits_at = [&](int64_t b) { return static_cast<const uint8_t *>(r.logits) + (size_t)b * r.stride * E::SIZE; };
+    auto fetch = [&](int64_t b) {  // by one thread: the CTA's share of a row
+        const RowPlace q = fixed ? p : place_row<DT>(r, b, rank, lg);
+        mbar_arrive_expect_tx(&full, (uint32_t)q.nv * 16u);
+        if (q.nv > 0)
+            bulk_g2s(ring, logits_at(b) + (size_t)(q.first - tid * AE) * E::SIZE, (uint32_t)q.nv * 16u, &full);
+    };
     if (tid == 0) {
         mbar_init(&full, 1);
         mbar_init(&empty, WARPS);
@@ -525,220 +971,233 @@ __global__ void __launch_bounds__(kRowThreads, 2) row_loss_kernel(RowLossArgs r,
         mbar_init(&joined[1], 1);
         mbar_init_fence();
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) buf[tid + u * THREADS] = none;
-    fence_proxy_async_smem();
+    __syncthreads();
+    if (warp == 0) {
+        const RowMeta a = find_row<DT>(r, zero, step), b = find_row<DT>(r, a.row < r.B ? a.row + step : r.B, step);
+        if (lane == 0) {
+            meta[0] = a;
+            meta[1] = b;
+            if (a.row < r.B) {
+                mbar_arrive_expect_tx(&joined[0], (uint32_t)(WARPS << lg) * 16u);
+                fetch(a.row);
+            }
+        }
+    }
     if (C > 1)
         cluster_sync();  // every CTA's barriers stand before another CTA counts on them
     else
         __syncthreads();
-    const bool fixed = ((size_t)r.stride * E::SIZE) % 16 == 0;  // every row lies alike
-    auto logits_at = [&](int64_t b) { return static_cast<const uint8_t *>(r.logits) + (size_t)b * r.stride * E::SIZE; };
-    auto zero_row = [&](int64_t b) {
-        if (rank == 0 && tid == 0) skip_row<MODE>(r, b);
-        if (!GRAD) return;
-        const RowPlace q = place_row<DT>(r, b, rank, lg);
-        uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)b * r.gstride * E::SIZE;
-        if (((reinterpret_cast<uintptr_t>(logits_at(b)) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0) {
-            for (int v = tid; v < q.nv; v += THREADS)
-                __stcs(reinterpret_cast<uint4 *>(gp + (size_t)(q.first + (v - tid) * AE) * E::SIZE),
-                       make_uint4(0u, 0u, 0u, 0u));
-        } else {
-            for (int i = tid; i < q.nv * AE; i += THREADS) Pack<DT>::store1(gp, q.first - tid * AE + i, 0.f);
-        }
-        if (q.ie >= 0) Pack<DT>::store1(gp, q.ie, 0.f);
-    };
-    auto fetch = [&](int64_t b, const RowPlace &q) {  // by thread 0: the CTA's share of a row
-        mbar_arrive_expect_tx(&full, (uint32_t)q.nv * 16u);
-        if (q.nv > 0)
-            bulk_g2s(buf, logits_at(b) + (size_t)(q.first - tid * AE) * E::SIZE, (uint32_t)q.nv * 16u, &full);
-    };
-    float w;
-    int64_t tok;
-    while (row < r.B && !row_named(r, row, &w, &tok)) {
-        zero_row(row);
-        row += step;
-    }
-    RowPlace p = place_row<DT>(r, row < r.B ? row : 0, rank, lg);
-    if (row < r.B && tid == 0) fetch(row, p);
+    pdl_launch_dependents();  // the next kernel waits for this one's end before it reads
     bool ok = true;  // a wait that ran out ends all waiting; the status word tells
-    for (uint32_t turn = 0; row < r.B; ++turn) {
+    for (uint32_t turn = 0;; ++turn) {
         const uint32_t half = turn & 1u;
-        if (tid == 0) mbar_arrive_expect_tx(&joined[half], (uint32_t)(WARPS << lg) * 16u);
-        const uint8_t *rp = logits_at(row);
+        const RowMeta &mt = meta[turn & 3u];
+        const int64_t row = mt.row;
+        for (; zero < row; zero += step) {  // rows that do not count
+            if (rank == 0 && tid == 0) skip_row<0>(r, zero);
+            const RowPlace q = place_row<DT>(r, zero, rank, lg);
+            uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)zero * r.gstride * E::SIZE;
+            if (((reinterpret_cast<uintptr_t>(logits_at(zero)) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0) {
+                for (int v = tid; v < q.nv; v += THREADS)
+                    __stcs(reinterpret_cast<uint4 *>(gp + (size_t)(q.first + (v - tid) * AE) * E::SIZE),
+                           make_uint4(0u, 0u, 0u, 0u));
+            } else {
+                for (int v = tid; v < q.nv * AE; v += THREADS) Pack<DT>::store1(gp, q.first - tid * AE + v, 0.f);
+            }
+            if (q.ie >= 0) Pack<DT>::store1(gp, q.ie, 0.f);
+        }
+        if (row >= r.B) break;
+        zero = row + step;
+        const float c2 = mt.c2;
         const int32_t *mrow = r.mask ? r.mask + (size_t)row * r.mstride : nullptr;
-        const float T = row_temperature(r, row), c2 = kLog2eL / T;
-        const float xt = token_logit(r, rp, mrow, DT, tok);
-        float xe = -INFINITY;
-        if (p.ie >= 0 && (!mrow || allowed_bit(mrow, p.ie))) xe = load_clean(rp, DT, p.ie);
-        // the next row that counts
-        int64_t next = row + step, tok_next = -1;
-        float w_next = 0.f;
-        while (next < r.B && !row_named(r, next, &w_next, &tok_next)) next += step;
-        const RowPlace pn = fixed || next >= r.B ? p : place_row<DT>(r, next, rank, lg);
+        if (!fixed) p = place_row<DT>(r, row, rank, lg);
         const int nu = (p.nv + THREADS - 1) / THREADS;
-
-        ok = ok && mbar_wait_bounded(&full, turn & 1u, status);
+        float xe = -INFINITY;
+        if (p.ie >= 0 && (!mrow || allowed_bit(mrow, p.ie))) xe = load_clean(logits_at(row), DT, p.ie);
         uint4 x[U];
-        // The token's logit belongs to the row, so it may raise a warp's
-        // reference; and a warp has then read it before it sends its sums,
-        // after which another CTA may write a gradient over it.
-        float mx = fmaxf(xe, xt);
+        {
+            uint32_t lo[U], hi[U];
+            if (mrow) {  // under the wait
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (u < nu) {
-                x[u] = buf[tid + u * THREADS];
-                if (mrow && tid + u * THREADS < p.nv) {
-                    const int32_t e = p.first + u * THREADS * AE;
-                    const uint32_t lo = (uint32_t)__ldg(mrow + (e >> 5));
-                    const uint32_t hi = ((e & 31) + AE > 32) ? (uint32_t)__ldg(mrow + (e >> 5) + 1) : 0u;
-                    mask_vec<DT>(x[u], __funnelshift_r(lo, hi, (uint32_t)(e & 31)) & ((1u << AE) - 1u));
-                }
-                Pack<DT>::clean(x[u]);
-                mx = fmaxf(mx, Pack<DT>::vmax(x[u]));
+                for (int u = 0; u < U; ++u)
+                    mask_words<AE>(mrow, p.first + u * THREADS * AE, tid + u * THREADS < p.nv, lo[u], hi[u]);
+            }
+            ok = ok && mbar_wait_bounded(&full, turn & 1u, status);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                x[u] = none_vec<DT>();
+                if (u + 1 < nu || tid + u * THREADS < p.nv) x[u] = ring[tid + u * THREADS];
+            }
+            if (mrow) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u < nu) mask_vec<DT>(x[u], mask_bits<AE>(lo[u], hi[u], p.first + u * THREADS * AE));
             }
         }
-        if (pn.nv < p.nv) {  // shared memory past the next row's share is padding again
-            __syncthreads();
-            if (tid < p.nv - pn.nv) buf[pn.nv + tid] = none;
+        float top = largest<DT>(x, nu);
+        if (top != top) {  // NaN counts as -inf
+            clean_all<DT>(x, nu);
+            top = largest<DT>(x, nu);
         }
-        mx = warp_max(mx);
+        top = warp_max(fmaxf(top, xe));
         if (lane == 0) arrive_one(&empty);
-        if (tid == 0) {
-            ok = ok && mbar_wait_bounded(&empty, turn & 1u, status);
+        if (warp == (int)(turn % WARPS) && lane == 0) {  // the next row's copy
+            const int64_t next = meta[(turn + 1u) & 3u].row;
             if (next < r.B) {
+                mbar_arrive_expect_tx(&joined[half ^ 1u], (uint32_t)(WARPS << lg) * 16u);
+                ok = ok && mbar_wait_bounded(&empty, turn & 1u, status);
                 fence_proxy_async_smem();
-                fetch(next, pn);
+                fetch(next);
             }
         }
         __syncwarp();
-        float sz = 0.f, st = 0.f;
-        if (mx > -INFINITY) {
-            const unsigned long long negm = pair_of(-mx, -mx), cc = pair_of(c2, c2);
-            unsigned long long Z = pair_of(0.f, 0.f), t = Z;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (u < nu) {
-                    float f[AE];
-                    E::unpack(x[u], f);
-#pragma unroll
-                    for (int q = 0; q < AE; q += 2) {
-                        unsigned long long e, y;
-                        exp_pair<ENT>(f[q], f[q + 1], negm, cc, e, y);
-                        Z = add2(Z, e);
-                        if (ENT) t = fma2(e, y, t);
-                    }
-                }
-            }
+        WarpSums sum = {top, 0.f, 0.f};
+        if (top > -INFINITY) {
+            const Ref ref = make_ref(top, c2);
+            if (ref.near)
+                add_vecs<DT, ENT, true>(x, nu, ref, sum);
+            else
+                add_vecs<DT, ENT, false>(x, nu, ref, sum);
             if (p.ie >= 0) {
                 unsigned long long e, y;
-                exp_pair<ENT>(xe, -INFINITY, negm, cc, e, y);
-                Z = add2(Z, e);
-                if (ENT) t = fma2(e, y, t);
+                if (ref.near)
+                    exp_pair<ENT, true>(xe, -INFINITY, ref, e, y);
+                else
+                    exp_pair<ENT, false>(xe, -INFINITY, ref, e, y);
+                float a, b, ignored;
+                split_pair(e, a, ignored);
+                split_pair(y, b, ignored);
+                sum.Z += a;
+                if (ENT) sum.t = fmaf(a, b, sum.t);
             }
-            float a, b;
-            split_pair(Z, a, b);
-            sz = warp_sum_f32(a + b);
-            if (ENT) {
-                split_pair(t, a, b);
-                st = warp_sum_f32(a + b);
+            // the warp's sums against its largest logit itself
+            float f;
+            const float d = near_shift(top, c2, &f);
+            sum.Z = warp_sum_f32(sum.Z);
+            if (ENT) sum.t = f * fmaf(-d, sum.Z, warp_sum_f32(sum.t));
+            sum.Z *= f;
+        }
+        // These slots were last read two rows ago: a warp sends after its CTA
+        // has finished the row before, for which every CTA had sent, and so
+        // finished the row before that.
+        if (lane < (int)C)
+            send_stat(&stats[half][(int)rank * WARPS + warp], &joined[half], (uint32_t)lane, top, sum.Z, sum.t);
+        if (warp == (int)((turn + 3u) % WARPS)) {  // finish the row
+            ok = ok && mbar_wait_bounded(&joined[half], (turn >> 1) & 1u, status);
+            const int n = WARPS << lg;
+            RowStat s = {-INFINITY, 0.f, 0.f};
+            for (int i = lane; i < n; i += 32) s.m = fmaxf(s.m, stats[half][i].x);
+            s.m = warp_max(s.m);
+            for (int i = lane; i < n; i += 32) {
+                const float4 v = stats[half][i];
+                const float d = v.x == s.m ? 0.f : fmaxf((v.x - s.m) * c2, kLowExp), f = ex2_approx(d);
+                s.Z = fmaf(v.y, f, s.Z);
+                if (ENT) s.t = fmaf(fmaf(v.y, d, v.z), f, s.t);
+            }
+            s.Z = s.m == INFINITY ? __int_as_float(0x7FC00000) : warp_sum_f32(s.Z);
+            if (ENT) s.t = warp_sum_f32(s.t);
+            const RowScalars gs = finish_row<0, ENT>(r, row, s, mt.xt, mt.T, mt.w, rank == 0 && lane == 0);
+            if (lane == 0) {
+                // a row that does not count (its token masked) gets zeros
+                const GradCoef kc = mt.xt > -INFINITY ? grad_coef<ENT>(gs, s) : GradCoef{0.f, 0.f};
+                float f;
+                const float d = near_shift(s.m, c2, &f);
+                finished = make_float4(f * fmaf(-d, kc.k2, kc.k1), f * kc.k2, gs.a, s.m);
             }
         }
-        // These slots were last read two rows ago: a warp sends a row's sums
-        // only after its CTA has finished the row before, for which it had
-        // every other CTA's sums of that row.
-        if (lane < (int)C) send_stat(&stats[half][(int)rank * WARPS + warp], &joined[half], (uint32_t)lane, mx, sz, st);
-        if (warp == 0) {
-            ok = ok && mbar_wait_bounded(&joined[half], (turn >> 1) & 1u, status);
-            if (GRAD || rank == 0) {
-                const int n = WARPS << lg;
-                RowStat s = {-INFINITY, 0.f, 0.f};
-                for (int i = lane; i < n; i += 32) s.m = fmaxf(s.m, stats[half][i].x);
-                s.m = warp_max(s.m);
-                for (int i = lane; i < n; i += 32) {
-                    const float4 v = stats[half][i];
-                    const float d = v.x == s.m ? 0.f : fmaxf((v.x - s.m) * c2, kLowExp), f = ex2_approx(d);
-                    s.Z = fmaf(v.y, f, s.Z);
-                    if (ENT) s.t = fmaf(fmaf(v.y, d, v.z), f, s.t);
-                }
-                s.Z = s.m == INFINITY ? __int_as_float(0x7FC00000) : warp_sum_f32(s.Z);
-                if (ENT) s.t = warp_sum_f32(s.t);
-                const RowScalars gs = finish_row<MODE, ENT>(r, row, s, xt, T, w, rank == 0 && lane == 0);
-                if (GRAD && lane == 0) {
-                    // a row that does not count (its token masked) gets zeros
-                    const GradCoef kc = xt > -INFINITY ? grad_coef<ENT>(gs, s) : GradCoef{0.f, 0.f};
-                    finished = make_float4(kc.k1, kc.k2, gs.a, s.m);
-                }
-            }
+        if (warp == (int)((turn + 6u) % WARPS)) {  // look two rows ahead
+            const int64_t next = meta[(turn + 1u) & 3u].row;
+            const RowMeta m2 = find_row<DT>(r, next < r.B ? next + step : r.B, step);
+            if (lane == 0) meta[(turn + 2u) & 3u] = m2;
         }
         __syncthreads();
-        if (GRAD) {
-            const float4 fin = finished;
-            const GradCoef k = {fin.x, fin.y};
-            const float m = fin.w;
-            const bool live = xt > -INFINITY;
-            uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)row * r.gstride * E::SIZE;
-            const bool same = ((reinterpret_cast<uintptr_t>(rp) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0;
-            uint8_t *gv = gp + (size_t)p.first * E::SIZE;
-            const unsigned long long negm = pair_of(-m, -m), cc = pair_of(c2, c2), k1 = pair_of(k.k1, k.k1),
-                                     k2 = pair_of(k.k2, k.k2);
+        const float4 k = finished;
+        const bool live = mt.xt > -INFINITY;
+        const Ref ref = make_ref(live ? k.w : 0.f, c2);
+        uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)row * r.gstride * E::SIZE;
+        const bool same = ((reinterpret_cast<uintptr_t>(logits_at(row)) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0;
+        uint8_t *gv = gp + (size_t)p.first * E::SIZE;
+        if (live && ref.near && same) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (u < nu) {
-                    float f[AE];
-                    E::unpack(x[u], f);
+                    grad_vec<DT, ENT, true>(x[u], ref, k.x, k.y);
+                    if (u + 1 < nu || tid + u * THREADS < p.nv)
+                        __stcs(reinterpret_cast<uint4 *>(gv) + u * THREADS, x[u]);
+                }
+            }
+        } else {
 #pragma unroll
-                    for (int q = 0; q < AE; q += 2) {
-                        unsigned long long e, y;
-                        exp_pair<ENT>(f[q], f[q + 1], negm, cc, e, y);
-                        split_pair(mul2(e, ENT ? fma2(k2, y, k1) : k1), f[q], f[q + 1]);
-                    }
-                    if (!live) {
+            for (int u = 0; u < U; ++u) {
+                if (tid + u * THREADS < p.nv) {
+                    if (!live)
+                        x[u] = make_uint4(0u, 0u, 0u, 0u);
+                    else if (ref.near)
+                        grad_vec<DT, ENT, true>(x[u], ref, k.x, k.y);
+                    else
+                        grad_vec<DT, ENT, false>(x[u], ref, k.x, k.y);
+                    if (same) {
+                        __stcs(reinterpret_cast<uint4 *>(gv) + u * THREADS, x[u]);
+                    } else {
+                        float f[AE];
+                        E::unpack(x[u], f);
 #pragma unroll
-                        for (int q = 0; q < AE; ++q) f[q] = 0.f;
-                    }
-                    if (tid + u * THREADS < p.nv) {
-                        if (same) {
-                            __stcs(reinterpret_cast<uint4 *>(gv) + u * THREADS, Pack<DT>::vec(f));
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < AE; ++q) Pack<DT>::store1(gv, u * THREADS * AE + q, f[q]);
-                        }
+                        for (int j = 0; j < AE; ++j) Pack<DT>::store1(gv, u * THREADS * AE + j, f[j]);
                     }
                 }
             }
-            if (p.ie >= 0) Pack<DT>::store1(gp, p.ie, live ? grad_el<ENT>(xe, m, c2, k) : 0.f);
-            if (live) {
-                // the token's element once more, by the thread that wrote it
-                const int32_t rel = (int32_t)tok - (p.first - tid * AE);
-                const bool mine = p.ie == (int32_t)tok ||
-                                  (rel >= 0 && rel < p.nv * AE && (rel / AE) % THREADS == tid);
-                if (mine) Pack<DT>::store1(gp, tok, __fadd_rn(grad_el<ENT>(xt, m, c2, k), fin.z));
-            }
         }
-        for (row += step; row < next; row += step) zero_row(row);
-        row = next;
-        w = w_next;
-        tok = tok_next;
-        p = pn;
+        if (p.ie >= 0) Pack<DT>::store1(gp, p.ie, live ? ref_grad<ENT>(xe, ref, k.x, k.y) : 0.f);
+        if (live) {
+            // the token's element once more, by the thread that wrote it
+            const int32_t tok = (int32_t)mt.tok, rel = tok - (p.first - tid * AE);
+            const bool mine = p.ie == tok || (rel >= 0 && rel < p.nv * AE && (rel / AE) % THREADS == tid);
+            if (mine) Pack<DT>::store1(gp, tok, __fadd_rn(ref_grad<ENT>(mt.xt, ref, k.x, k.y), k.z));
+        }
     }
     if (C > 1) cluster_sync();  // no CTA leaves while another may still write to it
 }
 
 // ------------------------------------------------------------ known sums
+// Block sum of doubles in a fixed order; the result on every thread.  These
+// sums are over rows, not logits (thousands of terms, not hundreds of
+// millions), so fp64 costs nothing and a sequence's log-ratio keeps the
+// differences that cancel in it.
+template <int THREADS>
+__device__ double block_sum(double v, double *sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    __syncthreads();  // sh may hold an earlier sum
+    if (lane == 0) sh[warp] = v;
+    __syncthreads();
+    double s = 0.0;
+    for (int i = 0; i < THREADS / 32; ++i) s += sh[i];
+    return s;
+}
+
 // The gradient of a row whose m, Z and coefficient are known:
 // coef / T (1{j = i} - p_j), element by element; grid (slices of a row, rows).
 // Rows are taken last to first: the sums' pass ended with the last ones,
-// whose logits are the ones still in L2.
+// whose logits are the ones still in L2.  The first CTA also writes the loss,
+// the mean of the pairs' losses, in a fixed order.
 constexpr int kKnownThreads = 256;
 constexpr int kKnownU = 4;
 
 template <int DT>
-__global__ void __launch_bounds__(kKnownThreads) row_grad_kernel(RowLossArgs r) {
+__global__ void __launch_bounds__(kKnownThreads) row_grad_kernel(RowLossArgs r, const float *pair_loss, int64_t pairs,
+                                                                 float *loss) {
     using E = Elem<DT>;
     constexpr int AE = E::AE;
+    __shared__ double sh[kKnownThreads / 32];
     pdl_wait_primary();
     const int tid = threadIdx.x;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+        double s = 0.0;
+        for (int64_t i = tid; i < pairs; i += kKnownThreads) s += (double)pair_loss[i];
+        s = block_sum<kKnownThreads>(s, sh);
+        if (tid == 0) *loss = pairs > 0 ? (float)(s / (double)pairs) : 0.f;
+    }
     const int64_t row = r.B - 1 - (int64_t)blockIdx.y - (int64_t)blockIdx.z * gridDim.y;
     if (row < 0) return;
     const uint8_t *rp = static_cast<const uint8_t *>(r.logits) + (size_t)row * r.stride * E::SIZE;

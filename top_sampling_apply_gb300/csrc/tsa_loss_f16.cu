@@ -3,21 +3,20 @@
 
 namespace tsa {
 
-namespace {
-
-template <int MODE, bool GRAD, bool ENT>
-const void *pick(int form) {
+const void *row_loss_kernel_f16(int mode, bool grad, bool ent) {
     using namespace loss_detail;
-    return form == 1 ? reinterpret_cast<const void *>(&row_loss_kernel<1, MODE, GRAD, ENT>)
-                     : reinterpret_cast<const void *>(&row_loss_stream_kernel<1, MODE, GRAD, ENT>);
+    if (mode == 1) return reinterpret_cast<const void *>(&row_loss_kernel<1, 1, false, false>);
+    if (grad)
+        return ent ? reinterpret_cast<const void *>(&row_loss_kernel<1, 0, true, true>)
+                   : reinterpret_cast<const void *>(&row_loss_kernel<1, 0, true, false>);
+    return ent ? reinterpret_cast<const void *>(&row_loss_kernel<1, 0, false, true>)
+               : reinterpret_cast<const void *>(&row_loss_kernel<1, 0, false, false>);
 }
 
-}  // namespace
-
-const void *row_loss_kernel_f16(int mode, bool grad, bool ent, int form) {
-    if (mode == 1) return pick<1, false, false>(form);
-    if (grad) return ent ? pick<0, true, true>(form) : pick<0, true, false>(form);
-    return ent ? pick<0, false, true>(form) : pick<0, false, false>(form);
+const void *row_held_kernel_f16(bool ent) {
+    using namespace loss_detail;
+    return ent ? reinterpret_cast<const void *>(&row_held_kernel<1, true>)
+               : reinterpret_cast<const void *>(&row_held_kernel<1, false>);
 }
 
 const void *row_grad_kernel_f16() { return reinterpret_cast<const void *>(&loss_detail::row_grad_kernel<1>); }

@@ -123,8 +123,9 @@ int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t 
     if (P < 0 || P > 0x3FFFFFFFll) return TSA_ERR_SHAPE;
     if (!isfinite(beta) || !isfinite(margin) || !(label_smoothing >= 0.f && label_smoothing <= 1.f))
         return TSA_ERR_VALUE;
-    if (P > 0 && (!seq_start || !loss_out || !pair_loss_out || !reward_out)) return TSA_ERR_NULL;
+    if (P > 0 && (!seq_start || !pair_loss_out || !reward_out)) return TSA_ERR_NULL;
     if (N > 0 && (!tokens || !logprob_out)) return TSA_ERR_NULL;
+    if ((P > 0 || N > 0) && !loss_out) return TSA_ERR_NULL;
     if (!aligned(tokens, 8) || !aligned(seq_start, 8) || !aligned(weight, 4) || !aligned(ref_logprob, 4) ||
         !aligned(loss_out, 4) || !aligned(pair_loss_out, 4) || !aligned(reward_out, 4) || !aligned(logprob_out, 4))
         return TSA_ERR_ALIGN;
@@ -169,13 +170,14 @@ int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t 
         p.coef = a.coef;
         if (pair_launch(p, a, s) != 0) return TSA_ERR_CUDA;
     }
-    if (loss_out && weighted_sum_launch(pair_loss_out, nullptr, P > 0 ? (float)(1.0 / (double)P) : 0.f, P, loss_out,
-                                        s) != 0)
-        return TSA_ERR_CUDA;
-    if (N == 0 || !grad_out) return TSA_OK;
+    if (N == 0 || !grad_out) {
+        if (!loss_out) return TSA_OK;
+        const float each_pair = P > 0 ? (float)(1.0 / (double)P) : 0.f;
+        return weighted_sum_launch(pair_loss_out, nullptr, each_pair, P, loss_out, s) == 0 ? TSA_OK : TSA_ERR_CUDA;
+    }
     a.grad = grad_out;
     a.gstride = grad_row_stride;
-    return row_grad_launch(a, dtype, s) == 0 ? TSA_OK : TSA_ERR_CUDA;
+    return row_grad_launch(a, dtype, pair_loss_out, P, loss_out, s) == 0 ? TSA_OK : TSA_ERR_CUDA;
 }
 
 int tsa_adamw_step(const tsa_adamw_tensor *tensors, int64_t count, tsa_dtype param_dtype, tsa_dtype grad_dtype,
