@@ -106,6 +106,13 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
 
 __device__ unsigned int g_lm_logprob_status;
 
+// x = z if a == b: a selection that keeps an array's elements in registers
+// (written as a loop of ifs it becomes an indexed array in local memory, which
+// every pass would have to fill).
+__device__ __forceinline__ void select_if(float &x, float z, int a, int b) {
+    asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, %3;\n\tselp.f32 %0, %1, %0, p;\n\t}" : "+f"(x) : "f"(z), "r"(a), "r"(b));
+}
+
 // A bounded wait whose outcome the whole warp shares.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, &g_lm_logprob_status));
@@ -115,18 +122,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
 // One persistent CTA an SM.  Warp 0 fetches tiles of 64 columns of H by TMA
 // into a ring of stages, warp 1 issues the products, and warps 2 to 5 reduce
 // the finished scores from one half of tensor memory while the next tile's
-// products fill the other half.
+// products fill the other half (warps 2 to 9 where the scores are many: two
+// for each quarter of the lanes, a half of the columns each).
 //
 // ROWS = false (few rows): the 128 lanes of tensor memory are vocabulary
 // entries and the N columns are the hidden rows, so the weight is all that
-// moves and nothing of the products is padding but N's remainder.  A thread
-// keeps one (m, Z) a hidden row over all its CTA's tiles; one part a CTA.
+// moves and nothing of the products is padding but N's remainder.  The
+// vocabulary is cut into one run of rows a CTA, a multiple of 32, so that every
+// SM moves the same bytes (whole tiles of 128 would leave a fifth of them idle
+// at V = 32,000); a tile's copies are 32 rows each, and a run's last tile takes
+// only the ones it needs.  A thread keeps one (m, Z) a hidden row over all its
+// CTA's tiles; one part a CTA.
 // ROWS = true: the lanes are 128 hidden rows and the columns N vocabulary
-// entries; a thread reduces its row's N scores by itself.  Tiles go through
-// the hidden rows first, so that a weight tile is fetched from HBM once and
-// from L2 by the other row blocks.  One part a tile of the vocabulary.
-constexpr int kTcThreads = 192;
+// entries; a thread reduces N / 2 of its row's scores by itself, 32 at a time
+// from registers while the next 32 come.  Tiles go through the hidden rows
+// first, so that a weight tile is fetched from HBM once and from L2 by the
+// other row blocks.  One part for every N / 2 entries of the vocabulary.
 constexpr int kTcK = 64;
+template <bool ROWS>
+constexpr int kTcThreads = ROWS ? 320 : 192;  // eight or four warps take the scores
 
 template <int N, bool ROWS, int STAGES>
 struct TcShape {
@@ -139,17 +153,23 @@ struct TcShape {
 };
 
 template <int N, bool ROWS, int STAGES>
-__global__ void __launch_bounds__(kTcThreads, 1) lm_logprob_kernel(const __grid_constant__ CUtensorMap map_a,
+__global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const __grid_constant__ CUtensorMap map_a,
                                                                    const __grid_constant__ CUtensorMap map_b,
-                                                                   LmLogprobArgs a, int64_t tiles, int row_blocks) {
+                                                                   LmLogprobArgs a, int64_t tiles, int row_blocks, int64_t run) {
     using S = TcShape<N, ROWS, STAGES>;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[STAGES], empty[STAGES], done[2], drained[2], last;
     __shared__ uint32_t tmem_slot;
     __shared__ float2 s_part[4][ROWS ? 1 : N];
+    __shared__ __align__(16) float s_bias[ROWS ? 8 : 1][ROWS ? N / 2 : 4];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kblocks = (int)((a.H + kTcK - 1) / kTcK);
+    // this CTA's vocabulary rows (few hidden rows), or tiles
+    const int64_t v_first = ROWS ? 0 : (int64_t)blockIdx.x * run;
+    const int64_t v_end = ROWS || v_first + run > a.V ? a.V : v_first + run;
+    const int64_t t_first = ROWS ? blockIdx.x : 0, t_step = ROWS ? gridDim.x : 1;
+    const int64_t t_end = ROWS ? tiles : (v_end - v_first + 127) / 128;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full[i], 1);
@@ -157,7 +177,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lm_logprob_kernel(const __grid_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&done[i], 1);
-            mbar_init(&drained[i], 128);
+            mbar_init(&drained[i], ROWS ? 256 : 128);
         }
         mbar_init(&last, 1);
         mbar_init_fence();
@@ -166,14 +186,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) lm_logprob_kernel(const __grid_
     mma_fence_before();
     __syncthreads();
     mma_fence_after();
+    pdl_launch_dependents();  // the joining kernel waits for this one's end before it reads
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const int32_t va = ROWS ? (int32_t)(t % row_blocks) * 128 : (int32_t)t * 128;
+            for (int64_t t = t_first; ok && t < t_end; t += t_step) {
+                const int32_t va = ROWS ? (int32_t)(t % row_blocks) * 128 : (int32_t)(v_first + t * 128);
+                const int groups = ROWS || v_end - va >= 128 ? 4 : (int)((v_end - va + 31) / 32);
                 const int32_t vb = ROWS ? (int32_t)(t / row_blocks) * N : 0;
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     const uint32_t s = it % STAGES;
@@ -182,8 +204,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) lm_logprob_kernel(const __grid_
                         break;
                     }
                     uint8_t *st = ring + (size_t)s * S::STAGE;
-                    mbar_arrive_expect_tx(&full[s], S::STAGE);
-                    tma_tile(st, &map_a, kb * kTcK, va, &full[s]);
+                    if (ROWS) {
+                        mbar_arrive_expect_tx(&full[s], S::STAGE);
+                        tma_tile(st, &map_a, kb * kTcK, va, &full[s]);
+                    } else {
+                        mbar_arrive_expect_tx(&full[s], (uint32_t)(groups * (S::A_BYTES / 4) + S::B_BYTES));
+                        for (int i = 0; i < groups; ++i)
+                            tma_tile(st + i * (S::A_BYTES / 4), &map_a, kb * kTcK, va + 32 * i, &full[s]);
+                    }
                     tma_tile(st + S::A_BYTES, &map_b, kb * kTcK, vb, &full[s]);
                 }
             }
@@ -199,7 +227,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lm_logprob_kernel(const __grid_
         if (lane == 0) {
             uint32_t it = 0, j = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++j) {
+            for (int64_t t = t_first; ok && t < t_end; t += t_step, ++j) {
                 const uint32_t b = j & 1u;
                 if (!mbar_wait_bounded(&drained[b], ((j >> 1) & 1u) ^ 1u, &g_lm_logprob_status)) break;
                 mma_fence_after();
@@ -229,63 +257,117 @@ __global__ void __launch_bounds__(kTcThreads, 1) lm_logprob_kernel(const __grid_
         const float kcap = a.cap > 0.f ? 2.f * kLog2eH / a.cap : 0.f;
         uint32_t j = 0;
         if constexpr (ROWS) {
-            for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
+            const int half = (warp - 2) >> 2;
+            float *bias = s_bias[warp - 2];
+            for (int64_t t = t_first; t < t_end; t += t_step, ++j) {
                 const uint32_t b = j & 1u;
                 const int64_t row = (t % row_blocks) * 128 + quarter * 32 + lane;
-                const int64_t v0 = (t / row_blocks) * N;
+                const int64_t v0 = (t / row_blocks) * N + half * (N / 2);
                 const bool in = row < a.M;
                 const float c2 = in ? kLog2eH / row_temp(a, row) : 1.f;
                 const int64_t want = in ? __ldg(a.tokens + row) - v0 : -1;
                 const int32_t *mrow = a.mask && in ? a.mask + row * a.mstride : nullptr;
+                if (a.bias) {
+                    __syncwarp();  // the last tile's values have been read
+#pragma unroll
+                    for (int i = 0; i < N / 2; i += 32)
+                        bias[i + lane] = v0 + i + lane < a.V ? __ldg(a.bias + v0 + i + lane) : 0.f;
+                    __syncwarp();
+                }
                 if (!warp_wait(&done[b], (j >> 1) & 1u)) break;
                 mma_fence_after();
+                const uint32_t at = tmem + lane_at + b * N + half * (N / 2);
                 float2 st = make_float2(-INFINITY, 0.f);
-#pragma unroll 1
-                for (int c = 0; c < N; c += 32) {
+                // 32 scores of the row, from column c of the half
+                auto take = [&](const uint32_t (&r)[32], int c) {
                     const int64_t left = a.V - (v0 + c);
-                    if (left <= 0) break;
-                    uint32_t r[32];
-                    __syncwarp();
-                    TmemLoad<32>::ld(tmem + lane_at + b * N + c, r);
+                    if (left <= 0) return;
                     uint32_t bits = left < 32 ? (1u << left) - 1u : 0xFFFFFFFFu;
                     if (mrow) bits &= (uint32_t)__ldg(mrow + ((v0 + c) >> 5));
-                    tmem_wait_ld();
-                    float z[32], top = -INFINITY;
+                    float z[32];
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) {
-                        float x = __uint_as_float(r[q]);
-                        if (a.bias) x += left < 32 && q >= left ? 0.f : __ldg(a.bias + v0 + c + q);
-                        if (a.cap > 0.f) x = soft_cap(x, a.cap, kcap);
-                        z[q] = (bits >> q) & 1u ? fmaxf(x, -INFINITY) : -INFINITY;
-                        top = fmaxf(top, z[q]);
+                    for (int q = 0; q < 32; ++q) z[q] = __uint_as_float(r[q]);
+                    if (a.bias) {
+#pragma unroll
+                        for (int q = 0; q < 32; q += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(bias + c + q);
+                            split_pair(add2(pair_of(z[q], z[q + 1]), pair_of(f.x, f.y)), z[q], z[q + 1]);
+                            split_pair(add2(pair_of(z[q + 2], z[q + 3]), pair_of(f.z, f.w)), z[q + 2], z[q + 3]);
+                        }
+                    }
+                    if (a.cap > 0.f) {
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) z[q] = soft_cap(z[q], a.cap, kcap);
+                    }
+                    if (bits != 0xFFFFFFFFu) {
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) z[q] = (bits >> q) & 1u ? z[q] : -INFINITY;
+                    }
+                    float sum = z[0], top = z[0];  // a sum is NaN if a score is
+#pragma unroll
+                    for (int q = 1; q < 32; ++q) top = fmaxf(top, z[q]);
+                    unsigned long long all = pair_of(z[0], z[1]);
+#pragma unroll
+                    for (int q = 2; q < 32; q += 2) all = add2(all, pair_of(z[q], z[q + 1]));
+                    float s1;
+                    split_pair(all, sum, s1);
+                    sum += s1;
+                    if (sum != sum) {  // a NaN (counts as -inf), or both infinities
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) z[q] = fmaxf(z[q], -INFINITY);
+                        top = z[0];
+#pragma unroll
+                        for (int q = 1; q < 32; ++q) top = fmaxf(top, z[q]);
                     }
                     const int64_t w = want - c;
                     if (w >= 0 && w < 32) {
                         float x = -INFINITY;
 #pragma unroll
-                        for (int q = 0; q < 32; ++q)
-                            if (q == (int)w) x = z[q];
+                        for (int q = 0; q < 32; ++q) select_if(x, z[q], (int)w, q);
                         a.tok[row] = x;
                     }
                     if (top > -INFINITY) {
                         if (top > st.x) st = join(st, make_float2(top, 0.f), c2);
+                        const unsigned long long neg = pair_of(-st.x, -st.x), cc = pair_of(c2, c2);
+                        unsigned long long acc = pair_of(st.y, 0.f);
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) st.y += ex2_approx((z[q] - st.x) * c2);
+                        for (int q = 0; q < 32; q += 2) {
+                            float e0, e1;
+                            split_pair(mul2(add2(pair_of(z[q], z[q + 1]), neg), cc), e0, e1);
+                            acc = add2(acc, pair_of(ex2_approx(e0), ex2_approx(e1)));
+                        }
+                        float s0;
+                        split_pair(acc, s0, s1);
+                        st.y = s0 + s1;
                     }
+                };
+                uint32_t ra[32], rb[32];
+                __syncwarp();
+                TmemLoad<32>::ld(at, ra);
+#pragma unroll 1
+                for (int c = 0; c < N / 2; c += 64) {
+                    __syncwarp();
+                    tmem_wait_ld();
+                    TmemLoad<32>::ld(at + c + 32, rb);
+                    take(ra, c);
+                    __syncwarp();
+                    tmem_wait_ld();
+                    if (c + 64 < N / 2) TmemLoad<32>::ld(at + c + 64, ra);
+                    take(rb, c + 32);
                 }
                 mma_fence_before();
                 mbar_arrive(&drained[b]);
-                if (in) a.part[(t / row_blocks) * a.M + row] = st;
+                if (in && v0 < a.V) a.part[((t / row_blocks) * 2 + half) * a.M + row] = st;
             }
         } else {
             float2 st[N];
 #pragma unroll
             for (int q = 0; q < N; ++q) st[q] = make_float2(-INFINITY, 0.f);
             bool ok = true;
-            for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
+            for (int64_t t = t_first; t < t_end; t += t_step, ++j) {
                 const uint32_t b = j & 1u;
-                const int64_t w0 = t * 128 + quarter * 32, v = w0 + lane;
-                const float bias = a.bias && v < a.V ? __ldg(a.bias + v) : 0.f;
+                const int64_t w0 = v_first + t * 128 + quarter * 32, v = w0 + lane;
+                const float bias = a.bias && v < v_end ? __ldg(a.bias + v) : 0.f;
                 if (!warp_wait(&done[b], (j >> 1) & 1u)) {
                     ok = false;
                     break;
@@ -300,11 +382,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) lm_logprob_kernel(const __grid_
                 for (int q = 0; q < N; ++q) {
                     if (q >= a.M) break;
                     float x = fmaxf(soft_cap(__uint_as_float(r[q]) + bias, a.cap, kcap), -INFINITY);
-                    if (v >= a.V) x = -INFINITY;
-                    if (a.mask && w0 < a.V &&
+                    if (v >= v_end) x = -INFINITY;  // lanes past the run hold what was there before
+                    if (a.mask && w0 < v_end &&
                         !(((uint32_t)__ldg(a.mask + q * a.mstride + (w0 >> 5)) >> lane) & 1u))
                         x = -INFINITY;
-                    if (__ldg(a.tokens + q) == v) a.tok[q] = x;
+                    if (v < v_end && __ldg(a.tokens + q) == v) a.tok[q] = x;
                     if (x > -INFINITY) st[q] = join(st[q], make_float2(x, 1.f), kLog2eH / row_temp(a, q));
                 }
             }
@@ -338,16 +420,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) lm_logprob_kernel(const __grid_
     if (warp == 1) tmem_free(tmem, S::COLS);
 }
 
-// A row's parts: 32 rows a CTA, 16 threads a row, then a tree over them.
-constexpr int kJoinY = 16;
-__global__ void __launch_bounds__(32 * kJoinY) lm_logprob_join_kernel(LmLogprobArgs a, int64_t parts) {
-    __shared__ float2 sh[kJoinY][32];
+// A row's parts: 8 rows a CTA, 64 threads a row (a pass over 2,048 parts is 32
+// loads a thread, four under way together), then a tree over them.
+constexpr int kJoinX = 8, kJoinY = 64;
+__global__ void __launch_bounds__(kJoinX *kJoinY) lm_logprob_join_kernel(LmLogprobArgs a, int64_t parts) {
+    __shared__ float2 sh[kJoinY][kJoinX];
     pdl_wait_primary();
-    const int64_t row = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    const int64_t row = (int64_t)blockIdx.x * kJoinX + threadIdx.x;
     const float T = row < a.M ? row_temp(a, row) : 1.f, c2 = kLog2eH / T;
     float2 s = make_float2(-INFINITY, 0.f);
-    if (row < a.M)
-        for (int64_t p = threadIdx.y; p < parts; p += kJoinY) s = join(s, a.part[p * a.M + row], c2);
+    if (row < a.M) {
+        const float2 *part = a.part + row;
+        int64_t p = threadIdx.y;
+        for (; p + 3 * kJoinY < parts; p += 4 * kJoinY) {
+            float2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = part[(p + i * kJoinY) * a.M];
+            s = join(s, join(join(v[0], v[1], c2), join(v[2], v[3], c2), c2), c2);
+        }
+        for (; p < parts; p += kJoinY) s = join(s, part[p * a.M], c2);
+    }
     sh[threadIdx.y][threadIdx.x] = s;
 #pragma unroll
     for (int o = kJoinY / 2; o > 0; o >>= 1) {
@@ -371,6 +463,8 @@ __global__ void __launch_bounds__(32 * kJoinY) lm_logprob_join_kernel(LmLogprobA
 // The row-block form needs full blocks to be worth its padding; up to 32 rows
 // are columns instead.
 constexpr int64_t kLmFew = 32;
+// One block of hidden rows: smaller tiles spread the vocabulary more evenly.
+constexpr int64_t kLmMid = 128;
 
 namespace {
 
@@ -417,26 +511,28 @@ int launch_products(const LmLogprobArgs &args, int64_t *parts, cudaStream_t st) 
     const void *fn = reinterpret_cast<const void *>(&lm_logprob_kernel<N, ROWS, STAGES>);
     CUtensorMap ma, mb;
     if (!make_map(&ma, ROWS ? args.hidden : args.weight, args.H, ROWS ? args.M : args.V,
-                  ROWS ? args.hstride : args.wstride, 128) ||
+                  ROWS ? args.hstride : args.wstride, ROWS ? 128 : 32) ||
         !make_map(&mb, ROWS ? args.weight : args.hidden, args.H, ROWS ? args.V : args.M,
                   ROWS ? args.wstride : args.hstride, N))
         return -1;
     if (prepare_kernel(fn, S::SMEM, 1) != 0) return -1;
     int row_blocks = ROWS ? (int)((args.M + 127) / 128) : 1;
     int64_t tiles = ROWS ? row_blocks * ((args.V + N - 1) / N) : (args.V + 127) / 128;
-    const int64_t grid = tiles < sm_count() ? tiles : sm_count();
-    *parts = ROWS ? tiles / row_blocks : grid;
+    const int64_t sms = sm_count();
+    int64_t run = ((args.V + sms - 1) / sms + 31) / 32 * 32;
+    const int64_t grid = ROWS ? (tiles < sms ? tiles : sms) : (args.V + run - 1) / run;
+    *parts = ROWS ? (args.V + N / 2 - 1) / (N / 2) : grid;
     LmLogprobArgs a = args;
-    void *params[] = {&ma, &mb, &a, &tiles, &row_blocks};
-    return cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kTcThreads), params, S::SMEM, st) == cudaSuccess ? 0 : -1;
+    void *params[] = {&ma, &mb, &a, &tiles, &row_blocks, &run};
+    return cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kTcThreads<ROWS>), params, S::SMEM, st) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace
 
-// The most parts any form writes: a vocabulary tile of 128, or a CTA an SM.
-int64_t lm_logprob_parts(int64_t, int64_t V) {
-    const int64_t n = (V + 127) / 128;
-    return n < 256 ? 256 : n;
+// The most parts a form writes: half a tile of the vocabulary, or a CTA an SM.
+int64_t lm_logprob_parts(int64_t M, int64_t V) {
+    if (M <= kLmFew) return 256;
+    return M <= kLmMid ? (V + 63) / 64 : (V + 127) / 128;
 }
 
 int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st) {
@@ -446,7 +542,7 @@ int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st) {
         r = launch_products<16, false, 11>(args, &parts, st);
     else if (args.M <= kLmFew)
         r = launch_products<32, false, 10>(args, &parts, st);
-    else if (args.M <= 128)
+    else if (args.M <= kLmMid)
         r = launch_products<128, true, 6>(args, &parts, st);
     else
         r = launch_products<256, true, 4>(args, &parts, st);
@@ -454,8 +550,8 @@ int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st) {
     LmLogprobArgs a = args;
     void *params[] = {&a, &parts};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.M + 31) / 32));
-    cfg.blockDim = dim3(32, kJoinY);
+    cfg.gridDim = dim3((unsigned)((a.M + kJoinX - 1) / kJoinX));
+    cfg.blockDim = dim3(kJoinX, kJoinY);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
