@@ -13,6 +13,7 @@ namespace tsa {
 namespace {
 
 using loss_detail::block_sum;
+using loss_detail::Sum2;
 
 constexpr int kSumThreads = 1024;
 constexpr int kPairThreads = 256;
@@ -20,15 +21,15 @@ constexpr int kPairThreads = 256;
 // One CTA, a fixed order: the same loss for the same rows on every call.
 __global__ void __launch_bounds__(kSumThreads) weighted_sum_kernel(const float *x, const float *w, float w_s,
                                                                    int64_t n, float *out) {
-    __shared__ double sh[kSumThreads / 32];
+    __shared__ Sum2 sh[kSumThreads / 32];
     pdl_wait_primary();
-    double s = 0.0;
+    Sum2 s = {0.f, 0.f};
     for (int64_t i = threadIdx.x; i < n; i += kSumThreads) {
         const float wi = w ? w[i] : w_s;
-        if (wi != 0.f) s += (double)wi * (double)x[i];
+        if (wi != 0.f) s.add_product(wi, x[i]);
     }
     s = block_sum<kSumThreads>(s, sh);
-    if (threadIdx.x == 0) out[0] = (float)s;
+    if (threadIdx.x == 0) out[0] = s.value();
 }
 
 // One CTA a pair: the two sequences' log-ratios, the pair's loss, and the
@@ -39,52 +40,63 @@ __global__ void __launch_bounds__(kSumThreads) weighted_sum_kernel(const float *
 // (skipped rows have Z = 1, m = 0 and log-probability 0, and the sums' pass
 // left their coefficient 0) and its log-probability is not -inf.
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(PairArgs a, RowLossArgs r) {
-    __shared__ double sh[kPairThreads / 32];
+    __shared__ Sum2 sh[kPairThreads / 32];
     pdl_launch_dependents();
     pdl_wait_primary();
     const int64_t p = blockIdx.x;
-    double R[2], W[2];
+    Sum2 R[2];
+    float W[2];
     int64_t lo[2], hi[2];
-    auto counts = [&](int64_t i) {
+    auto weight = [&](int64_t i) {  // 0 for a row that does not count
+        const float w = a.weight ? a.weight[i] : 1.f;
         const int64_t tok = r.tokens[i];
-        return (a.weight ? a.weight[i] : 1.f) != 0.f && tok >= 0 && tok < r.V && a.logprob[i] != -INFINITY &&
-               r.row_m[i] != -INFINITY;
+        return tok >= 0 && tok < r.V && a.logprob[i] != -INFINITY && r.row_m[i] != -INFINITY ? w : 0.f;
     };
     for (int s = 0; s < 2; ++s) {
         const int64_t q = p + s * a.P;
         lo[s] = min(max(a.seq_start[q], (int64_t)0), a.N);
         hi[s] = min(max(a.seq_start[q + 1], lo[s]), a.N);
-        double sum = 0.0, n = 0.0;
+        Sum2 sum = {0.f, 0.f}, n = {0.f, 0.f};
         for (int64_t i = lo[s] + threadIdx.x; i < hi[s]; i += kPairThreads) {
-            if (!counts(i)) continue;
-            const double w = a.weight ? a.weight[i] : 1.f;
-            sum += w * ((double)a.logprob[i] - (a.ref_logprob ? (double)a.ref_logprob[i] : 0.0));
-            n += w;
+            const float w = weight(i);
+            if (w == 0.f) continue;
+            // the difference with its rounding error
+            Sum2 d = {a.logprob[i], 0.f};
+            if (a.ref_logprob) d.add(-a.ref_logprob[i]);
+            sum.add_product(w, d.s);
+            sum.add_product(w, d.c);
+            n.add(w);
         }
         R[s] = block_sum<kPairThreads>(sum, sh);
-        W[s] = 1.0;
+        W[s] = 1.f;
         if (a.average) {
-            n = block_sum<kPairThreads>(n, sh);
-            W[s] = n != 0.0 ? 1.0 / n : 0.0;
-            R[s] *= W[s];
+            const float total = block_sum<kPairThreads>(n, sh).value();
+            W[s] = total != 0.f ? 1.f / total : 0.f;
+            Sum2 mean = {0.f, 0.f};
+            mean.add_product(R[s].s, W[s]);
+            mean.c += R[s].c * W[s];
+            R[s] = mean;
         }
     }
-    const double h = (double)a.beta * (R[0] - R[1]) - (double)a.margin, e = (double)a.smooth;
-    const float hf = (float)h;
+    Sum2 diff = R[0];
+    diff.add(Sum2{-R[1].s, -R[1].c});
+    const float h = a.beta * diff.value() - a.margin;
     // ln(1 + e^-|h|) and the two logistic values from one exponential
-    const float q = expf(-fabsf(hf)), l1 = log1pf(q), big = 1.f / (1.f + q), small = q / (1.f + q);
-    const float plus = hf > 0.f ? big : small, minus = hf > 0.f ? small : big;  // s(h), s(-h)
+    const float q = expf(-fabsf(h)), l1 = log1pf(q), big = 1.f / (1.f + q), small = q / (1.f + q);
+    const float plus = h > 0.f ? big : small, minus = h > 0.f ? small : big;  // s(h), s(-h)
     if (threadIdx.x == 0) {
-        const float soft_m = l1 + fmaxf(-hf, 0.f), soft_p = l1 + fmaxf(hf, 0.f);
-        a.pair_loss[p] = h != h ? hf : (1.f - a.smooth) * soft_m + (a.smooth != 0.f ? a.smooth * soft_p : 0.f);
-        a.reward[p] = (float)((double)a.beta * R[0]);
-        a.reward[p + a.P] = (float)((double)a.beta * R[1]);
+        const float soft_m = l1 + fmaxf(-h, 0.f), soft_p = l1 + fmaxf(h, 0.f);
+        a.pair_loss[p] = h != h ? h : (1.f - a.smooth) * soft_m + (a.smooth != 0.f ? a.smooth * soft_p : 0.f);
+        a.reward[p] = a.beta * R[0].value();
+        a.reward[p + a.P] = a.beta * R[1].value();
     }
-    const double dh = h != h ? h : -(1.0 - e) * (double)minus + e * (double)plus;
+    const float dh = h != h ? h : -(1.f - a.smooth) * minus + a.smooth * plus;
     for (int s = 0; s < 2; ++s) {
-        const double d = (s == 0 ? dh : -dh) * (double)a.beta / (double)a.P * W[s];
-        for (int64_t i = lo[s] + threadIdx.x; i < hi[s]; i += kPairThreads)
-            if (counts(i)) a.coef[i] = (float)(d * (double)(a.weight ? a.weight[i] : 1.f));
+        const float d = (s == 0 ? dh : -dh) * a.beta / (float)a.P * W[s];
+        for (int64_t i = lo[s] + threadIdx.x; i < hi[s]; i += kPairThreads) {
+            const float w = weight(i);
+            if (w != 0.f) a.coef[i] = d * w;
+        }
     }
 }
 

@@ -1159,21 +1159,51 @@ __global__ void __launch_bounds__(kHeldThreads, 2) row_held_kernel(RowLossArgs r
 }
 
 // ------------------------------------------------------------ known sums
-// Block sum of doubles in a fixed order; the result on every thread.  These
-// sums are over rows, not logits (thousands of terms, not hundreds of
-// millions), so fp64 costs nothing and a sequence's log-ratio keeps the
-// differences that cancel in it.
+// A sum with its rounding errors beside it (Knuth's two-sum), in fp32: about
+// 48 bits, so that a sequence's log-ratio keeps the differences that cancel in
+// it.  (FP64 does a few operations a cycle and SM here: with it these small
+// sums took 6 and 11 us.)
+struct Sum2 {
+    float s, c;
+    __device__ __forceinline__ void add(float x) {
+        const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
+        c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
+        s = t;
+    }
+    __device__ __forceinline__ void add_product(float a, float b) {
+        const float p = __fmul_rn(a, b);
+        add(p);
+        c = __fadd_rn(c, fmaf(a, b, -p));
+    }
+    __device__ __forceinline__ void add(const Sum2 &o) {
+        add(o.s);
+        c = __fadd_rn(c, o.c);
+    }
+    // infinities and NaN as the plain sum has them
+    __device__ __forceinline__ float value() const { return fabsf(s) < INFINITY ? __fadd_rn(s, c) : s; }
+};
+// Block sum in a fixed order; the result on every thread.
 template <int THREADS>
-__device__ double block_sum(double v, double *sh) {
+__device__ __forceinline__ Sum2 block_sum(Sum2 v, Sum2 *sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto down = [&]() {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        for (int o = 16; o > 0; o >>= 1) {
+            Sum2 w;
+            w.s = __shfl_down_sync(0xFFFFFFFFu, v.s, o);
+            w.c = __shfl_down_sync(0xFFFFFFFFu, v.c, o);
+            v.add(w);
+        }
+    };
+    down();
     __syncthreads();  // sh may hold an earlier sum
     if (lane == 0) sh[warp] = v;
     __syncthreads();
-    double s = 0.0;
-    for (int i = 0; i < THREADS / 32; ++i) s += sh[i];
-    return s;
+    v = lane < THREADS / 32 ? sh[lane] : Sum2{0.f, 0.f};
+    down();
+    v.s = __shfl_sync(0xFFFFFFFFu, v.s, 0);
+    v.c = __shfl_sync(0xFFFFFFFFu, v.c, 0);
+    return v;
 }
 
 // The gradient of a row whose m, Z and coefficient are known:
@@ -1189,14 +1219,14 @@ __global__ void __launch_bounds__(kKnownThreads) row_grad_kernel(RowLossArgs r, 
                                                                  float *loss) {
     using E = Elem<DT>;
     constexpr int AE = E::AE;
-    __shared__ double sh[kKnownThreads / 32];
+    __shared__ Sum2 sh[kKnownThreads / 32];
     pdl_wait_primary();
     const int tid = threadIdx.x;
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
-        double s = 0.0;
-        for (int64_t i = tid; i < pairs; i += kKnownThreads) s += (double)pair_loss[i];
+        Sum2 s = {0.f, 0.f};
+        for (int64_t i = tid; i < pairs; i += kKnownThreads) s.add(pair_loss[i]);
         s = block_sum<kKnownThreads>(s, sh);
-        if (tid == 0) *loss = pairs > 0 ? (float)(s / (double)pairs) : 0.f;
+        if (tid == 0) *loss = pairs > 0 ? s.value() / (float)pairs : 0.f;
     }
     const int64_t row = r.B - 1 - (int64_t)blockIdx.y - (int64_t)blockIdx.z * gridDim.y;
     if (row < 0) return;
