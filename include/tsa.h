@@ -316,12 +316,16 @@ int tsa_selective_log_softmax(const void *logits, tsa_dtype dtype, int64_t B, in
  *                may be `logits` itself (same row stride), and otherwise must
  *                not overlap it.  Fastest where its rows start at the same
  *                address modulo 16 bytes as the logits' rows.
+ *   workspace    at least tsa_policy_loss_workspace_bytes(B, V, dtype) bytes,
+ *                256-byte aligned, or NULL where that is 0 (rows of up to 512
+ *                KB) or grad_out is NULL
  * A skipped row's logits are not read; its loss, log-probability, entropy and
  * gradient are 0.  A row whose token the mask excludes, or whose mask leaves
  * nothing, also has loss and gradient 0; its logprob_out is -inf, or NaN for
  * the empty row.  NaN logits count as -inf; a +inf logit makes its row NaN.
- * Rows are read from HBM once.  The sums run in fp32 and the loss over rows in
- * a fixed order: equal calls give equal bits.
+ * Rows of up to 512 KB are read from HBM once; longer ones twice if there is a
+ * gradient.  The sums run in fp32 and the loss over rows in a fixed order:
+ * equal calls give equal bits.
  */
 int tsa_policy_loss(const void *logits, tsa_dtype dtype, int64_t B, int64_t V, int64_t logits_row_stride,
                     const int32_t *bitmask, int64_t mask_row_stride, const float *temperature,
@@ -329,7 +333,8 @@ int tsa_policy_loss(const void *logits, tsa_dtype dtype, int64_t B, int64_t V, i
                     const float *advantage, const float *ref_logprob, const float *weight, float clip_low,
                     float clip_high, float kl_coef, float entropy_coef, float *loss_out,
                     float *row_loss_out, float *logprob_out, float *entropy_out, void *grad_out,
-                    int64_t grad_row_stride, void *stream);
+                    int64_t grad_row_stride, void *workspace, size_t workspace_bytes, void *stream);
+size_t tsa_policy_loss_workspace_bytes(int64_t B, int64_t V, tsa_dtype dtype);
 
 /*
  * preference_loss -- the loss of preferred over rejected answers from their

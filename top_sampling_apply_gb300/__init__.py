@@ -64,7 +64,9 @@ def load_library(path: Optional[str] = None):
         lib.tsa_lm_head_topk_workspace_bytes.restype = sz
         lib.tsa_selective_log_softmax.argtypes = [P, ci, i64, i64, i64, P, i64, P, f32, P, P, P]
         lib.tsa_policy_loss.argtypes = [P, ci, i64, i64, i64, P, i64, P, f32, P, P, P, P, P, f32, f32, f32,
-                                        f32, P, P, P, P, P, i64, P]
+                                        f32, P, P, P, P, P, i64, P, sz, P]
+        lib.tsa_policy_loss_workspace_bytes.argtypes = [i64, i64, ci]
+        lib.tsa_policy_loss_workspace_bytes.restype = sz
         lib.tsa_preference_loss.argtypes = [P, ci, i64, i64, i64, f32, P, P, i64, P, P, f32, f32, f32, ci,
                                             P, P, P, P, P, i64, P, sz, P]
         lib.tsa_preference_loss_workspace_bytes.argtypes = [i64]
@@ -455,12 +457,14 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: torch.T
     loss = torch.empty((), dtype=torch.float32, device=logits.device)
     rows = torch.empty((3 if return_entropy else 2, B), dtype=torch.float32, device=logits.device).unbind(0)
     ent = rows[2] if return_entropy else None
+    nws = lib.tsa_policy_loss_workspace_bytes(B, V, _DT[logits.dtype]) if g is not None else 0
+    ws = torch.empty(nws, dtype=torch.uint8, device=logits.device) if nws else None
     _check(lib.tsa_policy_loss(logits.data_ptr(), _DT[logits.dtype], B, V, stride,
                                None if bitmask is None else bitmask.data_ptr(), mstride, T, Ts, tok, old, adv, ref,
                                wgt, clip_low, clip_high, kl_coef, entropy_coef, loss.data_ptr(),
                                rows[0].data_ptr(), rows[1].data_ptr(), None if ent is None else ent.data_ptr(),
                                None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
-                               _raw_stream(dev)))
+                               None if ws is None else ws.data_ptr(), nws, _raw_stream(dev)))
     return PolicyLoss(loss, rows[0], rows[1], ent, g)
 
 

@@ -153,7 +153,9 @@ struct RowLossArgs {
     float *row_loss, *logprob, *entropy;
     void *grad;
     int64_t gstride;
-    float *row_m, *row_z, *coef;  // mode 1: a row's maximum, its sum, and the gradient's coefficient
+    // a row between two passes, or NULL: k1, k2, a and m of its gradient; from
+    // mode 1's sums 0, Z, 0 and m
+    float4 *fin;
 };
 struct PairArgs {
     int64_t P, N;
@@ -161,26 +163,30 @@ struct PairArgs {
     const float *logprob, *ref_logprob, *weight;
     float beta, smooth, margin;
     int average;
-    float *pair_loss, *reward, *coef;
+    float *pair_loss, *reward;
 };
+// Whether rows of V logits are held on chip for their gradient; longer ones
+// take two passes (sums, then row_grad_launch) with `fin` between them.
+bool row_is_held(int64_t V, int dtype);
 int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cudaStream_t st);
 unsigned int *row_loss_status_ptr();
-// The gradient of rows whose sums are known, and the pairs' mean loss.
-int row_grad_launch(const RowLossArgs &args, int dtype, const float *pair_loss, int64_t pairs, float *loss,
+// The gradient of rows whose coefficients are known, and the pairs' mean loss
+// (loss NULL: none).
+int row_grad_launch(const RowLossArgs &args, int dtype, bool ent, const float *pair_loss, int64_t pairs, float *loss,
                     cudaStream_t st);
 int pair_launch(const PairArgs &args, const RowLossArgs &rows, cudaStream_t st);
 // out[0] = sum_i w_i x_i over the entries with w_i != 0 (w NULL: w_s each).
 int weighted_sum_launch(const float *x, const float *w, float w_s, int64_t n, float *out, cudaStream_t st);
-// The kernels of one element type: mode, gradient, entropy.
-const void *row_loss_kernel_f32(int mode, bool grad, bool ent);
-const void *row_loss_kernel_f16(int mode, bool grad, bool ent);
-const void *row_loss_kernel_bf16(int mode, bool grad, bool ent);
+// The kernels of one element type.
+const void *row_loss_kernel_f32(int mode, bool ent);
+const void *row_loss_kernel_f16(int mode, bool ent);
+const void *row_loss_kernel_bf16(int mode, bool ent);
 const void *row_held_kernel_f32(bool ent);
 const void *row_held_kernel_f16(bool ent);
 const void *row_held_kernel_bf16(bool ent);
-const void *row_grad_kernel_f32();
-const void *row_grad_kernel_f16();
-const void *row_grad_kernel_bf16();
+const void *row_grad_kernel_f32(bool ent);
+const void *row_grad_kernel_f16(bool ent);
+const void *row_grad_kernel_bf16(bool ent);
 
 // AdamW over many tensors: one tensor's pointers, and the step's numbers.
 struct AdamTensor {

@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kSumThreads) weighted_sum_kernel(const float *
 //     d loss / dh = -(1 - eps) / (1 + e^h) + eps / (1 + e^-h).
 // A row counts if its weight is not 0, its token is in the vocabulary
 // (skipped rows have Z = 1, m = 0 and log-probability 0, and the sums' pass
-// left their coefficient 0) and its log-probability is not -inf.
+// left their coefficients 0) and its log-probability is not -inf.
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(PairArgs a, RowLossArgs r) {
     __shared__ Sum2 sh[kPairThreads / 32];
     pdl_launch_dependents();
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(PairArgs a, RowLossA
     auto weight = [&](int64_t i) {  // 0 for a row that does not count
         const float w = a.weight ? a.weight[i] : 1.f;
         const int64_t tok = r.tokens[i];
-        return tok >= 0 && tok < r.V && a.logprob[i] != -INFINITY && r.row_m[i] != -INFINITY ? w : 0.f;
+        return tok >= 0 && tok < r.V && a.logprob[i] != -INFINITY && r.fin[i].w != -INFINITY ? w : 0.f;
     };
     for (int s = 0; s < 2; ++s) {
         const int64_t q = p + s * a.P;
@@ -95,17 +95,28 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(PairArgs a, RowLossA
         const float d = (s == 0 ? dh : -dh) * a.beta / (float)a.P * W[s];
         for (int64_t i = lo[s] + threadIdx.x; i < hi[s]; i += kPairThreads) {
             const float w = weight(i);
-            if (w != 0.f) a.coef[i] = d * w;
+            if (w == 0.f) continue;
+            // from (0, Z, 0, m) to k1, k2, a and m
+            const float4 k = r.fin[i];
+            const float T = r.temperature_s > 0.f ? r.temperature_s : 1.f, g = d * w / T;
+            float f;
+            loss_detail::near_shift(k.w, loss_detail::kLog2eL / T, &f);
+            r.fin[i] = make_float4(-g / k.y * f, 0.f, g, k.w);
         }
     }
 }
 
 __device__ unsigned int g_loss_status;
 
-const void *loss_kernel(int dtype, int mode, bool grad, bool ent) {
-    return dtype == 0 ? row_loss_kernel_f32(mode, grad, ent)
-                      : (dtype == 1 ? row_loss_kernel_f16(mode, grad, ent)
-                                    : row_loss_kernel_bf16(mode, grad, ent));
+const void *loss_kernel(int dtype, int mode, bool ent) {
+    return dtype == 0 ? row_loss_kernel_f32(mode, ent)
+                      : (dtype == 1 ? row_loss_kernel_f16(mode, ent) : row_loss_kernel_bf16(mode, ent));
+}
+const void *held_kernel(int dtype, bool ent) {
+    return dtype == 0 ? row_held_kernel_f32(ent) : (dtype == 1 ? row_held_kernel_f16(ent) : row_held_kernel_bf16(ent));
+}
+const void *grad_kernel(int dtype, bool ent) {
+    return dtype == 0 ? row_grad_kernel_f32(ent) : (dtype == 1 ? row_grad_kernel_f16(ent) : row_grad_kernel_bf16(ent));
 }
 
 // A launch that may start its prologue while the kernel before it drains;
@@ -152,14 +163,11 @@ static int64_t resident_clusters(const void *fn, const cudaLaunchConfig_t &cfg, 
     return n;
 }
 
-// The CTAs that share a streamed row.  With a gradient, enough that L2 keeps
-// part of a row until its second reading.  Fewer rows than SMs are spread
-// further, down to 256 vectors a CTA.
-static int row_cluster(int64_t B, int64_t V, int es, bool grad) {
+// The CTAs that share a streamed row: one, and more where there are fewer rows
+// than SMs, down to 256 vectors a CTA.
+static int row_cluster(int64_t B, int64_t V, int es) {
     const int64_t bytes = V * es;
     int C = 1;
-    if (grad)
-        while (C < loss_detail::kRowMaxCluster && bytes > (int64_t)C * 132 * 1024) C *= 2;
     while (C < loss_detail::kRowMaxCluster && B * C * 2 <= 152 && bytes / 16 >= 512 * C) C *= 2;
     return C;
 }
@@ -199,24 +207,23 @@ static int launch_rows(const void *fn, int64_t B, int C, int threads, size_t sme
     return cudaLaunchKernelExC(&cfg, fn, params) == cudaSuccess ? 0 : -1;
 }
 
+bool row_is_held(int64_t V, int dtype) { return held_cluster(1 << 20, V, dtype == 0 ? 4 : 2) > 0; }
+
 int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cudaStream_t st) {
     using namespace loss_detail;
     const int es = dtype == 0 ? 4 : 2;
-    const bool grad = args.grad != nullptr;
     RowLossArgs a = args;
     unsigned int *status = row_loss_status_ptr();
     if (!status) return -1;
-    const int H = grad ? held_cluster(args.B, args.V, es) : 0;
-    if (H > 0) {
-        const void *fn = dtype == 0 ? row_held_kernel_f32(ent)
-                                    : (dtype == 1 ? row_held_kernel_f16(ent) : row_held_kernel_bf16(ent));
-        int lg = 0;
-        while ((1 << lg) < H) ++lg;
-        void *params[] = {&a, &lg, &status};
-        return launch_rows(fn, args.B, H, kHeldThreads, kHeldSmem, params, st);
-    }
-    const int C = row_cluster(args.B, args.V, es, grad);
     int lg = 0;
+    if (args.grad) {
+        const int C = held_cluster(args.B, args.V, es);
+        if (C == 0) return -1;
+        while ((1 << lg) < C) ++lg;
+        void *params[] = {&a, &lg, &status};
+        return launch_rows(held_kernel(dtype, ent), args.B, C, kHeldThreads, kHeldSmem, params, st);
+    }
+    const int C = row_cluster(args.B, args.V, es);
     while ((1 << lg) < C) ++lg;
     const int64_t vecs = (args.V * es / 16 + C - 1) / C;  // a CTA's vectors at most
     int stages = (int)((vecs + kRowStage - 1) / kRowStage);
@@ -224,17 +231,13 @@ int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cuda
     // a stage as long as fits, in whole steps of the working warps
     int nu = (int)((vecs < kRowStage ? vecs : kRowStage) + kRowUsers - 1) / kRowUsers;
     if (nu < 1) nu = 1;
-    // about 48 KB of stages between a row's last sum and its first gradient
-    const int64_t bytes = (vecs * 16 + stages - 1) / stages;
-    int lag = (int)((49152 + bytes) / (bytes + 1));
-    lag = lag < 1 ? 1 : (lag > kRowMaxLag ? kRowMaxLag : lag);
-    void *params[] = {&a, &lg, &stages, &nu, &lag, &status};
-    return launch_rows(loss_kernel(dtype, mode, grad, ent), args.B, C, kRowThreads, kRowSmem, params, st);
+    void *params[] = {&a, &lg, &stages, &nu, &status};
+    return launch_rows(loss_kernel(dtype, mode, ent), args.B, C, kRowThreads, kRowSmem, params, st);
 }
 
-int row_grad_launch(const RowLossArgs &args, int dtype, const float *pair_loss, int64_t pairs, float *loss,
+int row_grad_launch(const RowLossArgs &args, int dtype, bool ent, const float *pair_loss, int64_t pairs, float *loss,
                     cudaStream_t st) {
-    const void *fn = dtype == 0 ? row_grad_kernel_f32() : (dtype == 1 ? row_grad_kernel_f16() : row_grad_kernel_bf16());
+    const void *fn = grad_kernel(dtype, ent);
     const int64_t per = (int64_t)loss_detail::kKnownThreads * loss_detail::kKnownU * (dtype == 0 ? 4 : 8);
     const unsigned slices = (unsigned)((args.V + per - 1) / per);
     const unsigned y = (unsigned)(args.B < 32768 ? args.B : 32768);

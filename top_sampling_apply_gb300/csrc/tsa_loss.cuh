@@ -147,9 +147,6 @@ __device__ __forceinline__ bool allowed_bit(const int32_t *mrow, int64_t i) {
 struct RowStat {
     float m, Z, t;
 };
-// e and the exponent of one logit against m (m finite or +inf).
-__device__ __forceinline__ float expo(float x, float m, float c2) { return __fmul_rn(__fsub_rn(x, m), c2); }
-
 // Both parts against the larger maximum: the part with the smaller one is
 // scaled by 2^d.  An empty part has Z = t = 0 and m = -inf; its exponent is
 // -inf or NaN, and the lower bound makes the factor 0.  merge(a, b) and
@@ -253,9 +250,6 @@ __device__ __forceinline__ RowScalars finish_row(const RowLossArgs &r, int64_t r
         }
     } else if (writer) {
         r.logprob[row] = lp;
-        r.row_m[row] = s.m;
-        r.row_z[row] = Z;
-        r.coef[row] = 0.f;
     }
     return g;
 }
@@ -265,11 +259,8 @@ __device__ __forceinline__ void skip_row(const RowLossArgs &r, int64_t row) {
     if (MODE == 0) {
         r.row_loss[row] = 0.f;
         if (r.entropy) r.entropy[row] = 0.f;
-    } else {
-        r.row_m[row] = 0.f;
-        r.row_z[row] = 1.f;
-        r.coef[row] = 0.f;
     }
+    if (r.fin) r.fin[row] = make_float4(0.f, MODE == 0 ? 0.f : 1.f, 0.f, 0.f);
 }
 
 // One gradient element from e_j and its exponent y: k1 e + k2 e y, with
@@ -291,42 +282,23 @@ __device__ __forceinline__ GradCoef grad_coef(const RowScalars &g, const RowStat
     return k;
 }
 
-// The element of a logit x; `a` is added at the token.  Products and sums are
-// kept apart (no fused multiply-add with `a`), so that an element has the same
-// bits in the vector and the element-wise path.
-template <bool ENT>
-__device__ __forceinline__ float grad_el(float x, float m, float c2, const GradCoef &k) {
-    float y = expo(x, m, c2);
-    if (ENT) y = fmaxf(y, kLowExp);
-    const float e = ex2_approx(y);
-    return __fmul_rn(e, ENT ? fmaf(k.k2, y, k.k1) : k.k1);
-}
-
 // ------------------------------------------------------------ the rows, streamed
-// One persistent CTA an SM takes rows as streams of 56 KB stages through a ring
-// in shared memory, filled by bulk copies.  Fourteen warps reduce the stages of
-// one row (m, Z, t, against a reference a warp) and, in turn with them, write
-// the gradient of the row before from its stages, which come a second time,
-// from L2: a row is 256 KB for 128,256 logits in 16 bits, and the two rows of
-// every SM are 78 MB.  Between a row's last sum and its first gradient stage
-// lies a stage of the next row, during which a warp of its own joins the sums
-// and finishes the row.  So no warp waits for another in the middle of a row,
-// HBM is read and written all the time, and what a row costs by itself is
-// spread over its whole length.  Longer rows are shared by the C CTAs of a
-// cluster, so that the rows in flight still fit L2; only the finishing warps
-// talk to one another then.
-//
-// The issue slots are scarce too: reading and writing a bf16 logit at 6.7 TB/s
-// leaves 22 instructions an element.  16-bit maxima and the NaN test work on
-// pairs, sums and products on packed fp32 pairs.
-constexpr int kRowVecs = 8;                               // 16-byte vectors a thread in a stage
-constexpr int kRowWarps = 14, kRowUsers = 32 * kRowWarps; // the warps that work on stages
+// The sums of rows of any length, without a gradient.  One persistent CTA an SM
+// takes rows as streams of 44 KB stages through a ring in shared memory, filled
+// by bulk copies.  22 warps reduce the stages (m, Z, t, against a reference a
+// warp) and go from one row to the next without a pause, a warp of its own
+// joins a row's sums and finishes it meanwhile, and another one looks for the
+// rows to come.  What a row costs by itself is spread over its whole length.
+// Fewer rows than SMs are shared by the C CTAs of a cluster, of which only the
+// finishing warps talk to one another.  512 x 128,256 fp32 with the entropies:
+// 52 us, 5.1 TB/s.
+constexpr int kRowVecs = 4;                               // 16-byte vectors a thread in a stage
+constexpr int kRowWarps = 22, kRowUsers = 32 * kRowWarps; // the warps that work on stages
 constexpr int kRowThreads = kRowUsers + 64;               // one more to copy, one to finish rows
 constexpr int kRowStage = kRowUsers * kRowVecs;           // vectors a stage
-constexpr int kRowSlots = 3;                              // stages in shared memory
+constexpr int kRowSlots = 4;                              // stages in shared memory
 constexpr int kRowRing = 16;                              // rows under way at most
 constexpr int kRowMaxCluster = 8;
-constexpr int kRowMaxLag = 8;
 
 // A row's (or a warp's) reference as its exponents are formed from it.  Near 0
 // the exponent is one fused multiply-add, l c2 - R with R = m c2 rounded; the
@@ -484,6 +456,43 @@ __device__ __forceinline__ void add_vecs(const uint4 (&x)[U], int nu, const Ref 
         s.t = a + b;
     }
 }
+// One more logit.
+template <bool ENT>
+__device__ __forceinline__ void add_one(float x, const Ref &ref, WarpSums &s) {
+    unsigned long long e, y;
+    if (ref.near)
+        exp_pair<ENT, true>(x, -INFINITY, ref, e, y);
+    else
+        exp_pair<ENT, false>(x, -INFINITY, ref, e, y);
+    float a, b, ignored;
+    split_pair(e, a, ignored);
+    split_pair(y, b, ignored);
+    s.Z += a;
+    if (ENT) s.t = fmaf(a, b, s.t);
+}
+// The warp's sums against its largest logit itself.
+template <bool ENT>
+__device__ __forceinline__ float4 against_top(const WarpSums &s, float c2) {
+    float Z = warp_sum_f32(s.Z), t = ENT ? warp_sum_f32(s.t) : 0.f;
+    if (s.m > -INFINITY) {
+        float f;
+        const float d = near_shift(s.m, c2, &f);
+        if (ENT) t = f * fmaf(-d, Z, t);
+        Z *= f;
+    }
+    return make_float4(s.m, Z, t, 0.f);
+}
+// k1, k2, a and m of a finished row, for exponents formed from m as Ref does;
+// zeros for a row that does not count (its token masked).
+template <bool ENT>
+__device__ __forceinline__ float4 finished_coef(const RowScalars &g, const RowStat &s, float xt, float c2) {
+    if (!(xt > -INFINITY)) return make_float4(0.f, 0.f, 0.f, 0.f);
+    const GradCoef k = grad_coef<ENT>(g, s);
+    float f;
+    const float d = near_shift(s.m, c2, &f);
+    return make_float4(f * fmaf(-d, k.k2, k.k1), f * k.k2, g.a, s.m);
+}
+
 // The largest logit of the warp among the first nu vectors of its threads, NaN
 // if there is one; and the vectors with -inf in the place of NaN.
 template <int DT, int U>
@@ -541,19 +550,16 @@ __device__ __forceinline__ void grad_vec(uint4 &x, const Ref &ref, float k1, flo
 }
 
 // `stages`: a CTA's stages of a row, of nu * kRowUsers vectors each (the last
-// ones may be short or empty); `lag`: the stages between a row's last sum and
-// its first gradient.
-template <int DT, int MODE, bool GRAD, bool ENT>
-__global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r, int lg, int stages, int nu, int lag,
+// ones may be short or empty).
+template <int DT, int MODE, bool ENT>
+__global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r, int lg, int stages, int nu,
                                                                   unsigned int *status) {
     using E = Elem<DT>;
     constexpr int AE = E::AE, U = kRowVecs, S = kRowSlots, RING = kRowRing;
     extern __shared__ __align__(128) uint4 ring[];
     __shared__ float4 sums[RING][kRowWarps];           // a row's (m, Z, t) by warp
     __shared__ float4 peers[RING][kRowMaxCluster];     // and by CTA of the cluster
-    __shared__ float4 finished[RING];                  // k1, k2, a and m of a finished row
     __shared__ RowMeta meta[RING];
-    __shared__ uint32_t dirty[RING];                   // whether a row has a NaN
     __shared__ uint64_t full[S], empty[S];             // a stage has come; every warp has read it
     __shared__ uint64_t known[RING], summed[RING], joined[RING], fin[RING];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -580,86 +586,63 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
         __syncthreads();
     pdl_launch_dependents();  // the next kernel waits for this one's end before it reads
     const int stage = nu * kRowUsers;
-    const int delay = stages + lag;  // a gradient stage follows its sums' stage by this many
-    bool ok = true;                  // a wait that ran out ends all waiting; the status word tells
+    bool ok = true;  // a wait that ran out ends all waiting; the status word tells
 
     if (warp == kRowWarps) {
-        // ---- copies: sums' stages and gradient stages in the order of their use
+        // ---- copies
         RowMeta mine;
         uint32_t found = 0;
         int64_t base = first_row;
         uint32_t slot = 0, phase = 1;
-        auto copy = [&](int64_t row, int s) {
+        for (uint32_t k = 0;; ++k) {
+            // the next row that counts: 32 rows looked at together
+            while (found == 0 && base < r.B) {
+                const int64_t b = base + lane * step;
+                float w = 0.f;
+                int64_t tok = -1;
+                const bool named = b < r.B && row_named(r, b, &w, &tok);
+                if (named) {
+                    mine.row = b;
+                    mine.tok = tok;
+                    mine.w = w;
+                    mine.T = row_temperature(r, b);
+                    mine.c2 = kLog2eL / mine.T;
+                    mine.xt = token_logit(r, logits_at(b), r.mask ? r.mask + (size_t)b * r.mstride : nullptr, DT, tok);
+                }
+                found = __ballot_sync(0xFFFFFFFFu, named);
+                base += 32 * step;
+            }
+            const int who = found ? __ffs((int)found) - 1 : 0;
+            const int64_t row = found ? __shfl_sync(0xFFFFFFFFu, mine.row, who) : r.B;
+            found &= found - 1;
+            // Rows k - 16 are done with: the stages hold back this warp to
+            // four rows before the summing ones, and those stay within eight of
+            // the finishing one.
+            if (lane == who) {
+                RowMeta m = mine;
+                m.row = row;
+                meta[k % RING] = m;
+                arrive_one(&known[k % RING]);
+            }
+            __syncwarp();
+            if (row >= r.B) break;
             const RowPlace p = place_row<DT>(r, row, rank, lg);
-            int cnt = p.nv - s * stage;
-            cnt = cnt < 0 ? 0 : (cnt > stage ? stage : cnt);
-            if (lane == 0) {
-                ok = ok && mbar_wait_bounded(&empty[slot], phase, status);
-                mbar_arrive_expect_tx(&full[slot], (uint32_t)cnt * 16u);
-                if (cnt > 0)
-                    bulk_g2s(ring + slot * kRowStage,
-                             logits_at(row) + (size_t)(p.first - tid * AE) * E::SIZE + (size_t)s * stage * 16u,
-                             (uint32_t)cnt * 16u, &full[slot]);
-            }
-            if (++slot == S) {
-                slot = 0;
-                phase ^= 1u;
-            }
-        };
-        int64_t row1 = 0;
-        uint32_t k1 = 0, k2 = 0;
-        int s1 = 0, s2 = 0;
-        bool end1 = false;
-        for (int g = 0;; ++g) {
-            if (!end1) {
-                if (s1 == 0) {
-                    // the next row that counts: 32 rows looked at together
-                    while (found == 0 && base < r.B) {
-                        const int64_t b = base + lane * step;
-                        float w = 0.f;
-                        int64_t tok = -1;
-                        const bool named = b < r.B && row_named(r, b, &w, &tok);
-                        if (named) {
-                            mine.row = b;
-                            mine.tok = tok;
-                            mine.w = w;
-                            mine.T = row_temperature(r, b);
-                            mine.c2 = kLog2eL / mine.T;
-                            mine.xt = token_logit(r, logits_at(b), r.mask ? r.mask + (size_t)b * r.mstride : nullptr,
-                                                  DT, tok);
-                        }
-                        found = __ballot_sync(0xFFFFFFFFu, named);
-                        base += 32 * step;
-                    }
-                    const int who = found ? __ffs((int)found) - 1 : 0;
-                    end1 = found == 0;
-                    found &= found - 1;
-                    row1 = end1 ? r.B : __shfl_sync(0xFFFFFFFFu, mine.row, who);
-                    if (lane == who) {
-                        RowMeta m = mine;
-                        m.row = row1;
-                        meta[k1 % RING] = m;
-                        dirty[k1 % RING] = 0u;
-                        arrive_one(&known[k1 % RING]);
-                    }
-                    __syncwarp();
+            for (int s = 0; s < stages; ++s) {
+                int cnt = p.nv - s * stage;
+                cnt = cnt < 0 ? 0 : (cnt > stage ? stage : cnt);
+                if (lane == 0) {
+                    ok = ok && mbar_wait_bounded(&empty[slot], phase, status);
+                    mbar_arrive_expect_tx(&full[slot], (uint32_t)cnt * 16u);
+                    if (cnt > 0)
+                        bulk_g2s(ring + slot * kRowStage,
+                                 logits_at(row) + (size_t)(p.first - tid * AE) * E::SIZE + (size_t)s * stage * 16u,
+                                 (uint32_t)cnt * 16u, &full[slot]);
                 }
-                if (!end1) {
-                    copy(row1, s1);
-                    if (++s1 == stages) {
-                        s1 = 0;
-                        ++k1;
-                    }
+                if (++slot == S) {
+                    slot = 0;
+                    phase ^= 1u;
                 }
             }
-            if (GRAD && g >= delay && k2 < k1) {
-                copy(meta[k2 % RING].row, s2);
-                if (++s2 == stages) {
-                    s2 = 0;
-                    ++k2;
-                }
-            }
-            if (end1 && (!GRAD || k2 == k1)) break;
         }
     } else if (warp == kRowWarps + 1) {
         // ---- finished rows
@@ -686,214 +669,99 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
                 s = join(lane < (int)C ? peers[i][lane] : make_float4(0.f, 0.f, 0.f, 0.f), lane < (int)C);
             }
             if (s.m == INFINITY) s.Z = __int_as_float(0x7FC00000);
-            const RowScalars gs = finish_row<MODE, ENT>(r, mt.row, s, mt.xt, mt.T, mt.w, rank == 0 && lane == 0);
-            if (lane == 0) {
-                // a row that does not count (its token masked) gets zeros
-                GradCoef kc = mt.xt > -INFINITY ? grad_coef<ENT>(gs, s) : GradCoef{0.f, 0.f};
-                float f;
-                const float d = near_shift(s.m, mt.c2, &f);
-                finished[i] = make_float4(f * fmaf(-d, kc.k2, kc.k1), f * kc.k2, gs.a, s.m);
-                arrive_one(&fin[i]);
+            if (rank == 0) {
+                const RowScalars gs = finish_row<MODE, ENT>(r, mt.row, s, mt.xt, mt.T, mt.w, lane == 0);
+                if (r.fin && lane == 0) {
+                    if (MODE == 0)
+                        r.fin[mt.row] = finished_coef<ENT>(gs, s, mt.xt, mt.c2);
+                    else
+                        r.fin[mt.row] = make_float4(0.f, s.Z, 0.f, s.m);
+                }
             }
             __syncwarp();
+            if (lane == 0) arrive_one(&fin[i]);
         }
     } else {
         // ---- stages
         RowPlace p = place_row<DT>(r, 0, rank, lg);
         uint32_t slot = 0, phase = 0;
-        int64_t zero = first_row;  // the next row that is either counted or set to 0
-        uint32_t k1 = 0, k2 = 0;
-        int s1 = 0, s2 = 0;
-        bool end1 = false;
-        WarpSums sum = {-INFINITY, 0.f, 0.f};
-        // a stage's vectors, masked; past cnt -inf
-        auto take = [&](uint4 (&x)[U], int cnt, int32_t e0, int64_t row) {
-            uint32_t lo[U], hi[U];
-            if (r.mask) {  // under the wait
-                const int32_t *mrow = r.mask + (size_t)row * r.mstride;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    mask_words<AE>(mrow, e0 + u * kRowUsers * AE, u < nu && tid + u * kRowUsers < cnt, lo[u], hi[u]);
-            }
-            ok = ok && mbar_wait_bounded(&full[slot], phase, status);
-            const uint4 *in = ring + slot * kRowStage + tid;
-            if (cnt >= stage) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (u < nu) x[u] = in[u * kRowUsers];
-            } else {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    x[u] = none_vec<DT>();
-                    if (u < nu && tid + u * kRowUsers < cnt) x[u] = in[u * kRowUsers];
-                }
-            }
-            if (r.mask) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (u < nu) mask_vec<DT>(x[u], mask_bits<AE>(lo[u], hi[u], e0 + u * kRowUsers * AE));
-            }
-        };
-        auto release = [&]() {  // the warp has its vectors in registers
-            __syncwarp();
-            if (lane == 0) arrive_one(&empty[slot]);
-            if (++slot == S) {
-                slot = 0;
-                phase ^= 1u;
-            }
-        };
-        auto extra = [&](int64_t row, int32_t ie) {  // the element outside the vectors
-            if (r.mask && !allowed_bit(r.mask + (size_t)row * r.mstride, ie)) return -INFINITY;
-            return load_clean(logits_at(row), DT, ie);
-        };
-        for (int g = 0;; ++g) {
-            if (!end1) {
-                const uint32_t i = k1 % RING;
-                if (s1 == 0) {
-                    ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_bounded(&known[i], (k1 / RING) & 1u, status));
-                    const int64_t row = ok ? meta[i].row : r.B;
-                    end1 = row >= r.B;
-                    for (; zero < row; zero += step) {  // rows that do not count
-                        if (rank == 0 && tid == 0) skip_row<MODE>(r, zero);
-                        if (!GRAD) continue;
-                        const RowPlace q = place_row<DT>(r, zero, rank, lg);
-                        uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)zero * r.gstride * E::SIZE;
-                        if (((reinterpret_cast<uintptr_t>(logits_at(zero)) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) ==
-                            0) {
-                            for (int v = tid; v < q.nv; v += kRowUsers)
-                                __stcs(reinterpret_cast<uint4 *>(gp + (size_t)(q.first + (v - tid) * AE) * E::SIZE),
-                                       make_uint4(0u, 0u, 0u, 0u));
-                        } else {
-                            for (int v = tid; v < q.nv * AE; v += kRowUsers)
-                                Pack<DT>::store1(gp, q.first - tid * AE + v, 0.f);
-                        }
-                        if (q.ie >= 0) Pack<DT>::store1(gp, q.ie, 0.f);
-                    }
-                    zero = row + step;
-                }
-                if (!end1) {
-                    const int64_t row = meta[i].row;
-                    const float c2 = meta[i].c2;
-                    if (!fixed) p = place_row<DT>(r, row, rank, lg);
-                    uint4 x[U];
-                    take(x, p.nv - s1 * stage, p.first + s1 * stage * AE, row);
-                    float top = largest<DT>(x, nu);
-                    release();
-                    if (top != top) {  // NaN counts as -inf
-                        clean_all<DT>(x, nu);
-                        top = largest<DT>(x, nu);
-                        if (lane == 0) dirty[i] = 1u;
-                    }
-                    float xe = -INFINITY;
-                    if (s1 == 0) {
-                        if (p.ie >= 0) xe = extra(row, p.ie);
-                        top = warp_max(fmaxf(top, xe));
-                    }
-                    if (top > sum.m) raise<ENT>(sum, top, c2);
-                    if (sum.m > -INFINITY) {
-                        const Ref ref = make_ref(sum.m, c2);
-                        if (ref.near)
-                            add_vecs<DT, ENT, true>(x, nu, ref, sum);
-                        else
-                            add_vecs<DT, ENT, false>(x, nu, ref, sum);
-                        if (s1 == 0 && p.ie >= 0) {
-                            unsigned long long e, y;
-                            if (ref.near)
-                                exp_pair<ENT, true>(xe, -INFINITY, ref, e, y);
-                            else
-                                exp_pair<ENT, false>(xe, -INFINITY, ref, e, y);
-                            float a, b, ignored;
-                            split_pair(e, a, ignored);
-                            split_pair(y, b, ignored);
-                            sum.Z += a;
-                            if (ENT) sum.t = fmaf(a, b, sum.t);
-                        }
-                    }
-                    if (++s1 == stages) {
-                        // the warp's sums against m itself
-                        float Z = warp_sum_f32(sum.Z), t = ENT ? warp_sum_f32(sum.t) : 0.f;
-                        if (sum.m > -INFINITY) {
-                            float f;
-                            const float d = near_shift(sum.m, c2, &f);
-                            if (ENT) t = f * fmaf(-d, Z, t);
-                            Z *= f;
-                        }
-                        // rows are finished in order; half a ring behind at most
-                        if (!GRAD && k1 >= RING / 2)
-                            ok = ok && mbar_wait_bounded(&fin[(k1 - RING / 2) % RING], ((k1 - RING / 2) / RING) & 1u,
-                                                         status);
-                        if (lane == 0) {
-                            sums[i][warp] = make_float4(sum.m, Z, t, 0.f);
-                            arrive_one(&summed[i]);
-                        }
-                        sum = {-INFINITY, 0.f, 0.f};
-                        s1 = 0;
-                        ++k1;
-                    }
-                }
-            }
-            if (GRAD && g >= delay && k2 < k1) {
-                const uint32_t i = k2 % RING;
-                if (s2 == 0) ok = ok && mbar_wait_bounded(&fin[i], (k2 / RING) & 1u, status);
-                const int64_t row = meta[i].row;
-                const float4 k = finished[i];
-                const float xt = meta[i].xt;
-                const bool live = xt > -INFINITY;
-                const Ref ref = make_ref(live ? k.w : 0.f, meta[i].c2);
-                const RowPlace q = fixed ? p : place_row<DT>(r, row, rank, lg);
-                uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)row * r.gstride * E::SIZE;
-                const bool same =
-                    ((reinterpret_cast<uintptr_t>(logits_at(row)) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0;
-                const int cnt = q.nv - s2 * stage;
+        int64_t zero = first_row;  // the next row that either counts or is skipped
+        for (uint32_t k = 0;; ++k) {
+            const uint32_t i = k % RING;
+            ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_bounded(&known[i], (k / RING) & 1u, status));
+            const int64_t row = ok ? meta[i].row : r.B;
+            if (rank == 0)
+                for (int64_t b = zero + (int64_t)tid * step; b < row; b += kRowUsers * step) skip_row<MODE>(r, b);
+            if (row >= r.B) break;
+            zero = row + step;
+            const float c2 = meta[i].c2;
+            if (!fixed) p = place_row<DT>(r, row, rank, lg);
+            WarpSums sum = {-INFINITY, 0.f, 0.f};
+#pragma unroll 1
+            for (int s = 0; s < stages; ++s) {
+                const int cnt = p.nv - s * stage;
+                const int32_t e0 = p.first + s * stage * AE;
                 uint4 x[U];
-                take(x, cnt, q.first + s2 * stage * AE, row);
-                release();
-                if (dirty[i]) clean_all<DT>(x, nu);
-                uint8_t *gv = gp + (size_t)(q.first + s2 * stage * AE) * E::SIZE;
-                if (live && ref.near && same && cnt >= stage) {
+                uint32_t lo[U], hi[U];
+                if (r.mask) {  // under the wait
+                    const int32_t *mrow = r.mask + (size_t)row * r.mstride;
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (u < nu) {
-                            grad_vec<DT, ENT, true>(x[u], ref, k.x, k.y);
-                            __stcs(reinterpret_cast<uint4 *>(gv) + u * kRowUsers, x[u]);
-                        }
-                    }
+                    for (int u = 0; u < U; ++u)
+                        mask_words<AE>(mrow, e0 + u * kRowUsers * AE, u < nu && tid + u * kRowUsers < cnt, lo[u], hi[u]);
+                }
+                ok = ok && mbar_wait_bounded(&full[slot], phase, status);
+                const uint4 *in = ring + slot * kRowStage + tid;
+                if (cnt >= stage) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (u < nu) x[u] = in[u * kRowUsers];
                 } else {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        if (u < nu && tid + u * kRowUsers < cnt) {
-                            if (!live)
-                                x[u] = make_uint4(0u, 0u, 0u, 0u);
-                            else if (ref.near)
-                                grad_vec<DT, ENT, true>(x[u], ref, k.x, k.y);
-                            else
-                                grad_vec<DT, ENT, false>(x[u], ref, k.x, k.y);
-                            if (same) {
-                                __stcs(reinterpret_cast<uint4 *>(gv) + u * kRowUsers, x[u]);
-                            } else {
-                                float f[AE];
-                                E::unpack(x[u], f);
-#pragma unroll
-                                for (int j = 0; j < AE; ++j) Pack<DT>::store1(gv, u * kRowUsers * AE + j, f[j]);
-                            }
-                        }
+                        x[u] = none_vec<DT>();
+                        if (u < nu && tid + u * kRowUsers < cnt) x[u] = in[u * kRowUsers];
                     }
                 }
-                if (s2 == 0 && q.ie >= 0)
-                    Pack<DT>::store1(gp, q.ie, live ? ref_grad<ENT>(extra(row, q.ie), ref, k.x, k.y) : 0.f);
-                if (live) {
-                    // the token's element once more, by the thread that wrote it
-                    const int32_t tok = (int32_t)meta[i].tok, rel = tok - (q.first - tid * AE) - s2 * stage * AE;
-                    const bool mine = (s2 == 0 && q.ie == tok) || (rel >= 0 && rel < stage * AE && rel < cnt * AE &&
-                                                                   (rel / AE) % kRowUsers == tid);
-                    if (mine) Pack<DT>::store1(gp, tok, __fadd_rn(ref_grad<ENT>(xt, ref, k.x, k.y), k.z));
+                if (r.mask) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (u < nu) mask_vec<DT>(x[u], mask_bits<AE>(lo[u], hi[u], e0 + u * kRowUsers * AE));
                 }
-                if (++s2 == stages) {
-                    s2 = 0;
-                    ++k2;
+                float top = largest<DT>(x, nu);
+                __syncwarp();
+                if (lane == 0) arrive_one(&empty[slot]);
+                if (++slot == S) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+                if (top != top) {  // NaN counts as -inf
+                    clean_all<DT>(x, nu);
+                    top = largest<DT>(x, nu);
+                }
+                float xe = -INFINITY;  // the element outside the vectors
+                if (s == 0) {
+                    if (p.ie >= 0 && (!r.mask || allowed_bit(r.mask + (size_t)row * r.mstride, p.ie)))
+                        xe = load_clean(logits_at(row), DT, p.ie);
+                    top = warp_max(fmaxf(top, xe));
+                }
+                if (top > sum.m) raise<ENT>(sum, top, c2);
+                if (sum.m > -INFINITY) {
+                    const Ref ref = make_ref(sum.m, c2);
+                    if (ref.near)
+                        add_vecs<DT, ENT, true>(x, nu, ref, sum);
+                    else
+                        add_vecs<DT, ENT, false>(x, nu, ref, sum);
+                    if (s == 0 && p.ie >= 0) add_one<ENT>(xe, ref, sum);
                 }
             }
-            if (end1 && (!GRAD || k2 == k1)) break;
+            const float4 total = against_top<ENT>(sum, c2);
+            // rows are finished in order; half a ring behind at most
+            if (k >= RING / 2)
+                ok = ok && mbar_wait_bounded(&fin[(k - RING / 2) % RING], ((k - RING / 2) / RING) & 1u, status);
+            if (lane == 0) {
+                sums[i][warp] = total;
+                arrive_one(&summed[i]);
+            }
         }
     }
     __syncwarp();
@@ -907,10 +775,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
 // A CTA's share comes by one bulk copy into shared memory and goes to registers
 // at once; the next row's copy starts as soon as every warp has read it.  The
 // warps send their sums to every CTA of the cluster (asynchronous stores that
-// count on the receiver's barrier).  HBM reads every logit once and L2 is not
-// needed, where the streamed form reads it a second time from L2, which keeps
-// little of it beside the gradient's stores: 4,096 x 128,256 bf16 take 434 us
-// there.
+// count on the receiver's barrier).  HBM reads every logit once.  (Streaming a
+// row a second time from L2 instead does not work: beside the gradient's stores
+// L2 keeps too little of it.  4,096 x 128,256 bf16 took 434 us so.)
 //
 // Two CTAs share an SM, so that one's exchange passes under the other's
 // arithmetic, and the issue slots decide (13 instructions an element where the
@@ -1058,30 +925,14 @@ __global__ void __launch_bounds__(kHeldThreads, 2) row_held_kernel(RowLossArgs r
                 add_vecs<DT, ENT, true>(x, nu, ref, sum);
             else
                 add_vecs<DT, ENT, false>(x, nu, ref, sum);
-            if (p.ie >= 0) {
-                unsigned long long e, y;
-                if (ref.near)
-                    exp_pair<ENT, true>(xe, -INFINITY, ref, e, y);
-                else
-                    exp_pair<ENT, false>(xe, -INFINITY, ref, e, y);
-                float a, b, ignored;
-                split_pair(e, a, ignored);
-                split_pair(y, b, ignored);
-                sum.Z += a;
-                if (ENT) sum.t = fmaf(a, b, sum.t);
-            }
-            // the warp's sums against its largest logit itself
-            float f;
-            const float d = near_shift(top, c2, &f);
-            sum.Z = warp_sum_f32(sum.Z);
-            if (ENT) sum.t = f * fmaf(-d, sum.Z, warp_sum_f32(sum.t));
-            sum.Z *= f;
+            if (p.ie >= 0) add_one<ENT>(xe, ref, sum);
         }
+        const float4 total = against_top<ENT>(sum, c2);
         // These slots were last read two rows ago: a warp sends after its CTA
         // has finished the row before, for which every CTA had sent, and so
         // finished the row before that.
         if (lane < (int)C)
-            send_stat(&stats[half][(int)rank * WARPS + warp], &joined[half], (uint32_t)lane, top, sum.Z, sum.t);
+            send_stat(&stats[half][(int)rank * WARPS + warp], &joined[half], (uint32_t)lane, total.x, total.y, total.z);
         if (warp == (int)((turn + 3u) % WARPS)) {  // finish the row
             ok = ok && mbar_wait_bounded(&joined[half], (turn >> 1) & 1u, status);
             const int n = WARPS << lg;
@@ -1097,13 +948,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) row_held_kernel(RowLossArgs r
             s.Z = s.m == INFINITY ? __int_as_float(0x7FC00000) : warp_sum_f32(s.Z);
             if (ENT) s.t = warp_sum_f32(s.t);
             const RowScalars gs = finish_row<0, ENT>(r, row, s, mt.xt, mt.T, mt.w, rank == 0 && lane == 0);
-            if (lane == 0) {
-                // a row that does not count (its token masked) gets zeros
-                const GradCoef kc = mt.xt > -INFINITY ? grad_coef<ENT>(gs, s) : GradCoef{0.f, 0.f};
-                float f;
-                const float d = near_shift(s.m, c2, &f);
-                finished = make_float4(f * fmaf(-d, kc.k2, kc.k1), f * kc.k2, gs.a, s.m);
-            }
+            if (lane == 0) finished = finished_coef<ENT>(gs, s, mt.xt, c2);
         }
         if (warp == (int)((turn + 6u) % WARPS)) {  // look two rows ahead
             const int64_t next = meta[(turn + 1u) & 3u].row;
@@ -1206,15 +1051,16 @@ __device__ __forceinline__ Sum2 block_sum(Sum2 v, Sum2 *sh) {
     return v;
 }
 
-// The gradient of a row whose m, Z and coefficient are known:
-// coef / T (1{j = i} - p_j), element by element; grid (slices of a row, rows).
-// Rows are taken last to first: the sums' pass ended with the last ones,
-// whose logits are the ones still in L2.  The first CTA also writes the loss,
-// the mean of the pairs' losses, in a fixed order.
+// The gradient of rows whose coefficients are known (k1, k2, a and m in `fin`),
+// element by element; grid (slices of 32 KB of a row, rows).  Rows are taken
+// last to first: the sums' pass ended with the last ones, whose logits are the
+// ones still in L2.  The first CTA also writes a preference loss, the mean of
+// the pairs' losses, in a fixed order.  3,400 rows of 128,256 bf16 logits and
+// 1,140 skipped ones: 291 us, 7.0 TB/s.
 constexpr int kKnownThreads = 256;
-constexpr int kKnownU = 4;
+constexpr int kKnownU = 8;
 
-template <int DT>
+template <int DT, bool ENT>
 __global__ void __launch_bounds__(kKnownThreads) row_grad_kernel(RowLossArgs r, const float *pair_loss, int64_t pairs,
                                                                  float *loss) {
     using E = Elem<DT>;
@@ -1222,7 +1068,7 @@ __global__ void __launch_bounds__(kKnownThreads) row_grad_kernel(RowLossArgs r, 
     __shared__ Sum2 sh[kKnownThreads / 32];
     pdl_wait_primary();
     const int tid = threadIdx.x;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+    if (loss && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
         Sum2 s = {0.f, 0.f};
         for (int64_t i = tid; i < pairs; i += kKnownThreads) s.add(pair_loss[i]);
         s = block_sum<kKnownThreads>(s, sh);
@@ -1232,54 +1078,68 @@ __global__ void __launch_bounds__(kKnownThreads) row_grad_kernel(RowLossArgs r, 
     if (row < 0) return;
     const uint8_t *rp = static_cast<const uint8_t *>(r.logits) + (size_t)row * r.stride * E::SIZE;
     uint8_t *gp = static_cast<uint8_t *>(r.grad) + (size_t)row * r.gstride * E::SIZE;
-    const Slice32 g = make_slice32<AE, E::SIZE>(rp, (int32_t)r.V, blockIdx.x, gridDim.x);
+    const int32_t V = (int32_t)r.V, head = min((int32_t)((0u - (uint32_t)(uintptr_t)rp) & 15u) / E::SIZE, V);
+    const int32_t nvec = (V - head) / AE, tail = (V - head) & (AE - 1);
+    const int32_t v0 = (int32_t)blockIdx.x * kKnownThreads * kKnownU + tid, left = nvec - v0;
     const bool same = ((reinterpret_cast<uintptr_t>(rp) ^ reinterpret_cast<uintptr_t>(gp)) & 15u) == 0;
-    const float coef = r.coef[row];
-    const bool live = coef != 0.f;
-    const float T = row_temperature(r, row), c2 = kLog2eL / T, m = r.row_m[row];
-    const float a = coef / T;
-    const GradCoef k = {-a / r.row_z[row], 0.f};
-    const int64_t tok = r.tokens[row];
-    auto store_el = [&](int32_t i) {
-        float f = live ? grad_el<false>(load_clean(rp, DT, i), m, c2, k) : 0.f;
-        if (live && i == tok) f = __fadd_rn(f, a);
-        Pack<DT>::store1(gp, i, f);
+    const int32_t e_first = head + v0 * AE;
+    // one element outside the vectors, by the first CTA of a row
+    const int32_t ie = blockIdx.x != 0 ? -1 : (tid < head ? tid : (tid >= 8 && tid - 8 < tail ? V - tail + tid - 8 : -1));
+    const float4 k = r.fin[row];
+    auto store = [&](int u, const uint4 &x) {
+        if (same) {
+            __stcs(reinterpret_cast<uint4 *>(gp + (size_t)e_first * E::SIZE) + u * kKnownThreads, x);
+        } else {
+            float f[AE];
+            E::unpack(x, f);
+#pragma unroll
+            for (int q = 0; q < AE; ++q) Pack<DT>::store1(gp, e_first + u * kKnownThreads * AE + q, f[q]);
+        }
     };
-    if (!same) {
-        for (int32_t i = g.lo + tid; i < g.hi; i += kKnownThreads) store_el(i);
+    if (k.x == 0.f && k.z == 0.f && (!ENT || k.y == 0.f)) {  // skipped, or nothing to change
+#pragma unroll
+        for (int u = 0; u < kKnownU; ++u)
+            if (u * kKnownThreads < left) store(u, make_uint4(0u, 0u, 0u, 0u));
+        if (ie >= 0) Pack<DT>::store1(gp, ie, 0.f);
         return;
     }
-    if (g.lo == 0 && tid < g.head) store_el(tid);
-    if (g.hi == (int32_t)r.V && tid < g.tail) store_el(g.hi - g.tail + tid);
-    for (int32_t v0 = g.vc0 + tid; v0 < g.vc0 + g.nv; v0 += kKnownThreads * kKnownU) {
-        uint4 x[kKnownU];
+    uint4 x[kKnownU];
 #pragma unroll
-        for (int u = 0; u < kKnownU; ++u) {
-            const int32_t v = v0 + u * kKnownThreads;
-            x[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (live && v < g.vc0 + g.nv) {
-                x[u] = *reinterpret_cast<const uint4 *>(rp + (size_t)(g.head + v * AE) * E::SIZE);
-                Pack<DT>::clean(x[u]);
-            }
-        }
+    for (int u = 0; u < kKnownU; ++u) {
+        x[u] = none_vec<DT>();
+        if (u * kKnownThreads < left)
+            x[u] = *(reinterpret_cast<const uint4 *>(rp + (size_t)e_first * E::SIZE) + u * kKnownThreads);
+    }
+    const int32_t *mrow = r.mask ? r.mask + (size_t)row * r.mstride : nullptr;
+    if (mrow) {
+        uint32_t lo[kKnownU], hi[kKnownU];
 #pragma unroll
-        for (int u = 0; u < kKnownU; ++u) {
-            const int32_t v = v0 + u * kKnownThreads;
-            if (v >= g.vc0 + g.nv) continue;
-            const int32_t e0 = g.head + v * AE;
-            if (live) {
-                float f[AE];
-                E::unpack(x[u], f);
+        for (int u = 0; u < kKnownU; ++u)
+            mask_words<AE>(mrow, e_first + u * kKnownThreads * AE, u * kKnownThreads < left, lo[u], hi[u]);
 #pragma unroll
-                for (int q = 0; q < AE; ++q) {
-                    f[q] = grad_el<false>(f[q], m, c2, k);
-                    if (e0 + q == (int32_t)tok) f[q] = __fadd_rn(f[q], a);
-                }
-                x[u] = Pack<DT>::vec(f);
-            }
-            __stcs(reinterpret_cast<uint4 *>(gp + (size_t)e0 * E::SIZE), x[u]);
+        for (int u = 0; u < kKnownU; ++u)
+            mask_vec<DT>(x[u], mask_bits<AE>(lo[u], hi[u], e_first + u * kKnownThreads * AE));
+    }
+    const Ref ref = make_ref(k.w, kLog2eL / row_temperature(r, row));
+    const float xe = ie >= 0 && (!mrow || allowed_bit(mrow, ie)) ? load_clean(rp, DT, ie) : -INFINITY;
+    const int32_t tok = (int32_t)r.tokens[row], rel = tok - (head + (v0 - tid) * AE);
+    const bool mine = tok == ie || (rel >= 0 && rel < kKnownThreads * kKnownU * AE && tok < V - tail &&
+                                    (rel / AE) % kKnownThreads == tid);
+    const float xt = mine ? load_clean(rp, DT, tok) : 0.f;  // before it may be written over
+#pragma unroll
+    for (int u = 0; u < kKnownU; ++u) {
+        if (u * kKnownThreads < left) {
+            Pack<DT>::clean(x[u]);
+            if (ref.near)
+                grad_vec<DT, ENT, true>(x[u], ref, k.x, k.y);
+            else
+                grad_vec<DT, ENT, false>(x[u], ref, k.x, k.y);
+            store(u, x[u]);
         }
     }
+    if (ie >= 0) Pack<DT>::store1(gp, ie, ref_grad<ENT>(xe, ref, k.x, k.y));
+    // the token's element once more, by the thread that wrote it
+    if (mine) Pack<DT>::store1(gp, tok, __fadd_rn(ref_grad<ENT>(xt, ref, k.x, k.y), k.z));
 }
 
 }  // namespace loss_detail

@@ -3,22 +3,20 @@
 
 namespace tsa {
 
-const void *row_loss_kernel_f32(int mode, bool grad, bool ent) {
-    using namespace loss_detail;
-    if (mode == 1) return reinterpret_cast<const void *>(&row_loss_kernel<0, 1, false, false>);
-    if (grad)
-        return ent ? reinterpret_cast<const void *>(&row_loss_kernel<0, 0, true, true>)
-                   : reinterpret_cast<const void *>(&row_loss_kernel<0, 0, true, false>);
-    return ent ? reinterpret_cast<const void *>(&row_loss_kernel<0, 0, false, true>)
-               : reinterpret_cast<const void *>(&row_loss_kernel<0, 0, false, false>);
-}
+using namespace loss_detail;
 
+const void *row_loss_kernel_f32(int mode, bool ent) {
+    if (mode == 1) return reinterpret_cast<const void *>(&row_loss_kernel<0, 1, false>);
+    return ent ? reinterpret_cast<const void *>(&row_loss_kernel<0, 0, true>)
+               : reinterpret_cast<const void *>(&row_loss_kernel<0, 0, false>);
+}
 const void *row_held_kernel_f32(bool ent) {
-    using namespace loss_detail;
     return ent ? reinterpret_cast<const void *>(&row_held_kernel<0, true>)
                : reinterpret_cast<const void *>(&row_held_kernel<0, false>);
 }
-
-const void *row_grad_kernel_f32() { return reinterpret_cast<const void *>(&loss_detail::row_grad_kernel<0>); }
+const void *row_grad_kernel_f32(bool ent) {
+    return ent ? reinterpret_cast<const void *>(&row_grad_kernel<0, true>)
+               : reinterpret_cast<const void *>(&row_grad_kernel<0, false>);
+}
 
 }  // namespace tsa

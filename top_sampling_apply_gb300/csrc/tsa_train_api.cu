@@ -54,12 +54,18 @@ int check_tensors(const tsa_adamw_tensor *t, int64_t count, size_t ps, size_t gs
 
 extern "C" {
 
+size_t tsa_policy_loss_workspace_bytes(int64_t B, int64_t V, tsa_dtype dtype) {
+    if (B < 1 || V < 1 || (dtype != TSA_F32 && dtype != TSA_F16 && dtype != TSA_BF16) || row_is_held(V, dtype)) return 0;
+    return align256((size_t)B * sizeof(float4));
+}
+
 int tsa_policy_loss(const void *logits, tsa_dtype dtype, int64_t B, int64_t V, int64_t logits_row_stride,
                     const int32_t *bitmask, int64_t mask_row_stride, const float *temperature, float temperature_s,
                     const int64_t *tokens, const float *old_logprob, const float *advantage,
                     const float *ref_logprob, const float *weight, float clip_low, float clip_high, float kl_coef,
                     float entropy_coef, float *loss_out, float *row_loss_out, float *logprob_out,
-                    float *entropy_out, void *grad_out, int64_t grad_row_stride, void *stream) {
+                    float *entropy_out, void *grad_out, int64_t grad_row_stride, void *workspace,
+                    size_t workspace_bytes, void *stream) {
     int st = rows_check_args(logits, dtype, B, V, logits_row_stride);
     if (st != TSA_OK) return st;
     if (!(clip_low >= 0.f) || !(clip_high >= 0.f) || !isfinite(clip_low) || !isfinite(clip_high) ||
@@ -74,6 +80,11 @@ int tsa_policy_loss(const void *logits, tsa_dtype dtype, int64_t B, int64_t V, i
         return TSA_ERR_ALIGN;
     st = check_grad(logits, grad_out, dtype, B, V, logits_row_stride, grad_row_stride);
     if (st != TSA_OK) return st;
+    const size_t need = grad_out ? tsa_policy_loss_workspace_bytes(B, V, dtype) : 0;
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return TSA_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return TSA_ERR_ALIGN;
+    }
     const cudaStream_t s = (cudaStream_t)stream;
     if (B == 0) {
         if (!loss_out) return TSA_OK;
@@ -101,15 +112,22 @@ int tsa_policy_loss(const void *logits, tsa_dtype dtype, int64_t B, int64_t V, i
     a.row_loss = row_loss_out;
     a.logprob = logprob_out;
     a.entropy = entropy_out;
-    a.grad = grad_out;
-    a.gstride = grad_row_stride;
     const bool ent = entropy_out != nullptr || entropy_coef != 0.f;
+    a.gstride = grad_row_stride;
+    if (need > 0)
+        a.fin = static_cast<float4 *>(workspace);
+    else
+        a.grad = grad_out;
     if (row_loss_launch(a, dtype, 0, ent, s) != 0) return TSA_ERR_CUDA;
+    if (need > 0) {
+        a.grad = grad_out;
+        if (row_grad_launch(a, dtype, ent, nullptr, 0, nullptr, s) != 0) return TSA_ERR_CUDA;
+    }
     return weighted_sum_launch(row_loss_out, weight, a.weight_s, B, loss_out, s) == 0 ? TSA_OK : TSA_ERR_CUDA;
 }
 
 size_t tsa_preference_loss_workspace_bytes(int64_t N) {
-    return N < 1 ? 0 : 3 * align256((size_t)N * sizeof(float));
+    return N < 1 ? 0 : align256((size_t)N * sizeof(float4));
 }
 
 int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t V, int64_t logits_row_stride,
@@ -137,8 +155,6 @@ int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t 
         if (!aligned(workspace, 256)) return TSA_ERR_ALIGN;
     }
     const cudaStream_t s = (cudaStream_t)stream;
-    const size_t each = need / 3;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
     RowLossArgs a = {};
     a.logits = logits;
     a.B = N;
@@ -149,9 +165,7 @@ int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t 
     a.weight = weight;
     a.weight_s = 1.f;
     a.logprob = logprob_out;
-    a.row_m = reinterpret_cast<float *>(ws);
-    a.row_z = reinterpret_cast<float *>(ws + each);
-    a.coef = reinterpret_cast<float *>(ws + 2 * each);
+    a.fin = static_cast<float4 *>(workspace);
     if (N > 0 && row_loss_launch(a, dtype, 1, false, s) != 0) return TSA_ERR_CUDA;
     if (P > 0) {
         PairArgs p = {};
@@ -167,7 +181,6 @@ int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t 
         p.average = average;
         p.pair_loss = pair_loss_out;
         p.reward = reward_out;
-        p.coef = a.coef;
         if (pair_launch(p, a, s) != 0) return TSA_ERR_CUDA;
     }
     if (N == 0 || !grad_out) {
@@ -177,7 +190,7 @@ int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t 
     }
     a.grad = grad_out;
     a.gstride = grad_row_stride;
-    return row_grad_launch(a, dtype, pair_loss_out, P, loss_out, s) == 0 ? TSA_OK : TSA_ERR_CUDA;
+    return row_grad_launch(a, dtype, false, pair_loss_out, P, loss_out, s) == 0 ? TSA_OK : TSA_ERR_CUDA;
 }
 
 int tsa_adamw_step(const tsa_adamw_tensor *tensors, int64_t count, tsa_dtype param_dtype, tsa_dtype grad_dtype,
