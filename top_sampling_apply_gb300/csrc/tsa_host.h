@@ -181,9 +181,9 @@ int weighted_sum_launch(const float *x, const float *w, float w_s, int64_t n, fl
 const void *row_loss_kernel_f32(int mode, bool ent);
 const void *row_loss_kernel_f16(int mode, bool ent);
 const void *row_loss_kernel_bf16(int mode, bool ent);
-const void *row_held_kernel_f32(bool ent);
-const void *row_held_kernel_f16(bool ent);
-const void *row_held_kernel_bf16(bool ent);
+const void *row_held_kernel_f32(bool ent, int threads);
+const void *row_held_kernel_f16(bool ent, int threads);
+const void *row_held_kernel_bf16(bool ent, int threads);
 const void *row_grad_kernel_f32(bool ent);
 const void *row_grad_kernel_f16(bool ent);
 const void *row_grad_kernel_bf16(bool ent);

@@ -112,8 +112,9 @@ const void *loss_kernel(int dtype, int mode, bool ent) {
     return dtype == 0 ? row_loss_kernel_f32(mode, ent)
                       : (dtype == 1 ? row_loss_kernel_f16(mode, ent) : row_loss_kernel_bf16(mode, ent));
 }
-const void *held_kernel(int dtype, bool ent) {
-    return dtype == 0 ? row_held_kernel_f32(ent) : (dtype == 1 ? row_held_kernel_f16(ent) : row_held_kernel_bf16(ent));
+const void *held_kernel(int dtype, bool ent, int threads) {
+    return dtype == 0 ? row_held_kernel_f32(ent, threads)
+                      : (dtype == 1 ? row_held_kernel_f16(ent, threads) : row_held_kernel_bf16(ent, threads));
 }
 const void *grad_kernel(int dtype, bool ent) {
     return dtype == 0 ? row_grad_kernel_f32(ent) : (dtype == 1 ? row_grad_kernel_f16(ent) : row_grad_kernel_bf16(ent));
@@ -172,12 +173,19 @@ static int row_cluster(int64_t B, int64_t V, int es) {
     return C;
 }
 
+// The threads of a CTA that holds a row, or its share of one.
+static int held_threads(int64_t V, int es) {
+    const int64_t nvec = V * es / 16;
+    for (int t = 128; t < loss_detail::kHeldThreads; t *= 2)
+        if (nvec <= (int64_t)t * loss_detail::kHeldVecs) return t;
+    return loss_detail::kHeldThreads;
+}
 // The CTAs that hold a row together, 0 if its vectors do not fit eight.  Fewer
 // rows than SMs are spread further, down to one vector a thread: 8 rows of
 // 8,192 fp32 logits use 64 CTAs instead of 8.
 static int held_cluster(int64_t B, int64_t V, int es) {
-    const int64_t nvec = V * es / 16 + 1;
-    const int64_t one = loss_detail::kHeldThreads, per = one * loss_detail::kHeldVecs;
+    const int64_t nvec = V * es / 16;
+    const int64_t one = held_threads(V, es), per = one * loss_detail::kHeldVecs;
     int C = 1;
     while (C <= loss_detail::kHeldCluster && (nvec + C - 1) / C > per) C *= 2;
     if (C > loss_detail::kHeldCluster) return 0;
@@ -221,7 +229,8 @@ int row_loss_launch(const RowLossArgs &args, int dtype, int mode, bool ent, cuda
         if (C == 0) return -1;
         while ((1 << lg) < C) ++lg;
         void *params[] = {&a, &lg, &status};
-        return launch_rows(held_kernel(dtype, ent), args.B, C, kHeldThreads, kHeldSmem, params, st);
+        const int threads = held_threads(args.V, es);
+        return launch_rows(held_kernel(dtype, ent, threads), args.B, C, threads, held_smem(threads), params, st);
     }
     const int C = row_cluster(args.B, args.V, es);
     while ((1 << lg) < C) ++lg;

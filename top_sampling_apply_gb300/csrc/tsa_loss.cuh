@@ -199,13 +199,37 @@ __device__ __forceinline__ float token_logit(const RowLossArgs &r, const void *r
     return load_clean(rp, dt, tok);
 }
 
+// What is to be known of a row before its sums are.  It is fetched rows ahead:
+// read when a row is finished, the last three cost every row a trip to memory.
+struct RowMeta {
+    int64_t row, tok;  // row = B: there are no more
+    float w, T, c2, xt;
+    float old, adv, ref;
+};
+template <int DT, int MODE>
+__device__ __forceinline__ RowMeta row_meta(const RowLossArgs &r, int64_t b, float w, int64_t tok) {
+    RowMeta m = {b, tok, w, 1.f, 1.f, -INFINITY, 0.f, 0.f, 0.f};
+    if (b < r.B) {
+        if (MODE == 0) {
+            m.old = __ldg(r.old_logprob + b);
+            m.adv = __ldg(r.advantage + b);
+            if (r.ref_logprob) m.ref = __ldg(r.ref_logprob + b);
+        }
+        m.T = row_temperature(r, b);
+        m.c2 = kLog2eL / m.T;
+        m.xt = token_logit(r, static_cast<const uint8_t *>(r.logits) + (size_t)b * r.stride * Elem<DT>::SIZE,
+                           r.mask ? r.mask + (size_t)b * r.mstride : nullptr, DT, tok);
+    }
+    return m;
+}
+
 // The loss of one row from its log-probability lp and entropy H, and its
 // derivative c by lp.  min() takes the unclipped branch on a tie, where both
 // branches have the same value; an advantage of 0 gives 0 even if the ratio
 // overflows.
-__device__ __forceinline__ float policy_row(const RowLossArgs &r, int64_t row, float lp, float H, float *c) {
-    const float A = __ldg(r.advantage + row);
-    const float ratio = expf(lp - __ldg(r.old_logprob + row));
+__device__ __forceinline__ float policy_row(const RowLossArgs &r, const RowMeta &mt, float lp, float H, float *c) {
+    const float A = mt.adv;
+    const float ratio = expf(lp - mt.old);
     float loss = 0.f, d = 0.f;
     if (A != 0.f) {
         const float s1 = ratio * A, s2 = fminf(fmaxf(ratio, r.clip_lo), r.clip_hi) * A;
@@ -215,7 +239,7 @@ __device__ __forceinline__ float policy_row(const RowLossArgs &r, int64_t row, f
         d = clipped ? 0.f : -s1;
     }
     if (r.ref_logprob) {
-        const float u = __ldg(r.ref_logprob + row) - lp;
+        const float u = mt.ref - lp;
         const float e1 = expm1f(u);
         loss += r.kl * (e1 - u);
         d -= r.kl * e1;
@@ -227,8 +251,10 @@ __device__ __forceinline__ float policy_row(const RowLossArgs &r, int64_t row, f
 // ------------------------------------------------------------ a finished row
 // Fills row outputs (by one thread) and returns the gradient's numbers.
 template <int MODE, bool ENT>
-__device__ __forceinline__ RowScalars finish_row(const RowLossArgs &r, int64_t row, const RowStat &s, float xt,
-                                                 float T, float w, bool writer) {
+__device__ __forceinline__ RowScalars finish_row(const RowLossArgs &r, const RowMeta &mt, const RowStat &s,
+                                                 bool writer) {
+    const int64_t row = mt.row;
+    const float xt = mt.xt, T = mt.T;
     RowScalars g = {0.f, 0.f};
     const float Z = s.m == INFINITY ? __int_as_float(0x7FC00000) : s.Z;
     const float lnZ = logf(Z);
@@ -237,9 +263,9 @@ __device__ __forceinline__ RowScalars finish_row(const RowLossArgs &r, int64_t r
     if (MODE == 0) {
         const float H = ENT ? lnZ - kLn2 * (s.t / Z) : 0.f;
         float c = 0.f;
-        const float loss = live ? policy_row(r, row, lp, H, &c) : 0.f;
+        const float loss = live ? policy_row(r, mt, lp, H, &c) : 0.f;
         if (live) {
-            const float wt = w / T;
+            const float wt = mt.w / T;
             g.b = ENT ? wt * r.ent : 0.f;
             g.a = wt * c;
         }
@@ -401,12 +427,6 @@ __device__ __forceinline__ void arrive_one(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 constexpr size_t kRowSmem = (size_t)kRowSlots * kRowStage * 16;
-
-// What a row's threads need to know of it.
-struct RowMeta {
-    int64_t row, tok;  // row = B: there are no more
-    float w, T, c2, xt;
-};
 
 // A warp's running sums against its reference m: in the form that m calls for
 // (see Ref).
@@ -590,8 +610,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
 
     if (warp == kRowWarps) {
         // ---- copies
-        RowMeta mine;
+        RowMeta mine = {r.B, -1, 0.f, 1.f, 1.f, 0.f, 0.f, 0.f, 0.f};
         uint32_t found = 0;
+        bool fresh = false;
         int64_t base = first_row;
         uint32_t slot = 0, phase = 1;
         for (uint32_t k = 0;; ++k) {
@@ -601,33 +622,15 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
                 float w = 0.f;
                 int64_t tok = -1;
                 const bool named = b < r.B && row_named(r, b, &w, &tok);
-                if (named) {
-                    mine.row = b;
-                    mine.tok = tok;
-                    mine.w = w;
-                    mine.T = row_temperature(r, b);
-                    mine.c2 = kLog2eL / mine.T;
-                    mine.xt = token_logit(r, logits_at(b), r.mask ? r.mask + (size_t)b * r.mstride : nullptr, DT, tok);
-                }
+                mine = {b, tok, w, 1.f, 1.f, 0.f, 0.f, 0.f, 0.f};
                 found = __ballot_sync(0xFFFFFFFFu, named);
+                fresh = true;
                 base += 32 * step;
             }
             const int who = found ? __ffs((int)found) - 1 : 0;
             const int64_t row = found ? __shfl_sync(0xFFFFFFFFu, mine.row, who) : r.B;
-            found &= found - 1;
-            // Rows k - 16 are done with: the stages hold back this warp to
-            // four rows before the summing ones, and those stay within eight of
-            // the finishing one.
-            if (lane == who) {
-                RowMeta m = mine;
-                m.row = row;
-                meta[k % RING] = m;
-                arrive_one(&known[k % RING]);
-            }
-            __syncwarp();
-            if (row >= r.B) break;
-            const RowPlace p = place_row<DT>(r, row, rank, lg);
-            for (int s = 0; s < stages; ++s) {
+            const RowPlace p = place_row<DT>(r, row < r.B ? row : 0, rank, lg);
+            auto copy = [&](int s) {
                 int cnt = p.nv - s * stage;
                 cnt = cnt < 0 ? 0 : (cnt > stage ? stage : cnt);
                 if (lane == 0) {
@@ -642,7 +645,24 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
                     slot = 0;
                     phase ^= 1u;
                 }
+            };
+            if (row < r.B) copy(0);
+            if (fresh && ((found >> lane) & 1u))  // the rest of what is known of 32 rows, under the copy
+                mine = row_meta<DT, MODE>(r, mine.row, mine.w, mine.tok);
+            fresh = false;
+            found &= found - 1;
+            // Rows k - 16 are done with: the stages hold back this warp to
+            // five rows before the summing ones, and those stay within eight of
+            // the finishing one.
+            if (lane == who) {
+                RowMeta m = mine;
+                m.row = row;
+                meta[k % RING] = m;
+                arrive_one(&known[k % RING]);
             }
+            __syncwarp();
+            if (row >= r.B) break;
+            for (int s = 1; s < stages; ++s) copy(s);
         }
     } else if (warp == kRowWarps + 1) {
         // ---- finished rows
@@ -670,7 +690,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
             }
             if (s.m == INFINITY) s.Z = __int_as_float(0x7FC00000);
             if (rank == 0) {
-                const RowScalars gs = finish_row<MODE, ENT>(r, mt.row, s, mt.xt, mt.T, mt.w, lane == 0);
+                const RowScalars gs = finish_row<MODE, ENT>(r, mt, s, lane == 0);
                 if (r.fin && lane == 0) {
                     if (MODE == 0)
                         r.fin[mt.row] = finished_coef<ENT>(gs, s, mt.xt, mt.c2);
@@ -786,33 +806,23 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
 // joins the sums and finishes.  4,096 x 128,256 bf16, an eighth of the rows
 // skipped: 353 us, 5.6 TB/s; with 256 threads of 16 vectors 366 us, with four
 // CTAs of 256 threads an SM, and clusters of 16 for fp32, 347 us.
-constexpr int kHeldVecs = 8, kHeldThreads = 512, kHeldWarps = kHeldThreads / 32;
+//
+// Rows of up to 16 or 32 KB take CTAs of 128 or 256 threads instead, so that an
+// SM has eight or four of them under way: the exchange of a row takes as long
+// as a short row's arithmetic (10,000 x 8,192 bf16: 164 us with 512 threads).
+constexpr int kHeldVecs = 8, kHeldThreads = 512;
 constexpr int kHeldCluster = 8;
-constexpr size_t kHeldSmem = (size_t)kHeldThreads * kHeldVecs * 16;
+constexpr size_t held_smem(int threads) { return (size_t)threads * kHeldVecs * 16; }
 
-// The first row from b on (by steps) that counts, by one warp; row = B if none.
-template <int DT>
-__device__ __forceinline__ RowMeta find_row(const RowLossArgs &r, int64_t b, int64_t step) {
-    RowMeta m = {r.B, -1, 0.f, 1.f, 1.f, -INFINITY};
-    float w = 0.f;
-    int64_t tok = 0;
-    while (b < r.B && !row_named(r, b, &w, &tok)) b += step;
-    if (b < r.B) {
-        m.row = b;
-        m.tok = tok;
-        m.w = w;
-        m.T = row_temperature(r, b);
-        m.c2 = kLog2eL / m.T;
-        m.xt = token_logit(r, static_cast<const uint8_t *>(r.logits) + (size_t)b * r.stride * Elem<DT>::SIZE,
-                           r.mask ? r.mask + (size_t)b * r.mstride : nullptr, DT, tok);
-    }
-    return m;
+// The first row from b on (by steps) that counts, B if none.
+__device__ __forceinline__ int64_t find_row(const RowLossArgs &r, int64_t b, int64_t step, float *w, int64_t *tok) {
+    while (b < r.B && !row_named(r, b, w, tok)) b += step;
+    return b < r.B ? b : r.B;
 }
-
-template <int DT, bool ENT>
-__global__ void __launch_bounds__(kHeldThreads, 2) row_held_kernel(RowLossArgs r, int lg, unsigned int *status) {
+template <int DT, bool ENT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLossArgs r, int lg, unsigned int *status) {
     using E = Elem<DT>;
-    constexpr int AE = E::AE, U = kHeldVecs, THREADS = kHeldThreads, WARPS = kHeldWarps;
+    constexpr int AE = E::AE, U = kHeldVecs, WARPS = THREADS / 32;
     extern __shared__ __align__(128) uint4 ring[];               // the CTA's vectors of a row
     __shared__ float4 stats[2][kHeldCluster * WARPS];            // the cluster's warps, this row and the next
     __shared__ RowMeta meta[4];
@@ -840,14 +850,20 @@ __global__ void __launch_bounds__(kHeldThreads, 2) row_held_kernel(RowLossArgs r
     }
     __syncthreads();
     if (warp == 0) {
-        const RowMeta a = find_row<DT>(r, zero, step), b = find_row<DT>(r, a.row < r.B ? a.row + step : r.B, step);
+        float w = 0.f;
+        int64_t tok = -1;
+        const int64_t a = find_row(r, zero, step, &w, &tok);
+        if (lane == 0 && a < r.B) {
+            mbar_arrive_expect_tx(&joined[0], (uint32_t)(WARPS << lg) * 16u);
+            fetch(a);
+        }
+        __syncwarp();
+        const RowMeta ma = row_meta<DT, 0>(r, a, w, tok);
+        const int64_t b = find_row(r, a < r.B ? a + step : r.B, step, &w, &tok);
+        const RowMeta mb = row_meta<DT, 0>(r, b, w, tok);
         if (lane == 0) {
-            meta[0] = a;
-            meta[1] = b;
-            if (a.row < r.B) {
-                mbar_arrive_expect_tx(&joined[0], (uint32_t)(WARPS << lg) * 16u);
-                fetch(a.row);
-            }
+            meta[0] = ma;
+            meta[1] = mb;
         }
     }
     if (C > 1)
@@ -947,12 +963,15 @@ __global__ void __launch_bounds__(kHeldThreads, 2) row_held_kernel(RowLossArgs r
             }
             s.Z = s.m == INFINITY ? __int_as_float(0x7FC00000) : warp_sum_f32(s.Z);
             if (ENT) s.t = warp_sum_f32(s.t);
-            const RowScalars gs = finish_row<0, ENT>(r, row, s, mt.xt, mt.T, mt.w, rank == 0 && lane == 0);
+            const RowScalars gs = finish_row<0, ENT>(r, mt, s, rank == 0 && lane == 0);
             if (lane == 0) finished = finished_coef<ENT>(gs, s, mt.xt, c2);
         }
         if (warp == (int)((turn + 6u) % WARPS)) {  // look two rows ahead
             const int64_t next = meta[(turn + 1u) & 3u].row;
-            const RowMeta m2 = find_row<DT>(r, next < r.B ? next + step : r.B, step);
+            float w = 0.f;
+            int64_t tok = -1;
+            const int64_t b = find_row(r, next < r.B ? next + step : r.B, step, &w, &tok);
+            const RowMeta m2 = row_meta<DT, 0>(r, b, w, tok);
             if (lane == 0) meta[(turn + 2u) & 3u] = m2;
         }
         __syncthreads();

@@ -10,10 +10,13 @@ const void *row_loss_kernel_bf16(int mode, bool ent) {
     return ent ? reinterpret_cast<const void *>(&row_loss_kernel<2, 0, true>)
                : reinterpret_cast<const void *>(&row_loss_kernel<2, 0, false>);
 }
-const void *row_held_kernel_bf16(bool ent) {
-    return ent ? reinterpret_cast<const void *>(&row_held_kernel<2, true>)
-               : reinterpret_cast<const void *>(&row_held_kernel<2, false>);
+template <bool ENT>
+static const void *held(int threads) {
+    return threads == 128   ? reinterpret_cast<const void *>(&row_held_kernel<2, ENT, 128>)
+           : threads == 256 ? reinterpret_cast<const void *>(&row_held_kernel<2, ENT, 256>)
+                            : reinterpret_cast<const void *>(&row_held_kernel<2, ENT, 512>);
 }
+const void *row_held_kernel_bf16(bool ent, int threads) { return ent ? held<true>(threads) : held<false>(threads); }
 const void *row_grad_kernel_bf16(bool ent) {
     return ent ? reinterpret_cast<const void *>(&row_grad_kernel<2, true>)
                : reinterpret_cast<const void *>(&row_grad_kernel<2, false>);

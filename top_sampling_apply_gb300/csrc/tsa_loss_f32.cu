@@ -10,10 +10,13 @@ const void *row_loss_kernel_f32(int mode, bool ent) {
     return ent ? reinterpret_cast<const void *>(&row_loss_kernel<0, 0, true>)
                : reinterpret_cast<const void *>(&row_loss_kernel<0, 0, false>);
 }
-const void *row_held_kernel_f32(bool ent) {
-    return ent ? reinterpret_cast<const void *>(&row_held_kernel<0, true>)
-               : reinterpret_cast<const void *>(&row_held_kernel<0, false>);
+template <bool ENT>
+static const void *held(int threads) {
+    return threads == 128   ? reinterpret_cast<const void *>(&row_held_kernel<0, ENT, 128>)
+           : threads == 256 ? reinterpret_cast<const void *>(&row_held_kernel<0, ENT, 256>)
+                            : reinterpret_cast<const void *>(&row_held_kernel<0, ENT, 512>);
 }
+const void *row_held_kernel_f32(bool ent, int threads) { return ent ? held<true>(threads) : held<false>(threads); }
 const void *row_grad_kernel_f32(bool ent) {
     return ent ? reinterpret_cast<const void *>(&row_grad_kernel<0, true>)
                : reinterpret_cast<const void *>(&row_grad_kernel<0, false>);
