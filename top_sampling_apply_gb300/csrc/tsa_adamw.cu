@@ -277,10 +277,17 @@ __device__ __forceinline__ void step8(const AdamPairs &a, const float (&g)[8], f
 #pragma unroll
     for (int q = 0; q < 8; q += 2) {
         const unsigned long long gs = mul2(pair_of(g[q], g[q + 1]), a.scale);
-        const unsigned long long mm = add2(mul2(a.b1, pair_of(m[q], m[q + 1])), mul2(a.b1c, gs));
-        const unsigned long long vv = add2(mul2(a.b2, pair_of(v[q], v[q + 1])), mul2(a.b2c, mul2(gs, gs)));
-        split_pair(mm, m[q], m[q + 1]);
-        split_pair(vv, v[q], v[q + 1]);
+        // the last sums one by one: a packed sum of packed products was fused
+        float m0, m1, n0, n1;
+        split_pair(mul2(a.b1, pair_of(m[q], m[q + 1])), m0, m1);
+        split_pair(mul2(a.b1c, gs), n0, n1);
+        m[q] = __fadd_rn(m0, n0);
+        m[q + 1] = __fadd_rn(m1, n1);
+        split_pair(mul2(a.b2, pair_of(v[q], v[q + 1])), m0, m1);
+        split_pair(mul2(a.b2c, mul2(gs, gs)), n0, n1);
+        v[q] = __fadd_rn(m0, n0);
+        v[q + 1] = __fadd_rn(m1, n1);
+        const unsigned long long mm = pair_of(m[q], m[q + 1]);
         // The root of v' (2^-126 at least: a smaller one's root is below
         // 2^-63 either way) and the reciprocal, each within 2^-22: the
         // update, some thousandths of p, is within 2^-20 of itself.

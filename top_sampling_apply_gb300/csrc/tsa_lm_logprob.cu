@@ -122,8 +122,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
 // One persistent CTA an SM.  Warp 0 fetches tiles of 64 columns of H by TMA
 // into a ring of stages, warp 1 issues the products, and warps 2 to 5 reduce
 // the finished scores from one half of tensor memory while the next tile's
-// products fill the other half (warps 2 to 9 where the scores are many: two
-// for each quarter of the lanes, a half of the columns each).
+// products fill the other half (warps 2 to 9 where the scores are many: four
+// for each quarter of the lanes, a quarter of the columns each).
 //
 // ROWS = false (few rows): the 128 lanes of tensor memory are vocabulary
 // entries and the N columns are the hidden rows, so the weight is all that
@@ -134,11 +134,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
 // only the ones it needs.  A thread keeps one (m, Z) a hidden row over all its
 // CTA's tiles; one part a CTA.
 // ROWS = true: the lanes are 128 hidden rows and the columns N vocabulary
-// entries; a thread reduces N / 2 of its row's scores by itself, 32 at a time
-// from registers while the next 32 come.  Tiles go through the hidden rows
+// entries; a thread reduces N / 2 of its row's scores by itself.  Tiles go through the hidden rows
 // first, so that a weight tile is fetched from HBM once and from L2 by the
 // other row blocks.  One part for every N / 2 entries of the vocabulary.
 constexpr int kTcK = 64;
+// The tensor cores add to their accumulator with truncation: a score of 320
+// steps (H = 5,120) came out 9e-6 of itself too small, and 2,048
+// log-probabilities were off by 2.4e-6 of themselves.  So the products of 512
+// columns (1,024 where the products bound the kernel) at a time go to tensor
+// memory and from there, rounded to nearest, into sums in registers: now 4e-7,
+// for 7 % of the time.
+template <bool ROWS>
+constexpr int kTcChunk = (ROWS ? 1024 : 512) / kTcK;  // steps of kTcK a chunk
 template <bool ROWS>
 constexpr int kTcThreads = ROWS ? 320 : 192;  // eight or four warps take the scores
 
@@ -161,7 +168,8 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
     __shared__ uint64_t full[STAGES], empty[STAGES], done[2], drained[2], last;
     __shared__ uint32_t tmem_slot;
     __shared__ float2 s_part[4][ROWS ? 1 : N];
-    __shared__ __align__(16) float s_bias[ROWS ? 8 : 1][ROWS ? N / 2 : 4];
+    constexpr int NC = N / 2;  // a thread's columns of many rows' scores
+    __shared__ __align__(16) float s_bias[ROWS ? 8 : 1][ROWS ? NC : 4];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kblocks = (int)((a.H + kTcK - 1) / kTcK);
@@ -227,11 +235,16 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
         if (lane == 0) {
             uint32_t it = 0, j = 0;
             bool ok = true;
-            for (int64_t t = t_first; ok && t < t_end; t += t_step, ++j) {
-                const uint32_t b = j & 1u;
-                if (!mbar_wait_bounded(&drained[b], ((j >> 1) & 1u) ^ 1u, &g_lm_logprob_status)) break;
-                mma_fence_after();
+            for (int64_t t = t_first; ok && t < t_end; t += t_step) {
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const uint32_t b = j & 1u;
+                    if (kb % kTcChunk<ROWS> == 0) {
+                        if (!mbar_wait_bounded(&drained[b], ((j >> 1) & 1u) ^ 1u, &g_lm_logprob_status)) {
+                            ok = false;
+                            break;
+                        }
+                        mma_fence_after();
+                    }
                     const uint32_t s = it % STAGES;
                     if (!mbar_wait_bounded(&full[s], (it / STAGES) & 1u, &g_lm_logprob_status)) {
                         ok = false;
@@ -242,10 +255,13 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
                     const uint64_t da = smem_tile(st), db = smem_tile(st + S::A_BYTES);
 #pragma unroll
                     for (int k = 0; k < kTcK / 16; ++k)
-                        mma_bf16(tmem + b * N, da + 2 * k, db + 2 * k, S::IDESC, kb > 0 || k > 0);
+                        mma_bf16(tmem + b * N, da + 2 * k, db + 2 * k, S::IDESC, kb % kTcChunk<ROWS> > 0 || k > 0);
                     mma_commit(&empty[s]);
+                    if (kb % kTcChunk<ROWS> == kTcChunk<ROWS> - 1 || kb == kblocks - 1) {
+                        mma_commit(&done[b]);
+                        ++j;
+                    }
                 }
-                if (ok) mma_commit(&done[b]);
             }
             // the products are finished before tensor memory is freed
             mma_commit(&last);
@@ -255,14 +271,15 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
         const int quarter = warp & 3;  // a warp reads the lanes of its number modulo 4
         const uint32_t lane_at = (uint32_t)quarter << 21;
         const float kcap = a.cap > 0.f ? 2.f * kLog2eH / a.cap : 0.f;
+        const int chunks = (kblocks + kTcChunk<ROWS> - 1) / kTcChunk<ROWS>;
         uint32_t j = 0;
         if constexpr (ROWS) {
             const int half = (warp - 2) >> 2;
             float *bias = s_bias[warp - 2];
-            for (int64_t t = t_first; t < t_end; t += t_step, ++j) {
-                const uint32_t b = j & 1u;
+            bool ok = true;
+            for (int64_t t = t_first; ok && t < t_end; t += t_step) {
                 const int64_t row = (t % row_blocks) * 128 + quarter * 32 + lane;
-                const int64_t v0 = (t / row_blocks) * N + half * (N / 2);
+                const int64_t v0 = (t / row_blocks) * N + half * NC;
                 const bool in = row < a.M;
                 const float c2 = in ? kLog2eH / row_temp(a, row) : 1.f;
                 const int64_t want = in ? __ldg(a.tokens + row) - v0 : -1;
@@ -270,61 +287,84 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
                 if (a.bias) {
                     __syncwarp();  // the last tile's values have been read
 #pragma unroll
-                    for (int i = 0; i < N / 2; i += 32)
+                    for (int i = 0; i < NC; i += 32)
                         bias[i + lane] = v0 + i + lane < a.V ? __ldg(a.bias + v0 + i + lane) : 0.f;
                     __syncwarp();
                 }
-                if (!warp_wait(&done[b], (j >> 1) & 1u)) break;
-                mma_fence_after();
-                const uint32_t at = tmem + lane_at + b * N + half * (N / 2);
+                float z[NC];
+                for (int c = 0; c < chunks; ++c, ++j) {
+                    const uint32_t b = j & 1u;
+                    ok = ok && warp_wait(&done[b], (j >> 1) & 1u);
+                    if (!ok) break;
+                    mma_fence_after();
+                    const uint32_t at = tmem + lane_at + b * N + half * NC;
+#pragma unroll
+                    for (int q = 0; q < NC; q += 16) {
+                        uint32_t r[16];
+                        __syncwarp();
+                        TmemLoad<16>::ld(at + q, r);
+                        tmem_wait_ld();
+                        if (c == 0) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) z[q + i] = __uint_as_float(r[i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2)
+                                split_pair(add2(pair_of(z[q + i], z[q + i + 1]),
+                                                pair_of(__uint_as_float(r[i]), __uint_as_float(r[i + 1]))),
+                                           z[q + i], z[q + i + 1]);
+                        }
+                    }
+                    mma_fence_before();
+                    mbar_arrive(&drained[b]);
+                }
                 float2 st = make_float2(-INFINITY, 0.f);
-                // 32 scores of the row, from column c of the half
-                auto take = [&](const uint32_t (&r)[32], int c) {
+                // 32 scores of the row at a time
+#pragma unroll
+                for (int c = 0; c < NC; c += 32) {
                     const int64_t left = a.V - (v0 + c);
-                    if (left <= 0) return;
+                    if (left <= 0 || !ok) break;
+                    float *x = z + c;
                     uint32_t bits = left < 32 ? (1u << left) - 1u : 0xFFFFFFFFu;
                     if (mrow) bits &= (uint32_t)__ldg(mrow + ((v0 + c) >> 5));
-                    float z[32];
-#pragma unroll
-                    for (int q = 0; q < 32; ++q) z[q] = __uint_as_float(r[q]);
                     if (a.bias) {
 #pragma unroll
                         for (int q = 0; q < 32; q += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(bias + c + q);
-                            split_pair(add2(pair_of(z[q], z[q + 1]), pair_of(f.x, f.y)), z[q], z[q + 1]);
-                            split_pair(add2(pair_of(z[q + 2], z[q + 3]), pair_of(f.z, f.w)), z[q + 2], z[q + 3]);
+                            split_pair(add2(pair_of(x[q], x[q + 1]), pair_of(f.x, f.y)), x[q], x[q + 1]);
+                            split_pair(add2(pair_of(x[q + 2], x[q + 3]), pair_of(f.z, f.w)), x[q + 2], x[q + 3]);
                         }
                     }
                     if (a.cap > 0.f) {
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) z[q] = soft_cap(z[q], a.cap, kcap);
+                        for (int q = 0; q < 32; ++q) x[q] = soft_cap(x[q], a.cap, kcap);
                     }
                     if (bits != 0xFFFFFFFFu) {
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) z[q] = (bits >> q) & 1u ? z[q] : -INFINITY;
+                        for (int q = 0; q < 32; ++q) x[q] = (bits >> q) & 1u ? x[q] : -INFINITY;
                     }
-                    float sum = z[0], top = z[0];  // a sum is NaN if a score is
+                    float sum = x[0], top = x[0];  // a sum is NaN if a score is
 #pragma unroll
-                    for (int q = 1; q < 32; ++q) top = fmaxf(top, z[q]);
-                    unsigned long long all = pair_of(z[0], z[1]);
+                    for (int q = 1; q < 32; ++q) top = fmaxf(top, x[q]);
+                    unsigned long long all = pair_of(x[0], x[1]);
 #pragma unroll
-                    for (int q = 2; q < 32; q += 2) all = add2(all, pair_of(z[q], z[q + 1]));
+                    for (int q = 2; q < 32; q += 2) all = add2(all, pair_of(x[q], x[q + 1]));
                     float s1;
                     split_pair(all, sum, s1);
                     sum += s1;
                     if (sum != sum) {  // a NaN (counts as -inf), or both infinities
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) z[q] = fmaxf(z[q], -INFINITY);
-                        top = z[0];
+                        for (int q = 0; q < 32; ++q) x[q] = fmaxf(x[q], -INFINITY);
+                        top = x[0];
 #pragma unroll
-                        for (int q = 1; q < 32; ++q) top = fmaxf(top, z[q]);
+                        for (int q = 1; q < 32; ++q) top = fmaxf(top, x[q]);
                     }
                     const int64_t w = want - c;
                     if (w >= 0 && w < 32) {
-                        float x = -INFINITY;
+                        float found = -INFINITY;
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) select_if(x, z[q], (int)w, q);
-                        a.tok[row] = x;
+                        for (int q = 0; q < 32; ++q) select_if(found, x[q], (int)w, q);
+                        a.tok[row] = found;
                     }
                     if (top > -INFINITY) {
                         if (top > st.x) st = join(st, make_float2(top, 0.f), c2);
@@ -333,30 +373,14 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
 #pragma unroll
                         for (int q = 0; q < 32; q += 2) {
                             float e0, e1;
-                            split_pair(mul2(add2(pair_of(z[q], z[q + 1]), neg), cc), e0, e1);
+                            split_pair(mul2(add2(pair_of(x[q], x[q + 1]), neg), cc), e0, e1);
                             acc = add2(acc, pair_of(ex2_approx(e0), ex2_approx(e1)));
                         }
                         float s0;
                         split_pair(acc, s0, s1);
                         st.y = s0 + s1;
                     }
-                };
-                uint32_t ra[32], rb[32];
-                __syncwarp();
-                TmemLoad<32>::ld(at, ra);
-#pragma unroll 1
-                for (int c = 0; c < N / 2; c += 64) {
-                    __syncwarp();
-                    tmem_wait_ld();
-                    TmemLoad<32>::ld(at + c + 32, rb);
-                    take(ra, c);
-                    __syncwarp();
-                    tmem_wait_ld();
-                    if (c + 64 < N / 2) TmemLoad<32>::ld(at + c + 64, ra);
-                    take(rb, c + 32);
                 }
-                mma_fence_before();
-                mbar_arrive(&drained[b]);
                 if (in && v0 < a.V) a.part[((t / row_blocks) * 2 + half) * a.M + row] = st;
             }
         } else {
@@ -364,24 +388,30 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
 #pragma unroll
             for (int q = 0; q < N; ++q) st[q] = make_float2(-INFINITY, 0.f);
             bool ok = true;
-            for (int64_t t = t_first; t < t_end; t += t_step, ++j) {
-                const uint32_t b = j & 1u;
+            for (int64_t t = t_first; ok && t < t_end; t += t_step) {
                 const int64_t w0 = v_first + t * 128 + quarter * 32, v = w0 + lane;
                 const float bias = a.bias && v < v_end ? __ldg(a.bias + v) : 0.f;
-                if (!warp_wait(&done[b], (j >> 1) & 1u)) {
-                    ok = false;
-                    break;
+                float z[N];
+                for (int c = 0; c < chunks; ++c, ++j) {
+                    const uint32_t b = j & 1u;
+                    ok = warp_wait(&done[b], (j >> 1) & 1u);
+                    if (!ok) break;
+                    mma_fence_after();
+                    uint32_t r[N];
+                    __syncwarp();
+                    TmemLoad<N>::ld(tmem + lane_at + b * N, r);
+                    tmem_wait_ld();
+                    mma_fence_before();
+                    mbar_arrive(&drained[b]);
+#pragma unroll
+                    for (int q = 0; q < N; ++q)
+                        z[q] = c == 0 ? __uint_as_float(r[q]) : z[q] + __uint_as_float(r[q]);
                 }
-                mma_fence_after();
-                uint32_t r[N];
-                TmemLoad<N>::ld(tmem + lane_at + b * N, r);
-                tmem_wait_ld();
-                mma_fence_before();
-                mbar_arrive(&drained[b]);
+                if (!ok) break;
 #pragma unroll
                 for (int q = 0; q < N; ++q) {
                     if (q >= a.M) break;
-                    float x = fmaxf(soft_cap(__uint_as_float(r[q]) + bias, a.cap, kcap), -INFINITY);
+                    float x = fmaxf(soft_cap(z[q] + bias, a.cap, kcap), -INFINITY);
                     if (v >= v_end) x = -INFINITY;  // lanes past the run hold what was there before
                     if (a.mask && w0 < v_end &&
                         !(((uint32_t)__ldg(a.mask + q * a.mstride + (w0 >> 5)) >> lane) & 1u))
