@@ -1,0 +1,182 @@
+"""Host-side argument validation of the training-side calls (no GPU work): the documented status comes back
+before anything is launched, and empty calls launch nothing."""
+import ctypes
+
+import pytest
+import torch
+
+from tests.test_abi import FAKE, S
+
+ODD2, ODD4 = ctypes.c_void_p(0x10002), ctypes.c_void_p(0x10004)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from top_sampling_apply_gb300 import _build
+
+    _build.build()
+    import top_sampling_apply_gb300 as tsa
+
+    return tsa.load_library()
+
+
+def policy(lib, logits=FAKE, dtype=0, B=2, V=100, stride=100, mask=None, mstride=0, T=None, tok=FAKE, old=FAKE,
+           adv=FAKE, ref=None, w=None, lo=0.2, hi=0.2, kl=0.0, ent=0.0, loss=FAKE, row=FAKE, lp=FAKE, entropy=None,
+           grad=None, gstride=0, ws=None, nws=0):
+    return lib.tsa_policy_loss(logits, dtype, B, V, stride, mask, mstride, T, 1.0, tok, old, adv, ref, w, lo, hi, kl,
+                               ent, loss, row, lp, entropy, grad, gstride, ws, nws, None)
+
+
+def test_policy_loss_validation(lib):
+    for kw in ({"logits": None}, {"tok": None}, {"old": None}, {"adv": None}, {"loss": None}, {"row": None},
+               {"lp": None}):
+        assert policy(lib, **kw) == S["TSA_ERR_NULL"], kw
+    for kw in ({"V": 0}, {"B": -1}, {"stride": 99}, {"grad": ctypes.c_void_p(0x20000), "gstride": 99},
+               {"grad": FAKE, "gstride": 101}, {"V": lib.tsa_max_vocab(0) + 1, "stride": 10**7}):
+        assert policy(lib, **kw) == S["TSA_ERR_SHAPE"], kw
+    for kw in ({"lo": -0.1}, {"hi": -1.0}, {"lo": float("nan")}, {"hi": float("inf")}, {"kl": float("nan")},
+               {"ent": float("inf")}):
+        assert policy(lib, **kw) == S["TSA_ERR_VALUE"], kw
+    assert policy(lib, dtype=3) == S["TSA_ERR_DTYPE"]
+    assert policy(lib, mask=FAKE, mstride=3) == S["TSA_ERR_STRIDE"]
+    for kw in ({"logits": ODD2}, {"tok": ODD4}, {"old": ODD2}, {"adv": ODD2}, {"ref": ODD2}, {"w": ODD2}, {"T": ODD2},
+               {"loss": ODD2}, {"row": ODD2}, {"lp": ODD2}, {"entropy": ODD2}, {"grad": ODD2, "gstride": 100},
+               {"mask": ODD2, "mstride": 4}):
+        assert policy(lib, **kw) == S["TSA_ERR_ALIGN"], kw
+    assert policy(lib, B=0, tok=None, old=None, adv=None, loss=None, row=None, lp=None) == S["TSA_OK"]
+
+
+def test_policy_loss_workspace(lib):
+    # rows of up to 512 KB are held on chip; longer ones keep 16 bytes a row between two passes
+    for dt, most in ((0, 131072), (1, 262144), (2, 262144)):
+        assert lib.tsa_policy_loss_workspace_bytes(7, most, dt) == 0
+        assert lib.tsa_policy_loss_workspace_bytes(7, most + 64, dt) == 256
+        assert lib.tsa_policy_loss_workspace_bytes(100, most + 64, dt) == 1792
+    assert lib.tsa_policy_loss_workspace_bytes(0, 300000, 2) == 0
+    long = dict(dtype=2, V=300000, stride=300000, grad=ctypes.c_void_p(0x20000), gstride=300000)
+    assert policy(lib, **long) == S["TSA_ERR_WORKSPACE"]
+    assert policy(lib, ws=FAKE, nws=255, **long) == S["TSA_ERR_WORKSPACE"]
+    assert policy(lib, ws=ctypes.c_void_p(0x10010), nws=256, **long) == S["TSA_ERR_ALIGN"]
+
+
+def preference(lib, logits=FAKE, N=4, V=100, stride=100, tok=FAKE, start=FAKE, P=1, w=None, ref=None, beta=0.1,
+               smooth=0.0, margin=0.0, loss=FAKE, pair=FAKE, reward=FAKE, lp=FAKE, grad=None, gstride=0, ws=FAKE,
+               nws=1 << 20, dtype=0):
+    return lib.tsa_preference_loss(logits, dtype, N, V, stride, 1.0, tok, start, P, w, ref, beta, smooth, margin, 0,
+                                   loss, pair, reward, lp, grad, gstride, ws, nws, None)
+
+
+def test_preference_loss_validation(lib):
+    for kw in ({"logits": None}, {"tok": None}, {"start": None}, {"loss": None}, {"pair": None}, {"reward": None},
+               {"lp": None}):
+        assert preference(lib, **kw) == S["TSA_ERR_NULL"], kw
+    for kw in ({"V": 0}, {"N": -1}, {"P": -1}, {"stride": 99}, {"grad": FAKE, "gstride": 50}):
+        assert preference(lib, **kw) == S["TSA_ERR_SHAPE"], kw
+    for kw in ({"beta": float("nan")}, {"smooth": -0.1}, {"smooth": 1.1}, {"smooth": float("nan")},
+               {"margin": float("inf")}):
+        assert preference(lib, **kw) == S["TSA_ERR_VALUE"], kw
+    assert preference(lib, dtype=9) == S["TSA_ERR_DTYPE"]
+    for kw in ({"tok": ODD4}, {"start": ODD4}, {"w": ODD2}, {"ref": ODD2}, {"loss": ODD2}, {"pair": ODD2},
+               {"reward": ODD2}, {"lp": ODD2}, {"ws": ctypes.c_void_p(0x10010)}):
+        assert preference(lib, **kw) == S["TSA_ERR_ALIGN"], kw
+    need = lib.tsa_preference_loss_workspace_bytes(4)
+    assert need == 256 and lib.tsa_preference_loss_workspace_bytes(0) == 0
+    assert preference(lib, ws=None) == S["TSA_ERR_WORKSPACE"]
+    assert preference(lib, nws=need - 1) == S["TSA_ERR_WORKSPACE"]
+    assert preference(lib, N=0, P=0, tok=None, start=None, loss=None, pair=None, reward=None, lp=None,
+                      ws=None) == S["TSA_OK"]
+
+
+def lm(lib, hidden=FAKE, M=2, H=64, hs=64, weight=FAKE, V=1000, wst=64, bias=None, cap=0.0, mask=None, mstride=0,
+       T=None, tok=FAKE, out=FAKE, ws=FAKE, nws=1 << 30):
+    return lib.tsa_lm_head_logprob(hidden, M, H, hs, weight, V, wst, bias, cap, mask, mstride, T, 1.0, tok, out, ws, nws,
+                                   None)
+
+
+def test_lm_head_logprob_validation(lib):
+    for kw in ({"M": -1}, {"H": 4}, {"H": 12}, {"H": 16392, "hs": 16392, "wst": 16392}, {"V": 0}, {"hs": 32},
+               {"wst": 32}):
+        assert lm(lib, **kw) == S["TSA_ERR_SHAPE"], kw
+    for kw in ({"cap": -1.0}, {"cap": float("nan")}, {"cap": float("inf")}):
+        assert lm(lib, **kw) == S["TSA_ERR_VALUE"], kw
+    for kw in ({"hidden": None}, {"weight": None}, {"tok": None}, {"out": None}):
+        assert lm(lib, **kw) == S["TSA_ERR_NULL"], kw
+    assert lm(lib, mask=FAKE, mstride=31) == S["TSA_ERR_STRIDE"]
+    for kw in ({"hidden": ctypes.c_void_p(0x10008)}, {"weight": ctypes.c_void_p(0x10008)}, {"hs": 68}, {"wst": 68},
+               {"bias": ODD2}, {"T": ODD2}, {"tok": ODD4}, {"out": ODD2}, {"ws": ctypes.c_void_p(0x10010)}):
+        assert lm(lib, **kw) == S["TSA_ERR_ALIGN"], kw
+    need = lib.tsa_lm_head_logprob_workspace_bytes(2, 1000)
+    assert need > 0 and lib.tsa_lm_head_logprob_workspace_bytes(0, 1000) == 0
+    # more rows than one pass takes share its workspace
+    assert lib.tsa_lm_head_logprob_workspace_bytes(10**6, 1000) == lib.tsa_lm_head_logprob_workspace_bytes(8192, 1000)
+    assert lm(lib, ws=None) == S["TSA_ERR_WORKSPACE"]
+    assert lm(lib, nws=need - 1) == S["TSA_ERR_WORKSPACE"]
+    assert lm(lib, M=0, hidden=None, weight=None) == S["TSA_OK"]
+
+
+def table(**kw):
+    import top_sampling_apply_gb300 as tsa
+
+    t = (tsa._AdamTensor * 2)()
+    for i in range(2):
+        for f in ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_exp", "exp_avg_sq_exp"):
+            setattr(t[i], f, 0x10000)
+        t[i].n = 10
+    for f, v in kw.items():
+        setattr(t[1], f, v)
+    return t
+
+
+def adam(lib, t=None, count=2, pd=0, gd=0, bits=32, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.0, step=1, scale=None):
+    return lib.tsa_adamw_step(t, count, pd, gd, bits, lr, b1, b2, eps, wd, step, scale, 0, 0, None)
+
+
+def test_adamw_validation(lib):
+    t = table()
+    for kw in ({"pd": 1}, {"pd": 3}, {"gd": 3}, {"gd": -1}):
+        assert adam(lib, t, **kw) == S["TSA_ERR_DTYPE"], kw
+    for kw in ({"bits": 16}, {"step": 0}, {"lr": -1.0}, {"lr": float("nan")}, {"b1": 1.0}, {"b1": -0.1}, {"b2": 1.0},
+               {"b2": float("nan")}, {"eps": -1.0}, {"eps": float("inf")}, {"wd": -1.0}):
+        assert adam(lib, t, **kw) == S["TSA_ERR_VALUE"], kw
+    assert adam(lib, t, count=-1) == S["TSA_ERR_SHAPE"]
+    assert adam(lib, None) == S["TSA_ERR_NULL"]
+    assert adam(lib, table(n=-1)) == S["TSA_ERR_SHAPE"]
+    assert adam(lib, table(n=(1 << 34) + 1)) == S["TSA_ERR_SHAPE"]
+    for f in ("param", "grad", "exp_avg", "exp_avg_sq"):
+        assert adam(lib, table(**{f: None})) == S["TSA_ERR_NULL"], f
+        assert adam(lib, table(**{f: 0x10002})) == S["TSA_ERR_ALIGN"], f
+    for f in ("exp_avg_exp", "exp_avg_sq_exp"):
+        assert adam(lib, table(**{f: None}), bits=8) == S["TSA_ERR_NULL"], f
+    assert adam(lib, t, scale=ODD2) == S["TSA_ERR_ALIGN"]
+    # nothing to do: no launch
+    assert adam(lib, None, count=0) == S["TSA_OK"]
+    empty = table(n=0, param=None, grad=None)
+    empty[0].n = 0
+    assert adam(lib, empty) == S["TSA_OK"]
+
+
+def test_adamw_state_values_validation(lib):
+    out = (ctypes.c_void_p * 2)(0x10000, 0x10000)
+    f = lib.tsa_adamw_state_values
+    assert f(table(), 2, None, out, None) == S["TSA_ERR_NULL"]
+    assert f(table(), 2, out, (ctypes.c_void_p * 2)(0x10000, None), None) == S["TSA_ERR_NULL"]
+    assert f(table(), 2, (ctypes.c_void_p * 2)(0x10001, 0x10000), out, None) == S["TSA_ERR_ALIGN"]
+    assert f(table(exp_avg_exp=None), 2, out, out, None) == S["TSA_ERR_NULL"]
+    assert f(None, 0, None, None, None) == S["TSA_OK"]
+
+
+def test_binding_rejects_host_tensors():
+    import top_sampling_apply_gb300 as tsa
+
+    x, i, v = torch.zeros(2, 10), torch.zeros(2, dtype=torch.int64), torch.zeros(2)
+    with pytest.raises(ValueError):
+        tsa.policy_loss(x, i, v, v)
+    with pytest.raises(ValueError):
+        tsa.preference_loss(x, i, torch.tensor([0, 1, 2]))
+    h = torch.zeros(2, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        tsa.lm_head_logprob(h, h, i)
+    with pytest.raises(ValueError):
+        tsa.adamw_plan([v], [v], [v], [v])
+    with pytest.raises(ValueError):
+        tsa.adamw_state([v], 16)
