@@ -8,6 +8,7 @@ computation runs in the library's CUDA kernels; there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -452,20 +453,26 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: torch.T
     ref = _vec(ref_logprob, B, torch.float32, dev, "ref_logprob")
     wgt = _vec(weight, B, torch.float32, dev, "weight")
     T, Ts = _temperature(temperature, B, dev)
-    mstride = 0 if bitmask is None else _mask_stride(bitmask, B, V, logits.device)
+    device, dt = logits.device, _DT[logits.dtype]
+    mstride = 0 if bitmask is None else _mask_stride(bitmask, B, V, device)
     g = _grad_rows(grad, logits)
-    loss = torch.empty((), dtype=torch.float32, device=logits.device)
-    rows = torch.empty((3 if return_entropy else 2, B), dtype=torch.float32, device=logits.device).unbind(0)
-    ent = rows[2] if return_entropy else None
-    nws = lib.tsa_policy_loss_workspace_bytes(B, V, _DT[logits.dtype]) if g is not None else 0
-    ws = torch.empty(nws, dtype=torch.uint8, device=logits.device) if nws else None
-    _check(lib.tsa_policy_loss(logits.data_ptr(), _DT[logits.dtype], B, V, stride,
-                               None if bitmask is None else bitmask.data_ptr(), mstride, T, Ts, tok, old, adv, ref,
-                               wgt, clip_low, clip_high, kl_coef, entropy_coef, loss.data_ptr(),
-                               rows[0].data_ptr(), rows[1].data_ptr(), None if ent is None else ent.data_ptr(),
-                               None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
-                               None if ws is None else ws.data_ptr(), nws, _raw_stream(dev)))
-    return PolicyLoss(loss, rows[0], rows[1], ent, g)
+    # an allocation each: on the host that is cheaper than views of one
+    empty, f32 = torch.empty, torch.float32
+    loss, row, lp = empty((), dtype=f32, device=device), empty(B, dtype=f32, device=device), \
+        empty(B, dtype=f32, device=device)
+    ent = empty(B, dtype=f32, device=device) if return_entropy else None
+    nws, ws = 0, None
+    if g is not None and V > 131072:  # shorter rows need none
+        nws = lib.tsa_policy_loss_workspace_bytes(B, V, dt)
+        ws = empty(nws, dtype=torch.uint8, device=device) if nws else None
+    st = lib.tsa_policy_loss(logits.data_ptr(), dt, B, V, stride, None if bitmask is None else bitmask.data_ptr(),
+                             mstride, T, Ts, tok, old, adv, ref, wgt, clip_low, clip_high, kl_coef, entropy_coef,
+                             loss.data_ptr(), row.data_ptr(), lp.data_ptr(), None if ent is None else ent.data_ptr(),
+                             None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
+                             None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
+    if st:
+        _check(st)
+    return PolicyLoss(loss, row, lp, ent, g)
 
 
 class PreferenceLoss(NamedTuple):
@@ -500,16 +507,18 @@ def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, seq_start: torch
     wgt = _vec(weight, N, torch.float32, dev, "weight")
     ref = _vec(ref_logprob, N, torch.float32, dev, "ref_logprob")
     g = _grad_rows(grad, logits)
-    lp = torch.empty(N, dtype=torch.float32, device=logits.device)
-    loss, pair, reward = torch.empty(3 * P + 1, dtype=torch.float32, device=logits.device).split([1, P, 2 * P])
-    loss = loss.view(())
+    device, empty, f32 = logits.device, torch.empty, torch.float32
+    loss, pair, reward, lp = empty((), dtype=f32, device=device), empty(P, dtype=f32, device=device), \
+        empty(2 * P, dtype=f32, device=device), empty(N, dtype=f32, device=device)
     nws = lib.tsa_preference_loss_workspace_bytes(N)
-    ws = torch.empty(nws, dtype=torch.uint8, device=logits.device) if nws else None
-    _check(lib.tsa_preference_loss(logits.data_ptr(), _DT[logits.dtype], N, V, stride, temperature, tok, start, P,
-                                   wgt, ref, beta, label_smoothing, margin, 1 if average else 0, loss.data_ptr(),
-                                   pair.data_ptr(), reward.data_ptr(), lp.data_ptr(),
-                                   None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
-                                   None if ws is None else ws.data_ptr(), nws, _raw_stream(dev)))
+    ws = empty(nws, dtype=torch.uint8, device=device) if nws else None
+    st = lib.tsa_preference_loss(logits.data_ptr(), _DT[logits.dtype], N, V, stride, temperature, tok, start, P, wgt,
+                                 ref, beta, label_smoothing, margin, 1 if average else 0, loss.data_ptr(),
+                                 pair.data_ptr(), reward.data_ptr(), lp.data_ptr(),
+                                 None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
+                                 None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
+    if st:
+        _check(st)
     return PreferenceLoss(loss, pair, reward, lp, g)
 
 
@@ -561,6 +570,7 @@ class AdamWPlan:
         self.exp_avg, self.exp_avg_sq = exp_avg, exp_avg_sq
         self.exp_avg_exp, self.exp_avg_sq_exp = exp_avg_exp, exp_avg_sq_exp
         self.bits = bits
+        self.sizes = [p.numel() for p in params]
         self.index = params[0].get_device() if params else torch.cuda.current_device()
         self._dts = (_DT[params[0].dtype], _DT[grads[0].dtype]) if params else (0, 0)
         self._table = (_AdamTensor * max(1, len(params)))()
@@ -644,17 +654,16 @@ def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
     lib = load_library()
     if plan.bits != 8:
         raise ValueError("32-bit states are their own values")
-    outs = []
+    T, sizes, outs, ptrs = torch.Tensor, plan.sizes, [], []
     for given, like in ((exp_avg_out, plan.exp_avg), (exp_avg_sq_out, plan.exp_avg_sq)):
         given = [torch.empty(t.shape, dtype=torch.bfloat16, device=t.device) for t in like] if given is None \
-            else list(given)
-        if len(given) != len(like) or any(g.dtype != torch.bfloat16 or g.device != t.device
-                                          or g.numel() != t.numel() or not g.is_contiguous()
-                                          for g, t in zip(given, like)):
+            else given if isinstance(given, list) else list(given)
+        if list(map(T.numel, given)) != sizes or any(t.dtype is not torch.bfloat16 for t in given) \
+                or any(d != plan.index for d in map(T.get_device, given)) or not all(map(T.is_contiguous, given)):
             raise ValueError("outputs must be contiguous bfloat16 tensors of the states' sizes")
         outs.append(given)
-    ptrs = [(ctypes.c_void_p * max(1, len(o)))(*[t.data_ptr() for t in o]) for o in outs]
-    _check(lib.tsa_adamw_state_values(plan._table, len(plan.params), ptrs[0], ptrs[1],
+        ptrs.append(array.array("Q", list(map(T.data_ptr, given))))
+    _check(lib.tsa_adamw_state_values(plan._table, len(sizes), ptrs[0].buffer_info()[0], ptrs[1].buffer_info()[0],
                                       _raw_stream(plan.index)))
     return outs[0], outs[1]
 
