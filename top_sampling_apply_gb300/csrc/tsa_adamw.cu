@@ -41,7 +41,7 @@ namespace tsa {
 
 namespace {
 
-constexpr int kAdThreads = 256;
+constexpr int kAdThreads = 128;
 constexpr int kAdPer = 8;                          // elements a lane: a warp is one block of 256
 constexpr int kAdIter = kAdThreads * kAdPer;       // elements a CTA takes at a time
 constexpr int kAdFew = 48, kAdMany = 512;          // tensors in a launch's parameters
@@ -161,9 +161,10 @@ __device__ __forceinline__ uint32_t block_base(const uint32_t (&mag)[8], uint32_
 // ------------------------------------------------------------ 8-bit codes
 // Two ways to read and write codes.  The general one handles code 0, values
 // under a block's range and non-finite ones, element by element in integers:
-// with them alone a step takes 106 instructions an element, 70 of them on the
-// half-rate integer pipe, and that bounded it (48 million bf16 parameters: 197
-// us).  With the others it takes 57, and 108 us.
+// with them alone a step took 106 instructions an element, 70 of them on the
+// half-rate integer pipe, and that bounded it (256 million bf16 parameters:
+// 1,040 us).  With the others it takes 57, and 560 us, 4.6 TB/s: the issue slots
+// still bound it, ten of the 57 being the random words.
 // The other one is for a warp whose 256 elements need none of that:
 //   - exp_avg's codes from 9 on are the bytes of e4m3, so
 //     the conversion instructions read and round (to nearest, ties to even)
@@ -367,7 +368,7 @@ __device__ __forceinline__ bool encode_fast(const float (&m)[8], const float (&v
 }
 
 template <int PD, int GD, int BITS, int N>
-__global__ void __launch_bounds__(kAdThreads, BITS == 8 ? 4 : 1) adamw_kernel(const __grid_constant__ AdamTable<N> tab,
+__global__ void __launch_bounds__(kAdThreads, BITS == 8 ? 7 : 1) adamw_kernel(const __grid_constant__ AdamTable<N> tab,
                                                            const __grid_constant__ AdamArgs a) {
     const float scale = a.scale ? *a.scale : 1.f;
     if (!(fabsf(scale) < INFINITY)) return;
@@ -435,11 +436,13 @@ __global__ void __launch_bounds__(kAdThreads, BITS == 8 ? 4 : 1) adamw_kernel(co
                 !__any_sync(0xFFFFFFFFu, zero_byte(cv.x) || zero_byte(cv.y))) {
                 decode_v_fast(cv, bv, v);
                 step8<true>(c, g, p, m, v);
+                store_params<PD>(t.param, i, cnt, whole, p, word);  // p and its random bits are done with
                 done = encode_fast(m, v, word, cm, cv, bm, bv);
             } else {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] = decode_v(((q < 4 ? cv.x : cv.y) >> (8 * (q & 3))) & 255u, 8u * bv);
                 step8<false>(c, g, p, m, v);
+                store_params<PD>(t.param, i, cnt, whole, p, word);
             }
             if (!done) {
                 bm = finite_base(m, 14u, cnt);
@@ -447,7 +450,6 @@ __global__ void __launch_bounds__(kAdThreads, BITS == 8 ? 4 : 1) adamw_kernel(co
                 cm = encode_m_any(m, bm, cnt);
                 cv = encode_v_any(v, bv, word, cnt);
             }
-            store_params<PD>(t.param, i, cnt, whole, p, word);
             store_codes(static_cast<uint8_t *>(t.m), i, cnt, whole, cm);
             store_codes(static_cast<uint8_t *>(t.v), i, cnt, whole, cv);
             if (lane == turn) {
@@ -521,12 +523,12 @@ const void *adam_kernel(int pd, int gd, int bits) {
     return nullptr;
 }
 
-// A chunk's length in steps of 2,048 elements: one while that leaves the GPU
+// A chunk's length in steps of 1,024 elements: one while that leaves the GPU
 // few chunks, so that small lists spread over every SM.  Large lists take up
-// to 4 with fp32 states (100 million parameters: 402 us; 8 steps 407, 16
-// 414), which end more evenly, and up to 16 with 8-bit ones (256 million: 811
-// us with the values' call; 8 steps 816, 4 steps 843), where a warp keeps its
-// blocks' exponents over a chunk.
+// to 4 with fp32 states (100 million parameters: 400 us, 7.0 TB/s; 8 steps 406),
+// which end more evenly, and up to 16 with 8-bit ones (256 million with the
+// values' call: 797 us; 32 steps 799), where a warp keeps its blocks' exponents
+// over a chunk.
 int chunk_iters(int64_t total, int most) {
     const int64_t steps = (total + kAdIter - 1) / kAdIter;
     int n = 1;
