@@ -452,7 +452,9 @@ int tsa_adamw_state_values(const tsa_adamw_tensor *tensors, int64_t count, void 
  *                [0, V) or a row with no allowed finite score)
  *   workspace    at least tsa_lm_head_logprob_workspace_bytes(M, V) bytes,
  *                256-byte aligned
- * bf16 products, fp32 sums.  The weight is read once for up to 8192 rows.
+ * bf16 products, fp32 sums (of at most 1024 columns in the tensor cores, which
+ * truncate, and to nearest beyond).  The weight is read once for up to 8192
+ * rows.
  */
 int tsa_lm_head_logprob(const void *hidden, int64_t M, int64_t H, int64_t hidden_row_stride,
                         const void *weight, int64_t V, int64_t weight_row_stride, const float *bias,

@@ -1,6 +1,7 @@
-"""Per-row vocabulary selection on GB300: thin Python binding of libtsa.so.
+"""Per-row vocabulary selection on GB300, and the training step on the rows it
+sampled: thin Python binding of libtsa.so.
 
-The three calls mirror the C ABI in include/tsa.h (logits-processor, "API";
+The calls mirror the C ABI in include/tsa.h (logits-processor, "API";
 lm-head-topk, "API").  This module only marshals arguments: it checks torch
 tensors' device, dtype and contiguity, passes raw pointers and the current
 CUDA stream, and maps status codes to exceptions.  Every step of the
@@ -19,7 +20,8 @@ import torch
 from . import _build
 
 __all__ = ["apply_token_bitmask", "sample", "topk", "policy_loss", "preference_loss", "PolicyLoss",
-           "PreferenceLoss", "lm_head_logprob", "AdamWPlan", "adamw_state", "adamw_plan", "adamw_step", "adamw_state_values", "device_status", "max_vocab", "load_library", "TSAError"]
+           "PreferenceLoss", "lm_head_logprob", "AdamWPlan", "adamw_state", "adamw_plan", "adamw_step",
+           "adamw_state_values", "device_status", "max_vocab", "load_library", "TSAError"]
 
 _DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _lock = threading.Lock()

@@ -134,9 +134,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
 // only the ones it needs.  A thread keeps one (m, Z) a hidden row over all its
 // CTA's tiles; one part a CTA.
 // ROWS = true: the lanes are 128 hidden rows and the columns N vocabulary
-// entries; a thread reduces N / 2 of its row's scores by itself.  Tiles go through the hidden rows
-// first, so that a weight tile is fetched from HBM once and from L2 by the
-// other row blocks.  One part for every N / 2 entries of the vocabulary.
+// entries; a thread reduces N / 2 of its row's scores by itself.  Tiles go
+// through the hidden rows first, so that a weight tile is fetched from HBM once
+// and from L2 by the other row blocks.  One part for every N / 2 entries of the
+// vocabulary.
 constexpr int kTcK = 64;
 // The tensor cores add to their accumulator with truncation: a score of 320
 // steps (H = 5,120) came out 9e-6 of itself too small, and 2,048

@@ -403,6 +403,13 @@ __device__ __forceinline__ RowPlace place_row(const RowLossArgs &r, int64_t row,
     if (rank + 1 == 1u << lg && tid >= 8 && tid - 8 < tail) p.ie = V - tail + (tid - 8);
     return p;
 }
+// By a warp: the mask words of `count` elements from `first` on go to L2, 128
+// bytes a lane.
+__device__ __forceinline__ void prefetch_mask(const RowLossArgs &r, int64_t row, int32_t first, int32_t count) {
+    const int32_t w = (first >> 5) + (int32_t)(threadIdx.x & 31) * 32;
+    if (w <= (first + count - 1) >> 5)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(r.mask + (size_t)row * r.mstride + w));
+}
 // The largest of the warp's values (no NaN among them), on every lane.
 __device__ __forceinline__ float warp_max(float x) {
     float m;
@@ -641,6 +648,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
                                  logits_at(row) + (size_t)(p.first - tid * AE) * E::SIZE + (size_t)s * stage * 16u,
                                  (uint32_t)cnt * 16u, &full[slot]);
                 }
+                if (r.mask) prefetch_mask(r, row, p.first - tid * AE + s * stage * AE, cnt * AE);
                 if (++slot == S) {
                     slot = 0;
                     phase ^= 1u;
@@ -717,18 +725,20 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
             const float c2 = meta[i].c2;
             if (!fixed) p = place_row<DT>(r, row, rank, lg);
             WarpSums sum = {-INFINITY, 0.f, 0.f};
+            uint32_t lo[U], hi[U];
+            auto words = [&](int s) {  // a stage's mask words, under the work on the one before
+                const int32_t *mrow = r.mask + (size_t)row * r.mstride;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    mask_words<AE>(mrow, p.first + (s * stage + u * kRowUsers) * AE,
+                                   u < nu && tid + u * kRowUsers < p.nv - s * stage, lo[u], hi[u]);
+            };
+            if (r.mask) words(0);
 #pragma unroll 1
             for (int s = 0; s < stages; ++s) {
                 const int cnt = p.nv - s * stage;
                 const int32_t e0 = p.first + s * stage * AE;
                 uint4 x[U];
-                uint32_t lo[U], hi[U];
-                if (r.mask) {  // under the wait
-                    const int32_t *mrow = r.mask + (size_t)row * r.mstride;
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        mask_words<AE>(mrow, e0 + u * kRowUsers * AE, u < nu && tid + u * kRowUsers < cnt, lo[u], hi[u]);
-                }
                 ok = ok && mbar_wait_bounded(&full[slot], phase, status);
                 const uint4 *in = ring + slot * kRowStage + tid;
                 if (cnt >= stage) {
@@ -746,6 +756,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
 #pragma unroll
                     for (int u = 0; u < U; ++u)
                         if (u < nu) mask_vec<DT>(x[u], mask_bits<AE>(lo[u], hi[u], e0 + u * kRowUsers * AE));
+                    if (s + 1 < stages) words(s + 1);
                 }
                 float top = largest<DT>(x, nu);
                 __syncwarp();
@@ -800,16 +811,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
 // L2 keeps too little of it.  4,096 x 128,256 bf16 took 434 us so.)
 //
 // Two CTAs share an SM, so that one's exchange passes under the other's
-// arithmetic, and the issue slots decide (13 instructions an element where the
-// first form took 27).  What a row needs once, one warp does for all, another
-// one each row: one starts the next copy, one looks for the row after it, one
-// joins the sums and finishes.  4,096 x 128,256 bf16, an eighth of the rows
-// skipped: 353 us, 5.6 TB/s; with 256 threads of 16 vectors 366 us, with four
-// CTAs of 256 threads an SM, and clusters of 16 for fp32, 347 us.
+// arithmetic: 15 instructions an element, and 58 % of the issue slots are used;
+// waiting at a row's barriers takes the most time beside them.  What a row needs
+// once, one warp does for all, another one each row: one starts the next copy,
+// one looks for the row after it, one joins the sums and finishes.  4,096 x
+// 128,256 bf16, an eighth of the rows skipped: 331 us, 6.0 TB/s.  (Before a
+// row's token score and arguments were fetched rows ahead it was 353 us; 366 us
+// then with 256 threads of 16 vectors, and 347 us with four CTAs of 256 threads
+// an SM, which needs clusters of 16 for fp32.)
 //
 // Rows of up to 16 or 32 KB take CTAs of 128 or 256 threads instead, so that an
 // SM has eight or four of them under way: the exchange of a row takes as long
-// as a short row's arithmetic (10,000 x 8,192 bf16: 164 us with 512 threads).
+// as a short row's arithmetic (10,000 x 8,192 bf16: 164 us with 512 threads, 66 us
+// with 128).
 constexpr int kHeldVecs = 8, kHeldThreads = 512;
 constexpr int kHeldCluster = 8;
 constexpr size_t held_smem(int threads) { return (size_t)threads * kHeldVecs * 16; }
@@ -828,6 +842,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLo
     __shared__ RowMeta meta[4];
     __shared__ float4 finished;                                  // k1, k2, a and m
     __shared__ uint64_t full, empty, joined[2];
+    constexpr int MW = AE + 1;                                   // words that 32 vectors' bits lie in
+    __shared__ uint32_t words[WARPS][U * MW + 1];                // each warp's own mask words of a row; the
+                                                                 // last one is read with its bits unused
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t C = 1u << lg, rank = C > 1 ? cluster_ctarank() : 0u;
     const int64_t step = gridDim.x >> lg;
@@ -840,6 +857,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLo
         mbar_arrive_expect_tx(&full, (uint32_t)q.nv * 16u);
         if (q.nv > 0)
             bulk_g2s(ring, logits_at(b) + (size_t)(q.first - tid * AE) * E::SIZE, (uint32_t)q.nv * 16u, &full);
+    };
+    auto fetch_mask = [&](int64_t b) {  // by every warp: the mask words of its vectors; 0 beyond the row
+        const RowPlace q = fixed ? p : place_row<DT>(r, b, rank, lg);
+        const int32_t *mrow = r.mask + (size_t)b * r.mstride;
+        const int32_t w0 = (q.first - lane * AE) >> 5;
+        const uint32_t n = (uint32_t)(r.V + 31) >> 5;
+#pragma unroll
+        for (int i = 0; i < U * MW; i += 32) {
+            const int k = i + lane;
+            const uint32_t w = (uint32_t)(w0 + k / MW * (THREADS * AE / 32) + k % MW);
+            if (k < U * MW) cp_async_4(&words[warp][k], mrow + (w < n ? w : 0u), w < n);
+        }
+        cp_async_commit();
     };
     if (tid == 0) {
         mbar_init(&full, 1);
@@ -872,6 +902,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLo
         __syncthreads();
     pdl_launch_dependents();  // the next kernel waits for this one's end before it reads
     bool ok = true;  // a wait that ran out ends all waiting; the status word tells
+    if (r.mask && meta[0].row < r.B) fetch_mask(meta[0].row);
     for (uint32_t turn = 0;; ++turn) {
         const uint32_t half = turn & 1u;
         const RowMeta &mt = meta[turn & 3u];
@@ -896,26 +927,27 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLo
         if (!fixed) p = place_row<DT>(r, row, rank, lg);
         const int nu = (p.nv + THREADS - 1) / THREADS;
         float xe = -INFINITY;
-        if (p.ie >= 0 && (!mrow || allowed_bit(mrow, p.ie))) xe = load_clean(logits_at(row), DT, p.ie);
+        if (p.ie >= 0) {
+            xe = load_clean(logits_at(row), DT, p.ie);
+            if (mrow && !allowed_bit(mrow, p.ie)) xe = -INFINITY;
+        }
         uint4 x[U];
-        {
-            uint32_t lo[U], hi[U];
-            if (mrow) {  // under the wait
+        ok = ok && mbar_wait_bounded(&full, turn & 1u, status);
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    mask_words<AE>(mrow, p.first + u * THREADS * AE, tid + u * THREADS < p.nv, lo[u], hi[u]);
-            }
-            ok = ok && mbar_wait_bounded(&full, turn & 1u, status);
+        for (int u = 0; u < U; ++u) {
+            x[u] = none_vec<DT>();
+            if (u + 1 < nu || tid + u * THREADS < p.nv) x[u] = ring[tid + u * THREADS];
+        }
+        __syncwarp();
+        if (lane == 0) arrive_one(&empty);
+        if (mrow) {
+            cp_async_wait<0>();
+            __syncwarp();
+            // 32 vectors a step are a whole number of words: one place and one shift for all
+            const uint32_t *mw = words[warp] + ((p.first >> 5) - ((p.first - lane * AE) >> 5));
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                x[u] = none_vec<DT>();
-                if (u + 1 < nu || tid + u * THREADS < p.nv) x[u] = ring[tid + u * THREADS];
-            }
-            if (mrow) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (u < nu) mask_vec<DT>(x[u], mask_bits<AE>(lo[u], hi[u], p.first + u * THREADS * AE));
-            }
+            for (int u = 0; u < U; ++u)
+                if (u < nu) mask_vec<DT>(x[u], mask_bits<AE>(mw[u * MW], mw[u * MW + 1], p.first));
         }
         float top = largest<DT>(x, nu);
         if (top != top) {  // NaN counts as -inf
@@ -923,7 +955,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLo
             top = largest<DT>(x, nu);
         }
         top = warp_max(fmaxf(top, xe));
-        if (lane == 0) arrive_one(&empty);
         if (warp == (int)(turn % WARPS) && lane == 0) {  // the next row's copy
             const int64_t next = meta[(turn + 1u) & 3u].row;
             if (next < r.B) {
@@ -975,6 +1006,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLo
             if (lane == 0) meta[(turn + 2u) & 3u] = m2;
         }
         __syncthreads();
+        if (r.mask && meta[(turn + 1u) & 3u].row < r.B) fetch_mask(meta[(turn + 1u) & 3u].row);
         const float4 k = finished;
         const bool live = mt.xt > -INFINITY;
         const Ref ref = make_ref(live ? k.w : 0.f, c2);
