@@ -811,14 +811,21 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
 // L2 keeps too little of it.  4,096 x 128,256 bf16 took 434 us so.)
 //
 // Two CTAs share an SM, so that one's exchange passes under the other's
-// arithmetic: 15 instructions an element, and 58 % of the issue slots are used;
+// arithmetic: 16 instructions an element, and 58 % of the issue slots are used;
 // waiting at a row's barriers takes the most time beside them.  What a row needs
 // once, one warp does for all, another one each row: one starts the next copy,
 // one looks for the row after it, one joins the sums and finishes.  4,096 x
-// 128,256 bf16, an eighth of the rows skipped: 331 us, 6.0 TB/s.  (Before a
+// 128,256 bf16, an eighth of the rows skipped: 323 us, 6.1 TB/s.  (Before a
 // row's token score and arguments were fetched rows ahead it was 353 us; 366 us
 // then with 256 threads of 16 vectors, and 347 us with four CTAs of 256 threads
-// an SM, which needs clusters of 16 for fp32.)
+// an SM, which needs clusters of 16 for fp32; with
+// the arguments of 32 rows looked up at a time instead of one a row, 327 us.)
+//
+// A warp copies the mask words of its own part of the next row into shared
+// memory under the gradient of this one (72 words in 16 bits, each read from
+// memory once): 1,023 x 32,001 f16 with a mask and the entropies 43
+// us, 52 when each vector's words were loaded under the row's wait (39 without
+// a mask).
 //
 // Rows of up to 16 or 32 KB take CTAs of 128 or 256 threads instead, so that an
 // SM has eight or four of them under way: the exchange of a row takes as long
