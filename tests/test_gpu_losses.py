@@ -481,3 +481,24 @@ def test_refusals(tsa):
         tsa.preference_loss(x, tok, torch.tensor([0, 1, 2]))
     with pytest.raises(tsa.TSAError):
         tsa.preference_loss(x, tok, torch.tensor([0, 1, 2], device=DEV), label_smoothing=1.5)
+
+
+@pytest.mark.parametrize("average", [False, True])
+@pytest.mark.parametrize("smooth", [0.0, 0.1])
+@pytest.mark.parametrize("row,inf_in", [(1, 0), (6, 2)])
+def test_preference_infinite_reference(tsa, row, inf_in, smooth, average):
+    # a token that the reference's mask excludes has ref -inf: the log-ratio is +inf, the pair's loss by the formula 0 or
+    # +inf, and the gradient that of a saturated logistic, as a far finite reference has it
+    c = pref_case(np.random.default_rng(30), [0, 3, 5, 9, 11], 2003, torch.float32, True, pad=0.0)
+    far = dict(c, refl=c["refl"].copy())
+    far["refl"][row] = -1e6  # h is 1e5 and more: the logistic of it is 0 or 1 in 64 bits too
+    c["refl"][row] = -np.inf
+    kw = dict(beta=0.5, label_smoothing=smooth, average=average)
+    r, f = call_pref(tsa, c, **kw), call_pref(tsa, far, **kw)
+    check_preference(f, far, 2003, torch.float32, 0.5, smooth, 0.0, average)
+    assert r.reward[inf_in].item() == float("inf")
+    assert r.pair_loss[0].item() == (0.0 if inf_in == 0 and smooth == 0.0 else float("inf"))
+    assert r.loss.item() == (float("inf") if r.pair_loss[0].item() else r.pair_loss[1].item() / 2)
+    others = [s for s in range(4) if s != inf_in]
+    assert torch.equal(r.reward[others], f.reward[others]) and torch.equal(r.pair_loss[1], f.pair_loss[1])
+    assert torch.equal(r.grad, f.grad) and torch.equal(r.logprob, f.logprob)

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(PairArgs a, RowLossA
             Sum2 d = {a.logprob[i], 0.f};
             if (a.ref_logprob) d.add(-a.ref_logprob[i]);
             sum.add_product(w, d.s);
-            sum.add_product(w, d.c);
+            if (fabsf(d.s) < INFINITY) sum.add_product(w, d.c);  // a reference of -inf leaves no error, but NaN
             n.add(w);
         }
         R[s] = block_sum<kPairThreads>(sum, sh);
