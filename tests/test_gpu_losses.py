@@ -502,3 +502,11 @@ def test_preference_infinite_reference(tsa, row, inf_in, smooth, average):
     others = [s for s in range(4) if s != inf_in]
     assert torch.equal(r.reward[others], f.reward[others]) and torch.equal(r.pair_loss[1], f.pair_loss[1])
     assert torch.equal(r.grad, f.grad) and torch.equal(r.logprob, f.logprob)
+
+
+def test_preference_smoothing_of_one(tsa):
+    # label_smoothing 1 leaves the rejected answer's term alone: 0 where that answer is infinitely preferred
+    x, tok = torch.zeros(2, 8, device=DEV), torch.zeros(2, dtype=torch.int64, device=DEV)
+    start = torch.tensor([0, 1, 2], device=DEV)
+    r = tsa.preference_loss(x, tok, start, ref_logprob=f32([0.0, -np.inf]), label_smoothing=1.0)
+    assert r.loss.item() == 0.0 and r.pair_loss[0].item() == 0.0 and torch.all(r.grad == 0)

@@ -86,7 +86,10 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(PairArgs a, RowLossA
     const float plus = h > 0.f ? big : small, minus = h > 0.f ? small : big;  // s(h), s(-h)
     if (threadIdx.x == 0) {
         const float soft_m = l1 + fmaxf(-h, 0.f), soft_p = l1 + fmaxf(h, 0.f);
-        a.pair_loss[p] = h != h ? h : (1.f - a.smooth) * soft_m + (a.smooth != 0.f ? a.smooth * soft_p : 0.f);
+        // a coefficient of 0 leaves its term out, even where that is infinite
+        a.pair_loss[p] = h != h ? h
+                                : (a.smooth != 1.f ? (1.f - a.smooth) * soft_m : 0.f) +
+                                      (a.smooth != 0.f ? a.smooth * soft_p : 0.f);
         a.reward[p] = a.beta * R[0].value();
         a.reward[p + a.P] = a.beta * R[1].value();
     }
