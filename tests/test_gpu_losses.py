@@ -510,3 +510,17 @@ def test_preference_smoothing_of_one(tsa):
     start = torch.tensor([0, 1, 2], device=DEV)
     r = tsa.preference_loss(x, tok, start, ref_logprob=f32([0.0, -np.inf]), label_smoothing=1.0)
     assert r.loss.item() == 0.0 and r.pair_loss[0].item() == 0.0 and torch.all(r.grad == 0)
+
+
+@pytest.mark.parametrize("V", [700, 300001])
+def test_policy_without_a_kl_coefficient_has_no_kl_term(tsa, V):
+    # kl_coef 0 beside a reference that excludes the token, or holds it far more likely than exp can tell
+    c = policy_case(np.random.default_rng(31), 4, V, torch.float32, False, False, 0.0, 0.02)
+    want = call(tsa, c)
+    ref = f32([-np.inf, 1000.0, -0.5, np.inf])
+    for kw in ({}, {"grad": False}):
+        got = call(tsa, c, ref_logprob=ref, kl_coef=0.0, **kw)
+        for name in ("loss", "row_loss", "logprob", "entropy"):
+            assert torch.equal(getattr(got, name), getattr(want, name)) or kw, name
+        assert torch.isfinite(got.loss) and torch.isfinite(got.row_loss).all()
+        assert kw or torch.equal(got.grad, want.grad)

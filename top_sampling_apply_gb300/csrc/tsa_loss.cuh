@@ -238,7 +238,7 @@ __device__ __forceinline__ float policy_row(const RowLossArgs &r, const RowMeta 
         loss = clipped ? -s2 : -s1;
         d = clipped ? 0.f : -s1;
     }
-    if (r.ref_logprob) {
+    if (r.ref_logprob && r.kl != 0.f) {  // 0 times a term that overflows would be NaN
         const float u = mt.ref - lp;
         const float e1 = expm1f(u);
         loss += r.kl * (e1 - u);
