@@ -445,6 +445,7 @@ int tsa_adamw_state_values(const tsa_adamw_tensor *tensors, int64_t count, void 
  *                16384; both row strides multiples of 8 elements and both
  *                bases 16-byte aligned (TSA_ERR_ALIGN)
  *   bias         float [V] or NULL; softcap >= 0, finite (0: none)
+ *                (a capped score is within 2^-21 of itself, whatever the cap)
  *   bitmask, mask_row_stride, temperature, temperature_s: as for
  *                selective_log_softmax, one row for each hidden row
  *   tokens       [M] int64; out [M] float, with selective_log_softmax's special

@@ -168,3 +168,39 @@ def test_refusals(tsa):
     with pytest.raises(tsa.TSAError):  # a base off the 16-byte grid
         tsa.lm_head_logprob(torch.zeros(40, dtype=torch.bfloat16, device=DEV)[1:33].view(2, 16), w, tok)
     assert tsa.lm_head_logprob(h[:0], w, tok[:0]).shape == (0,)
+
+
+@pytest.mark.parametrize("cap", [1e-3, 0.5, 8.0, 30.0, 1e3, 1e5, 1e7, 3e38])
+@pytest.mark.parametrize("M", [3, 20, 90, 260])
+@pytest.mark.parametrize("size", [0.02, 6.0])
+def test_soft_caps_of_every_size(tsa, M, cap, size):
+    # One column of hidden values 1 and -1: the scores are the weights themselves, without an error of their own.  A
+    # capped score is off by 2^-21 of itself (not of the cap), a log-probability by at most twice that, and by the sums'
+    # rounding as above.
+    g = torch.Generator(device=DEV).manual_seed(M)
+    V = 2500
+    h, w = torch.zeros(M, 8, device=DEV), torch.zeros(V, 8, device=DEV)
+    h[:, 3] = torch.where(torch.arange(M, device=DEV) % 2 == 0, 1.0, -1.0)
+    w[:, 3] = torch.randn(V, generator=g, device=DEV) * size
+    h, w = h.bfloat16(), w.bfloat16()
+    tok = torch.randint(0, V, (M,), generator=g, device=DEV)
+    got = tsa.lm_head_logprob(h, w, tok, softcap=cap).double()
+    z = h.double() @ w.double().T
+    z = cap * torch.tanh(z / cap)
+    want = z.gather(1, tok[:, None])[:, 0] - torch.logsumexp(z, 1)
+    tol = 2 * 2.0 ** -21 * z.abs().amax(1) + (4 + 60 + V / 128 + 64) * U + 3 * U * want.abs()
+    assert torch.all((got - want).abs() <= tol), (got - want).abs().max().item()
+
+
+def test_soft_cap_of_infinite_scores(tsa):
+    # an infinite score is the cap itself; a NaN counts as -inf
+    w = torch.zeros(40, 8, device=DEV).bfloat16()
+    tok = torch.tensor([0, 1, 2, 5], device=DEV)
+    b = torch.zeros(40, device=DEV)
+    b[0], b[1], b[2], b[3] = float("inf"), float("-inf"), 2.0, float("nan")
+    for M in (4, 40):
+        h = torch.zeros(M, 8, device=DEV).bfloat16()
+        got = tsa.lm_head_logprob(h, w, tok.repeat(M // 4), bias=b, softcap=4.0).double().cpu().numpy()[:4]
+        y = 4.0 * np.tanh(np.array([np.inf, -np.inf, 2.0 / 4.0] + [0.0] * 36))
+        want = y[[0, 1, 2, 4]] - np.log(np.exp(y).sum())
+        assert np.all(np.abs(got - want) <= 2 * 2.0 ** -21 * 4 + 133 * U), (got, want)
