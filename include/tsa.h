@@ -380,7 +380,8 @@ size_t tsa_preference_loss_workspace_bytes(int64_t N);
  *   v' = beta2 v + (1 - beta2) g^2
  *   p' = p (1 - lr weight_decay)
  *        - lr / (1 - beta1^step) m' / (sqrt(v' / (1 - beta2^step)) + eps)
- * computed in fp32 from the unrounded m' and v'.
+ * computed in fp32 from the unrounded m' and v', denormal ones included; m' = v'
+ * = 0 with eps = 0 is an update of 0.
  *   tensors      HOST array of `count` descriptions, read during the call; its
  *                pointers are device pointers to contiguous elements, aligned
  *                to their element size (16-byte aligned ones take the fastest

@@ -258,3 +258,29 @@ def test_refusals(tsa):
     with pytest.raises(ValueError):
         tsa.adamw_state_values(plan)
     tsa.adamw_step(tsa.adamw_plan([], [], [], []), 1, 0.1)  # an empty list is a no-op
+
+
+@pytest.mark.parametrize("pdt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("eps", [0.0, 1e-25])
+def test_second_moments_below_the_normal_numbers(tsa, pdt, eps):
+    # gradients of 1e-20 to 1e-17: v' is 1e-43 to 1e-37, and with no eps to speak of the step still has the size of lr.
+    # v' is a square, a product and a sum with an absolute error of 2^-150 each beside their relative ones, and its
+    # root has half its relative error.
+    rng = np.random.default_rng(6)
+    n = 3001
+    p = torch.from_numpy((0.1 * rng.standard_normal(n)).astype(np.float32)).to(DEV).to(pdt)
+    g = torch.from_numpy((10.0 ** rng.uniform(-20, -17, n) * rng.choice([-1, 1], n)).astype(np.float32)).to(DEV)
+    m, v, _, _ = tsa.adamw_state([p], 32)
+    old = arr(p)
+    pe, me, ve = adamw.step(old, arr(g), np.zeros(n), np.zeros(n), 1, 1e-2, 0.9, 0.999, eps, 0.0)
+    tsa.adamw_step(tsa.adamw_plan([p], [g], m, v), 1, 1e-2, eps=eps, weight_decay=0.0, seed=8, offset=1)
+    upd = np.abs(pe - old)
+    assert upd.min() > 5e-3
+    tv = 6 * U * ve + 3 * 2.0 ** -150
+    assert np.all(np.abs(arr(v[0]) - ve) <= tv)
+    tp = upd * (2.0 ** -20 + 4 * U + tv / ve) + 3 * U * np.abs(pe)
+    if pdt == torch.float32:
+        assert np.all(np.abs(arr(p) - pe) <= tp)
+    else:
+        word = adamw.words(8, 1, 0, n)
+        assert np.all((arr(p) >= adamw.bf16_by_word(pe - tp, word)) & (arr(p) <= adamw.bf16_by_word(pe + tp, word)))

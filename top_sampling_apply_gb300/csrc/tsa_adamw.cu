@@ -270,8 +270,7 @@ __device__ __forceinline__ uint32_t finite_base(const float (&x)[8], uint32_t sp
 struct AdamPairs {
     unsigned long long scale, b1, b1c, b2, b2c, rsc2, eps, rate, keep;
 };
-// m, v, p of eight elements by one step.  PLAIN: v' is normal, so its root
-// needs no lower bound.
+// m, v, p of eight elements by one step.  PLAIN: v' is a normal number.
 template <bool PLAIN>
 __device__ __forceinline__ void step8(const AdamPairs &a, const float (&g)[8], float (&p)[8], float (&m)[8],
                                       float (&v)[8]) {
@@ -289,12 +288,19 @@ __device__ __forceinline__ void step8(const AdamPairs &a, const float (&g)[8], f
         v[q] = __fadd_rn(m0, n0);
         v[q + 1] = __fadd_rn(m1, n1);
         const unsigned long long mm = pair_of(m[q], m[q + 1]);
-        // The root of v' (2^-126 at least: a smaller one's root is below
-        // 2^-63 either way) and the reciprocal, each within 2^-22: the
-        // update, some thousandths of p, is within 2^-20 of itself.
+        // The root of v' and the reciprocal, each within 2^-22: the update, some
+        // thousandths of p, is within 2^-20 of itself.  v' may lie below the
+        // normal numbers (the square of a gradient of 1e-19), where it still
+        // decides the step if eps does not; a v' of 0 counts as the least number
+        // above it, so that 0 / 0 is 0.
         float r0, r1, d0, d1;
-        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(PLAIN ? v[q] : fmaxf(v[q], 0x1p-126f)));
-        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(PLAIN ? v[q + 1] : fmaxf(v[q + 1], 0x1p-126f)));
+        if (PLAIN) {
+            asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(v[q]));
+            asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(v[q + 1]));
+        } else {
+            asm("sqrt.approx.f32 %0, %1;" : "=f"(r0) : "f"(fmaxf(v[q], 0x1p-149f)));
+            asm("sqrt.approx.f32 %0, %1;" : "=f"(r1) : "f"(fmaxf(v[q + 1], 0x1p-149f)));
+        }
         split_pair(fma2(pair_of(r0, r1), a.rsc2, a.eps), d0, d1);
         asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d0));
         asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d1));
