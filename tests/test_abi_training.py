@@ -180,3 +180,112 @@ def test_binding_rejects_host_tensors():
         tsa.adamw_plan([v], [v], [v], [v])
     with pytest.raises(ValueError):
         tsa.adamw_state([v], 16)
+
+
+class OnDevice1:
+    """What the binding asks of a tensor, for one on cuda:1."""
+    is_cuda, device, requires_grad = True, torch.device("cuda", 1), False
+
+    def __init__(self, *shape, dtype=torch.float32, **kw):
+        shape = shape[0] if shape and isinstance(shape[0], tuple) else shape
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def dim(self):
+        return len(self.shape)
+
+    def size(self, i):
+        return self.shape[i]
+
+    def numel(self):
+        return self.shape.numel()
+
+    def stride(self, i):
+        return self.shape[i + 1:].numel()
+
+    def get_device(self):
+        return 1
+
+    def is_contiguous(self):
+        return True
+
+    def is_inference(self):
+        return True
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return 0x10000
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    # a launch goes to the current device: each call makes its tensors' device current, and leaves things as they were
+    import top_sampling_apply_gb300 as tsa
+
+    current, ran = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *a):
+            current[0] = self.before
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_bytes"):
+                return lambda *a: 0
+            return lambda *a: ran.append((name, current[0])) or 0
+
+    monkeypatch.setattr(tsa, "_lib", Lib())
+    monkeypatch.setattr(tsa, "_current_device", lambda: current[0])
+    monkeypatch.setattr(tsa, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(tsa, "_stream", lambda t: 0)
+    monkeypatch.setattr(tsa.torch.cuda, "device", Device)
+    monkeypatch.setattr(tsa.torch, "empty", OnDevice1)
+    f, i, h = OnDevice1(2), OnDevice1(2, dtype=torch.int64), OnDevice1(2, 16, dtype=torch.bfloat16)
+    x, bits = OnDevice1(2, 32), OnDevice1(2, 1, dtype=torch.int32)
+    tsa.policy_loss(x, i, f, f)
+    tsa.preference_loss(x, i, OnDevice1(3, dtype=torch.int64))
+    tsa.lm_head_logprob(h, h, i)
+    tsa.adamw_step(tsa.adamw_plan([f], [f], [f], [f]), 1, 0.1)
+    tsa.sample(x)
+    tsa.sample_icdf(x, f)
+    tsa.sample_noalloc(x, i)
+    tsa.topk(x, 2)
+    tsa.selective_log_softmax(x, i)
+    tsa.apply_token_bitmask(x, bits)
+    tsa.lm_head_topk(h, h, 2)
+    tsa.bitmask_from_allowed(OnDevice1(2, 32, dtype=torch.bool))
+    assert [n for n, d in ran if d != 1] == [] and len(ran) == 12 and current == [0]
+    ran.clear()
+    current[0] = 1  # already current
+    monkeypatch.setattr(tsa.torch.cuda, "device", None)
+    tsa.policy_loss(x, i, f, f)
+    assert ran == [("tsa_policy_loss", 1)]
+
+
+def test_an_error_leaves_the_device_as_it_was(monkeypatch):
+    import top_sampling_apply_gb300 as tsa
+
+    left = []
+
+    class Device:
+        def __init__(self, index):
+            pass
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *a):
+            left.append(1)
+
+    tsa.load_library()
+    monkeypatch.setattr(tsa, "_current_device", lambda: 0)
+    monkeypatch.setattr(tsa.torch.cuda, "device", Device)
+    with pytest.raises(tsa.TSAError) as e:
+        tsa._call(1, lambda *a: S["TSA_ERR_SHAPE"], 1, 2)
+    assert left == [1] and e.value.status == S["TSA_ERR_SHAPE"]

@@ -106,6 +106,21 @@ def _check(status: int):
         raise TSAError(status, lib.tsa_status_string(status).decode())
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _call(index: int, fn, *args):
+    """A call of the library for tensors on CUDA device ``index``: a launch goes to the current
+    device, so that one is made current if another is."""
+    if _current_device() == index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args)
+    if status:
+        _check(status)
+
+
 def _stream(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
 
@@ -150,8 +165,8 @@ def apply_token_bitmask(logits: torch.Tensor, bitmask: torch.Tensor) -> torch.Te
         raise ValueError("bitmask must have B rows and unit stride along W")
     if bitmask.shape[1] < (V + 31) // 32:
         raise ValueError("bitmask needs ceil(V / 32) words per row")
-    _check(lib.tsa_apply_token_bitmask(_ptr(logits), _DT[logits.dtype], B, V, stride,
-                                       _ptr(bitmask), bitmask.stride(0), _stream(logits)))
+    _call(logits.get_device(), lib.tsa_apply_token_bitmask, _ptr(logits), _DT[logits.dtype], B, V, stride,
+          _ptr(bitmask), bitmask.stride(0), _stream(logits))
     return logits
 
 
@@ -205,11 +220,9 @@ def sample(logits: torch.Tensor, temperature: Param = 1.0, top_k: Param = 0, top
         nws = int(lib.tsa_sample_workspace_bytes(B, V, _DT[logits.dtype]))
         ws = _workspace(nws, dev) if nws > 0 else None
         call = lib.tsa_sample
-    _check(call(_ptr(logits), _DT[logits.dtype], B, V, stride, _ptr(bitmask), mstride,
-                          _ptr(T), float(Ts), _ptr(K), int(Ks), _ptr(Pp), float(Ps), _ptr(M),
-                          float(Ms), int(seed) & 0xFFFFFFFFFFFFFFFF,
-                          int(offset) & 0xFFFFFFFFFFFFFFFF, _ptr(tokens), _ptr(vstar), _ptr(ws),
-                          nws, _stream(logits)))
+    _call(logits.get_device(), call, _ptr(logits), _DT[logits.dtype], B, V, stride, _ptr(bitmask), mstride, _ptr(T),
+          float(Ts), _ptr(K), int(Ks), _ptr(Pp), float(Ps), _ptr(M), float(Ms), int(seed) & 0xFFFFFFFFFFFFFFFF,
+          int(offset) & 0xFFFFFFFFFFFFFFFF, _ptr(tokens), _ptr(vstar), _ptr(ws), nws, _stream(logits))
     return (tokens, vstar) if return_min_kept else tokens
 
 
@@ -235,10 +248,9 @@ def sample_icdf(logits: torch.Tensor, uniform: torch.Tensor, temperature: Param 
     vstar = torch.empty(B, dtype=torch.float32, device=dev)
     nws = int(lib.tsa_sample_workspace_bytes(B, V, _DT[logits.dtype]))
     ws = _workspace(nws, dev) if nws > 0 else None
-    _check(lib.tsa_sample_icdf(_ptr(logits), _DT[logits.dtype], B, V, stride, _ptr(bitmask), mstride,
-                               _ptr(T), float(Ts), _ptr(K), int(Ks), _ptr(Pp), float(Ps), _ptr(M),
-                               float(Ms), _ptr(uniform), _ptr(tokens), _ptr(vstar), _ptr(ws), nws,
-                               _stream(logits)))
+    _call(logits.get_device(), lib.tsa_sample_icdf, _ptr(logits), _DT[logits.dtype], B, V, stride, _ptr(bitmask),
+          mstride, _ptr(T), float(Ts), _ptr(K), int(Ks), _ptr(Pp), float(Ps), _ptr(M), float(Ms), _ptr(uniform),
+          _ptr(tokens), _ptr(vstar), _ptr(ws), nws, _stream(logits))
     return (tokens, vstar) if return_min_kept else tokens
 
 
@@ -254,8 +266,8 @@ def bitmask_from_allowed(allowed: torch.Tensor, out: Optional[torch.Tensor] = No
     if bits.dtype != torch.int32 or bits.device != allowed.device or bits.shape[0] != B \
             or bits.shape[1] < W or bits.stride(1) != 1:
         raise ValueError("out must be an int32 [B, >= ceil(V / 32)] tensor on the same device")
-    _check(lib.tsa_bitmask_from_allowed(_ptr(allowed), B, V, allowed.stride(0), _ptr(bits),
-                                        bits.stride(0), _stream(allowed)))
+    _call(allowed.get_device(), lib.tsa_bitmask_from_allowed, _ptr(allowed), B, V, allowed.stride(0), _ptr(bits),
+          bits.stride(0), _stream(allowed))
     return bits
 
 
@@ -292,9 +304,8 @@ def selective_log_softmax(logits: torch.Tensor, index: torch.Tensor, temperature
     else:
         mstride = 0
     res = out if out is not None else torch.empty(B, dtype=torch.float32, device=dev)
-    _check(lib.tsa_selective_log_softmax(_ptr(logits), _DT[logits.dtype], B, V, stride, _ptr(bitmask),
-                                         mstride, _ptr(T), float(Ts), _ptr(index), _ptr(res),
-                                         _stream(logits)))
+    _call(logits.get_device(), lib.tsa_selective_log_softmax, _ptr(logits), _DT[logits.dtype], B, V, stride,
+          _ptr(bitmask), mstride, _ptr(T), float(Ts), _ptr(index), _ptr(res), _stream(logits))
     return res
 
 
@@ -328,11 +339,10 @@ def sample_noalloc(logits: torch.Tensor, tokens_out: torch.Tensor, temperature: 
         mstride = bitmask.stride(0)
     else:
         mstride = 0
-    _check(lib.tsa_sample_noalloc(_ptr(logits), _DT[logits.dtype], B, V, stride, _ptr(bitmask),
-                                  mstride, _ptr(T), float(Ts), _ptr(K), int(Ks), _ptr(Pp), float(Ps),
-                                  _ptr(M), float(Ms), int(seed) & 0xFFFFFFFFFFFFFFFF,
-                                  int(offset) & 0xFFFFFFFFFFFFFFFF, _ptr(tokens_out),
-                                  _ptr(min_kept_out), _stream(logits)))
+    _call(logits.get_device(), lib.tsa_sample_noalloc, _ptr(logits), _DT[logits.dtype], B, V, stride, _ptr(bitmask),
+          mstride, _ptr(T), float(Ts), _ptr(K), int(Ks), _ptr(Pp), float(Ps), _ptr(M), float(Ms),
+          int(seed) & 0xFFFFFFFFFFFFFFFF, int(offset) & 0xFFFFFFFFFFFFFFFF, _ptr(tokens_out), _ptr(min_kept_out),
+          _stream(logits))
     return tokens_out
 
 
@@ -363,8 +373,8 @@ def lm_head_topk(hidden: torch.Tensor, weight: torch.Tensor, k: int, bias: Optio
     indices = torch.empty(M, k, dtype=torch.int64, device=dev)
     nws = int(lib.tsa_lm_head_topk_workspace_bytes(M, V, k))
     ws = _workspace(nws, dev) if nws > 0 else None
-    _check(lib.tsa_lm_head_topk(_ptr(hidden), M, H, hidden.stride(0), _ptr(weight), V, weight.stride(0), _ptr(bias),
-                                int(k), _ptr(values), _ptr(indices), _ptr(ws), nws, _stream(hidden)))
+    _call(hidden.get_device(), lib.tsa_lm_head_topk, _ptr(hidden), M, H, hidden.stride(0), _ptr(weight), V,
+          weight.stride(0), _ptr(bias), int(k), _ptr(values), _ptr(indices), _ptr(ws), nws, _stream(hidden))
     return values, indices
 
 
@@ -375,8 +385,8 @@ def topk(logits: torch.Tensor, k: int):
     B, V, stride = _rows(logits)
     values = torch.empty(B, k, dtype=torch.float32, device=logits.device)
     indices = torch.empty(B, k, dtype=torch.int64, device=logits.device)
-    _check(lib.tsa_topk(_ptr(logits), _DT[logits.dtype], B, V, stride, int(k), _ptr(values),
-                        _ptr(indices), None, 0, _stream(logits)))
+    _call(logits.get_device(), lib.tsa_topk, _ptr(logits), _DT[logits.dtype], B, V, stride, int(k), _ptr(values),
+          _ptr(indices), None, 0, _stream(logits))
     return values, indices
 
 
@@ -467,13 +477,11 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: torch.T
     if g is not None and V > 131072:  # shorter rows need none
         nws = lib.tsa_policy_loss_workspace_bytes(B, V, dt)
         ws = empty(nws, dtype=torch.uint8, device=device) if nws else None
-    st = lib.tsa_policy_loss(logits.data_ptr(), dt, B, V, stride, None if bitmask is None else bitmask.data_ptr(),
-                             mstride, T, Ts, tok, old, adv, ref, wgt, clip_low, clip_high, kl_coef, entropy_coef,
-                             loss.data_ptr(), row.data_ptr(), lp.data_ptr(), None if ent is None else ent.data_ptr(),
-                             None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
-                             None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
-    if st:
-        _check(st)
+    _call(dev, lib.tsa_policy_loss, logits.data_ptr(), dt, B, V, stride,
+          None if bitmask is None else bitmask.data_ptr(), mstride, T, Ts, tok, old, adv, ref, wgt, clip_low,
+          clip_high, kl_coef, entropy_coef, loss.data_ptr(), row.data_ptr(), lp.data_ptr(),
+          None if ent is None else ent.data_ptr(), None if g is None else g.data_ptr(),
+          0 if g is None else g.stride(0), None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
     return PolicyLoss(loss, row, lp, ent, g)
 
 
@@ -514,13 +522,10 @@ def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, seq_start: torch
         empty(2 * P, dtype=f32, device=device), empty(N, dtype=f32, device=device)
     nws = lib.tsa_preference_loss_workspace_bytes(N)
     ws = empty(nws, dtype=torch.uint8, device=device) if nws else None
-    st = lib.tsa_preference_loss(logits.data_ptr(), _DT[logits.dtype], N, V, stride, temperature, tok, start, P, wgt,
-                                 ref, beta, label_smoothing, margin, 1 if average else 0, loss.data_ptr(),
-                                 pair.data_ptr(), reward.data_ptr(), lp.data_ptr(),
-                                 None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
-                                 None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
-    if st:
-        _check(st)
+    _call(dev, lib.tsa_preference_loss, logits.data_ptr(), _DT[logits.dtype], N, V, stride, temperature, tok, start,
+          P, wgt, ref, beta, label_smoothing, margin, 1 if average else 0, loss.data_ptr(), pair.data_ptr(),
+          reward.data_ptr(), lp.data_ptr(), None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
+          None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
     return PreferenceLoss(loss, pair, reward, lp, g)
 
 
@@ -549,10 +554,9 @@ def lm_head_logprob(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.Te
     mstride = 0 if bitmask is None else _mask_stride(bitmask, M, V, hidden.device)
     nws = lib.tsa_lm_head_logprob_workspace_bytes(M, V)
     ws = torch.empty(nws, dtype=torch.uint8, device=hidden.device) if nws else None
-    _check(lib.tsa_lm_head_logprob(hidden.data_ptr(), M, H, hidden.stride(0), weight.data_ptr(), V,
-                                   weight.stride(0), b, softcap, None if bitmask is None else bitmask.data_ptr(),
-                                   mstride, T, Ts, tok, to, None if ws is None else ws.data_ptr(), nws,
-                                   _raw_stream(dev)))
+    _call(dev, lib.tsa_lm_head_logprob, hidden.data_ptr(), M, H, hidden.stride(0), weight.data_ptr(), V,
+          weight.stride(0), b, softcap, None if bitmask is None else bitmask.data_ptr(), mstride, T, Ts, tok, to,
+          None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
     return res
 
 
@@ -645,9 +649,9 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
     every step."""
     lib = _lib or load_library()
     scale = _vec(grad_scale, 1, torch.float32, plan.index, "grad_scale")
-    _check(lib.tsa_adamw_step(plan._table, len(plan.params), plan._dts[0], plan._dts[1], plan.bits, lr, beta1, beta2,
-                              eps, weight_decay, step, scale, int(seed) & 0xFFFFFFFFFFFFFFFF,
-                              int(offset) & 0xFFFFFFFFFFFFFFFF, _raw_stream(plan.index)))
+    _call(plan.index, lib.tsa_adamw_step, plan._table, len(plan.params), plan._dts[0], plan._dts[1], plan.bits, lr,
+          beta1, beta2, eps, weight_decay, step, scale, int(seed) & 0xFFFFFFFFFFFFFFFF,
+          int(offset) & 0xFFFFFFFFFFFFFFFF, _raw_stream(plan.index))
 
 
 def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
@@ -665,8 +669,8 @@ def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
             raise ValueError("outputs must be contiguous bfloat16 tensors of the states' sizes")
         outs.append(given)
         ptrs.append(array.array("Q", list(map(T.data_ptr, given))))
-    _check(lib.tsa_adamw_state_values(plan._table, len(sizes), ptrs[0].buffer_info()[0], ptrs[1].buffer_info()[0],
-                                      _raw_stream(plan.index)))
+    _call(plan.index, lib.tsa_adamw_state_values, plan._table, len(sizes), ptrs[0].buffer_info()[0],
+          ptrs[1].buffer_info()[0], _raw_stream(plan.index))
     return outs[0], outs[1]
 
 
