@@ -284,3 +284,25 @@ def test_second_moments_below_the_normal_numbers(tsa, pdt, eps):
     else:
         word = adamw.words(8, 1, 0, n)
         assert np.all((arr(p) >= adamw.bf16_by_word(pe - tp, word)) & (arr(p) <= adamw.bf16_by_word(pe + tp, word)))
+
+
+def test_a_step_is_seen_by_autograd(tsa):
+    p = torch.randn(8, device=DEV, requires_grad=True)
+    flat = torch.randn(12, device=DEV)
+    q, r = flat[:5], flat[5:]
+    x = torch.randn(5, device=DEV, requires_grad=True)
+    y, z = (p * p).sum(), (x * q).sum()  # their backward needs p and q as they were
+    ps = [p, q, r]
+    plan = tsa.adamw_plan(ps, [torch.ones_like(t) for t in ps], *tsa.adamw_state(ps, 8))
+    tsa.adamw_step(plan, 1, 0.1)
+    for loss in (y, z):
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    (p * p).sum().backward()
+    outs = [[torch.empty(t.shape, dtype=torch.bfloat16, device=DEV) for t in ps] for _ in range(2)]
+    versions = [t._version for o in outs for t in o]
+    tsa.adamw_state_values(plan, *outs)
+    assert all(t._version > v for t, v in zip(outs[0] + outs[1], versions))
+    with torch.inference_mode():
+        t = torch.ones(4, device=DEV)
+    tsa.adamw_step(tsa.adamw_plan([t], [torch.ones(4, device=DEV)], *tsa.adamw_state([t], 32)), 1, 0.1)

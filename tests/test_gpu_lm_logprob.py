@@ -204,3 +204,15 @@ def test_soft_cap_of_infinite_scores(tsa):
         y = 4.0 * np.tanh(np.array([np.inf, -np.inf, 2.0 / 4.0] + [0.0] * 36))
         want = y[[0, 1, 2, 4]] - np.log(np.exp(y).sum())
         assert np.all(np.abs(got - want) <= 2 * 2.0 ** -21 * 4 + 133 * U), (got, want)
+
+
+def test_an_output_written_over_is_seen_by_autograd(tsa):
+    c = make(1, 5, 100, 64)
+    out, x = torch.ones(5, device=DEV), torch.ones(5, device=DEV, requires_grad=True)
+    y = (x * out).sum()  # its backward needs out as it was
+    assert tsa.lm_head_logprob(c["h"], c["w"], c["tok"], out=out) is out
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        out = torch.ones(5, device=DEV)
+    tsa.lm_head_logprob(c["h"], c["w"], c["tok"], out=out)

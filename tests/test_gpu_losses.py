@@ -524,3 +524,34 @@ def test_policy_without_a_kl_coefficient_has_no_kl_term(tsa, V):
             assert torch.equal(getattr(got, name), getattr(want, name)) or kw, name
         assert torch.isfinite(got.loss) and torch.isfinite(got.row_loss).all()
         assert kw or torch.equal(got.grad, want.grad)
+
+
+@pytest.mark.parametrize("loss", ["policy", "preference"])
+def test_a_gradient_over_the_logits_is_seen_by_autograd(tsa, loss):
+    tok, v = torch.zeros(2, dtype=torch.int64, device=DEV), torch.ones(2, device=DEV)
+
+    def run(y, grad):
+        if loss == "policy":
+            return tsa.policy_loss(y, tok, -v, v, grad=grad)
+        return tsa.preference_loss(y, tok, torch.tensor([0, 1, 2], device=DEV), grad=grad)
+
+    x = torch.randn(2, 64, device=DEV, requires_grad=True)
+    y = torch.tanh(x)  # its backward needs y as it was
+    r = run(y, y)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward(r.grad)
+    # a product does not need its output: the gradient goes on
+    w = torch.randn(64, 80, device=DEV)
+    y = x @ w
+    want = run(y.detach(), True).grad
+    r = run(y, y)
+    y.backward(r.grad.detach())
+    assert torch.equal(r.grad, want) and torch.allclose(x.grad, want @ w.t(), rtol=1e-4, atol=1e-6)
+    other = torch.empty_like(want)
+    before = other._version
+    run(y.detach(), other)
+    assert other._version > before
+    with torch.inference_mode():
+        z = torch.randn(2, 64, device=DEV)
+        run(z, z)
+    run(z, z)  # an inference tensor has no version

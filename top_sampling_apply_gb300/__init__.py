@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import itertools
 import os
 import threading
 from typing import NamedTuple, Optional, Union
@@ -119,6 +120,12 @@ def _call(index: int, fn, *args):
             status = fn(*args)
     if status:
         _check(status)
+
+
+def _written(tensors) -> None:
+    """Raises the versions of tensors written in place, as torch's own operations do: autograd then
+    refuses a backward pass that needs what they held."""
+    torch.autograd.graph.increment_version(tensors)
 
 
 def _stream(t: torch.Tensor) -> int:
@@ -455,7 +462,8 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: torch.T
     token of -1 skips its row, as a weight of 0 does, and skipped rows' logits are not read.
     ``grad``: True for a new tensor, a tensor to write (``logits`` itself for in place), or
     False for the loss alone.  There is no autograd graph: the gradient is returned, and
-    ``logits.backward(r.grad)`` carries it further."""
+    ``logits.backward(r.grad)`` carries it further (in place only where what made the logits
+    does not need them again: autograd refuses otherwise)."""
     lib = _lib or load_library()
     B, V, stride = _rows(logits)
     dev = logits.get_device()
@@ -482,6 +490,8 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: torch.T
           clip_high, kl_coef, entropy_coef, loss.data_ptr(), row.data_ptr(), lp.data_ptr(),
           None if ent is None else ent.data_ptr(), None if g is None else g.data_ptr(),
           0 if g is None else g.stride(0), None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
+    if g is grad and not g.is_inference():
+        _written(g)
     return PolicyLoss(loss, row, lp, ent, g)
 
 
@@ -526,6 +536,8 @@ def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, seq_start: torch
           P, wgt, ref, beta, label_smoothing, margin, 1 if average else 0, loss.data_ptr(), pair.data_ptr(),
           reward.data_ptr(), lp.data_ptr(), None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
           None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
+    if g is grad and not g.is_inference():
+        _written(g)
     return PreferenceLoss(loss, pair, reward, lp, g)
 
 
@@ -557,6 +569,8 @@ def lm_head_logprob(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.Te
     _call(dev, lib.tsa_lm_head_logprob, hidden.data_ptr(), M, H, hidden.stride(0), weight.data_ptr(), V,
           weight.stride(0), b, softcap, None if bitmask is None else bitmask.data_ptr(), mstride, T, Ts, tok, to,
           None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
+    if out is not None and not out.is_inference():
+        _written(out)
     return res
 
 
@@ -579,6 +593,9 @@ class AdamWPlan:
         self.sizes = [p.numel() for p in params]
         self.index = params[0].get_device() if params else torch.cuda.current_device()
         self._dts = (_DT[params[0].dtype], _DT[grads[0].dtype]) if params else (0, 0)
+        # the tensors whose versions a step raises: views share their base's
+        bases = [p if p._base is None else p._base for p in params if not p.is_inference()]
+        self._versions = list({id(t): t for t in bases}.values())
         self._table = (_AdamTensor * max(1, len(params)))()
         for i, p in enumerate(params):
             t = self._table[i]
@@ -652,6 +669,7 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
     _call(plan.index, lib.tsa_adamw_step, plan._table, len(plan.params), plan._dts[0], plan._dts[1], plan.bits, lr,
           beta1, beta2, eps, weight_decay, step, scale, int(seed) & 0xFFFFFFFFFFFFFFFF,
           int(offset) & 0xFFFFFFFFFFFFFFFF, _raw_stream(plan.index))
+    _written(plan._versions)
 
 
 def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
@@ -671,6 +689,9 @@ def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
         ptrs.append(array.array("Q", list(map(T.data_ptr, given))))
     _call(plan.index, lib.tsa_adamw_state_values, plan._table, len(sizes), ptrs[0].buffer_info()[0],
           ptrs[1].buffer_info()[0], _raw_stream(plan.index))
+    for given, mine in zip((exp_avg_out, exp_avg_sq_out), outs):
+        if given is not None:
+            _written(list(itertools.filterfalse(T.is_inference, mine)))
     return outs[0], outs[1]
 
 
