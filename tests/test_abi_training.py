@@ -289,3 +289,15 @@ def test_an_error_leaves_the_device_as_it_was(monkeypatch):
     with pytest.raises(tsa.TSAError) as e:
         tsa._call(1, lambda *a: S["TSA_ERR_SHAPE"], 1, 2)
     assert left == [1] and e.value.status == S["TSA_ERR_SHAPE"]
+
+
+def test_a_plan_checks_its_tensors_however_it_is_made():
+    import top_sampling_apply_gb300 as tsa
+
+    v = torch.zeros(2)
+    with pytest.raises(ValueError):
+        tsa.AdamWPlan([v], [v], [v], [v])
+    with pytest.raises(ValueError):
+        tsa.AdamWPlan([v], [], [v], [v])
+    with pytest.raises(ValueError):
+        tsa.AdamWPlan([], [], [], [], [v], [v])

@@ -581,11 +581,40 @@ class _AdamTensor(ctypes.Structure):
 
 
 class AdamWPlan:
-    """A list of parameters with their gradients and states, laid out once for
+    """A list of parameters with their gradients and states, checked and laid out once for
     ``adamw_step``.  It holds the tensors; a gradient that becomes another tensor needs a new
     plan (zero gradients in place between steps)."""
 
-    def __init__(self, params, grads, exp_avg, exp_avg_sq, exp_avg_exp, exp_avg_sq_exp, bits):
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, exp_avg_exp=None, exp_avg_sq_exp=None):
+        params, grads, exp_avg, exp_avg_sq = list(params), list(grads), list(exp_avg), list(exp_avg_sq)
+        n = len(params)
+        bits = 8 if exp_avg and exp_avg[0].dtype == torch.uint8 else 32
+        lists = [("params", params), ("grads", grads), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)]
+        if bits == 8:
+            if exp_avg_exp is None or exp_avg_sq_exp is None:
+                raise ValueError("8-bit states need exp_avg_exp and exp_avg_sq_exp")
+            exp_avg_exp, exp_avg_sq_exp = list(exp_avg_exp), list(exp_avg_sq_exp)
+            lists += [("exp_avg_exp", exp_avg_exp), ("exp_avg_sq_exp", exp_avg_sq_exp)]
+        elif exp_avg_exp is not None or exp_avg_sq_exp is not None:
+            raise ValueError("32-bit states have no exponents")
+        for name, seq in lists:
+            if len(seq) != n:
+                raise ValueError("%s must have as many tensors as params" % name)
+        if n:
+            dev = params[0].device
+            dts = {"params": params[0].dtype, "grads": grads[0].dtype}
+            state = torch.uint8 if bits == 8 else torch.float32
+            if not params[0].is_cuda:
+                raise ValueError("params must be CUDA tensors")
+            if dts["params"] not in (torch.float32, torch.bfloat16) or dts["grads"] not in _DT:
+                raise ValueError("params must be float32 or bfloat16, grads float32, float16 or bfloat16")
+            for name, seq in lists:
+                dt = dts.get(name, state)
+                for i, t in enumerate(seq):
+                    want = (params[i].numel() + 255) // 256 if name.endswith("_exp") else params[i].numel()
+                    if t.device != dev or t.dtype != dt or not t.is_contiguous() or t.numel() != want:
+                        raise ValueError("%s[%d] must be a contiguous %s tensor of %d elements on %s"
+                                         % (name, i, dt, want, dev))
         self.params, self.grads = params, grads
         self.exp_avg, self.exp_avg_sq = exp_avg, exp_avg_sq
         self.exp_avg_exp, self.exp_avg_sq_exp = exp_avg_exp, exp_avg_sq_exp
@@ -623,36 +652,7 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, exp_avg_exp=None, exp_avg_sq_
     """Checks and lays out the tensors of ``adamw_step``: contiguous CUDA tensors, parameters
     float32 or bfloat16, gradients float32, float16 or bfloat16, states float32 or uint8 with a
     uint8 exponent a block of 256 (see ``adamw_state``)."""
-    params, grads, exp_avg, exp_avg_sq = list(params), list(grads), list(exp_avg), list(exp_avg_sq)
-    n = len(params)
-    bits = 8 if exp_avg and exp_avg[0].dtype == torch.uint8 else 32
-    lists = [("params", params), ("grads", grads), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)]
-    if bits == 8:
-        if exp_avg_exp is None or exp_avg_sq_exp is None:
-            raise ValueError("8-bit states need exp_avg_exp and exp_avg_sq_exp")
-        exp_avg_exp, exp_avg_sq_exp = list(exp_avg_exp), list(exp_avg_sq_exp)
-        lists += [("exp_avg_exp", exp_avg_exp), ("exp_avg_sq_exp", exp_avg_sq_exp)]
-    elif exp_avg_exp is not None or exp_avg_sq_exp is not None:
-        raise ValueError("32-bit states have no exponents")
-    for name, seq in lists:
-        if len(seq) != n:
-            raise ValueError("%s must have as many tensors as params" % name)
-    if n:
-        dev = params[0].device
-        dts = {"params": params[0].dtype, "grads": grads[0].dtype}
-        state = torch.uint8 if bits == 8 else torch.float32
-        if not params[0].is_cuda:
-            raise ValueError("params must be CUDA tensors")
-        if dts["params"] not in (torch.float32, torch.bfloat16) or dts["grads"] not in _DT:
-            raise ValueError("params must be float32 or bfloat16, grads float32, float16 or bfloat16")
-        for name, seq in lists:
-            dt = dts.get(name, state)
-            for i, t in enumerate(seq):
-                want = (params[i].numel() + 255) // 256 if name.endswith("_exp") else params[i].numel()
-                if t.device != dev or t.dtype != dt or not t.is_contiguous() or t.numel() != want:
-                    raise ValueError("%s[%d] must be a contiguous %s tensor of %d elements on %s"
-                                     % (name, i, dt, want, dev))
-    return AdamWPlan(params, grads, exp_avg, exp_avg_sq, exp_avg_exp, exp_avg_sq_exp, bits)
+    return AdamWPlan(params, grads, exp_avg, exp_avg_sq, exp_avg_exp, exp_avg_sq_exp)
 
 
 def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
