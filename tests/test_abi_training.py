@@ -217,6 +217,9 @@ class OnDevice1:
     def data_ptr(self):
         return 0x10000
 
+    def untyped_storage(self):
+        return self
+
 
 def test_calls_run_on_their_tensors_device(monkeypatch):
     # a launch goes to the current device: each call makes its tensors' device current, and leaves things as they were

@@ -306,3 +306,20 @@ def test_a_step_is_seen_by_autograd(tsa):
     with torch.inference_mode():
         t = torch.ones(4, device=DEV)
     tsa.adamw_step(tsa.adamw_plan([t], [torch.ones(4, device=DEV)], *tsa.adamw_state([t], 32)), 1, 0.1)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_plan_keeps_the_memory_it_writes(tsa, bits):
+    # a parameter that moves to other memory, and states that are dropped: what is allocated next is not the plan's
+    n = 3 << 20
+    p, g = torch.zeros(n, device=DEV), torch.ones(n, device=DEV)
+    st = tsa.adamw_state([p], bits)
+    plan = tsa.adamw_plan([p], [g], *st)
+    where = [p.data_ptr(), st[0][0].data_ptr(), st[1][0].data_ptr()]
+    p.data = torch.full((n,), 2.0, device=DEV)
+    for t in st[0] + st[1]:
+        t.data = torch.empty(0, device=DEV, dtype=t.dtype)
+    new = [torch.full((n,), 7, device=DEV, dtype=dt) for dt in 2 * [torch.float32, st[0][0].dtype, st[1][0].dtype]]
+    assert not {t.data_ptr() for t in new} & set(where)
+    tsa.adamw_step(plan, 1, 0.1)
+    assert all(torch.all(t == 7) for t in new) and torch.all(p == 2.0)

@@ -582,8 +582,9 @@ class _AdamTensor(ctypes.Structure):
 
 class AdamWPlan:
     """A list of parameters with their gradients and states, checked and laid out once for
-    ``adamw_step``.  It holds the tensors; a gradient that becomes another tensor needs a new
-    plan (zero gradients in place between steps)."""
+    ``adamw_step``.  It holds the tensors and the memory they have when it is made: a gradient
+    that becomes another tensor (``zero_grad(set_to_none=True)``), or a parameter whose ``data``
+    is assigned anew, needs a new plan."""
 
     def __init__(self, params, grads, exp_avg, exp_avg_sq, exp_avg_exp=None, exp_avg_sq_exp=None):
         params, grads, exp_avg, exp_avg_sq = list(params), list(grads), list(exp_avg), list(exp_avg_sq)
@@ -625,6 +626,8 @@ class AdamWPlan:
         # the tensors whose versions a step raises: views share their base's
         bases = [p if p._base is None else p._base for p in params if not p.is_inference()]
         self._versions = list({id(t): t for t in bases}.values())
+        # the table's addresses stay the plan's own, whatever becomes of the tensors
+        self._memory = [t.untyped_storage() for _, seq in lists for t in seq]
         self._table = (_AdamTensor * max(1, len(params)))()
         for i, p in enumerate(params):
             t = self._table[i]
