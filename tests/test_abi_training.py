@@ -304,3 +304,36 @@ def test_a_plan_checks_its_tensors_however_it_is_made():
         tsa.AdamWPlan([v], [], [v], [v])
     with pytest.raises(ValueError):
         tsa.AdamWPlan([], [], [], [], [v], [v])
+
+
+def test_what_is_set_on_kernels_is_kept_for_any_number_of_them(tmp_path):
+    # kernels times devices may pass any fixed count: one process on eight GPUs has hundreds
+    import os
+    import subprocess
+
+    src = tmp_path / "table.cpp"
+    src.write_text(r"""
+#include "tsa_prepared.h"
+#include <cstdio>
+int main() {
+    static tsa::PreparedTable t;
+    static char fn[300];
+    tsa::Prepared *at[300][8];
+    for (int i = 0; i < 300; ++i)
+        for (int d = 0; d < 8; ++d) {
+            tsa::Prepared *p = t.find(fn + i, d);
+            if (!p || p->smem != 0 || p->cluster16 != 0) return 1;
+            p->smem = 1000 * i + d;
+            at[i][d] = p;
+        }
+    for (int i = 0; i < 300; ++i)
+        for (int d = 0; d < 8; ++d) {
+            tsa::Prepared *p = t.find(fn + i, d);
+            if (p != at[i][d] || p->fn != fn + i || p->device != d || p->smem != (size_t)(1000 * i + d)) return 2;
+        }
+    return 0;
+}
+""")
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "top_sampling_apply_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", csrc, str(src), "-o", str(tmp_path / "table")], check=True)
+    assert subprocess.run([str(tmp_path / "table")]).returncode == 0

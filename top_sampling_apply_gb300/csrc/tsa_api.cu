@@ -7,6 +7,7 @@
 #include "../../include/tsa.h"
 #include "tsa_device.cuh"
 #include "tsa_host.h"
+#include "tsa_prepared.h"
 
 namespace tsa {
 
@@ -16,15 +17,8 @@ constexpr size_t kPipeSlice = 33280;        // double-buffered slice for 3 CTAs 
 constexpr int kMaxSlices = 64;
 constexpr int kMaxTopk = 2048;
 
-struct Prepared {
-    const void *fn;
-    int device;
-    size_t smem;
-    int cluster16;
-};
 std::mutex g_mu;
-Prepared g_prepared[128];
-int g_nprepared = 0;
+PreparedTable g_prepared;
 
 int esize_of(int dtype) { return dtype == TSA_F32 ? 4 : 2; }
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -77,17 +71,8 @@ int prepare_kernel(const void *fn, size_t smem, int cluster) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
     std::lock_guard<std::mutex> lock(g_mu);
-    Prepared *p = nullptr;
-    for (int i = 0; i < g_nprepared; ++i)
-        if (g_prepared[i].fn == fn && g_prepared[i].device == dev) p = &g_prepared[i];
-    if (!p) {
-        if (g_nprepared == 128) return -1;
-        p = &g_prepared[g_nprepared++];
-        p->fn = fn;
-        p->device = dev;
-        p->smem = 0;
-        p->cluster16 = 0;
-    }
+    Prepared *p = g_prepared.find(fn, dev);
+    if (!p) return -1;
     if (smem > p->smem) {
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
             return -1;
