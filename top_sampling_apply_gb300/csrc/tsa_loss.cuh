@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
         uint32_t found = 0;
         bool fresh = false;
         int64_t base = first_row;
-        uint32_t slot = 0, phase = 1;
+        uint32_t slot = 0, phase = 1, issued = 0;
         for (uint32_t k = 0;; ++k) {
             // the next row that counts: 32 rows looked at together
             while (found == 0 && base < r.B) {
@@ -640,13 +640,14 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
             auto copy = [&](int s) {
                 int cnt = p.nv - s * stage;
                 cnt = cnt < 0 ? 0 : (cnt > stage ? stage : cnt);
-                if (lane == 0) {
-                    ok = ok && mbar_wait_bounded(&empty[slot], phase, status);
+                if (lane == 0) ok = ok && mbar_wait_bounded(&empty[slot], phase, status);
+                if (lane == 0 && ok) {
                     mbar_arrive_expect_tx(&full[slot], (uint32_t)cnt * 16u);
                     if (cnt > 0)
                         bulk_g2s(ring + slot * kRowStage,
                                  logits_at(row) + (size_t)(p.first - tid * AE) * E::SIZE + (size_t)s * stage * 16u,
                                  (uint32_t)cnt * 16u, &full[slot]);
+                    ++issued;
                 }
                 if (r.mask) prefetch_mask(r, row, p.first - tid * AE + s * stage * AE, cnt * AE);
                 if (++slot == S) {
@@ -671,7 +672,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
             __syncwarp();
             if (row >= r.B) break;
             for (int s = 1; s < stages; ++s) copy(s);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;  // the other warps' waits for this row run out too
         }
+        // no copy may land after the CTA is gone, not even after a wait that ran out
+        if (lane == 0)
+            for (uint32_t i = issued < S ? 0u : issued - S; i < issued; ++i)
+                mbar_wait_bounded(&full[i % S], (i / S) & 1u, status);
     } else if (warp == kRowWarps + 1) {
         // ---- finished rows
         for (uint32_t k = 0;; ++k) {
@@ -760,7 +766,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
                 }
                 float top = largest<DT>(x, nu);
                 __syncwarp();
-                if (lane == 0) arrive_one(&empty[slot]);
+                if (lane == 0 && ok) arrive_one(&empty[slot]);  // a stage that has not come is not free
                 if (++slot == S) {
                     slot = 0;
                     phase ^= 1u;
@@ -939,14 +945,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLo
             if (mrow && !allowed_bit(mrow, p.ie)) xe = -INFINITY;
         }
         uint4 x[U];
-        ok = ok && mbar_wait_bounded(&full, turn & 1u, status);
+        if (ok && !mbar_wait_bounded(&full, turn & 1u, status)) {
+            ok = false;
+            mbar_wait_bounded(&full, turn & 1u, status);  // the copy may not land after the CTA is gone
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             x[u] = none_vec<DT>();
             if (u + 1 < nu || tid + u * THREADS < p.nv) x[u] = ring[tid + u * THREADS];
         }
         __syncwarp();
-        if (lane == 0) arrive_one(&empty);
+        if (lane == 0 && ok) arrive_one(&empty);
         if (mrow) {
             cp_async_wait<0>();
             __syncwarp();
@@ -964,11 +973,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLo
         top = warp_max(fmaxf(top, xe));
         if (warp == (int)(turn % WARPS) && lane == 0) {  // the next row's copy
             const int64_t next = meta[(turn + 1u) & 3u].row;
-            if (next < r.B) {
+            if (next < r.B && ok) {
                 mbar_arrive_expect_tx(&joined[half ^ 1u], (uint32_t)(WARPS << lg) * 16u);
-                ok = ok && mbar_wait_bounded(&empty, turn & 1u, status);
-                fence_proxy_async_smem();
-                fetch(next);
+                ok = mbar_wait_bounded(&empty, turn & 1u, status);
+                if (ok) {
+                    fence_proxy_async_smem();
+                    fetch(next);
+                }
             }
         }
         __syncwarp();
