@@ -216,3 +216,31 @@ def test_an_output_written_over_is_seen_by_autograd(tsa):
     with torch.inference_mode():
         out = torch.ones(5, device=DEV)
     tsa.lm_head_logprob(c["h"], c["w"], c["tok"], out=out)
+
+
+@pytest.mark.parametrize("M", [3, 20, 40, 128, 129, 300])
+@pytest.mark.parametrize("H", [1032, 2056, 5120])
+def test_products_of_several_chunks(tsa, M, H):
+    # more columns than one sum in the tensor cores takes, and more tiles than SMs
+    c = make(M + H, M, 20011, H, bias=True, mask=M == 40 or M == 20, rowT=True)
+    got = tsa.lm_head_logprob(c["h"], c["w"], c["tok"], bias=c["b"], softcap=30.0, temperature=c["T"],
+                              bitmask=None if c["allowed"] is None else bits_of(c["allowed"]))
+    check(c, got, 30.0)
+
+
+@pytest.mark.parametrize("M,columns", [(3, 512), (20, 512), (40, 1024), (128, 1024), (300, 1024)])
+def test_long_sums_are_rounded_outside_the_tensor_cores(tsa, M, columns):
+    # Positive products, so that truncation adds up: the score z of token 0 is about 3,000, and the other token's score
+    # is 0, so its log-probability is -z.  The tensor cores lose at most an ulp, 2^-23 of their sum, at each step of 16
+    # columns, and the sum over a chunk's steps is on average half its end; the chunks' sums are rounded to nearest.
+    # (Truncated over all 320 steps z comes out 9e-6 of itself too small.)
+    H = 5120
+    g = torch.Generator(device=DEV).manual_seed(M)
+    h = torch.randn(M, H, generator=g, device=DEV).abs().bfloat16()
+    w = torch.zeros(2, H, device=DEV)
+    w[0] = torch.randn(H, generator=g, device=DEV).abs()
+    w = w.bfloat16()
+    got = tsa.lm_head_logprob(h, w, torch.ones(M, dtype=torch.int64, device=DEV)).double()
+    z = h.double() @ w[0].double()
+    steps = columns // 16
+    assert torch.all((got + z).abs() <= z * ((steps + 1) / 2 * 2.0 ** -23 + H / columns * U + 3 * U))
