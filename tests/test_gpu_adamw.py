@@ -323,3 +323,47 @@ def test_a_plan_keeps_the_memory_it_writes(tsa, bits):
     assert not {t.data_ptr() for t in new} & set(where)
     tsa.adamw_step(plan, 1, 0.1)
     assert all(torch.all(t == 7) for t in new) and torch.all(p == 2.0)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_replays_in_a_graph(tsa, bits):
+    keys = ("p", "g", "m", "v") + (("me", "ve") if bits == 8 else ())
+    a, b, w = (make(np.random.default_rng(8), [3000, 17], torch.bfloat16, torch.bfloat16, bits) for _ in range(3))
+    scale = torch.full((1,), 0.5, device=DEV)
+
+    def step(plan):
+        tsa.adamw_step(plan, 4, grad_scale=scale, seed=11, offset=4, **HP)
+
+    step(plan_of(tsa, w, bits))
+    if bits == 8:
+        tsa.adamw_state_values(plan_of(tsa, w, bits))
+    torch.cuda.synchronize()
+    plan = plan_of(tsa, a, bits)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(plan)
+        vals = tsa.adamw_state_values(plan) if bits == 8 else None
+    eager = plan_of(tsa, b, bits)
+    for k in range(2):
+        for t in a + b:
+            t["g"][1].copy_(torch.arange(t["n"], device=DEV) * (1e-4 * (k + 1)))
+        g.replay()
+        step(eager)
+        for x, y in zip(a, b):
+            for key in keys:
+                assert torch.equal(x[key][1], y[key][1]), key
+        if bits == 8:
+            for x, y in zip(vals, tsa.adamw_state_values(eager)):
+                assert all(torch.equal(p, q) for p, q in zip(x, y))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_several_tables_of_tensors_of_several_chunks(tsa, bits):
+    # 600 tensors are two tables, and three million elements make a chunk 2,048 of them
+    rng = np.random.default_rng(7)
+    ts = make(rng, rng.integers(1, 10001, 600).tolist(), torch.bfloat16, torch.bfloat16, bits)
+    assert sum(t["n"] for t in ts) > 152 * 16 * 1024
+    before = [(arr(x["p"][1]), arr(x["g"][1]), *values(x, bits)) for x in ts]
+    tsa.adamw_step(plan_of(tsa, ts, bits), 3, seed=10, offset=3, **HP)
+    check_step(ts, before, 0, bits, torch.bfloat16, 3, 1.0, 10, 3)
+    check_guards(ts, 0)

@@ -244,3 +244,24 @@ def test_long_sums_are_rounded_outside_the_tensor_cores(tsa, M, columns):
     z = h.double() @ w[0].double()
     steps = columns // 16
     assert torch.all((got + z).abs() <= z * ((steps + 1) / 2 * 2.0 ** -23 + H / columns * U + 3 * U))
+
+
+@pytest.mark.parametrize("M", [2, 70, 300])
+def test_replays_in_a_graph(tsa, M):
+    cases = [make(s, M, 3001, 1096, bias=True) for s in (1, 2)]
+    a = {k: cases[0][k].clone() for k in ("h", "w", "tok", "b")}
+    out = torch.empty(M, device=DEV)
+
+    def run(to=None):
+        return tsa.lm_head_logprob(a["h"], a["w"], a["tok"], bias=a["b"], softcap=20.0, out=to)
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(out)
+    for c in cases[::-1]:
+        for k in a:
+            a[k].copy_(c[k])
+        g.replay()
+        assert torch.equal(out, run())

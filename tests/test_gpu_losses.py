@@ -555,3 +555,56 @@ def test_a_gradient_over_the_logits_is_seen_by_autograd(tsa, loss):
         z = torch.randn(2, 64, device=DEV)
         run(z, z)
     run(z, z)  # an inference tensor has no version
+
+
+@pytest.mark.parametrize("dtype,B,V,grad", [(torch.bfloat16, 40, 9001, True), (torch.float32, 9, 5000, False),
+                                            (torch.float16, 3, 300000, True)])
+def test_policy_replays_in_a_graph(tsa, dtype, B, V, grad):
+    cases = [policy_case(np.random.default_rng(s), B, V, dtype, True, True, 0.1, 0.02) for s in (40, 41)]
+    keys = ("x", "tok", "old", "adv", "refl", "w", "T")
+    put = lambda c, k: (c[k] if torch.is_tensor(c[k]) else torch.from_numpy(np.asarray(c[k]))).to(DEV)  # noqa: E731
+    a = {k: put(cases[0], k) for k in keys}
+    a["mask"] = pack(cases[0]["allowed"])
+
+    def run():
+        return tsa.policy_loss(a["x"], a["tok"], a["old"], a["adv"], ref_logprob=a["refl"], weight=a["w"], kl_coef=0.1,
+                               entropy_coef=0.02, temperature=a["T"], bitmask=a["mask"], return_entropy=True, grad=grad)
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = run()
+    for c in cases[::-1]:
+        for k in keys:
+            a[k].copy_(put(c, k))
+        a["mask"].copy_(pack(c["allowed"]))
+        g.replay()
+        for p, q in zip(r, run()):
+            assert p is q is None or torch.equal(p, q)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_preference_replays_in_a_graph(tsa, in_place):
+    start = [0, 4, 5, 11, 14]
+    cases = [pref_case(np.random.default_rng(s), start, 4001, torch.bfloat16, True) for s in (42, 43)]
+    keys = ("x", "tok", "w", "refl")
+    put = lambda c, k: (c[k] if torch.is_tensor(c[k]) else torch.from_numpy(np.asarray(c[k]))).to(DEV)  # noqa: E731
+    a = {k: put(cases[0], k) for k in keys}
+    st = torch.tensor(start, device=DEV)
+
+    def run(x):
+        return tsa.preference_loss(x, a["tok"], st, weight=a["w"], ref_logprob=a["refl"], grad=x if in_place else True)
+
+    run(a["x"].clone())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = run(a["x"])
+    for c in cases[::-1]:
+        for k in keys:
+            a[k].copy_(put(c, k))
+        want = run(a["x"].clone())
+        g.replay()
+        for p, q in zip(r, want):
+            assert torch.equal(p, q)
