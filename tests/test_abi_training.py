@@ -184,7 +184,7 @@ def test_binding_rejects_host_tensors():
 
 class OnDevice1:
     """What the binding asks of a tensor, for one on cuda:1."""
-    is_cuda, device, requires_grad = True, torch.device("cuda", 1), False
+    is_cuda, device, requires_grad, _base = True, torch.device("cuda", 1), False, None
 
     def __init__(self, *shape, dtype=torch.float32, **kw):
         shape = shape[0] if shape and isinstance(shape[0], tuple) else shape
@@ -206,9 +206,6 @@ class OnDevice1:
         return 1
 
     def is_contiguous(self):
-        return True
-
-    def is_inference(self):
         return True
 
     def element_size(self):
@@ -247,6 +244,7 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
     monkeypatch.setattr(tsa, "_current_device", lambda: current[0])
     monkeypatch.setattr(tsa, "_raw_stream", lambda index: 0)
     monkeypatch.setattr(tsa, "_stream", lambda t: 0)
+    monkeypatch.setattr(tsa, "_written", lambda tensors: None)
     monkeypatch.setattr(tsa.torch.cuda, "device", Device)
     monkeypatch.setattr(tsa.torch, "empty", OnDevice1)
     f, i, h = OnDevice1(2), OnDevice1(2, dtype=torch.int64), OnDevice1(2, 16, dtype=torch.bfloat16)

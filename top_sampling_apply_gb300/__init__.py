@@ -11,7 +11,6 @@ from __future__ import annotations
 
 import array
 import ctypes
-import itertools
 import os
 import threading
 from typing import NamedTuple, Optional, Union
@@ -124,7 +123,7 @@ def _call(index: int, fn, *args):
 
 def _written(tensors) -> None:
     """Raises the versions of tensors written in place, as torch's own operations do: autograd then
-    refuses a backward pass that needs what they held."""
+    refuses a backward pass that needs what they held.  Inference tensors have none."""
     torch.autograd.graph.increment_version(tensors)
 
 
@@ -490,7 +489,7 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: torch.T
           clip_high, kl_coef, entropy_coef, loss.data_ptr(), row.data_ptr(), lp.data_ptr(),
           None if ent is None else ent.data_ptr(), None if g is None else g.data_ptr(),
           0 if g is None else g.stride(0), None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
-    if g is grad and not g.is_inference():
+    if g is grad:
         _written(g)
     return PolicyLoss(loss, row, lp, ent, g)
 
@@ -536,7 +535,7 @@ def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, seq_start: torch
           P, wgt, ref, beta, label_smoothing, margin, 1 if average else 0, loss.data_ptr(), pair.data_ptr(),
           reward.data_ptr(), lp.data_ptr(), None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
           None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
-    if g is grad and not g.is_inference():
+    if g is grad:
         _written(g)
     return PreferenceLoss(loss, pair, reward, lp, g)
 
@@ -569,7 +568,7 @@ def lm_head_logprob(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.Te
     _call(dev, lib.tsa_lm_head_logprob, hidden.data_ptr(), M, H, hidden.stride(0), weight.data_ptr(), V,
           weight.stride(0), b, softcap, None if bitmask is None else bitmask.data_ptr(), mstride, T, Ts, tok, to,
           None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
-    if out is not None and not out.is_inference():
+    if out is not None:
         _written(out)
     return res
 
@@ -624,7 +623,7 @@ class AdamWPlan:
         self.index = params[0].get_device() if params else torch.cuda.current_device()
         self._dts = (_DT[params[0].dtype], _DT[grads[0].dtype]) if params else (0, 0)
         # the tensors whose versions a step raises: views share their base's
-        bases = [p if p._base is None else p._base for p in params if not p.is_inference()]
+        bases = [p if p._base is None else p._base for p in params]
         self._versions = list({id(t): t for t in bases}.values())
         # the table's addresses stay the plan's own, whatever becomes of the tensors
         self._memory = [t.untyped_storage() for _, seq in lists for t in seq]
@@ -694,7 +693,7 @@ def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
           ptrs[1].buffer_info()[0], _raw_stream(plan.index))
     for given, mine in zip((exp_avg_out, exp_avg_sq_out), outs):
         if given is not None:
-            _written(list(itertools.filterfalse(T.is_inference, mine)))
+            _written(mine)
     return outs[0], outs[1]
 
 
