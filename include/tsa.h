@@ -41,7 +41,8 @@ typedef enum { TSA_F32 = 0, TSA_F16 = 1, TSA_BF16 = 2 } tsa_dtype;
 enum {
     TSA_OK = 0,
     TSA_ERR_NULL = -1,           /* a required pointer is NULL */
-    TSA_ERR_SHAPE = -2,          /* B < 0, V < 1, V too large, or row stride < V */
+    TSA_ERR_SHAPE = -2,          /* a size or a row stride is out of its range: B < 0, V < 1, V too large,
+                                    row stride < V, H not a multiple of 8 */
     TSA_ERR_DTYPE = -3,          /* dtype not one of tsa_dtype */
     TSA_ERR_K_RANGE = -4,        /* topk: k < 1, k > 2048 or k > V */
     TSA_ERR_STRIDE = -5,         /* mask_row_stride < ceil(V / 32) */

@@ -51,7 +51,6 @@ def grid(x, exps, signed, rand=None):
     """The value that x is rounded to on its block's grid: by the 16 random bits upwards (unsigned), or to the
     nearest with ties to even (signed); values above 0 stay at or above the first code (unsigned)."""
     x = np.asarray(x, np.float64)
-    b = np.repeat(np.asarray(exps, np.int64), BLOCK)[:len(x)]
     mag = np.abs(x)
     E = np.maximum(exponent(mag), 1)
     ulp = np.ldexp(1.0, (E - 130).astype(np.int32))
@@ -60,7 +59,6 @@ def grid(x, exps, signed, rand=None):
     low = value(np.ones(len(x), np.int64), exps, False)  # code 1
     y = np.where(y < low, 0.0 if signed else low, y)
     top = value(np.full(len(x), 127 if signed else 255, np.int64), exps, False)
-    del b
     return np.where(mag == 0, 0.0, np.sign(x) * np.minimum(y, top))
 
 

@@ -120,7 +120,7 @@ const char *tsa_status_string(int status) {
     switch (status) {
     case TSA_OK: return "ok";
     case TSA_ERR_NULL: return "a required pointer is NULL";
-    case TSA_ERR_SHAPE: return "invalid shape (B < 0, V < 1, V above the maximum, or row stride < V)";
+    case TSA_ERR_SHAPE: return "invalid shape (a size or a row stride is out of its range)";
     case TSA_ERR_DTYPE: return "unsupported dtype";
     case TSA_ERR_K_RANGE: return "k out of range (1 <= k <= min(2048, V))";
     case TSA_ERR_STRIDE: return "mask row stride < ceil(V / 32)";

@@ -151,9 +151,6 @@ __device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int3
         "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 
 __device__ unsigned int g_lm_logprob_status;
 

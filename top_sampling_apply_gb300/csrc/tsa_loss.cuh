@@ -430,9 +430,6 @@ __device__ __forceinline__ void send_stat(float4 *slot, uint64_t *bar, uint32_t 
         "f"(m), "f"(Z), "f"(t), "r"(dsmem_addr(bar, rank))
         : "memory");
 }
-__device__ __forceinline__ void arrive_one(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 constexpr size_t kRowSmem = (size_t)kRowSlots * kRowStage * 16;
 
 // A warp's running sums against its reference m: in the form that m calls for
@@ -667,7 +664,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
                 RowMeta m = mine;
                 m.row = row;
                 meta[k % RING] = m;
-                arrive_one(&known[k % RING]);
+                mbar_arrive(&known[k % RING]);
             }
             __syncwarp();
             if (row >= r.B) break;
@@ -713,7 +710,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
                 }
             }
             __syncwarp();
-            if (lane == 0) arrive_one(&fin[i]);
+            if (lane == 0) mbar_arrive(&fin[i]);
         }
     } else {
         // ---- stages
@@ -766,7 +763,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
                 }
                 float top = largest<DT>(x, nu);
                 __syncwarp();
-                if (lane == 0 && ok) arrive_one(&empty[slot]);  // a stage that has not come is not free
+                if (lane == 0 && ok) mbar_arrive(&empty[slot]);  // a stage that has not come is not free
                 if (++slot == S) {
                     slot = 0;
                     phase ^= 1u;
@@ -797,7 +794,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
                 ok = ok && mbar_wait_bounded(&fin[(k - RING / 2) % RING], ((k - RING / 2) / RING) & 1u, status);
             if (lane == 0) {
                 sums[i][warp] = total;
-                arrive_one(&summed[i]);
+                mbar_arrive(&summed[i]);
             }
         }
     }
@@ -955,7 +952,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLo
             if (u + 1 < nu || tid + u * THREADS < p.nv) x[u] = ring[tid + u * THREADS];
         }
         __syncwarp();
-        if (lane == 0 && ok) arrive_one(&empty);
+        if (lane == 0 && ok) mbar_arrive(&empty);
         if (mrow) {
             cp_async_wait<0>();
             __syncwarp();

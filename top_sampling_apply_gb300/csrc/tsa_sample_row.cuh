@@ -149,9 +149,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 // Two fp32 lanes in one 64-bit register, for the packed f32x2 arithmetic.
 __device__ __forceinline__ unsigned long long f2_pack(float a, float b) {
     unsigned long long r;

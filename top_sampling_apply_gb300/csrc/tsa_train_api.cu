@@ -18,14 +18,12 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The gradient's rows: the logits themselves with their own stride, or rows
 // apart from them.
-int check_grad(const void *logits, const void *grad, int dtype, int64_t B, int64_t V, int64_t stride,
-               int64_t gstride) {
+int check_grad(const void *logits, const void *grad, int dtype, int64_t V, int64_t stride, int64_t gstride) {
     if (!grad) return TSA_OK;
     const size_t es = dtype == TSA_F32 ? 4 : 2;
     if (gstride < V) return TSA_ERR_SHAPE;
     if (!aligned(grad, es)) return TSA_ERR_ALIGN;
     if (grad == logits && gstride != stride) return TSA_ERR_SHAPE;
-    (void)B;
     return TSA_OK;
 }
 
@@ -78,7 +76,7 @@ int tsa_policy_loss(const void *logits, tsa_dtype dtype, int64_t B, int64_t V, i
         !aligned(advantage, 4) || !aligned(ref_logprob, 4) || !aligned(weight, 4) || !aligned(loss_out, 4) ||
         !aligned(row_loss_out, 4) || !aligned(logprob_out, 4) || !aligned(entropy_out, 4))
         return TSA_ERR_ALIGN;
-    st = check_grad(logits, grad_out, dtype, B, V, logits_row_stride, grad_row_stride);
+    st = check_grad(logits, grad_out, dtype, V, logits_row_stride, grad_row_stride);
     if (st != TSA_OK) return st;
     const size_t need = grad_out ? tsa_policy_loss_workspace_bytes(B, V, dtype) : 0;
     if (need > 0) {
@@ -147,7 +145,7 @@ int tsa_preference_loss(const void *logits, tsa_dtype dtype, int64_t N, int64_t 
     if (!aligned(tokens, 8) || !aligned(seq_start, 8) || !aligned(weight, 4) || !aligned(ref_logprob, 4) ||
         !aligned(loss_out, 4) || !aligned(pair_loss_out, 4) || !aligned(reward_out, 4) || !aligned(logprob_out, 4))
         return TSA_ERR_ALIGN;
-    st = check_grad(logits, grad_out, dtype, N, V, logits_row_stride, grad_row_stride);
+    st = check_grad(logits, grad_out, dtype, V, logits_row_stride, grad_row_stride);
     if (st != TSA_OK) return st;
     const size_t need = tsa_preference_loss_workspace_bytes(N);
     if (need > 0) {
