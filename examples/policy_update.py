@@ -32,6 +32,7 @@ def train(steps=60, vocab=4096, rows=2048, width=256, seed=0, device="cuda"):
     context = torch.arange(rows, device=device) % CLASSES
     hidden = features[context]
     temperature, rewards, update = 0.9, [], 0
+    rounding = seed + 1  # another key than the draws'
     for step in range(steps):
         logits = hidden @ head.t()
         tokens = tsa.sample(logits, temperature, top_p=0.99, seed=seed, offset=step)
@@ -45,7 +46,7 @@ def train(steps=60, vocab=4096, rows=2048, width=256, seed=0, device="cuda"):
                                    temperature=temperature, grad=logits)
             torch.mm(loss.grad.t(), hidden, out=grad)
             update += 1
-            tsa.adamw_step(plan, update, 2e-3, weight_decay=0.0, seed=seed, offset=update)
+            tsa.adamw_step(plan, update, 2e-3, weight_decay=0.0, seed=rounding, offset=update)
         rewards.append(reward.mean())
     # preference: of two one-token answers to a context, the rewarded one
     pairs = rows // 2
@@ -60,7 +61,7 @@ def train(steps=60, vocab=4096, rows=2048, width=256, seed=0, device="cuda"):
         loss = tsa.preference_loss(logits, tokens, start, ref_logprob=ref, beta=0.5, grad=logits)
         torch.mm(loss.grad.t(), hidden, out=grad)
         update += 1
-        tsa.adamw_step(plan, update, 2e-3, weight_decay=0.0, seed=seed, offset=update)
+        tsa.adamw_step(plan, update, 2e-3, weight_decay=0.0, seed=rounding, offset=update)
     margin = (loss.reward[:pairs] - loss.reward[pairs:]).mean()
     return rewards[0].item(), rewards[-1].item(), margin.item()
 

@@ -308,7 +308,7 @@ int tsa_selective_log_softmax(const void *logits, tsa_dtype dtype, int64_t B, in
  *                with nothing allowed) skips its row
  *   old_logprob, advantage  [B] float; an advantage of 0 contributes 0 even
  *                where the ratio overflows
- *   ref_logprob  [B] float or NULL: no KL term
+ *   ref_logprob  [B] float or NULL: no KL term (nor with kl_coef 0, whatever it holds)
  *   weight       [B] float or NULL: 1 / B for every row; 0 skips a row
  *   clip_low, clip_high >= 0, kl_coef, entropy_coef: finite (TSA_ERR_VALUE)
  *   loss_out     [1] float (0 for B == 0); row_loss_out, logprob_out [B] float
@@ -320,6 +320,8 @@ int tsa_selective_log_softmax(const void *logits, tsa_dtype dtype, int64_t B, in
  *   workspace    at least tsa_policy_loss_workspace_bytes(B, V, dtype) bytes,
  *                256-byte aligned, or NULL where that is 0 (rows of up to 512
  *                KB) or grad_out is NULL
+ * f16 gradients of less than 2^-25 become 0, as 1/4096 of a probability of 1e-4
+ * does: larger weights carry a loss scale, which adamw_step's grad_scale takes out.
  * A skipped row's logits are not read; its loss, log-probability, entropy and
  * gradient are 0.  A row whose token the mask excludes, or whose mask leaves
  * nothing, also has loss and gradient 0; its logprob_out is -inf, or NaN for
@@ -355,7 +357,9 @@ size_t tsa_policy_loss_workspace_bytes(int64_t B, int64_t V, tsa_dtype dtype);
  *                [0, N]; rows outside every sequence get gradient 0, and
  *                values out of range are brought into it
  *   weight       [N] float or NULL (1): 0 skips a row (prompt or padding)
- *   ref_logprob  [N] float or NULL (reference-free)
+ *   ref_logprob  [N] float or NULL (reference-free); -inf, for a token that the
+ *                reference excludes, gives the infinite R and loss of the formula
+ *                and the gradient of the logistic's end
  *   0 <= label_smoothing <= 1, beta and margin finite (TSA_ERR_VALUE)
  *   loss_out     [1] float; pair_loss_out [P], reward_out [2 P], logprob_out
  *                [N] float
@@ -397,7 +401,8 @@ size_t tsa_preference_loss_workspace_bytes(int64_t N);
  *                inverse loss scale.  If it is not finite, the step changes
  *                nothing.
  *   seed, offset the key of the random words used in rounding; advance offset
- *                every step
+ *                every step.  sample's words come from the same function: give one of
+ *                the two another seed
  * bf16 parameters are rounded stochastically: an update far below half a step
  * of the parameter still moves it in the mean.
  * An 8-bit state holds blocks of 256 elements, each with one exponent b (the

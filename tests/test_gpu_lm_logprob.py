@@ -233,7 +233,7 @@ def test_long_sums_are_rounded_outside_the_tensor_cores(tsa, M, columns):
     # Positive products, so that truncation adds up: the score z of token 0 is about 3,000, and the other token's score
     # is 0, so its log-probability is -z.  The tensor cores lose at most an ulp, 2^-23 of their sum, at each step of 16
     # columns, and the sum over a chunk's steps is on average half its end; the chunks' sums are rounded to nearest.
-    # (Truncated over all 320 steps z comes out 9e-6 of itself too small.)
+    # (Truncated over all 320 steps z comes out 1.8e-5 of itself too small.)
     H = 5120
     g = torch.Generator(device=DEV).manual_seed(M)
     h = torch.randn(M, H, generator=g, device=DEV).abs().bfloat16()

@@ -665,7 +665,7 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
     ``step`` counts from 1 (bias correction).  ``grad_scale``: a float32 [1] tensor that
     multiplies the gradients; a value that is not finite skips the step.  ``seed``, ``offset``
     key the random rounding of bf16 parameters and 8-bit second moments; advance ``offset``
-    every step."""
+    every step, and use another seed than ``sample``'s, whose words come from the same function."""
     lib = _lib or load_library()
     scale = _vec(grad_scale, 1, torch.float32, plan.index, "grad_scale")
     _call(plan.index, lib.tsa_adamw_step, plan._table, len(plan.params), plan._dts[0], plan._dts[1], plan.bits, lr,

@@ -164,7 +164,9 @@ __device__ __forceinline__ uint32_t block_base(const uint32_t (&mag)[8], uint32_
 // with them alone a step took 106 instructions an element, 70 of them on the
 // half-rate integer pipe, and that bounded it (256 million bf16 parameters:
 // 1,040 us).  With the others it takes 57, and 560 us, 4.6 TB/s: the issue slots
-// still bound it, ten of the 57 being the random words.
+// still bound it, ten of the 57 being the random words.  Seven CTAs an SM leave 72
+// registers a thread, and 16 to 72 bytes of them are spilled (the most with 16-bit
+// parameters and gradients).
 // The other one is for a warp whose 256 elements need none of that:
 //   - exp_avg's codes from 9 on are the bytes of e4m3, so
 //     the conversion instructions read and round (to nearest, ties to even)
@@ -531,10 +533,10 @@ const void *adam_kernel(int pd, int gd, int bits) {
 
 // A chunk's length in steps of 1,024 elements: one while that leaves the GPU
 // few chunks, so that small lists spread over every SM.  Large lists take up
-// to 4 with fp32 states (100 million parameters: 400 us, 7.0 TB/s; 8 steps 406),
-// which end more evenly, and up to 16 with 8-bit ones (256 million with the
-// values' call: 797 us; 32 steps 799), where a warp keeps its blocks' exponents
-// over a chunk.
+// to 4 with fp32 states (100 million parameters: 401 us, 7.0 TB/s; 8 steps 6 us
+// more), which end more evenly, and up to 16 with 8-bit ones (256 million with the
+// values' call: 802 us; 32 steps 2 us more), where a warp keeps its blocks'
+// exponents over a chunk.
 int chunk_iters(int64_t total, int most) {
     const int64_t steps = (total + kAdIter - 1) / kAdIter;
     int n = 1;

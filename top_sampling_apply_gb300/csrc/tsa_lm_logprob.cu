@@ -192,7 +192,8 @@ constexpr int kTcK = 64;
 // log-probabilities were off by 2.4e-6 of themselves.  So the products of 512
 // columns (1,024 where the products bound the kernel) at a time go to tensor
 // memory and from there, rounded to nearest, into sums in registers: now 4e-7,
-// for 7 % of the time.
+// for 7 % of the time.  (256 vocabulary entries a tile are 128 sums a thread, and 48 bytes of it
+// are spilled.)
 template <bool ROWS>
 constexpr int kTcChunk = (ROWS ? 1024 : 512) / kTcK;  // steps of kTcK a chunk
 template <bool ROWS>
@@ -542,7 +543,9 @@ __global__ void __launch_bounds__(kJoinX *kJoinY) lm_logprob_join_kernel(LmLogpr
 // The row-block form needs full blocks to be worth its padding; up to 32 rows
 // are columns instead.
 constexpr int64_t kLmFew = 32;
-// One block of hidden rows: smaller tiles spread the vocabulary more evenly.
+// One block of hidden rows: smaller tiles spread the vocabulary more evenly.  100
+// rows x 128,256 x 4,096: 200 us, 79 % of the copy rate for the weight alone (one
+// row 162 us).
 constexpr int64_t kLmMid = 128;
 
 namespace {

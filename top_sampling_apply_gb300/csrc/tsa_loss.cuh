@@ -353,7 +353,13 @@ __device__ __forceinline__ float near_shift(float m, float c2, float *f) {
     *f = fmaf(z, fmaf(z, 0.5f, 1.f), 1.f);
     return d;
 }
-// e and, with an entropy, the bounded exponents of two logits.
+// e and, with an entropy, the bounded exponents of two logits.  ex2.approx is
+// one instruction and off by 1.5e-7 of its value at most (6e-8 rms), on average
+// 5e-8 too small (measured over [-20, 0)); c2's own rounding, 1.3e-8 of itself at T = 1,
+// makes distant terms too large.  A log-probability takes 1e-8 to 5e-8 of bias from
+// the two beside the 3e-7 to 6e-7 rms of its fp32 roundings, which fp32 sums of expf
+// have as well (their bias is about 1e-8); the sum of a sequence's keeps the bias, so its
+// reward is off by about twice as much.  Taking it out would cost an instruction a pair.
 template <bool ENT, bool NEAR>
 __device__ __forceinline__ void exp_pair(float a, float b, const Ref &r, unsigned long long &e, unsigned long long &y) {
     const unsigned long long x = pair_of(a, b);
@@ -818,11 +824,16 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
 // waiting at a row's barriers takes the most time beside them.  What a row needs
 // once, one warp does for all, another one each row: one starts the next copy,
 // one looks for the row after it, one joins the sums and finishes.  4,096 x
-// 128,256 bf16, an eighth of the rows skipped: 323 us, 6.1 TB/s.  (Before a
-// row's token score and arguments were fetched rows ahead it was 353 us; 366 us
-// then with 256 threads of 16 vectors, and 347 us with four CTAs of 256 threads
-// an SM, which needs clusters of 16 for fp32; with
-// the arguments of 32 rows looked up at a time instead of one a row, 327 us.)
+// 128,256 bf16, an eighth of the rows skipped: 325 us, 6.1 TB/s.  (Before a
+// row's token score and arguments were fetched rows ahead it was 30 us more; 13 us
+// more still with 256 threads of 16 vectors; 6 us less than that with four CTAs
+// of 256 threads an SM, which needs clusters of 16 for fp32; the arguments of 32
+// rows looked up at a time instead of one a row cost 4 us.)
+//
+// Two CTAs of 512 threads leave a thread 64 registers, and half of them are the
+// row.  16 to 20 bytes a thread are spilled in every row's turn, 28 to 48 with an
+// entropy: a part of what that costs (8,192 x 32,000 bf16: 226 us with it, 180
+// without).
 //
 // A warp copies the mask words of its own part of the next row into shared
 // memory under the gradient of this one (72 words in 16 bits, each read from
@@ -832,7 +843,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
 //
 // Rows of up to 16 or 32 KB take CTAs of 128 or 256 threads instead, so that an
 // SM has eight or four of them under way: the exchange of a row takes as long
-// as a short row's arithmetic (10,000 x 8,192 bf16: 164 us with 512 threads, 66 us
+// as a short row's arithmetic (10,000 x 8,192 bf16: 164 us with 512 threads, 67 us
 // with 128).
 constexpr int kHeldVecs = 8, kHeldThreads = 512;
 constexpr int kHeldCluster = 8;
