@@ -335,3 +335,21 @@ int main() {
     csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "top_sampling_apply_gb300", "csrc")
     subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", csrc, str(src), "-o", str(tmp_path / "table")], check=True)
     assert subprocess.run([str(tmp_path / "table")]).returncode == 0
+
+
+def test_no_gradient_asked_for(monkeypatch):
+    # None, like False, asks for the loss alone: there is nothing to raise the version of
+    import top_sampling_apply_gb300 as tsa
+
+    class Lib:
+        def __getattr__(self, name):
+            return (lambda *a: 256) if name.endswith("_bytes") else lambda *a: 0
+
+    monkeypatch.setattr(tsa, "_lib", Lib())
+    monkeypatch.setattr(tsa, "_current_device", lambda: 1)
+    monkeypatch.setattr(tsa, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(tsa.torch, "empty", OnDevice1)
+    f, i, x = OnDevice1(2), OnDevice1(2, dtype=torch.int64), OnDevice1(2, 32)
+    for grad in (None, False):
+        assert tsa.policy_loss(x, i, f, f, grad=grad).grad is None
+        assert tsa.preference_loss(x, i, OnDevice1(3, dtype=torch.int64), grad=grad).grad is None

@@ -489,7 +489,7 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: torch.T
           clip_high, kl_coef, entropy_coef, loss.data_ptr(), row.data_ptr(), lp.data_ptr(),
           None if ent is None else ent.data_ptr(), None if g is None else g.data_ptr(),
           0 if g is None else g.stride(0), None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
-    if g is grad:
+    if g is not None and g is grad:
         _written(g)
     return PolicyLoss(loss, row, lp, ent, g)
 
@@ -535,7 +535,7 @@ def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, seq_start: torch
           P, wgt, ref, beta, label_smoothing, margin, 1 if average else 0, loss.data_ptr(), pair.data_ptr(),
           reward.data_ptr(), lp.data_ptr(), None if g is None else g.data_ptr(), 0 if g is None else g.stride(0),
           None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
-    if g is grad:
+    if g is not None and g is grad:
         _written(g)
     return PreferenceLoss(loss, pair, reward, lp, g)
 
