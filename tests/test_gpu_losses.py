@@ -608,3 +608,37 @@ def test_preference_replays_in_a_graph(tsa, in_place):
         g.replay()
         for p, q in zip(r, want):
             assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_log_probabilities_do_not_err_to_one_side(tsa, dtype):
+    # A sequence's log-ratio adds up what its log-probabilities are off by on average.  With T = 1 that follows from two
+    # things: ex2.approx is 5e-8 too small on average where it is not 1, and log2(e) as an fp32 number is 1.335e-8 of
+    # itself too small, which makes a term at distance d from the row's largest d times that too large.  All else is
+    # rounding to nearest, of which 4 standard errors may be left over these rows, and 1.5e-8 (an eighth of an fp32 ulp
+    # of 1) where rows of like sums round alike.
+    g = torch.Generator(device=DEV).manual_seed(50)
+    V, N = 128256, 2048
+    start, v = torch.tensor([0, N // 2, N], device=DEV), torch.zeros(N, device=DEV)
+    off = {"preference": [], "policy": []}
+    want = []
+    for _ in range(8):
+        rank = torch.randperm(V, generator=g, device=DEV).float().add_(1.0)
+        x = torch.randn(N, V, generator=g, device=DEV).mul_(2.0).sub_(rank.log_().mul_(1.1)).to(dtype)
+        tok = torch.randint(0, V, (N,), generator=g, device=DEV)
+        got = {"preference": tsa.preference_loss(x, tok, start, grad=False).logprob,
+               "policy": tsa.policy_loss(x, tok, v, v).logprob}
+        for a in range(0, N, 512):
+            d = x[a:a + 512].double()
+            d -= d.amax(1, keepdim=True)
+            e = d.exp()
+            Z = e.sum(1)
+            lp = d.gather(1, tok[a:a + 512, None])[:, 0] - Z.log()
+            want.append(5e-8 * (1 - 1 / Z) + 1.335e-8 * (e * d).sum(1) / Z)
+            for k in off:
+                off[k].append(got[k][a:a + 512].double() - lp)
+    want = torch.cat(want).mean().item()
+    for k, o in off.items():
+        o = torch.cat(o)
+        left = 1.5e-8 + 4 * o.std().item() / len(o) ** 0.5
+        assert abs(o.mean().item() - want) <= left, (k, o.mean().item(), want, left)

@@ -356,10 +356,9 @@ __device__ __forceinline__ float near_shift(float m, float c2, float *f) {
 // e and, with an entropy, the bounded exponents of two logits.  ex2.approx is
 // one instruction and off by 1.5e-7 of its value at most (6e-8 rms), on average
 // 5e-8 too small (measured over [-20, 0)); c2's own rounding, 1.3e-8 of itself at T = 1,
-// makes distant terms too large.  A log-probability takes 1e-8 to 5e-8 of bias from
-// the two beside the 3e-7 to 6e-7 rms of its fp32 roundings, which fp32 sums of expf
-// have as well (their bias is about 1e-8); the sum of a sequence's keeps the bias, so its
-// reward is off by about twice as much.  Taking it out would cost an instruction a pair.
+// makes distant terms too large.  The two nearly cancel: a log-probability is off by
+// 3e-7 to 6e-7 rms and by less than 2e-8 on average over rows of 8,192 to 128,256
+// logits, where fp32 sums of expf give the same rms and 1e-8.
 template <bool ENT, bool NEAR>
 __device__ __forceinline__ void exp_pair(float a, float b, const Ref &r, unsigned long long &e, unsigned long long &y) {
     const unsigned long long x = pair_of(a, b);
@@ -443,6 +442,23 @@ constexpr size_t kRowSmem = (size_t)kRowSlots * kRowStage * 16;
 struct WarpSums {
     float m, Z, t;  // m is the warp's, Z and t the thread's
 };
+// 2^d for d <= 0 from e^x's series at |x| <= ln(2) / 2 (its ninth term is 5e-9),
+// rounded to nearest: the factor that brings a part of a row's sums to a larger
+// reference.  By ex2.approx every such factor took another 5e-8 off, two or three
+// times in a long row, and a sequence's log-ratio added that up: its reward
+// was off by 2.5e-6 to 3.6e-6 of itself over 2,000 rows of 128,256 bf16 logits, and
+// is by 0.9e-6 to 1.3e-6 now.
+__device__ __forceinline__ float exp2_factor(float d) {
+    const float n = rintf(d), r = d - n;
+    float p = 1.525273380405984e-5f;
+    p = fmaf(p, r, 1.5403530393381608e-4f);
+    p = fmaf(p, r, 1.3333558146428443e-3f);
+    p = fmaf(p, r, 9.618129107628477e-3f);
+    p = fmaf(p, r, 5.550410866482158e-2f);
+    p = fmaf(p, r, 2.402265069591007e-1f);
+    p = fmaf(fmaf(p, r, kLn2), r, 1.f);
+    return n > -126.f ? __int_as_float(__float_as_int(p) + ((int)n << 23)) : 0.f;
+}
 // A larger reference: Z and t are brought from the old one's form to the new one's.
 template <bool ENT>
 __device__ __forceinline__ void raise(WarpSums &s, float m, float c2) {
@@ -450,7 +466,7 @@ __device__ __forceinline__ void raise(WarpSums &s, float m, float c2) {
         float fo, fn;
         const float d0 = near_shift(s.m, c2, &fo), d1 = near_shift(m, c2, &fn);
         // from the old form to the old m, to the new m, to the new form
-        const float d = fmaxf((s.m - m) * c2, kLowExp), f = ex2_approx(d) * fo * (2.f - fn);
+        const float d = fmaxf((s.m - m) * c2, kLowExp), f = exp2_factor(d) * fo * (2.f - fn);
         // y_new = y_old - d0 + (m_old - m_new) c2 + d1
         if (ENT) s.t = f * fmaf(s.Z, d - d0 + d1, s.t);
         s.Z *= f;
@@ -694,7 +710,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
                 RowStat s;
                 s.m = warp_max(in ? v.x : -INFINITY);
                 const float d = in ? (v.x == s.m ? 0.f : fmaxf((v.x - s.m) * mt.c2, kLowExp)) : kLowExp;
-                const float f = ex2_approx(d);
+                const float f = exp2_factor(d);
                 s.Z = warp_sum_f32(in ? v.y * f : 0.f);
                 s.t = ENT ? warp_sum_f32(in ? fmaf(v.y, d, v.z) * f : 0.f) : 0.f;
                 return s;
@@ -1014,7 +1030,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_held_kernel(RowLo
             s.m = warp_max(s.m);
             for (int i = lane; i < n; i += 32) {
                 const float4 v = stats[half][i];
-                const float d = v.x == s.m ? 0.f : fmaxf((v.x - s.m) * c2, kLowExp), f = ex2_approx(d);
+                const float d = v.x == s.m ? 0.f : fmaxf((v.x - s.m) * c2, kLowExp), f = exp2_factor(d);
                 s.Z = fmaf(v.y, f, s.Z);
                 if (ENT) s.t = fmaf(fmaf(v.y, d, v.z), f, s.t);
             }
