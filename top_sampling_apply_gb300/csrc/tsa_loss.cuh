@@ -147,35 +147,6 @@ __device__ __forceinline__ bool allowed_bit(const int32_t *mrow, int64_t i) {
 struct RowStat {
     float m, Z, t;
 };
-// Both parts against the larger maximum: the part with the smaller one is
-// scaled by 2^d.  An empty part has Z = t = 0 and m = -inf; its exponent is
-// -inf or NaN, and the lower bound makes the factor 0.  merge(a, b) and
-// merge(b, a) have the same bits (on equal maxima the factor is 1 and the
-// sums commute), so all lanes of a butterfly agree.
-__device__ __forceinline__ RowStat merge(const RowStat &a, const RowStat &b, float c2) {
-    const bool up = b.m > a.m;
-    const RowStat hi = up ? b : a, lo = up ? a : b;
-    const bool tie = hi.m == lo.m;
-    const float d = tie ? 0.f : fmaxf((lo.m - hi.m) * c2, kLowExp);
-    const float f = tie ? 1.f : ex2_approx(d);
-    RowStat r;
-    r.m = hi.m;
-    r.Z = fmaf(lo.Z, f, hi.Z);
-    r.t = fmaf(fmaf(lo.Z, d, lo.t), f, hi.t);
-    return r;
-}
-__device__ __forceinline__ RowStat warp_merge(RowStat s, float c2) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        RowStat b;
-        b.m = __shfl_xor_sync(0xFFFFFFFFu, s.m, o);
-        b.Z = __shfl_xor_sync(0xFFFFFFFFu, s.Z, o);
-        b.t = __shfl_xor_sync(0xFFFFFFFFu, s.t, o);
-        s = merge(s, b, c2);
-    }
-    return s;
-}
-
 // ------------------------------------------------------------ arguments
 struct RowScalars {  // what a finished row writes and what its gradient needs
     float a, b;      // the two numbers of the gradient
