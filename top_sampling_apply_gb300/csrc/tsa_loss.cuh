@@ -811,11 +811,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_kernel(RowLossArgs r,
 // waiting at a row's barriers takes the most time beside them.  What a row needs
 // once, one warp does for all, another one each row: one starts the next copy,
 // one looks for the row after it, one joins the sums and finishes.  4,096 x
-// 128,256 bf16, an eighth of the rows skipped: 325 us, 6.1 TB/s.  (Before a
-// row's token score and arguments were fetched rows ahead it was 30 us more; 13 us
-// more still with 256 threads of 16 vectors; 6 us less than that with four CTAs
-// of 256 threads an SM, which needs clusters of 16 for fp32; the arguments of 32
-// rows looked up at a time instead of one a row cost 4 us.)
+// 128,256 bf16, an eighth of the rows skipped: 325 us, 6.1 TB/s.  (It was 353 us
+// before a row's token score and arguments were fetched rows ahead; at that time
+// 366 us with 256 threads of 16 vectors, and 347 us with four CTAs of 256 threads
+// an SM, which needs clusters of 16 for fp32.  Looking up the arguments of 32 rows
+// at a time instead of one a row cost 4 us.)
 //
 // Two CTAs of 512 threads leave a thread 64 registers, and half of them are the
 // row.  16 to 20 bytes a thread are spilled in every row's turn, 28 to 48 with an
