@@ -471,6 +471,117 @@ int tsa_lm_head_logprob(const void *hidden, int64_t M, int64_t H, int64_t hidden
                         void *workspace, size_t workspace_bytes, void *stream);
 size_t tsa_lm_head_logprob_workspace_bytes(int64_t M, int64_t V);
 
+/*
+ * rms_norm -- the root-mean-square norm that makes the hidden rows of the
+ * lm_head_* calls, with the residual's addition and, on request, rows in 8
+ * bits.  With s = x, or x + residual rounded to dtype,
+ *   rstd = 1 / sqrt(mean(s^2) + eps),  y = s rstd weight
+ *   out  = y rounded to dtype, or with `quantize` != 0 int8 codes
+ *          round(y / scale), ties to even, of scale = max|y| / 127
+ *   x            [N, x_row_stride] of dtype, 1 <= H <= 16384
+ *   weight       [H] of weight_dtype: dtype or TSA_F32
+ *   residual     [N, residual_row_stride] of dtype or NULL
+ *   eps          >= 0, finite (TSA_ERR_VALUE)
+ *   out          [N, out_row_stride] of dtype, or int8
+ *   scale_out    [N] float; required with quantize, else not used
+ *   residual_out [N, residual_out_row_stride] of dtype or NULL: s (needs a
+ *                residual: TSA_ERR_NULL)
+ *   rstd_out     [N] float or NULL: what rms_norm_backward takes
+ * An output may be an input itself (same start and row stride), out and
+ * residual_out not the same one; otherwise they must not overlap.  16-byte
+ * aligned rows with H a multiple of 16 bytes take the fastest path.  Squares
+ * and sums in fp32: elements beyond 1e19 overflow.  A row of zeros has scale 0
+ * and codes 0; with eps = 0 it is NaN, as the formula is.  An 8-bit row that is
+ * not finite has codes 0 and a scale of NaN.
+ */
+int tsa_rms_norm(const void *x, tsa_dtype dtype, int64_t N, int64_t H, int64_t x_row_stride, const void *weight,
+                 tsa_dtype weight_dtype, const void *residual, int64_t residual_row_stride, float eps,
+                 int quantize, void *out, int64_t out_row_stride, float *scale_out, void *residual_out,
+                 int64_t residual_out_row_stride, float *rstd_out, void *stream);
+
+/*
+ * rms_norm_backward -- the gradients of rms_norm's (unquantised) result.  With
+ * g the gradient of the result, f = weight g and h = x rstd,
+ *   grad_x = rstd (f - h mean(f h)) + grad_residual,  grad_weight = sum over rows of g h
+ *   x            the rows that were normalised (residual_out where there was a
+ *                residual); rstd [N] as rms_norm gave it
+ *   grad, x, grad_residual, grad_x_out  [N, row stride] of dtype;
+ *                grad_residual NULL for none.  grad_x_out may be grad, x or
+ *                grad_residual itself (same start and row stride)
+ *   grad_weight_out  [H] of weight_dtype (zeros for N == 0)
+ *   workspace    at least tsa_rms_norm_backward_workspace_bytes(N, H) bytes,
+ *                256-byte aligned
+ * fp32 sums, over rows in a fixed order: equal calls give equal bits.
+ */
+int tsa_rms_norm_backward(const void *grad, int64_t grad_row_stride, const void *x, tsa_dtype dtype, int64_t N,
+                          int64_t H, int64_t x_row_stride, const void *weight, tsa_dtype weight_dtype,
+                          const float *rstd, const void *grad_residual, int64_t grad_residual_row_stride,
+                          void *grad_x_out, int64_t grad_x_row_stride, void *grad_weight_out, void *workspace,
+                          size_t workspace_bytes, void *stream);
+size_t tsa_rms_norm_backward_workspace_bytes(int64_t N, int64_t H);
+
+/*
+ * quantize_rows -- rows in 8 bits: scale = max|x| / 127 of each row, codes
+ * round(x / scale), ties to even; rows of zeros and rows that are not finite
+ * as in rms_norm.  Lays out the weight of lm_head_int8.
+ *   x [N, x_row_stride] of dtype, 1 <= H <= 16384; out [N, out_row_stride];
+ *   scale_out [N] float
+ */
+int tsa_quantize_rows(const void *x, tsa_dtype dtype, int64_t N, int64_t H, int64_t x_row_stride, int8_t *out,
+                      int64_t out_row_stride, float *scale_out, void *stream);
+
+/*
+ * lm_head_int8 -- the scores of a head in 8-bit integers, with a scale for each
+ * hidden row and each vocabulary entry:
+ *   out[m, v] = hidden_scale[m] weight_scale[v] sum_k hidden[m, k] weight[v, k]  (+ bias[v])
+ * The integer sum is exact; the result is rounded to out_dtype from fp32.
+ *   hidden       int8 [M, hidden_row_stride], weight int8 [V, weight_row_stride];
+ *                H a multiple of 16, 16 <= H <= 16384, row strides multiples of
+ *                16, both bases 16-byte aligned (TSA_ERR_ALIGN)
+ *   hidden_scale [M], weight_scale [V] float; bias [V] float or NULL
+ *   out          [M, out_row_stride] of out_dtype: the logits of sample and topk
+ */
+int tsa_lm_head_int8(const int8_t *hidden, int64_t M, int64_t H, int64_t hidden_row_stride,
+                     const float *hidden_scale, const int8_t *weight, int64_t V, int64_t weight_row_stride,
+                     const float *weight_scale, const float *bias, void *out, tsa_dtype out_dtype,
+                     int64_t out_row_stride, void *stream);
+
+/*
+ * lm_head_cross_entropy -- the cross entropy of scores that are never written,
+ * and its gradients.  With z = hidden . weight^T (+ bias), capped to softcap
+ * tanh(z / softcap) where softcap > 0, and l = ln sum_v exp(z_v):
+ *   row_loss = l - z[target] + z_loss l^2,  loss = sum over rows of row_weight row_loss
+ *   G[m, v]  = row_weight ((1 + 2 z_loss l) exp(z_v - l) - 1{v = target}) (1 - (z_v / softcap)^2)
+ *   grad_hidden = G . weight,  grad_weight = G^T . hidden,  grad_bias = sum over rows of G
+ *   hidden, weight, bias, softcap: as for lm_head_logprob; M <= 2^20
+ *   targets      [M] int64; a target outside [0, V) skips its row
+ *   row_weight   [M] float or NULL: 1 / (number of rows that count); 0 skips a row
+ *   z_loss       finite (TSA_ERR_VALUE); 0 leaves its term out
+ *   loss_out     [1] float (0 where no row counts); row_loss_out, lse_out [M] float
+ *   grad_hidden_out  bf16 [M, grad_hidden_row_stride] or NULL, grad_weight_out
+ *                bf16 [V, grad_weight_row_stride] or NULL: 16-byte aligned, row
+ *                strides multiples of 8.  They must not overlap an input.
+ *   grad_bias_out  [V] float or NULL (needs a bias: TSA_ERR_NULL)
+ *   workspace    at least tsa_lm_head_cross_entropy_workspace_bytes(M, H, V,
+ *                grads, bias) bytes, 256-byte aligned; grads: whether any
+ *                gradient is asked for, bias: whether the bias's is
+ * A skipped row's hidden row is not used, whatever it holds; its loss, lse and
+ * gradient are 0.  NaN scores count as -inf; a +inf score gives its row an
+ * lse of +inf, a loss of NaN and NaN in the gradients that it takes part in.
+ * bf16 products and fp32 sums.  G goes through bf16 (half a step of 2^-8 of each
+ * of its elements), grad_bias does not.  The weight is read once for the sums and
+ * once or twice more for the gradients.  Sums in a fixed order: equal calls give
+ * equal bits.
+ */
+int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t hidden_row_stride,
+                              const void *weight, int64_t V, int64_t weight_row_stride, const float *bias,
+                              float softcap, const int64_t *targets, const float *row_weight, float z_loss,
+                              float *loss_out, float *row_loss_out, float *lse_out, void *grad_hidden_out,
+                              int64_t grad_hidden_row_stride, void *grad_weight_out,
+                              int64_t grad_weight_row_stride, float *grad_bias_out, void *workspace,
+                              size_t workspace_bytes, void *stream);
+size_t tsa_lm_head_cross_entropy_workspace_bytes(int64_t M, int64_t H, int64_t V, int grads, int bias);
+
 /* Human-readable name of a status code. */
 const char *tsa_status_string(int status);
 

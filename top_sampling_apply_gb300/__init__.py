@@ -1,5 +1,5 @@
-"""Per-row vocabulary selection on GB300, and the training step on the rows it
-sampled: thin Python binding of libtsa.so.
+"""Per-row vocabulary selection on GB300, the training step on the rows it
+sampled, and the norm, scores and loss at the vocabulary head: thin Python binding of libtsa.so.
 
 The calls mirror the C ABI in include/tsa.h (logits-processor, "API";
 lm-head-topk, "API").  This module only marshals arguments: it checks torch
@@ -21,7 +21,8 @@ from . import _build
 
 __all__ = ["apply_token_bitmask", "sample", "topk", "policy_loss", "preference_loss", "PolicyLoss",
            "PreferenceLoss", "lm_head_logprob", "AdamWPlan", "adamw_state", "adamw_plan", "adamw_step",
-           "adamw_state_values", "device_status", "max_vocab", "load_library", "TSAError"]
+           "adamw_state_values", "rms_norm", "RMSNorm", "rms_norm_backward", "quantize_rows", "lm_head_int8",
+           "lm_head_cross_entropy", "CrossEntropy", "device_status", "max_vocab", "load_library", "TSAError"]
 
 _DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _lock = threading.Lock()
@@ -77,6 +78,16 @@ def load_library(path: Optional[str] = None):
         lib.tsa_lm_head_logprob.argtypes = [P, i64, i64, i64, P, i64, i64, P, f32, P, i64, P, f32, P, P, P, sz, P]
         lib.tsa_lm_head_logprob_workspace_bytes.argtypes = [i64, i64]
         lib.tsa_lm_head_logprob_workspace_bytes.restype = sz
+        lib.tsa_lm_head_cross_entropy.argtypes = [P, i64, i64, i64, P, i64, i64, P, f32, P, P, f32, P, P, P, P, i64,
+                                                  P, i64, P, P, sz, P]
+        lib.tsa_lm_head_cross_entropy_workspace_bytes.argtypes = [i64, i64, i64, ci, ci]
+        lib.tsa_lm_head_cross_entropy_workspace_bytes.restype = sz
+        lib.tsa_rms_norm.argtypes = [P, ci, i64, i64, i64, P, ci, P, i64, f32, ci, P, i64, P, P, i64, P, P]
+        lib.tsa_rms_norm_backward.argtypes = [P, i64, P, ci, i64, i64, i64, P, ci, P, P, i64, P, i64, P, P, sz, P]
+        lib.tsa_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
+        lib.tsa_rms_norm_backward_workspace_bytes.restype = sz
+        lib.tsa_quantize_rows.argtypes = [P, ci, i64, i64, i64, P, i64, P, P]
+        lib.tsa_lm_head_int8.argtypes = [P, i64, i64, i64, P, P, i64, i64, P, P, P, ci, i64, P]
         f64 = ctypes.c_double
         lib.tsa_adamw_step.argtypes = [P, i64, ci, ci, i32, f64, f64, f64, f64, f64, i64, P, u64, u64, P]
         lib.tsa_adamw_state_values.argtypes = [P, i64, P, P, P]
@@ -93,7 +104,8 @@ def load_library(path: Optional[str] = None):
         for fn in ("tsa_apply_token_bitmask", "tsa_sample", "tsa_sample_noalloc", "tsa_topk",
                    "tsa_sample_icdf", "tsa_bitmask_from_allowed", "tsa_sample_sequential", "tsa_lm_head_topk",
                    "tsa_policy_loss", "tsa_preference_loss", "tsa_lm_head_logprob", "tsa_adamw_step",
-                   "tsa_adamw_state_values",
+                   "tsa_adamw_state_values", "tsa_lm_head_cross_entropy", "tsa_rms_norm", "tsa_rms_norm_backward",
+                   "tsa_quantize_rows", "tsa_lm_head_int8",
                    "tsa_device_status", "tsa_selftest_wait_timeout"):
             getattr(lib, fn).restype = ci
         _lib = lib
@@ -695,6 +707,215 @@ def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
         if given is not None:
             _written(mine)
     return outs[0], outs[1]
+
+
+def _matrix(t: torch.Tensor, index: int, shape, dtype: torch.dtype, name: str, unit: str = "H") -> torch.Tensor:
+    """Checks a [rows, columns] tensor of unit stride along its columns on CUDA device ``index``."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or (t.size(0) > 0 and t.stride(1) != 1
+                                                                              and t.size(1) > 1):
+        raise ValueError("%s must be a %s %s tensor on cuda:%d with unit stride along %s"
+                         % (name, dtype, list(shape), index, unit))
+    return t
+
+
+def _hidden_rows(t: torch.Tensor, name: str):
+    if not t.is_cuda or t.dtype not in _DT or t.dim() != 2 or (t.size(1) > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be a CUDA float32, float16 or bfloat16 2-D tensor with unit stride along H" % name)
+    return t.size(0), t.size(1), t.get_device()
+
+
+def _norm_weight(weight: torch.Tensor, x: torch.Tensor) -> None:
+    if weight.dtype not in (x.dtype, torch.float32) or weight.get_device() != x.get_device() or weight.dim() != 1 \
+            or weight.size(0) != x.size(1) or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous [H] tensor of the rows' dtype or float32 on their device")
+
+
+class RMSNorm(NamedTuple):
+    """What ``rms_norm`` returns."""
+    out: torch.Tensor  # [N, H] of the rows' dtype, or int8
+    scale: Optional[torch.Tensor]  # float32 [N]: what an int8 row's codes are multiplied by
+    residual: Optional[torch.Tensor]  # [N, H]: the rows with the residual added, rounded to their dtype
+    rstd: torch.Tensor  # float32 [N]: what ``rms_norm_backward`` takes
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             quantize: bool = False, out: Optional[torch.Tensor] = None,
+             residual_out: Optional[torch.Tensor] = None) -> RMSNorm:
+    """The root-mean-square norm that makes the hidden rows of the ``lm_head_*`` calls.
+
+    With s = x, or x + ``residual`` rounded to their dtype, out = s / sqrt(mean(s^2) + eps) *
+    ``weight``.  ``quantize`` gives the rows in 8 bits, as ``lm_head_int8`` takes them: scale = max|y| / 127 of the
+    unrounded row y, and codes round(y / scale), ties to even.  x [N, H <= 16384] float32,
+    float16 or bfloat16, weight [H] of that dtype or float32.  ``out`` may be x or residual (not if
+    ``quantize``), and ``residual_out`` too: x, residual or a tensor of its own."""
+    lib = _lib or load_library()
+    N, H, dev = _hidden_rows(x, "x")
+    _norm_weight(weight, x)
+    device = x.device
+    y = torch.empty((N, H), dtype=torch.int8 if quantize else x.dtype, device=device) if out is None else \
+        _matrix(out, dev, (N, H), torch.int8 if quantize else x.dtype, "out")
+    total = None
+    if residual is not None:
+        _matrix(residual, dev, (N, H), x.dtype, "residual")
+        total = torch.empty((N, H), dtype=x.dtype, device=device) if residual_out is None else \
+            _matrix(residual_out, dev, (N, H), x.dtype, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    scale = torch.empty(N, dtype=torch.float32, device=device) if quantize else None
+    rstd = torch.empty(N, dtype=torch.float32, device=device)
+    _call(dev, lib.tsa_rms_norm, x.data_ptr(), _DT[x.dtype], N, H, x.stride(0), weight.data_ptr(), _DT[weight.dtype],
+          None if residual is None else residual.data_ptr(), 0 if residual is None else residual.stride(0), eps,
+          1 if quantize else 0, y.data_ptr(), y.stride(0), None if scale is None else scale.data_ptr(),
+          None if total is None else total.data_ptr(), 0 if total is None else total.stride(0), rstd.data_ptr(),
+          _raw_stream(dev))
+    if out is not None:
+        _written(out)
+    if residual_out is not None:
+        _written(residual_out)
+    return RMSNorm(y, scale, total, rstd)
+
+
+def rms_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                      grad_residual: Optional[torch.Tensor] = None, grad_x: Optional[torch.Tensor] = None,
+                      grad_weight: Optional[torch.Tensor] = None):
+    """The gradients (grad_x, grad_weight) of ``rms_norm`` for the gradient ``grad`` of its
+    (unquantised) result.  ``x``: the rows that were normalised (its ``residual`` where one was added), ``rstd`` as it
+    gave it.  ``grad_residual``, the gradient that arrives along the residual stream, is added to grad_x, which
+    is then that of x and of the residual alike.  ``grad_x`` may be ``grad``, ``grad_residual`` or a tensor of its
+    own; ``grad_weight`` has the weight's dtype.  Sums in float32, over rows in a fixed order."""
+    lib = _lib or load_library()
+    N, H, dev = _hidden_rows(x, "x")
+    _norm_weight(weight, x)
+    _matrix(grad, dev, (N, H), x.dtype, "grad")
+    if grad_residual is not None:
+        _matrix(grad_residual, dev, (N, H), x.dtype, "grad_residual")
+    r = _vec(rstd, N, torch.float32, dev, "rstd")
+    dx = torch.empty((N, H), dtype=x.dtype, device=x.device) if grad_x is None else \
+        _matrix(grad_x, dev, (N, H), x.dtype, "grad_x")
+    dw = torch.empty(H, dtype=weight.dtype, device=x.device) if grad_weight is None else grad_weight
+    to = _vec(dw, H, weight.dtype, dev, "grad_weight")
+    nws = lib.tsa_rms_norm_backward_workspace_bytes(N, H)
+    ws = torch.empty(nws, dtype=torch.uint8, device=x.device) if nws else None
+    _call(dev, lib.tsa_rms_norm_backward, grad.data_ptr(), grad.stride(0), x.data_ptr(), _DT[x.dtype], N, H,
+          x.stride(0), weight.data_ptr(), _DT[weight.dtype], r,
+          None if grad_residual is None else grad_residual.data_ptr(),
+          0 if grad_residual is None else grad_residual.stride(0), dx.data_ptr(), dx.stride(0), to,
+          None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
+    for t in (grad_x, grad_weight):
+        if t is not None:
+            _written(t)
+    return dx, dw
+
+
+def quantize_rows(x: torch.Tensor, out: Optional[torch.Tensor] = None):
+    """Rows in 8 bits: (codes int8 [N, H], scale float32 [N]) with scale = max|x| / 127 of each row and codes
+    round(x / scale), ties to even.  A row of zeros has scale 0; a row that is not finite codes 0 and a scale of
+    NaN.  Lays out the weight of ``lm_head_int8``, whose rows are vocabulary entries."""
+    lib = _lib or load_library()
+    N, H, dev = _hidden_rows(x, "x")
+    q = torch.empty((N, H), dtype=torch.int8, device=x.device) if out is None else \
+        _matrix(out, dev, (N, H), torch.int8, "out")
+    scale = torch.empty(N, dtype=torch.float32, device=x.device)
+    _call(dev, lib.tsa_quantize_rows, x.data_ptr(), _DT[x.dtype], N, H, x.stride(0), q.data_ptr(), q.stride(0),
+          scale.data_ptr(), _raw_stream(dev))
+    if out is not None:
+        _written(out)
+    return q, scale
+
+
+def lm_head_int8(hidden: torch.Tensor, hidden_scale: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor,
+                 bias: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The scores [M, V] of a head in 8-bit integers, for ``sample``, ``topk`` and the losses: hidden_scale[m]
+    weight_scale[v] times the exact integer product of int8 hidden [M, H] and int8 weight [V, H], plus ``bias`` (float32
+    [V]), rounded once to ``dtype``.  ``rms_norm(quantize=True)`` makes the hidden rows, ``quantize_rows`` the weight."""
+    lib = _lib or load_library()
+    for t, name in ((hidden, "hidden"), (weight, "weight")):
+        if t.dtype is not torch.int8 or not t.is_cuda or t.dim() != 2 or t.stride(1) != 1:
+            raise ValueError("%s must be a CUDA int8 2-D tensor with unit stride along H" % name)
+    M, H = hidden.shape
+    V = weight.size(0)
+    dev = hidden.get_device()
+    if weight.size(1) != H or weight.get_device() != dev:
+        raise ValueError("weight must be [V, H] on the hidden rows' device")
+    hs = _vec(hidden_scale, M, torch.float32, dev, "hidden_scale")
+    ws = _vec(weight_scale, V, torch.float32, dev, "weight_scale")
+    b = _vec(bias, V, torch.float32, dev, "bias")
+    if dtype not in _DT:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    z = torch.empty((M, V), dtype=dtype, device=hidden.device) if out is None else \
+        _matrix(out, dev, (M, V), dtype, "out", "V")
+    _call(dev, lib.tsa_lm_head_int8, hidden.data_ptr(), M, H, hidden.stride(0), hs, weight.data_ptr(), V,
+          weight.stride(0), ws, b, z.data_ptr(), _DT[dtype], z.stride(0), _raw_stream(dev))
+    if out is not None:
+        _written(out)
+    return z
+
+
+class CrossEntropy(NamedTuple):
+    """What ``lm_head_cross_entropy`` returns."""
+    loss: torch.Tensor  # float32 scalar: the weighted sum over rows
+    row_loss: torch.Tensor  # float32 [M]
+    lse: torch.Tensor  # float32 [M]: the log-sum-exp of each row's scores
+    grad_hidden: Optional[torch.Tensor]  # bfloat16 [M, H]
+    grad_weight: Optional[torch.Tensor]  # bfloat16 [V, H]
+    grad_bias: Optional[torch.Tensor]  # float32 [V]
+
+
+def lm_head_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                          bias: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                          row_weight: Optional[torch.Tensor] = None, z_loss: float = 0.0,
+                          grad_hidden: Union[bool, torch.Tensor] = True,
+                          grad_weight: Union[bool, torch.Tensor] = True,
+                          grad_bias: Union[bool, torch.Tensor] = True) -> CrossEntropy:
+    """The cross entropy of the scores hidden @ weight^T (+ bias, capped to softcap tanh(z /
+    softcap) where softcap > 0) against ``targets``, and its gradients, without the scores: they are
+    formed a piece of the vocabulary at a time.
+
+    A row's loss is lse - z[target] + z_loss lse^2 with lse = ln sum exp(z); the loss is the sum of
+    ``row_weight`` times it (None: the mean over the rows that count).  A target outside [0, V) or a weight of
+    0 skips a row: its hidden row is not used and its outputs are 0.  hidden bf16 [M, H], weight
+    bf16 [V, H], targets int64 [M], bias and row_weight float32.  Each gradient: True for a new tensor, a
+    tensor to write (an ``adamw_plan``'s, say), or False for none; with all False the loss alone."""
+    lib = _lib or load_library()
+    for t, name in ((hidden, "hidden"), (weight, "weight")):
+        if t.dtype is not torch.bfloat16 or not t.is_cuda or t.dim() != 2 or t.stride(1) != 1:
+            raise ValueError("%s must be a CUDA bfloat16 2-D tensor with unit stride along H" % name)
+    M, H = hidden.shape
+    V = weight.size(0)
+    dev = hidden.get_device()
+    if weight.size(1) != H or weight.get_device() != dev:
+        raise ValueError("weight must be [V, H] on the hidden rows' device")
+    t = _vec(targets, M, torch.int64, dev, "targets")
+    b = _vec(bias, V, torch.float32, dev, "bias")
+    w = _vec(row_weight, M, torch.float32, dev, "row_weight")
+    empty, device, bf16, f32 = torch.empty, hidden.device, torch.bfloat16, torch.float32
+    given = [g for g in (grad_hidden, grad_weight, grad_bias) if isinstance(g, torch.Tensor)]
+    dh = _matrix(grad_hidden, dev, (M, H), bf16, "grad_hidden") if isinstance(grad_hidden, torch.Tensor) else \
+        empty((M, H), dtype=bf16, device=device) if grad_hidden else None
+    dw = _matrix(grad_weight, dev, (V, H), bf16, "grad_weight") if isinstance(grad_weight, torch.Tensor) else \
+        empty((V, H), dtype=bf16, device=device) if grad_weight else None
+    db = None
+    if isinstance(grad_bias, torch.Tensor):
+        if bias is None:
+            raise ValueError("grad_bias needs a bias")
+        db = grad_bias
+    elif grad_bias and bias is not None:
+        db = empty(V, dtype=f32, device=device)
+    to_b = _vec(db, V, f32, dev, "grad_bias")
+    loss, row, lse = empty((), dtype=f32, device=device), empty(M, dtype=f32, device=device), \
+        empty(M, dtype=f32, device=device)
+    grads = dh is not None or dw is not None or db is not None
+    nws = lib.tsa_lm_head_cross_entropy_workspace_bytes(M, H, V, 1 if grads else 0, 0 if db is None else 1)
+    ws = empty(nws, dtype=torch.uint8, device=device) if nws else None
+    _call(dev, lib.tsa_lm_head_cross_entropy, hidden.data_ptr(), M, H, hidden.stride(0), weight.data_ptr(), V,
+          weight.stride(0), b, softcap, t, w, z_loss, loss.data_ptr(), row.data_ptr(), lse.data_ptr(),
+          None if dh is None else dh.data_ptr(), 0 if dh is None else dh.stride(0),
+          None if dw is None else dw.data_ptr(), 0 if dw is None else dw.stride(0), to_b,
+          None if ws is None else ws.data_ptr(), nws, _raw_stream(dev))
+    if given:
+        _written(given)
+    return CrossEntropy(loss, row, lse, dh, dw, db)
 
 
 def device_status(clear: bool = True) -> int:

@@ -224,11 +224,94 @@ struct LmLogprobArgs {
     float *out;
     float2 *part;            // [parts][rows]: a part's largest score and its sum against it
     float *tok;              // [rows]: the token's score
+    // the cross entropy's: the log-sum-exp [M], and a device count of rows
+    // (NULL: all), of which these are the ones from `first` on
+    float *lse;
+    const int32_t *count;
+    int64_t first;
 };
 constexpr int64_t kLmRows = 8192;  // rows a pass over the weight takes
 int64_t lm_logprob_parts(int64_t M, int64_t V);
 int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st);
 unsigned int *lm_logprob_status_ptr();
+
+// The root-mean-square norm of rows with the residual's addition, and rows in
+// 8 bits; its backward pass.
+constexpr int64_t kNormMaxH = 16384;
+struct NormArgs {
+    const void *x;  // [N, xs]
+    int64_t N, H, xs;
+    const void *w;  // [H], of the rows' type or fp32
+    bool w_f32;
+    const void *r;  // [N, rs] or NULL
+    int64_t rs;
+    float eps;
+    void *out;      // [N, os] of the rows' type, or int8
+    int64_t os;
+    float *scale;   // [N], 8-bit rows only
+    void *res;      // [N, ress] or NULL: the sum
+    int64_t ress;
+    float *rstd;    // [N] or NULL
+};
+// norm false: the rows themselves in 8 bits (w, r, eps, res and rstd not used).
+int norm_launch(const NormArgs &args, int dtype, bool norm, bool q, cudaStream_t st);
+struct NormBackArgs {
+    const void *g, *x;
+    int64_t N, H, gs, xs;
+    const void *w;
+    bool w_f32;
+    const float *rstd;
+    const void *gr;  // [N, grs] or NULL
+    int64_t grs;
+    void *dx;
+    int64_t dxs;
+    void *dw;        // [H] of the weight's type
+    float *part;     // [norm_back_parts][H]
+};
+int64_t norm_back_parts(int64_t N, int64_t H);
+int norm_back_launch(const NormBackArgs &args, int dtype, cudaStream_t st);
+
+// Scores from 8-bit integers.
+struct Int8Args {
+    const int8_t *hidden;  // [M, hstride]
+    int64_t M, H, hstride;
+    const int8_t *weight;  // [V, wstride]
+    int64_t V, wstride;
+    const float *hscale, *wscale, *bias;
+    void *out;             // [M, ostride] of dtype
+    int64_t ostride;
+    int dtype;
+};
+int int8_launch(const Int8Args &args, cudaStream_t st);
+
+// The cross entropy from the hidden rows, with its gradients.
+struct XentArgs {
+    const uint16_t *hidden;  // bf16 [M, hstride]
+    int64_t M, H, hstride;
+    const uint16_t *weight;  // bf16 [V, wstride]
+    int64_t V, wstride;
+    const float *bias;
+    float cap, z_loss;
+    const int64_t *targets;
+    const float *row_weight;
+    float *loss, *row_loss, *lse;
+    uint16_t *dh, *dw;       // bf16 [M, dhstride], [V, dwstride], or NULL
+    int64_t dhstride, dwstride;
+    float *db;               // [V] or NULL
+    // workspace; "c": of the rows that count, one after another
+    int32_t *count, *place, *rows;  // [1], [M]: a row's place or -1, [M]: a place's row
+    int64_t *tokens;
+    float *weight_c, *row_loss_c, *logprob_c, *lse_c;
+    float4 *coef;            // what a place's gradient needs
+    uint16_t *hidden_c;      // [padded, H]
+    uint16_t *grad;          // [padded, piece]: a piece of the vocabulary's part of G
+    float *acc;              // [padded, H]: dH so far
+    float *db_part;
+};
+__host__ __device__ inline int64_t xent_padded(int64_t M) { return M < 1 ? 128 : (M + 127) / 128 * 128; }
+constexpr int64_t kXentMaxRows = 1 << 20;
+int64_t xent_piece(int64_t M, int64_t V);
+int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t st);
 
 int selftest_launch(uint32_t limit_us, cudaStream_t st);
 

@@ -4,18 +4,16 @@
 // without writing the scores.  A first kernel forms, for every part of the
 // vocabulary and every row, the largest score m and Z = sum exp((z - m) / T),
 // and stores the token's own score; a second one joins a row's parts.
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "tsa_device.cuh"
 #include "tsa_host.h"
+#include "tsa_tcgen05.cuh"
 
 namespace tsa {
 
 namespace {
-
-constexpr float kLog2eH = 1.4426950408889634f;
 
 __device__ __forceinline__ float row_temp(const LmLogprobArgs &a, int64_t row) {
     const float T = a.temperature ? __ldg(a.temperature + row) : a.temperature_s;
@@ -29,129 +27,6 @@ __device__ __forceinline__ float2 join(float2 a, float2 b, float c2) {
     const float f = hi.x == lo.x ? 1.f : ex2_approx(fmaxf((lo.x - hi.x) * c2, -1.0e4f));
     return make_float2(hi.x, fmaf(lo.y, f, hi.y));
 }
-// cap tanh(z / cap), within 2^-21 of itself for every cap.  With x = z / cap:
-//   |x| <= 5/8  z P(x^2), P a polynomial of degree 5 with P(0) = 1, fitted to equal relative error (Remez's exchange;
-//               with its coefficients in fp32 within 2^-26 of tanh(x) / x).
-//   else        cap (1 - 2 / (1 + e^(2 |x|))) with z's sign.  Near x = 0 that difference is off by 2^-23 of the cap, not of
-//               the score: 6e-5 at a score of 3 and a cap of 1,000, and 8e-3 at a cap of 100,000.
-// Scores of a model rarely pass 5/8 of the cap, and the polynomial needs no exponential and no division: 2,048 rows x
-// 130,000 x 256 at a cap of 30 309 us, 198 us without a cap (336 us with the second form alone).  With every thread's
-// scores on both sides (cap 8) it is 456 us, and 1,681 instead of 1,630 us for 128,256 x 5,120.
-struct Cap {
-    float cap, inv, k, bend;  // 1 / cap, 2 log2(e) / cap, 5/8 cap
-};
-__device__ __forceinline__ Cap make_cap(float cap) {
-    const float inv = cap > 0.f ? fminf(1.f / cap, 3.4028234e38f) : 0.f;
-    return Cap{cap, inv, inv * (2.f * kLog2eH), 0.625f * cap};
-}
-constexpr float kCap1 = -0.3333328068256378f, kCap2 = 0.13331441581249237f, kCap3 = -0.05373971536755562f,
-                kCap4 = 0.0206390880048275f, kCap5 = -0.005704986862838268f;
-__device__ __forceinline__ void cap_near(float &a, float &b, const Cap &c) {
-    const auto both = [](float x) { return pair_of(x, x); };
-    const unsigned long long z = pair_of(a, b), x = mul2(z, both(c.inv)), s = mul2(x, x);
-    unsigned long long p = fma2(both(kCap5), s, both(kCap4));
-    p = fma2(fma2(fma2(p, s, both(kCap3)), s, both(kCap2)), s, both(kCap1));
-    split_pair(mul2(z, fma2(p, s, both(1.f))), a, b);
-}
-// n scores, a multiple of 8.
-template <int n>
-__device__ __forceinline__ void soft_cap(float *z, const Cap &c) {
-    float top = 0.f;
-#pragma unroll
-    for (int q = 0; q < n; ++q) top = fmaxf(top, fabsf(z[q]));
-    if (top > c.bend) {
-        // eight at a time, in this order: all at once they do not fit the registers
-#pragma unroll
-        for (int g = 0; g < n; g += 8) {
-            float u[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(u[q]) : "f"(fabsf(z[g + q]) * c.k));
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(u[q]) : "f"(fmaf(0.5f, u[q], 0.5f)));
-#pragma unroll
-            for (int q = 0; q < 8; ++q) u[q] = copysignf(fmaf(-c.cap, u[q], c.cap), z[g + q]);
-#pragma unroll
-            for (int q = 0; q < 8; q += 2) {
-                float a = z[g + q], b = z[g + q + 1];
-                cap_near(a, b, c);
-                z[g + q] = fabsf(z[g + q]) > c.bend ? u[q] : a;
-                z[g + q + 1] = fabsf(z[g + q + 1]) > c.bend ? u[q + 1] : b;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int q = 0; q < n; q += 2) cap_near(z[q], z[q + 1], c);
-    }
-}
-
-// ------------------------------------------------------------ tensor memory
-// tcgen05 (PTX ISA): one thread issues D[128, N] += A[128, 16] B[N, 16]^T from
-// two shared-memory tiles into tensor memory; a warp reads its 32 lanes of D.
-__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
-}
-__device__ __forceinline__ void mma_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void mma_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
-}
-// Arrive on `bar` once every MMA this thread has issued so far is complete.
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-template <int N> struct TmemLoad;
-template <> struct TmemLoad<16> {
-    __device__ static __forceinline__ void ld(uint32_t a, uint32_t (&r)[16]) {
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-            : "r"(a)
-            : "memory");
-    }
-};
-template <> struct TmemLoad<32> {
-    __device__ static __forceinline__ void ld(uint32_t a, uint32_t (&r)[32]) {
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-              "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-              "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-            : "r"(a)
-            : "memory");
-    }
-};
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// A tile of 64 bf16 columns, 128 bytes a row, as TMA writes it with the
-// 128-byte swizzle: rows follow one another, eight rows (1,024 bytes) repeat
-// the pattern, K is contiguous.  The 16 columns of step k start 32 k bytes in.
-__device__ __forceinline__ uint64_t smem_tile(const void *p) {
-    return ((uint64_t)(smem_u32(p) >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int32_t x, int32_t y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-            "r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-
 __device__ unsigned int g_lm_logprob_status;
 
 // x = z if a == b: a selection that keeps an array's elements in registers
@@ -161,6 +36,12 @@ __device__ __forceinline__ void select_if(float &x, float z, int a, int b) {
     asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, %3;\n\tselp.f32 %0, %1, %0, p;\n\t}" : "+f"(x) : "f"(z), "r"(a), "r"(b));
 }
 
+// The rows that count: all, or as many as a kernel before left on the device.
+__device__ __forceinline__ int64_t row_count(const LmLogprobArgs &a) {
+    if (!a.count) return a.M;
+    const int64_t n = (int64_t)*a.count - a.first;
+    return n < 0 ? 0 : n < a.M ? n : a.M;
+}
 // A bounded wait whose outcome the whole warp shares.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, &g_lm_logprob_status));
@@ -186,7 +67,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
 // through the hidden rows first, so that a weight tile is fetched from HBM once
 // and from L2 by the other row blocks.  One part for every N / 2 entries of the
 // vocabulary.
-constexpr int kTcK = 64;
 // The tensor cores add to their accumulator with truncation: a score of 320
 // steps (H = 5,120) came out 9e-6 of itself too small, and 2,048
 // log-probabilities were off by 2.4e-6 of themselves.  So the products of 512
@@ -212,7 +92,7 @@ struct TcShape {
 template <int N, bool ROWS, int STAGES>
 __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const __grid_constant__ CUtensorMap map_a,
                                                                    const __grid_constant__ CUtensorMap map_b,
-                                                                   LmLogprobArgs a, int64_t tiles, int row_blocks, int64_t run) {
+                                                                   const LmLogprobArgs a, int64_t v_tiles, int64_t run) {
     using S = TcShape<N, ROWS, STAGES>;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[STAGES], empty[STAGES], done[2], drained[2], last;
@@ -223,6 +103,9 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kblocks = (int)((a.H + kTcK - 1) / kTcK);
+    const int64_t M = row_count(a);
+    const int row_blocks = ROWS ? (int)((M + 127) / 128) : 1;
+    const int64_t tiles = v_tiles * row_blocks;
     // this CTA's vocabulary rows (few hidden rows), or tiles
     const int64_t v_first = ROWS ? 0 : (int64_t)blockIdx.x * run;
     const int64_t v_end = ROWS || v_first + run > a.V ? a.V : v_first + run;
@@ -330,7 +213,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
             for (int64_t t = t_first; ok && t < t_end; t += t_step) {
                 const int64_t row = (t % row_blocks) * 128 + quarter * 32 + lane;
                 const int64_t v0 = (t / row_blocks) * N + half * NC;
-                const bool in = row < a.M;
+                const bool in = row < M;
                 const float c2 = in ? kLog2eH / row_temp(a, row) : 1.f;
                 const int64_t want = in ? __ldg(a.tokens + row) - v0 : -1;
                 const int32_t *mrow = a.mask && in ? a.mask + row * a.mstride : nullptr;
@@ -428,7 +311,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
                         st.y = s0 + s1;
                     }
                 }
-                if (in && v0 < a.V) a.part[((t / row_blocks) * 2 + half) * a.M + row] = st;
+                if (in && v0 < a.V) a.part[((t / row_blocks) * 2 + half) * M + row] = st;
             }
         } else {
             float2 st[N];
@@ -460,7 +343,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
                 if (a.cap > 0.f) soft_cap<N>(z, cap);
 #pragma unroll
                 for (int q = 0; q < N; ++q) {
-                    if (q >= a.M) break;
+                    if (q >= M) break;
                     float x = fmaxf(z[q], -INFINITY);
                     if (v >= v_end) x = -INFINITY;  // lanes past the run hold what was there before
                     if (a.mask && w0 < v_end &&
@@ -473,7 +356,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
             if (ok) {
 #pragma unroll
                 for (int q = 0; q < N; ++q) {
-                    if (q >= a.M) break;
+                    if (q >= M) break;
                     const float c2 = kLog2eH / row_temp(a, q);
                     float2 x = st[q];
 #pragma unroll
@@ -490,11 +373,11 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
     }
     __syncthreads();
     if constexpr (!ROWS) {
-        if (threadIdx.x < N && (int64_t)threadIdx.x < a.M) {
+        if (threadIdx.x < N && (int64_t)threadIdx.x < M) {
             const float c2 = kLog2eH / row_temp(a, threadIdx.x);
             float2 x = s_part[0][threadIdx.x];
             for (int w = 1; w < 4; ++w) x = join(x, s_part[w][threadIdx.x], c2);
-            a.part[(int64_t)blockIdx.x * a.M + threadIdx.x] = x;
+            a.part[(int64_t)blockIdx.x * M + threadIdx.x] = x;
         }
     }
     if (warp == 1) tmem_free(tmem, S::COLS);
@@ -503,22 +386,23 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
 // A row's parts: 8 rows a CTA, 64 threads a row (a pass over 2,048 parts is 32
 // loads a thread, four under way together), then a tree over them.
 constexpr int kJoinX = 8, kJoinY = 64;
-__global__ void __launch_bounds__(kJoinX *kJoinY) lm_logprob_join_kernel(LmLogprobArgs a, int64_t parts) {
+__global__ void __launch_bounds__(kJoinX *kJoinY) lm_logprob_join_kernel(const LmLogprobArgs a, int64_t parts) {
     __shared__ float2 sh[kJoinY][kJoinX];
     pdl_wait_primary();
+    const int64_t M = row_count(a);
     const int64_t row = (int64_t)blockIdx.x * kJoinX + threadIdx.x;
-    const float T = row < a.M ? row_temp(a, row) : 1.f, c2 = kLog2eH / T;
+    const float T = row < M ? row_temp(a, row) : 1.f, c2 = kLog2eH / T;
     float2 s = make_float2(-INFINITY, 0.f);
-    if (row < a.M) {
+    if (row < M) {
         const float2 *part = a.part + row;
         int64_t p = threadIdx.y;
         for (; p + 3 * kJoinY < parts; p += 4 * kJoinY) {
             float2 v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = part[(p + i * kJoinY) * a.M];
+            for (int i = 0; i < 4; ++i) v[i] = part[(p + i * kJoinY) * M];
             s = join(s, join(join(v[0], v[1], c2), join(v[2], v[3], c2), c2), c2);
         }
-        for (; p < parts; p += kJoinY) s = join(s, part[p * a.M], c2);
+        for (; p < parts; p += kJoinY) s = join(s, part[p * M], c2);
     }
     sh[threadIdx.y][threadIdx.x] = s;
 #pragma unroll
@@ -527,7 +411,7 @@ __global__ void __launch_bounds__(kJoinX *kJoinY) lm_logprob_join_kernel(LmLogpr
         if (threadIdx.y < o)
             sh[threadIdx.y][threadIdx.x] = join(sh[threadIdx.y][threadIdx.x], sh[threadIdx.y + o][threadIdx.x], c2);
     }
-    if (threadIdx.y != 0 || row >= a.M) return;
+    if (threadIdx.y != 0 || row >= M) return;
     s = sh[0][threadIdx.x];
     const int64_t i = a.tokens[row];
     float r = __int_as_float(0x7FC00000);
@@ -536,6 +420,7 @@ __global__ void __launch_bounds__(kJoinX *kJoinY) lm_logprob_join_kernel(LmLogpr
         r = z > -INFINITY ? (z - s.x) / T - logf(s.y) : -INFINITY;
     }
     a.out[row] = r;
+    if (a.lse) a.lse[row] = s.x < INFINITY ? s.x / T + logf(s.y) : s.x;
 }
 
 }  // namespace
@@ -550,43 +435,6 @@ constexpr int64_t kLmMid = 128;
 
 namespace {
 
-typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encoder() {
-    static EncodeFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) !=
-                cudaSuccess ||
-            r != cudaDriverEntryPointSuccess)
-            return (EncodeFn) nullptr;
-        return (EncodeFn)p;
-    }();
-    return fn;
-}
-
-// bf16 [rows, cols] with `stride` elements a row, in boxes of 64 columns.
-bool make_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t stride, int box_rows) {
-    const EncodeFn fn = encoder();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {kTcK, (cuuint32_t)box_rows}, step[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, step,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-        return 152;
-    return n;
-}
-
 template <int N, bool ROWS, int STAGES>
 int launch_products(const LmLogprobArgs &args, int64_t *parts, cudaStream_t st) {
     using S = TcShape<N, ROWS, STAGES>;
@@ -598,14 +446,14 @@ int launch_products(const LmLogprobArgs &args, int64_t *parts, cudaStream_t st) 
                   ROWS ? args.wstride : args.hstride, N))
         return -1;
     if (prepare_kernel(fn, S::SMEM, 1) != 0) return -1;
-    int row_blocks = ROWS ? (int)((args.M + 127) / 128) : 1;
-    int64_t tiles = ROWS ? row_blocks * ((args.V + N - 1) / N) : (args.V + 127) / 128;
+    int64_t v_tiles = ROWS ? (args.V + N - 1) / N : (args.V + 127) / 128;
+    const int64_t tiles = v_tiles * (ROWS ? (args.M + 127) / 128 : 1);
     const int64_t sms = sm_count();
     int64_t run = ((args.V + sms - 1) / sms + 31) / 32 * 32;
     const int64_t grid = ROWS ? (tiles < sms ? tiles : sms) : (args.V + run - 1) / run;
     *parts = ROWS ? (args.V + N / 2 - 1) / (N / 2) : grid;
     LmLogprobArgs a = args;
-    void *params[] = {&ma, &mb, &a, &tiles, &row_blocks, &run};
+    void *params[] = {&ma, &mb, &a, &v_tiles, &run};
     return cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kTcThreads<ROWS>), params, S::SMEM, st) == cudaSuccess ? 0 : -1;
 }
 
