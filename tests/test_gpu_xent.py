@@ -199,6 +199,11 @@ def test_more_rows_than_one_pass(tsa):
     check(c, tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"]))
 
 
+def test_several_pieces_of_the_vocabulary(tsa):
+    c = make(5, 8192 + 300, 9001, 64, bias=True, skip=0.01)
+    check(c, tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"]))
+
+
 def test_large(tsa):
     c = make(6, 700, 20001, 1024, bias=True, skip=0.2)
     x = check(c, tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"]))

@@ -46,7 +46,7 @@ XentLayout xent_layout(int64_t M, int64_t H, int64_t V, bool grads, bool bias) {
         at += align256(bytes);
         return start;
     };
-    l.count = take(4);
+    l.count = take(8);
     l.place = take(m * 4);
     l.rows = take(n * 4);
     l.tokens = take(n * 8);
@@ -60,7 +60,7 @@ XentLayout xent_layout(int64_t M, int64_t H, int64_t V, bool grads, bool bias) {
     l.tok = take((size_t)few * 4);
     l.grad = take(grads ? n * piece * 2 : 0);
     l.acc = take(grads && piece < (size_t)V ? n * (size_t)H * 4 : 0);
-    l.db = take(grads && bias ? n / 64 * piece * 4 : 0);
+    l.db = take(grads && bias ? n / 32 * piece * 4 : 0);
     l.end = at;
     return l;
 }
@@ -273,6 +273,7 @@ int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t 
     a.dwstride = grad_weight_row_stride;
     a.db = grad_bias_out;
     a.count = reinterpret_cast<int32_t *>(ws + l.count);
+    a.scale = reinterpret_cast<float *>(ws + l.count) + 1;
     a.place = reinterpret_cast<int32_t *>(ws + l.place);
     a.rows = reinterpret_cast<int32_t *>(ws + l.rows);
     a.tokens = reinterpret_cast<int64_t *>(ws + l.tokens);

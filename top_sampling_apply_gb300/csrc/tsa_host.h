@@ -299,6 +299,7 @@ struct XentArgs {
     int64_t dhstride, dwstride;
     float *db;               // [V] or NULL
     // workspace; "c": of the rows that count, one after another
+    float *scale;            // [1]: the largest row weight, which G is without
     int32_t *count, *place, *rows;  // [1], [M]: a row's place or -1, [M]: a place's row
     int64_t *tokens;
     float *weight_c, *row_loss_c, *logprob_c, *lse_c;
@@ -311,6 +312,7 @@ struct XentArgs {
 __host__ __device__ inline int64_t xent_padded(int64_t M) { return M < 1 ? 128 : (M + 127) / 128 * 128; }
 constexpr int64_t kXentMaxRows = 1 << 20;
 int64_t xent_piece(int64_t M, int64_t V);
+unsigned int *xent_status_ptr();
 int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t st);
 
 int selftest_launch(uint32_t limit_us, cudaStream_t st);

@@ -25,8 +25,10 @@ namespace {
 // multiple of 128 get a weight of 0 and no target.
 __global__ void __launch_bounds__(1024) xent_rows_kernel(const XentArgs a) {
     __shared__ int s_warp[32], s_base;
+    __shared__ uint32_t s_top;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) s_base = 0;
+    if (threadIdx.x == 0) s_base = 0, s_top = 0;
+    uint32_t top = 0;
     __syncthreads();
     for (int64_t m0 = 0; m0 < a.M; m0 += 1024) {
         const int64_t m = m0 + threadIdx.x;
@@ -37,6 +39,7 @@ __global__ void __launch_bounds__(1024) xent_rows_kernel(const XentArgs a) {
             if (a.row_weight) w = a.row_weight[m];
         }
         const bool live = t >= 0 && t < a.V && w != 0.f;
+        if (live) top = max(top, __float_as_uint(fabsf(w)));
         const uint32_t vote = __ballot_sync(0xFFFFFFFFu, live);
         if (lane == 0) s_warp[warp] = __popc(vote);
         __syncthreads();
@@ -64,8 +67,14 @@ __global__ void __launch_bounds__(1024) xent_rows_kernel(const XentArgs a) {
         }
         __syncthreads();
     }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (lane == 0) atomicMax(&s_top, top);
+    __syncthreads();
     const int n = s_base;
-    if (threadIdx.x == 0) a.count[0] = n;
+    if (threadIdx.x == 0) {
+        a.count[0] = n;
+        a.scale[0] = n < 1 ? 1.f : a.row_weight ? __uint_as_float(s_top) : 1.f / (float)n;
+    }
     const int64_t pad = xent_padded(a.M);
     for (int64_t i = threadIdx.x; i < pad; i += 1024) {
         if (i >= n) {
@@ -114,128 +123,573 @@ __global__ void __launch_bounds__(256) xent_finish_kernel(const XentArgs a) {
     a.row_loss_c[i] = loss;
     a.row_loss[a.rows[i]] = loss;
     a.lse[a.rows[i]] = l;
-    a.coef[i] = make_float4(c != 0.f ? w * fmaf(2.f * c, l, 1.f) : w, w, l, 0.f);
+    const float part = a.row_weight ? w / a.scale[0] : 1.f;
+    a.coef[i] = make_float4(c != 0.f ? part * fmaf(2.f * c, l, 1.f) : part, part, l, 0.f);
 }
 
-__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+__device__ unsigned int g_xent_status;
 
-// 64 x 64 outputs of sum_k A(m, k) B(n, k) a CTA of 256 threads, both from any
-// strides; 4 x 4 outputs a thread.
-struct Operand {
-    const uint16_t *p;
-    int64_t row, col, rows;  // strides of m (or n) and k; rows beyond `rows` are 0
+__device__ __forceinline__ bool xent_wait(uint64_t *bar, uint32_t parity) {
+    return mbar_wait_bounded(bar, parity, &g_xent_status);
+}
+__device__ __forceinline__ bool xent_warp_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, xent_wait(bar, parity));
+}
+
+// The rows that the products go over: those that count, up to whole tiles.
+__device__ __forceinline__ int32_t xent_end(const XentArgs &a) {
+    const int32_t n = a.count[0];
+    return n < 1 ? 128 : (n + 127) / 128 * 128;
+}
+
+// Both kernels are one persistent CTA an SM in the form of lm_head_logprob's
+// products: warp 0 fetches tiles of 64 K columns by TMA into a ring of stages,
+// warp 1 issues the products of 128 x N tiles, warps 2 to 9 take finished sums
+// from one half of tensor memory while the next tile's products fill the other
+// half: four warps for each quarter of the lanes, half of the columns each.
+// Results leave through 4 KB of shared memory a warp and TMA, so that
+// whole lines are written.
+constexpr int kXentThreads = 320;
+constexpr int kXentSlab = 32 * 128;  // 32 rows of 64 bf16
+
+template <int N>
+struct XentShape {
+    static constexpr int A_BYTES = 128 * kTcK * 2, B_BYTES = N * kTcK * 2, STAGE = A_BYTES + B_BYTES;
+    static constexpr int STAGES = N == 256 ? 4 : 6;
+    static constexpr int SMEM = STAGES * STAGE + 8 * kXentSlab + 1024;
+    static constexpr int NC = N / 2;  // a thread's columns
+    static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N / 8) << 17) | (8u << 24);
+    static constexpr uint32_t A_ACROSS = 1u << 15, B_ACROSS = 1u << 16;  // M or N contiguous instead of K
 };
-__device__ __forceinline__ void tile_64(const Operand &A, const Operand &B, int64_t m0, int64_t n0, int64_t K,
-                                        float (&acc)[4][4]) {
-    __shared__ float sa[16][65], sb[16][65];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int64_t k0 = 0; k0 < K; k0 += 16) {
-        for (int i = threadIdx.x; i < 1024; i += 256) {
-            // along whichever of the two is contiguous
-            const int ra = A.col == 1 ? i >> 4 : i & 63, ka = A.col == 1 ? i & 15 : i >> 6;
-            const int rb = B.col == 1 ? i >> 4 : i & 63, kb = B.col == 1 ? i & 15 : i >> 6;
-            sa[ka][ra] = m0 + ra < A.rows && k0 + ka < K ? bf(A.p[(m0 + ra) * A.row + (k0 + ka) * A.col]) : 0.f;
-            sb[kb][rb] = n0 + rb < B.rows && k0 + kb < K ? bf(B.p[(n0 + rb) * B.row + (k0 + kb) * B.col]) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx + 16 * j], acc[i][j]);
-        __syncthreads();
-    }
-}
 
-__global__ void __launch_bounds__(256) xent_scores_kernel(const XentArgs a, int64_t v0, int64_t width) {
-    __shared__ float s_col[16][64];
-    const int n = a.count[0], tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t m0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-    const int64_t end = n < 1 ? 128 : ((int64_t)n + 127) / 128 * 128;
-    if (m0 >= end) return;
-    float z[4][4] = {};
-    tile_64({a.hidden_c, a.H, 1, end}, {a.weight, a.wstride, 1, a.V}, m0, v0 + c0, a.H, z);
-    float col[4] = {};
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + ty * 4 + i;
-        const float4 k = a.coef[m];
-        const int64_t t = a.tokens[m] - v0;
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = c0 + tx + 16 * j, v = v0 + c;
-            float g = 0.f;
-            if (c < width && v < a.V && m < n) {
-                float x = z[i][j] + (a.bias ? a.bias[v] : 0.f), slope = 1.f;
-                if (a.cap > 0.f) {
-                    const float y = tanhf(x / a.cap);
-                    x = a.cap * y;
-                    slope = 1.f - y * y;
-                }
-                x = fmaxf(x, -INFINITY);
-                g = (k.x * expf(x - k.z) - (c == t ? k.y : 0.f)) * slope;
-            }
-            col[j] += g;
-            if (c < width) a.grad[m * width + c] = __bfloat16_as_ushort(__float2bfloat16_rn(g));
+template <int STAGES>
+struct XentBars {
+    uint64_t full[STAGES], empty[STAGES], done[2], drained[2], last;
+    uint32_t tmem;
+};
+template <int STAGES>
+__device__ __forceinline__ void xent_setup(XentBars<STAGES> &s, uint32_t cols) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.done[i], 1);
+            mbar_init(&s.drained[i], 256);
+        }
+        mbar_init(&s.last, 1);
+        mbar_init_fence();
     }
-    if (!a.db) return;
-    for (int j = 0; j < 4; ++j) s_col[ty][tx + 16 * j] = col[j];
+    if ((threadIdx.x >> 5) == 1) tmem_alloc(&s.tmem, cols);
+    mma_fence_before();
     __syncthreads();
-    if (threadIdx.x < 64 && c0 + threadIdx.x < width) {
-        float s = 0.f;
-        for (int i = 0; i < 16; ++i) s += s_col[i][threadIdx.x];
-        a.db_part[(m0 / 64) * width + c0 + threadIdx.x] = s;
+    mma_fence_after();
+}
+
+// A thread's 64 results in bf16 as its row of the warp's slab, with the
+// 128-byte swizzle of the maps that they are stored through.
+__device__ __forceinline__ void slab_row(uint8_t *slab, int lane, const float *x) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * q + 2 * i], x[8 * q + 2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(slab + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
     }
 }
-
-__global__ void __launch_bounds__(256) xent_bias_kernel(const XentArgs a, int64_t v0, int64_t width) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= width || v0 + c >= a.V) return;
-    const int n = a.count[0];
-    float s = 0.f;
-    for (int64_t p = 0; p * 64 < n; ++p) s += a.db_part[p * width + c];
-    a.db[v0 + c] = s;
+__device__ __forceinline__ void slab_store(const CUtensorMap *map, uint8_t *slab, int lane, int32_t x, int32_t y) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tma_store(map, slab, x, y);
+}
+__device__ __forceinline__ void slab_wait(int lane) {
+    if (lane == 0) tma_store_read();
+    __syncwarp();
 }
 
-// z = 0: a piece's dW; 1: its part of dH.
-__global__ void __launch_bounds__(256) xent_products_kernel(const XentArgs a, int64_t v0, int64_t width, int dh) {
-    const int n = a.count[0], tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t m0 = (int64_t)blockIdx.y * 64, h0 = (int64_t)blockIdx.x * 64;
-    const int64_t end = n < 1 ? 128 : ((int64_t)n + 127) / 128 * 128;
-    const int64_t last = v0 + width < a.V ? v0 + width : a.V;
-    float z[4][4] = {};
-    if (dh) {
-        if (m0 >= n) return;
-        tile_64({a.grad, width, 1, end}, {a.weight + v0 * a.wstride, 1, a.wstride, a.H}, m0, h0, last - v0, z);
+// Sums over the warp's lanes of 32 values a lane: lane i gets the sum of the
+// i-th (31 exchanges instead of 5 for each).
+__device__ __forceinline__ float lane_sums(float (&x)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+            const float keep = up ? x[j + o] : x[j], send = up ? x[j] : x[j + o];
+            x[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+        }
+    }
+    return x[0];
+}
+
+// Scores of a tile once more (the same products and sums as in the first pass,
+// in chunks of 1,024 columns), and from them a piece's part of G.  Lanes are
+// rows; tiles go through the rows first.
+constexpr int kXentChunk = 1024 / kTcK;
+
+template <int N>
+__global__ void __launch_bounds__(kXentThreads, 1) xent_scores_kernel(const __grid_constant__ CUtensorMap map_h,
+                                                                      const __grid_constant__ CUtensorMap map_w,
+                                                                      const __grid_constant__ CUtensorMap map_g,
+                                                                      const XentArgs a, int64_t v0, int32_t width) {
+    using S = XentShape<N>;
+    constexpr int STAGES = S::STAGES, NC = S::NC;
+    extern __shared__ uint8_t raw[];
+    __shared__ XentBars<STAGES> s;
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kblocks = (int)((a.H + kTcK - 1) / kTcK);
+    const int32_t row_blocks = xent_end(a) / 128;
+    const int32_t left = (int32_t)(a.V - v0 < width ? a.V - v0 : width);  // the piece's entries
+    const int32_t tiles = row_blocks * (width / N);
+    xent_setup(s, 2 * N);
+    const uint32_t tmem = s.tmem;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const int32_t ya = t % row_blocks * 128, yb = t / row_blocks * N;
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const uint32_t i = it % STAGES;
+                    if (!xent_wait(&s.empty[i], ((it / STAGES) & 1u) ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = ring + (size_t)i * S::STAGE;
+                    mbar_arrive_expect_tx(&s.full[i], S::STAGE);
+                    tma_tile(st, &map_h, kb * kTcK, ya, &s.full[i]);
+                    tma_tile(st + S::A_BYTES, &map_w, kb * kTcK, yb, &s.full[i]);
+                }
+            }
+            // no copy may land, and no commit arrive, after the CTA is gone
+            const uint32_t k = it < STAGES ? it : STAGES;
+            for (uint32_t i = it - k; i < it; ++i)
+                xent_wait(ok ? &s.empty[i % STAGES] : &s.full[i % STAGES], (i / STAGES) & 1u);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0, j = 0;
+            bool ok = true;
+            for (int32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const uint32_t b = j & 1u, i = it % STAGES;
+                    if (kb % kXentChunk == 0) {
+                        if (!xent_wait(&s.drained[b], ((j >> 1) & 1u) ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        mma_fence_after();
+                    }
+                    if (!xent_wait(&s.full[i], (it / STAGES) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    mma_fence_after();
+                    const uint8_t *st = ring + (size_t)i * S::STAGE;
+                    const uint64_t da = smem_tile(st), db = smem_tile(st + S::A_BYTES);
+#pragma unroll
+                    for (int k = 0; k < kTcK / 16; ++k)
+                        mma_bf16(tmem + b * N, da + 2 * k, db + 2 * k, S::IDESC, kb % kXentChunk > 0 || k > 0);
+                    mma_commit(&s.empty[i]);
+                    if (kb % kXentChunk == kXentChunk - 1 || kb == kblocks - 1) {
+                        mma_commit(&s.done[b]);
+                        ++j;
+                    }
+                }
+            }
+            mma_commit(&s.last);  // the products are finished before tensor memory is freed
+            xent_wait(&s.last, 0);
+        }
     } else {
-        tile_64({a.grad, 1, width, width}, {a.hidden_c, 1, a.H, a.H}, m0, h0, end, z);
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i, h = h0 + tx + 16 * j;
-            if (h >= a.H) continue;
-            if (!dh) {
-                if (v0 + m < last && m < width)
-                    a.dw[(v0 + m) * a.dwstride + h] = __bfloat16_as_ushort(__float2bfloat16_rn(z[i][j]));
-            } else if (m < n) {
-                float s = z[i][j];
-                if (v0 > 0) s += a.acc[m * a.H + h];
-                if (last < a.V)
-                    a.acc[m * a.H + h] = s;
-                else
-                    a.dh[a.rows[m] * a.dhstride + h] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t at = tmem + ((uint32_t)quarter << 21) + half * NC;
+        const Cap cap = make_cap(a.cap);
+        const int chunks = (kblocks + kXentChunk - 1) / kXentChunk;
+        uint8_t *slab = ring + (size_t)STAGES * S::STAGE + (warp - 2) * kXentSlab;
+        uint32_t j = 0;
+        bool ok = true;
+        for (int32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            const int32_t first = t % row_blocks * 128 + quarter * 32;  // the warp's rows
+            const int32_t c0 = t / row_blocks * N + half * NC;          // and columns in the piece
+            const float4 k = a.coef[first + lane];
+            const int64_t want = a.tokens[first + lane] - v0 - c0;
+            float z[NC];
+            for (int c = 0; c < chunks; ++c, ++j) {
+                const uint32_t b = j & 1u;
+                ok = ok && xent_warp_wait(&s.done[b], (j >> 1) & 1u);
+                if (!ok) break;
+                mma_fence_after();
+#pragma unroll
+                for (int q = 0; q < NC; q += 16) {
+                    uint32_t r[16];
+                    __syncwarp();
+                    TmemLoad<16>::ld(at + b * N + q, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        if (c == 0) {
+                            z[q + i] = __uint_as_float(r[i]);
+                            z[q + i + 1] = __uint_as_float(r[i + 1]);
+                        } else {
+                            split_pair(add2(pair_of(z[q + i], z[q + i + 1]),
+                                            pair_of(__uint_as_float(r[i]), __uint_as_float(r[i + 1]))),
+                                       z[q + i], z[q + i + 1]);
+                        }
+                    }
+                }
+                mma_fence_before();
+                mbar_arrive(&s.drained[b]);
+            }
+            if (!ok) break;
+            if (a.bias) {  // the warp's entries, by way of its slab
+                slab_wait(lane);
+                float *bias = reinterpret_cast<float *>(slab);
+#pragma unroll
+                for (int i = 0; i < NC; i += 32)
+                    bias[i + lane] = c0 + i + lane < left ? __ldg(a.bias + v0 + c0 + i + lane) : 0.f;
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < NC; q += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(bias + q);
+                    split_pair(add2(pair_of(z[q], z[q + 1]), pair_of(f.x, f.y)), z[q], z[q + 1]);
+                    split_pair(add2(pair_of(z[q + 2], z[q + 3]), pair_of(f.z, f.w)), z[q + 2], z[q + 3]);
+                }
+                __syncwarp();
+            }
+            const float neg = -k.z * kLog2eH;
+#pragma unroll
+            for (int g0 = 0; g0 < NC; g0 += 64) {
+#pragma unroll
+                for (int h0 = 0; h0 < 64; h0 += 32) {
+                    float *x = z + g0 + h0;
+                    if (a.cap > 0.f) soft_cap<32>(x, cap);
+                    const int32_t in = left - (c0 + g0 + h0);
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {
+                        const float y = fmaxf(x[q], -INFINITY);  // NaN counts as -inf
+                        float p = k.x * ex2_approx(fmaf(y, kLog2eH, neg));
+                        if (want - (g0 + h0) == q) p -= k.y;
+                        if (a.cap > 0.f) {  // (a score of NaN has no slope)
+                            const float share = y * cap.inv;
+                            p = y > -INFINITY ? p * fmaf(-share, share, 1.f) : 0.f;
+                        }
+                        x[q] = q < in ? p : 0.f;
+                    }
+                    if (a.db) {
+                        float col[32];
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) col[q] = x[q];
+                        const float sum = lane_sums(col, lane);
+                        a.db_part[(int64_t)(first / 32) * width + c0 + g0 + h0 + lane] = sum;
+                    }
+                }
+                slab_wait(lane);
+                slab_row(slab, lane, z + g0);
+                slab_store(&map_g, slab, lane, c0 + g0, first);
             }
         }
+        if (lane == 0) tma_store_done();
+    }
+    __syncthreads();
+    if (warp == 1) tmem_free(tmem, 2 * N);
+}
+
+// db of a piece: 32 columns a CTA, the rows' parts over 32 rows of threads.
+__global__ void __launch_bounds__(1024) xent_bias_kernel(const XentArgs a, int64_t v0, int32_t width) {
+    __shared__ float sh[32][33];
+    const int32_t c = blockIdx.x * 32 + threadIdx.x, parts = xent_end(a) / 32;
+    float s = 0.f;
+    if (c < width)
+        for (int32_t p = threadIdx.y; p < parts; p += 32) s += a.db_part[(int64_t)p * width + c];
+    sh[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    s = warp_sum_f32(sh[threadIdx.x][threadIdx.y]);  // column threadIdx.y
+    const int64_t v = v0 + blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && v < a.V && v < v0 + width) a.db[v] = s * a.scale[0];
+}
+
+// The two products of a piece of G, as units of 128 x 256 results:
+//     dW[v, h] = sum_m G[m, v] H[m, h],  dH[m, h] (+)= sum_v G[m, v] W[v, h],
+// G without the largest row weight, which the results are multiplied by: rounded
+// to bf16 with it, weights that are all the same (a mean's 1 / n) would shift
+// every gradient by one and the same share, of up to 2^-9.
+// G, H and W are taken as they lie: the operands of dW, and W, have K across
+// their rows, which the tensor cores read just as well.  A CTA first takes its
+// share of the dH units (long K: a piece of the vocabulary), then a run of the
+// dW units whose length evens out what the first left uneven.  dH is added up
+// over the pieces in fp32, each unit by the one CTA that holds it.
+struct XentUnits {
+    int32_t hb, dh, dw, kh, kw;  // column blocks; dH and dW units; their K steps
+    int32_t w0, w1;              // this CTA's dW units
+    __device__ __forceinline__ void plan(const XentArgs &a, int32_t left, int32_t end) {
+        hb = (int32_t)((a.H + 255) / 256);
+        dh = a.dh ? end / 128 * hb : 0;
+        dw = a.dw ? (left + 127) / 128 * hb : 0;
+        kh = (left + kTcK - 1) / kTcK;
+        kw = end / kTcK;
+        // the first `more` CTAs have a dH unit more, and `fewer` dW units each
+        const int64_t ctas = gridDim.x, b = blockIdx.x, cost = kw + 4;  // a unit's results take about four steps
+        const int64_t more = dh % ctas;
+        int64_t fewer = 0;
+        if (more > 0) {
+            fewer = (((int64_t)dh * kh + (int64_t)dw * cost) / ctas - (dh / ctas + 1) * kh) / cost;
+            if (fewer < 0) fewer = 0;
+            if (fewer > dw / ctas) fewer = dw / ctas;
+        }
+        const int64_t rest = dw - more * fewer;
+        if (b < more) {
+            w0 = (int32_t)(b * fewer);
+            w1 = (int32_t)(w0 + fewer);
+        } else {
+            w0 = (int32_t)(more * fewer + (b - more) * rest / (ctas - more));
+            w1 = (int32_t)(more * fewer + (b - more + 1) * rest / (ctas - more));
+        }
+    }
+    // This CTA's i-th unit: whether it has one, of which kind, and its number.
+    __device__ __forceinline__ bool get(int32_t i, bool &is_dh, int32_t &u) const {
+        const int32_t b = blockIdx.x, ctas = gridDim.x;
+        const int32_t own = b < dh % ctas ? dh / ctas + 1 : dh / ctas;
+        is_dh = i < own;
+        u = is_dh ? b + i * ctas : w0 + i - own;
+        return is_dh || u < w1;
+    }
+};
+
+// Sums of 8,192 K in tensor memory at most: longer ones would feel that the
+// tensor cores cut what they add (512 steps: under 2^-14 of the sum).
+constexpr int kXentLong = 8192 / kTcK;
+
+__global__ void __launch_bounds__(kXentThreads, 1)
+    xent_products_kernel(const __grid_constant__ CUtensorMap map_gk, const __grid_constant__ CUtensorMap map_gm,
+                         const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
+                         const __grid_constant__ CUtensorMap map_dw, const XentArgs a, int64_t v0, int32_t width) {
+    using S = XentShape<256>;
+    constexpr int STAGES = S::STAGES, NC = S::NC, BOX = 64 * 128;
+    extern __shared__ uint8_t raw[];
+    __shared__ XentBars<STAGES> s;
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t n = a.count[0], end = xent_end(a);
+    const float scale = a.scale[0];
+    const int32_t left = (int32_t)(a.V - v0 < width ? a.V - v0 : width);
+    XentUnits units;
+    units.plan(a, left, end);
+    xent_setup(s, 512);
+    const uint32_t tmem = s.tmem;
+    bool is_dh;
+    int32_t u;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int32_t x = 0; ok && units.get(x, is_dh, u); ++x) {
+                // dH: row blocks first, so that the CTAs share the columns of W
+                const int32_t ya = is_dh ? u % (end / 128) * 128 : u / units.hb * 128;
+                const int32_t xb = (is_dh ? u / (end / 128) : u % units.hb) * 256;
+                const int ks = is_dh ? units.kh : units.kw;
+                for (int kb = 0; kb < ks; ++kb, ++it) {
+                    const uint32_t i = it % STAGES;
+                    if (!xent_wait(&s.empty[i], ((it / STAGES) & 1u) ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = ring + (size_t)i * S::STAGE;
+                    mbar_arrive_expect_tx(&s.full[i], S::STAGE);
+                    if (is_dh) {
+                        tma_tile(st, &map_gk, kb * kTcK, ya, &s.full[i]);
+                    } else {
+                        tma_tile(st, &map_gm, ya, kb * kTcK, &s.full[i]);
+                        tma_tile(st + BOX, &map_gm, ya + 64, kb * kTcK, &s.full[i]);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        tma_tile(st + S::A_BYTES + q * BOX, is_dh ? &map_w : &map_h, xb + 64 * q, kb * kTcK, &s.full[i]);
+                }
+            }
+            const uint32_t k = it < STAGES ? it : STAGES;
+            for (uint32_t i = it - k; i < it; ++i)
+                xent_wait(ok ? &s.empty[i % STAGES] : &s.full[i % STAGES], (i / STAGES) & 1u);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0, j = 0;
+            bool ok = true;
+            for (int32_t x = 0; ok && units.get(x, is_dh, u); ++x) {
+                const int ks = is_dh ? units.kh : units.kw;
+                const uint32_t idesc = S::IDESC | S::B_ACROSS | (is_dh ? 0u : S::A_ACROSS);
+                for (int kb = 0; kb < ks; ++kb, ++it) {
+                    const uint32_t b = j & 1u, i = it % STAGES;
+                    if (kb % kXentLong == 0) {
+                        if (!xent_wait(&s.drained[b], ((j >> 1) & 1u) ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        mma_fence_after();
+                    }
+                    if (!xent_wait(&s.full[i], (it / STAGES) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    mma_fence_after();
+                    const uint8_t *st = ring + (size_t)i * S::STAGE;
+                    const uint64_t da = is_dh ? smem_tile(st) : smem_tile_across(st, BOX);
+                    const uint64_t db = smem_tile_across(st + S::A_BYTES, BOX);
+                    const uint32_t step = is_dh ? 2 : 128;
+#pragma unroll
+                    for (int k = 0; k < kTcK / 16; ++k)
+                        mma_bf16(tmem + b * 256, da + step * k, db + 128 * k, idesc, kb % kXentLong > 0 || k > 0);
+                    mma_commit(&s.empty[i]);
+                    if (kb % kXentLong == kXentLong - 1 || kb == ks - 1) {
+                        mma_commit(&s.done[b]);
+                        ++j;
+                    }
+                }
+            }
+            mma_commit(&s.last);
+            xent_wait(&s.last, 0);
+        }
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t at = tmem + ((uint32_t)quarter << 21) + half * NC;
+        uint8_t *slab = ring + (size_t)STAGES * S::STAGE + (warp - 2) * kXentSlab;
+        uint32_t j = 0;
+        bool ok = true;
+        for (int32_t x = 0; ok && units.get(x, is_dh, u); ++x) {
+            const int32_t y0 = (is_dh ? u % (end / 128) : u / units.hb) * 128 + quarter * 32;
+            const int32_t h0 = (is_dh ? u / (end / 128) : u % units.hb) * 256 + half * NC;
+            const int chunks = ((is_dh ? units.kh : units.kw) + kXentLong - 1) / kXentLong;
+            float z[NC];
+            for (int c = 0; c < chunks; ++c, ++j) {
+                const uint32_t b = j & 1u;
+                ok = ok && xent_warp_wait(&s.done[b], (j >> 1) & 1u);
+                if (!ok) break;
+                mma_fence_after();
+#pragma unroll
+                for (int q = 0; q < NC; q += 16) {
+                    uint32_t r[16];
+                    __syncwarp();
+                    TmemLoad<16>::ld(at + b * 256 + q, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[q + i] = (c == 0 ? 0.f : z[q + i]) + __uint_as_float(r[i]);
+                }
+                mma_fence_before();
+                mbar_arrive(&s.drained[b]);
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int q = 0; q < NC; ++q) z[q] *= scale;
+            if (!is_dh) {
+#pragma unroll
+                for (int g = 0; g < NC; g += 64) {
+                    if (h0 + g >= a.H || y0 >= left) break;
+                    slab_wait(lane);
+                    slab_row(slab, lane, z + g);
+                    slab_store(&map_dw, slab, lane, h0 + g, y0);
+                }
+                continue;
+            }
+            const int32_t m = y0 + lane;
+            if (m >= n) continue;
+            float *acc = a.acc + (int64_t)m * a.H + h0;
+            uint16_t *to = a.dh + (int64_t)a.rows[m] * a.dhstride + h0;
+            const bool last = v0 + left >= a.V;
+#pragma unroll
+            for (int q = 0; q < NC; q += 8) {
+                if (h0 + q >= a.H) break;  // H is a multiple of 8
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = z[q + i];
+                if (v0 > 0) {
+                    const float4 p = *reinterpret_cast<const float4 *>(acc + q), r = *reinterpret_cast<const float4 *>(acc + q + 4);
+                    y[0] += p.x, y[1] += p.y, y[2] += p.z, y[3] += p.w, y[4] += r.x, y[5] += r.y, y[6] += r.z, y[7] += r.w;
+                }
+                if (last) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+                        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    *reinterpret_cast<uint4 *>(to + q) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    *reinterpret_cast<float4 *>(acc + q) = make_float4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<float4 *>(acc + q + 4) = make_float4(y[4], y[5], y[6], y[7]);
+                }
+            }
+        }
+        if (lane == 0) tma_store_done();
+    }
+    __syncthreads();
+    if (warp == 1) tmem_free(tmem, 512);
 }
 
 }  // namespace
 
-// A piece of the vocabulary: its part of G takes at most 128 MB.
+// Pieces of the vocabulary of one size: a piece's part of G takes about 64 MB,
+// half of L2, so that the products find much of it there.
 int64_t xent_piece(int64_t M, int64_t V) {
-    const int64_t most = (V + 255) / 256 * 256;
-    const int64_t fit = ((int64_t)128 << 20) / (2 * xent_padded(M)) / 256 * 256;
-    return fit < 256 ? 256 : fit < most ? fit : most;
+    const int64_t fit = ((int64_t)64 << 20) / (2 * xent_padded(M)) / 256 * 256;
+    const int64_t most = fit < 256 ? 256 : fit;
+    const int64_t pieces = (V + most - 1) / most;
+    return ((V + pieces - 1) / pieces + 255) / 256 * 256;
 }
+
+unsigned int *xent_status_ptr() {
+    void *p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_xent_status) != cudaSuccess) return nullptr;
+    return reinterpret_cast<unsigned int *>(p);
+}
+
+namespace {
+
+template <int N>
+int launch_scores(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_t st) {
+    using S = XentShape<N>;
+    const void *fn = reinterpret_cast<const void *>(&xent_scores_kernel<N>);
+    const int64_t pad = xent_padded(args.M), left = args.V - v0 < piece ? args.V - v0 : piece;
+    CUtensorMap mh, mw, mg;
+    if (!make_map(&mh, args.hidden_c, args.H, pad, args.H, 128) ||
+        !make_map(&mw, args.weight + v0 * args.wstride, args.H, left, args.wstride, N) ||
+        !make_map(&mg, args.grad, piece, pad, piece, 32) || prepare_kernel(fn, S::SMEM, 1) != 0)
+        return -1;
+    XentArgs a = args;
+    int32_t width = (int32_t)piece;
+    const int64_t tiles = pad / 128 * (piece / N), sms = sm_count();
+    void *params[] = {&mh, &mw, &mg, &a, &v0, &width};
+    return cudaLaunchKernel(fn, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kXentThreads), params, S::SMEM, st) ==
+                   cudaSuccess
+               ? 0
+               : -1;
+}
+
+int launch_products(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_t st) {
+    using S = XentShape<256>;
+    const void *fn = reinterpret_cast<const void *>(&xent_products_kernel);
+    const int64_t pad = xent_padded(args.M), left = args.V - v0 < piece ? args.V - v0 : piece;
+    CUtensorMap gk, gm, mw, mh, dw;
+    if (!make_map(&gk, args.grad, piece, pad, piece, 128) || !make_map(&gm, args.grad, piece, pad, piece, 64) ||
+        !make_map(&mw, args.weight + v0 * args.wstride, args.H, left, args.wstride, 64) ||
+        !make_map(&mh, args.hidden_c, args.H, pad, args.H, 64) ||
+        !make_map(&dw, args.dw ? args.dw + v0 * args.dwstride : args.hidden_c, args.H, args.dw ? left : pad,
+                  args.dw ? args.dwstride : args.H, 32) ||
+        prepare_kernel(fn, S::SMEM, 1) != 0)
+        return -1;
+    XentArgs a = args;
+    int32_t width = (int32_t)piece;
+    void *params[] = {&gk, &gm, &mw, &mh, &dw, &a, &v0, &width};
+    return cudaLaunchKernel(fn, dim3((unsigned)sm_count()), dim3(kXentThreads), params, S::SMEM, st) == cudaSuccess ? 0
+                                                                                                                   : -1;
+}
+
+}  // namespace
 
 int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t st) {
     const XentArgs &a = args;
@@ -259,12 +713,13 @@ int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t 
     if (!a.dh && !a.dw && !a.db) return 0;
     const int64_t piece = xent_piece(a.M, a.V);
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
-        const unsigned rows = (unsigned)(pad / 64), cols = (unsigned)(piece / 64), width = (unsigned)((a.H + 63) / 64);
-        xent_scores_kernel<<<dim3(cols, rows), 256, 0, st>>>(a, v0, piece);
-        if (a.db) xent_bias_kernel<<<(unsigned)((piece + 255) / 256), 256, 0, st>>>(a, v0, piece);
-        if (a.dh) xent_products_kernel<<<dim3(width, rows), 256, 0, st>>>(a, v0, piece, 1);
-        if (a.dw) xent_products_kernel<<<dim3(width, cols), 256, 0, st>>>(a, v0, piece, 0);
-        if (cudaGetLastError() != cudaSuccess) return -1;
+        // one block of rows: smaller tiles spread the vocabulary more evenly
+        if ((pad == 128 ? launch_scores<128>(a, v0, piece, st) : launch_scores<256>(a, v0, piece, st)) != 0) return -1;
+        if (a.db) {
+            xent_bias_kernel<<<(unsigned)((piece + 31) / 32), dim3(32, 32), 0, st>>>(a, v0, (int32_t)piece);
+            if (cudaGetLastError() != cudaSuccess) return -1;
+        }
+        if ((a.dh || a.dw) && launch_products(a, v0, piece, st) != 0) return -1;
     }
     return 0;
 }
