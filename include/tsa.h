@@ -553,7 +553,7 @@ int tsa_lm_head_int8(const int8_t *hidden, int64_t M, int64_t H, int64_t hidden_
  *   row_loss = l - z[target] + z_loss l^2,  loss = sum over rows of row_weight row_loss
  *   G[m, v]  = row_weight ((1 + 2 z_loss l) exp(z_v - l) - 1{v = target}) (1 - (z_v / softcap)^2)
  *   grad_hidden = G . weight,  grad_weight = G^T . hidden,  grad_bias = sum over rows of G
- *   hidden, weight, bias, softcap: as for lm_head_logprob; M <= 2^20
+ *   hidden, weight, bias, softcap: as for lm_head_logprob; M <= 2^16
  *   targets      [M] int64; a target outside [0, V) skips its row
  *   row_weight   [M] float or NULL: 1 / (number of rows that count); 0 skips a row
  *   z_loss       finite (TSA_ERR_VALUE); 0 leaves its term out

@@ -59,7 +59,8 @@ XentLayout xent_layout(int64_t M, int64_t H, int64_t V, bool grads, bool bias) {
     l.part = take((size_t)lm_logprob_parts(few, V) * (size_t)few * sizeof(float2));
     l.tok = take((size_t)few * 4);
     l.grad = take(grads ? n * piece * 2 : 0);
-    l.acc = take(grads && piece < (size_t)V ? n * (size_t)H * 4 : 0);
+    const int splits = xent_splits(M, H, V);
+    l.acc = take(grads && (piece < (size_t)V || splits > 1) ? (size_t)splits * n * (size_t)H * 4 : 0);
     l.db = take(grads && bias ? n / 32 * piece * 4 : 0);
     l.end = at;
     return l;
@@ -285,6 +286,8 @@ int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t 
     a.hidden_c = reinterpret_cast<uint16_t *>(ws + l.hidden);
     a.grad = reinterpret_cast<uint16_t *>(ws + l.grad);
     a.acc = reinterpret_cast<float *>(ws + l.acc);
+    a.padded = xent_padded(M);
+    a.splits = xent_splits(M, H, V);
     a.db_part = reinterpret_cast<float *>(ws + l.db);
     LmLogprobArgs p = {};  // the scores' first pass, over the rows that count
     p.hidden = a.hidden_c;

@@ -306,12 +306,15 @@ struct XentArgs {
     float4 *coef;            // what a place's gradient needs
     uint16_t *hidden_c;      // [padded, H]
     uint16_t *grad;          // [padded, piece]: a piece of the vocabulary's part of G
-    float *acc;              // [padded, H]: dH so far
+    float *acc;              // [splits][padded, H]: dH so far
+    int64_t padded;
+    int splits;
     float *db_part;
 };
 __host__ __device__ inline int64_t xent_padded(int64_t M) { return M < 1 ? 128 : (M + 127) / 128 * 128; }
-constexpr int64_t kXentMaxRows = 1 << 20;
+constexpr int64_t kXentMaxRows = 1 << 16, kXentMaxPiece = 1 << 16;
 int64_t xent_piece(int64_t M, int64_t V);
+int xent_splits(int64_t M, int64_t H, int64_t V);
 unsigned int *xent_status_ptr();
 int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t st);
 

@@ -187,6 +187,11 @@ __device__ __forceinline__ void xent_setup(XentBars<STAGES> &s, uint32_t cols) {
     mma_fence_after();
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // A thread's 64 results in bf16 as its row of the warp's slab, with the
 // 128-byte swizzle of the maps that they are stored through.
 __device__ __forceinline__ void slab_row(uint8_t *slab, int lane, const float *x) {
@@ -194,10 +199,7 @@ __device__ __forceinline__ void slab_row(uint8_t *slab, int lane, const float *x
     for (int q = 0; q < 8; ++q) {
         uint32_t u[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * q + 2 * i], x[8 * q + 2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
+        for (int i = 0; i < 4; ++i) u[i] = pack_bf16(x[8 * q + 2 * i], x[8 * q + 2 * i + 1]);
         *reinterpret_cast<uint4 *>(slab + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
     }
 }
@@ -421,17 +423,19 @@ __global__ void __launch_bounds__(1024) xent_bias_kernel(const XentArgs a, int64
 // every gradient by one and the same share, of up to 2^-9.
 // G, H and W are taken as they lie: the operands of dW, and W, have K across
 // their rows, which the tensor cores read just as well.  A CTA first takes its
-// share of the dH units (long K: a piece of the vocabulary), then a run of the
-// dW units whose length evens out what the first left uneven.  dH is added up
-// over the pieces in fp32, each unit by the one CTA that holds it.
+// share of the dH units (long K: a piece of the vocabulary, or a part of it),
+// then a run of the dW units whose length evens out what the first left uneven.
+// dH is added up over the pieces in fp32, each unit by the one CTA that holds it.
 struct XentUnits {
-    int32_t hb, dh, dw, kh, kw;  // column blocks; dH and dW units; their K steps
-    int32_t w0, w1;              // this CTA's dW units
+    int32_t rb, hb, dh, dw, all, kh, kw;  // row and column blocks; dH and dW units; K steps of a piece and of a unit each
+    int32_t w0, w1;                       // this CTA's dW units
     __device__ __forceinline__ void plan(const XentArgs &a, int32_t left, int32_t end) {
+        rb = end / 128;
         hb = (int32_t)((a.H + 255) / 256);
-        dh = a.dh ? end / 128 * hb : 0;
+        dh = a.dh ? rb * hb * a.splits : 0;
         dw = a.dw ? (left + 127) / 128 * hb : 0;
-        kh = (left + kTcK - 1) / kTcK;
+        all = (left + kTcK - 1) / kTcK;
+        kh = (all + a.splits - 1) / a.splits;
         kw = end / kTcK;
         // the first `more` CTAs have a dH unit more, and `fewer` dW units each
         const int64_t ctas = gridDim.x, b = blockIdx.x, cost = kw + 4;  // a unit's results take about four steps
@@ -451,20 +455,56 @@ struct XentUnits {
             w1 = (int32_t)(more * fewer + (b - more + 1) * rest / (ctas - more));
         }
     }
-    // This CTA's i-th unit: whether it has one, of which kind, and its number.
-    __device__ __forceinline__ bool get(int32_t i, bool &is_dh, int32_t &u) const {
+    // This CTA's i-th unit, if it has one: its kind, its first row (of dH or dW)
+    // and column, its first K step and their number.  dH units go through the
+    // row blocks first, so that the CTAs share columns of W.
+    struct Unit {
+        bool is_dh;
+        int32_t y, x, split, k0, ks;
+    };
+    __device__ __forceinline__ bool get(int32_t i, Unit &u) const {
         const int32_t b = blockIdx.x, ctas = gridDim.x;
         const int32_t own = b < dh % ctas ? dh / ctas + 1 : dh / ctas;
-        is_dh = i < own;
-        u = is_dh ? b + i * ctas : w0 + i - own;
-        return is_dh || u < w1;
+        u.is_dh = i < own;
+        if (u.is_dh) {
+            const int32_t t = b + i * ctas, tile = t % (rb * hb);
+            u.split = t / (rb * hb);
+            u.y = tile % rb * 128;
+            u.x = tile / rb * 256;
+            u.k0 = u.split * kh;
+            u.ks = max(0, min(kh, all - u.k0));
+            return true;
+        }
+        const int32_t t = w0 + i - own;
+        u.y = t / hb * 128;
+        u.x = t % hb * 256;
+        u.split = u.k0 = 0;
+        u.ks = kw;
+        return t < w1;
     }
 };
 
-// Sums of 8,192 K in tensor memory at most: longer ones would feel that the
-// tensor cores cut what they add (512 steps: under 2^-14 of the sum).
-constexpr int kXentLong = 8192 / kTcK;
+// Eight results of dH: on top of those of earlier pieces, into the fp32 sums or
+// rounded to the gradient.
+__device__ __forceinline__ void dh_results(const float *z, float *acc, bool add, uint16_t *to) {
+    float4 p = make_float4(z[0], z[1], z[2], z[3]), r = make_float4(z[4], z[5], z[6], z[7]);
+    if (add) {
+        const float4 s = reinterpret_cast<const float4 *>(acc)[0], t = reinterpret_cast<const float4 *>(acc)[1];
+        p.x += s.x, p.y += s.y, p.z += s.z, p.w += s.w;
+        r.x += t.x, r.y += t.y, r.z += t.z, r.w += t.w;
+    }
+    if (!to) {
+        reinterpret_cast<float4 *>(acc)[0] = p;
+        reinterpret_cast<float4 *>(acc)[1] = r;
+        return;
+    }
+    *reinterpret_cast<uint4 *>(to) = make_uint4(pack_bf16(p.x, p.y), pack_bf16(p.z, p.w), pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
+}
 
+// A unit's sum stays in tensor memory from its first K to its last, 65,536 at
+// most (kXentMaxRows, and the width of a piece): the tensor cores cut what they
+// add, by 2^-24 of the sum on average a step of 16, which over 4,096 steps is
+// 2^-12 at most against the 2^-9 of the result's rounding.
 __global__ void __launch_bounds__(kXentThreads, 1)
     xent_products_kernel(const __grid_constant__ CUtensorMap map_gk, const __grid_constant__ CUtensorMap map_gm,
                          const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
@@ -482,19 +522,14 @@ __global__ void __launch_bounds__(kXentThreads, 1)
     units.plan(a, left, end);
     xent_setup(s, 512);
     const uint32_t tmem = s.tmem;
-    bool is_dh;
-    int32_t u;
+    XentUnits::Unit u;
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int32_t x = 0; ok && units.get(x, is_dh, u); ++x) {
-                // dH: row blocks first, so that the CTAs share the columns of W
-                const int32_t ya = is_dh ? u % (end / 128) * 128 : u / units.hb * 128;
-                const int32_t xb = (is_dh ? u / (end / 128) : u % units.hb) * 256;
-                const int ks = is_dh ? units.kh : units.kw;
-                for (int kb = 0; kb < ks; ++kb, ++it) {
+            for (int32_t x = 0; ok && units.get(x, u); ++x) {
+                for (int kb = u.k0; kb < u.k0 + u.ks; ++kb, ++it) {
                     const uint32_t i = it % STAGES;
                     if (!xent_wait(&s.empty[i], ((it / STAGES) & 1u) ^ 1u)) {
                         ok = false;
@@ -502,15 +537,15 @@ __global__ void __launch_bounds__(kXentThreads, 1)
                     }
                     uint8_t *st = ring + (size_t)i * S::STAGE;
                     mbar_arrive_expect_tx(&s.full[i], S::STAGE);
-                    if (is_dh) {
-                        tma_tile(st, &map_gk, kb * kTcK, ya, &s.full[i]);
+                    if (u.is_dh) {
+                        tma_tile(st, &map_gk, kb * kTcK, u.y, &s.full[i]);
                     } else {
-                        tma_tile(st, &map_gm, ya, kb * kTcK, &s.full[i]);
-                        tma_tile(st + BOX, &map_gm, ya + 64, kb * kTcK, &s.full[i]);
+                        tma_tile(st, &map_gm, u.y, kb * kTcK, &s.full[i]);
+                        tma_tile(st + BOX, &map_gm, u.y + 64, kb * kTcK, &s.full[i]);
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        tma_tile(st + S::A_BYTES + q * BOX, is_dh ? &map_w : &map_h, xb + 64 * q, kb * kTcK, &s.full[i]);
+                        tma_tile(st + S::A_BYTES + q * BOX, u.is_dh ? &map_w : &map_h, u.x + 64 * q, kb * kTcK, &s.full[i]);
                 }
             }
             const uint32_t k = it < STAGES ? it : STAGES;
@@ -521,12 +556,12 @@ __global__ void __launch_bounds__(kXentThreads, 1)
         if (lane == 0) {
             uint32_t it = 0, j = 0;
             bool ok = true;
-            for (int32_t x = 0; ok && units.get(x, is_dh, u); ++x) {
-                const int ks = is_dh ? units.kh : units.kw;
-                const uint32_t idesc = S::IDESC | S::B_ACROSS | (is_dh ? 0u : S::A_ACROSS);
+            for (int32_t x = 0; ok && units.get(x, u); ++x) {
+                const int ks = u.ks;
+                const uint32_t idesc = S::IDESC | S::B_ACROSS | (u.is_dh ? 0u : S::A_ACROSS);
                 for (int kb = 0; kb < ks; ++kb, ++it) {
                     const uint32_t b = j & 1u, i = it % STAGES;
-                    if (kb % kXentLong == 0) {
+                    if (kb == 0) {
                         if (!xent_wait(&s.drained[b], ((j >> 1) & 1u) ^ 1u)) {
                             ok = false;
                             break;
@@ -539,14 +574,14 @@ __global__ void __launch_bounds__(kXentThreads, 1)
                     }
                     mma_fence_after();
                     const uint8_t *st = ring + (size_t)i * S::STAGE;
-                    const uint64_t da = is_dh ? smem_tile(st) : smem_tile_across(st, BOX);
+                    const uint64_t da = u.is_dh ? smem_tile(st) : smem_tile_across(st, BOX);
                     const uint64_t db = smem_tile_across(st + S::A_BYTES, BOX);
-                    const uint32_t step = is_dh ? 2 : 128;
+                    const uint32_t step = u.is_dh ? 2 : 128;
 #pragma unroll
                     for (int k = 0; k < kTcK / 16; ++k)
-                        mma_bf16(tmem + b * 256, da + step * k, db + 128 * k, idesc, kb % kXentLong > 0 || k > 0);
+                        mma_bf16(tmem + b * 256, da + step * k, db + 128 * k, idesc, kb > 0 || k > 0);
                     mma_commit(&s.empty[i]);
-                    if (kb % kXentLong == kXentLong - 1 || kb == ks - 1) {
+                    if (kb == ks - 1) {
                         mma_commit(&s.done[b]);
                         ++j;
                     }
@@ -561,68 +596,46 @@ __global__ void __launch_bounds__(kXentThreads, 1)
         uint8_t *slab = ring + (size_t)STAGES * S::STAGE + (warp - 2) * kXentSlab;
         uint32_t j = 0;
         bool ok = true;
-        for (int32_t x = 0; ok && units.get(x, is_dh, u); ++x) {
-            const int32_t y0 = (is_dh ? u % (end / 128) : u / units.hb) * 128 + quarter * 32;
-            const int32_t h0 = (is_dh ? u / (end / 128) : u % units.hb) * 256 + half * NC;
-            const int chunks = ((is_dh ? units.kh : units.kw) + kXentLong - 1) / kXentLong;
-            float z[NC];
-            for (int c = 0; c < chunks; ++c, ++j) {
-                const uint32_t b = j & 1u;
-                ok = ok && xent_warp_wait(&s.done[b], (j >> 1) & 1u);
+        for (int32_t x = 0; ok && units.get(x, u); ++x) {
+            const int32_t y0 = u.y + quarter * 32, h0 = u.x + half * NC;
+            const uint32_t b = j & 1u;
+            if (u.ks > 0) {  // (a part of a short last piece may be empty)
+                ok = xent_warp_wait(&s.done[b], (j >> 1) & 1u);
                 if (!ok) break;
                 mma_fence_after();
-#pragma unroll
-                for (int q = 0; q < NC; q += 16) {
-                    uint32_t r[16];
-                    __syncwarp();
-                    TmemLoad<16>::ld(at + b * 256 + q, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) z[q + i] = (c == 0 ? 0.f : z[q + i]) + __uint_as_float(r[i]);
-                }
-                mma_fence_before();
-                mbar_arrive(&s.drained[b]);
-            }
-            if (!ok) break;
-#pragma unroll
-            for (int q = 0; q < NC; ++q) z[q] *= scale;
-            if (!is_dh) {
-#pragma unroll
-                for (int g = 0; g < NC; g += 64) {
-                    if (h0 + g >= a.H || y0 >= left) break;
-                    slab_wait(lane);
-                    slab_row(slab, lane, z + g);
-                    slab_store(&map_dw, slab, lane, h0 + g, y0);
-                }
-                continue;
+                ++j;
             }
             const int32_t m = y0 + lane;
-            if (m >= n) continue;
-            float *acc = a.acc + (int64_t)m * a.H + h0;
-            uint16_t *to = a.dh + (int64_t)a.rows[m] * a.dhstride + h0;
-            const bool last = v0 + left >= a.V;
+            const bool mine = u.is_dh && m < n, last = a.splits == 1 && v0 + left >= a.V;
+            float *acc = mine ? a.acc + ((int64_t)u.split * a.padded + m) * a.H + h0 : nullptr;
+            uint16_t *to = mine && last ? a.dh + (int64_t)a.rows[m] * a.dhstride + h0 : nullptr;
 #pragma unroll
-            for (int q = 0; q < NC; q += 8) {
-                if (h0 + q >= a.H) break;  // H is a multiple of 8
-                float y[8];
+            for (int g = 0; g < NC; g += 64) {
+                if (h0 + g >= a.H || (!u.is_dh && y0 >= left)) break;
+                float z[64];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = z[q + i];
-                if (v0 > 0) {
-                    const float4 p = *reinterpret_cast<const float4 *>(acc + q), r = *reinterpret_cast<const float4 *>(acc + q + 4);
-                    y[0] += p.x, y[1] += p.y, y[2] += p.z, y[3] += p.w, y[4] += r.x, y[5] += r.y, y[6] += r.z, y[7] += r.w;
+                for (int q = 0; q < 64; q += 16) {
+                    uint32_t r[16];
+                    __syncwarp();
+                    TmemLoad<16>::ld(at + b * 256 + g + q, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[q + i] = u.ks > 0 ? __uint_as_float(r[i]) * scale : 0.f;
                 }
-                if (last) {
-                    uint32_t w[4];
+                if (!u.is_dh) {
+                    slab_wait(lane);
+                    slab_row(slab, lane, z);
+                    slab_store(&map_dw, slab, lane, h0 + g, y0);
+                } else if (mine) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-                        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                    for (int q = 0; q < 64; q += 8) {
+                        if (h0 + g + q < a.H) dh_results(z + q, acc + g + q, v0 > 0, last ? to + g + q : nullptr);
                     }
-                    *reinterpret_cast<uint4 *>(to + q) = make_uint4(w[0], w[1], w[2], w[3]);
-                } else {
-                    *reinterpret_cast<float4 *>(acc + q) = make_float4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<float4 *>(acc + q + 4) = make_float4(y[4], y[5], y[6], y[7]);
                 }
+            }
+            if (u.ks > 0) {
+                mma_fence_before();
+                mbar_arrive(&s.drained[b]);
             }
         }
         if (lane == 0) tma_store_done();
@@ -631,13 +644,40 @@ __global__ void __launch_bounds__(kXentThreads, 1)
     if (warp == 1) tmem_free(tmem, 512);
 }
 
+// dH from the parts of a split K.
+__global__ void __launch_bounds__(128) xent_join_kernel(const XentArgs a) {
+    const int32_t m = blockIdx.x;
+    if (m >= a.count[0]) return;
+    const float *acc = a.acc + (int64_t)m * a.H;
+    uint16_t *to = a.dh + (int64_t)a.rows[m] * a.dhstride;
+    for (int64_t h = threadIdx.x * 4; h < a.H; h += 512) {
+        float4 s = *reinterpret_cast<const float4 *>(acc + h);
+        for (int i = 1; i < a.splits; ++i) {
+            const float4 p = *reinterpret_cast<const float4 *>(acc + (int64_t)i * a.padded * a.H + h);
+            s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+        }
+        *reinterpret_cast<uint2 *>(to + h) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    }
+}
+
 }  // namespace
+
+// Parts of the K of dH's units (a piece of the vocabulary): as many as keep a
+// unit under half of what an SM has to do, down to 16 steps.
+int xent_splits(int64_t M, int64_t H, int64_t V) {
+    const int64_t pad = xent_padded(M), piece = xent_piece(M, V), hb = (H + 255) / 256;
+    const int64_t left = piece < V ? piece : V, k = (left + kTcK - 1) / kTcK;
+    const int64_t steps = pad / 128 * hb * k + (left + 127) / 128 * hb * (pad / kTcK + 4);
+    const int64_t half = steps / 304 < 16 ? 16 : steps / 304;
+    const int64_t n = (k + half - 1) / half;
+    return (int)(n < 64 ? n : 64);
+}
 
 // Pieces of the vocabulary of one size: a piece's part of G takes about 64 MB,
 // half of L2, so that the products find much of it there.
 int64_t xent_piece(int64_t M, int64_t V) {
     const int64_t fit = ((int64_t)64 << 20) / (2 * xent_padded(M)) / 256 * 256;
-    const int64_t most = fit < 256 ? 256 : fit;
+    const int64_t most = fit < 256 ? 256 : fit < kXentMaxPiece ? fit : kXentMaxPiece;
     const int64_t pieces = (V + most - 1) / most;
     return ((V + pieces - 1) / pieces + 255) / 256 * 256;
 }
@@ -720,6 +760,10 @@ int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t 
             if (cudaGetLastError() != cudaSuccess) return -1;
         }
         if ((a.dh || a.dw) && launch_products(a, v0, piece, st) != 0) return -1;
+    }
+    if (a.dh && a.splits > 1) {
+        xent_join_kernel<<<(unsigned)a.M, 128, 0, st>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return -1;
     }
     return 0;
 }
