@@ -535,16 +535,19 @@ int tsa_quantize_rows(const void *x, tsa_dtype dtype, int64_t N, int64_t H, int6
  * hidden row and each vocabulary entry:
  *   out[m, v] = hidden_scale[m] weight_scale[v] sum_k hidden[m, k] weight[v, k]  (+ bias[v])
  * The integer sum is exact; the result is rounded to out_dtype from fp32.
- *   hidden       int8 [M, hidden_row_stride], weight int8 [V, weight_row_stride];
+ *   hidden       int8 [M, hidden_row_stride], M <= 2^20, weight int8 [V, weight_row_stride];
  *                H a multiple of 16, 16 <= H <= 16384, row strides multiples of
  *                16, both bases 16-byte aligned (TSA_ERR_ALIGN)
  *   hidden_scale [M], weight_scale [V] float; bias [V] float or NULL
  *   out          [M, out_row_stride] of out_dtype: the logits of sample and topk
+ *   workspace    at least tsa_lm_head_int8_workspace_bytes(M, H) bytes, 256-byte
+ *                aligned
  */
 int tsa_lm_head_int8(const int8_t *hidden, int64_t M, int64_t H, int64_t hidden_row_stride,
                      const float *hidden_scale, const int8_t *weight, int64_t V, int64_t weight_row_stride,
                      const float *weight_scale, const float *bias, void *out, tsa_dtype out_dtype,
-                     int64_t out_row_stride, void *stream);
+                     int64_t out_row_stride, void *workspace, size_t workspace_bytes, void *stream);
+size_t tsa_lm_head_int8_workspace_bytes(int64_t M, int64_t H);
 
 /*
  * lm_head_cross_entropy -- the cross entropy of scores that are never written,

@@ -83,21 +83,26 @@ def test_rms_norm_backward_validation(lib):
     assert back(lib, nws=need - 1) == S["TSA_ERR_WORKSPACE"]
 
 
-def int8(lib, h=FAKE, M=2, H=64, hs=64, hsc=FAKE, w=FAKE, V=100, wst=64, wsc=FAKE, b=None, out=OTHER, dt=2, os=100):
-    return lib.tsa_lm_head_int8(h, M, H, hs, hsc, w, V, wst, wsc, b, out, dt, os, None)
+def int8(lib, h=FAKE, M=2, H=64, hs=64, hsc=FAKE, w=FAKE, V=100, wst=64, wsc=FAKE, b=None, out=OTHER, dt=2, os=100,
+         ws=FAKE, nws=1 << 20):
+    return lib.tsa_lm_head_int8(h, M, H, hs, hsc, w, V, wst, wsc, b, out, dt, os, ws, nws, None)
 
 
 def test_lm_head_int8_validation(lib):
     assert int8(lib, dt=3) == S["TSA_ERR_DTYPE"]
-    for kw in ({"M": -1}, {"H": 8}, {"H": 24}, {"H": 16400, "hs": 16400, "wst": 16400}, {"V": 0}, {"hs": 48},
+    for kw in ({"M": -1}, {"M": (1 << 20) + 1}, {"H": 8}, {"H": 24}, {"H": 16400, "hs": 16400, "wst": 16400}, {"V": 0}, {"hs": 48},
                {"wst": 48}, {"os": 99}):
         assert int8(lib, **kw) == S["TSA_ERR_SHAPE"], kw
     for kw in ({"h": None}, {"w": None}, {"hsc": None}, {"wsc": None}, {"out": None}):
         assert int8(lib, **kw) == S["TSA_ERR_NULL"], kw
     for kw in ({"h": ODD8}, {"w": ODD8}, {"hs": 72}, {"wst": 72}, {"hsc": ODD2}, {"wsc": ODD2}, {"b": ODD2},
-               {"out": ODD1}, {"dt": 0, "out": ODD2}):
+               {"out": ODD1}, {"dt": 0, "out": ODD2}, {"ws": P(0x10010)}):
         assert int8(lib, **kw) == S["TSA_ERR_ALIGN"], kw
-    assert int8(lib, M=0, h=None, w=None, out=None) == S["TSA_OK"]
+    need = lib.tsa_lm_head_int8_workspace_bytes(2, 64)
+    assert need == 256 and lib.tsa_lm_head_int8_workspace_bytes(0, 64) == 0
+    assert int8(lib, ws=None) == S["TSA_ERR_WORKSPACE"]
+    assert int8(lib, nws=need - 1) == S["TSA_ERR_WORKSPACE"]
+    assert int8(lib, M=0, h=None, w=None, out=None, ws=None) == S["TSA_OK"]
 
 
 def xent(lib, h=FAKE, M=2, H=64, hs=64, w=FAKE, V=100, wst=64, b=None, cap=0.0, t=FAKE, rw=None, z=0.0, loss=FAKE,

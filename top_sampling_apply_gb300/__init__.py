@@ -87,7 +87,9 @@ def load_library(path: Optional[str] = None):
         lib.tsa_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
         lib.tsa_rms_norm_backward_workspace_bytes.restype = sz
         lib.tsa_quantize_rows.argtypes = [P, ci, i64, i64, i64, P, i64, P, P]
-        lib.tsa_lm_head_int8.argtypes = [P, i64, i64, i64, P, P, i64, i64, P, P, P, ci, i64, P]
+        lib.tsa_lm_head_int8.argtypes = [P, i64, i64, i64, P, P, i64, i64, P, P, P, ci, i64, P, sz, P]
+        lib.tsa_lm_head_int8_workspace_bytes.argtypes = [i64, i64]
+        lib.tsa_lm_head_int8_workspace_bytes.restype = sz
         f64 = ctypes.c_double
         lib.tsa_adamw_step.argtypes = [P, i64, ci, ci, i32, f64, f64, f64, f64, f64, i64, P, u64, u64, P]
         lib.tsa_adamw_state_values.argtypes = [P, i64, P, P, P]
@@ -845,8 +847,11 @@ def lm_head_int8(hidden: torch.Tensor, hidden_scale: torch.Tensor, weight: torch
         raise ValueError("dtype must be float32, float16 or bfloat16")
     z = torch.empty((M, V), dtype=dtype, device=hidden.device) if out is None else \
         _matrix(out, dev, (M, V), dtype, "out", "V")
+    nws = lib.tsa_lm_head_int8_workspace_bytes(M, H)
+    work = torch.empty(nws, dtype=torch.uint8, device=hidden.device) if nws else None
     _call(dev, lib.tsa_lm_head_int8, hidden.data_ptr(), M, H, hidden.stride(0), hs, weight.data_ptr(), V,
-          weight.stride(0), ws, b, z.data_ptr(), _DT[dtype], z.stride(0), _raw_stream(dev))
+          weight.stride(0), ws, b, z.data_ptr(), _DT[dtype], z.stride(0), None if work is None else work.data_ptr(),
+          nws, _raw_stream(dev))
     if out is not None:
         _written(out)
     return z

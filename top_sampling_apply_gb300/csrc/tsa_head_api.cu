@@ -183,11 +183,16 @@ int tsa_rms_norm_backward(const void *grad, int64_t grad_row_stride, const void 
     return norm_back_launch(a, dtype, (cudaStream_t)stream) == 0 ? TSA_OK : TSA_ERR_CUDA;
 }
 
+size_t tsa_lm_head_int8_workspace_bytes(int64_t M, int64_t H) {
+    return M < 1 || H < 1 ? 0 : align256((size_t)M * (size_t)H * 2);
+}
+
 int tsa_lm_head_int8(const int8_t *hidden, int64_t M, int64_t H, int64_t hidden_row_stride, const float *hidden_scale,
                      const int8_t *weight, int64_t V, int64_t weight_row_stride, const float *weight_scale,
-                     const float *bias, void *out, tsa_dtype out_dtype, int64_t out_row_stride, void *stream) {
+                     const float *bias, void *out, tsa_dtype out_dtype, int64_t out_row_stride, void *workspace,
+                     size_t workspace_bytes, void *stream) {
     if (out_dtype != TSA_F32 && out_dtype != TSA_F16 && out_dtype != TSA_BF16) return TSA_ERR_DTYPE;
-    if (M < 0 || M > 0x7FFFFFFFll || H < 16 || H > 16384 || H % 16 != 0 || V < 1 || V > tsa_max_vocab(out_dtype) ||
+    if (M < 0 || M > (1ll << 20) || H < 16 || H > 16384 || H % 16 != 0 || V < 1 || V > tsa_max_vocab(out_dtype) ||
         hidden_row_stride < H || weight_row_stride < H || out_row_stride < V)
         return TSA_ERR_SHAPE;
     if (M == 0) return TSA_OK;
@@ -196,7 +201,10 @@ int tsa_lm_head_int8(const int8_t *hidden, int64_t M, int64_t H, int64_t hidden_
         !aligned(hidden_scale, 4) || !aligned(weight_scale, 4) || !aligned(bias, 4) ||
         !aligned(out, out_dtype == TSA_F32 ? 4 : 2))
         return TSA_ERR_ALIGN;
+    if (!workspace || workspace_bytes < tsa_lm_head_int8_workspace_bytes(M, H)) return TSA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return TSA_ERR_ALIGN;
     Int8Args a = {};
+    a.half = static_cast<uint16_t *>(workspace);
     a.hidden = hidden;
     a.M = M;
     a.H = H;

@@ -281,7 +281,9 @@ struct Int8Args {
     void *out;             // [M, ostride] of dtype
     int64_t ostride;
     int dtype;
+    uint16_t *half;        // workspace: [M, H], the hidden rows in f16
 };
+unsigned int *int8_status_ptr();
 int int8_launch(const Int8Args &args, cudaStream_t st);
 
 // The cross entropy from the hidden rows, with its gradients.

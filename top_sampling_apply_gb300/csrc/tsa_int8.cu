@@ -2,6 +2,12 @@
 // each vocabulary entry:
 //     z[m, v] = hs[m] ws[v] sum_k h[m, k] w[v, k]  (+ b[v]),
 // the sum over integers exact.
+//
+// The tensor cores of this GPU have next to no rate for 8-bit integers, but
+// f16 holds every one of them exactly, and the fp32 sums of 1,024 of their
+// products, at most 2^24 of them, are exact too.  So the weight, which is what
+// there is most of, goes through memory in 8 bits and becomes f16 on the way
+// into tensor memory; sums of 1,024 columns are added up as integers in registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -9,53 +15,362 @@
 
 #include "tsa_device.cuh"
 #include "tsa_host.h"
+#include "tsa_tcgen05.cuh"
 
 namespace tsa {
 
 namespace {
 
-__device__ __forceinline__ void store_score(void *p, int64_t i, float x, int dtype) {
-    if (dtype == 0)
+__device__ unsigned int g_int8_status;
+
+__device__ __forceinline__ bool int8_wait(uint64_t *bar, uint32_t parity) {
+    return mbar_wait_bounded(bar, parity, &g_int8_status);
+}
+__device__ __forceinline__ bool int8_warp_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, int8_wait(bar, parity));
+}
+
+// D[128, N] += A[128, 16] B[N, 16]^T with A in tensor memory: a lane a row,
+// two f16 values a column.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t a, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Four 8-bit integers as f16.  An f16 of bits 0x6400 | u is 1024 + u for u
+// under 1024: with u = x + 128 what is left is to subtract 1152, exactly.
+__device__ __forceinline__ void to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = x ^ 0x80808080u;
+    const __half2 k = __half2half2(__ushort_as_half((unsigned short)0x6480));
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    __half2 p = __hsub2(*reinterpret_cast<__half2 *>(&a), k), q = __hsub2(*reinterpret_cast<__half2 *>(&b), k);
+    lo = *reinterpret_cast<uint32_t *>(&p);
+    hi = *reinterpret_cast<uint32_t *>(&q);
+}
+
+// The hidden rows in f16: 16 columns a thread.
+__global__ void __launch_bounds__(256) int8_hidden_kernel(const Int8Args a) {
+    pdl_launch_dependents();
+    const int64_t cols = a.H / 16, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.M * cols) return;
+    const int64_t m = i / cols, k = i % cols * 16;
+    const uint4 x = *reinterpret_cast<const uint4 *>(a.hidden + m * a.hstride + k);
+    uint4 y, z;
+    to_f16(x.x, y.x, y.y);
+    to_f16(x.y, y.z, y.w);
+    to_f16(x.z, z.x, z.y);
+    to_f16(x.w, z.z, z.w);
+    uint4 *out = reinterpret_cast<uint4 *>(a.half + m * a.H + k);
+    out[0] = y;
+    out[1] = z;
+}
+
+// One persistent CTA an SM.  Warp 0 fetches 128 columns of the weight's rows
+// (a lane of tensor memory each) and of N hidden rows by TMA into a ring of
+// stages; eight warps turn the weight's bytes into f16 in tensor memory, two
+// groups of four taking steps in turn; warp 1 issues the products of four such
+// slots; four or eight warps take finished sums from one half of the
+// accumulators while the next products fill the other half.
+//
+// Up to 128 hidden rows the kernel is a stream of the weight, and the vocabulary
+// is cut into one run of rows a CTA, a multiple of 32, so that every SM moves
+// the same bytes; a run's last tile copies only the rows that it needs.  With
+// more hidden rows tiles go through those first, so that a weight tile comes from
+// HBM once and from L2 for the other blocks.
+constexpr int kI8K = 128;              // columns of a stage
+constexpr int kI8Chunk = 1024 / kI8K;  // stages whose sums are exact
+constexpr int kI8Slots = 4;            // of the weight in tensor memory, 64 columns each
+
+template <int N>
+struct Int8Shape {
+    static constexpr int A_BYTES = 128 * kI8K, B_BYTES = N * kI8K * 2, STAGE = A_BYTES + B_BYTES;
+    static constexpr int STAGES = N <= 32 ? 8 : N == 64 ? 6 : 4;
+    static constexpr int SMEM = STAGES * STAGE + 1024;
+    static constexpr int EPI = N <= 32 ? 4 : 8;  // warps that take the sums
+    static constexpr int NC = N <= 32 ? N : N / 2;
+    static constexpr int THREADS = 64 + 256 + 32 * EPI;
+    static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(N / 8) << 17) | (8u << 24);  // f16, fp32 sums, M = 128
+};
+
+template <int DT>
+__device__ __forceinline__ void store_score(void *p, int64_t i, float x) {
+    if constexpr (DT == 0)
         static_cast<float *>(p)[i] = x;
-    else if (dtype == 1)
+    else if constexpr (DT == 1)
         static_cast<__half *>(p)[i] = __float2half_rn(x);
     else
         static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
 }
 
-// A warp a vocabulary entry, eight hidden rows at a time, 16 columns a lane.
-__global__ void __launch_bounds__(256) int8_scores_kernel(const Int8Args a) {
-    const int64_t v = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (v >= a.V) return;
-    for (int64_t m0 = (int64_t)blockIdx.y * 8; m0 < a.M; m0 += (int64_t)gridDim.y * 8) {
-        int acc[8] = {};
-        for (int64_t k = lane * 16; k < a.H; k += 512) {
-            const int4 w = *reinterpret_cast<const int4 *>(a.weight + v * a.wstride + k);
+template <int N, int DT>
+__global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
+    int8_scores_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
+                       const Int8Args a, int32_t row_blocks, int32_t tiles, int32_t run) {
+    using S = Int8Shape<N>;
+    constexpr int STAGES = S::STAGES, NC = S::NC;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[STAGES], empty[STAGES], a_full[kI8Slots], a_empty[kI8Slots], done[2], drained[2], last;
+    __shared__ uint32_t tmem_slot;
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int steps = (int)((a.H + kI8K - 1) / kI8K);
+    // run > 0: this CTA's vocabulary rows; else whole tiles, in turn
+    const int32_t V = (int32_t)a.V, v_first = run > 0 ? (int32_t)blockIdx.x * run : 0;
+    const int32_t v_end = run > 0 && v_first + run < V ? v_first + run : V;
+    const int32_t t_first = run > 0 ? 0 : blockIdx.x, t_step = run > 0 ? 1 : gridDim.x;
+    const int32_t t_end = run > 0 ? (v_end - v_first + 127) / 128 : tiles;
+    const auto tile_v = [&](int32_t t) { return run > 0 ? v_first + t * 128 : t / row_blocks * 128; };
+    const auto tile_m = [&](int32_t t) { return run > 0 ? 0 : t % row_blocks * N; };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kI8Slots; ++i) {
+            mbar_init(&a_full[i], 128);
+            mbar_init(&a_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&done[i], 1);
+            mbar_init(&drained[i], 32 * S::EPI);
+        }
+        mbar_init(&last, 1);
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc(&tmem_slot, 512);
+    mma_fence_before();
+    __syncthreads();
+    mma_fence_after();
+    const uint32_t tmem = tmem_slot, slots = tmem + 256;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            const auto weight = [&](uint32_t s, int32_t v, int k) {
+                const int groups = v_end - v >= 128 ? 4 : (v_end - v + 31) / 32;
+                mbar_arrive_expect_tx(&full[s], (uint32_t)(groups * (S::A_BYTES / 4) + S::B_BYTES));
+                for (int i = 0; i < groups; ++i)
+                    tma_tile(ring + (size_t)s * S::STAGE + i * (S::A_BYTES / 4), &map_w, k * kI8K, v + 32 * i, &full[s]);
+            };
+            const auto hidden = [&](uint32_t s, int32_t m, int k) {
+                uint8_t *st = ring + (size_t)s * S::STAGE + S::A_BYTES;
+                tma_tile(st, &map_h, k * kI8K, m, &full[s]);
+                tma_tile(st + S::B_BYTES / 2, &map_h, k * kI8K + 64, m, &full[s]);
+            };
+            // the weight does not wait for the kernel that makes the hidden rows
+            uint32_t ahead = 0;
+            for (int32_t t = t_first; t < t_end && ahead < STAGES; t += t_step)
+                for (int k = 0; k < steps && ahead < STAGES; ++k, ++ahead) weight(ahead, tile_v(t), k);
+            pdl_wait_primary();
+            for (int32_t t = t_first; ok && t < t_end; t += t_step) {
+                for (int k = 0; k < steps; ++k, ++it) {
+                    const uint32_t s = it % STAGES;
+                    if (it >= ahead) {
+                        if (!int8_wait(&empty[s], ((it / STAGES) & 1u) ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        weight(s, tile_v(t), k);
+                    }
+                    hidden(s, tile_m(t), k);
+                }
+            }
+            // no copy may land, and no commit arrive, after the CTA is gone
+            const uint32_t n = it < STAGES ? it : STAGES;
+            for (uint32_t i = it - n; i < it; ++i)
+                int8_wait(ok ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0, j = 0;
+            bool ok = true;
+            for (int32_t t = t_first; ok && t < t_end; t += t_step) {
+                for (int k = 0; k < steps; ++k, ++it) {
+                    const uint32_t b = j & 1u, s = it % STAGES, slot = it % kI8Slots;
+                    if (k % kI8Chunk == 0) {
+                        if (!int8_wait(&drained[b], ((j >> 1) & 1u) ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    // (the hidden rows have landed too: who filled the slot waited for the stage)
+                    if (!int8_wait(&a_full[slot], (it / kI8Slots) & 1u) || !int8_wait(&full[s], (it / STAGES) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    mma_fence_after();
+                    const uint8_t *st = ring + (size_t)s * S::STAGE + S::A_BYTES;
+                    const uint64_t d0 = smem_tile(st), d1 = smem_tile(st + S::B_BYTES / 2);
+                    const int parts = k + 1 < steps ? 8 : (int)(a.H - (int64_t)k * kI8K) / 16;
+                    for (int p = 0; p < parts; ++p)
+                        mma_f16_ts(tmem + b * 128, slots + slot * 64 + p * 8, (p < 4 ? d0 : d1) + 2 * (p & 3), S::IDESC,
+                                   k % kI8Chunk > 0 || p > 0);
+                    mma_commit(&empty[s]);
+                    mma_commit(&a_empty[slot]);
+                    if (k % kI8Chunk == kI8Chunk - 1 || k == steps - 1) {
+                        mma_commit(&done[b]);
+                        ++j;
+                    }
+                }
+            }
+            mma_commit(&last);  // the products are finished before tensor memory is freed
+            int8_wait(&last, 0);
+        }
+    } else if (warp < 10) {
+        const int quarter = warp & 3, group = (warp - 2) >> 2;
+        const uint32_t at = slots + ((uint32_t)quarter << 21);
+        const int row = quarter * 32 + lane;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int32_t t = t_first; ok && t < t_end; t += t_step) {
+            for (int k = 0; k < steps; ++k, ++it) {
+                if ((it & 1u) != (uint32_t)group) continue;
+                const uint32_t s = it % STAGES, slot = it % kI8Slots;
+                ok = int8_warp_wait(&full[s], (it / STAGES) & 1u) &&
+                     int8_warp_wait(&a_empty[slot], ((it / kI8Slots) & 1u) ^ 1u);
+                if (!ok) break;
+                mma_fence_after();
+                const uint8_t *src = ring + (size_t)s * S::STAGE + row * kI8K;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (m0 + i >= a.M) break;
-                const int4 h = *reinterpret_cast<const int4 *>(a.hidden + (m0 + i) * a.hstride + k);
-                acc[i] = __dp4a(w.x, h.x, __dp4a(w.y, h.y, __dp4a(w.z, h.z, __dp4a(w.w, h.w, acc[i]))));
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(src + (((h * 4 + c) ^ (row & 7)) << 4));
+                        to_f16(x.x, r[8 * c], r[8 * c + 1]);
+                        to_f16(x.y, r[8 * c + 2], r[8 * c + 3]);
+                        to_f16(x.z, r[8 * c + 4], r[8 * c + 5]);
+                        to_f16(x.w, r[8 * c + 6], r[8 * c + 7]);
+                    }
+                    __syncwarp();
+                    tmem_store(at + slot * 64 + h * 32, r);
+                }
+                tmem_wait_st();
+                mma_fence_before();
+                mbar_arrive(&a_full[slot]);
             }
         }
+    } else {
+        const int quarter = warp & 3, half = (warp - 10) >> 2;
+        const uint32_t at = tmem + ((uint32_t)quarter << 21) + half * NC;
+        const int chunks = (steps + kI8Chunk - 1) / kI8Chunk;
+        uint32_t j = 0;
+        bool ok = true;
+        for (int32_t t = t_first; ok && t < t_end; t += t_step) {
+            const int32_t v = tile_v(t) + quarter * 32 + lane, m0 = tile_m(t) + half * NC;
+            const bool in = v < v_end;
+            const float ws = in ? __ldg(a.wscale + v) : 0.f, bias = in && a.bias ? __ldg(a.bias + v) : 0.f;
+            int sum[NC];
+            for (int c = 0; c < chunks; ++c, ++j) {
+                const uint32_t b = j & 1u;
+                ok = int8_warp_wait(&done[b], (j >> 1) & 1u);
+                if (!ok) break;
+                mma_fence_after();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int s = __reduce_add_sync(0xFFFFFFFFu, acc[i]);
-            if (lane == i && m0 + i < a.M) {
-                const float z = (float)s * a.hscale[m0 + i] * a.wscale[v] + (a.bias ? a.bias[v] : 0.f);
-                store_score(a.out, (m0 + i) * a.ostride + v, z, a.dtype);
+                for (int q = 0; q < NC; q += 16) {
+                    uint32_t r[16];
+                    __syncwarp();
+                    TmemLoad<16>::ld(at + b * 128 + q, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum[q + i] = (c == 0 ? 0 : sum[q + i]) + __float2int_rn(__uint_as_float(r[i]));
+                }
+                mma_fence_before();
+                mbar_arrive(&drained[b]);
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int q = 0; q < NC; ++q) {
+                if (m0 + q >= a.M) break;
+                const float z = (float)sum[q] * __ldg(a.hscale + m0 + q) * ws + bias;
+                if (in) store_score<DT>(a.out, (m0 + q) * a.ostride + v, z);
             }
         }
     }
+    __syncthreads();
+    if (warp == 1) tmem_free(tmem, 512);
+}
+
+// 8-bit [rows, cols] in boxes of 128 columns by 32 rows, f16 [rows, cols] in
+// boxes of 64 columns.
+bool make_int8_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t stride) {
+    const EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride};
+    const cuuint32_t box[2] = {kI8K, 32}, step[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N, int DT>
+int launch_scores(const Int8Args &args, cudaStream_t st) {
+    using S = Int8Shape<N>;
+    const void *fn = reinterpret_cast<const void *>(&int8_scores_kernel<N, DT>);
+    CUtensorMap mw, mh;
+    if (!make_int8_map(&mw, args.weight, args.H, args.V, args.wstride) ||
+        !make_map(&mh, args.half, args.H, args.M, args.H, N) || prepare_kernel(fn, S::SMEM, 1) != 0)
+        return -1;
+    const int64_t sms = sm_count(), blocks = (args.M + N - 1) / N, all = blocks * ((args.V + 127) / 128);
+    const int64_t each = ((args.V + sms - 1) / sms + 31) / 32 * 32;
+    Int8Args a = args;
+    int32_t row_blocks = (int32_t)blocks, tiles = (int32_t)all, run = blocks == 1 ? (int32_t)each : 0;
+    const int64_t grid = run > 0 ? (args.V + run - 1) / run : all < sms ? all : sms;
+    void *params[] = {&mw, &mh, &a, &row_blocks, &tiles, &run};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(S::THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, params) == cudaSuccess ? 0 : -1;
+}
+template <int DT>
+int launch_rows(const Int8Args &a, cudaStream_t st) {
+    return a.M <= 16   ? launch_scores<16, DT>(a, st)
+           : a.M <= 32 ? launch_scores<32, DT>(a, st)
+           : a.M <= 64 ? launch_scores<64, DT>(a, st)
+                       : launch_scores<128, DT>(a, st);
 }
 
 }  // namespace
 
-int int8_launch(const Int8Args &a, cudaStream_t st) {
-    const int64_t y = (a.M + 7) / 8;
-    int8_scores_kernel<<<dim3((unsigned)((a.V + 7) / 8), (unsigned)(y < 65535 ? y : 65535)), 256, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+unsigned int *int8_status_ptr() {
+    void *p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_int8_status) != cudaSuccess) return nullptr;
+    return reinterpret_cast<unsigned int *>(p);
+}
+
+int int8_launch(const Int8Args &args, cudaStream_t st) {
+    Int8Args a = args;
+    void *params[] = {&a};
+    const int64_t threads = a.M * (a.H / 16);
+    if (cudaLaunchKernel(reinterpret_cast<const void *>(&int8_hidden_kernel), dim3((unsigned)((threads + 255) / 256)),
+                         dim3(256), params, 0, st) != cudaSuccess)
+        return -1;
+    return a.dtype == 0 ? launch_rows<0>(a, st) : a.dtype == 1 ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
 }
 
 }  // namespace tsa
