@@ -99,7 +99,7 @@ def test_lm_head_int8_validation(lib):
                {"out": ODD1}, {"dt": 0, "out": ODD2}, {"ws": P(0x10010)}):
         assert int8(lib, **kw) == S["TSA_ERR_ALIGN"], kw
     need = lib.tsa_lm_head_int8_workspace_bytes(2, 64)
-    assert need == 256 and lib.tsa_lm_head_int8_workspace_bytes(0, 64) == 0
+    assert need == 512 and lib.tsa_lm_head_int8_workspace_bytes(0, 64) == 0
     assert int8(lib, ws=None) == S["TSA_ERR_WORKSPACE"]
     assert int8(lib, nws=need - 1) == S["TSA_ERR_WORKSPACE"]
     assert int8(lib, M=0, h=None, w=None, out=None, ws=None) == S["TSA_OK"]

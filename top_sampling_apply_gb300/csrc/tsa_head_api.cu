@@ -184,7 +184,7 @@ int tsa_rms_norm_backward(const void *grad, int64_t grad_row_stride, const void 
 }
 
 size_t tsa_lm_head_int8_workspace_bytes(int64_t M, int64_t H) {
-    return M < 1 || H < 1 ? 0 : align256((size_t)M * (size_t)H * 2);
+    return M < 1 || H < 1 ? 0 : align256((size_t)M * (size_t)int8_padded(H) * 2);
 }
 
 int tsa_lm_head_int8(const int8_t *hidden, int64_t M, int64_t H, int64_t hidden_row_stride, const float *hidden_scale,

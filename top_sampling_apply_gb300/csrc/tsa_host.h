@@ -281,8 +281,10 @@ struct Int8Args {
     void *out;             // [M, ostride] of dtype
     int64_t ostride;
     int dtype;
-    uint16_t *half;        // workspace: [M, H], the hidden rows in f16
+    uint16_t *half;        // workspace: [M, int8_padded(H)], the hidden rows in f16
 };
+constexpr int kInt8Stage = 128;
+__host__ __device__ inline int64_t int8_padded(int64_t H) { return (H + kInt8Stage - 1) / kInt8Stage * kInt8Stage; }
 unsigned int *int8_status_ptr();
 int int8_launch(const Int8Args &args, cudaStream_t st);
 

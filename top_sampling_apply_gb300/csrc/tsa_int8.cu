@@ -31,12 +31,12 @@ __device__ __forceinline__ bool int8_warp_wait(uint64_t *bar, uint32_t parity) {
 }
 
 // D[128, N] += A[128, 16] B[N, 16]^T with A in tensor memory: a lane a row,
-// two f16 values a column.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+// two f16 values a column.  B's descriptor comes in its two halves.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 x, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], x, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 __device__ __forceinline__ void tmem_store(uint32_t a, const uint32_t (&r)[32]) {
@@ -63,19 +63,20 @@ __device__ __forceinline__ void to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
     hi = *reinterpret_cast<uint32_t *>(&q);
 }
 
-// The hidden rows in f16: 16 columns a thread.
+// The hidden rows in f16, their columns filled up to whole stages with zeros:
+// 16 columns a thread.
 __global__ void __launch_bounds__(256) int8_hidden_kernel(const Int8Args a) {
     pdl_launch_dependents();
-    const int64_t cols = a.H / 16, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t padded = int8_padded(a.H), cols = padded / 16, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= a.M * cols) return;
     const int64_t m = i / cols, k = i % cols * 16;
-    const uint4 x = *reinterpret_cast<const uint4 *>(a.hidden + m * a.hstride + k);
-    uint4 y, z;
+    uint4 x = make_uint4(0, 0, 0, 0), y, z;
+    if (k < a.H) x = *reinterpret_cast<const uint4 *>(a.hidden + m * a.hstride + k);
     to_f16(x.x, y.x, y.y);
     to_f16(x.y, y.z, y.w);
     to_f16(x.z, z.x, z.y);
     to_f16(x.w, z.z, z.w);
-    uint4 *out = reinterpret_cast<uint4 *>(a.half + m * a.H + k);
+    uint4 *out = reinterpret_cast<uint4 *>(a.half + m * padded + k);
     out[0] = y;
     out[1] = z;
 }
@@ -92,7 +93,12 @@ __global__ void __launch_bounds__(256) int8_hidden_kernel(const Int8Args a) {
 // the same bytes; a run's last tile copies only the rows that it needs.  With
 // more hidden rows tiles go through those first, so that a weight tile comes from
 // HBM once and from L2 for the other blocks.
-constexpr int kI8K = 128;              // columns of a stage
+//
+// A copy or product that one thread issues costs it some 100 cycles, and more
+// where its operands are not the same in the whole warp: whole tiles are one copy
+// each (six a stage had bound the kernel: 16 rows x 128,256 x 5,120 235 us), and
+// the two issuing warps go through their loops together.
+constexpr int kI8K = kInt8Stage;       // columns of a stage
 constexpr int kI8Chunk = 1024 / kI8K;  // stages whose sums are exact
 constexpr int kI8Slots = 4;            // of the weight in tensor memory, 64 columns each
 
@@ -119,15 +125,15 @@ __device__ __forceinline__ void store_score(void *p, int64_t i, float x) {
 
 template <int N, int DT>
 __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
-    int8_scores_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
-                       const Int8Args a, int32_t row_blocks, int32_t tiles, int32_t run) {
+    int8_scores_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_part,
+                       const __grid_constant__ CUtensorMap map_h, const Int8Args a, int32_t row_blocks, int32_t tiles, int32_t run) {
     using S = Int8Shape<N>;
     constexpr int STAGES = S::STAGES, NC = S::NC;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[STAGES], empty[STAGES], a_full[kI8Slots], a_empty[kI8Slots], done[2], drained[2], last;
     __shared__ uint32_t tmem_slot;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int steps = (int)((a.H + kI8K - 1) / kI8K);
     // run > 0: this CTA's vocabulary rows; else whole tiles, in turn
     const int32_t V = (int32_t)a.V, v_first = run > 0 ? (int32_t)blockIdx.x * run : 0;
@@ -159,79 +165,78 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
     const uint32_t tmem = tmem_slot, slots = tmem + 256;
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            const auto weight = [&](uint32_t s, int32_t v, int k) {
-                const int groups = v_end - v >= 128 ? 4 : (v_end - v + 31) / 32;
-                mbar_arrive_expect_tx(&full[s], (uint32_t)(groups * (S::A_BYTES / 4) + S::B_BYTES));
-                for (int i = 0; i < groups; ++i)
-                    tma_tile(ring + (size_t)s * S::STAGE + i * (S::A_BYTES / 4), &map_w, k * kI8K, v + 32 * i, &full[s]);
-            };
-            const auto hidden = [&](uint32_t s, int32_t m, int k) {
-                uint8_t *st = ring + (size_t)s * S::STAGE + S::A_BYTES;
-                tma_tile(st, &map_h, k * kI8K, m, &full[s]);
-                tma_tile(st + S::B_BYTES / 2, &map_h, k * kI8K + 64, m, &full[s]);
-            };
-            // the weight does not wait for the kernel that makes the hidden rows
-            uint32_t ahead = 0;
-            for (int32_t t = t_first; t < t_end && ahead < STAGES; t += t_step)
-                for (int k = 0; k < steps && ahead < STAGES; ++k, ++ahead) weight(ahead, tile_v(t), k);
-            pdl_wait_primary();
-            for (int32_t t = t_first; ok && t < t_end; t += t_step) {
-                for (int k = 0; k < steps; ++k, ++it) {
-                    const uint32_t s = it % STAGES;
-                    if (it >= ahead) {
-                        if (!int8_wait(&empty[s], ((it / STAGES) & 1u) ^ 1u)) {
-                            ok = false;
-                            break;
-                        }
-                        weight(s, tile_v(t), k);
-                    }
-                    hidden(s, tile_m(t), k);
+        uint32_t it = 0;
+        bool ok = true;
+        const auto weight = [&](uint32_t s, int32_t v, int k) {
+            uint8_t *st = ring + (size_t)s * S::STAGE;
+            const int32_t left = v_end - v;
+            if (lane == 0) {
+                if (left > 96) {
+                    mbar_arrive_expect_tx(&full[s], S::STAGE);
+                    tma_tile(st, &map_w, k * kI8K, v, &full[s]);
+                } else {
+                    const int groups = (left + 31) / 32;
+                    mbar_arrive_expect_tx(&full[s], (uint32_t)(groups * (S::A_BYTES / 4) + S::B_BYTES));
+                    for (int i = 0; i < groups; ++i)
+                        tma_tile(st + i * (S::A_BYTES / 4), &map_part, k * kI8K, v + 32 * i, &full[s]);
                 }
             }
-            // no copy may land, and no commit arrive, after the CTA is gone
-            const uint32_t n = it < STAGES ? it : STAGES;
-            for (uint32_t i = it - n; i < it; ++i)
-                int8_wait(ok ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u);
+        };
+        // the weight does not wait for the kernel that makes the hidden rows
+        uint32_t ahead = 0;
+        for (int32_t t = t_first; t < t_end && ahead < STAGES; t += t_step)
+            for (int k = 0; k < steps && ahead < STAGES; ++k, ++ahead) weight(ahead, tile_v(t), k);
+        pdl_wait_primary();
+        uint32_t s = 0, phase = 1;
+        for (int32_t t = t_first; ok && t < t_end; t += t_step) {
+            const int32_t v = tile_v(t), m = tile_m(t);
+            for (int k = 0; k < steps; ++k, ++it) {
+                if (it >= ahead) {
+                    ok = int8_warp_wait(&empty[s], phase);
+                    if (!ok) break;
+                    weight(s, v, k);
+                }
+                if (lane == 0) tma_tile_3d(ring + (size_t)s * S::STAGE + S::A_BYTES, &map_h, 0, m, 2 * k, &full[s]);
+                if (++s == STAGES) s = 0, phase ^= 1u;
+            }
         }
+        // no copy may land, and no commit arrive, after the CTA is gone
+        const uint32_t n = it < STAGES ? it : STAGES;
+        for (uint32_t i = it - n; i < it; ++i)
+            int8_warp_wait(ok ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u);
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0, j = 0;
-            bool ok = true;
-            for (int32_t t = t_first; ok && t < t_end; t += t_step) {
-                for (int k = 0; k < steps; ++k, ++it) {
-                    const uint32_t b = j & 1u, s = it % STAGES, slot = it % kI8Slots;
-                    if (k % kI8Chunk == 0) {
-                        if (!int8_wait(&drained[b], ((j >> 1) & 1u) ^ 1u)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                    // (the hidden rows have landed too: who filled the slot waited for the stage)
-                    if (!int8_wait(&a_full[slot], (it / kI8Slots) & 1u) || !int8_wait(&full[s], (it / STAGES) & 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    mma_fence_after();
-                    const uint8_t *st = ring + (size_t)s * S::STAGE + S::A_BYTES;
-                    const uint64_t d0 = smem_tile(st), d1 = smem_tile(st + S::B_BYTES / 2);
-                    const int parts = k + 1 < steps ? 8 : (int)(a.H - (int64_t)k * kI8K) / 16;
-                    for (int p = 0; p < parts; ++p)
-                        mma_f16_ts(tmem + b * 128, slots + slot * 64 + p * 8, (p < 4 ? d0 : d1) + 2 * (p & 3), S::IDESC,
+        uint32_t j = 0, s = 0, slot = 0, phase = 0;
+        const uint64_t desc = smem_tile(ring + S::A_BYTES);
+        const uint32_t lo = (uint32_t)desc, hi = (uint32_t)(desc >> 32);
+        bool ok = true;
+        for (int32_t t = t_first; ok && t < t_end; t += t_step) {
+            for (int k = 0; k < steps; ++k) {
+                const uint32_t b = j & 1u;
+                if (k % kI8Chunk == 0) ok = int8_warp_wait(&drained[b], ((j >> 1) & 1u) ^ 1u);
+                // (the hidden rows have landed too: who filled the slot waited for the stage)
+                ok = ok && int8_warp_wait(&a_full[slot], phase);
+                if (!ok) break;
+                mma_fence_after();
+                const uint32_t d = tmem + b * 128, sa = slots + slot * 64, sb = lo + s * (S::STAGE >> 4);
+                const bool end = k % kI8Chunk == kI8Chunk - 1 || k == steps - 1;
+                if (lane == 0) {
+#pragma unroll
+                    for (int p = 0; p < 8; ++p)
+                        mma_f16_ts(d, sa + p * 8, sb + (p >> 2) * (S::B_BYTES / 2 >> 4) + (p & 3) * 2, hi, S::IDESC,
                                    k % kI8Chunk > 0 || p > 0);
                     mma_commit(&empty[s]);
                     mma_commit(&a_empty[slot]);
-                    if (k % kI8Chunk == kI8Chunk - 1 || k == steps - 1) {
-                        mma_commit(&done[b]);
-                        ++j;
-                    }
+                    if (end) mma_commit(&done[b]);
                 }
+                __syncwarp();
+                if (end) ++j;
+                if (++s == STAGES) s = 0;
+                if (++slot == kI8Slots) slot = 0, phase ^= 1u;
             }
-            mma_commit(&last);  // the products are finished before tensor memory is freed
-            int8_wait(&last, 0);
         }
+        // the products are finished before tensor memory is freed
+        if (lane == 0) mma_commit(&last);
+        int8_warp_wait(&last, 0);
     } else if (warp < 10) {
         const int quarter = warp & 3, group = (warp - 2) >> 2;
         const uint32_t at = slots + ((uint32_t)quarter << 21);
@@ -308,14 +313,13 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
     if (warp == 1) tmem_free(tmem, 512);
 }
 
-// 8-bit [rows, cols] in boxes of 128 columns by 32 rows, f16 [rows, cols] in
-// boxes of 64 columns.
-bool make_int8_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t stride) {
+// 8-bit [rows, cols] in boxes of 128 columns.
+bool make_int8_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t stride, int box_rows) {
     const EncodeFn fn = encoder();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)stride};
-    const cuuint32_t box[2] = {kI8K, 32}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {kI8K, (cuuint32_t)box_rows}, step[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, step,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -325,16 +329,18 @@ template <int N, int DT>
 int launch_scores(const Int8Args &args, cudaStream_t st) {
     using S = Int8Shape<N>;
     const void *fn = reinterpret_cast<const void *>(&int8_scores_kernel<N, DT>);
-    CUtensorMap mw, mh;
-    if (!make_int8_map(&mw, args.weight, args.H, args.V, args.wstride) ||
-        !make_map(&mh, args.half, args.H, args.M, args.H, N) || prepare_kernel(fn, S::SMEM, 1) != 0)
+    CUtensorMap mw, mp, mh;
+    const int64_t padded = int8_padded(args.H);
+    if (!make_int8_map(&mw, args.weight, args.H, args.V, args.wstride, 128) ||
+        !make_int8_map(&mp, args.weight, args.H, args.V, args.wstride, 32) ||
+        !make_map_blocks(&mh, args.half, padded, args.M, padded, N, 2) || prepare_kernel(fn, S::SMEM, 1) != 0)
         return -1;
     const int64_t sms = sm_count(), blocks = (args.M + N - 1) / N, all = blocks * ((args.V + 127) / 128);
     const int64_t each = ((args.V + sms - 1) / sms + 31) / 32 * 32;
     Int8Args a = args;
     int32_t row_blocks = (int32_t)blocks, tiles = (int32_t)all, run = blocks == 1 ? (int32_t)each : 0;
     const int64_t grid = run > 0 ? (args.V + run - 1) / run : all < sms ? all : sms;
-    void *params[] = {&mw, &mh, &a, &row_blocks, &tiles, &run};
+    void *params[] = {&mw, &mp, &mh, &a, &row_blocks, &tiles, &run};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(S::THREADS);
@@ -366,7 +372,7 @@ unsigned int *int8_status_ptr() {
 int int8_launch(const Int8Args &args, cudaStream_t st) {
     Int8Args a = args;
     void *params[] = {&a};
-    const int64_t threads = a.M * (a.H / 16);
+    const int64_t threads = a.M * (int8_padded(a.H) / 16);
     if (cudaLaunchKernel(reinterpret_cast<const void *>(&int8_hidden_kernel), dim3((unsigned)((threads + 255) / 256)),
                          dim3(256), params, 0, st) != cudaSuccess)
         return -1;

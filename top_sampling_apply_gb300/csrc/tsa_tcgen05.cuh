@@ -152,6 +152,14 @@ __device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int3
         : "memory");
 }
 
+__device__ __forceinline__ void tma_tile_3d(void *dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // ------------------------------------------------------------ tensor maps
 constexpr int kTcK = 64;  // bf16 columns of a tile: 128 bytes
 
@@ -180,6 +188,20 @@ inline bool make_map(CUtensorMap *map, const void *base, int64_t cols, int64_t r
     const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
     const cuuint32_t box[2] = {kTcK, (cuuint32_t)box_rows}, step[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same seen as blocks of 64 columns, [cols / 64][rows][64], cols a multiple
+// of 64: a box is box_rows rows of `blocks` of them, one block after another.
+inline bool make_map_blocks(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t stride, int box_rows,
+                            int blocks) {
+    const EncodeFn fn = encoder();
+    if (!fn || cols % kTcK != 0) return false;
+    const cuuint64_t dims[3] = {kTcK, (cuuint64_t)rows, (cuuint64_t)(cols / kTcK)};
+    const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, kTcK * 2};
+    const cuuint32_t box[3] = {kTcK, (cuuint32_t)box_rows, (cuuint32_t)blocks}, step[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, step,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
