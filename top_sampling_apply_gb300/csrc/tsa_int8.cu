@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(256) int8_hidden_kernel(const Int8Args a) {
 // One persistent CTA an SM.  Warp 0 fetches 128 columns of the weight's rows
 // (a lane of tensor memory each) and of N hidden rows by TMA into a ring of
 // stages; eight warps turn the weight's bytes into f16 in tensor memory, two
-// groups of four taking steps in turn; warp 1 issues the products of four such
-// slots; four or eight warps take finished sums from one half of the
+// groups of four taking stages in turn (a stage's 64 columns of it are free when
+// the stage is); warp 1 issues the products; four or eight warps take finished sums from one half of the
 // accumulators while the next products fill the other half.
 //
 // Up to 128 hidden rows the kernel is a stream of the weight, and the vocabulary
@@ -100,12 +100,12 @@ __global__ void __launch_bounds__(256) int8_hidden_kernel(const Int8Args a) {
 // the two issuing warps go through their loops together.
 constexpr int kI8K = kInt8Stage;       // columns of a stage
 constexpr int kI8Chunk = 1024 / kI8K;  // stages whose sums are exact
-constexpr int kI8Slots = 4;            // of the weight in tensor memory, 64 columns each
 
 template <int N>
 struct Int8Shape {
     static constexpr int A_BYTES = 128 * kI8K, B_BYTES = N * kI8K * 2, STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = N <= 32 ? 8 : N == 64 ? 6 : 4;
+    static constexpr int STAGES = N <= 32 ? 7 : N == 64 ? 6 : 4;
+    static constexpr int SUMS = 512 - 64 * STAGES < 256 ? (512 - 64 * STAGES) / 2 : 128;  // columns of half the sums
     static constexpr int SMEM = STAGES * STAGE + 1024;
     static constexpr int EPI = N <= 32 ? 4 : 8;  // warps that take the sums
     static constexpr int NC = N <= 32 ? N : N / 2;
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
     using S = Int8Shape<N>;
     constexpr int STAGES = S::STAGES, NC = S::NC;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[STAGES], empty[STAGES], a_full[kI8Slots], a_empty[kI8Slots], done[2], drained[2], last;
+    __shared__ uint64_t full[STAGES], empty[STAGES], a_full[STAGES], done[2], drained[2], last;
     __shared__ uint32_t tmem_slot;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -146,10 +146,7 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < kI8Slots; ++i) {
             mbar_init(&a_full[i], 128);
-            mbar_init(&a_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&done[i], 1);
@@ -162,7 +159,7 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
     mma_fence_before();
     __syncthreads();
     mma_fence_after();
-    const uint32_t tmem = tmem_slot, slots = tmem + 256;
+    const uint32_t tmem = tmem_slot, slots = tmem + 512 - 64 * STAGES;
 
     if (warp == 0) {
         uint32_t it = 0;
@@ -205,37 +202,38 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
         for (uint32_t i = it - n; i < it; ++i)
             int8_warp_wait(ok ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u);
     } else if (warp == 1) {
-        uint32_t j = 0, s = 0, slot = 0, phase = 0;
+        uint32_t j = 0, s = 0, phase = 0;
         const uint64_t desc = smem_tile(ring + S::A_BYTES);
         const uint32_t lo = (uint32_t)desc, hi = (uint32_t)(desc >> 32);
-        bool ok = true;
+        bool ok = true, ready = false;
         for (int32_t t = t_first; ok && t < t_end; t += t_step) {
             for (int k = 0; k < steps; ++k) {
                 const uint32_t b = j & 1u;
                 if (k % kI8Chunk == 0) ok = int8_warp_wait(&drained[b], ((j >> 1) & 1u) ^ 1u);
                 // (the hidden rows have landed too: who filled the slot waited for the stage)
-                ok = ok && int8_warp_wait(&a_full[slot], phase);
+                ok = ok && (ready || int8_warp_wait(&a_full[s], phase));
                 if (!ok) break;
                 mma_fence_after();
-                const uint32_t d = tmem + b * 128, sa = slots + slot * 64, sb = lo + s * (S::STAGE >> 4);
+                // a look at the next step, whose answer comes while this one's products are issued
+                const uint32_t s1 = s + 1 == STAGES ? 0 : s + 1, phase1 = s1 == 0 ? phase ^ 1u : phase;
+                const bool seen = mbar_test_wait(&a_full[s1], phase1);
+                const uint32_t d = tmem + b * S::SUMS, sa = slots + s * 64, sb = lo + s * (S::STAGE >> 4);
                 const bool end = k % kI8Chunk == kI8Chunk - 1 || k == steps - 1;
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int p = 0; p < 8; ++p)
                         mma_f16_ts(d, sa + p * 8, sb + (p >> 2) * (S::B_BYTES / 2 >> 4) + (p & 3) * 2, hi, S::IDESC,
                                    k % kI8Chunk > 0 || p > 0);
                     mma_commit(&empty[s]);
-                    mma_commit(&a_empty[slot]);
                     if (end) mma_commit(&done[b]);
                 }
-                __syncwarp();
+                ready = __all_sync(0xFFFFFFFFu, seen);
                 if (end) ++j;
-                if (++s == STAGES) s = 0;
-                if (++slot == kI8Slots) slot = 0, phase ^= 1u;
+                s = s1, phase = phase1;
             }
         }
         // the products are finished before tensor memory is freed
-        if (lane == 0) mma_commit(&last);
+        if (elect_one()) mma_commit(&last);
         int8_warp_wait(&last, 0);
     } else if (warp < 10) {
         const int quarter = warp & 3, group = (warp - 2) >> 2;
@@ -245,10 +243,11 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
         bool ok = true;
         for (int32_t t = t_first; ok && t < t_end; t += t_step) {
             for (int k = 0; k < steps; ++k, ++it) {
-                if ((it & 1u) != (uint32_t)group) continue;
-                const uint32_t s = it % STAGES, slot = it % kI8Slots;
-                ok = int8_warp_wait(&full[s], (it / STAGES) & 1u) &&
-                     int8_warp_wait(&a_empty[slot], ((it / kI8Slots) & 1u) ^ 1u);
+                // By the stage, not the step: a group has to see every phase of a barrier that it waits for.  (A
+                // wait for a phase passes while the one before it is open.)
+                const uint32_t s = it % STAGES;
+                if ((s & 1u) != (uint32_t)group) continue;
+                ok = int8_warp_wait(&full[s], (it / STAGES) & 1u);
                 if (!ok) break;
                 mma_fence_after();
                 const uint8_t *src = ring + (size_t)s * S::STAGE + row * kI8K;
@@ -264,11 +263,11 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
                         to_f16(x.w, r[8 * c + 6], r[8 * c + 7]);
                     }
                     __syncwarp();
-                    tmem_store(at + slot * 64 + h * 32, r);
+                    tmem_store(at + s * 64 + h * 32, r);
                 }
                 tmem_wait_st();
                 mma_fence_before();
-                mbar_arrive(&a_full[slot]);
+                mbar_arrive(&a_full[s]);
             }
         }
     } else {
@@ -291,7 +290,7 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
                 for (int q = 0; q < NC; q += 16) {
                     uint32_t r[16];
                     __syncwarp();
-                    TmemLoad<16>::ld(at + b * 128 + q, r);
+                    TmemLoad<16>::ld(at + b * S::SUMS + q, r);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
