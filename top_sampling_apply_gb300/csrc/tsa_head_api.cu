@@ -55,7 +55,7 @@ XentLayout xent_layout(int64_t M, int64_t H, int64_t V, bool grads, bool bias) {
     l.logprob = take(n * 4);
     l.lse = take(n * 4);
     l.coef = take(n * 16);
-    l.hidden = take(n * (size_t)H * 2);
+    l.hidden = take(n * (size_t)xent_width(H) * 2);
     l.part = take((size_t)lm_logprob_parts(few, V) * (size_t)few * sizeof(float2));
     l.tok = take((size_t)few * 4);
     l.grad = take(grads ? n * piece * 2 : 0);
@@ -300,7 +300,7 @@ int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t 
     LmLogprobArgs p = {};  // the scores' first pass, over the rows that count
     p.hidden = a.hidden_c;
     p.H = H;
-    p.hstride = H;
+    p.hstride = xent_width(H);
     p.weight = a.weight;
     p.V = V;
     p.wstride = weight_row_stride;

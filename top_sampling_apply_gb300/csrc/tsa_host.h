@@ -308,7 +308,7 @@ struct XentArgs {
     int64_t *tokens;
     float *weight_c, *row_loss_c, *logprob_c, *lse_c;
     float4 *coef;            // what a place's gradient needs
-    uint16_t *hidden_c;      // [padded, H]
+    uint16_t *hidden_c;      // [padded, xent_width(H)]
     uint16_t *grad;          // [padded, piece]: a piece of the vocabulary's part of G
     float *acc;              // [splits][padded, H]: dH so far
     int64_t padded;
@@ -316,6 +316,7 @@ struct XentArgs {
     float *db_part;
 };
 __host__ __device__ inline int64_t xent_padded(int64_t M) { return M < 1 ? 128 : (M + 127) / 128 * 128; }
+__host__ __device__ inline int64_t xent_width(int64_t H) { return (H + 63) / 64 * 64; }
 constexpr int64_t kXentMaxRows = 1 << 16, kXentMaxPiece = 1 << 16;
 int64_t xent_piece(int64_t M, int64_t V);
 int xent_splits(int64_t M, int64_t H, int64_t V);

@@ -87,22 +87,24 @@ __global__ void __launch_bounds__(1024) xent_rows_kernel(const XentArgs a) {
     }
 }
 
-// The rows that count, one after another; zeros up to a multiple of 128 of
-// them (128 at least), and in the outputs of skipped rows.
+// The rows that count, one after another, each filled up to whole tiles of
+// columns with zeros; zeros up to a multiple of 128 rows (128 at least), and in
+// the outputs of skipped rows.
 __global__ void __launch_bounds__(128) xent_gather_kernel(const XentArgs a) {
-    const int64_t b = blockIdx.x, vecs = a.H / 8;
+    const int64_t b = blockIdx.x, vecs = a.H / 8, wide = xent_width(a.H) / 8;
     const int n = a.count[0];
     const uint4 zero = make_uint4(0, 0, 0, 0);
     if (b >= a.M) {
         const int64_t i = n + (b - a.M), end = n < 1 ? 128 : ((int64_t)n + 127) / 128 * 128;
         if (i < end)
-            for (int64_t v = threadIdx.x; v < vecs; v += 128) reinterpret_cast<uint4 *>(a.hidden_c)[i * vecs + v] = zero;
+            for (int64_t v = threadIdx.x; v < wide; v += 128) reinterpret_cast<uint4 *>(a.hidden_c)[i * wide + v] = zero;
         return;
     }
     const int at = a.place[b];
     if (at >= 0) {
         const uint4 *from = reinterpret_cast<const uint4 *>(a.hidden + b * a.hstride);
-        for (int64_t v = threadIdx.x; v < vecs; v += 128) reinterpret_cast<uint4 *>(a.hidden_c)[at * vecs + v] = from[v];
+        for (int64_t v = threadIdx.x; v < wide; v += 128)
+            reinterpret_cast<uint4 *>(a.hidden_c)[at * wide + v] = v < vecs ? from[v] : zero;
         return;
     }
     if (a.dh)
@@ -151,6 +153,7 @@ __device__ __forceinline__ int32_t xent_end(const XentArgs &a) {
 // whole lines are written.
 constexpr int kXentThreads = 320;
 constexpr int kXentSlab = 32 * 128;  // 32 rows of 64 bf16
+constexpr uint32_t kAcrossA = 1u << 15, kAcrossB = 1u << 16;  // instruction descriptor: M or N contiguous instead of K
 
 template <int N>
 struct XentShape {
@@ -159,7 +162,6 @@ struct XentShape {
     static constexpr int SMEM = STAGES * STAGE + 8 * kXentSlab + 1024;
     static constexpr int NC = N / 2;  // a thread's columns
     static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N / 8) << 17) | (8u << 24);
-    static constexpr uint32_t A_ACROSS = 1u << 15, B_ACROSS = 1u << 16;  // M or N contiguous instead of K
 };
 
 template <int STAGES>
@@ -191,6 +193,46 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+
+// A warp's way round the ring, together: a stage, its barriers, and their
+// phase.  One lane issues, from operands that are the same in all of them
+// (a copy or product costs a thread on its own twice as much).
+template <int STAGES>
+struct XentRing {
+    XentBars<STAGES> &bars;
+    uint8_t *ring;
+    uint32_t bytes, s, phase, turns;
+    bool ok, ready;
+    __device__ __forceinline__ XentRing(XentBars<STAGES> &b, uint8_t *r, uint32_t stage_bytes, bool fill)
+        : bars(b), ring(r), bytes(stage_bytes), s(0), phase(fill ? 1 : 0), turns(0), ok(true), ready(false) {}
+    __device__ __forceinline__ uint8_t *stage() const { return ring + s * bytes; }
+    __device__ __forceinline__ uint64_t *full() const { return &bars.full[s]; }
+    __device__ __forceinline__ uint64_t *empty() const { return &bars.empty[s]; }
+    __device__ __forceinline__ bool wait_empty() { return ok = xent_warp_wait(empty(), phase); }
+    // With a look at the next stage, whose answer comes while this one's products are issued.
+    __device__ __forceinline__ bool wait_full() {
+        ok = ok && (ready || xent_warp_wait(full(), phase));
+        mma_fence_after();
+        const bool wraps = s + 1 == STAGES;
+        seen = mbar_test_wait(&bars.full[wraps ? 0 : s + 1], wraps ? phase ^ 1u : phase);
+        return ok;
+    }
+    __device__ __forceinline__ void next() {
+        if (++s == STAGES) s = 0, phase ^= 1u, ++turns;
+        ready = __all_sync(0xFFFFFFFFu, seen);
+    }
+    // No copy may land, and no commit arrive, after the CTA is gone: the last
+    // use of every stage is waited for, its copies alone if a wait ran out.
+    __device__ __forceinline__ void finish() {
+        for (int i = 0; i < STAGES; ++i) {
+            if (turns > 0 || i < (int)s) {
+                const uint32_t use = i < (int)s ? turns : turns - 1;
+                xent_warp_wait(ok ? &bars.empty[i] : &bars.full[i], use & 1u);
+            }
+        }
+    }
+    bool seen = false;
+};
 
 // A thread's 64 results in bf16 as its row of the warp's slab, with the
 // 128-byte swizzle of the maps that they are stored through.
@@ -243,7 +285,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_scores_kernel(const __gr
     extern __shared__ uint8_t raw[];
     __shared__ XentBars<STAGES> s;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int kblocks = (int)((a.H + kTcK - 1) / kTcK);
     const int32_t row_blocks = xent_end(a) / 128;
     const int32_t left = (int32_t)(a.V - v0 < width ? a.V - v0 : width);  // the piece's entries
@@ -252,62 +294,43 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_scores_kernel(const __gr
     const uint32_t tmem = s.tmem;
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const int32_t ya = t % row_blocks * 128, yb = t / row_blocks * N;
-                for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    const uint32_t i = it % STAGES;
-                    if (!xent_wait(&s.empty[i], ((it / STAGES) & 1u) ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *st = ring + (size_t)i * S::STAGE;
-                    mbar_arrive_expect_tx(&s.full[i], S::STAGE);
-                    tma_tile(st, &map_h, kb * kTcK, ya, &s.full[i]);
-                    tma_tile(st + S::A_BYTES, &map_w, kb * kTcK, yb, &s.full[i]);
+        XentRing<STAGES> r(s, ring, S::STAGE, true);
+        for (int32_t t = blockIdx.x; r.ok && t < tiles; t += gridDim.x) {
+            const int32_t ya = t % row_blocks * 128, yb = t / row_blocks * N;
+            for (int kb = 0; kb < kblocks; ++kb, r.next()) {
+                if (!r.wait_empty()) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(r.full(), S::STAGE);
+                    tma_tile(r.stage(), &map_h, kb * kTcK, ya, r.full());
+                    tma_tile(r.stage() + S::A_BYTES, &map_w, kb * kTcK, yb, r.full());
                 }
+                __syncwarp();
             }
-            // no copy may land, and no commit arrive, after the CTA is gone
-            const uint32_t k = it < STAGES ? it : STAGES;
-            for (uint32_t i = it - k; i < it; ++i)
-                xent_wait(ok ? &s.empty[i % STAGES] : &s.full[i % STAGES], (i / STAGES) & 1u);
         }
+        r.finish();
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0, j = 0;
-            bool ok = true;
-            for (int32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    const uint32_t b = j & 1u, i = it % STAGES;
-                    if (kb % kXentChunk == 0) {
-                        if (!xent_wait(&s.drained[b], ((j >> 1) & 1u) ^ 1u)) {
-                            ok = false;
-                            break;
-                        }
-                        mma_fence_after();
-                    }
-                    if (!xent_wait(&s.full[i], (it / STAGES) & 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    mma_fence_after();
-                    const uint8_t *st = ring + (size_t)i * S::STAGE;
-                    const uint64_t da = smem_tile(st), db = smem_tile(st + S::A_BYTES);
+        XentRing<STAGES> r(s, ring, S::STAGE, false);
+        uint32_t j = 0;
+        for (int32_t t = blockIdx.x; r.ok && t < tiles; t += gridDim.x) {
+            for (int kb = 0; kb < kblocks; ++kb) {
+                const uint32_t b = j & 1u;
+                if (kb % kXentChunk == 0) r.ok = xent_warp_wait(&s.drained[b], ((j >> 1) & 1u) ^ 1u);
+                if (!r.wait_full()) break;
+                const bool end = kb % kXentChunk == kXentChunk - 1 || kb == kblocks - 1;
+                const uint64_t da = smem_tile(r.stage()), db = smem_tile(r.stage() + S::A_BYTES);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTcK / 16; ++k)
                         mma_bf16(tmem + b * N, da + 2 * k, db + 2 * k, S::IDESC, kb % kXentChunk > 0 || k > 0);
-                    mma_commit(&s.empty[i]);
-                    if (kb % kXentChunk == kXentChunk - 1 || kb == kblocks - 1) {
-                        mma_commit(&s.done[b]);
-                        ++j;
-                    }
+                    mma_commit(r.empty());
+                    if (end) mma_commit(&s.done[b]);
                 }
+                if (end) ++j;
+                r.next();
             }
-            mma_commit(&s.last);  // the products are finished before tensor memory is freed
-            xent_wait(&s.last, 0);
         }
+        if (elect_one()) mma_commit(&s.last);  // the products are finished before tensor memory is freed
+        xent_warp_wait(&s.last, 0);
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t at = tmem + ((uint32_t)quarter << 21) + half * NC;
@@ -508,13 +531,14 @@ __device__ __forceinline__ void dh_results(const float *z, float *acc, bool add,
 __global__ void __launch_bounds__(kXentThreads, 1)
     xent_products_kernel(const __grid_constant__ CUtensorMap map_gk, const __grid_constant__ CUtensorMap map_gm,
                          const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
-                         const __grid_constant__ CUtensorMap map_dw, const XentArgs a, int64_t v0, int32_t width) {
+                         const __grid_constant__ CUtensorMap map_dw, const XentArgs a, int64_t v0, int32_t width,
+                         int w_blocks) {
     using S = XentShape<256>;
     constexpr int STAGES = S::STAGES, NC = S::NC, BOX = 64 * 128;
     extern __shared__ uint8_t raw[];
     __shared__ XentBars<STAGES> s;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int32_t n = a.count[0], end = xent_end(a);
     const float scale = a.scale[0];
     const int32_t left = (int32_t)(a.V - v0 < width ? a.V - v0 : width);
@@ -525,71 +549,53 @@ __global__ void __launch_bounds__(kXentThreads, 1)
     XentUnits::Unit u;
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int32_t x = 0; ok && units.get(x, u); ++x) {
-                for (int kb = u.k0; kb < u.k0 + u.ks; ++kb, ++it) {
-                    const uint32_t i = it % STAGES;
-                    if (!xent_wait(&s.empty[i], ((it / STAGES) & 1u) ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *st = ring + (size_t)i * S::STAGE;
-                    mbar_arrive_expect_tx(&s.full[i], S::STAGE);
-                    if (u.is_dh) {
-                        tma_tile(st, &map_gk, kb * kTcK, u.y, &s.full[i]);
+        XentRing<STAGES> r(s, ring, S::STAGE, true);
+        for (int32_t x = 0; r.ok && units.get(x, u); ++x) {
+            for (int kb = u.k0; kb < u.k0 + u.ks; ++kb, r.next()) {
+                if (!r.wait_empty()) break;
+                if (elect_one()) {
+                    uint8_t *st = r.stage(), *sb = st + S::A_BYTES;
+                    mbar_arrive_expect_tx(r.full(), S::STAGE);
+                    if (!u.is_dh) {
+                        tma_tile_3d(st, &map_gm, 0, kb * kTcK, u.y / kTcK, r.full());
+                        tma_tile_3d(sb, &map_h, 0, kb * kTcK, u.x / kTcK, r.full());
                     } else {
-                        tma_tile(st, &map_gm, u.y, kb * kTcK, &s.full[i]);
-                        tma_tile(st + BOX, &map_gm, u.y + 64, kb * kTcK, &s.full[i]);
-                    }
+                        tma_tile(st, &map_gk, kb * kTcK, u.y, r.full());
+                        if (w_blocks) {
+                            tma_tile_3d(sb, &map_w, 0, kb * kTcK, u.x / kTcK, r.full());
+                        } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tma_tile(st + S::A_BYTES + q * BOX, u.is_dh ? &map_w : &map_h, u.x + 64 * q, kb * kTcK, &s.full[i]);
-                }
-            }
-            const uint32_t k = it < STAGES ? it : STAGES;
-            for (uint32_t i = it - k; i < it; ++i)
-                xent_wait(ok ? &s.empty[i % STAGES] : &s.full[i % STAGES], (i / STAGES) & 1u);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0, j = 0;
-            bool ok = true;
-            for (int32_t x = 0; ok && units.get(x, u); ++x) {
-                const int ks = u.ks;
-                const uint32_t idesc = S::IDESC | S::B_ACROSS | (u.is_dh ? 0u : S::A_ACROSS);
-                for (int kb = 0; kb < ks; ++kb, ++it) {
-                    const uint32_t b = j & 1u, i = it % STAGES;
-                    if (kb == 0) {
-                        if (!xent_wait(&s.drained[b], ((j >> 1) & 1u) ^ 1u)) {
-                            ok = false;
-                            break;
+                            for (int q = 0; q < 4; ++q) tma_tile(sb + q * BOX, &map_w, u.x + 64 * q, kb * kTcK, r.full());
                         }
-                        mma_fence_after();
                     }
-                    if (!xent_wait(&s.full[i], (it / STAGES) & 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    mma_fence_after();
-                    const uint8_t *st = ring + (size_t)i * S::STAGE;
-                    const uint64_t da = u.is_dh ? smem_tile(st) : smem_tile_across(st, BOX);
-                    const uint64_t db = smem_tile_across(st + S::A_BYTES, BOX);
-                    const uint32_t step = u.is_dh ? 2 : 128;
+                }
+                __syncwarp();
+            }
+        }
+        r.finish();
+    } else if (warp == 1) {
+        XentRing<STAGES> r(s, ring, S::STAGE, false);
+        uint32_t j = 0;
+        for (int32_t x = 0; r.ok && units.get(x, u); ++x) {
+            if (u.ks == 0) continue;
+            const uint32_t b = j & 1u, idesc = S::IDESC | kAcrossB | (u.is_dh ? 0u : kAcrossA), step = u.is_dh ? 2 : 128;
+            r.ok = xent_warp_wait(&s.drained[b], ((j >> 1) & 1u) ^ 1u);
+            for (int kb = 0; kb < u.ks; ++kb, r.next()) {
+                if (!r.wait_full()) break;
+                const uint64_t da = u.is_dh ? smem_tile(r.stage()) : smem_tile_across(r.stage(), BOX);
+                const uint64_t db = smem_tile_across(r.stage() + S::A_BYTES, BOX);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTcK / 16; ++k)
                         mma_bf16(tmem + b * 256, da + step * k, db + 128 * k, idesc, kb > 0 || k > 0);
-                    mma_commit(&s.empty[i]);
-                    if (kb == ks - 1) {
-                        mma_commit(&s.done[b]);
-                        ++j;
-                    }
+                    mma_commit(r.empty());
+                    if (kb == u.ks - 1) mma_commit(&s.done[b]);
                 }
             }
-            mma_commit(&s.last);
-            xent_wait(&s.last, 0);
+            ++j;
         }
+        if (elect_one()) mma_commit(&s.last);
+        xent_warp_wait(&s.last, 0);
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t at = tmem + ((uint32_t)quarter << 21) + half * NC;
@@ -696,7 +702,7 @@ int launch_scores(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_t 
     const void *fn = reinterpret_cast<const void *>(&xent_scores_kernel<N>);
     const int64_t pad = xent_padded(args.M), left = args.V - v0 < piece ? args.V - v0 : piece;
     CUtensorMap mh, mw, mg;
-    if (!make_map(&mh, args.hidden_c, args.H, pad, args.H, 128) ||
+    if (!make_map(&mh, args.hidden_c, args.H, pad, xent_width(args.H), 128) ||
         !make_map(&mw, args.weight + v0 * args.wstride, args.H, left, args.wstride, N) ||
         !make_map(&mg, args.grad, piece, pad, piece, 32) || prepare_kernel(fn, S::SMEM, 1) != 0)
         return -1;
@@ -714,17 +720,21 @@ int launch_products(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_
     using S = XentShape<256>;
     const void *fn = reinterpret_cast<const void *>(&xent_products_kernel);
     const int64_t pad = xent_padded(args.M), left = args.V - v0 < piece ? args.V - v0 : piece;
+    const int64_t wide = xent_width(args.H);
+    const uint16_t *weight = args.weight + v0 * args.wstride;
+    int w_blocks = args.H % kTcK == 0;  // else the last block would reach beyond the last row
     CUtensorMap gk, gm, mw, mh, dw;
-    if (!make_map(&gk, args.grad, piece, pad, piece, 128) || !make_map(&gm, args.grad, piece, pad, piece, 64) ||
-        !make_map(&mw, args.weight + v0 * args.wstride, args.H, left, args.wstride, 64) ||
-        !make_map(&mh, args.hidden_c, args.H, pad, args.H, 64) ||
+    if (!make_map(&gk, args.grad, piece, pad, piece, 128) || !make_map_blocks(&gm, args.grad, piece, pad, piece, 64, 2) ||
+        !(w_blocks ? make_map_blocks(&mw, weight, args.H, left, args.wstride, 64, 4)
+                   : make_map(&mw, weight, args.H, left, args.wstride, 64)) ||
+        !make_map_blocks(&mh, args.hidden_c, wide, pad, wide, 64, 4) ||
         !make_map(&dw, args.dw ? args.dw + v0 * args.dwstride : args.hidden_c, args.H, args.dw ? left : pad,
-                  args.dw ? args.dwstride : args.H, 32) ||
+                  args.dw ? args.dwstride : wide, 32) ||
         prepare_kernel(fn, S::SMEM, 1) != 0)
         return -1;
     XentArgs a = args;
     int32_t width = (int32_t)piece;
-    void *params[] = {&gk, &gm, &mw, &mh, &dw, &a, &v0, &width};
+    void *params[] = {&gk, &gm, &mw, &mh, &dw, &a, &v0, &width, &w_blocks};
     return cudaLaunchKernel(fn, dim3((unsigned)sm_count()), dim3(kXentThreads), params, S::SMEM, st) == cudaSuccess ? 0
                                                                                                                    : -1;
 }
@@ -739,7 +749,7 @@ int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t 
     for (int64_t m = 0; m < a.M; m += kLmRows) {
         LmLogprobArgs s = scores;
         s.M = a.M - m < kLmRows ? a.M - m : kLmRows;
-        s.hidden = scores.hidden + m * a.H;
+        s.hidden = scores.hidden + m * xent_width(a.H);
         s.tokens = scores.tokens + m;
         s.out = scores.out + m;
         s.lse = scores.lse + m;
