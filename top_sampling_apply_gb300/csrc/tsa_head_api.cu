@@ -33,10 +33,10 @@ bool same_rows(const void *out, int64_t stride, const void *in, int64_t in_strid
 
 // The cross entropy's workspace: where each part starts, and its end.
 struct XentLayout {
-    size_t count, place, rows, tokens, weight, loss, logprob, lse, coef, hidden, part, tok, grad, acc, db, end;
+    size_t count, rows, tokens, weight, loss, coef, hidden, part, tok, grad, acc, db, end;
 };
 XentLayout xent_layout(int64_t M, int64_t H, int64_t V, bool grads, bool bias) {
-    const size_t n = (size_t)xent_padded(M), m = (size_t)M;
+    const size_t n = (size_t)xent_padded(M);
     const int64_t few = M < kLmRows ? M : kLmRows;
     const size_t piece = (size_t)xent_piece(M, V);
     XentLayout l;
@@ -47,13 +47,10 @@ XentLayout xent_layout(int64_t M, int64_t H, int64_t V, bool grads, bool bias) {
         return start;
     };
     l.count = take(8);
-    l.place = take(m * 4);
     l.rows = take(n * 4);
     l.tokens = take(n * 8);
     l.weight = take(n * 4);
     l.loss = take(n * 4);
-    l.logprob = take(n * 4);
-    l.lse = take(n * 4);
     l.coef = take(n * 16);
     l.hidden = take(n * (size_t)xent_width(H) * 2);
     l.part = take((size_t)lm_logprob_parts(few, V) * (size_t)few * sizeof(float2));
@@ -283,13 +280,10 @@ int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t 
     a.db = grad_bias_out;
     a.count = reinterpret_cast<int32_t *>(ws + l.count);
     a.scale = reinterpret_cast<float *>(ws + l.count) + 1;
-    a.place = reinterpret_cast<int32_t *>(ws + l.place);
     a.rows = reinterpret_cast<int32_t *>(ws + l.rows);
     a.tokens = reinterpret_cast<int64_t *>(ws + l.tokens);
     a.weight_c = reinterpret_cast<float *>(ws + l.weight);
     a.row_loss_c = reinterpret_cast<float *>(ws + l.loss);
-    a.logprob_c = reinterpret_cast<float *>(ws + l.logprob);
-    a.lse_c = reinterpret_cast<float *>(ws + l.lse);
     a.coef = reinterpret_cast<float4 *>(ws + l.coef);
     a.hidden_c = reinterpret_cast<uint16_t *>(ws + l.hidden);
     a.grad = reinterpret_cast<uint16_t *>(ws + l.grad);
@@ -308,8 +302,6 @@ int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t 
     p.cap = softcap;
     p.temperature_s = 1.f;
     p.tokens = a.tokens;
-    p.out = a.logprob_c;
-    p.lse = a.lse_c;
     p.count = a.count;
     p.part = reinterpret_cast<float2 *>(ws + l.part);
     p.tok = reinterpret_cast<float *>(ws + l.tok);

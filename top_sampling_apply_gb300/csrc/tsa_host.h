@@ -224,14 +224,15 @@ struct LmLogprobArgs {
     float *out;
     float2 *part;            // [parts][rows]: a part's largest score and its sum against it
     float *tok;              // [rows]: the token's score
-    // the cross entropy's: the log-sum-exp [M], and a device count of rows
-    // (NULL: all), of which these are the ones from `first` on
-    float *lse;
+    // the cross entropy's: a device count of rows (NULL: all), of which these
+    // are the ones from `first` on
     const int32_t *count;
     int64_t first;
 };
 constexpr int64_t kLmRows = 8192;  // rows a pass over the weight takes
 int64_t lm_logprob_parts(int64_t M, int64_t V);
+// The parts alone, `parts` of them a row.
+int lm_logprob_products(const LmLogprobArgs &args, int64_t *parts, cudaStream_t st);
 int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st);
 unsigned int *lm_logprob_status_ptr();
 
@@ -304,9 +305,9 @@ struct XentArgs {
     float *db;               // [V] or NULL
     // workspace; "c": of the rows that count, one after another
     float *scale;            // [1]: the largest row weight, which G is without
-    int32_t *count, *place, *rows;  // [1], [M]: a row's place or -1, [M]: a place's row
+    int32_t *count, *rows;   // [1]; [M]: a place's row
     int64_t *tokens;
-    float *weight_c, *row_loss_c, *logprob_c, *lse_c;
+    float *weight_c, *row_loss_c;
     float4 *coef;            // what a place's gradient needs
     uint16_t *hidden_c;      // [padded, xent_width(H)]
     uint16_t *grad;          // [padded, piece]: a piece of the vocabulary's part of G

@@ -19,14 +19,6 @@ __device__ __forceinline__ float row_temp(const LmLogprobArgs &a, int64_t row) {
     const float T = a.temperature ? __ldg(a.temperature + row) : a.temperature_s;
     return T > 0.f ? T : 1.f;
 }
-// (m, Z) of two parts against the larger maximum; c2 = log2(e) / T.  An empty
-// part is (-inf, 0).
-__device__ __forceinline__ float2 join(float2 a, float2 b, float c2) {
-    const bool up = b.x > a.x;
-    const float2 hi = up ? b : a, lo = up ? a : b;
-    const float f = hi.x == lo.x ? 1.f : ex2_approx(fmaxf((lo.x - hi.x) * c2, -1.0e4f));
-    return make_float2(hi.x, fmaf(lo.y, f, hi.y));
-}
 __device__ unsigned int g_lm_logprob_status;
 
 // x = z if a == b: a selection that keeps an array's elements in registers
@@ -103,14 +95,10 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kblocks = (int)((a.H + kTcK - 1) / kTcK);
-    const int64_t M = row_count(a);
-    const int row_blocks = ROWS ? (int)((M + 127) / 128) : 1;
-    const int64_t tiles = v_tiles * row_blocks;
     // this CTA's vocabulary rows (few hidden rows), or tiles
     const int64_t v_first = ROWS ? 0 : (int64_t)blockIdx.x * run;
     const int64_t v_end = ROWS || v_first + run > a.V ? a.V : v_first + run;
     const int64_t t_first = ROWS ? blockIdx.x : 0, t_step = ROWS ? gridDim.x : 1;
-    const int64_t t_end = ROWS ? tiles : (v_end - v_first + 127) / 128;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full[i], 1);
@@ -128,6 +116,11 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
     __syncthreads();
     mma_fence_after();
     pdl_launch_dependents();  // the joining kernel waits for this one's end before it reads
+    pdl_wait_primary();
+    const int64_t M = row_count(a);
+    const int row_blocks = ROWS ? (int)((M + 127) / 128) : 1;
+    const int64_t tiles = v_tiles * row_blocks;
+    const int64_t t_end = ROWS ? tiles : (v_end - v_first + 127) / 128;
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0) {
@@ -297,7 +290,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
                         a.tok[row] = found;
                     }
                     if (top > -INFINITY) {
-                        if (top > st.x) st = join(st, make_float2(top, 0.f), c2);
+                        if (top > st.x) st = lm_join(st, make_float2(top, 0.f), c2);
                         const unsigned long long neg = pair_of(-st.x, -st.x), cc = pair_of(c2, c2);
                         unsigned long long acc = pair_of(st.y, 0.f);
 #pragma unroll
@@ -350,7 +343,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
                         !(((uint32_t)__ldg(a.mask + q * a.mstride + (w0 >> 5)) >> lane) & 1u))
                         x = -INFINITY;
                     if (v < v_end && __ldg(a.tokens + q) == v) a.tok[q] = x;
-                    if (x > -INFINITY) st[q] = join(st[q], make_float2(x, 1.f), kLog2eH / row_temp(a, q));
+                    if (x > -INFINITY) st[q] = lm_join(st[q], make_float2(x, 1.f), kLog2eH / row_temp(a, q));
                 }
             }
             if (ok) {
@@ -364,7 +357,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
                         float2 y;
                         y.x = __shfl_xor_sync(0xFFFFFFFFu, x.x, o);
                         y.y = __shfl_xor_sync(0xFFFFFFFFu, x.y, o);
-                        x = join(x, y, c2);
+                        x = lm_join(x, y, c2);
                     }
                     if (lane == 0) s_part[quarter][q] = x;
                 }
@@ -376,7 +369,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
         if (threadIdx.x < N && (int64_t)threadIdx.x < M) {
             const float c2 = kLog2eH / row_temp(a, threadIdx.x);
             float2 x = s_part[0][threadIdx.x];
-            for (int w = 1; w < 4; ++w) x = join(x, s_part[w][threadIdx.x], c2);
+            for (int w = 1; w < 4; ++w) x = lm_join(x, s_part[w][threadIdx.x], c2);
             a.part[(int64_t)blockIdx.x * M + threadIdx.x] = x;
         }
     }
@@ -389,29 +382,28 @@ constexpr int kJoinX = 8, kJoinY = 64;
 __global__ void __launch_bounds__(kJoinX *kJoinY) lm_logprob_join_kernel(const LmLogprobArgs a, int64_t parts) {
     __shared__ float2 sh[kJoinY][kJoinX];
     pdl_wait_primary();
-    const int64_t M = row_count(a);
     const int64_t row = (int64_t)blockIdx.x * kJoinX + threadIdx.x;
-    const float T = row < M ? row_temp(a, row) : 1.f, c2 = kLog2eH / T;
+    const float T = row < a.M ? row_temp(a, row) : 1.f, c2 = kLog2eH / T;
     float2 s = make_float2(-INFINITY, 0.f);
-    if (row < M) {
+    if (row < a.M) {
         const float2 *part = a.part + row;
         int64_t p = threadIdx.y;
         for (; p + 3 * kJoinY < parts; p += 4 * kJoinY) {
             float2 v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = part[(p + i * kJoinY) * M];
-            s = join(s, join(join(v[0], v[1], c2), join(v[2], v[3], c2), c2), c2);
+            for (int i = 0; i < 4; ++i) v[i] = part[(p + i * kJoinY) * a.M];
+            s = lm_join(s, lm_join(lm_join(v[0], v[1], c2), lm_join(v[2], v[3], c2), c2), c2);
         }
-        for (; p < parts; p += kJoinY) s = join(s, part[p * M], c2);
+        for (; p < parts; p += kJoinY) s = lm_join(s, part[p * a.M], c2);
     }
     sh[threadIdx.y][threadIdx.x] = s;
 #pragma unroll
     for (int o = kJoinY / 2; o > 0; o >>= 1) {
         __syncthreads();
         if (threadIdx.y < o)
-            sh[threadIdx.y][threadIdx.x] = join(sh[threadIdx.y][threadIdx.x], sh[threadIdx.y + o][threadIdx.x], c2);
+            sh[threadIdx.y][threadIdx.x] = lm_join(sh[threadIdx.y][threadIdx.x], sh[threadIdx.y + o][threadIdx.x], c2);
     }
-    if (threadIdx.y != 0 || row >= M) return;
+    if (threadIdx.y != 0 || row >= a.M) return;
     s = sh[0][threadIdx.x];
     const int64_t i = a.tokens[row];
     float r = __int_as_float(0x7FC00000);
@@ -420,7 +412,6 @@ __global__ void __launch_bounds__(kJoinX *kJoinY) lm_logprob_join_kernel(const L
         r = z > -INFINITY ? (z - s.x) / T - logf(s.y) : -INFINITY;
     }
     a.out[row] = r;
-    if (a.lse) a.lse[row] = s.x < INFINITY ? s.x / T + logf(s.y) : s.x;
 }
 
 }  // namespace
@@ -454,7 +445,17 @@ int launch_products(const LmLogprobArgs &args, int64_t *parts, cudaStream_t st) 
     *parts = ROWS ? (args.V + N / 2 - 1) / (N / 2) : grid;
     LmLogprobArgs a = args;
     void *params[] = {&ma, &mb, &a, &v_tiles, &run};
-    return cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kTcThreads<ROWS>), params, S::SMEM, st) == cudaSuccess ? 0 : -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kTcThreads<ROWS>);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.count ? 1 : 0;  // only behind a kernel of the same call
+    return cudaLaunchKernelExC(&cfg, fn, params) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace
@@ -465,18 +466,16 @@ int64_t lm_logprob_parts(int64_t M, int64_t V) {
     return M <= kLmMid ? (V + 63) / 64 : (V + 127) / 128;
 }
 
+int lm_logprob_products(const LmLogprobArgs &args, int64_t *parts, cudaStream_t st) {
+    if (args.M <= 16) return launch_products<16, false, 11>(args, parts, st);
+    if (args.M <= kLmFew) return launch_products<32, false, 10>(args, parts, st);
+    if (args.M <= kLmMid) return launch_products<128, true, 6>(args, parts, st);
+    return launch_products<256, true, 4>(args, parts, st);
+}
+
 int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st) {
     int64_t parts = 0;
-    int r;
-    if (args.M <= 16)
-        r = launch_products<16, false, 11>(args, &parts, st);
-    else if (args.M <= kLmFew)
-        r = launch_products<32, false, 10>(args, &parts, st);
-    else if (args.M <= kLmMid)
-        r = launch_products<128, true, 6>(args, &parts, st);
-    else
-        r = launch_products<256, true, 4>(args, &parts, st);
-    if (r != 0) return -1;
+    if (lm_logprob_products(args, &parts, st) != 0) return -1;
     LmLogprobArgs a = args;
     void *params[] = {&a, &parts};
     cudaLaunchConfig_t cfg = {};

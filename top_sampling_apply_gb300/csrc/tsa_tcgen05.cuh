@@ -12,6 +12,14 @@ namespace tsa {
 
 constexpr float kLog2eH = 1.4426950408889634f;
 
+// (m, Z) of two parts against the larger maximum; c2 = log2(e) / T.  An empty
+// part is (-inf, 0).
+__device__ __forceinline__ float2 lm_join(float2 a, float2 b, float c2) {
+    const bool up = b.x > a.x;
+    const float2 hi = up ? b : a, lo = up ? a : b;
+    const float f = hi.x == lo.x ? 1.f : ex2_approx(fmaxf((lo.x - hi.x) * c2, -1.0e4f));
+    return make_float2(hi.x, fmaf(lo.y, f, hi.y));
+}
 // cap tanh(z / cap), within 2^-21 of itself for every cap.  With x = z / cap:
 //   |x| <= 5/8  z P(x^2), P a polynomial of degree 5 with P(0) = 1, fitted to equal relative error (Remez's exchange;
 //               with its coefficients in fp32 within 2^-26 of tanh(x) / x).

@@ -20,113 +20,126 @@ namespace tsa {
 
 namespace {
 
-// One CTA: where each row that counts goes, in order; its target and weight.
-// Without weights each has 1 / (number of them).  Places up to the next
-// multiple of 128 get a weight of 0 and no target.
-__global__ void __launch_bounds__(1024) xent_rows_kernel(const XentArgs a) {
-    __shared__ int s_warp[32], s_base;
-    __shared__ uint32_t s_top;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) s_base = 0, s_top = 0;
-    uint32_t top = 0;
-    __syncthreads();
-    for (int64_t m0 = 0; m0 < a.M; m0 += 1024) {
-        const int64_t m = m0 + threadIdx.x;
-        int64_t t = -1;
-        float w = 1.f;
-        if (m < a.M) {
-            t = a.targets[m];
-            if (a.row_weight) w = a.row_weight[m];
-        }
-        const bool live = t >= 0 && t < a.V && w != 0.f;
-        if (live) top = max(top, __float_as_uint(fabsf(w)));
-        const uint32_t vote = __ballot_sync(0xFFFFFFFFu, live);
-        if (lane == 0) s_warp[warp] = __popc(vote);
-        __syncthreads();
-        if (warp == 0) {
-            const int own = s_warp[lane];
-            int sum = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                if (lane >= o) sum += x;
-            }
-            s_warp[lane] = sum - own + s_base;
-            __syncwarp();
-            if (lane == 31) s_base += sum;
-        }
-        __syncthreads();
-        if (m < a.M) {
-            const int at = s_warp[warp] + __popc(vote & ((1u << lane) - 1u));
-            a.place[m] = live ? at : -1;
-            if (live) {
-                a.rows[at] = (int32_t)m;
-                a.tokens[at] = t;
-                a.weight_c[at] = w;
-            }
-        }
-        __syncthreads();
-    }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (lane == 0) atomicMax(&s_top, top);
-    __syncthreads();
-    const int n = s_base;
-    if (threadIdx.x == 0) {
-        a.count[0] = n;
-        a.scale[0] = n < 1 ? 1.f : a.row_weight ? __uint_as_float(s_top) : 1.f / (float)n;
-    }
-    const int64_t pad = xent_padded(a.M);
-    for (int64_t i = threadIdx.x; i < pad; i += 1024) {
-        if (i >= n) {
-            a.tokens[i] = -1;
-            a.weight_c[i] = 0.f;
-            a.row_loss_c[i] = 0.f;
-        } else if (!a.row_weight) {
-            a.weight_c[i] = 1.f / (float)n;
-        }
-    }
+// The rows that count, one after another in their order, each filled up to whole
+// tiles of columns with zeros; their targets and weights (without weights each
+// has 1 / (number of them)); zeros up to a multiple of 128 rows (128 at least),
+// and in the outputs of skipped rows.  A warp a row.  Every CTA counts for itself
+// the rows before its own, and all: M / 256 loads a thread, against a launch
+// of their own for a prefix sum.
+constexpr int kXentPrep = 8;
+
+__device__ __forceinline__ bool xent_live(const XentArgs &a, int64_t m, float &w) {
+    const int64_t t = a.targets[m];
+    w = a.row_weight ? a.row_weight[m] : 1.f;
+    return t >= 0 && t < a.V && w != 0.f;
 }
 
-// The rows that count, one after another, each filled up to whole tiles of
-// columns with zeros; zeros up to a multiple of 128 rows (128 at least), and in
-// the outputs of skipped rows.
-__global__ void __launch_bounds__(128) xent_gather_kernel(const XentArgs a) {
-    const int64_t b = blockIdx.x, vecs = a.H / 8, wide = xent_width(a.H) / 8;
-    const int n = a.count[0];
+__global__ void __launch_bounds__(32 * kXentPrep) xent_prepare_kernel(const XentArgs a) {
+    __shared__ int s_all[kXentPrep], s_before[kXentPrep];
+    __shared__ uint32_t s_top[kXentPrep];
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t m0 = (int64_t)blockIdx.x * kXentPrep, m = m0 + warp;
+    int all = 0, before = 0;
+    uint32_t top = 0;
+    for (int64_t i = threadIdx.x; i < a.M; i += 32 * kXentPrep) {
+        float w;
+        if (xent_live(a, i, w)) {
+            ++all;
+            before += i < m0;
+            top = max(top, __float_as_uint(fabsf(w)));
+        }
+    }
+    all = __reduce_add_sync(0xFFFFFFFFu, all);
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (lane == 0) s_all[warp] = all, s_before[warp] = before, s_top[warp] = top;
+    __syncthreads();
+    all = before = 0, top = 0;
+#pragma unroll
+    for (int i = 0; i < kXentPrep; ++i) all += s_all[i], before += s_before[i], top = max(top, s_top[i]);
+    const int64_t n = all, end = n < 1 ? 128 : (n + 127) / 128 * 128;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.count[0] = (int32_t)n;
+        a.scale[0] = n < 1 ? 1.f : a.row_weight ? __uint_as_float(top) : 1.f / (float)n;
+    }
+    const int64_t vecs = a.H / 8, wide = xent_width(a.H) / 8;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    if (b >= a.M) {
-        const int64_t i = n + (b - a.M), end = n < 1 ? 128 : ((int64_t)n + 127) / 128 * 128;
-        if (i < end)
-            for (int64_t v = threadIdx.x; v < wide; v += 128) reinterpret_cast<uint4 *>(a.hidden_c)[i * wide + v] = zero;
+    uint4 *rows = reinterpret_cast<uint4 *>(a.hidden_c);
+    if (m0 >= a.M) {  // the CTAs behind the last row
+        const int64_t i = n + m - (a.M + kXentPrep - 1) / kXentPrep * kXentPrep;
+        if (i >= end) return;
+        for (int64_t v = lane; v < wide; v += 32) rows[i * wide + v] = zero;
+        if (lane == 0) a.tokens[i] = -1;
         return;
     }
-    const int at = a.place[b];
-    if (at >= 0) {
-        const uint4 *from = reinterpret_cast<const uint4 *>(a.hidden + b * a.hstride);
-        for (int64_t v = threadIdx.x; v < wide; v += 128)
-            reinterpret_cast<uint4 *>(a.hidden_c)[at * wide + v] = v < vecs ? from[v] : zero;
+    float w = 0.f;
+    const bool one = lane < kXentPrep && m0 + lane < a.M && xent_live(a, m0 + lane, w);
+    const uint32_t vote = __ballot_sync(0xFFFFFFFFu, one);
+    if (m >= a.M) return;
+    if (m >= n && lane == 0) a.weight_c[m] = a.row_loss_c[m] = 0.f;  // as a place, it has no row
+    if (vote >> warp & 1u) {
+        const int64_t at = before + __popc(vote & ((1u << warp) - 1u));
+        const uint4 *from = reinterpret_cast<const uint4 *>(a.hidden + m * a.hstride);
+        for (int64_t v = lane; v < wide; v += 32) rows[at * wide + v] = v < vecs ? from[v] : zero;
+        if (lane == warp) {
+            a.rows[at] = (int32_t)m;
+            a.tokens[at] = a.targets[m];
+            a.weight_c[at] = a.row_weight ? w : 1.f / (float)n;
+        }
         return;
     }
     if (a.dh)
-        for (int64_t v = threadIdx.x; v < vecs; v += 128) reinterpret_cast<uint4 *>(a.dh + b * a.dhstride)[v] = zero;
-    if (threadIdx.x == 0) a.row_loss[b] = a.lse[b] = 0.f;
+        for (int64_t v = lane; v < vecs; v += 32) reinterpret_cast<uint4 *>(a.dh + m * a.dhstride)[v] = zero;
+    if (lane == 0) a.row_loss[m] = a.lse[m] = 0.f;
 }
 
-// The losses of the rows that count, and what their gradients need.
-__global__ void __launch_bounds__(256) xent_finish_kernel(const XentArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= xent_padded(a.M)) return;
-    if (i >= a.count[0]) {
+// The losses of a pass's rows from their parts, and what their gradients need;
+// places up to the next multiple of 128 have none.  8 rows a CTA, 64 threads a
+// row, then a tree over them.
+constexpr int kXentJoinX = 8, kXentJoinY = 64;
+__global__ void __launch_bounds__(kXentJoinX *kXentJoinY) xent_loss_kernel(const XentArgs a, const LmLogprobArgs s,
+                                                                           int64_t parts) {
+    __shared__ float2 sh[kXentJoinY][kXentJoinX];
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const int64_t n = a.count[0], at = (int64_t)blockIdx.x * kXentJoinX + threadIdx.x, i = s.first + at;
+    const int64_t M = n - s.first < s.M ? n - s.first : s.M;  // the pass's rows
+    float2 x = make_float2(-INFINITY, 0.f);
+    if (at < M) {
+        const float2 *part = s.part + at;
+        int64_t p = threadIdx.y;
+        for (; p + 3 * kXentJoinY < parts; p += 4 * kXentJoinY) {
+            float2 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = part[(p + q * kXentJoinY) * M];
+            x = lm_join(x, lm_join(lm_join(v[0], v[1], kLog2eH), lm_join(v[2], v[3], kLog2eH), kLog2eH), kLog2eH);
+        }
+        for (; p < parts; p += kXentJoinY) x = lm_join(x, part[p * M], kLog2eH);
+    }
+    sh[threadIdx.y][threadIdx.x] = x;
+#pragma unroll
+    for (int o = kXentJoinY / 2; o > 0; o >>= 1) {
+        __syncthreads();
+        if (threadIdx.y < o)
+            sh[threadIdx.y][threadIdx.x] = lm_join(sh[threadIdx.y][threadIdx.x], sh[threadIdx.y + o][threadIdx.x], kLog2eH);
+    }
+    if (threadIdx.y != 0 || i >= (n < 1 ? 128 : (n + 127) / 128 * 128)) return;
+    if (i >= n) {
         a.coef[i] = make_float4(0.f, 0.f, INFINITY, 0.f);
         return;
     }
-    const float l = a.lse_c[i], w = a.weight_c[i], c = a.z_loss;
-    const float loss = -a.logprob_c[i] + (c != 0.f ? c * l * l : 0.f);
+    if (at >= M) return;  // the next pass's
+    x = sh[0][threadIdx.x];
+    const float ln = logf(x.y), l = x.x < INFINITY ? x.x + ln : x.x, c = a.z_loss;
+    // the score less the sum's reference is exact where they are near
+    float loss = x.x > -INFINITY && x.x < INFINITY ? ln - (s.tok[at] - x.x) : __int_as_float(0x7FC00000);
+    if (c != 0.f) loss += c * l * l;
     a.row_loss_c[i] = loss;
     a.row_loss[a.rows[i]] = loss;
     a.lse[a.rows[i]] = l;
-    const float part = a.row_weight ? w / a.scale[0] : 1.f;
-    a.coef[i] = make_float4(c != 0.f ? part * fmaf(2.f * c, l, 1.f) : part, part, l, 0.f);
+    const float w = a.row_weight ? a.weight_c[i] / a.scale[0] : 1.f;
+    a.coef[i] = make_float4(c != 0.f ? w * fmaf(2.f * c, l, 1.f) : w, w, l, 0.f);
 }
 
 __device__ unsigned int g_xent_status;
@@ -287,10 +300,12 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_scores_kernel(const __gr
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int kblocks = (int)((a.H + kTcK - 1) / kTcK);
+    xent_setup(s, 2 * N);
+    pdl_launch_dependents();
+    pdl_wait_primary();
     const int32_t row_blocks = xent_end(a) / 128;
     const int32_t left = (int32_t)(a.V - v0 < width ? a.V - v0 : width);  // the piece's entries
     const int32_t tiles = row_blocks * (width / N);
-    xent_setup(s, 2 * N);
     const uint32_t tmem = s.tmem;
 
     if (warp == 0) {
@@ -428,6 +443,8 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_scores_kernel(const __gr
 // db of a piece: 32 columns a CTA, the rows' parts over 32 rows of threads.
 __global__ void __launch_bounds__(1024) xent_bias_kernel(const XentArgs a, int64_t v0, int32_t width) {
     __shared__ float sh[32][33];
+    pdl_launch_dependents();
+    pdl_wait_primary();
     const int32_t c = blockIdx.x * 32 + threadIdx.x, parts = xent_end(a) / 32;
     float s = 0.f;
     if (c < width)
@@ -539,12 +556,14 @@ __global__ void __launch_bounds__(kXentThreads, 1)
     __shared__ XentBars<STAGES> s;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    xent_setup(s, 512);
+    pdl_launch_dependents();
+    pdl_wait_primary();
     const int32_t n = a.count[0], end = xent_end(a);
     const float scale = a.scale[0];
     const int32_t left = (int32_t)(a.V - v0 < width ? a.V - v0 : width);
     XentUnits units;
     units.plan(a, left, end);
-    xent_setup(s, 512);
     const uint32_t tmem = s.tmem;
     XentUnits::Unit u;
 
@@ -653,6 +672,8 @@ __global__ void __launch_bounds__(kXentThreads, 1)
 // dH from the parts of a split K.
 __global__ void __launch_bounds__(128) xent_join_kernel(const XentArgs a) {
     const int32_t m = blockIdx.x;
+    pdl_launch_dependents();
+    pdl_wait_primary();
     if (m >= a.count[0]) return;
     const float *acc = a.acc + (int64_t)m * a.H;
     uint16_t *to = a.dh + (int64_t)a.rows[m] * a.dhstride;
@@ -696,6 +717,22 @@ unsigned int *xent_status_ptr() {
 
 namespace {
 
+// A launch that may begin while the kernel before it drains; it waits for that
+// one's end before it reads memory.
+int launch(const void *fn, dim3 grid, dim3 block, size_t smem, void **params, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, params) == cudaSuccess ? 0 : -1;
+}
+
 template <int N>
 int launch_scores(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_t st) {
     using S = XentShape<N>;
@@ -710,10 +747,7 @@ int launch_scores(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_t 
     int32_t width = (int32_t)piece;
     const int64_t tiles = pad / 128 * (piece / N), sms = sm_count();
     void *params[] = {&mh, &mw, &mg, &a, &v0, &width};
-    return cudaLaunchKernel(fn, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kXentThreads), params, S::SMEM, st) ==
-                   cudaSuccess
-               ? 0
-               : -1;
+    return launch(fn, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kXentThreads), S::SMEM, params, st);
 }
 
 int launch_products(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_t st) {
@@ -735,47 +769,48 @@ int launch_products(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_
     XentArgs a = args;
     int32_t width = (int32_t)piece;
     void *params[] = {&gk, &gm, &mw, &mh, &dw, &a, &v0, &width, &w_blocks};
-    return cudaLaunchKernel(fn, dim3((unsigned)sm_count()), dim3(kXentThreads), params, S::SMEM, st) == cudaSuccess ? 0
-                                                                                                                   : -1;
+    return launch(fn, dim3((unsigned)sm_count()), dim3(kXentThreads), S::SMEM, params, st);
 }
 
 }  // namespace
 
 int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t st) {
-    const XentArgs &a = args;
-    xent_rows_kernel<<<1, 1024, 0, st>>>(a);
-    xent_gather_kernel<<<(unsigned)(a.M + 128), 128, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return -1;
+    XentArgs a = args;
+    void *one[] = {&a};
+    const int64_t pad = xent_padded(a.M), piece = xent_piece(a.M, a.V);
+    if (cudaLaunchKernel(reinterpret_cast<const void *>(&xent_prepare_kernel),
+                         dim3((unsigned)((a.M + kXentPrep - 1) / kXentPrep + 128 / kXentPrep)), dim3(32 * kXentPrep), one, 0,
+                         st) != cudaSuccess)
+        return -1;
     for (int64_t m = 0; m < a.M; m += kLmRows) {
         LmLogprobArgs s = scores;
-        s.M = a.M - m < kLmRows ? a.M - m : kLmRows;
+        const bool more = a.M - m > kLmRows;
+        s.M = more ? kLmRows : a.M - m;
         s.hidden = scores.hidden + m * xent_width(a.H);
         s.tokens = scores.tokens + m;
-        s.out = scores.out + m;
-        s.lse = scores.lse + m;
         s.first = m;
-        if (lm_logprob_launch(s, st) != 0) return -1;
+        int64_t parts = 0;
+        if (lm_logprob_products(s, &parts, st) != 0) return -1;
+        void *params[] = {&a, &s, &parts};
+        const int64_t places = more ? kLmRows : pad - m;
+        if (launch(reinterpret_cast<const void *>(&xent_loss_kernel), dim3((unsigned)(places / kXentJoinX)),
+                   dim3(kXentJoinX, kXentJoinY), 0, params, st) != 0)
+            return -1;
     }
-    const int64_t pad = xent_padded(a.M);
-    xent_finish_kernel<<<(unsigned)((pad + 255) / 256), 256, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return -1;
-    if (weighted_sum_launch(a.row_loss_c, a.weight_c, 0.f, a.M, a.loss, st) != 0) return -1;
-    if (!a.dh && !a.dw && !a.db) return 0;
-    const int64_t piece = xent_piece(a.M, a.V);
-    for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
+    for (int64_t v0 = 0; (a.dh || a.dw || a.db) && v0 < a.V; v0 += piece) {
         // one block of rows: smaller tiles spread the vocabulary more evenly
         if ((pad == 128 ? launch_scores<128>(a, v0, piece, st) : launch_scores<256>(a, v0, piece, st)) != 0) return -1;
-        if (a.db) {
-            xent_bias_kernel<<<(unsigned)((piece + 31) / 32), dim3(32, 32), 0, st>>>(a, v0, (int32_t)piece);
-            if (cudaGetLastError() != cudaSuccess) return -1;
-        }
+        int32_t width = (int32_t)piece;
+        void *params[] = {&a, &v0, &width};
+        if (a.db && launch(reinterpret_cast<const void *>(&xent_bias_kernel), dim3((unsigned)((piece + 31) / 32)),
+                           dim3(32, 32), 0, params, st) != 0)
+            return -1;
         if ((a.dh || a.dw) && launch_products(a, v0, piece, st) != 0) return -1;
     }
-    if (a.dh && a.splits > 1) {
-        xent_join_kernel<<<(unsigned)a.M, 128, 0, st>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return -1;
-    }
-    return 0;
+    if (a.dh && a.splits > 1 &&
+        launch(reinterpret_cast<const void *>(&xent_join_kernel), dim3((unsigned)a.M), dim3(128), 0, one, st) != 0)
+        return -1;
+    return weighted_sum_launch(a.row_loss_c, a.weight_c, 0.f, a.M, a.loss, st);
 }
 
 }  // namespace tsa
