@@ -182,6 +182,31 @@ def test_norm_of_many_rows(tsa):
     check_back(tsa, r, x, w, None)
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("H", [2056, 5120, 6152, 8192, 16384])
+def test_many_long_rows(tsa, dt, H):
+    """Rows that go through shared memory, with strides, over their inputs, and with a wider weight."""
+    N = 700
+    x, r, w = rows(1, N, H, dt, 8), rows(2, N, H, dt, 24, 8), rows(3, 1, H, torch.float32)[0]
+    s = head.add_residual(x, r)
+    y, rstd = head.rms_norm(s, w, 1e-6)
+    kept = r.clone()
+    a = tsa.rms_norm(x, w, residual=r, residual_out=r)
+    assert torch.equal(r, s)
+    near(a.rstd, rstd, 30 * U * rstd)
+    near(a.out, y, 32 * U * y.abs(), dt)
+    b = tsa.rms_norm(x, w, residual=kept, quantize=True)
+    assert torch.equal(b.residual, s) and torch.equal(b.rstd, a.rstd)
+    check_codes(b.out, b.scale, y)
+    y, _ = head.rms_norm(x, w, 1e-6)
+    near(tsa.rms_norm(x, w).out, y, 32 * U * y.abs(), dt)
+    check_back(tsa, kept, x, w, None)
+    check_back(tsa, kept, x, w, r)
+    a = tsa.rms_norm_backward(kept, x, w, b.rstd, grad_residual=r)
+    c = tsa.rms_norm_backward(kept, x, w, b.rstd, grad_residual=r, grad_x=kept)
+    assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1]) and tsa.device_status() == 0
+
+
 def test_norm_of_no_rows(tsa):
     x, w = torch.empty(0, 64, device=DEV), torch.ones(64, device=DEV)
     assert tsa.rms_norm(x, w, quantize=True).out.shape == (0, 64)

@@ -418,7 +418,7 @@ int tsa_device_status(int clear) {
                              sample_row_spec_status_ptr_f32(), sample_row_spec_status_ptr_f16(),
                              sample_row_spec_status_ptr_bf16(), lm_logprob_status_ptr(),
                              row_loss_status_ptr(),       xent_status_ptr(),
-                             int8_status_ptr()};
+                             int8_status_ptr(),           norm_status_ptr()};
     constexpr int kWords = sizeof(ptrs) / sizeof(ptrs[0]);
     void *p = nullptr;
     if (cudaGetSymbolAddress(&p, g_selftest_status) == cudaSuccess) ptrs[3] = (unsigned int *)p;

@@ -269,6 +269,7 @@ struct NormBackArgs {
     void *dw;        // [H] of the weight's type
     float *part;     // [norm_back_parts][H]
 };
+unsigned int *norm_status_ptr();
 int64_t norm_back_parts(int64_t N, int64_t H);
 int norm_back_launch(const NormBackArgs &args, int dtype, cudaStream_t st);
 

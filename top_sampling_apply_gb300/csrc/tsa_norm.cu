@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "tsa_device.cuh"
 #include "tsa_host.h"
 
@@ -16,25 +18,35 @@ namespace tsa {
 
 namespace {
 
-constexpr int kNormThreads = 512;  // most threads a row: 32 elements each are kNormMaxH
+constexpr int kNormElems = 16;  // a thread's elements of a long row
+// Most threads a row: 512 keep 128 registers each, enough to hold the next row
+// too; rows of more than 8,192 elements take up to 1,024 threads.
+constexpr int norm_threads(bool big) { return big ? 1024 : 512; }
+static_assert(kNormElems * norm_threads(true) == kNormMaxH, "the longest row fits");
+
+__device__ unsigned int g_norm_status;
 
 // W elements of a row at `i`: a 16-byte vector, or single elements where a
 // row does not start on 16 bytes.  Plain loads: an output may be an input's
 // own memory, and every element is read by the thread that writes it.
 template <int DT, int W>
 struct Part {
-    static __device__ __forceinline__ void load(const void *p, int64_t i, float *x) {
-        if constexpr (W > 1) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + i * Elem<DT>::SIZE);
-            Elem<DT>::unpack(v, x);
-        } else if constexpr (DT == 0) {
-            x[0] = static_cast<const float *>(p)[i];
-        } else if constexpr (DT == 1) {
-            x[0] = __half2float(static_cast<const __half *>(p)[i]);
-        } else {
-            x[0] = __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-        }
+    // What a load brings, before it is unpacked: 16 bytes, or an element.
+    using Raw = std::conditional_t<(W > 1), uint4, std::conditional_t<DT == 0, uint32_t, uint16_t>>;
+    static __device__ __forceinline__ Raw fetch(const void *p, int64_t i) {
+        return *reinterpret_cast<const Raw *>(static_cast<const uint8_t *>(p) + i * Elem<DT>::SIZE);
     }
+    static __device__ __forceinline__ void unpack(const Raw &r, float *x) {
+        if constexpr (W > 1)
+            Elem<DT>::unpack(r, x);
+        else if constexpr (DT == 0)
+            x[0] = __uint_as_float(r);
+        else if constexpr (DT == 1)
+            x[0] = __half2float(__ushort_as_half(r));
+        else
+            x[0] = __uint_as_float((uint32_t)r << 16);
+    }
+    static __device__ __forceinline__ void load(const void *p, int64_t i, float *x) { unpack(fetch(p, i), x); }
     static __device__ __forceinline__ void store(void *p, int64_t i, const float *x) {
         if constexpr (W > 1) {
             uint4 v;
@@ -128,9 +140,25 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*sh)[32], int 
     return s;
 }
 
+// A row's scale from its largest absolute value, and what a value is rounded to
+// its code from.  A largest value under 2^-100 would overflow the reciprocal:
+// such rows are brought up by 2^64 first.  A row that is not finite has codes 0
+// under a scale of NaN.
+struct Codes {
+    float scale, up, f;
+    bool finite;
+    __device__ __forceinline__ explicit Codes(float most) {
+        finite = most < INFINITY;
+        up = most < 0x1p-100f ? 0x1p64f : 1.f;
+        f = finite && most > 0.f ? 127.f / (most * up) : 0.f;
+        scale = finite ? most / 127.f : __int_as_float(0x7FC00000);
+    }
+    __device__ __forceinline__ float of(float x) const { return finite ? x * up * f : 0.f; }
+};
+
 // NORM = false: the rows themselves in 8 bits.
 template <int DT, int W, int E, bool NORM, bool Q>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
     using P = Part<DT, W>;
     constexpr int NV = E / W;
     __shared__ float sh_sum[2][32];
@@ -188,20 +216,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
 #pragma unroll
             for (int j = 0; j < W; ++j) top = max(top, __float_as_uint(fabsf(v[i][j])));
         }
-        const float most = __uint_as_float(row_max(top, sh_max, 0));
-        // A largest value under 2^-100 would overflow the reciprocal: such rows
-        // are brought up by 2^64 first.  A row that is not finite has codes 0
-        // under a scale of NaN.
-        const bool finite = most < INFINITY;
-        const float up = most < 0x1p-100f ? 0x1p64f : 1.f;
-        const float f = finite && most > 0.f ? 127.f / (most * up) : 0.f;
-        if (in && threadIdx.x == 0) a.scale[row] = finite ? most / 127.f : __int_as_float(0x7FC00000);
+        const Codes k(__uint_as_float(row_max(top, sh_max, 0)));
+        if (in && threadIdx.x == 0) a.scale[row] = k.scale;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
             if (in && c < H) {
 #pragma unroll
-                for (int j = 0; j < W; ++j) v[i][j] = finite ? v[i][j] * up * f : 0.f;
+                for (int j = 0; j < W; ++j) v[i][j] = k.of(v[i][j]);
                 P::store_codes(static_cast<int8_t *>(a.out), row * a.os + c, v[i]);
             }
         }
@@ -210,8 +232,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
 
 // Rows go round the CTAs, so that a thread keeps its columns' part of dw in
 // registers; a part a CTA (and row of threads) goes to the workspace.
-template <int DT, int W, int E>
-__global__ void __launch_bounds__(kNormThreads) norm_back_kernel(NormBackArgs a) {
+template <int DT, int W, int E, bool BIG>
+__global__ void __launch_bounds__(norm_threads(BIG)) norm_back_kernel(NormBackArgs a) {
+    constexpr bool AHEAD = W > 1 && !BIG;  // whether the registers hold the next row
     using P = Part<DT, W>;
     constexpr int NV = E / W;
     __shared__ float sh[2][32];
@@ -222,22 +245,37 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(NormBackArgs a)
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < W; ++j) acc[i][j] = 0.f;
-    int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < a.N; r0 += (int64_t)gridDim.x * blockDim.y, turn ^= 1) {
-        const int64_t row = r0 + threadIdx.y;
-        const bool in = row < a.N;
-        const float rstd = in ? a.rstd[row] : 0.f;
-        float h[NV][W], f[NV][W], dot = 0.f;
+    typename P::Raw rx[NV], rg[NV], rr[NV];
+    float next = 0.f;
+    const auto fetch = [&](int64_t row) {
+        if (row >= a.N) return;
+        next = a.rstd[row];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
-#pragma unroll
-            for (int j = 0; j < W; ++j) h[i][j] = f[i][j] = 0.f;
-            if (in && c < H) {
-                P::load(a.x, row * a.xs + c, h[i]);
-                P::load(a.g, row * a.gs + c, f[i]);
+            if (c < H) {
+                rx[i] = P::fetch(a.x, row * a.xs + c);
+                rg[i] = P::fetch(a.g, row * a.gs + c);
+                if (a.gr) rr[i] = P::fetch(a.gr, row * a.grs + c);
             }
         }
+    };
+    int turn = 0;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.y;
+    if (AHEAD) fetch((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
+    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < a.N; r0 += stride, turn ^= 1) {
+        const int64_t row = r0 + threadIdx.y;
+        const bool in = row < a.N;
+        if (!AHEAD) fetch(row);
+        const float rstd = next;
+        float h[NV][W], f[NV][W], add[NV][W], dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            P::unpack(rx[i], h[i]);
+            P::unpack(rg[i], f[i]);
+            P::unpack(rr[i], add[i]);
+        }
+        if (AHEAD) fetch(row + stride);  // under this row's sums
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
@@ -258,12 +296,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(NormBackArgs a)
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
             if (in && c < H) {
-                float add[W];
 #pragma unroll
-                for (int j = 0; j < W; ++j) add[j] = 0.f;
-                if (a.gr) P::load(a.gr, row * a.grs + c, add);
-#pragma unroll
-                for (int j = 0; j < W; ++j) f[i][j] = fmaf(rstd, fmaf(-h[i][j], mean, f[i][j]), add[j]);
+                for (int j = 0; j < W; ++j)
+                    f[i][j] = fmaf(rstd, fmaf(-h[i][j], mean, f[i][j]), a.gr ? add[i][j] : 0.f);
                 P::store(a.dx, row * a.dxs + c, f[i]);
             }
         }
@@ -274,6 +309,193 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(NormBackArgs a)
 #pragma unroll
         for (int j = 0; j < W; ++j)
             if (c0 + i * step + j < H) a.part[part * a.H + c0 + i * step + j] = acc[i][j];
+}
+
+// Many long rows: a persistent CTA goes through its rows with the next ones on
+// their way into shared memory by bulk copies, and its columns' weights in
+// registers.  A stage is free once every thread is past the barrier of the row
+// after it, so that copies run STAGES - 1 rows ahead.
+struct RowRing {
+    uint8_t *mem;
+    uint64_t *full;
+    int *dead;  // a wait ran out: the CTA finishes without waiting
+    int stages, rows;
+    uint32_t bytes;  // of a row
+    int64_t n, first, step;  // rows in all, this CTA's first, and from one to the next
+    // The i-th row of this CTA: `src` gives the rows of each input.
+    template <class F>
+    __device__ __forceinline__ void issue(int i, F src) const {
+        const int64_t row = first + i * step;
+        if (threadIdx.x != 0 || row >= n) return;
+        const int s = i % stages;
+        mbar_arrive_expect_tx(&full[s], bytes * rows);
+        for (int j = 0; j < rows; ++j) bulk_g2s(mem + (size_t)(s * rows + j) * bytes, src(j, row), bytes, &full[s]);
+    }
+    __device__ __forceinline__ const uint8_t *wait(int i) const {
+        const int s = i % stages;
+        if (*(volatile int *)dead == 0 && !mbar_wait_bounded(&full[s], (i / stages) & 1u, &g_norm_status)) *(volatile int *)dead = 1;
+        return mem + (size_t)s * rows * bytes;
+    }
+    // No copy may land after the CTA is gone (they all have, unless a wait ran out).
+    __device__ __forceinline__ void finish(int done) const {
+        if (threadIdx.x != 0 || *(volatile int *)dead == 0) return;
+        for (int i = done < stages ? 0 : done - stages; first + i * step < n && i < done + stages; ++i)
+            mbar_wait_bounded(&full[i % stages], (i / stages) & 1u, &g_norm_status);
+    }
+};
+__device__ __forceinline__ RowRing make_ring(uint8_t *raw, uint64_t *full, int *dead, int stages, int rows, uint32_t bytes,
+                                             int64_t n) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+        *dead = 0;
+        mbar_init_fence();
+    }
+    __syncthreads();
+    return RowRing{raw, full, dead, stages, rows, bytes, n, blockIdx.x, gridDim.x};
+}
+constexpr int kRingStages = 4;
+// 384 threads: two CTAs an SM with up to 85 registers a thread (128 would leave
+// one, 64 spill); more, for rows of over 6,144 elements, 64.
+constexpr int ring_threads(bool big) { return big ? 1024 : 384; }
+
+template <int DT, bool Q, bool BIG>
+__global__ void __launch_bounds__(ring_threads(BIG), BIG ? 1 : 2) norm_ring_kernel(NormArgs a, int stages) {
+    constexpr int W = Elem<DT>::AE, NV = kNormElems / W;
+    using P = Part<DT, W>;
+    extern __shared__ __align__(16) uint8_t raw[];
+    __shared__ uint64_t full[kRingStages];
+    __shared__ int dead;
+    __shared__ float sh_sum[2][32];
+    __shared__ uint32_t sh_max[2][32];
+    const int H = (int)a.H, step = blockDim.x * W, c0 = threadIdx.x * W;
+    const RowRing ring = make_ring(raw, full, &dead, stages, a.r ? 2 : 1, (uint32_t)(H * Elem<DT>::SIZE), a.N);
+    const auto src = [&](int j, int64_t row) {
+        return static_cast<const uint8_t *>(j == 0 ? a.x : a.r) + row * (j == 0 ? a.xs : a.rs) * Elem<DT>::SIZE;
+    };
+    for (int i = 0; i < stages - 1; ++i) ring.issue(i, src);
+    float w[NV][W];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (c0 + i * step < H) P::weight(a.w, a.w_f32, c0 + i * step, w[i]);
+    int it = 0;
+    for (int64_t row = ring.first; row < a.N; row += ring.step, ++it) {
+        const uint8_t *in = ring.wait(it);
+        float v[NV][W], s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + i * step;
+            if (c < H) {
+                P::load(in, c, v[i]);
+                if (a.r) {
+                    float r[W];
+                    P::load(in + ring.bytes, c, r);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[i][j] = P::held(v[i][j] + r[j]);
+                    if (a.res) P::store(a.res, row * a.ress + c, v[i]);
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j) s = fmaf(v[i][j], v[i][j], s);
+            }
+        }
+        s = row_sum(s, sh_sum, it & 1);
+        ring.issue(it + stages - 1, src);
+        const float rstd = 1.f / sqrtf(s / (float)H + a.eps);
+        if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + i * step;
+            if (c < H) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    v[i][j] = v[i][j] * rstd * w[i][j];
+                    top = max(top, __float_as_uint(fabsf(v[i][j])));
+                }
+                if (!Q) P::store(a.out, row * a.os + c, v[i]);
+            }
+        }
+        if constexpr (Q) {
+            const Codes k(__uint_as_float(row_max(top, sh_max, it & 1)));
+            if (threadIdx.x == 0) a.scale[row] = k.scale;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = c0 + i * step;
+                if (c < H) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[i][j] = k.of(v[i][j]);
+                    P::store_codes(static_cast<int8_t *>(a.out), row * a.os + c, v[i]);
+                }
+            }
+        }
+    }
+    ring.finish(it);
+}
+
+template <int DT, bool BIG>
+__global__ void __launch_bounds__(ring_threads(BIG), BIG ? 1 : 2) norm_back_ring_kernel(NormBackArgs a, int stages) {
+    constexpr int W = Elem<DT>::AE, NV = kNormElems / W;
+    using P = Part<DT, W>;
+    extern __shared__ __align__(16) uint8_t raw[];
+    __shared__ uint64_t full[kRingStages];
+    __shared__ int dead;
+    __shared__ float sh[2][32];
+    const int H = (int)a.H, step = blockDim.x * W, c0 = threadIdx.x * W;
+    const RowRing ring = make_ring(raw, full, &dead, stages, a.gr ? 3 : 2, (uint32_t)(H * Elem<DT>::SIZE), a.N);
+    const auto src = [&](int j, int64_t row) {
+        const void *p = j == 0 ? a.x : j == 1 ? a.g : a.gr;
+        return static_cast<const uint8_t *>(p) + row * (j == 0 ? a.xs : j == 1 ? a.gs : a.grs) * Elem<DT>::SIZE;
+    };
+    for (int i = 0; i < stages - 1; ++i) ring.issue(i, src);
+    float w[NV][W], acc[NV][W];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[i][j] = 0.f;
+        if (c0 + i * step < H) P::weight(a.w, a.w_f32, c0 + i * step, w[i]);
+    }
+    int it = 0;
+    for (int64_t row = ring.first; row < a.N; row += ring.step, ++it) {
+        const float rstd = a.rstd[row];
+        const uint8_t *in = ring.wait(it);
+        float h[NV][W], f[NV][W], dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + i * step;
+            if (c < H) {
+                P::load(in, c, h[i]);
+                P::load(in + ring.bytes, c, f[i]);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    h[i][j] *= rstd;
+                    acc[i][j] = fmaf(f[i][j], h[i][j], acc[i][j]);
+                    f[i][j] *= w[i][j];
+                    dot = fmaf(f[i][j], h[i][j], dot);
+                }
+            }
+        }
+        const float mean = row_sum(dot, sh, it & 1) / (float)H;
+        // every thread is past the row before, whose stage the next copy takes
+        ring.issue(it + stages - 1, src);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + i * step;
+            if (c < H) {
+                float add[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j) add[j] = 0.f;
+                if (a.gr) P::load(in + 2 * ring.bytes, c, add);
+#pragma unroll
+                for (int j = 0; j < W; ++j) f[i][j] = fmaf(rstd, fmaf(-h[i][j], mean, f[i][j]), add[j]);
+                P::store(a.dx, row * a.dxs + c, f[i]);
+            }
+        }
+    }
+    ring.finish(it);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (c0 + i * step < H) a.part[blockIdx.x * a.H + c0 + i * step + j] = acc[i][j];
 }
 
 // dw: 32 columns a CTA, the parts over 32 rows of threads, then a tree.
@@ -298,23 +520,54 @@ dim3 norm_block(int64_t H, int E) {
     return dim3(t, t >= 128 ? 1 : 128 / t);
 }
 // Elements a thread: few for short rows, so that enough loads are under way.
-int norm_elems(int64_t H) { return H <= 2048 ? 8 : H <= 8192 ? 16 : 32; }
+int norm_elems(int64_t H) { return H <= 2048 ? 8 : kNormElems; }
+
+// Whether many long rows go through shared memory, and how.  Fewer than four
+// rows an SM leave nothing to fetch ahead.
+struct RingPlan {
+    int stages, ctas;  // 0: no ring
+    size_t smem;
+};
+RingPlan ring_plan(int64_t N, int64_t H, int es, int rows) {
+    RingPlan p = {0, 0, 0};
+    if (H <= 2048 || N < 4 * 152) return p;
+    const size_t stage = (size_t)H * es * rows;
+    p.ctas = stage <= 32 * 1024 ? 2 : 1;
+    p.stages = (int)((size_t)(200 * 1024) / p.ctas / stage);
+    if (p.stages > kRingStages) p.stages = kRingStages;
+    if (p.stages < 2) p.stages = 0;
+    p.smem = stage * p.stages;
+    return p;
+}
 
 template <int DT, int W, bool NORM, bool Q>
 const void *norm_fn(int E) {
-    return E == 8    ? reinterpret_cast<const void *>(&norm_kernel<DT, W, 8, NORM, Q>)
-           : E == 16 ? reinterpret_cast<const void *>(&norm_kernel<DT, W, 16, NORM, Q>)
-                     : reinterpret_cast<const void *>(&norm_kernel<DT, W, 32, NORM, Q>);
+    return E == 8 ? reinterpret_cast<const void *>(&norm_kernel<DT, W, 8, NORM, Q>)
+                  : reinterpret_cast<const void *>(&norm_kernel<DT, W, kNormElems, NORM, Q>);
 }
 template <int DT, int W>
 const void *norm_form(int E, bool norm, bool q) {
     return !norm ? norm_fn<DT, W, false, true>(E) : q ? norm_fn<DT, W, true, true>(E) : norm_fn<DT, W, true, false>(E);
 }
+template <int DT, bool BIG>
+const void *norm_ring_fn(bool q) {
+    return q ? reinterpret_cast<const void *>(&norm_ring_kernel<DT, true, BIG>)
+             : reinterpret_cast<const void *>(&norm_ring_kernel<DT, false, BIG>);
+}
+template <int DT>
+const void *norm_ring_fn(bool q, bool big) {
+    return big ? norm_ring_fn<DT, true>(q) : norm_ring_fn<DT, false>(q);
+}
 template <int DT, int W>
-const void *back_fn(int E) {
-    return E == 8    ? reinterpret_cast<const void *>(&norm_back_kernel<DT, W, 8>)
-           : E == 16 ? reinterpret_cast<const void *>(&norm_back_kernel<DT, W, 16>)
-                     : reinterpret_cast<const void *>(&norm_back_kernel<DT, W, 32>);
+const void *back_fn(int E, bool big) {
+    return E == 8 ? reinterpret_cast<const void *>(&norm_back_kernel<DT, W, 8, false>)
+           : big  ? reinterpret_cast<const void *>(&norm_back_kernel<DT, W, kNormElems, true>)
+                  : reinterpret_cast<const void *>(&norm_back_kernel<DT, W, kNormElems, false>);
+}
+template <int DT>
+const void *back_ring_fn(bool big) {
+    return big ? reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, true>)
+               : reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, false>);
 }
 
 // Whether every row of a tensor starts on `bytes` (a row alone needs no stride).
@@ -330,6 +583,18 @@ int norm_launch(const NormArgs &args, int dtype, bool norm, bool q, cudaStream_t
     const bool vec = a.H % ae == 0 && rows_on(a.x, a.xs, a.N, es, 16) && rows_on(a.r, a.rs, a.N, es, 16) &&
                      rows_on(a.res, a.ress, a.N, es, 16) && rows_on(a.w, 0, 1, 1, 16) &&
                      rows_on(a.out, a.os, a.N, q ? 1 : es, q ? ae : 16);
+    const RingPlan ring = vec && norm ? ring_plan(a.N, a.H, es, a.r ? 2 : 1) : RingPlan{0, 0, 0};
+    if (ring.stages > 0) {
+        const bool big = a.H > kNormElems * ring_threads(false);
+        const void *fn = dtype == 0 ? norm_ring_fn<0>(q, big) : dtype == 1 ? norm_ring_fn<1>(q, big) : norm_ring_fn<2>(q, big);
+        if (prepare_kernel(fn, ring.smem, 1) != 0) return -1;
+        int stages = ring.stages;
+        void *params[] = {&a, &stages};
+        return cudaLaunchKernel(fn, dim3((unsigned)(152 * ring.ctas)), norm_block(a.H, kNormElems), params, ring.smem, st) ==
+                       cudaSuccess
+                   ? 0
+                   : -1;
+    }
     const int E = norm_elems(a.H);
     const void *fn = dtype == 0   ? (vec ? norm_form<0, 4>(E, norm, q) : norm_form<0, 1>(E, norm, q))
                      : dtype == 1 ? (vec ? norm_form<1, 8>(E, norm, q) : norm_form<1, 1>(E, norm, q))
@@ -339,6 +604,12 @@ int norm_launch(const NormArgs &args, int dtype, bool norm, bool q, cudaStream_t
     return cudaLaunchKernel(fn, dim3((unsigned)((a.N + block.y - 1) / block.y)), block, params, 0, st) == cudaSuccess
                ? 0
                : -1;
+}
+
+unsigned int *norm_status_ptr() {
+    void *p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_norm_status) != cudaSuccess) return nullptr;
+    return reinterpret_cast<unsigned int *>(p);
 }
 
 // Parts of dw: two CTAs an SM, and no more than there are rows.
@@ -355,10 +626,20 @@ int norm_back_launch(const NormBackArgs &args, int dtype, cudaStream_t st) {
     const int E = norm_elems(a.H);
     const dim3 block = norm_block(a.H, E);
     int64_t parts = norm_back_parts(a.N, a.H);
-    if (a.N > 0) {
-        const void *fn = dtype == 0   ? (vec ? back_fn<0, 4>(E) : back_fn<0, 1>(E))
-                         : dtype == 1 ? (vec ? back_fn<1, 8>(E) : back_fn<1, 1>(E))
-                                      : (vec ? back_fn<2, 8>(E) : back_fn<2, 1>(E));
+    const RingPlan ring = vec ? ring_plan(a.N, a.H, es, a.gr ? 3 : 2) : RingPlan{0, 0, 0};
+    if (ring.stages > 0) {
+        const bool big = a.H > kNormElems * ring_threads(false);
+        const void *fn = dtype == 0 ? back_ring_fn<0>(big) : dtype == 1 ? back_ring_fn<1>(big) : back_ring_fn<2>(big);
+        if (prepare_kernel(fn, ring.smem, 1) != 0) return -1;
+        int stages = ring.stages;
+        void *params[] = {&a, &stages};
+        parts = 152 * ring.ctas;
+        if (cudaLaunchKernel(fn, dim3((unsigned)parts), block, params, ring.smem, st) != cudaSuccess) return -1;
+    } else if (a.N > 0) {
+        const bool big = a.H > kNormElems * norm_threads(false);
+        const void *fn = dtype == 0   ? (vec ? back_fn<0, 4>(E, big) : back_fn<0, 1>(E, big))
+                         : dtype == 1 ? (vec ? back_fn<1, 8>(E, big) : back_fn<1, 1>(E, big))
+                                      : (vec ? back_fn<2, 8>(E, big) : back_fn<2, 1>(E, big));
         void *params[] = {&a};
         if (cudaLaunchKernel(fn, dim3((unsigned)(parts / block.y)), block, params, 0, st) != cudaSuccess) return -1;
     }
