@@ -82,11 +82,16 @@ __global__ void __launch_bounds__(256) int8_hidden_kernel(const Int8Args a) {
 }
 
 // One persistent CTA an SM.  Warp 0 fetches 128 columns of the weight's rows
-// (a lane of tensor memory each) and of N hidden rows by TMA into a ring of
-// stages; eight warps turn the weight's bytes into f16 in tensor memory, two
-// groups of four taking stages in turn (a stage's 64 columns of it are free when
-// the stage is); warp 1 issues the products; four or eight warps take finished sums from one half of the
-// accumulators while the next products fill the other half.
+// (a lane of tensor memory each) by TMA into one ring of stages, warp 2 the same
+// columns of N hidden rows into another; eight warps turn the weight's bytes into
+// f16 in four slots of tensor memory, two groups of four taking steps in turn;
+// warp 1 issues the products; four or eight warps take finished sums from one
+// half of the accumulators while the next products fill the other half.
+//
+// Rings of their own: a stage of the weight is free as soon as it is in tensor
+// memory, 700 cycles after it landed, and not after its products, 1,500 to 2,000
+// cycles later; with one ring for both (112 KB of the weight under way) 16 rows x
+// 128,256 x 5,120 took 134 us.
 //
 // Up to 128 hidden rows the kernel is a stream of the weight, and the vocabulary
 // is cut into one run of rows a CTA, a multiple of 32, so that every SM moves
@@ -94,23 +99,37 @@ __global__ void __launch_bounds__(256) int8_hidden_kernel(const Int8Args a) {
 // more hidden rows tiles go through those first, so that a weight tile comes from
 // HBM once and from L2 for the other blocks.
 //
-// A copy or product that one thread issues costs it some 100 cycles, and more
-// where its operands are not the same in the whole warp: whole tiles are one copy
-// each (six a stage had bound the kernel: 16 rows x 128,256 x 5,120 235 us), and
-// the two issuing warps go through their loops together.
-constexpr int kI8K = kInt8Stage;       // columns of a stage
-constexpr int kI8Chunk = 1024 / kI8K;  // stages whose sums are exact
+// A copy or product that one thread issues costs it some 100 cycles, ten times
+// what it costs a warp that goes through its loop together: whole tiles are one
+// copy each (with six a stage and single threads issuing, 16 rows took 235 us).
+constexpr int kI8K = kInt8Stage;       // columns of a step
+constexpr int kI8Chunk = 1024 / kI8K;  // steps whose sums are exact
+constexpr int kI8Slots = 4;            // of the weight in tensor memory, 64 columns each
 
 template <int N>
 struct Int8Shape {
-    static constexpr int A_BYTES = 128 * kI8K, B_BYTES = N * kI8K * 2, STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = N <= 32 ? 7 : N == 64 ? 6 : 4;
-    static constexpr int SUMS = 512 - 64 * STAGES < 256 ? (512 - 64 * STAGES) / 2 : 128;  // columns of half the sums
-    static constexpr int SMEM = STAGES * STAGE + 1024;
+    static constexpr int A_BYTES = 128 * kI8K, B_BYTES = N * kI8K * 2;
+    // Stages of the two rings; the weight's even, as two groups of warps take them in turn.  The hidden rows' copies
+    // come from L2 but take longer, as all SMs ask for the same lines at once: 64 rows x 128,256 x 5,120 take 136 us
+    // with ten stages and four, 120 with eight and six, and 128 rows 153 with six and four, 147 with four and five.
+    static constexpr int A_STAGES = N <= 32 ? 10 : N == 64 ? 8 : 4;
+    static constexpr int B_STAGES = N <= 16 ? 16 : N <= 64 ? 6 : 5;
+    static_assert(A_STAGES % 2 == 0, "a group of warps meets a stage in each of its phases");
+    static constexpr int SMEM = A_STAGES * A_BYTES + B_STAGES * B_BYTES + 1024;
     static constexpr int EPI = N <= 32 ? 4 : 8;  // warps that take the sums
     static constexpr int NC = N <= 32 ? N : N / 2;
-    static constexpr int THREADS = 64 + 256 + 32 * EPI;
+    static constexpr int THREADS = 128 + 256 + 32 * EPI;
     static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(N / 8) << 17) | (8u << 24);  // f16, fp32 sums, M = 128
+};
+
+// A warp's way round a ring: the stage, and the phase that it waits for.
+template <int STAGES>
+struct Int8Place {
+    uint32_t s = 0, phase;
+    __device__ __forceinline__ explicit Int8Place(uint32_t p) : phase(p) {}
+    __device__ __forceinline__ void next() {
+        if (++s == STAGES) s = 0, phase ^= 1u;
+    }
 };
 
 template <int DT>
@@ -128,11 +147,13 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
     int8_scores_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_part,
                        const __grid_constant__ CUtensorMap map_h, const Int8Args a, int32_t row_blocks, int32_t tiles, int32_t run) {
     using S = Int8Shape<N>;
-    constexpr int STAGES = S::STAGES, NC = S::NC;
+    constexpr int NA = S::A_STAGES, NB = S::B_STAGES, NC = S::NC;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[STAGES], empty[STAGES], a_full[STAGES], done[2], drained[2], last;
+    __shared__ uint64_t w_full[NA], w_empty[NA], h_full[NB], h_empty[NB], a_full[kI8Slots], a_empty[kI8Slots], done[2],
+        drained[2], last;
     __shared__ uint32_t tmem_slot;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *ring_h = ring + NA * S::A_BYTES;
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int steps = (int)((a.H + kI8K - 1) / kI8K);
     // run > 0: this CTA's vocabulary rows; else whole tiles, in turn
@@ -143,10 +164,17 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
     const auto tile_v = [&](int32_t t) { return run > 0 ? v_first + t * 128 : t / row_blocks * 128; };
     const auto tile_m = [&](int32_t t) { return run > 0 ? 0 : t % row_blocks * N; };
     if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+        for (int i = 0; i < NA; ++i) {
+            mbar_init(&w_full[i], 1);
+            mbar_init(&w_empty[i], 128);
+        }
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(&h_full[i], 1);
+            mbar_init(&h_empty[i], 1);
+        }
+        for (int i = 0; i < kI8Slots; ++i) {
             mbar_init(&a_full[i], 128);
+            mbar_init(&a_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&done[i], 1);
@@ -155,102 +183,112 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
         mbar_init(&last, 1);
         mbar_init_fence();
     }
-    if (warp == 1) tmem_alloc(&tmem_slot, 512);
+    if (warp == 3) tmem_alloc(&tmem_slot, 512);
     mma_fence_before();
     __syncthreads();
     mma_fence_after();
-    const uint32_t tmem = tmem_slot, slots = tmem + 512 - 64 * STAGES;
+    const uint32_t tmem = tmem_slot, slots = tmem + 256;
 
     if (warp == 0) {
-        uint32_t it = 0;
+        Int8Place<NA> at(1);
+        uint32_t uses = 0;
         bool ok = true;
-        const auto weight = [&](uint32_t s, int32_t v, int k) {
-            uint8_t *st = ring + (size_t)s * S::STAGE;
-            const int32_t left = v_end - v;
-            if (lane == 0) {
-                if (left > 96) {
-                    mbar_arrive_expect_tx(&full[s], S::STAGE);
-                    tma_tile(st, &map_w, k * kI8K, v, &full[s]);
-                } else {
-                    const int groups = (left + 31) / 32;
-                    mbar_arrive_expect_tx(&full[s], (uint32_t)(groups * (S::A_BYTES / 4) + S::B_BYTES));
-                    for (int i = 0; i < groups; ++i)
-                        tma_tile(st + i * (S::A_BYTES / 4), &map_part, k * kI8K, v + 32 * i, &full[s]);
-                }
-            }
-        };
-        // the weight does not wait for the kernel that makes the hidden rows
-        uint32_t ahead = 0;
-        for (int32_t t = t_first; t < t_end && ahead < STAGES; t += t_step)
-            for (int k = 0; k < steps && ahead < STAGES; ++k, ++ahead) weight(ahead, tile_v(t), k);
-        pdl_wait_primary();
-        uint32_t s = 0, phase = 1;
         for (int32_t t = t_first; ok && t < t_end; t += t_step) {
-            const int32_t v = tile_v(t), m = tile_m(t);
-            for (int k = 0; k < steps; ++k, ++it) {
-                if (it >= ahead) {
-                    ok = int8_warp_wait(&empty[s], phase);
-                    if (!ok) break;
-                    weight(s, v, k);
+            const int32_t v = tile_v(t), left = v_end - v;
+            for (int k = 0; k < steps; ++k, ++uses, at.next()) {
+                ok = int8_warp_wait(&w_empty[at.s], at.phase);
+                if (!ok) break;
+                if (elect_one()) {
+                    uint8_t *st = ring + at.s * S::A_BYTES;
+                    if (left > 96) {
+                        mbar_arrive_expect_tx(&w_full[at.s], S::A_BYTES);
+                        tma_tile(st, &map_w, k * kI8K, v, &w_full[at.s]);
+                    } else {
+                        const int groups = (left + 31) / 32;
+                        mbar_arrive_expect_tx(&w_full[at.s], (uint32_t)(groups * (S::A_BYTES / 4)));
+                        for (int i = 0; i < groups; ++i)
+                            tma_tile(st + i * (S::A_BYTES / 4), &map_part, k * kI8K, v + 32 * i, &w_full[at.s]);
+                    }
                 }
-                if (lane == 0) tma_tile_3d(ring + (size_t)s * S::STAGE + S::A_BYTES, &map_h, 0, m, 2 * k, &full[s]);
-                if (++s == STAGES) s = 0, phase ^= 1u;
+                __syncwarp();
             }
         }
-        // no copy may land, and no commit arrive, after the CTA is gone
-        const uint32_t n = it < STAGES ? it : STAGES;
-        for (uint32_t i = it - n; i < it; ++i)
-            int8_warp_wait(ok ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u);
+        // no copy may land after the CTA is gone
+        for (uint32_t i = uses < NA ? 0 : uses - NA; i < uses; ++i) int8_warp_wait(&w_full[i % NA], (i / NA) & 1u);
+    } else if (warp == 2) {
+        pdl_wait_primary();  // (the weight does not wait for the kernel that makes the hidden rows)
+        Int8Place<NB> at(1);
+        uint32_t uses = 0;
+        bool ok = true;
+        for (int32_t t = t_first; ok && t < t_end; t += t_step) {
+            const int32_t m = tile_m(t);
+            for (int k = 0; k < steps; ++k, ++uses, at.next()) {
+                ok = int8_warp_wait(&h_empty[at.s], at.phase);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&h_full[at.s], S::B_BYTES);
+                    tma_tile_3d(ring_h + at.s * S::B_BYTES, &map_h, 0, m, 2 * k, &h_full[at.s]);
+                }
+                __syncwarp();
+            }
+        }
+        for (uint32_t i = uses < NB ? 0 : uses - NB; i < uses; ++i)
+            int8_warp_wait(ok ? &h_empty[i % NB] : &h_full[i % NB], (i / NB) & 1u);
     } else if (warp == 1) {
-        uint32_t j = 0, s = 0, phase = 0;
-        const uint64_t desc = smem_tile(ring + S::A_BYTES);
+        Int8Place<kI8Slots> slot(0);
+        Int8Place<NB> at(0);
+        uint32_t j = 0, uses = 0;
+        const uint64_t desc = smem_tile(ring_h);
         const uint32_t lo = (uint32_t)desc, hi = (uint32_t)(desc >> 32);
         bool ok = true, ready = false;
         for (int32_t t = t_first; ok && t < t_end; t += t_step) {
             for (int k = 0; k < steps; ++k) {
-                const uint32_t b = j & 1u;
+                const uint32_t b = j & 1u, s = at.s, l = slot.s;
                 if (k % kI8Chunk == 0) ok = int8_warp_wait(&drained[b], ((j >> 1) & 1u) ^ 1u);
-                // (the hidden rows have landed too: who filled the slot waited for the stage)
-                ok = ok && (ready || int8_warp_wait(&a_full[s], phase));
+                ok = ok && (ready || (int8_warp_wait(&h_full[s], at.phase) && int8_warp_wait(&a_full[l], slot.phase)));
                 if (!ok) break;
                 mma_fence_after();
                 // a look at the next step, whose answer comes while this one's products are issued
-                const uint32_t s1 = s + 1 == STAGES ? 0 : s + 1, phase1 = s1 == 0 ? phase ^ 1u : phase;
-                const bool seen = mbar_test_wait(&a_full[s1], phase1);
-                const uint32_t d = tmem + b * S::SUMS, sa = slots + s * 64, sb = lo + s * (S::STAGE >> 4);
+                at.next();
+                slot.next();
+                const bool seen = mbar_test_wait(&h_full[at.s], at.phase) && mbar_test_wait(&a_full[slot.s], slot.phase);
+                const uint32_t d = tmem + b * 128, sa = slots + l * 64, sb = lo + s * (S::B_BYTES >> 4);
                 const bool end = k % kI8Chunk == kI8Chunk - 1 || k == steps - 1;
+                ++uses;
                 if (elect_one()) {
 #pragma unroll
                     for (int p = 0; p < 8; ++p)
                         mma_f16_ts(d, sa + p * 8, sb + (p >> 2) * (S::B_BYTES / 2 >> 4) + (p & 3) * 2, hi, S::IDESC,
                                    k % kI8Chunk > 0 || p > 0);
-                    mma_commit(&empty[s]);
+                    mma_commit(&h_empty[s]);
+                    mma_commit(&a_empty[l]);
                     if (end) mma_commit(&done[b]);
                 }
                 ready = __all_sync(0xFFFFFFFFu, seen);
                 if (end) ++j;
-                s = s1, phase = phase1;
             }
         }
-        // the products are finished before tensor memory is freed
+        // no commit may arrive after the CTA is gone, and the products are finished before tensor memory is freed
         if (elect_one()) mma_commit(&last);
         int8_warp_wait(&last, 0);
-    } else if (warp < 10) {
-        const int quarter = warp & 3, group = (warp - 2) >> 2;
+        for (uint32_t i = uses < kI8Slots ? 0 : uses - kI8Slots; i < uses; ++i)
+            int8_warp_wait(&a_empty[i % kI8Slots], (i / kI8Slots) & 1u);
+    } else if (warp >= 4 && warp < 12) {
+        const int quarter = warp & 3, group = (warp - 4) >> 2;
         const uint32_t at = slots + ((uint32_t)quarter << 21);
         const int row = quarter * 32 + lane;
         uint32_t it = 0;
         bool ok = true;
         for (int32_t t = t_first; ok && t < t_end; t += t_step) {
             for (int k = 0; k < steps; ++k, ++it) {
-                // By the stage, not the step: a group has to see every phase of a barrier that it waits for.  (A
-                // wait for a phase passes while the one before it is open.)
-                const uint32_t s = it % STAGES;
-                if ((s & 1u) != (uint32_t)group) continue;
-                ok = int8_warp_wait(&full[s], (it / STAGES) & 1u);
+                // The rings are even, so that a group sees every phase of the barriers that it waits for.  (A wait
+                // for a phase passes while the one before it is open.)
+                if ((it & 1u) != (uint32_t)group) continue;
+                const uint32_t s = it % NA, l = it % kI8Slots;
+                ok = int8_warp_wait(&w_full[s], (it / NA) & 1u) && int8_warp_wait(&a_empty[l], ((it / kI8Slots) & 1u) ^ 1u);
                 if (!ok) break;
                 mma_fence_after();
-                const uint8_t *src = ring + (size_t)s * S::STAGE + row * kI8K;
+                const uint8_t *src = ring + s * S::A_BYTES + row * kI8K;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t r[32];
@@ -263,15 +301,16 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
                         to_f16(x.w, r[8 * c + 6], r[8 * c + 7]);
                     }
                     __syncwarp();
-                    tmem_store(at + s * 64 + h * 32, r);
+                    tmem_store(at + l * 64 + h * 32, r);
                 }
+                mbar_arrive(&w_empty[s]);
                 tmem_wait_st();
                 mma_fence_before();
-                mbar_arrive(&a_full[s]);
+                mbar_arrive(&a_full[l]);
             }
         }
-    } else {
-        const int quarter = warp & 3, half = (warp - 10) >> 2;
+    } else if (warp >= 12) {
+        const int quarter = warp & 3, half = (warp - 12) >> 2;
         const uint32_t at = tmem + ((uint32_t)quarter << 21) + half * NC;
         const int chunks = (steps + kI8Chunk - 1) / kI8Chunk;
         uint32_t j = 0;
@@ -290,7 +329,7 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
                 for (int q = 0; q < NC; q += 16) {
                     uint32_t r[16];
                     __syncwarp();
-                    TmemLoad<16>::ld(at + b * S::SUMS + q, r);
+                    TmemLoad<16>::ld(at + b * 128 + q, r);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -309,7 +348,7 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
         }
     }
     __syncthreads();
-    if (warp == 1) tmem_free(tmem, 512);
+    if (warp == 3) tmem_free(tmem, 512);
 }
 
 // 8-bit [rows, cols] in boxes of 128 columns.
