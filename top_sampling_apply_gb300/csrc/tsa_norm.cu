@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
 // registers; a part a CTA (and row of threads) goes to the workspace.
 template <int DT, int W, int E, bool BIG>
 __global__ void __launch_bounds__(norm_threads(BIG)) norm_back_kernel(NormBackArgs a) {
-    constexpr bool AHEAD = W > 1 && !BIG;  // whether the registers hold the next row
+    // whether the registers hold the next row too, and the weights
+    constexpr bool AHEAD = !BIG && (W > 1 || E == 8), KEEP = E == 8;
     using P = Part<DT, W>;
     constexpr int NV = E / W;
     __shared__ float sh[2][32];
@@ -262,6 +263,12 @@ __global__ void __launch_bounds__(norm_threads(BIG)) norm_back_kernel(NormBackAr
     };
     int turn = 0;
     const int64_t stride = (int64_t)gridDim.x * blockDim.y;
+    float kept[KEEP ? NV : 1][W];
+    if (KEEP) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (c0 + i * step < H) P::weight(a.w, a.w_f32, c0 + i * step, kept[KEEP ? i : 0]);
+    }
     if (AHEAD) fetch((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
     for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < a.N; r0 += stride, turn ^= 1) {
         const int64_t row = r0 + threadIdx.y;
@@ -281,12 +288,12 @@ __global__ void __launch_bounds__(norm_threads(BIG)) norm_back_kernel(NormBackAr
             const int c = c0 + i * step;
             if (in && c < H) {
                 float w[W];
-                P::weight(a.w, a.w_f32, c, w);
+                if (!KEEP) P::weight(a.w, a.w_f32, c, w);
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     h[i][j] *= rstd;
                     acc[i][j] = fmaf(f[i][j], h[i][j], acc[i][j]);
-                    f[i][j] *= w[j];
+                    f[i][j] *= KEEP ? kept[KEEP ? i : 0][j] : w[j];
                     dot = fmaf(f[i][j], h[i][j], dot);
                 }
             }
@@ -519,8 +526,9 @@ dim3 norm_block(int64_t H, int E) {
     const int t = (int)(((H + E - 1) / E + 31) / 32 * 32);
     return dim3(t, t >= 128 ? 1 : 128 / t);
 }
-// Elements a thread: few for short rows, so that enough loads are under way.
-int norm_elems(int64_t H) { return H <= 2048 ? 8 : kNormElems; }
+// Elements a thread: few for short rows, so that enough loads are under way, and
+// for rows of single elements, of which the registers hold no more than 8 three times.
+int norm_elems(int64_t H, bool vec) { return H <= (vec ? 2048 : 4096) ? 8 : kNormElems; }
 
 // Whether many long rows go through shared memory, and how.  Fewer than four
 // rows an SM leave nothing to fetch ahead.
@@ -559,7 +567,7 @@ const void *norm_ring_fn(bool q, bool big) {
     return big ? norm_ring_fn<DT, true>(q) : norm_ring_fn<DT, false>(q);
 }
 template <int DT, int W>
-const void *back_fn(int E, bool big) {
+const void *back_fn(int E, bool big) {  // big only with 16 elements
     return E == 8 ? reinterpret_cast<const void *>(&norm_back_kernel<DT, W, 8, false>)
            : big  ? reinterpret_cast<const void *>(&norm_back_kernel<DT, W, kNormElems, true>)
                   : reinterpret_cast<const void *>(&norm_back_kernel<DT, W, kNormElems, false>);
@@ -595,7 +603,7 @@ int norm_launch(const NormArgs &args, int dtype, bool norm, bool q, cudaStream_t
                    ? 0
                    : -1;
     }
-    const int E = norm_elems(a.H);
+    const int E = norm_elems(a.H, vec);
     const void *fn = dtype == 0   ? (vec ? norm_form<0, 4>(E, norm, q) : norm_form<0, 1>(E, norm, q))
                      : dtype == 1 ? (vec ? norm_form<1, 8>(E, norm, q) : norm_form<1, 1>(E, norm, q))
                                   : (vec ? norm_form<2, 8>(E, norm, q) : norm_form<2, 1>(E, norm, q));
@@ -613,9 +621,13 @@ unsigned int *norm_status_ptr() {
 }
 
 // Parts of dw: two CTAs an SM, and no more than there are rows.
-int64_t norm_back_parts(int64_t N, int64_t H) {
-    const int64_t y = norm_block(H, norm_elems(H)).y, ctas = (N + y - 1) / y;
+int64_t norm_back_parts(int64_t N, int64_t H, bool vec) {
+    const int64_t y = norm_block(H, norm_elems(H, vec)).y, ctas = (N + y - 1) / y;
     return (ctas < 304 ? ctas : 304) * y;
+}
+int64_t norm_back_parts(int64_t N, int64_t H) {
+    const int64_t a = norm_back_parts(N, H, true), b = norm_back_parts(N, H, false);
+    return a > b ? a : b;
 }
 
 int norm_back_launch(const NormBackArgs &args, int dtype, cudaStream_t st) {
@@ -623,9 +635,9 @@ int norm_back_launch(const NormBackArgs &args, int dtype, cudaStream_t st) {
     const int es = dtype == 0 ? 4 : 2, ae = 16 / es;
     const bool vec = a.H % ae == 0 && rows_on(a.x, a.xs, a.N, es, 16) && rows_on(a.g, a.gs, a.N, es, 16) &&
                      rows_on(a.gr, a.grs, a.N, es, 16) && rows_on(a.dx, a.dxs, a.N, es, 16) && rows_on(a.w, 0, 1, 1, 16);
-    const int E = norm_elems(a.H);
+    const int E = norm_elems(a.H, vec);
     const dim3 block = norm_block(a.H, E);
-    int64_t parts = norm_back_parts(a.N, a.H);
+    int64_t parts = norm_back_parts(a.N, a.H, vec);
     const RingPlan ring = vec ? ring_plan(a.N, a.H, es, a.gr ? 3 : 2) : RingPlan{0, 0, 0};
     if (ring.stages > 0) {
         const bool big = a.H > kNormElems * ring_threads(false);

@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <numeric>
+
 #include "tsa_device.cuh"
 #include "tsa_host.h"
 #include "tsa_tcgen05.cuh"
@@ -700,13 +702,17 @@ int xent_splits(int64_t M, int64_t H, int64_t V) {
     return (int)(n < 64 ? n : 64);
 }
 
-// Pieces of the vocabulary of one size: a piece's part of G takes about 64 MB,
-// half of L2, so that the products find much of it there.
+// The width of a piece of the vocabulary.  Its part of G takes up to 64 MB, half
+// of L2, so that the products find much of it there; and where that leaves a
+// choice, its tiles are a multiple of the SMs (16 blocks of rows: 57 tiles of 256
+// entries are six turns of 152 SMs, 63 would be 6.6).
 int64_t xent_piece(int64_t M, int64_t V) {
-    const int64_t fit = ((int64_t)64 << 20) / (2 * xent_padded(M)) / 256 * 256;
-    const int64_t most = fit < 256 ? 256 : fit < kXentMaxPiece ? fit : kXentMaxPiece;
-    const int64_t pieces = (V + most - 1) / most;
-    return ((V + pieces - 1) / pieces + 255) / 256 * 256;
+    const int64_t blocks = xent_padded(M) / 128, all = (V + 255) / 256;
+    int64_t fit = ((int64_t)64 << 20) / (2 * 128 * 256) / blocks;
+    fit = fit < 1 ? 1 : fit > kXentMaxPiece / 256 ? kXentMaxPiece / 256 : fit;
+    if (fit >= all) return all * 256;
+    const int64_t turn = 152 / std::gcd((int64_t)152, blocks);
+    return (fit < turn ? fit : fit / turn * turn) * 256;
 }
 
 unsigned int *xent_status_ptr() {
