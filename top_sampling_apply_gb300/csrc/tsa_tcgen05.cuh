@@ -101,6 +101,57 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
+// The same by P CTAs of a cluster together (P = 2: each holds 128 of the 256 rows
+// of A and D, and half of B's; the first one issues, from the same places in
+// both, and tells both).
+template <int P>
+__device__ __forceinline__ void tmem_alloc_by(uint32_t *slot, uint32_t cols) {
+    if constexpr (P == 1) {
+        tmem_alloc(slot, cols);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int P>
+__device__ __forceinline__ void tmem_free_by(uint32_t addr, uint32_t cols) {
+    if constexpr (P == 1)
+        tmem_free(addr, cols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+template <int P>
+__device__ __forceinline__ void mma_bf16_by(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    if constexpr (P == 1)
+        mma_bf16(d, a, b, idesc, add);
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
+}
+template <int P>
+__device__ __forceinline__ void mma_commit_by(uint64_t *bar) {
+    if constexpr (P == 1)
+        mma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+}
+// To this CTA alone: nothing arrives at one that may be gone.
+template <int P>
+__device__ __forceinline__ void mma_commit_own(uint64_t *bar) {
+    if constexpr (P == 1)
+        mma_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                     : "memory");
+}
 template <int N> struct TmemLoad;
 template <> struct TmemLoad<16> {
     __device__ static __forceinline__ void ld(uint32_t a, uint32_t (&r)[16]) {
@@ -166,6 +217,39 @@ __device__ __forceinline__ void tma_tile_3d(void *dst, const CUtensorMap *map, i
             "r"(smem_u32(dst)),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
+}
+
+// Copies whose barrier, given by its address in the cluster, may be in the first
+// CTA of the pair.
+template <int P>
+__device__ __forceinline__ void tma_tile_by(void *dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar) {
+    if constexpr (P == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+                "r"(smem_u32(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+            "[%4];" ::"r"(smem_u32(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+template <int P>
+__device__ __forceinline__ void tma_blocks_by(void *dst, const CUtensorMap *map, int32_t y, int32_t z, uint32_t bar) {
+    if constexpr (P == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+                "r"(smem_u32(dst)),
+            "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+            "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+            "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar)
+            : "memory");
 }
 
 // ------------------------------------------------------------ tensor maps

@@ -170,21 +170,26 @@ constexpr int kXentThreads = 320;
 constexpr int kXentSlab = 32 * 128;  // 32 rows of 64 bf16
 constexpr uint32_t kAcrossA = 1u << 15, kAcrossB = 1u << 16;  // instruction descriptor: M or N contiguous instead of K
 
-template <int N>
+// P CTAs work on a tile together.  Two of a cluster take 256 rows, each its 128 and
+// half of the columns' operand, which then passes through L2 and shared memory
+// once for both: a third of the traffic less.  These kernels run at the GPU's power
+// limit, where what is not moved is time.
+template <int N, int P>
 struct XentShape {
-    static constexpr int A_BYTES = 128 * kTcK * 2, B_BYTES = N * kTcK * 2, STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = N == 256 ? 4 : 6;
+    static constexpr int A_BYTES = 128 * kTcK * 2, B_BYTES = N / P * kTcK * 2, STAGE = A_BYTES + B_BYTES;
+    static constexpr int STAGES = 192 * 1024 / STAGE;
     static constexpr int SMEM = STAGES * STAGE + 8 * kXentSlab + 1024;
     static constexpr int NC = N / 2;  // a thread's columns
-    static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N / 8) << 17) | (8u << 24);
+    static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N / 8) << 17) | ((8u * P) << 24);
 };
 
+// (`full`, `drained` and `last` of the pair's first CTA alone are used.)
 template <int STAGES>
 struct XentBars {
     uint64_t full[STAGES], empty[STAGES], done[2], drained[2], last;
     uint32_t tmem;
 };
-template <int STAGES>
+template <int P, int STAGES>
 __device__ __forceinline__ void xent_setup(XentBars<STAGES> &s, uint32_t cols) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -193,15 +198,42 @@ __device__ __forceinline__ void xent_setup(XentBars<STAGES> &s, uint32_t cols) {
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.done[i], 1);
-            mbar_init(&s.drained[i], 256);
+            mbar_init(&s.drained[i], 8 * P);
         }
         mbar_init(&s.last, 1);
         mbar_init_fence();
     }
-    if ((threadIdx.x >> 5) == 1) tmem_alloc(&s.tmem, cols);
+    __syncthreads();
+    if constexpr (P > 1) cluster_sync();  // the barriers are there before the other CTA's arrivals
+    if ((threadIdx.x >> 5) == 1) tmem_alloc_by<P>(&s.tmem, cols);
     mma_fence_before();
     __syncthreads();
     mma_fence_after();
+}
+template <int P>
+__device__ __forceinline__ void xent_close(uint32_t tmem, uint32_t cols) {
+    __syncthreads();
+    if constexpr (P > 1) cluster_sync();  // nothing of this CTA is read or arrived at any more
+    if ((threadIdx.x >> 5) == 1) tmem_free_by<P>(tmem, cols);
+}
+// This warp has read its sums: to the CTA that issues.
+template <int P>
+__device__ __forceinline__ void xent_drained(uint64_t *bar, int lane) {
+    mma_fence_before();
+    __syncwarp();
+    if (lane != 0) return;
+    if constexpr (P == 1)
+        mbar_arrive(bar);
+    else
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(dsmem_addr(bar, 0)) : "memory");
+}
+// The issuing warp's wait for them.
+template <int P>
+__device__ __forceinline__ bool xent_wait_drained(uint64_t *bar, uint32_t parity) {
+    const bool ok = xent_warp_wait(bar, parity);
+    if constexpr (P > 1) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    mma_fence_after();
+    return ok;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -212,7 +244,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // A warp's way round the ring, together: a stage, its barriers, and their
 // phase.  One lane issues, from operands that are the same in all of them
 // (a copy or product costs a thread on its own twice as much).
-template <int STAGES>
+template <int STAGES, int P>
 struct XentRing {
     XentBars<STAGES> &bars;
     uint8_t *ring;
@@ -224,6 +256,11 @@ struct XentRing {
     __device__ __forceinline__ uint64_t *full() const { return &bars.full[s]; }
     __device__ __forceinline__ uint64_t *empty() const { return &bars.empty[s]; }
     __device__ __forceinline__ bool wait_empty() { return ok = xent_warp_wait(empty(), phase); }
+    // What arrives at the issuing CTA's barrier: the copies of both, which its own producer announces.
+    __device__ __forceinline__ uint32_t filled() const { return P == 1 ? smem_u32(full()) : dsmem_addr(full(), 0); }
+    __device__ __forceinline__ void expect(uint32_t rank) const {
+        if (rank == 0) mbar_arrive_expect_tx(full(), P * bytes);
+    }
     // With a look at the next stage, whose answer comes while this one's products are issued.
     __device__ __forceinline__ bool wait_full() {
         ok = ok && (ready || xent_warp_wait(full(), phase));
@@ -237,7 +274,8 @@ struct XentRing {
         ready = __all_sync(0xFFFFFFFFu, seen);
     }
     // No copy may land, and no commit arrive, after the CTA is gone: the last
-    // use of every stage is waited for, its copies alone if a wait ran out.
+    // use of every stage is waited for, its copies alone if a wait ran out (a pair's
+    // second CTA does not see those: its waits run out long after they have landed).
     __device__ __forceinline__ void finish() {
         for (int i = 0; i < STAGES; ++i) {
             if (turns > 0 || i < (int)s) {
@@ -285,70 +323,75 @@ __device__ __forceinline__ float lane_sums(float (&x)[32], int lane) {
     return x[0];
 }
 
-// Scores of a tile once more (the same products and sums as in the first pass,
-// in chunks of 1,024 columns), and from them a piece's part of G.  Lanes are
-// rows; tiles go through the rows first.
+// Scores of a tile, in chunks of 1,024 columns (the tensor cores cut what they
+// add).  Lanes are rows; tiles go through the rows first.  SUMS: a pass's parts of
+// the log-sum-exps, as lm_head_logprob's kernel leaves them; else, from the same
+// scores once more, a piece's part of G.
 constexpr int kXentChunk = 1024 / kTcK;
 
-template <int N>
-__global__ void __launch_bounds__(kXentThreads, 1) xent_scores_kernel(const __grid_constant__ CUtensorMap map_h,
-                                                                      const __grid_constant__ CUtensorMap map_w,
-                                                                      const __grid_constant__ CUtensorMap map_g,
-                                                                      const XentArgs a, int64_t v0, int32_t width) {
-    using S = XentShape<N>;
+template <int N, int P, bool SUMS>
+__global__ void __launch_bounds__(kXentThreads, 1)
+    xent_scores_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_w,
+                       const __grid_constant__ CUtensorMap map_g, const XentArgs a, int64_t v0, int32_t width,
+                       const LmLogprobArgs pass) {
+    using S = XentShape<N, P>;
     constexpr int STAGES = S::STAGES, NC = S::NC;
     extern __shared__ uint8_t raw[];
     __shared__ XentBars<STAGES> s;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int kblocks = (int)((a.H + kTcK - 1) / kTcK);
-    xent_setup(s, 2 * N);
+    const uint32_t rank = P == 1 ? 0 : cluster_ctarank();
+    xent_setup<P>(s, 2 * N);
     pdl_launch_dependents();
     pdl_wait_primary();
-    const int32_t row_blocks = xent_end(a) / 128;
+    // the pass's rows, or all up to whole tiles
+    const int32_t row0 = SUMS ? (int32_t)pass.first : 0;
+    const int32_t rows = SUMS ? (int32_t)max((int64_t)0, min(a.count[0] - pass.first, pass.M)) : xent_end(a);
+    const int32_t row_blocks = (rows + 128 * P - 1) / (128 * P), t_first = blockIdx.x / P, t_step = gridDim.x / P;
     const int32_t left = (int32_t)(a.V - v0 < width ? a.V - v0 : width);  // the piece's entries
-    const int32_t tiles = row_blocks * (width / N);
+    const int32_t tiles = row_blocks * (SUMS ? (left + N - 1) / N : width / N);
     const uint32_t tmem = s.tmem;
 
     if (warp == 0) {
-        XentRing<STAGES> r(s, ring, S::STAGE, true);
-        for (int32_t t = blockIdx.x; r.ok && t < tiles; t += gridDim.x) {
-            const int32_t ya = t % row_blocks * 128, yb = t / row_blocks * N;
+        XentRing<STAGES, P> r(s, ring, S::STAGE, true);
+        for (int32_t t = t_first; r.ok && t < tiles; t += t_step) {
+            const int32_t ya = row0 + (t % row_blocks * P + rank) * 128, yb = t / row_blocks * N + rank * (N / P);
             for (int kb = 0; kb < kblocks; ++kb, r.next()) {
                 if (!r.wait_empty()) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(r.full(), S::STAGE);
-                    tma_tile(r.stage(), &map_h, kb * kTcK, ya, r.full());
-                    tma_tile(r.stage() + S::A_BYTES, &map_w, kb * kTcK, yb, r.full());
+                    r.expect(rank);
+                    tma_tile_by<P>(r.stage(), &map_h, kb * kTcK, ya, r.filled());
+                    tma_tile_by<P>(r.stage() + S::A_BYTES, &map_w, kb * kTcK, yb, r.filled());
                 }
                 __syncwarp();
             }
         }
         r.finish();
-    } else if (warp == 1) {
-        XentRing<STAGES> r(s, ring, S::STAGE, false);
+    } else if (warp == 1 && rank == 0) {  // (a pair's first CTA issues for both)
+        XentRing<STAGES, P> r(s, ring, S::STAGE, false);
         uint32_t j = 0;
-        for (int32_t t = blockIdx.x; r.ok && t < tiles; t += gridDim.x) {
+        for (int32_t t = t_first; r.ok && t < tiles; t += t_step) {
             for (int kb = 0; kb < kblocks; ++kb) {
                 const uint32_t b = j & 1u;
-                if (kb % kXentChunk == 0) r.ok = xent_warp_wait(&s.drained[b], ((j >> 1) & 1u) ^ 1u);
+                if (kb % kXentChunk == 0) r.ok = xent_wait_drained<P>(&s.drained[b], ((j >> 1) & 1u) ^ 1u);
                 if (!r.wait_full()) break;
                 const bool end = kb % kXentChunk == kXentChunk - 1 || kb == kblocks - 1;
                 const uint64_t da = smem_tile(r.stage()), db = smem_tile(r.stage() + S::A_BYTES);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTcK / 16; ++k)
-                        mma_bf16(tmem + b * N, da + 2 * k, db + 2 * k, S::IDESC, kb % kXentChunk > 0 || k > 0);
-                    mma_commit(r.empty());
-                    if (end) mma_commit(&s.done[b]);
+                        mma_bf16_by<P>(tmem + b * N, da + 2 * k, db + 2 * k, S::IDESC, kb % kXentChunk > 0 || k > 0);
+                    mma_commit_by<P>(r.empty());
+                    if (end) mma_commit_by<P>(&s.done[b]);
                 }
                 if (end) ++j;
                 r.next();
             }
         }
-        if (elect_one()) mma_commit(&s.last);  // the products are finished before tensor memory is freed
+        if (elect_one()) mma_commit_own<P>(&s.last);  // the products are finished before tensor memory is freed
         xent_warp_wait(&s.last, 0);
-    } else {
+    } else if (warp > 1) {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t at = tmem + ((uint32_t)quarter << 21) + half * NC;
         const Cap cap = make_cap(a.cap);
@@ -356,11 +399,13 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_scores_kernel(const __gr
         uint8_t *slab = ring + (size_t)STAGES * S::STAGE + (warp - 2) * kXentSlab;
         uint32_t j = 0;
         bool ok = true;
-        for (int32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            const int32_t first = t % row_blocks * 128 + quarter * 32;  // the warp's rows
-            const int32_t c0 = t / row_blocks * N + half * NC;          // and columns in the piece
-            const float4 k = a.coef[first + lane];
-            const int64_t want = a.tokens[first + lane] - v0 - c0;
+        for (int32_t t = t_first; ok && t < tiles; t += t_step) {
+            const int32_t first = (t % row_blocks * P + rank) * 128 + quarter * 32;  // the warp's rows
+            const int32_t c0 = t / row_blocks * N + half * NC;                      // and columns in the piece
+            // (a pair's second 128 rows may be beyond the last)
+            const bool in_row = SUMS ? first + lane < rows : first < rows;
+            const float4 k = !SUMS && in_row ? a.coef[first + lane] : make_float4(0.f, 0.f, INFINITY, 0.f);
+            const int64_t want = in_row ? a.tokens[row0 + first + lane] - v0 - c0 : -1;
             float z[NC];
             for (int c = 0; c < chunks; ++c, ++j) {
                 const uint32_t b = j & 1u;
@@ -385,10 +430,10 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_scores_kernel(const __gr
                         }
                     }
                 }
-                mma_fence_before();
-                mbar_arrive(&s.drained[b]);
+                xent_drained<P>(&s.drained[b], lane);
             }
             if (!ok) break;
+            if (!SUMS && !in_row) continue;
             if (a.bias) {  // the warp's entries, by way of its slab
                 slab_wait(lane);
                 float *bias = reinterpret_cast<float *>(slab);
@@ -403,6 +448,45 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_scores_kernel(const __gr
                     split_pair(add2(pair_of(z[q + 2], z[q + 3]), pair_of(f.z, f.w)), z[q + 2], z[q + 3]);
                 }
                 __syncwarp();
+            }
+            if constexpr (SUMS) {
+                float2 st = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int c = 0; c < NC; c += 32) {
+                    const int32_t in = left - (c0 + c);
+                    if (in <= 0) break;
+                    float *x = z + c;
+                    if (a.cap > 0.f) soft_cap<32>(x, cap);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {
+                        x[q] = q < in ? fmaxf(x[q], -INFINITY) : -INFINITY;  // NaN counts as -inf
+                        top = fmaxf(top, x[q]);
+                    }
+                    const int64_t w = want - c;
+                    if (w >= 0 && w < 32) {
+                        float found = -INFINITY;
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) found = w == q ? x[q] : found;
+                        pass.tok[first + lane] = found;
+                    }
+                    if (top > -INFINITY) {
+                        if (top > st.x) st = lm_join(st, make_float2(top, 0.f), kLog2eH);
+                        const unsigned long long neg = pair_of(-st.x, -st.x), cc = pair_of(kLog2eH, kLog2eH);
+                        unsigned long long acc = pair_of(st.y, 0.f);
+#pragma unroll
+                        for (int q = 0; q < 32; q += 2) {
+                            float e0, e1;
+                            split_pair(mul2(add2(pair_of(x[q], x[q + 1]), neg), cc), e0, e1);
+                            acc = add2(acc, pair_of(ex2_approx(e0), ex2_approx(e1)));
+                        }
+                        float s0, s1;
+                        split_pair(acc, s0, s1);
+                        st.y = s0 + s1;
+                    }
+                }
+                if (in_row && c0 < left) pass.part[(int64_t)(t / row_blocks * 2 + half) * rows + first + lane] = st;
+                continue;
             }
             const float neg = -k.z * kLog2eH;
 #pragma unroll
@@ -438,8 +522,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_scores_kernel(const __gr
         }
         if (lane == 0) tma_store_done();
     }
-    __syncthreads();
-    if (warp == 1) tmem_free(tmem, 2 * N);
+    xent_close<P>(tmem, 2 * N);
 }
 
 // db of a piece: 32 columns a CTA, the rows' parts over 32 rows of threads.
@@ -471,16 +554,18 @@ __global__ void __launch_bounds__(1024) xent_bias_kernel(const XentArgs a, int64
 struct XentUnits {
     int32_t rb, hb, dh, dw, all, kh, kw;  // row and column blocks; dH and dW units; K steps of a piece and of a unit each
     int32_t w0, w1;                       // this CTA's dW units
-    __device__ __forceinline__ void plan(const XentArgs &a, int32_t left, int32_t end) {
-        rb = end / 128;
+    int32_t group, groups, tall;          // this CTA's pair, pairs, and their rows
+    __device__ __forceinline__ void plan(const XentArgs &a, int32_t left, int32_t end, int32_t P) {
+        group = blockIdx.x / P, groups = gridDim.x / P, tall = 128 * P;
+        rb = (end + tall - 1) / tall;
         hb = (int32_t)((a.H + 255) / 256);
         dh = a.dh ? rb * hb * a.splits : 0;
-        dw = a.dw ? (left + 127) / 128 * hb : 0;
+        dw = a.dw ? (left + tall - 1) / tall * hb : 0;
         all = (left + kTcK - 1) / kTcK;
         kh = (all + a.splits - 1) / a.splits;
         kw = end / kTcK;
         // the first `more` CTAs have a dH unit more, and `fewer` dW units each
-        const int64_t ctas = gridDim.x, b = blockIdx.x, cost = kw + 4;  // a unit's results take about four steps
+        const int64_t ctas = groups, b = group, cost = kw + 4;  // a unit's results take about four steps
         const int64_t more = dh % ctas;
         int64_t fewer = 0;
         if (more > 0) {
@@ -505,20 +590,20 @@ struct XentUnits {
         int32_t y, x, split, k0, ks;
     };
     __device__ __forceinline__ bool get(int32_t i, Unit &u) const {
-        const int32_t b = blockIdx.x, ctas = gridDim.x;
+        const int32_t b = group, ctas = groups;
         const int32_t own = b < dh % ctas ? dh / ctas + 1 : dh / ctas;
         u.is_dh = i < own;
         if (u.is_dh) {
             const int32_t t = b + i * ctas, tile = t % (rb * hb);
             u.split = t / (rb * hb);
-            u.y = tile % rb * 128;
+            u.y = tile % rb * tall;
             u.x = tile / rb * 256;
             u.k0 = u.split * kh;
             u.ks = max(0, min(kh, all - u.k0));
             return true;
         }
         const int32_t t = w0 + i - own;
-        u.y = t / hb * 128;
+        u.y = t / hb * tall;
         u.x = t % hb * 256;
         u.split = u.k0 = 0;
         u.ks = kw;
@@ -547,46 +632,50 @@ __device__ __forceinline__ void dh_results(const float *z, float *acc, bool add,
 // most (kXentMaxRows, and the width of a piece): the tensor cores cut what they
 // add, by 2^-24 of the sum on average a step of 16, which over 4,096 steps is
 // 2^-12 at most against the 2^-9 of the result's rounding.
+template <int P>
 __global__ void __launch_bounds__(kXentThreads, 1)
     xent_products_kernel(const __grid_constant__ CUtensorMap map_gk, const __grid_constant__ CUtensorMap map_gm,
                          const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
                          const __grid_constant__ CUtensorMap map_dw, const XentArgs a, int64_t v0, int32_t width,
                          int w_blocks) {
-    using S = XentShape<256>;
+    using S = XentShape<256, P>;
     constexpr int STAGES = S::STAGES, NC = S::NC, BOX = 64 * 128;
     extern __shared__ uint8_t raw[];
     __shared__ XentBars<STAGES> s;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    xent_setup(s, 512);
+    const uint32_t rank = P == 1 ? 0 : cluster_ctarank();
+    xent_setup<P>(s, 512);
     pdl_launch_dependents();
     pdl_wait_primary();
     const int32_t n = a.count[0], end = xent_end(a);
     const float scale = a.scale[0];
     const int32_t left = (int32_t)(a.V - v0 < width ? a.V - v0 : width);
     XentUnits units;
-    units.plan(a, left, end);
+    units.plan(a, left, end, P);
     const uint32_t tmem = s.tmem;
     XentUnits::Unit u;
 
     if (warp == 0) {
-        XentRing<STAGES> r(s, ring, S::STAGE, true);
+        XentRing<STAGES, P> r(s, ring, S::STAGE, true);
         for (int32_t x = 0; r.ok && units.get(x, u); ++x) {
             for (int kb = u.k0; kb < u.k0 + u.ks; ++kb, r.next()) {
                 if (!r.wait_empty()) break;
                 if (elect_one()) {
                     uint8_t *st = r.stage(), *sb = st + S::A_BYTES;
-                    mbar_arrive_expect_tx(r.full(), S::STAGE);
+                    const int32_t ya = u.y + rank * 128, xb = u.x + rank * (256 / P);
+                    r.expect(rank);
                     if (!u.is_dh) {
-                        tma_tile_3d(st, &map_gm, 0, kb * kTcK, u.y / kTcK, r.full());
-                        tma_tile_3d(sb, &map_h, 0, kb * kTcK, u.x / kTcK, r.full());
+                        tma_blocks_by<P>(st, &map_gm, kb * kTcK, ya / kTcK, r.filled());
+                        tma_blocks_by<P>(sb, &map_h, kb * kTcK, xb / kTcK, r.filled());
                     } else {
-                        tma_tile(st, &map_gk, kb * kTcK, u.y, r.full());
+                        tma_tile_by<P>(st, &map_gk, kb * kTcK, ya, r.filled());
                         if (w_blocks) {
-                            tma_tile_3d(sb, &map_w, 0, kb * kTcK, u.x / kTcK, r.full());
+                            tma_blocks_by<P>(sb, &map_w, kb * kTcK, xb / kTcK, r.filled());
                         } else {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) tma_tile(sb + q * BOX, &map_w, u.x + 64 * q, kb * kTcK, r.full());
+                            for (int q = 0; q < 4 / P; ++q)
+                                tma_tile_by<P>(sb + q * BOX, &map_w, xb + 64 * q, kb * kTcK, r.filled());
                         }
                     }
                 }
@@ -594,13 +683,13 @@ __global__ void __launch_bounds__(kXentThreads, 1)
             }
         }
         r.finish();
-    } else if (warp == 1) {
-        XentRing<STAGES> r(s, ring, S::STAGE, false);
+    } else if (warp == 1 && rank == 0) {  // (a pair's first CTA issues for both)
+        XentRing<STAGES, P> r(s, ring, S::STAGE, false);
         uint32_t j = 0;
         for (int32_t x = 0; r.ok && units.get(x, u); ++x) {
             if (u.ks == 0) continue;
             const uint32_t b = j & 1u, idesc = S::IDESC | kAcrossB | (u.is_dh ? 0u : kAcrossA), step = u.is_dh ? 2 : 128;
-            r.ok = xent_warp_wait(&s.drained[b], ((j >> 1) & 1u) ^ 1u);
+            r.ok = xent_wait_drained<P>(&s.drained[b], ((j >> 1) & 1u) ^ 1u);
             for (int kb = 0; kb < u.ks; ++kb, r.next()) {
                 if (!r.wait_full()) break;
                 const uint64_t da = u.is_dh ? smem_tile(r.stage()) : smem_tile_across(r.stage(), BOX);
@@ -608,23 +697,23 @@ __global__ void __launch_bounds__(kXentThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTcK / 16; ++k)
-                        mma_bf16(tmem + b * 256, da + step * k, db + 128 * k, idesc, kb > 0 || k > 0);
-                    mma_commit(r.empty());
-                    if (kb == u.ks - 1) mma_commit(&s.done[b]);
+                        mma_bf16_by<P>(tmem + b * 256, da + step * k, db + 128 * k, idesc, kb > 0 || k > 0);
+                    mma_commit_by<P>(r.empty());
+                    if (kb == u.ks - 1) mma_commit_by<P>(&s.done[b]);
                 }
             }
             ++j;
         }
-        if (elect_one()) mma_commit(&s.last);
+        if (elect_one()) mma_commit_own<P>(&s.last);
         xent_warp_wait(&s.last, 0);
-    } else {
+    } else if (warp > 1) {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t at = tmem + ((uint32_t)quarter << 21) + half * NC;
         uint8_t *slab = ring + (size_t)STAGES * S::STAGE + (warp - 2) * kXentSlab;
         uint32_t j = 0;
         bool ok = true;
         for (int32_t x = 0; ok && units.get(x, u); ++x) {
-            const int32_t y0 = u.y + quarter * 32, h0 = u.x + half * NC;
+            const int32_t y0 = u.y + rank * 128 + quarter * 32, h0 = u.x + half * NC;
             const uint32_t b = j & 1u;
             if (u.ks > 0) {  // (a part of a short last piece may be empty)
                 ok = xent_warp_wait(&s.done[b], (j >> 1) & 1u);
@@ -660,15 +749,11 @@ __global__ void __launch_bounds__(kXentThreads, 1)
                     }
                 }
             }
-            if (u.ks > 0) {
-                mma_fence_before();
-                mbar_arrive(&s.drained[b]);
-            }
+            if (u.ks > 0) xent_drained<P>(&s.drained[b], lane);
         }
         if (lane == 0) tma_store_done();
     }
-    __syncthreads();
-    if (warp == 1) tmem_free(tmem, 512);
+    xent_close<P>(tmem, 512);
 }
 
 // dH from the parts of a split K.
@@ -724,50 +809,64 @@ unsigned int *xent_status_ptr() {
 namespace {
 
 // A launch that may begin while the kernel before it drains; it waits for that
-// one's end before it reads memory.
-int launch(const void *fn, dim3 grid, dim3 block, size_t smem, void **params, cudaStream_t st) {
+// one's end before it reads memory.  Clusters of P CTAs.
+int launch(const void *fn, dim3 grid, dim3 block, size_t smem, void **params, cudaStream_t st, int P = 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)P;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = P > 1 ? 2 : 1;
     return cudaLaunchKernelExC(&cfg, fn, params) == cudaSuccess ? 0 : -1;
 }
 
-template <int N>
-int launch_scores(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_t st) {
-    using S = XentShape<N>;
-    const void *fn = reinterpret_cast<const void *>(&xent_scores_kernel<N>);
+// CTAs of a persistent launch: as many as there are SMs, whole pairs.
+unsigned persistent(int64_t tiles, int P) {
+    const int64_t groups = sm_count() / P;
+    return (unsigned)((tiles < groups ? tiles : groups) * P);
+}
+
+template <int N, int P, bool SUMS>
+int launch_scores(const XentArgs &args, int64_t v0, int64_t piece, const LmLogprobArgs &args_pass, cudaStream_t st) {
+    using S = XentShape<N, P>;
+    const void *fn = reinterpret_cast<const void *>(&xent_scores_kernel<N, P, SUMS>);
     const int64_t pad = xent_padded(args.M), left = args.V - v0 < piece ? args.V - v0 : piece;
     CUtensorMap mh, mw, mg;
     if (!make_map(&mh, args.hidden_c, args.H, pad, xent_width(args.H), 128) ||
-        !make_map(&mw, args.weight + v0 * args.wstride, args.H, left, args.wstride, N) ||
-        !make_map(&mg, args.grad, piece, pad, piece, 32) || prepare_kernel(fn, S::SMEM, 1) != 0)
+        !make_map(&mw, args.weight + v0 * args.wstride, args.H, left, args.wstride, N / P) ||
+        !make_map(&mg, SUMS ? args.hidden_c : args.grad, SUMS ? args.H : piece, pad, SUMS ? xent_width(args.H) : piece, 32) ||
+        prepare_kernel(fn, S::SMEM, 1) != 0)
         return -1;
     XentArgs a = args;
+    LmLogprobArgs pass = args_pass;
     int32_t width = (int32_t)piece;
-    const int64_t tiles = pad / 128 * (piece / N), sms = sm_count();
-    void *params[] = {&mh, &mw, &mg, &a, &v0, &width};
-    return launch(fn, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kXentThreads), S::SMEM, params, st);
+    const int64_t rows = SUMS ? pass.M : pad;
+    const unsigned grid = persistent((rows + 128 * P - 1) / (128 * P) * ((left + N - 1) / N), P);
+    void *params[] = {&mh, &mw, &mg, &a, &v0, &width, &pass};
+    return launch(fn, dim3(grid), dim3(kXentThreads), S::SMEM, params, st, P);
 }
 
+template <int P>
 int launch_products(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_t st) {
-    using S = XentShape<256>;
-    const void *fn = reinterpret_cast<const void *>(&xent_products_kernel);
+    using S = XentShape<256, P>;
+    const void *fn = reinterpret_cast<const void *>(&xent_products_kernel<P>);
     const int64_t pad = xent_padded(args.M), left = args.V - v0 < piece ? args.V - v0 : piece;
     const int64_t wide = xent_width(args.H);
     const uint16_t *weight = args.weight + v0 * args.wstride;
     int w_blocks = args.H % kTcK == 0;  // else the last block would reach beyond the last row
     CUtensorMap gk, gm, mw, mh, dw;
     if (!make_map(&gk, args.grad, piece, pad, piece, 128) || !make_map_blocks(&gm, args.grad, piece, pad, piece, 64, 2) ||
-        !(w_blocks ? make_map_blocks(&mw, weight, args.H, left, args.wstride, 64, 4)
+        !(w_blocks ? make_map_blocks(&mw, weight, args.H, left, args.wstride, 64, 4 / P)
                    : make_map(&mw, weight, args.H, left, args.wstride, 64)) ||
-        !make_map_blocks(&mh, args.hidden_c, wide, pad, wide, 64, 4) ||
+        !make_map_blocks(&mh, args.hidden_c, wide, pad, wide, 64, 4 / P) ||
         !make_map(&dw, args.dw ? args.dw + v0 * args.dwstride : args.hidden_c, args.H, args.dw ? left : pad,
                   args.dw ? args.dwstride : wide, 32) ||
         prepare_kernel(fn, S::SMEM, 1) != 0)
@@ -775,7 +874,13 @@ int launch_products(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_
     XentArgs a = args;
     int32_t width = (int32_t)piece;
     void *params[] = {&gk, &gm, &mw, &mh, &dw, &a, &v0, &width, &w_blocks};
-    return launch(fn, dim3((unsigned)sm_count()), dim3(kXentThreads), S::SMEM, params, st);
+    return launch(fn, dim3(persistent(sm_count(), P)), dim3(kXentThreads), S::SMEM, params, st, P);
+}
+
+// Whether pairs of CTAs take the rows, 256 at a time.
+bool xent_pairs(int64_t M) {
+    const int64_t blocks = xent_padded(M) / 128;
+    return blocks % 2 == 0 || blocks > 8;
 }
 
 }  // namespace
@@ -796,7 +901,12 @@ int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t 
         s.tokens = scores.tokens + m;
         s.first = m;
         int64_t parts = 0;
-        if (lm_logprob_products(s, &parts, st) != 0) return -1;
+        if (xent_pairs(a.M)) {
+            parts = (a.V + 127) / 128;
+            if (launch_scores<256, 2, true>(a, 0, (a.V + 255) / 256 * 256, s, st) != 0) return -1;
+        } else if (lm_logprob_products(s, &parts, st) != 0) {
+            return -1;
+        }
         void *params[] = {&a, &s, &parts};
         const int64_t places = more ? kLmRows : pad - m;
         if (launch(reinterpret_cast<const void *>(&xent_loss_kernel), dim3((unsigned)(places / kXentJoinX)),
@@ -805,13 +915,18 @@ int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t 
     }
     for (int64_t v0 = 0; (a.dh || a.dw || a.db) && v0 < a.V; v0 += piece) {
         // one block of rows: smaller tiles spread the vocabulary more evenly
-        if ((pad == 128 ? launch_scores<128>(a, v0, piece, st) : launch_scores<256>(a, v0, piece, st)) != 0) return -1;
+        const bool pairs = xent_pairs(a.M);
+        if ((pairs        ? launch_scores<256, 2, false>(a, v0, piece, scores, st)
+             : pad == 128 ? launch_scores<128, 1, false>(a, v0, piece, scores, st)
+                          : launch_scores<256, 1, false>(a, v0, piece, scores, st)) != 0)
+            return -1;
         int32_t width = (int32_t)piece;
         void *params[] = {&a, &v0, &width};
         if (a.db && launch(reinterpret_cast<const void *>(&xent_bias_kernel), dim3((unsigned)((piece + 31) / 32)),
                            dim3(32, 32), 0, params, st) != 0)
             return -1;
-        if ((a.dh || a.dw) && launch_products(a, v0, piece, st) != 0) return -1;
+        if ((a.dh || a.dw) && (pairs ? launch_products<2>(a, v0, piece, st) : launch_products<1>(a, v0, piece, st)) != 0)
+            return -1;
     }
     if (a.dh && a.splits > 1 &&
         launch(reinterpret_cast<const void *>(&xent_join_kernel), dim3((unsigned)a.M), dim3(128), 0, one, st) != 0)
