@@ -558,7 +558,8 @@ size_t tsa_lm_head_int8_workspace_bytes(int64_t M, int64_t H);
  *   grad_hidden = G . weight,  grad_weight = G^T . hidden,  grad_bias = sum over rows of G
  *   hidden, weight, bias, softcap: as for lm_head_logprob; M <= 2^16
  *   targets      [M] int64; a target outside [0, V) skips its row
- *   row_weight   [M] float or NULL: 1 / (number of rows that count); 0 skips a row
+ *   row_weight   [M] float, finite, or NULL: 1 / (number of rows that count); 0
+ *                skips a row
  *   z_loss       finite (TSA_ERR_VALUE); 0 leaves its term out
  *   loss_out     [1] float (0 where no row counts); row_loss_out, lse_out [M] float
  *   grad_hidden_out  bf16 [M, grad_hidden_row_stride] or NULL, grad_weight_out
@@ -570,7 +571,8 @@ size_t tsa_lm_head_int8_workspace_bytes(int64_t M, int64_t H);
  *                gradient is asked for, bias: whether the bias's is
  * A skipped row's hidden row is not used, whatever it holds; its loss, lse and
  * gradient are 0.  NaN scores count as -inf; a +inf score gives its row an
- * lse of +inf, a loss of NaN and NaN in the gradients that it takes part in.
+ * lse of +inf, and a row without a finite score one of -inf; both have a loss of
+ * NaN and NaN in the gradients that they take part in.
  * bf16 products and fp32 sums.  G goes through bf16 (half a step of 2^-8 of each
  * of its elements), grad_bias does not.  The weight is read once for the sums and
  * once or twice more for the gradients.  Sums in a fixed order: equal calls give

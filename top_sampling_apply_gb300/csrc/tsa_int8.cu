@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(256) int8_hidden_kernel(const Int8Args a) {
 
 // One persistent CTA an SM.  Warp 0 fetches 128 columns of the weight's rows
 // (a lane of tensor memory each) by TMA into one ring of stages, warp 2 the same
-// columns of N hidden rows into another; eight warps turn the weight's bytes into
-// f16 in four slots of tensor memory, two groups of four taking steps in turn;
+// columns of N hidden rows into another; four or eight warps turn the weight's bytes
+// into f16 in four slots of tensor memory, groups of four taking steps in turn;
 // warp 1 issues the products; four or eight warps take finished sums from one
 // half of the accumulators while the next products fill the other half.
 //
@@ -114,11 +114,13 @@ struct Int8Shape {
     // with ten stages and four, 120 with eight and six, and 128 rows 153 with six and four, 147 with four and five.
     static constexpr int A_STAGES = N <= 32 ? 10 : N == 64 ? 8 : 4;
     static constexpr int B_STAGES = N <= 16 ? 16 : N <= 64 ? 6 : 5;
-    static_assert(A_STAGES % 2 == 0, "a group of warps meets a stage in each of its phases");
+    static_assert(A_STAGES % 2 == 0 && kI8Slots % 2 == 0, "a group of warps meets a stage in each of its phases");
     static constexpr int SMEM = A_STAGES * A_BYTES + B_STAGES * B_BYTES + 1024;
     static constexpr int EPI = N <= 32 ? 4 : 8;  // warps that take the sums
     static constexpr int NC = N <= 32 ? N : N / 2;
-    static constexpr int THREADS = 128 + 256 + 32 * EPI;
+    // Groups of four warps that convert: one needs 600 to 700 cycles a step, and 128 rows' products take 1,000.
+    static constexpr int GROUPS = N == 128 ? 1 : 2;
+    static constexpr int THREADS = 128 + 128 * GROUPS + 32 * EPI;
     static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(N / 8) << 17) | (8u << 24);  // f16, fp32 sums, M = 128
 };
 
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
         int8_warp_wait(&last, 0);
         for (uint32_t i = uses < kI8Slots ? 0 : uses - kI8Slots; i < uses; ++i)
             int8_warp_wait(&a_empty[i % kI8Slots], (i / kI8Slots) & 1u);
-    } else if (warp >= 4 && warp < 12) {
+    } else if (warp >= 4 && warp < 4 + 4 * S::GROUPS) {
         const int quarter = warp & 3, group = (warp - 4) >> 2;
         const uint32_t at = slots + ((uint32_t)quarter << 21);
         const int row = quarter * 32 + lane;
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
             for (int k = 0; k < steps; ++k, ++it) {
                 // The rings are even, so that a group sees every phase of the barriers that it waits for.  (A wait
                 // for a phase passes while the one before it is open.)
-                if ((it & 1u) != (uint32_t)group) continue;
+                if (it % S::GROUPS != (uint32_t)group) continue;
                 const uint32_t s = it % NA, l = it % kI8Slots;
                 ok = int8_warp_wait(&w_full[s], (it / NA) & 1u) && int8_warp_wait(&a_empty[l], ((it / kI8Slots) & 1u) ^ 1u);
                 if (!ok) break;
@@ -309,8 +311,8 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
                 mbar_arrive(&a_full[l]);
             }
         }
-    } else if (warp >= 12) {
-        const int quarter = warp & 3, half = (warp - 12) >> 2;
+    } else if (warp >= 4 + 4 * S::GROUPS) {
+        const int quarter = warp & 3, half = (warp - 4 - 4 * S::GROUPS) >> 2;
         const uint32_t at = tmem + ((uint32_t)quarter << 21) + half * NC;
         const int chunks = (steps + kI8Chunk - 1) / kI8Chunk;
         uint32_t j = 0;
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
             const int32_t v = tile_v(t) + quarter * 32 + lane, m0 = tile_m(t) + half * NC;
             const bool in = v < v_end;
             const float ws = in ? __ldg(a.wscale + v) : 0.f, bias = in && a.bias ? __ldg(a.bias + v) : 0.f;
-            int sum[NC];
+            int sum[NC];  // (of one chunk the fp32 sums as they are, exact and whole)
             for (int c = 0; c < chunks; ++c, ++j) {
                 const uint32_t b = j & 1u;
                 ok = int8_warp_wait(&done[b], (j >> 1) & 1u);
@@ -332,18 +334,41 @@ __global__ void __launch_bounds__(Int8Shape<N>::THREADS, 1)
                     TmemLoad<16>::ld(at + b * 128 + q, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sum[q + i] = (c == 0 ? 0 : sum[q + i]) + __float2int_rn(__uint_as_float(r[i]));
+                    for (int i = 0; i < 16; ++i) {
+                        if (chunks == 1)
+                            sum[q + i] = (int)r[i];
+                        else
+                            sum[q + i] = (c == 0 ? 0 : sum[q + i]) + __float2int_rn(__uint_as_float(r[i]));
+                    }
                 }
                 mma_fence_before();
                 mbar_arrive(&drained[b]);
             }
             if (!ok) break;
 #pragma unroll
-            for (int q = 0; q < NC; ++q) {
-                if (m0 + q >= a.M) break;
-                const float z = (float)sum[q] * __ldg(a.hscale + m0 + q) * ws + bias;
-                if (in) store_score<DT>(a.out, (m0 + q) * a.ostride + v, z);
+            for (int q0 = 0; q0 < NC; q0 += 16) {
+                // a lane brings one row's scale, and every lane gets them in turn
+                const int32_t m = m0 + q0, rows = (int32_t)min((int64_t)16, a.M - m);
+                const float hs = lane < rows ? __ldg(a.hscale + m + lane) : 0.f;
+                float z[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const float x = chunks == 1 ? __int_as_float(sum[q0 + q]) : (float)sum[q0 + q];
+                    z[q] = x * __shfl_sync(0xFFFFFFFFu, hs, q) * ws + bias;
+                }
+                // 16 stores in a row, where none is left out (each of those is a branch, and nothing overlaps: 2,048 rows x
+                // 50,000 x 256 took 242 us with a store to a score, 137 so)
+                const int64_t to = (int64_t)m * a.ostride + v;
+                if (rows == 16) {
+                    if (in) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) store_score<DT>(a.out, to + q * a.ostride, z[q]);
+                    }
+                } else if (in) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (q < rows) store_score<DT>(a.out, to + q * a.ostride, z[q]);
+                }
             }
         }
     }

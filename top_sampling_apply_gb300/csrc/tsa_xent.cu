@@ -4,10 +4,10 @@
 //     g_j = w ((1 + 2 c l) exp(z_j - l) - [j = t]) (1 - (z_j / cap)^2),
 //     dH = G W,  dW = G^T H,  db = sum over rows of G.
 // The rows that count are brought together first, so that skipped ones cost
-// nothing and whatever they hold stays out of the products.  Their
-// log-sum-exps come from the products of lm_head_logprob; then the vocabulary
-// goes by in pieces: a piece's scores again, turned into its part of G in
-// bf16, and that part's products.
+// nothing and whatever they hold stays out of the products.  A first pass over
+// the scores gives their log-sum-exps; then the vocabulary goes by in pieces: a
+// piece's scores again, turned into its part of G in bf16, and that part's
+// products.  That is 8 M V H operations where 6 would do if the scores were kept.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -788,13 +788,14 @@ int xent_splits(int64_t M, int64_t H, int64_t V) {
 }
 
 // The width of a piece of the vocabulary.  Its part of G takes up to 64 MB, half
-// of L2, so that the products find much of it there; and where that leaves a
-// choice, its tiles are a multiple of the SMs (16 blocks of rows: 57 tiles of 256
-// entries are six turns of 152 SMs, 63 would be 6.6).
+// of L2, so that the products find much of it there, but it has 4,096 entries at
+// least (of more than 8,192 rows), as dH's fp32 sums are read and written once a
+// piece; and where that leaves a choice, its tiles are a multiple of the SMs (16
+// blocks of rows: 57 tiles of 256 entries are six turns of 152 SMs, 63 would be 6.6).
 int64_t xent_piece(int64_t M, int64_t V) {
     const int64_t blocks = xent_padded(M) / 128, all = (V + 255) / 256;
     int64_t fit = ((int64_t)64 << 20) / (2 * 128 * 256) / blocks;
-    fit = fit < 1 ? 1 : fit > kXentMaxPiece / 256 ? kXentMaxPiece / 256 : fit;
+    fit = fit < 16 ? 16 : fit > kXentMaxPiece / 256 ? kXentMaxPiece / 256 : fit;
     if (fit >= all) return all * 256;
     const int64_t turn = 152 / std::gcd((int64_t)152, blocks);
     return (fit < turn ? fit : fit / turn * turn) * 256;
@@ -877,11 +878,12 @@ int launch_products(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_
     return launch(fn, dim3(persistent(sm_count(), P)), dim3(kXentThreads), S::SMEM, params, st, P);
 }
 
-// Whether pairs of CTAs take the rows, 256 at a time.
-bool xent_pairs(int64_t M) {
-    const int64_t blocks = xent_padded(M) / 128;
-    return blocks % 2 == 0 || blocks > 8;
-}
+// Whether pairs of CTAs take the rows, 256 at a time; an odd block of 128 (and how
+// many blocks count is known on the GPU alone: skipped rows are left out) then
+// costs two.  In a long run, single CTAs and pairs: 256 rows x 32,000 x 2,048 178
+// and 182 us, 343 rows 211 and 230, 512 rows 249 and 238, 640 x 64,000 x 2,048 562
+// and 562, 1,100 x 32,000 x 4,096 1,067 and 975, 2,048 x 128,256 x 5,120 7,190 and 6,640.
+bool xent_pairs(int64_t M) { return xent_padded(M) / 128 >= 8; }
 
 }  // namespace
 
