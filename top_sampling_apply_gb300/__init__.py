@@ -713,21 +713,23 @@ def adamw_state_values(plan: AdamWPlan, exp_avg_out=None, exp_avg_sq_out=None):
 
 def _matrix(t: torch.Tensor, index: int, shape, dtype: torch.dtype, name: str, unit: str = "H") -> torch.Tensor:
     """Checks a [rows, columns] tensor of unit stride along its columns on CUDA device ``index``."""
-    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or (t.size(0) > 0 and t.stride(1) != 1
-                                                                              and t.size(1) > 1):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or \
+            (t.stride(1) != 1 and shape[1] > 1 and shape[0] > 0):
         raise ValueError("%s must be a %s %s tensor on cuda:%d with unit stride along %s"
                          % (name, dtype, list(shape), index, unit))
     return t
 
 
 def _hidden_rows(t: torch.Tensor, name: str):
-    if not t.is_cuda or t.dtype not in _DT or t.dim() != 2 or (t.size(1) > 1 and t.stride(1) != 1):
+    if not t.is_cuda or t.dtype not in _DT or t.dim() != 2 or (t.stride(1) != 1 and t.size(1) > 1):
         raise ValueError("%s must be a CUDA float32, float16 or bfloat16 2-D tensor with unit stride along H" % name)
-    return t.size(0), t.size(1), t.get_device()
+    N, H = t.shape
+    return N, H, t.get_device()
 
 
 def _norm_weight(weight: torch.Tensor, x: torch.Tensor) -> None:
-    if weight.dtype not in (x.dtype, torch.float32) or weight.get_device() != x.get_device() or weight.dim() != 1 \
+    dt = weight.dtype
+    if (dt is not x.dtype and dt is not torch.float32) or weight.get_device() != x.get_device() or weight.dim() != 1 \
             or weight.size(0) != x.size(1) or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous [H] tensor of the rows' dtype or float32 on their device")
 
@@ -753,23 +755,29 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     lib = _lib or load_library()
     N, H, dev = _hidden_rows(x, "x")
     _norm_weight(weight, x)
-    device = x.device
-    y = torch.empty((N, H), dtype=torch.int8 if quantize else x.dtype, device=device) if out is None else \
-        _matrix(out, dev, (N, H), torch.int8 if quantize else x.dtype, "out")
-    total = None
+    dt, device, empty = x.dtype, x.device, torch.empty
+    # an allocation each: on the host that is cheaper than views of one
+    if out is not None:
+        y = _matrix(out, dev, (N, H), torch.int8 if quantize else dt, "out")
+    elif quantize:
+        y = empty((N, H), dtype=torch.int8, device=device)
+    else:
+        y = empty((N, H), dtype=dt, device=device)
+    total = r = to = scale = None
+    rs = ts = 0
     if residual is not None:
-        _matrix(residual, dev, (N, H), x.dtype, "residual")
-        total = torch.empty((N, H), dtype=x.dtype, device=device) if residual_out is None else \
-            _matrix(residual_out, dev, (N, H), x.dtype, "residual_out")
+        _matrix(residual, dev, (N, H), dt, "residual")
+        total = empty((N, H), dtype=dt, device=device) if residual_out is None else \
+            _matrix(residual_out, dev, (N, H), dt, "residual_out")
+        r, rs, to, ts = residual.data_ptr(), residual.stride(0), total.data_ptr(), total.stride(0)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    scale = torch.empty(N, dtype=torch.float32, device=device) if quantize else None
-    rstd = torch.empty(N, dtype=torch.float32, device=device)
-    _call(dev, lib.tsa_rms_norm, x.data_ptr(), _DT[x.dtype], N, H, x.stride(0), weight.data_ptr(), _DT[weight.dtype],
-          None if residual is None else residual.data_ptr(), 0 if residual is None else residual.stride(0), eps,
-          1 if quantize else 0, y.data_ptr(), y.stride(0), None if scale is None else scale.data_ptr(),
-          None if total is None else total.data_ptr(), 0 if total is None else total.stride(0), rstd.data_ptr(),
-          _raw_stream(dev))
+    if quantize:
+        scale = empty(N, dtype=torch.float32, device=device)
+    rstd = empty(N, dtype=torch.float32, device=device)
+    _call(dev, lib.tsa_rms_norm, x.data_ptr(), _DT[dt], N, H, x.stride(0), weight.data_ptr(), _DT[weight.dtype], r, rs,
+          eps, 1 if quantize else 0, y.data_ptr(), y.stride(0), None if scale is None else scale.data_ptr(), to, ts,
+          rstd.data_ptr(), _raw_stream(dev))
     if out is not None:
         _written(out)
     if residual_out is not None:
