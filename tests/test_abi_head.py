@@ -131,7 +131,46 @@ def test_lm_head_cross_entropy_validation(lib):
         assert xent(lib, nws=n - 1, **kw) == S["TSA_ERR_WORKSPACE"], kw
 
 
-def test_binding_refuses(monkeypatch):
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    import top_sampling_apply_gb300 as tsa
+    from tests.test_abi_training import OnDevice1
+
+    current, ran = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *a):
+            current[0] = self.before
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_bytes"):
+                return lambda *a: 256
+            return lambda *a: ran.append((name, current[0])) or 0
+
+    monkeypatch.setattr(tsa, "_lib", Lib())
+    monkeypatch.setattr(tsa, "_current_device", lambda: current[0])
+    monkeypatch.setattr(tsa, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(tsa, "_written", lambda tensors: None)
+    monkeypatch.setattr(tsa.torch.cuda, "device", Device)
+    monkeypatch.setattr(tsa.torch, "empty", OnDevice1)
+    h, w = OnDevice1(2, 16, dtype=torch.bfloat16), OnDevice1(16, dtype=torch.bfloat16)
+    q, f = OnDevice1(2, 16, dtype=torch.int8), OnDevice1(2)
+    tsa.rms_norm(h, w, residual=h, quantize=True)
+    tsa.rms_norm_backward(h, h, w, f, grad_residual=h)
+    tsa.quantize_rows(h)
+    tsa.lm_head_int8(q, f, q, f)
+    tsa.lm_head_cross_entropy(h, h, OnDevice1(2, dtype=torch.int64), bias=f)
+    assert ran == [("tsa_rms_norm", 1), ("tsa_rms_norm_backward", 1), ("tsa_quantize_rows", 1), ("tsa_lm_head_int8", 1),
+                   ("tsa_lm_head_cross_entropy", 1)] and current == [0]
+
+
+def test_binding_refuses_host_tensors():
     import top_sampling_apply_gb300 as tsa
 
     x, w = torch.zeros(2, 16), torch.zeros(16)
