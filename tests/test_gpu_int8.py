@@ -92,6 +92,29 @@ def test_large(tsa):
     check(c, tsa.lm_head_int8(c["h"], c["hs"], c["w"], c["ws"]), False)
 
 
+def test_scores_of_more_elements_than_32_bits_count(tsa):
+    M, V = 17_500, 128_256
+    c = make(5, M, V, 64)
+    assert M * V > 2 ** 31
+    got = tsa.lm_head_int8(c["h"], c["hs"], c["w"], c["ws"])
+    last = dict(c, h=c["h"][-300:], hs=c["hs"][-300:])
+    check(last, got[-300:], False)
+
+
+def test_calls_at_once_on_two_streams(tsa):
+    cs = [make(30 + i, M, 9000, 1024) for i, M in enumerate((5, 60, 500))]
+    want = [tsa.lm_head_int8(c["h"], c["hs"], c["w"], c["ws"]) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                got.append(tsa.lm_head_int8(c["h"], c["hs"], c["w"], c["ws"]))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_streams_graphs_and_versions(tsa):
     for M in (3, 70):
         c = make(4, M, 2000, 512)

@@ -207,6 +207,21 @@ def test_many_long_rows(tsa, dt, H):
     assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1]) and tsa.device_status() == 0
 
 
+def test_norm_of_more_elements_than_32_bits_count(tsa):
+    N, H = 132_000, 16384
+    x = torch.empty(N, H, dtype=torch.bfloat16, device=DEV)
+    x[-64:] = rows(1, 64, H, torch.bfloat16)
+    x[:-64] = x[-64:].repeat(N // 64, 1)[:N - 64]
+    w = rows(2, 1, H, torch.bfloat16)[0]
+    assert x.numel() > 2 ** 31
+    a = tsa.rms_norm(x, w)
+    y, _ = head.rms_norm(x[-64:], w, 1e-6)
+    near(a.out[-64:], y, 32 * U * y.abs(), torch.bfloat16)
+    dx, _ = tsa.rms_norm_backward(x, x, w, a.rstd, grad_x=a.out)
+    want, few = tsa.rms_norm_backward(x[-64:], x[-64:], w, a.rstd[-64:])
+    assert torch.equal(dx[-64:], want)
+
+
 def test_norm_of_no_rows(tsa):
     x, w = torch.empty(0, 64, device=DEV), torch.ones(64, device=DEV)
     assert tsa.rms_norm(x, w, quantize=True).out.shape == (0, 64)

@@ -204,6 +204,50 @@ def test_several_pieces_of_the_vocabulary(tsa):
     check(c, tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"]))
 
 
+def test_most_rows(tsa):
+    c = make(9, 65536, 130, 64, skip=0.02)
+    check(c, tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"]))
+    with pytest.raises(tsa.TSAError):
+        tsa.lm_head_cross_entropy(torch.cat([c["h"], c["h"][:1]]), c["w"], torch.cat([c["t"], c["t"][:1]]))
+
+
+def test_weight_of_more_elements_than_32_bits_count(tsa):
+    M, V, H = 40, 560_000, 4096
+    g = torch.Generator(device=DEV).manual_seed(0)
+    w = torch.empty(V, H, dtype=torch.bfloat16, device=DEV).normal_(0.0, 0.05, generator=g)
+    h = torch.randn(M, H, generator=g, device=DEV).bfloat16()
+    t = torch.randint(V - 5000, V, (M,), generator=g, device=DEV)
+    assert w.numel() > 2 ** 31
+    r = tsa.lm_head_cross_entropy(h, w, t)
+    z = torch.cat([h.double() @ w[i:i + 70_000].double().T for i in range(0, V, 70_000)], 1)
+    lse = torch.logsumexp(z, -1)
+    G = torch.exp(z - lse[:, None]) / M
+    G[torch.arange(M, device=DEV), t] -= 1.0 / M
+    assert ((r.lse.double() - lse).abs() < 1e-4).all()
+    # bf16 G and results: 2^-8 of the sums of absolute terms
+    last = slice(V - 6000, V)
+    want, bound = G[:, last].T @ h.double(), G[:, last].abs().T @ h.double().abs()
+    assert ((r.grad_weight[last].double() - want).abs() <= 2.0 ** -7 * bound + 1e-30).all()
+    dh = sum(G[:, i:i + 70_000] @ w[i:i + 70_000].double() for i in range(0, V, 70_000))
+    assert (r.grad_hidden.double() - dh).norm() / dh.norm() < 2.0 ** -8
+
+
+def test_calls_at_once_on_two_streams(tsa):
+    cs = [make(20 + i, M, 5000, 512, skip=0.1) for i, M in enumerate((70, 300, 1100))]
+    want = [tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"]) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                got.append(tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"]))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a[:5], b[:5]))
+    assert tsa.device_status() == 0
+
+
 def test_large(tsa):
     c = make(6, 700, 20001, 1024, bias=True, skip=0.2)
     x = check(c, tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"]))
