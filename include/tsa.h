@@ -564,7 +564,8 @@ size_t tsa_lm_head_int8_workspace_bytes(int64_t M, int64_t H);
  *   loss_out     [1] float (0 where no row counts); row_loss_out, lse_out [M] float
  *   grad_hidden_out  bf16 [M, grad_hidden_row_stride] or NULL, grad_weight_out
  *                bf16 [V, grad_weight_row_stride] or NULL: 16-byte aligned, row
- *                strides multiples of 8.  They must not overlap an input.
+ *                strides multiples of 8.  They must not overlap an input (the same
+ *                start: TSA_ERR_SHAPE).
  *   grad_bias_out  [V] float or NULL (needs a bias: TSA_ERR_NULL)
  *   workspace    at least tsa_lm_head_cross_entropy_workspace_bytes(M, H, V,
  *                grads, bias) bytes, 256-byte aligned; grads: whether any

@@ -113,7 +113,8 @@ def xent(lib, h=FAKE, M=2, H=64, hs=64, w=FAKE, V=100, wst=64, b=None, cap=0.0, 
 
 def test_lm_head_cross_entropy_validation(lib):
     for kw in ({"M": -1}, {"M": (1 << 16) + 1}, {"H": 4}, {"H": 12}, {"H": 16392, "hs": 16392, "wst": 16392}, {"V": 0},
-               {"hs": 32}, {"wst": 32}, {"dh": OTHER, "dhs": 32}, {"dw": OTHER, "dws": 32}):
+               {"hs": 32}, {"wst": 32}, {"dh": OTHER, "dhs": 32}, {"dw": OTHER, "dws": 32}, {"dh": FAKE}, {"dw": FAKE},
+               {"b": OTHER, "db": OTHER}):
         assert xent(lib, **kw) == S["TSA_ERR_SHAPE"], kw
     for kw in ({"cap": -1.0}, {"cap": float("nan")}, {"cap": float("inf")}, {"z": float("nan")}, {"z": float("inf")}):
         assert xent(lib, **kw) == S["TSA_ERR_VALUE"], kw

@@ -37,7 +37,7 @@ struct XentLayout {
 };
 XentLayout xent_layout(int64_t M, int64_t H, int64_t V, bool grads, bool bias) {
     const size_t n = (size_t)xent_padded(M);
-    const int64_t few = M < kLmRows ? M : kLmRows;
+    const int64_t few = M < kXentPass ? M : kXentPass;
     const size_t piece = (size_t)xent_piece(M, V);
     XentLayout l;
     size_t at = 0;
@@ -53,7 +53,7 @@ XentLayout xent_layout(int64_t M, int64_t H, int64_t V, bool grads, bool bias) {
     l.loss = take(n * 4);
     l.coef = take(n * 16);
     l.hidden = take(n * (size_t)xent_width(H) * 2);
-    l.part = take((size_t)lm_logprob_parts(few, V) * (size_t)few * sizeof(float2));
+    l.part = take((size_t)xent_parts(M, V) * (size_t)few * sizeof(float2));
     l.tok = take((size_t)few * 4);
     l.grad = take(grads ? n * piece * 2 : 0);
     const int splits = xent_splits(M, H, V);
@@ -233,6 +233,10 @@ int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t 
         hidden_row_stride < H || weight_row_stride < H || (grad_hidden_out && grad_hidden_row_stride < H) ||
         (grad_weight_out && grad_weight_row_stride < H))
         return TSA_ERR_SHAPE;
+    // later pieces read what earlier ones would have written
+    if ((grad_hidden_out && grad_hidden_out == hidden) || (grad_weight_out && grad_weight_out == weight) ||
+        (grad_bias_out && grad_bias_out == bias))
+        return TSA_ERR_SHAPE;
     if (!(softcap >= 0.f) || !isfinite(softcap) || !isfinite(z_loss)) return TSA_ERR_VALUE;
     if (!weight || !loss_out || (M > 0 && (!hidden || !targets || !row_loss_out || !lse_out)) ||
         (grad_bias_out && !bias))
@@ -291,21 +295,9 @@ int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t 
     a.padded = xent_padded(M);
     a.splits = xent_splits(M, H, V);
     a.db_part = reinterpret_cast<float *>(ws + l.db);
-    LmLogprobArgs p = {};  // the scores' first pass, over the rows that count
-    p.hidden = a.hidden_c;
-    p.H = H;
-    p.hstride = xent_width(H);
-    p.weight = a.weight;
-    p.V = V;
-    p.wstride = weight_row_stride;
-    p.bias = bias;
-    p.cap = softcap;
-    p.temperature_s = 1.f;
-    p.tokens = a.tokens;
-    p.count = a.count;
-    p.part = reinterpret_cast<float2 *>(ws + l.part);
-    p.tok = reinterpret_cast<float *>(ws + l.tok);
-    return xent_launch(a, p, s) == 0 ? TSA_OK : TSA_ERR_CUDA;
+    a.part = reinterpret_cast<float2 *>(ws + l.part);
+    a.tok = reinterpret_cast<float *>(ws + l.tok);
+    return xent_launch(a, s) == 0 ? TSA_OK : TSA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -224,15 +224,9 @@ struct LmLogprobArgs {
     float *out;
     float2 *part;            // [parts][rows]: a part's largest score and its sum against it
     float *tok;              // [rows]: the token's score
-    // the cross entropy's: a device count of rows (NULL: all), of which these
-    // are the ones from `first` on
-    const int32_t *count;
-    int64_t first;
 };
 constexpr int64_t kLmRows = 8192;  // rows a pass over the weight takes
 int64_t lm_logprob_parts(int64_t M, int64_t V);
-// The parts alone, `parts` of them a row.
-int lm_logprob_products(const LmLogprobArgs &args, int64_t *parts, cudaStream_t st);
 int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st);
 unsigned int *lm_logprob_status_ptr();
 
@@ -309,6 +303,8 @@ struct XentArgs {
     int32_t *count, *rows;   // [1]; [M]: a place's row
     int64_t *tokens;
     float *weight_c, *row_loss_c;
+    float2 *part;            // of a pass's rows: a part's largest score and its sum against it
+    float *tok;              // of a pass's rows: the target's score
     float4 *coef;            // what a place's gradient needs
     uint16_t *hidden_c;      // [padded, xent_width(H)]
     uint16_t *grad;          // [padded, piece]: a piece of the vocabulary's part of G
@@ -323,7 +319,9 @@ constexpr int64_t kXentMaxRows = 1 << 16, kXentMaxPiece = 1 << 16;
 int64_t xent_piece(int64_t M, int64_t V);
 int xent_splits(int64_t M, int64_t H, int64_t V);
 unsigned int *xent_status_ptr();
-int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t st);
+constexpr int64_t kXentPass = 8192;  // rows of a first pass over the scores
+inline int64_t xent_parts(int64_t M, int64_t V) { return M <= 128 ? (V + 63) / 64 : (V + 127) / 128; }
+int xent_launch(const XentArgs &args, cudaStream_t st);
 
 int selftest_launch(uint32_t limit_us, cudaStream_t st);
 

@@ -28,12 +28,6 @@ __device__ __forceinline__ void select_if(float &x, float z, int a, int b) {
     asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, %3;\n\tselp.f32 %0, %1, %0, p;\n\t}" : "+f"(x) : "f"(z), "r"(a), "r"(b));
 }
 
-// The rows that count: all, or as many as a kernel before left on the device.
-__device__ __forceinline__ int64_t row_count(const LmLogprobArgs &a) {
-    if (!a.count) return a.M;
-    const int64_t n = (int64_t)*a.count - a.first;
-    return n < 0 ? 0 : n < a.M ? n : a.M;
-}
 // A bounded wait whose outcome the whole warp shares.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, &g_lm_logprob_status));
@@ -84,7 +78,7 @@ struct TcShape {
 template <int N, bool ROWS, int STAGES>
 __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const __grid_constant__ CUtensorMap map_a,
                                                                    const __grid_constant__ CUtensorMap map_b,
-                                                                   const LmLogprobArgs a, int64_t v_tiles, int64_t run) {
+                                                                   LmLogprobArgs a, int64_t tiles, int row_blocks, int64_t run) {
     using S = TcShape<N, ROWS, STAGES>;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[STAGES], empty[STAGES], done[2], drained[2], last;
@@ -99,6 +93,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
     const int64_t v_first = ROWS ? 0 : (int64_t)blockIdx.x * run;
     const int64_t v_end = ROWS || v_first + run > a.V ? a.V : v_first + run;
     const int64_t t_first = ROWS ? blockIdx.x : 0, t_step = ROWS ? gridDim.x : 1;
+    const int64_t t_end = ROWS ? tiles : (v_end - v_first + 127) / 128;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full[i], 1);
@@ -116,11 +111,6 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
     __syncthreads();
     mma_fence_after();
     pdl_launch_dependents();  // the joining kernel waits for this one's end before it reads
-    pdl_wait_primary();
-    const int64_t M = row_count(a);
-    const int row_blocks = ROWS ? (int)((M + 127) / 128) : 1;
-    const int64_t tiles = v_tiles * row_blocks;
-    const int64_t t_end = ROWS ? tiles : (v_end - v_first + 127) / 128;
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0) {
@@ -206,7 +196,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
             for (int64_t t = t_first; ok && t < t_end; t += t_step) {
                 const int64_t row = (t % row_blocks) * 128 + quarter * 32 + lane;
                 const int64_t v0 = (t / row_blocks) * N + half * NC;
-                const bool in = row < M;
+                const bool in = row < a.M;
                 const float c2 = in ? kLog2eH / row_temp(a, row) : 1.f;
                 const int64_t want = in ? __ldg(a.tokens + row) - v0 : -1;
                 const int32_t *mrow = a.mask && in ? a.mask + row * a.mstride : nullptr;
@@ -304,7 +294,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
                         st.y = s0 + s1;
                     }
                 }
-                if (in && v0 < a.V) a.part[((t / row_blocks) * 2 + half) * M + row] = st;
+                if (in && v0 < a.V) a.part[((t / row_blocks) * 2 + half) * a.M + row] = st;
             }
         } else {
             float2 st[N];
@@ -336,7 +326,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
                 if (a.cap > 0.f) soft_cap<N>(z, cap);
 #pragma unroll
                 for (int q = 0; q < N; ++q) {
-                    if (q >= M) break;
+                    if (q >= a.M) break;
                     float x = fmaxf(z[q], -INFINITY);
                     if (v >= v_end) x = -INFINITY;  // lanes past the run hold what was there before
                     if (a.mask && w0 < v_end &&
@@ -349,7 +339,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
             if (ok) {
 #pragma unroll
                 for (int q = 0; q < N; ++q) {
-                    if (q >= M) break;
+                    if (q >= a.M) break;
                     const float c2 = kLog2eH / row_temp(a, q);
                     float2 x = st[q];
 #pragma unroll
@@ -366,11 +356,11 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
     }
     __syncthreads();
     if constexpr (!ROWS) {
-        if (threadIdx.x < N && (int64_t)threadIdx.x < M) {
+        if (threadIdx.x < N && (int64_t)threadIdx.x < a.M) {
             const float c2 = kLog2eH / row_temp(a, threadIdx.x);
             float2 x = s_part[0][threadIdx.x];
             for (int w = 1; w < 4; ++w) x = lm_join(x, s_part[w][threadIdx.x], c2);
-            a.part[(int64_t)blockIdx.x * M + threadIdx.x] = x;
+            a.part[(int64_t)blockIdx.x * a.M + threadIdx.x] = x;
         }
     }
     if (warp == 1) tmem_free(tmem, S::COLS);
@@ -379,7 +369,7 @@ __global__ void __launch_bounds__(kTcThreads<ROWS>, 1) lm_logprob_kernel(const _
 // A row's parts: 8 rows a CTA, 64 threads a row (a pass over 2,048 parts is 32
 // loads a thread, four under way together), then a tree over them.
 constexpr int kJoinX = 8, kJoinY = 64;
-__global__ void __launch_bounds__(kJoinX *kJoinY) lm_logprob_join_kernel(const LmLogprobArgs a, int64_t parts) {
+__global__ void __launch_bounds__(kJoinX *kJoinY) lm_logprob_join_kernel(LmLogprobArgs a, int64_t parts) {
     __shared__ float2 sh[kJoinY][kJoinX];
     pdl_wait_primary();
     const int64_t row = (int64_t)blockIdx.x * kJoinX + threadIdx.x;
@@ -437,25 +427,15 @@ int launch_products(const LmLogprobArgs &args, int64_t *parts, cudaStream_t st) 
                   ROWS ? args.wstride : args.hstride, N))
         return -1;
     if (prepare_kernel(fn, S::SMEM, 1) != 0) return -1;
-    int64_t v_tiles = ROWS ? (args.V + N - 1) / N : (args.V + 127) / 128;
-    const int64_t tiles = v_tiles * (ROWS ? (args.M + 127) / 128 : 1);
+    int row_blocks = ROWS ? (int)((args.M + 127) / 128) : 1;
+    int64_t tiles = ROWS ? row_blocks * ((args.V + N - 1) / N) : (args.V + 127) / 128;
     const int64_t sms = sm_count();
     int64_t run = ((args.V + sms - 1) / sms + 31) / 32 * 32;
     const int64_t grid = ROWS ? (tiles < sms ? tiles : sms) : (args.V + run - 1) / run;
     *parts = ROWS ? (args.V + N / 2 - 1) / (N / 2) : grid;
     LmLogprobArgs a = args;
-    void *params[] = {&ma, &mb, &a, &v_tiles, &run};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kTcThreads<ROWS>);
-    cfg.dynamicSmemBytes = S::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.count ? 1 : 0;  // only behind a kernel of the same call
-    return cudaLaunchKernelExC(&cfg, fn, params) == cudaSuccess ? 0 : -1;
+    void *params[] = {&ma, &mb, &a, &tiles, &row_blocks, &run};
+    return cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kTcThreads<ROWS>), params, S::SMEM, st) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace
@@ -466,16 +446,18 @@ int64_t lm_logprob_parts(int64_t M, int64_t V) {
     return M <= kLmMid ? (V + 63) / 64 : (V + 127) / 128;
 }
 
-int lm_logprob_products(const LmLogprobArgs &args, int64_t *parts, cudaStream_t st) {
-    if (args.M <= 16) return launch_products<16, false, 11>(args, parts, st);
-    if (args.M <= kLmFew) return launch_products<32, false, 10>(args, parts, st);
-    if (args.M <= kLmMid) return launch_products<128, true, 6>(args, parts, st);
-    return launch_products<256, true, 4>(args, parts, st);
-}
-
 int lm_logprob_launch(const LmLogprobArgs &args, cudaStream_t st) {
     int64_t parts = 0;
-    if (lm_logprob_products(args, &parts, st) != 0) return -1;
+    int r;
+    if (args.M <= 16)
+        r = launch_products<16, false, 11>(args, &parts, st);
+    else if (args.M <= kLmFew)
+        r = launch_products<32, false, 10>(args, &parts, st);
+    else if (args.M <= kLmMid)
+        r = launch_products<128, true, 6>(args, &parts, st);
+    else
+        r = launch_products<256, true, 4>(args, &parts, st);
+    if (r != 0) return -1;
     LmLogprobArgs a = args;
     void *params[] = {&a, &parts};
     cudaLaunchConfig_t cfg = {};

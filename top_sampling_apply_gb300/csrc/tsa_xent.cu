@@ -96,11 +96,16 @@ __global__ void __launch_bounds__(32 * kXentPrep) xent_prepare_kernel(const Xent
     if (lane == 0) a.row_loss[m] = a.lse[m] = 0.f;
 }
 
+// A first pass over the scores of some of the rows that count.
+struct XentPass {
+    int64_t first, M;  // M at most
+};
+
 // The losses of a pass's rows from their parts, and what their gradients need;
 // places up to the next multiple of 128 have none.  8 rows a CTA, 64 threads a
 // row, then a tree over them.
 constexpr int kXentJoinX = 8, kXentJoinY = 64;
-__global__ void __launch_bounds__(kXentJoinX *kXentJoinY) xent_loss_kernel(const XentArgs a, const LmLogprobArgs s,
+__global__ void __launch_bounds__(kXentJoinX *kXentJoinY) xent_loss_kernel(const XentArgs a, const XentPass s,
                                                                            int64_t parts) {
     __shared__ float2 sh[kXentJoinY][kXentJoinX];
     pdl_launch_dependents();
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kXentJoinX *kXentJoinY) xent_loss_kernel(const
     const int64_t M = n - s.first < s.M ? n - s.first : s.M;  // the pass's rows
     float2 x = make_float2(-INFINITY, 0.f);
     if (at < M) {
-        const float2 *part = s.part + at;
+        const float2 *part = a.part + at;
         int64_t p = threadIdx.y;
         for (; p + 3 * kXentJoinY < parts; p += 4 * kXentJoinY) {
             float2 v[4];
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(kXentJoinX *kXentJoinY) xent_loss_kernel(const
     x = sh[0][threadIdx.x];
     const float ln = logf(x.y), l = x.x < INFINITY ? x.x + ln : x.x, c = a.z_loss;
     // the score less the sum's reference is exact where they are near
-    float loss = x.x > -INFINITY && x.x < INFINITY ? ln - (s.tok[at] - x.x) : __int_as_float(0x7FC00000);
+    float loss = x.x > -INFINITY && x.x < INFINITY ? ln - (a.tok[at] - x.x) : __int_as_float(0x7FC00000);
     if (c != 0.f) loss += c * l * l;
     a.row_loss_c[i] = loss;
     a.row_loss[a.rows[i]] = loss;
@@ -325,7 +330,7 @@ __device__ __forceinline__ float lane_sums(float (&x)[32], int lane) {
 
 // Scores of a tile, in chunks of 1,024 columns (the tensor cores cut what they
 // add).  Lanes are rows; tiles go through the rows first.  SUMS: a pass's parts of
-// the log-sum-exps, as lm_head_logprob's kernel leaves them; else, from the same
+// the log-sum-exps, one a half tile of the vocabulary; else, from the same
 // scores once more, a piece's part of G.
 constexpr int kXentChunk = 1024 / kTcK;
 
@@ -333,7 +338,7 @@ template <int N, int P, bool SUMS>
 __global__ void __launch_bounds__(kXentThreads, 1)
     xent_scores_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_g, const XentArgs a, int64_t v0, int32_t width,
-                       const LmLogprobArgs pass) {
+                       const XentPass pass) {
     using S = XentShape<N, P>;
     constexpr int STAGES = S::STAGES, NC = S::NC;
     extern __shared__ uint8_t raw[];
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(kXentThreads, 1)
                         float found = -INFINITY;
 #pragma unroll
                         for (int q = 0; q < 32; ++q) found = w == q ? x[q] : found;
-                        pass.tok[first + lane] = found;
+                        a.tok[first + lane] = found;
                     }
                     if (top > -INFINITY) {
                         if (top > st.x) st = lm_join(st, make_float2(top, 0.f), kLog2eH);
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(kXentThreads, 1)
                         st.y = s0 + s1;
                     }
                 }
-                if (in_row && c0 < left) pass.part[(int64_t)(t / row_blocks * 2 + half) * rows + first + lane] = st;
+                if (in_row && c0 < left) a.part[(int64_t)(t / row_blocks * 2 + half) * rows + first + lane] = st;
                 continue;
             }
             const float neg = -k.z * kLog2eH;
@@ -836,7 +841,7 @@ unsigned persistent(int64_t tiles, int P) {
 }
 
 template <int N, int P, bool SUMS>
-int launch_scores(const XentArgs &args, int64_t v0, int64_t piece, const LmLogprobArgs &args_pass, cudaStream_t st) {
+int launch_scores(const XentArgs &args, int64_t v0, int64_t piece, XentPass pass, cudaStream_t st) {
     using S = XentShape<N, P>;
     const void *fn = reinterpret_cast<const void *>(&xent_scores_kernel<N, P, SUMS>);
     const int64_t pad = xent_padded(args.M), left = args.V - v0 < piece ? args.V - v0 : piece;
@@ -847,7 +852,6 @@ int launch_scores(const XentArgs &args, int64_t v0, int64_t piece, const LmLogpr
         prepare_kernel(fn, S::SMEM, 1) != 0)
         return -1;
     XentArgs a = args;
-    LmLogprobArgs pass = args_pass;
     int32_t width = (int32_t)piece;
     const int64_t rows = SUMS ? pass.M : pad;
     const unsigned grid = persistent((rows + 128 * P - 1) / (128 * P) * ((left + N - 1) / N), P);
@@ -887,40 +891,35 @@ bool xent_pairs(int64_t M) { return xent_padded(M) / 128 >= 8; }
 
 }  // namespace
 
-int xent_launch(const XentArgs &args, const LmLogprobArgs &scores, cudaStream_t st) {
+int xent_launch(const XentArgs &args, cudaStream_t st) {
     XentArgs a = args;
     void *one[] = {&a};
     const int64_t pad = xent_padded(a.M), piece = xent_piece(a.M, a.V);
+    const bool pairs = xent_pairs(a.M);
     if (cudaLaunchKernel(reinterpret_cast<const void *>(&xent_prepare_kernel),
                          dim3((unsigned)((a.M + kXentPrep - 1) / kXentPrep + 128 / kXentPrep)), dim3(32 * kXentPrep), one, 0,
                          st) != cudaSuccess)
         return -1;
-    for (int64_t m = 0; m < a.M; m += kLmRows) {
-        LmLogprobArgs s = scores;
-        const bool more = a.M - m > kLmRows;
-        s.M = more ? kLmRows : a.M - m;
-        s.hidden = scores.hidden + m * xent_width(a.H);
-        s.tokens = scores.tokens + m;
-        s.first = m;
-        int64_t parts = 0;
-        if (xent_pairs(a.M)) {
-            parts = (a.V + 127) / 128;
-            if (launch_scores<256, 2, true>(a, 0, (a.V + 255) / 256 * 256, s, st) != 0) return -1;
-        } else if (lm_logprob_products(s, &parts, st) != 0) {
+    for (int64_t m = 0; m < a.M; m += kXentPass) {
+        const bool more = a.M - m > kXentPass;
+        XentPass pass = {m, more ? kXentPass : a.M - m};
+        int64_t parts = xent_parts(a.M, a.V);
+        // one block of rows: smaller tiles spread the vocabulary more evenly
+        if ((pairs        ? launch_scores<256, 2, true>(a, 0, (a.V + 255) / 256 * 256, pass, st)
+             : pad == 128 ? launch_scores<128, 1, true>(a, 0, (a.V + 127) / 128 * 128, pass, st)
+                          : launch_scores<256, 1, true>(a, 0, (a.V + 255) / 256 * 256, pass, st)) != 0)
             return -1;
-        }
-        void *params[] = {&a, &s, &parts};
-        const int64_t places = more ? kLmRows : pad - m;
+        void *params[] = {&a, &pass, &parts};
+        const int64_t places = more ? kXentPass : pad - m;
         if (launch(reinterpret_cast<const void *>(&xent_loss_kernel), dim3((unsigned)(places / kXentJoinX)),
                    dim3(kXentJoinX, kXentJoinY), 0, params, st) != 0)
             return -1;
     }
     for (int64_t v0 = 0; (a.dh || a.dw || a.db) && v0 < a.V; v0 += piece) {
-        // one block of rows: smaller tiles spread the vocabulary more evenly
-        const bool pairs = xent_pairs(a.M);
-        if ((pairs        ? launch_scores<256, 2, false>(a, v0, piece, scores, st)
-             : pad == 128 ? launch_scores<128, 1, false>(a, v0, piece, scores, st)
-                          : launch_scores<256, 1, false>(a, v0, piece, scores, st)) != 0)
+        const XentPass none = {0, 0};
+        if ((pairs        ? launch_scores<256, 2, false>(a, v0, piece, none, st)
+             : pad == 128 ? launch_scores<128, 1, false>(a, v0, piece, none, st)
+                          : launch_scores<256, 1, false>(a, v0, piece, none, st)) != 0)
             return -1;
         int32_t width = (int32_t)piece;
         void *params[] = {&a, &v0, &width};
