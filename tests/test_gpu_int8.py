@@ -87,6 +87,12 @@ def test_scales_that_are_zero_or_not_finite(tsa):
     assert torch.isfinite(got[[0, 3, 4]][:, 10:]).all()
 
 
+@pytest.mark.parametrize("M,H", [(1, 16384), (3, 16384), (10, 5120), (16, 3040), (40, 16384), (130, 8192)])
+def test_wide_rows(tsa, M, H):
+    c = make(M + H, M, 700, H, pad=32)
+    check(c, tsa.lm_head_int8(c["h"], c["hs"], c["w"], c["ws"], dtype=torch.float32), False)
+
+
 def test_large(tsa):
     c = make(2, 300, 50001, 2064)
     check(c, tsa.lm_head_int8(c["h"], c["hs"], c["w"], c["ws"]), False)
