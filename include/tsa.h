@@ -576,7 +576,7 @@ size_t tsa_lm_head_int8_workspace_bytes(int64_t M, int64_t H);
  * NaN and NaN in the gradients that they take part in.
  * bf16 products and fp32 sums.  G goes through bf16 (half a step of 2^-8 of each
  * of its elements), grad_bias does not.  The weight is read once for the sums and
- * once or twice more for the gradients.  Sums in a fixed order: equal calls give
+ * twice more for the gradients.  Sums in a fixed order: equal calls give
  * equal bits.
  */
 int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t hidden_row_stride,

@@ -178,8 +178,9 @@ def test_repeats_on_another_stream(tsa):
     assert all(torch.equal(p, q) for p, q in zip(a, b)) and tsa.device_status() == 0
 
 
-def test_captured_and_replayed_on_new_inputs(tsa):
-    c, d = make(3, 150, 3000, 256, skip=0.1), make(4, 150, 3000, 256, skip=0.5)
+@pytest.mark.parametrize("M", [20, 150, 1000])
+def test_captured_and_replayed_on_new_inputs(tsa, M):
+    c, d = make(3, M, 3000, 256, skip=0.1), make(4, M, 3000, 256, skip=0.5)
     graph = torch.cuda.CUDAGraph()
     tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"])
     torch.cuda.synchronize()

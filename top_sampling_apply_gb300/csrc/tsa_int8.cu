@@ -97,7 +97,9 @@ __global__ void __launch_bounds__(256) int8_hidden_kernel(const Int8Args a) {
 // is cut into one run of rows a CTA, a multiple of 32, so that every SM moves
 // the same bytes; a run's last tile copies only the rows that it needs.  With
 // more hidden rows tiles go through those first, so that a weight tile comes from
-// HBM once and from L2 for the other blocks.
+// HBM once and from L2 for the other blocks.  V x H = 128,256 x 5,120: 16 rows 112
+// us, 5.9 TB/s (88 % of a copy), 64 rows 117 us, 128 rows 142 us; 2,048 rows x 32,000
+// x 4,096 376 us, 1,430 TFLOP/s, bound by copies from L2 and the conversions.
 //
 // A copy or product that one thread issues costs it some 100 cycles, ten times
 // what it costs a warp that goes through its loop together: whole tiles are one
