@@ -365,12 +365,13 @@ __device__ __forceinline__ RowRing make_ring(uint8_t *raw, uint64_t *full, int *
     return RowRing{raw, full, dead, stages, rows, bytes, n, blockIdx.x, gridDim.x};
 }
 constexpr int kRingStages = 4;
-// 384 threads: two CTAs an SM with up to 85 registers a thread (128 would leave
-// one, 64 spill); more, for rows of over 6,144 elements, 64.
-constexpr int ring_threads(bool big) { return big ? 1024 : 384; }
+// Threads and CTAs an SM that the registers are counted for: up to 384 with 80
+// registers a thread, two CTAs and more; 512 with 128, which the backward pass
+// needs (with 64 it spills: 8,192 x 8,192 139 us instead of 95); 1,024 with 64.
+constexpr int ring_threads(int c) { return c == 0 ? 384 : c == 1 ? 512 : 1024; }
 
-template <int DT, bool Q, bool BIG>
-__global__ void __launch_bounds__(ring_threads(BIG), BIG ? 1 : 2) norm_ring_kernel(NormArgs a, int stages) {
+template <int DT, bool Q, int C>
+__global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_ring_kernel(NormArgs a, int stages) {
     constexpr int W = Elem<DT>::AE, NV = kNormElems / W;
     using P = Part<DT, W>;
     extern __shared__ __align__(16) uint8_t raw[];
@@ -442,8 +443,8 @@ __global__ void __launch_bounds__(ring_threads(BIG), BIG ? 1 : 2) norm_ring_kern
     ring.finish(it);
 }
 
-template <int DT, bool BIG>
-__global__ void __launch_bounds__(ring_threads(BIG), BIG ? 1 : 2) norm_back_ring_kernel(NormBackArgs a, int stages) {
+template <int DT, int C>
+__global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_back_ring_kernel(NormBackArgs a, int stages) {
     constexpr int W = Elem<DT>::AE, NV = kNormElems / W;
     using P = Part<DT, W>;
     extern __shared__ __align__(16) uint8_t raw[];
@@ -535,17 +536,23 @@ dim3 norm_block(int64_t H, int E) {
 int norm_elems(int64_t H, bool vec) { return H <= (vec ? 2048 : 4096) ? 8 : kNormElems; }
 
 // Whether many long rows go through shared memory, and how.  Fewer than four
-// rows an SM leave nothing to fetch ahead.
+// rows an SM leave next to nothing to fetch ahead (bf16 with a residual, ring and
+// registers: 608 x 5,120 7.4 and 6.8 us, 1,216 x 5,120 11.8 and 12.1, 1,216 x 8,192
+// 15.8 and 20.5), and rows of up to 2,048 elements take small CTAs of which many fit.
 struct RingPlan {
-    int stages, ctas;  // 0: no ring
+    int stages, ctas, cls;  // stages 0: no ring
     size_t smem;
 };
 RingPlan ring_plan(int64_t N, int64_t H, int es, int rows) {
-    RingPlan p = {0, 0, 0};
+    RingPlan p = {0, 0, 0, 0};
     if (H <= 2048 || N < 4 * 152) return p;
-    const size_t stage = (size_t)H * es * rows;
-    p.ctas = stage <= 32 * 1024 ? 2 : 1;
-    p.stages = (int)((size_t)(200 * 1024) / p.ctas / stage);
+    const size_t stage = (size_t)H * es * rows, all = 200 * 1024;
+    const int threads = (int)norm_block(H, kNormElems).x;
+    while (ring_threads(p.cls) < threads) ++p.cls;
+    // two stages each at least, and 80 registers a thread
+    const size_t fit = all / (2 * stage), regs = p.cls == 0 ? 65536 / (80 * threads) : 1;
+    p.ctas = (int)(fit < 1 ? 1 : fit < regs ? fit : regs);
+    p.stages = (int)(all / p.ctas / stage);
     if (p.stages > kRingStages) p.stages = kRingStages;
     if (p.stages < 2) p.stages = 0;
     p.smem = stage * p.stages;
@@ -561,14 +568,14 @@ template <int DT, int W>
 const void *norm_form(int E, bool norm, bool q) {
     return !norm ? norm_fn<DT, W, false, true>(E) : q ? norm_fn<DT, W, true, true>(E) : norm_fn<DT, W, true, false>(E);
 }
-template <int DT, bool BIG>
+template <int DT, int C>
 const void *norm_ring_fn(bool q) {
-    return q ? reinterpret_cast<const void *>(&norm_ring_kernel<DT, true, BIG>)
-             : reinterpret_cast<const void *>(&norm_ring_kernel<DT, false, BIG>);
+    return q ? reinterpret_cast<const void *>(&norm_ring_kernel<DT, true, C>)
+             : reinterpret_cast<const void *>(&norm_ring_kernel<DT, false, C>);
 }
 template <int DT>
-const void *norm_ring_fn(bool q, bool big) {
-    return big ? norm_ring_fn<DT, true>(q) : norm_ring_fn<DT, false>(q);
+const void *norm_ring_fn(bool q, int cls) {
+    return cls == 0 ? norm_ring_fn<DT, 0>(q) : cls == 1 ? norm_ring_fn<DT, 1>(q) : norm_ring_fn<DT, 2>(q);
 }
 template <int DT, int W>
 const void *back_fn(int E, bool big) {  // big only with 16 elements
@@ -577,9 +584,10 @@ const void *back_fn(int E, bool big) {  // big only with 16 elements
                   : reinterpret_cast<const void *>(&norm_back_kernel<DT, W, kNormElems, false>);
 }
 template <int DT>
-const void *back_ring_fn(bool big) {
-    return big ? reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, true>)
-               : reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, false>);
+const void *back_ring_fn(int cls) {
+    return cls == 0   ? reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, 0>)
+           : cls == 1 ? reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, 1>)
+                      : reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, 2>);
 }
 
 // Whether every row of a tensor starts on `bytes` (a row alone needs no stride).
@@ -595,10 +603,11 @@ int norm_launch(const NormArgs &args, int dtype, bool norm, bool q, cudaStream_t
     const bool vec = a.H % ae == 0 && rows_on(a.x, a.xs, a.N, es, 16) && rows_on(a.r, a.rs, a.N, es, 16) &&
                      rows_on(a.res, a.ress, a.N, es, 16) && rows_on(a.w, 0, 1, 1, 16) &&
                      rows_on(a.out, a.os, a.N, q ? 1 : es, q ? ae : 16);
-    const RingPlan ring = vec && norm ? ring_plan(a.N, a.H, es, a.r ? 2 : 1) : RingPlan{0, 0, 0};
+    const RingPlan ring = vec && norm ? ring_plan(a.N, a.H, es, a.r ? 2 : 1) : RingPlan{0, 0, 0, 0};
     if (ring.stages > 0) {
-        const bool big = a.H > kNormElems * ring_threads(false);
-        const void *fn = dtype == 0 ? norm_ring_fn<0>(q, big) : dtype == 1 ? norm_ring_fn<1>(q, big) : norm_ring_fn<2>(q, big);
+        const void *fn = dtype == 0   ? norm_ring_fn<0>(q, ring.cls)
+                         : dtype == 1 ? norm_ring_fn<1>(q, ring.cls)
+                                      : norm_ring_fn<2>(q, ring.cls);
         if (prepare_kernel(fn, ring.smem, 1) != 0) return -1;
         int stages = ring.stages;
         void *params[] = {&a, &stages};
@@ -624,7 +633,8 @@ unsigned int *norm_status_ptr() {
     return reinterpret_cast<unsigned int *>(p);
 }
 
-// Parts of dw: two CTAs an SM, and no more than there are rows.
+// Parts of dw: two CTAs an SM (a ring of rows over 4,096 has no more), and no more
+// than there are rows.
 int64_t norm_back_parts(int64_t N, int64_t H, bool vec) {
     const int64_t y = norm_block(H, norm_elems(H, vec)).y, ctas = (N + y - 1) / y;
     return (ctas < 304 ? ctas : 304) * y;
@@ -642,10 +652,14 @@ int norm_back_launch(const NormBackArgs &args, int dtype, cudaStream_t st) {
     const int E = norm_elems(a.H, vec);
     const dim3 block = norm_block(a.H, E);
     int64_t parts = norm_back_parts(a.N, a.H, vec);
-    const RingPlan ring = vec ? ring_plan(a.N, a.H, es, a.gr ? 3 : 2) : RingPlan{0, 0, 0};
+    // Up to 4,096 elements two CTAs an SM hold their next row in registers, and as much is under way (16,384 x 4,096
+    // bf16 with a residual's gradient, registers and ring: 85 and 96 us, x 5,120 149 and 118, 8,192 x 8,192 94 and 95,
+    // 4,096 x 16,384 159 and 140).
+    const RingPlan ring = vec && a.H > 4096 ? ring_plan(a.N, a.H, es, a.gr ? 3 : 2) : RingPlan{0, 0, 0, 0};
     if (ring.stages > 0) {
-        const bool big = a.H > kNormElems * ring_threads(false);
-        const void *fn = dtype == 0 ? back_ring_fn<0>(big) : dtype == 1 ? back_ring_fn<1>(big) : back_ring_fn<2>(big);
+        const void *fn = dtype == 0   ? back_ring_fn<0>(ring.cls)
+                         : dtype == 1 ? back_ring_fn<1>(ring.cls)
+                                      : back_ring_fn<2>(ring.cls);
         if (prepare_kernel(fn, ring.smem, 1) != 0) return -1;
         int stages = ring.stages;
         void *params[] = {&a, &stages};
