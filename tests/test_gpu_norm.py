@@ -131,7 +131,7 @@ def test_norm_special_rows(tsa):
     assert torch.isnan(tsa.rms_norm(x[:1], w, eps=0.0).out).all()
 
 
-def check_back(tsa, g, x, w, gr, dx=None):
+def check_back(tsa, g, x, w, gr, dx=None, parts=300):
     N, H = x.shape
     rstd = head.rms_norm(x, w, 1e-6)[1].float()
     want, dw, h, f = head.rms_norm_backward(g, x, w, rstd, gr)
@@ -140,7 +140,7 @@ def check_back(tsa, g, x, w, gr, dx=None):
     mean = (f * h).abs().mean(-1, keepdim=True)
     tol = r * U * (2 * f.abs() + h.abs() * 60 * mean) + 3 * U * (want.abs() + r * f.abs() + r * h.abs() * mean)
     near(got[0], want, tol, x.dtype)
-    adds = N / min(N, 300) + 300 / 32 + 12
+    adds = N / min(N, parts) + parts / 32 + 12
     near(got[1], dw, (adds + 2) * U * (g.double() * h).abs().sum(0), w.dtype)
     return got
 
@@ -205,6 +205,43 @@ def test_many_long_rows(tsa, dt, H):
     a = tsa.rms_norm_backward(kept, x, w, b.rstd, grad_residual=r)
     c = tsa.rms_norm_backward(kept, x, w, b.rstd, grad_residual=r, grad_x=kept)
     assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1]) and tsa.device_status() == 0
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("N", [608, 2500])
+@pytest.mark.parametrize("H,pad,first", [(512, 1, 1), (513, 0, 0), (1001, 0, 3), (1001, 4, 1), (2064, 1, 5), (2064, 8, 1), (4881, 0, 0),
+                                         (6145, 7, 7), (8193, 0, 2), (12345, 0, 0), (16377, 0, 1), (16383, 0, 1)])
+def test_many_rows_that_start_anywhere(tsa, dt, N, H, pad, first):
+    """Rows whose starts lie at every place of 16 bytes, alike in each tensor: what is next to a row (NaN here) neither
+    counts nor is written."""
+    x, r, g = (rows(i, N, H, dt, pad, first) for i in (1, 2, 3))
+    out, res, dx = (rows(i, N, H, dt, pad, first) for i in (4, 5, 6))
+    w = rows(7, 1, H, dt)[0]
+    codes = torch.full((first + N * (H + pad),), 99, dtype=torch.int8, device=DEV)
+    q = codes[first:].as_strided((N, H), (H + pad, 1))
+    s = head.add_residual(x, r)
+    y, rstd = head.rms_norm(s, w, 1e-6)
+    a = tsa.rms_norm(x, w, residual=r, out=out, residual_out=res)
+    assert torch.equal(res, s)
+    near(a.rstd, rstd, 30 * U * rstd)
+    near(out, y, 32 * U * y.abs(), dt)
+    b = tsa.rms_norm(x, w, residual=r, quantize=True, out=q, residual_out=res)
+    assert torch.equal(res, s) and torch.equal(b.rstd, a.rstd)
+    check_codes(q, b.scale, y)
+    # up to eight parts of dw an SM, two rows each: N / parts + parts / 32 + 10 adds
+    parts = 152 * min(8, N // 304)
+    check_back(tsa, g, x, w, None, dx=dx, parts=parts)
+    check_back(tsa, g, x, w, r, dx=dx, parts=parts)
+    for t, beside in ((out, torch.isnan), (res, torch.isnan), (dx, torch.isnan), (q, lambda v: v == 99)):
+        buf = t.as_strided((t.storage_offset() + N * (H + pad),), (1,), 0)
+        assert beside(buf[:first]).all() and beside(buf[first:].view(N, H + pad)[:, H:]).all()
+    kept = tsa.rms_norm_backward(g, x, w, a.rstd, grad_residual=r, grad_x=dx)
+    over = tsa.rms_norm_backward(g, x, w, a.rstd, grad_residual=r, grad_x=g)
+    assert torch.equal(over[0], kept[0]) and torch.equal(over[1], kept[1])
+    y, _ = head.rms_norm(x, w, 1e-6)
+    tsa.rms_norm(x, w, out=x)
+    near(x, y, 32 * U * y.abs(), dt)
+    assert tsa.device_status() == 0
 
 
 def test_norm_of_more_elements_than_32_bits_count(tsa):

@@ -326,12 +326,19 @@ __global__ void __launch_bounds__(norm_threads(BIG)) norm_back_kernel(NormBackAr
 // after it, so that copies run STAGES - 1 rows ahead.  16,384 x 5,120 bf16 with a
 // residual: forward 108 us, 6.2 TB/s (124 with a CTA a row), backward 116 us, 5.8
 // TB/s (149 with the next row in registers, 214 without it).
+//
+// Rows that start anywhere (ODD: odd lengths, strides or bases, alike in every tensor) are taken 16 bytes at a time
+// all the same.  The grid is a multiple of 152 = 8 * 19 CTAs, so that each of a CTA's rows starts as far into 16
+// bytes as its first one does: its columns are shifted by that once, weights and the parts of dw with them, and only a
+// row's first and last 16 bytes are cut.  By single elements from the ring 16,384 x 4,881 takes 255 us forward and 488
+// backward, shifted 126 and 183.
+template <int SIZE, bool ODD>  // bytes of an element; whether rows start anywhere
 struct RowRing {
     uint8_t *mem;
     uint64_t *full;
     int *dead;  // a wait ran out: the CTA finishes without waiting
     int stages, rows;
-    uint32_t bytes;  // of a row
+    uint32_t bytes, pitch;  // of a row, and of its place
     int64_t n, first, step;  // rows in all, this CTA's first, and from one to the next
     // The i-th row of this CTA: `src` gives the rows of each input.
     template <class F>
@@ -339,13 +346,46 @@ struct RowRing {
         const int64_t row = first + i * step;
         if (threadIdx.x != 0 || row >= n) return;
         const int s = i % stages;
-        mbar_arrive_expect_tx(&full[s], bytes * rows);
-        for (int j = 0; j < rows; ++j) bulk_g2s(mem + (size_t)(s * rows + j) * bytes, src(j, row), bytes, &full[s]);
+        if constexpr (!ODD) {
+            mbar_arrive_expect_tx(&full[s], bytes * rows);
+            for (int j = 0; j < rows; ++j) bulk_g2s(mem + (size_t)(s * rows + j) * bytes, src(j, row), bytes, &full[s]);
+            return;
+        }
+        uint32_t sum = 0;
+        for (int j = 0; j < rows; ++j) {
+            const uint8_t *p = src(j, row);
+            const Span at = span(p, row);
+            sum += at.hi - at.lo;
+            uint8_t *to = mem + (size_t)(s * rows + j) * pitch;
+            for (uint32_t b = at.skip; b < at.lo; b += SIZE) put(to + b, p + (b - at.skip));
+            for (uint32_t b = at.hi; b < at.end; b += SIZE) put(to + b, p + (b - at.skip));
+        }
+        mbar_arrive_expect_tx(&full[s], sum);  // the waiting threads see the writes above, too
+        for (int j = 0; j < rows; ++j) {
+            const uint8_t *p = src(j, row);
+            const Span at = span(p, row);
+            bulk_g2s(mem + (size_t)(s * rows + j) * pitch + at.lo, p - at.skip + at.lo, at.hi - at.lo, &full[s]);
+        }
+    }
+    // A row in its place, from `skip` to `end`, and the whole 16 bytes that are copied.  Those at the first row's start
+    // and at the last one's end may hold memory that is not the tensor's: that row's part of them goes by elements.
+    struct Span {
+        uint32_t skip, end, lo, hi;
+    };
+    __device__ __forceinline__ Span span(const uint8_t *p, int64_t row) const {
+        const uint32_t skip = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15), end = skip + bytes;
+        return Span{skip, end, skip > 0 && row == 0 ? 16u : 0u, row == n - 1 ? end & ~15u : (end + 15) & ~15u};
+    }
+    __device__ __forceinline__ void put(uint8_t *to, const uint8_t *from) const {
+        if constexpr (SIZE == 4)
+            *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(from);
+        else
+            *reinterpret_cast<uint16_t *>(to) = *reinterpret_cast<const uint16_t *>(from);
     }
     __device__ __forceinline__ const uint8_t *wait(int i) const {
         const int s = i % stages;
         if (*(volatile int *)dead == 0 && !mbar_wait_bounded(&full[s], (i / stages) & 1u, &g_norm_status)) *(volatile int *)dead = 1;
-        return mem + (size_t)s * rows * bytes;
+        return mem + (size_t)s * rows * pitch;
     }
     // No copy may land after the CTA is gone (they all have, unless a wait ran out).
     __device__ __forceinline__ void finish(int done) const {
@@ -354,15 +394,21 @@ struct RowRing {
             mbar_wait_bounded(&full[i % stages], (i / stages) & 1u, &g_norm_status);
     }
 };
-__device__ __forceinline__ RowRing make_ring(uint8_t *raw, uint64_t *full, int *dead, int stages, int rows, uint32_t bytes,
-                                             int64_t n) {
+// Bytes of a row's place: ODD rows start up to 15 bytes into it.
+__host__ __device__ constexpr uint32_t ring_pitch(uint32_t bytes, bool odd) {
+    return odd ? (bytes + 15) / 16 * 16 + 16 : bytes;
+}
+template <int SIZE, bool ODD>
+__device__ __forceinline__ RowRing<SIZE, ODD> make_ring(uint8_t *raw, uint64_t *full, int *dead, int stages, int rows, int H,
+                                                        int64_t n) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
         *dead = 0;
         mbar_init_fence();
     }
     __syncthreads();
-    return RowRing{raw, full, dead, stages, rows, bytes, n, blockIdx.x, gridDim.x};
+    const uint32_t bytes = (uint32_t)(H * SIZE);
+    return RowRing<SIZE, ODD>{raw, full, dead, stages, rows, bytes, ring_pitch(bytes, ODD), n, blockIdx.x, gridDim.x};
 }
 constexpr int kRingStages = 4;
 // Threads and CTAs an SM that the registers are counted for: up to 384 with 80
@@ -370,25 +416,74 @@ constexpr int kRingStages = 4;
 // needs (with 64 it spills: 8,192 x 8,192 139 us instead of 95); 1,024 with 64.
 constexpr int ring_threads(int c) { return c == 0 ? 384 : c == 1 ? 512 : 1024; }
 
-template <int DT, bool Q, int C>
+// 16 bytes of a row from column c on, of which the first may be before the row and the last behind it: what is not the
+// row's reads as 0 and is not written.
+template <int DT, bool ODD>
+struct Cut {
+    static constexpr int W = Elem<DT>::AE;
+    using P = Part<DT, W>;
+    using One = Part<DT, 1>;
+    static __device__ __forceinline__ bool whole(int c, int H) { return !ODD || (c >= 0 && c + W <= H); }
+    static __device__ __forceinline__ void load(const uint8_t *place, int shift, int c, int H, float *x) {
+        P::load(place, c + shift, x);
+        if (whole(c, H)) return;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (c + j < 0 || c + j >= H) x[j] = 0.f;
+    }
+    static __device__ __forceinline__ void weight(const void *w, bool f32, int c, int H, float *x) {
+        if constexpr (!ODD) {
+            P::weight(w, f32, c, x);
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                x[j] = 0.f;
+                if (c + j >= 0 && c + j < H) One::weight(w, f32, c + j, x + j);
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t row, int c, int H, const float *x) {
+        if (whole(c, H)) {
+            P::store(p, row + c, x);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (c + j >= 0 && c + j < H) One::store(p, row + c + j, x + j);
+    }
+    static __device__ __forceinline__ void store_codes(int8_t *p, int64_t row, int c, int H, const float *x) {
+        if (whole(c, H)) {
+            P::store_codes(p, row + c, x);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (c + j >= 0 && c + j < H) One::store_codes(p, row + c + j, x + j);
+    }
+};
+
+template <int DT, bool ODD, bool Q, int C>
 __global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_ring_kernel(NormArgs a, int stages) {
     constexpr int W = Elem<DT>::AE, NV = kNormElems / W;
     using P = Part<DT, W>;
+    using R = Cut<DT, ODD>;
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ uint64_t full[kRingStages];
     __shared__ int dead;
     __shared__ float sh_sum[2][32];
     __shared__ uint32_t sh_max[2][32];
-    const int H = (int)a.H, step = blockDim.x * W, c0 = threadIdx.x * W;
-    const RowRing ring = make_ring(raw, full, &dead, stages, a.r ? 2 : 1, (uint32_t)(H * Elem<DT>::SIZE), a.N);
+    const int H = (int)a.H, step = blockDim.x * W;
+    const auto ring = make_ring<Elem<DT>::SIZE, ODD>(raw, full, &dead, stages, a.r ? 2 : 1, H, a.N);
     const auto src = [&](int j, int64_t row) {
         return static_cast<const uint8_t *>(j == 0 ? a.x : a.r) + row * (j == 0 ? a.xs : a.rs) * Elem<DT>::SIZE;
     };
     for (int i = 0; i < stages - 1; ++i) ring.issue(i, src);
+    const int shift = ODD ? (int)((reinterpret_cast<uintptr_t>(src(0, ring.first)) & 15) / Elem<DT>::SIZE) : 0;
+    const int c0 = threadIdx.x * W - shift;
     float w[NV][W];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (c0 + i * step < H) P::weight(a.w, a.w_f32, c0 + i * step, w[i]);
+        if (c0 + i * step < H) R::weight(a.w, a.w_f32, c0 + i * step, H, w[i]);
     int it = 0;
     for (int64_t row = ring.first; row < a.N; row += ring.step, ++it) {
         const uint8_t *in = ring.wait(it);
@@ -397,13 +492,13 @@ __global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_ring_ker
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
             if (c < H) {
-                P::load(in, c, v[i]);
+                R::load(in, shift, c, H, v[i]);
                 if (a.r) {
                     float r[W];
-                    P::load(in + ring.bytes, c, r);
+                    R::load(in + ring.pitch, shift, c, H, r);
 #pragma unroll
                     for (int j = 0; j < W; ++j) v[i][j] = P::held(v[i][j] + r[j]);
-                    if (a.res) P::store(a.res, row * a.ress + c, v[i]);
+                    if (a.res) R::store(a.res, row * a.ress, c, H, v[i]);
                 }
 #pragma unroll
                 for (int j = 0; j < W; ++j) s = fmaf(v[i][j], v[i][j], s);
@@ -423,7 +518,7 @@ __global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_ring_ker
                     v[i][j] = v[i][j] * rstd * w[i][j];
                     top = max(top, __float_as_uint(fabsf(v[i][j])));
                 }
-                if (!Q) P::store(a.out, row * a.os + c, v[i]);
+                if (!Q) R::store(a.out, row * a.os, c, H, v[i]);
             }
         }
         if constexpr (Q) {
@@ -435,7 +530,7 @@ __global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_ring_ker
                 if (c < H) {
 #pragma unroll
                     for (int j = 0; j < W; ++j) v[i][j] = k.of(v[i][j]);
-                    P::store_codes(static_cast<int8_t *>(a.out), row * a.os + c, v[i]);
+                    R::store_codes(static_cast<int8_t *>(a.out), row * a.os, c, H, v[i]);
                 }
             }
         }
@@ -443,27 +538,29 @@ __global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_ring_ker
     ring.finish(it);
 }
 
-template <int DT, int C>
+template <int DT, bool ODD, int C>
 __global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_back_ring_kernel(NormBackArgs a, int stages) {
     constexpr int W = Elem<DT>::AE, NV = kNormElems / W;
-    using P = Part<DT, W>;
+    using R = Cut<DT, ODD>;
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ uint64_t full[kRingStages];
     __shared__ int dead;
     __shared__ float sh[2][32];
-    const int H = (int)a.H, step = blockDim.x * W, c0 = threadIdx.x * W;
-    const RowRing ring = make_ring(raw, full, &dead, stages, a.gr ? 3 : 2, (uint32_t)(H * Elem<DT>::SIZE), a.N);
+    const int H = (int)a.H, step = blockDim.x * W;
+    const auto ring = make_ring<Elem<DT>::SIZE, ODD>(raw, full, &dead, stages, a.gr ? 3 : 2, H, a.N);
     const auto src = [&](int j, int64_t row) {
         const void *p = j == 0 ? a.x : j == 1 ? a.g : a.gr;
         return static_cast<const uint8_t *>(p) + row * (j == 0 ? a.xs : j == 1 ? a.gs : a.grs) * Elem<DT>::SIZE;
     };
     for (int i = 0; i < stages - 1; ++i) ring.issue(i, src);
+    const int shift = ODD ? (int)((reinterpret_cast<uintptr_t>(src(0, ring.first)) & 15) / Elem<DT>::SIZE) : 0;
+    const int c0 = threadIdx.x * W - shift;
     float w[NV][W], acc[NV][W];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
         for (int j = 0; j < W; ++j) acc[i][j] = 0.f;
-        if (c0 + i * step < H) P::weight(a.w, a.w_f32, c0 + i * step, w[i]);
+        if (c0 + i * step < H) R::weight(a.w, a.w_f32, c0 + i * step, H, w[i]);
     }
     int it = 0;
     for (int64_t row = ring.first; row < a.N; row += ring.step, ++it) {
@@ -474,8 +571,8 @@ __global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_back_rin
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
             if (c < H) {
-                P::load(in, c, h[i]);
-                P::load(in + ring.bytes, c, f[i]);
+                R::load(in, shift, c, H, h[i]);
+                R::load(in + ring.pitch, shift, c, H, f[i]);
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     h[i][j] *= rstd;
@@ -495,10 +592,10 @@ __global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_back_rin
                 float add[W];
 #pragma unroll
                 for (int j = 0; j < W; ++j) add[j] = 0.f;
-                if (a.gr) P::load(in + 2 * ring.bytes, c, add);
+                if (a.gr) R::load(in + 2 * ring.pitch, shift, c, H, add);
 #pragma unroll
                 for (int j = 0; j < W; ++j) f[i][j] = fmaf(rstd, fmaf(-h[i][j], mean, f[i][j]), add[j]);
-                P::store(a.dx, row * a.dxs + c, f[i]);
+                R::store(a.dx, row * a.dxs, c, H, f[i]);
             }
         }
     }
@@ -507,7 +604,7 @@ __global__ void __launch_bounds__(ring_threads(C), C == 0 ? 2 : 1) norm_back_rin
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < W; ++j)
-            if (c0 + i * step < H) a.part[blockIdx.x * a.H + c0 + i * step + j] = acc[i][j];
+            if (c0 + i * step + j >= 0 && c0 + i * step + j < H) a.part[blockIdx.x * a.H + c0 + i * step + j] = acc[i][j];
 }
 
 // dw: 32 columns a CTA, the parts over 32 rows of threads, then a tree.
@@ -540,24 +637,41 @@ int norm_elems(int64_t H, bool vec) { return H <= (vec ? 2048 : 4096) ? 8 : kNor
 // registers: 608 x 5,120 7.4 and 6.8 us, 1,216 x 5,120 11.8 and 12.1, 1,216 x 8,192
 // 15.8 and 20.5), and rows of up to 2,048 elements take small CTAs of which many fit.
 struct RingPlan {
-    int stages, ctas, cls;  // stages 0: no ring
+    int stages, ctas, cls, threads;  // stages 0: no ring
     size_t smem;
 };
-RingPlan ring_plan(int64_t N, int64_t H, int es, int rows) {
-    RingPlan p = {0, 0, 0, 0};
-    if (H <= 2048 || N < 4 * 152) return p;
-    const size_t stage = (size_t)H * es * rows, all = 200 * 1024;
-    const int threads = (int)norm_block(H, kNormElems).x;
-    while (ring_threads(p.cls) < threads) ++p.cls;
-    // two stages each at least, and 80 registers a thread
-    const size_t fit = all / (2 * stage), regs = p.cls == 0 ? 65536 / (80 * threads) : 1;
-    p.ctas = (int)(fit < 1 ? 1 : fit < regs ? fit : regs);
+constexpr int kRingCtas = 8, kRingBackRows = 2;
+// Threads of a row of H elements, of which `odd` ones may start up to 15 bytes into their first 16.
+int ring_block(int64_t H, int es, bool odd) { return (int)norm_block(H + (odd ? 16 / es - 1 : 0), kNormElems).x; }
+// CTAs an SM that 80 registers a thread leave, and that have `each` rows
+int64_t ring_most(int64_t N, int threads, int each) {
+    const int64_t regs = threads > ring_threads(0) ? 1 : 65536 / (80 * threads), rows = N / 152 / each;
+    const int64_t most = regs < rows ? regs : rows;
+    return most < kRingCtas ? most : kRingCtas;
+}
+RingPlan ring_plan(int64_t N, int64_t H, int es, int rows, int64_t least, bool odd, int each) {
+    RingPlan p = {0, 0, 0, 0, 0};
+    if (H <= least || N < 4 * 152) return p;
+    const size_t stage = (size_t)ring_pitch((uint32_t)(H * es), odd) * rows, all = 200 * 1024;
+    p.threads = ring_block(H, es, odd);
+    if (p.threads > ring_threads(2)) return p;
+    while (ring_threads(p.cls) < p.threads) ++p.cls;
+    // two stages each at least
+    const int64_t fit = (int64_t)(all / (2 * stage)), most = ring_most(N, p.threads, each);
+    p.ctas = (int)(fit < 1 ? 1 : fit < most ? fit : most);
     p.stages = (int)(all / p.ctas / stage);
     if (p.stages > kRingStages) p.stages = kRingStages;
     if (p.stages < 2) p.stages = 0;
     p.smem = stage * p.stages;
     return p;
 }
+// Rows that start anywhere go through the ring from 512 elements on (two warps: the stages' uses are a barrier apart);
+// in registers they go by single elements.  bf16 with a residual, registers and ring: 608 x 515 4.9 and 3.8 us, 16,384 x
+// 1,001 76 and 36, 608 x 4,881 26.7 and 8.2, 16,384 x 4,881 436 and 126, 4,096 x 12,345 338 and 83.  The backward pass
+// has as many parts of dw as CTAs, two rows each at least (with one 1,216 x 1,001 takes 14.1 us, with two 12.6, with
+// four 15.1), so that few short rows stay in registers: 1,216 x 1,001 10.7 and 12.6 us, 2,432 x 1,001 15.8 and 16.7, but
+// 4,096 x 515 20.7 and 20.2, 16,384 x 1,001 73 and 55, 1,216 x 2,051 18.0 and 14.8, 16,384 x 4,881 1,167 and 183.
+constexpr int64_t kRingOdd = 512;
 
 template <int DT, int W, bool NORM, bool Q>
 const void *norm_fn(int E) {
@@ -568,14 +682,18 @@ template <int DT, int W>
 const void *norm_form(int E, bool norm, bool q) {
     return !norm ? norm_fn<DT, W, false, true>(E) : q ? norm_fn<DT, W, true, true>(E) : norm_fn<DT, W, true, false>(E);
 }
-template <int DT, int C>
+template <int DT, bool ODD, int C>
 const void *norm_ring_fn(bool q) {
-    return q ? reinterpret_cast<const void *>(&norm_ring_kernel<DT, true, C>)
-             : reinterpret_cast<const void *>(&norm_ring_kernel<DT, false, C>);
+    return q ? reinterpret_cast<const void *>(&norm_ring_kernel<DT, ODD, true, C>)
+             : reinterpret_cast<const void *>(&norm_ring_kernel<DT, ODD, false, C>);
+}
+template <int DT, bool ODD>
+const void *norm_ring_fn(bool q, int cls) {
+    return cls == 0 ? norm_ring_fn<DT, ODD, 0>(q) : cls == 1 ? norm_ring_fn<DT, ODD, 1>(q) : norm_ring_fn<DT, ODD, 2>(q);
 }
 template <int DT>
-const void *norm_ring_fn(bool q, int cls) {
-    return cls == 0 ? norm_ring_fn<DT, 0>(q) : cls == 1 ? norm_ring_fn<DT, 1>(q) : norm_ring_fn<DT, 2>(q);
+const void *norm_ring_fn(bool odd, bool q, int cls) {
+    return odd ? norm_ring_fn<DT, true>(q, cls) : norm_ring_fn<DT, false>(q, cls);
 }
 template <int DT, int W>
 const void *back_fn(int E, bool big) {  // big only with 16 elements
@@ -583,16 +701,28 @@ const void *back_fn(int E, bool big) {  // big only with 16 elements
            : big  ? reinterpret_cast<const void *>(&norm_back_kernel<DT, W, kNormElems, true>)
                   : reinterpret_cast<const void *>(&norm_back_kernel<DT, W, kNormElems, false>);
 }
-template <int DT>
+template <int DT, bool ODD>
 const void *back_ring_fn(int cls) {
-    return cls == 0   ? reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, 0>)
-           : cls == 1 ? reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, 1>)
-                      : reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, 2>);
+    return cls == 0   ? reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, ODD, 0>)
+           : cls == 1 ? reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, ODD, 1>)
+                      : reinterpret_cast<const void *>(&norm_back_ring_kernel<DT, ODD, 2>);
+}
+template <int DT>
+const void *back_ring_fn(bool odd, int cls) {
+    return odd ? back_ring_fn<DT, true>(cls) : back_ring_fn<DT, false>(cls);
 }
 
 // Whether every row of a tensor starts on `bytes` (a row alone needs no stride).
 bool rows_on(const void *p, int64_t stride, int64_t N, int es, int bytes) {
     return !p || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && (N <= 1 || stride * es % bytes == 0));
+}
+
+// Whether a tensor's rows each start as far into 16 bytes of x's type as x's do (`es` bytes an element, x's `xes`), and
+// far enough from one another that what shares a row's first and last 16 bytes is in the tensor but at its two ends.
+bool rows_alike(const void *p, int64_t stride, int es, const void *x, int64_t xs, int xes) {
+    const int64_t ae = 16 / xes;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p) / es, x_at = reinterpret_cast<uintptr_t>(x) / xes;
+    return !p || (stride >= ae && (stride - xs) % ae == 0 && at % ae == x_at % ae);
 }
 
 }  // namespace
@@ -603,15 +733,18 @@ int norm_launch(const NormArgs &args, int dtype, bool norm, bool q, cudaStream_t
     const bool vec = a.H % ae == 0 && rows_on(a.x, a.xs, a.N, es, 16) && rows_on(a.r, a.rs, a.N, es, 16) &&
                      rows_on(a.res, a.ress, a.N, es, 16) && rows_on(a.w, 0, 1, 1, 16) &&
                      rows_on(a.out, a.os, a.N, q ? 1 : es, q ? ae : 16);
-    const RingPlan ring = vec && norm ? ring_plan(a.N, a.H, es, a.r ? 2 : 1) : RingPlan{0, 0, 0, 0};
+    const bool odd = !vec && rows_alike(a.x, a.xs, es, a.x, a.xs, es) && rows_alike(a.r, a.rs, es, a.x, a.xs, es) &&
+                     rows_alike(a.res, a.ress, es, a.x, a.xs, es) && rows_alike(a.out, a.os, q ? 1 : es, a.x, a.xs, es);
+    const RingPlan ring =
+        norm && (vec || odd) ? ring_plan(a.N, a.H, es, a.r ? 2 : 1, vec ? 2048 : kRingOdd, odd, 1) : RingPlan{0, 0, 0, 0, 0};
     if (ring.stages > 0) {
-        const void *fn = dtype == 0   ? norm_ring_fn<0>(q, ring.cls)
-                         : dtype == 1 ? norm_ring_fn<1>(q, ring.cls)
-                                      : norm_ring_fn<2>(q, ring.cls);
+        const void *fn = dtype == 0   ? norm_ring_fn<0>(odd, q, ring.cls)
+                         : dtype == 1 ? norm_ring_fn<1>(odd, q, ring.cls)
+                                      : norm_ring_fn<2>(odd, q, ring.cls);
         if (prepare_kernel(fn, ring.smem, 1) != 0) return -1;
         int stages = ring.stages;
         void *params[] = {&a, &stages};
-        return cudaLaunchKernel(fn, dim3((unsigned)(152 * ring.ctas)), norm_block(a.H, kNormElems), params, ring.smem, st) ==
+        return cudaLaunchKernel(fn, dim3((unsigned)(152 * ring.ctas)), dim3((unsigned)ring.threads), params, ring.smem, st) ==
                        cudaSuccess
                    ? 0
                    : -1;
@@ -633,15 +766,15 @@ unsigned int *norm_status_ptr() {
     return reinterpret_cast<unsigned int *>(p);
 }
 
-// Parts of dw: two CTAs an SM (a ring of rows over 4,096 has no more), and no more
-// than there are rows.
+// Parts of dw: two CTAs an SM (a ring's up to eight), and no more than there are rows.
 int64_t norm_back_parts(int64_t N, int64_t H, bool vec) {
     const int64_t y = norm_block(H, norm_elems(H, vec)).y, ctas = (N + y - 1) / y;
     return (ctas < 304 ? ctas : 304) * y;
 }
 int64_t norm_back_parts(int64_t N, int64_t H) {
-    const int64_t a = norm_back_parts(N, H, true), b = norm_back_parts(N, H, false);
-    return a > b ? a : b;
+    const int64_t a = norm_back_parts(N, H, true), b = norm_back_parts(N, H, false),
+                  c = H > kRingOdd && N >= 4 * 152 ? 152 * ring_most(N, ring_block(H, 4, false), kRingBackRows) : 0;
+    return a > b ? (a > c ? a : c) : b > c ? b : c;
 }
 
 int norm_back_launch(const NormBackArgs &args, int dtype, cudaStream_t st) {
@@ -655,16 +788,21 @@ int norm_back_launch(const NormBackArgs &args, int dtype, cudaStream_t st) {
     // Up to 4,096 elements two CTAs an SM hold their next row in registers, and as much is under way (16,384 x 4,096
     // bf16 with a residual's gradient, registers and ring: 85 and 96 us, x 5,120 149 and 118, 8,192 x 8,192 94 and 95,
     // 4,096 x 16,384 159 and 140).
-    const RingPlan ring = vec && a.H > 4096 ? ring_plan(a.N, a.H, es, a.gr ? 3 : 2) : RingPlan{0, 0, 0, 0};
+    const bool odd = !vec && rows_alike(a.x, a.xs, es, a.x, a.xs, es) && rows_alike(a.g, a.gs, es, a.x, a.xs, es) &&
+                     rows_alike(a.gr, a.grs, es, a.x, a.xs, es) && rows_alike(a.dx, a.dxs, es, a.x, a.xs, es);
+    const int64_t least = vec ? 4096 : a.N > 16 * 152 ? kRingOdd : 2048;
+    const RingPlan ring =
+        vec || odd ? ring_plan(a.N, a.H, es, a.gr ? 3 : 2, least, odd, kRingBackRows) : RingPlan{0, 0, 0, 0, 0};
     if (ring.stages > 0) {
-        const void *fn = dtype == 0   ? back_ring_fn<0>(ring.cls)
-                         : dtype == 1 ? back_ring_fn<1>(ring.cls)
-                                      : back_ring_fn<2>(ring.cls);
+        const void *fn = dtype == 0   ? back_ring_fn<0>(odd, ring.cls)
+                         : dtype == 1 ? back_ring_fn<1>(odd, ring.cls)
+                                      : back_ring_fn<2>(odd, ring.cls);
         if (prepare_kernel(fn, ring.smem, 1) != 0) return -1;
         int stages = ring.stages;
         void *params[] = {&a, &stages};
         parts = 152 * ring.ctas;
-        if (cudaLaunchKernel(fn, dim3((unsigned)parts), block, params, ring.smem, st) != cudaSuccess) return -1;
+        if (cudaLaunchKernel(fn, dim3((unsigned)parts), dim3((unsigned)ring.threads), params, ring.smem, st) != cudaSuccess)
+            return -1;
     } else if (a.N > 0) {
         const bool big = a.H > kNormElems * norm_threads(false);
         const void *fn = dtype == 0   ? (vec ? back_fn<0, 4>(E, big) : back_fn<0, 1>(E, big))
