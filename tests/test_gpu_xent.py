@@ -313,3 +313,31 @@ def test_refusals(tsa):
                  lambda: f(h[:, :12].contiguous(), w[:, :12].contiguous(), t)):
         with pytest.raises(tsa.TSAError):
             call()
+
+
+@pytest.mark.parametrize("M", [4, 140, 1000])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+def test_a_row_without_a_finite_score(tsa, M, cap):
+    """It has an lse of -inf, a loss of NaN and a gradient of NaN; a skipped row like it has nothing of that."""
+    c = make(M, M, 700, 72, bias=True)
+    c["h"][1], c["h"][2], c["t"][2] = float("nan"), float("nan"), -1
+    r = tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"], softcap=cap)
+    assert r.lse[1] == float("-inf") and torch.isnan(r.row_loss[1]) and torch.isnan(r.loss)
+    assert torch.isnan(r.grad_hidden[1]).all() and torch.isnan(r.grad_weight).all() and torch.isnan(r.grad_bias).all()
+    others = torch.arange(M, device=DEV) != 1
+    assert torch.isfinite(r.grad_hidden[others]).all() and torch.isfinite(r.row_loss[others]).all()
+    assert r.lse[2] == 0 and r.row_loss[2] == 0 and (r.grad_hidden[2] == 0).all()
+
+
+@pytest.mark.parametrize("M", [4, 140, 1000])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+def test_a_score_of_nan_in_a_row_that_counts(tsa, M, cap):
+    """It counts as -inf: no part in the row's loss, and none in the gradients of the other entries."""
+    c = make(M, M, 700, 72, bias=True)
+    c["b"][9] = float("nan")
+    c["t"][c["t"] == 9] = 8
+    r = tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"], softcap=cap)
+    keep = torch.arange(700, device=DEV) != 9
+    d = dict(c, w=c["w"][keep], b=c["b"][keep], t=torch.where(c["t"] > 9, c["t"] - 1, c["t"]))
+    assert (r.grad_weight[9] == 0).all() and r.grad_bias[9] == 0
+    check(d, r._replace(grad_weight=r.grad_weight[keep], grad_bias=r.grad_bias[keep]), cap)

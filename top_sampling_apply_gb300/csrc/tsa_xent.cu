@@ -496,6 +496,8 @@ __global__ void __launch_bounds__(kXentThreads, 1)
                 continue;
             }
             const float neg = -k.z * kLog2eH;
+            // A score of NaN has no slope, and no part in a row's gradient, but where the row has no finite score at all.
+            const float flat = k.z > -INFINITY ? 0.f : __int_as_float(0x7FC00000);
 #pragma unroll
             for (int g0 = 0; g0 < NC; g0 += 64) {
 #pragma unroll
@@ -508,9 +510,9 @@ __global__ void __launch_bounds__(kXentThreads, 1)
                         const float y = fmaxf(x[q], -INFINITY);  // NaN counts as -inf
                         float p = k.x * ex2_approx(fmaf(y, kLog2eH, neg));
                         if (want - (g0 + h0) == q) p -= k.y;
-                        if (a.cap > 0.f) {  // (a score of NaN has no slope)
+                        if (a.cap > 0.f) {
                             const float share = y * cap.inv;
-                            p = y > -INFINITY ? p * fmaf(-share, share, 1.f) : 0.f;
+                            p = y > -INFINITY ? p * fmaf(-share, share, 1.f) : flat;
                         }
                         x[q] = q < in ? p : 0.f;
                     }
