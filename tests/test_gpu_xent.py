@@ -341,3 +341,13 @@ def test_a_score_of_nan_in_a_row_that_counts(tsa, M, cap):
     d = dict(c, w=c["w"][keep], b=c["b"][keep], t=torch.where(c["t"] > 9, c["t"] - 1, c["t"]))
     assert (r.grad_weight[9] == 0).all() and r.grad_bias[9] == 0
     check(d, r._replace(grad_weight=r.grad_weight[keep], grad_bias=r.grad_bias[keep]), cap)
+
+
+@pytest.mark.parametrize("M", [4, 140, 1000])
+def test_no_row_counts_and_what_the_head_holds_is_not_finite(tsa, M):
+    c = make(M, M, 700, 72, bias=True)
+    c["t"].fill_(-1)
+    c["b"][3], c["b"][4], c["b"][5], c["w"][6], c["w"][7] = (float(x) for x in ("inf", "-inf", "nan", "inf", "nan"))
+    for cap in (0.0, 5.0):
+        for x in tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"], softcap=cap):
+            assert (x == 0).all()

@@ -305,7 +305,7 @@ struct XentArgs {
     float *weight_c, *row_loss_c;
     float2 *part;            // of a pass's rows: a part's largest score and its sum against it
     float *tok;              // of a pass's rows: the target's score
-    float4 *coef;            // what a place's gradient needs
+    float4 *coef;            // what a place's gradient needs, and 1 if it has a row
     uint16_t *hidden_c;      // [padded, xent_width(H)]
     uint16_t *grad;          // [padded, piece]: a piece of the vocabulary's part of G
     float *acc;              // [splits][padded, H]: dH so far

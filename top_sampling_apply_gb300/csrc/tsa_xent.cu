@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kXentJoinX *kXentJoinY) xent_loss_kernel(const
     a.row_loss[a.rows[i]] = loss;
     a.lse[a.rows[i]] = l;
     const float w = a.row_weight ? a.weight_c[i] / a.scale[0] : 1.f;
-    a.coef[i] = make_float4(c != 0.f ? w * fmaf(2.f * c, l, 1.f) : w, w, l, 0.f);
+    a.coef[i] = make_float4(c != 0.f ? w * fmaf(2.f * c, l, 1.f) : w, w, l, 1.f);
 }
 
 __device__ unsigned int g_xent_status;
@@ -496,15 +496,18 @@ __global__ void __launch_bounds__(kXentThreads, 1)
                 continue;
             }
             const float neg = -k.z * kLog2eH;
+            // A place's entries in the piece: none behind the last row, where the products are 0 but a bias of +inf would
+            // make NaN of them.
+            const int32_t here = k.w > 0.f ? left - c0 : 0;
             // A score of NaN has no slope, and no part in a row's gradient, but where the row has no finite score at all.
-            const float flat = k.z > -INFINITY ? 0.f : __int_as_float(0x7FC00000);
+            const float flat = neg < INFINITY ? 0.f : __int_as_float(0x7FC00000);
 #pragma unroll
             for (int g0 = 0; g0 < NC; g0 += 64) {
 #pragma unroll
                 for (int h0 = 0; h0 < 64; h0 += 32) {
                     float *x = z + g0 + h0;
                     if (a.cap > 0.f) soft_cap<32>(x, cap);
-                    const int32_t in = left - (c0 + g0 + h0);
+                    const int32_t in = here - (g0 + h0);
 #pragma unroll
                     for (int q = 0; q < 32; ++q) {
                         const float y = fmaxf(x[q], -INFINITY);  // NaN counts as -inf
