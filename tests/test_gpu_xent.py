@@ -351,3 +351,59 @@ def test_no_row_counts_and_what_the_head_holds_is_not_finite(tsa, M):
     for cap in (0.0, 5.0):
         for x in tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"], softcap=cap):
             assert (x == 0).all()
+
+
+def fastest_ms(f, n=8):
+    best = float("inf")
+    for _ in range(n):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        torch.cuda.synchronize()
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+# two pieces of the vocabulary, whole, and one entry more: pairs of CTAs, single ones, one block of rows
+@pytest.mark.parametrize("M,V", [(1000, 2 * 29_184), (300, 2 * 38_912), (100, 2 * 38_912)])
+def test_a_last_piece_costs_what_it_holds(tsa, M, V):
+    c, d = make(1, M, V, 1024), make(1, M, V + 1, 1024)
+    whole, more = (fastest_ms(lambda: tsa.lm_head_cross_entropy(x["h"], x["w"], x["t"])) for x in (c, d))
+    assert more < 1.5 * whole, (more, whole)
+
+
+def live_rows(c, n):
+    """All but n of the rows skipped, in no order, and what the skipped ones hold a NaN."""
+    M = len(c["t"])
+    out = torch.randperm(M, generator=torch.Generator().manual_seed(M + n))[n:].to(DEV)
+    c["t"] = c["t"].clamp(min=0)
+    c["t"][out], c["h"][out] = -1, float("nan")
+    return c
+
+
+def in_workspace_of(tsa, c, fill):
+    """The call through the C entry, with a workspace that holds `fill` in every byte."""
+    lib, (M, H), V = tsa.load_library(), c["h"].shape, c["w"].shape[0]
+    dh, dw = torch.empty_like(c["h"]), torch.empty_like(c["w"])
+    db, loss, row, lse = (torch.empty(n, device=DEV) for n in (V, 1, M, M))
+    n = lib.tsa_lm_head_cross_entropy_workspace_bytes(M, H, V, 1, 1)
+    ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+    st = lib.tsa_lm_head_cross_entropy(
+        c["h"].data_ptr(), M, H, c["h"].stride(0), c["w"].data_ptr(), V, c["w"].stride(0), c["b"].data_ptr(), 0.0,
+        c["t"].data_ptr(), None, 0.0, loss.data_ptr(), row.data_ptr(), lse.data_ptr(), dh.data_ptr(), dh.stride(0),
+        dw.data_ptr(), dw.stride(0), db.data_ptr(), ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    torch.cuda.synchronize()
+    return loss, row, lse, dh, dw, db
+
+
+# one block of rows, several, pairs; vocabularies of a part of a tile, of just over a piece, and of pieces and a half
+@pytest.mark.parametrize("M,live,V", [(20, 20, 300), (20, 15, 65_600), (300, 200, 1000), (300, 300, 65_537),
+                                      (1000, 1000, 29_185), (1100, 700, 29_000), (1100, 100, 1111), (9000, 8500, 6001)])
+def test_workspaces_that_hold_anything(tsa, M, live, V):
+    c = live_rows(make(M, M, V, 136, bias=True), live)
+    a, b = in_workspace_of(tsa, c, 0xFF), in_workspace_of(tsa, c, 0)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    check(c, tsa.CrossEntropy(a[0][0], *a[1:]))

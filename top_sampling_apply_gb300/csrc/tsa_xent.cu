@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kXentThreads, 1)
     const int32_t rows = SUMS ? (int32_t)max((int64_t)0, min(a.count[0] - pass.first, pass.M)) : xent_end(a);
     const int32_t row_blocks = (rows + 128 * P - 1) / (128 * P), t_first = blockIdx.x / P, t_step = gridDim.x / P;
     const int32_t left = (int32_t)(a.V - v0 < width ? a.V - v0 : width);  // the piece's entries
-    const int32_t tiles = row_blocks * (SUMS ? (left + N - 1) / N : width / N);
+    const int32_t tiles = row_blocks * ((left + N - 1) / N);  // (the products take whole tiles of G, and none behind them)
     const uint32_t tmem = s.tmem;
 
     if (warp == 0) {
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(1024) xent_bias_kernel(const XentArgs a, int64
     pdl_wait_primary();
     const int32_t c = blockIdx.x * 32 + threadIdx.x, parts = xent_end(a) / 32;
     float s = 0.f;
-    if (c < width)
+    if (c < width && v0 + c < a.V)
         for (int32_t p = threadIdx.y; p < parts; p += 32) s += a.db_part[(int64_t)p * width + c];
     sh[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
