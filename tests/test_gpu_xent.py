@@ -407,3 +407,38 @@ def test_workspaces_that_hold_anything(tsa, M, live, V):
     a, b = in_workspace_of(tsa, c, 0xFF), in_workspace_of(tsa, c, 0)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
     check(c, tsa.CrossEntropy(a[0][0], *a[1:]))
+
+
+# pairs of CTAs (rows from 897 on): 1, 2, 5, 8 and 9 blocks of 128 rows that count; widths of one and several K steps,
+# column blocks and chunks of sums, multiples of 64 and not
+@pytest.mark.parametrize("M,live", [(897, 897), (1023, 640), (1100, 1100), (1300, 130), (1100, 100)])
+@pytest.mark.parametrize("V,H", [(3001, 136), (2500, 264), (4099, 520), (3000, 1088), (2001, 2056)])
+@pytest.mark.parametrize("cap,z_loss", [(0.0, 0.0), (5.0, 1e-3)])
+def test_pairs_of_ctas(tsa, M, live, V, H, cap, z_loss):
+    c = live_rows(make(M + V, M, V, H, bias=True, weighted=True, pad=24), live)
+    r = tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"], softcap=cap, row_weight=c["row_weight"],
+                                  z_loss=z_loss)
+    check(c, r, cap, z_loss)
+    c["row_weight"] = c["b"] = None
+    r = tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], softcap=cap, z_loss=z_loss)
+    check(c, r, cap, z_loss)
+
+
+@pytest.mark.parametrize("M", [1, 100, 200, 1000])
+@pytest.mark.parametrize("V,H", [(500, 1032), (700, 2056), (300, 5120), (400, 16376), (200, 16384)])
+def test_wide_rows(tsa, M, V, H):
+    c = make(M + H, M, V, H, bias=True, skip=0.1 if M > 1 else 0.0, pad=8)
+    check(c, tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"], softcap=20.0, z_loss=1e-4), 20.0, 1e-4)
+
+
+def test_each_gradient_of_pairs(tsa):
+    c = live_rows(make(9, 1100, 3001, 328, bias=True), 900)
+    whole = tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"])
+    check(c, whole)
+    for k in range(8):
+        r = tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"], bias=c["b"], grad_hidden=bool(k & 1),
+                                      grad_weight=bool(k & 2), grad_bias=bool(k & 4))
+        for on, name in ((k & 1, "grad_hidden"), (k & 2, "grad_weight"), (k & 4, "grad_bias")):
+            a, b = getattr(r, name), getattr(whole, name)
+            assert (a is None) if not on else torch.equal(a, b), (k, name)
+        assert torch.equal(r.loss, whole.loss) and torch.equal(r.row_loss, whole.row_loss)
