@@ -442,3 +442,20 @@ def test_each_gradient_of_pairs(tsa):
             a, b = getattr(r, name), getattr(whole, name)
             assert (a is None) if not on else torch.equal(a, b), (k, name)
         assert torch.equal(r.loss, whole.loss) and torch.equal(r.row_loss, whole.row_loss)
+
+
+def test_sums_over_the_most_rows_are_not_cut_short(tsa):
+    """Scores of 0 over three entries make G exact: bf16(1/3), and bf16(-2/3) at the target.  Rows in the order of their
+    targets let the sums of dW climb and come back.  Tensor cores cut a sum at each 16 rows, by 2^-22 of it at most; a
+    sum of fp32 that begins anew each 8,192 rows is then off by that of its steps, 2^-24 of the whole for each part
+    added, and half a bf16 step in the end."""
+    M, V, H = 65536, 3, 128
+    h = (1 + torch.rand(M, H, generator=torch.Generator(device=DEV).manual_seed(0), device=DEV)).bfloat16()
+    t = torch.arange(M, device=DEV) * V // M
+    r = tsa.lm_head_cross_entropy(h, torch.zeros(V, H, dtype=torch.bfloat16, device=DEV), t)
+    for v in range(V):
+        G = torch.where(t == v, -0.66796875, 0.333984375).double()
+        steps = (G[:, None] * h.double()).view(8, 512, 16, H).sum(2)
+        want, parts = steps.sum((0, 1)) / M, steps.cumsum(1)
+        tol = (2.0 ** -22 * parts.abs().sum((0, 1)) + 8 * U * parts[:, -1].cumsum(0).abs().amax(0)) / M
+        near(r.grad_weight[v], want, tol + 2.0 ** -8 * (want.abs() + tol), v)

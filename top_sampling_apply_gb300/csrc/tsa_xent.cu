@@ -640,10 +640,14 @@ __device__ __forceinline__ void dh_results(const float *z, float *acc, bool add,
     *reinterpret_cast<uint4 *>(to) = make_uint4(pack_bf16(p.x, p.y), pack_bf16(p.z, p.w), pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
 }
 
-// A unit's sum stays in tensor memory from its first K to its last, 65,536 at
-// most (kXentMaxRows, and the width of a piece): the tensor cores cut what they
-// add, by 2^-24 of the sum on average a step of 16, which over 4,096 steps is
-// 2^-12 at most against the 2^-9 of the result's rounding.
+// The tensor cores cut what they add, a step of 16 by 2^-23 of the sum so far on average, always towards zero.  Sums
+// over rows turn from one sign to the other (p h of all rows, -h of the entry's own), and what was cut on the way up stays:
+// so a sum in tensor memory ends after 8,192 of K, 512 steps, and those are added in fp32.  What is lost is then 2^-15 of
+// a part's largest sum, whatever K is.  65,536 rows x 256 x 128 in the order of their targets, hidden rows of mean 1: dW was
+// off by 0.55 % of itself with one sum for all rows where exact sums of the same G give 0.39 %, and 1.0e-4 of the sum
+// of absolute terms too small in the mean; by 0.42 % against 0.40 and 2.6e-5 so.  Up to 8,192 rows nothing is to be seen.
+constexpr int kXentSums = 8192 / kTcK;
+
 template <int P>
 __global__ void __launch_bounds__(kXentThreads, 1)
     xent_products_kernel(const __grid_constant__ CUtensorMap map_gk, const __grid_constant__ CUtensorMap map_gm,
@@ -699,22 +703,23 @@ __global__ void __launch_bounds__(kXentThreads, 1)
         XentRing<STAGES, P> r(s, ring, S::STAGE, false);
         uint32_t j = 0;
         for (int32_t x = 0; r.ok && units.get(x, u); ++x) {
-            if (u.ks == 0) continue;
-            const uint32_t b = j & 1u, idesc = S::IDESC | kAcrossB | (u.is_dh ? 0u : kAcrossA), step = u.is_dh ? 2 : 128;
-            r.ok = xent_wait_drained<P>(&s.drained[b], ((j >> 1) & 1u) ^ 1u);
+            const uint32_t idesc = S::IDESC | kAcrossB | (u.is_dh ? 0u : kAcrossA), step = u.is_dh ? 2 : 128;
             for (int kb = 0; kb < u.ks; ++kb, r.next()) {
+                const uint32_t b = j & 1u;
+                if (kb % kXentSums == 0) r.ok = xent_wait_drained<P>(&s.drained[b], ((j >> 1) & 1u) ^ 1u);
                 if (!r.wait_full()) break;
+                const bool end = kb % kXentSums == kXentSums - 1 || kb == u.ks - 1;
                 const uint64_t da = u.is_dh ? smem_tile(r.stage()) : smem_tile_across(r.stage(), BOX);
                 const uint64_t db = smem_tile_across(r.stage() + S::A_BYTES, BOX);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTcK / 16; ++k)
-                        mma_bf16_by<P>(tmem + b * 256, da + step * k, db + 128 * k, idesc, kb > 0 || k > 0);
+                        mma_bf16_by<P>(tmem + b * 256, da + step * k, db + 128 * k, idesc, kb % kXentSums > 0 || k > 0);
                     mma_commit_by<P>(r.empty());
-                    if (kb == u.ks - 1) mma_commit_by<P>(&s.done[b]);
+                    if (end) mma_commit_by<P>(&s.done[b]);
                 }
+                if (end) ++j;
             }
-            ++j;
         }
         if (elect_one()) mma_commit_own<P>(&s.last);
         xent_warp_wait(&s.last, 0);
@@ -726,42 +731,51 @@ __global__ void __launch_bounds__(kXentThreads, 1)
         bool ok = true;
         for (int32_t x = 0; ok && units.get(x, u); ++x) {
             const int32_t y0 = u.y + rank * 128 + quarter * 32, h0 = u.x + half * NC;
-            const uint32_t b = j & 1u;
-            if (u.ks > 0) {  // (a part of a short last piece may be empty)
+            const bool used = u.is_dh || y0 < left;
+            float z[NC];
+#pragma unroll
+            for (int q = 0; q < NC; ++q) z[q] = 0.f;
+            for (int k0 = 0; k0 < u.ks; k0 += kXentSums, ++j) {  // (a part of a short last piece may be empty)
+                const uint32_t b = j & 1u;
                 ok = xent_warp_wait(&s.done[b], (j >> 1) & 1u);
                 if (!ok) break;
                 mma_fence_after();
-                ++j;
+#pragma unroll
+                for (int q = 0; q < NC; q += 16) {
+                    if (!used || h0 + q >= a.H) break;
+                    uint32_t r[16];
+                    __syncwarp();
+                    TmemLoad<16>::ld(at + b * 256 + q, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2)
+                        split_pair(add2(pair_of(z[q + i], z[q + i + 1]),
+                                        pair_of(__uint_as_float(r[i]), __uint_as_float(r[i + 1]))),
+                                   z[q + i], z[q + i + 1]);
+                }
+                xent_drained<P>(&s.drained[b], lane);
             }
+            if (!ok) break;
             const int32_t m = y0 + lane;
             const bool mine = u.is_dh && m < n, last = a.splits == 1 && v0 + left >= a.V;
             float *acc = mine ? a.acc + ((int64_t)u.split * a.padded + m) * a.H + h0 : nullptr;
             uint16_t *to = mine && last ? a.dh + (int64_t)a.rows[m] * a.dhstride + h0 : nullptr;
 #pragma unroll
             for (int g = 0; g < NC; g += 64) {
-                if (h0 + g >= a.H || (!u.is_dh && y0 >= left)) break;
-                float z[64];
+                if (!used || h0 + g >= a.H) break;
 #pragma unroll
-                for (int q = 0; q < 64; q += 16) {
-                    uint32_t r[16];
-                    __syncwarp();
-                    TmemLoad<16>::ld(at + b * 256 + g + q, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) z[q + i] = u.ks > 0 ? __uint_as_float(r[i]) * scale : 0.f;
-                }
+                for (int q = 0; q < 64; ++q) z[g + q] *= scale;
                 if (!u.is_dh) {
                     slab_wait(lane);
-                    slab_row(slab, lane, z);
+                    slab_row(slab, lane, z + g);
                     slab_store(&map_dw, slab, lane, h0 + g, y0);
                 } else if (mine) {
 #pragma unroll
                     for (int q = 0; q < 64; q += 8) {
-                        if (h0 + g + q < a.H) dh_results(z + q, acc + g + q, v0 > 0, last ? to + g + q : nullptr);
+                        if (h0 + g + q < a.H) dh_results(z + g + q, acc + g + q, v0 > 0, last ? to + g + q : nullptr);
                     }
                 }
             }
-            if (u.ks > 0) xent_drained<P>(&s.drained[b], lane);
         }
         if (lane == 0) tma_store_done();
     }
