@@ -180,3 +180,15 @@ def test_binding_refuses_host_tensors():
                  lambda: tsa.lm_head_int8(q, v, q, v), lambda: tsa.lm_head_cross_entropy(b, b, i)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_refused_shapes_want_no_workspace(lib):
+    """The binding makes room before the call checks its shapes: one that is refused must not ask for any."""
+    x, q = lib.tsa_lm_head_cross_entropy_workspace_bytes, lib.tsa_lm_head_int8_workspace_bytes
+    most = lib.tsa_max_vocab(2)
+    for M, H, V in (((1 << 16) + 1, 64, 100), (1 << 40, 4096, 128256), (2, 16392, 100), (2, 1 << 50, 100),
+                    (2, 64, most + 1), (2, 64, 1 << 60), (-1, 64, 100), (2, 0, 100), (2, 64, 0)):
+        assert x(M, H, V, 1, 1) == 0, (M, H, V)
+    for M, H in (((1 << 20) + 1, 64), (1 << 60, 64), (2, 16400), (2, 1 << 60), (0, 64), (2, 0)):
+        assert q(M, H) == 0, (M, H)
+    assert x(1 << 16, 16384, most, 1, 1) > 0 and q(1 << 20, 16384) == (1 << 20) * 16384 * 2

@@ -15,6 +15,8 @@ namespace {
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+constexpr int64_t kHeadMaxH = 16384, kInt8MaxRows = 1 << 20;
+
 int check_norm_rows(tsa_dtype dtype, int64_t N, int64_t H, int64_t stride) {
     if (dtype != TSA_F32 && dtype != TSA_F16 && dtype != TSA_BF16) return TSA_ERR_DTYPE;
     if (N < 0 || N > 0x7FFFFFFFll || H < 1 || H > kNormMaxH || stride < H) return TSA_ERR_SHAPE;
@@ -181,7 +183,7 @@ int tsa_rms_norm_backward(const void *grad, int64_t grad_row_stride, const void 
 }
 
 size_t tsa_lm_head_int8_workspace_bytes(int64_t M, int64_t H) {
-    return M < 1 || H < 1 ? 0 : align256((size_t)M * (size_t)int8_padded(H) * 2);
+    return M < 1 || M > kInt8MaxRows || H < 1 || H > kHeadMaxH ? 0 : align256((size_t)M * (size_t)int8_padded(H) * 2);
 }
 
 int tsa_lm_head_int8(const int8_t *hidden, int64_t M, int64_t H, int64_t hidden_row_stride, const float *hidden_scale,
@@ -189,7 +191,7 @@ int tsa_lm_head_int8(const int8_t *hidden, int64_t M, int64_t H, int64_t hidden_
                      const float *bias, void *out, tsa_dtype out_dtype, int64_t out_row_stride, void *workspace,
                      size_t workspace_bytes, void *stream) {
     if (out_dtype != TSA_F32 && out_dtype != TSA_F16 && out_dtype != TSA_BF16) return TSA_ERR_DTYPE;
-    if (M < 0 || M > (1ll << 20) || H < 16 || H > 16384 || H % 16 != 0 || V < 1 || V > tsa_max_vocab(out_dtype) ||
+    if (M < 0 || M > kInt8MaxRows || H < 16 || H > kHeadMaxH || H % 16 != 0 || V < 1 || V > tsa_max_vocab(out_dtype) ||
         hidden_row_stride < H || weight_row_stride < H || out_row_stride < V)
         return TSA_ERR_SHAPE;
     if (M == 0) return TSA_OK;
@@ -219,7 +221,7 @@ int tsa_lm_head_int8(const int8_t *hidden, int64_t M, int64_t H, int64_t hidden_
 }
 
 size_t tsa_lm_head_cross_entropy_workspace_bytes(int64_t M, int64_t H, int64_t V, int grads, int bias) {
-    if (M < 1 || H < 8 || V < 1) return 0;
+    if (M < 1 || M > kXentMaxRows || H < 8 || H > kHeadMaxH || V < 1 || V > tsa_max_vocab(TSA_BF16)) return 0;
     return xent_layout(M, H, V, grads != 0, bias != 0).end;
 }
 
@@ -229,7 +231,7 @@ int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t 
                               float *row_loss_out, float *lse_out, void *grad_hidden_out,
                               int64_t grad_hidden_row_stride, void *grad_weight_out, int64_t grad_weight_row_stride,
                               float *grad_bias_out, void *workspace, size_t workspace_bytes, void *stream) {
-    if (M < 0 || M > kXentMaxRows || H < 8 || H > 16384 || H % 8 != 0 || V < 1 || V > tsa_max_vocab(TSA_BF16) ||
+    if (M < 0 || M > kXentMaxRows || H < 8 || H > kHeadMaxH || H % 8 != 0 || V < 1 || V > tsa_max_vocab(TSA_BF16) ||
         hidden_row_stride < H || weight_row_stride < H || (grad_hidden_out && grad_hidden_row_stride < H) ||
         (grad_weight_out && grad_weight_row_stride < H))
         return TSA_ERR_SHAPE;
