@@ -459,3 +459,10 @@ def test_sums_over_the_most_rows_are_not_cut_short(tsa):
         want, parts = steps.sum((0, 1)) / M, steps.cumsum(1)
         tol = (2.0 ** -22 * parts.abs().sum((0, 1)) + 8 * U * parts[:, -1].cumsum(0).abs().amax(0)) / M
         near(r.grad_weight[v], want, tol + 2.0 ** -8 * (want.abs() + tol), v)
+
+
+# of a piece of 30,000 entries each sum of dH takes a third: 10,000 terms, on single CTAs and on pairs
+@pytest.mark.parametrize("M,V,H", [(300, 30_000, 4096), (1000, 29_000, 2048)])
+def test_sums_of_hidden_gradients_in_several_parts(tsa, M, V, H):
+    c = make(M, M, V, H, skip=0.05)
+    check(c, tsa.lm_head_cross_entropy(c["h"], c["w"], c["t"]))

@@ -171,8 +171,8 @@ __device__ __forceinline__ int32_t xent_end(const XentArgs &a) {
 // half: four warps for each quarter of the lanes, half of the columns each.
 // Results leave through 4 KB of shared memory a warp and TMA, so that
 // whole lines are written.  1,024 rows x 32,000 x 4,096: a pass over the scores
-// 160 to 166 us, 1.6 to 1.7 PFLOP/s, both products 298 us, 1.8 PFLOP/s, the tensor
-// pipe busy for 76 to 85 % of the time; in a long run the power limit binds.
+// 164 to 168 us, 1.6 PFLOP/s, both products 309 us, 1.7 PFLOP/s, the tensor
+// pipe busy for 76 to 83 % of the time; in a long run the power limit binds.
 constexpr int kXentThreads = 320;
 constexpr int kXentSlab = 32 * 128;  // 32 rows of 64 bf16
 constexpr uint32_t kAcrossA = 1u << 15, kAcrossB = 1u << 16;  // instruction descriptor: M or N contiguous instead of K
@@ -646,9 +646,13 @@ __device__ __forceinline__ void dh_results(const float *z, float *acc, bool add,
 // a part's largest sum, whatever K is.  65,536 rows x 256 x 128 in the order of their targets, hidden rows of mean 1: dW was
 // off by 0.55 % of itself with one sum for all rows where exact sums of the same G give 0.39 %, and 1.0e-4 of the sum
 // of absolute terms too small in the mean; by 0.42 % against 0.40 and 2.6e-5 so.  Up to 8,192 rows nothing is to be seen.
+//
+// LONG: units of more than 8,192 of K, whose sums are in registers until they leave; those of shorter units go
+// from tensor memory to where they are stored 64 at a time (16 x 8,192 x 1,024 43 us, 45 by way of registers; 343 x
+// 32,000 x 2,048 203 and 206).
 constexpr int kXentSums = 8192 / kTcK;
 
-template <int P>
+template <int P, bool LONG>
 __global__ void __launch_bounds__(kXentThreads, 1)
     xent_products_kernel(const __grid_constant__ CUtensorMap map_gk, const __grid_constant__ CUtensorMap map_gm,
                          const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
@@ -729,31 +733,37 @@ __global__ void __launch_bounds__(kXentThreads, 1)
         uint8_t *slab = ring + (size_t)STAGES * S::STAGE + (warp - 2) * kXentSlab;
         uint32_t j = 0;
         bool ok = true;
-        for (int32_t x = 0; ok && units.get(x, u); ++x) {
+        for (int32_t i = 0; ok && units.get(i, u); ++i) {
             const int32_t y0 = u.y + rank * 128 + quarter * 32, h0 = u.x + half * NC;
             const bool used = u.is_dh || y0 < left;
-            float z[NC];
+            const uint32_t b = j & 1u;  // (of a single sum)
+            float z[LONG ? NC : 64];
+            if constexpr (LONG) {
 #pragma unroll
-            for (int q = 0; q < NC; ++q) z[q] = 0.f;
-            for (int k0 = 0; k0 < u.ks; k0 += kXentSums, ++j) {  // (a part of a short last piece may be empty)
-                const uint32_t b = j & 1u;
-                ok = xent_warp_wait(&s.done[b], (j >> 1) & 1u);
-                if (!ok) break;
-                mma_fence_after();
+                for (int q = 0; q < NC; ++q) z[q] = 0.f;
+                for (int k0 = 0; k0 < u.ks; k0 += kXentSums, ++j) {
+                    ok = xent_warp_wait(&s.done[j & 1u], (j >> 1) & 1u);
+                    if (!ok) break;
+                    mma_fence_after();
 #pragma unroll
-                for (int q = 0; q < NC; q += 16) {
-                    if (!used || h0 + q >= a.H) break;
-                    uint32_t r[16];
-                    __syncwarp();
-                    TmemLoad<16>::ld(at + b * 256 + q, r);
-                    tmem_wait_ld();
+                    for (int q = 0; q < NC; q += 16) {
+                        if (!used || h0 + q >= a.H) break;
+                        uint32_t r[16];
+                        __syncwarp();
+                        TmemLoad<16>::ld(at + (j & 1u) * 256 + q, r);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        split_pair(add2(pair_of(z[q + i], z[q + i + 1]),
-                                        pair_of(__uint_as_float(r[i]), __uint_as_float(r[i + 1]))),
-                                   z[q + i], z[q + i + 1]);
+                        for (int i = 0; i < 16; i += 2)
+                            split_pair(add2(pair_of(z[q + i], z[q + i + 1]),
+                                            pair_of(__uint_as_float(r[i]), __uint_as_float(r[i + 1]))),
+                                       z[q + i], z[q + i + 1]);
+                    }
+                    xent_drained<P>(&s.drained[j & 1u], lane);
                 }
-                xent_drained<P>(&s.drained[b], lane);
+            } else if (u.ks > 0) {  // (a part of a short last piece may be empty)
+                ok = xent_warp_wait(&s.done[b], (j >> 1) & 1u);
+                mma_fence_after();
+                ++j;
             }
             if (!ok) break;
             const int32_t m = y0 + lane;
@@ -763,19 +773,33 @@ __global__ void __launch_bounds__(kXentThreads, 1)
 #pragma unroll
             for (int g = 0; g < NC; g += 64) {
                 if (!used || h0 + g >= a.H) break;
+                float *x = z + (LONG ? g : 0);
+                if constexpr (!LONG) {
 #pragma unroll
-                for (int q = 0; q < 64; ++q) z[g + q] *= scale;
+                    for (int q = 0; q < 64; q += 16) {
+                        uint32_t r[16];
+                        __syncwarp();
+                        TmemLoad<16>::ld(at + b * 256 + g + q, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[q + i] = u.ks > 0 ? __uint_as_float(r[i]) * scale : 0.f;
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 64; ++q) x[q] *= scale;
+                }
                 if (!u.is_dh) {
                     slab_wait(lane);
-                    slab_row(slab, lane, z + g);
+                    slab_row(slab, lane, x);
                     slab_store(&map_dw, slab, lane, h0 + g, y0);
                 } else if (mine) {
 #pragma unroll
                     for (int q = 0; q < 64; q += 8) {
-                        if (h0 + g + q < a.H) dh_results(z + g + q, acc + g + q, v0 > 0, last ? to + g + q : nullptr);
+                        if (h0 + g + q < a.H) dh_results(x + q, acc + g + q, v0 > 0, last ? to + g + q : nullptr);
                     }
                 }
             }
+            if (!LONG && u.ks > 0) xent_drained<P>(&s.drained[b], lane);
         }
         if (lane == 0) tma_store_done();
     }
@@ -880,10 +904,10 @@ int launch_scores(const XentArgs &args, int64_t v0, int64_t piece, XentPass pass
     return launch(fn, dim3(grid), dim3(kXentThreads), S::SMEM, params, st, P);
 }
 
-template <int P>
+template <int P, bool LONG>
 int launch_products(const XentArgs &args, int64_t v0, int64_t piece, cudaStream_t st) {
     using S = XentShape<256, P>;
-    const void *fn = reinterpret_cast<const void *>(&xent_products_kernel<P>);
+    const void *fn = reinterpret_cast<const void *>(&xent_products_kernel<P, LONG>);
     const int64_t pad = xent_padded(args.M), left = args.V - v0 < piece ? args.V - v0 : piece;
     const int64_t wide = xent_width(args.H);
     const uint16_t *weight = args.weight + v0 * args.wstride;
@@ -917,6 +941,9 @@ int xent_launch(const XentArgs &args, cudaStream_t st) {
     void *one[] = {&a};
     const int64_t pad = xent_padded(a.M), piece = xent_piece(a.M, a.V);
     const bool pairs = xent_pairs(a.M);
+    // K steps of the longest unit: all rows for dW, a part of a piece for dH
+    const int64_t steps = ((a.V < piece ? a.V : piece) + kTcK - 1) / kTcK, part = (steps + a.splits - 1) / a.splits;
+    const bool sums = (a.dw && pad / kTcK > kXentSums) || (a.dh && part > kXentSums);
     if (cudaLaunchKernel(reinterpret_cast<const void *>(&xent_prepare_kernel),
                          dim3((unsigned)((a.M + kXentPrep - 1) / kXentPrep + 128 / kXentPrep)), dim3(32 * kXentPrep), one, 0,
                          st) != cudaSuccess)
@@ -949,7 +976,9 @@ int xent_launch(const XentArgs &args, cudaStream_t st) {
         if (a.db && launch(reinterpret_cast<const void *>(&xent_bias_kernel), dim3((unsigned)((piece + 31) / 32)),
                            dim3(32, 32), 0, params, st) != 0)
             return -1;
-        if ((a.dh || a.dw) && (pairs ? launch_products<2>(a, v0, piece, st) : launch_products<1>(a, v0, piece, st)) != 0)
+        if ((a.dh || a.dw) && (pairs  ? sums ? launch_products<2, true>(a, v0, piece, st) : launch_products<2, false>(a, v0, piece, st)
+                               : sums ? launch_products<1, true>(a, v0, piece, st)
+                                      : launch_products<1, false>(a, v0, piece, st)) != 0)
             return -1;
     }
     if (a.dh && a.splits > 1 &&
