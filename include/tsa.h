@@ -573,11 +573,14 @@ size_t tsa_lm_head_int8_workspace_bytes(int64_t M, int64_t H);
  * A skipped row's hidden row is not used, whatever it holds; its loss, lse and
  * gradient are 0.  NaN scores count as -inf; a +inf score gives its row an
  * lse of +inf, and a row without a finite score one of -inf; both have a loss of
- * NaN and NaN in the gradients that they take part in.
- * bf16 products and fp32 sums.  G goes through bf16 (half a step of 2^-8 of each
- * of its elements), grad_bias does not.  The weight is read once for the sums and
- * twice more for the gradients.  Sums in a fixed order: equal calls give
- * equal bits.
+ * NaN.  The latter makes every gradient that it takes part in NaN, with a softcap
+ * and without; a row with a +inf score makes its own NaN, and that entry's.
+ * bf16 products and fp32 sums.  The tensor cores cut what they add towards zero,
+ * by about 2^-23 of the sum for each 16 terms: sums begin anew each 1,024 columns
+ * of the scores and 8,192 terms of the gradients, and those are added in fp32.  G
+ * goes through bf16 (half a step of 2^-8 of each of its elements), grad_bias does
+ * not.  The weight is read once for each 8,192 rows for the sums and twice more
+ * for the gradients.  Sums in a fixed order: equal calls give equal bits.
  */
 int tsa_lm_head_cross_entropy(const void *hidden, int64_t M, int64_t H, int64_t hidden_row_stride,
                               const void *weight, int64_t V, int64_t weight_row_stride, const float *bias,

@@ -232,8 +232,11 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
 
 // Rows go round the CTAs, so that a thread keeps its columns' part of dw in
 // registers; a part a CTA (and row of threads) goes to the workspace.  What bounds
-// it is a row's latency: 1,001 x 2,051 f32 take 16 us, 3.3 turns of 304 CTAs and
-// the launch that adds the parts.
+// it is a row's latency: 1,216 x 1,001 bf16 take 9.4 us, four turns of 304 CTAs and
+// the launch that adds the parts.  BIG, for rows of more than 8,192 elements, is
+// for those that the ring has no two stages for: the compiler spills 172 to 304
+// bytes a thread of rows of vectors and 756 to 1,028 of rows of single elements
+// (4,096 x 12,344 f32 with a residual's gradient 246 us, x 12,345 642).
 template <int DT, int W, int E, bool BIG>
 __global__ void __launch_bounds__(norm_threads(BIG)) norm_back_kernel(NormBackArgs a) {
     // whether the registers hold the next row too, and the weights
